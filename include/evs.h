@@ -79,7 +79,9 @@ enum {
     EVS_FLAG_BAD_K = 2u,          /* slice saw k outside [0, gamma] or a bad candidate  */
     EVS_FLAG_EMPTY_RESIDUAL = 4u, /* max(0, p - q) summed to 0 in fp32; p was used      */
     EVS_FLAG_BAD_TOKEN = 8u,      /* a token id outside [0, vocab) was clamped          */
-    EVS_FLAG_TIMEOUT = 16u        /* a kernel gave up a bounded wait; its output is void */
+    EVS_FLAG_TIMEOUT = 16u,       /* a kernel gave up a bounded wait; its output is void */
+    EVS_FLAG_BAD_LEN = 32u,       /* a sequence length outside its range was clamped     */
+    EVS_FLAG_EMPTY_ROW = 64u      /* a row whose tokens are all ruled out: no draw (-1)  */
 };
 
 #define EVS_MAX_LAYERS 64
@@ -330,6 +332,145 @@ evs_status evs_projection_noalloc(const void* X, int32_t x_rows, const void* W, 
  * nothing. EVS_ERR_INVALID_ARG for a null flags pointer, EVS_ERR_CUDA if a CUDA call
  * fails. */
 evs_status evs_projection_noalloc_flags(uint32_t* flags, int32_t clear, void* stream);
+
+/* ---- Stand-alone operators ----------------------------------------------------------
+ * No handle: every call says what it works on. The caller owns all memory; the work is
+ * enqueued on stream (a cudaStream_t of the current device) and nothing is allocated or
+ * synchronised, so calls may be captured into CUDA graphs. Strides are in elements, the last
+ * dimension is contiguous, offsets are 64-bit. Sums, statistics and states are fp32 or wider.
+ * flags, in every struct: device uint32 or NULL, an EVS_FLAG_* word that the kernels OR into
+ * (never cleared by them). Bad arguments return EVS_ERR_INVALID_ARG before anything is
+ * enqueued; an empty call (no rows, no sequences) returns EVS_OK and does nothing. */
+
+/* The filtered draw. Per row r, with l the logits, T, k, p and m the row's parameters:
+ *   w_i = exp((l_i - max l) / T), tokens ordered by (l descending, id ascending);
+ *   keep the first k; of these the shortest prefix whose mass before a token is below p times
+ *   their mass (at least one token); of these the tokens with w_i >= m * max w;
+ *   token = the smallest id whose cumulative kept mass over ascending ids exceeds u * total.
+ * The weights are summed in 64-bit fixed point: the same inputs give the same token whatever
+ * the launch, and the order of equal logits is that of their ids. NaN and -inf logits are ruled
+ * out; where the largest logit is +inf, the +inf tokens share the mass. A row with every token
+ * ruled out gives token -1, logprob -inf, zero probabilities and EVS_FLAG_EMPTY_ROW. */
+typedef struct {
+    int32_t rows, vocab;         /* vocab 1 .. 262144                                       */
+    int32_t dtype;               /* EVS_DTYPE_* of the logits                               */
+    int64_t ld;                  /* row stride of logits (>= vocab)                         */
+    const void* logits;          /* device [rows][vocab]                                    */
+    const float* temperature;    /* device [rows] or NULL (1); not above 0: the argmax      */
+    const int32_t* top_k;        /* device [rows] or NULL; outside [1, vocab): off          */
+    const float* top_p;          /* device [rows] or NULL; >= 1 or NaN: off, <= 0: one token */
+    const float* min_p;          /* device [rows] or NULL; not above 0: off, above 1: as 1  */
+    const float* uniforms;       /* device [rows], in [0, 1) (clamped)                      */
+    int32_t* token;              /* device [rows]                                           */
+    float* logprob;              /* device [rows] or NULL: log of the token's kept share    */
+    float* probs;                /* device [rows][vocab] or NULL: the distribution drawn from */
+    int64_t probs_ld;            /* row stride of probs                                     */
+    uint32_t* flags;
+} evs_sample_args;
+evs_status evs_sample(const evs_sample_args* args, void* stream);
+
+/* The native decode step (evs_decode_step) with the filtered draw over the step's logits in
+ * place of the draw from softmax(logits / temperature); the configuration's mode and temperature
+ * are not used. draw: temperature, top_k, top_p, min_p, uniforms, logprob, probs and probs_ld are
+ * taken from it ([batch] rows); its other members are ignored. next: device int32 [B], may alias
+ * tokens. EVS_FLAG_EMPTY_ROW goes to the handle's flag word. */
+evs_status evs_decode_filtered(evs_handle* h, const int32_t* tokens, const evs_sample_args* draw, int32_t* next);
+
+/* Attention for a batch that shares a prefix. Query (b, c, i) of head h reads, with the K/V head
+ * g = h / (heads / kv_heads): the `prefix` shared rows (one copy for the whole batch), the own
+ * rows [0, own_len[b] - own_skip) of its sequence (all its candidates share them), and the block
+ * rows j <= i of its candidate. o = softmax(scale q k^T) v over them; lse = log of the sum of
+ * exponentials. The block rows lie in k_block / v_block, or (both NULL, n_cand 1) in the own rows
+ * behind the readable ones, row own_len[b] - own_skip + j.
+ * Lengths outside [0, own_max] are clamped (EVS_FLAG_BAD_LEN); block rows past own_max are left
+ * out (EVS_FLAG_KV_OVERFLOW); a query left without any key gives o = 0 and lse = -inf. Rows that
+ * no query reads may hold anything. K, V and o are dtype; q is q_dtype, rounded to bf16 where the
+ * products run on tensor cores (dtype bf16, head_dim 64 or 128, rows on 16 bytes); statistics and
+ * accumulators are fp32, softmax weights enter the tensor-core products as bf16. */
+typedef struct {
+    int32_t batch, n_cand, block;        /* 1 .. 1024 sequences, <= 64 candidates, <= 128 positions */
+    int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
+    int32_t dtype, q_dtype;              /* EVS_DTYPE_*                                     */
+    int32_t prefix, own_max;             /* shared rows; rows of one sequence's own K/V     */
+    int32_t own_skip;                    /* subtracted from own_len (rows counted elsewhere) */
+    float scale;                         /* 0: 1 / sqrt(head_dim)                           */
+    const void* q;                       /* device, row (b * n_cand + c) * block + i: heads x head_dim */
+    int64_t q_ld;
+    const void *k_prefix, *v_prefix;     /* device [kv_heads][prefix][head_dim]             */
+    int64_t prefix_row, prefix_head;     /* strides of both                                 */
+    const void *k_own, *v_own;           /* device [batch][kv_heads][own_max][head_dim]     */
+    int64_t own_row, own_head, own_seq;
+    const int32_t* own_len;              /* device [batch]                                  */
+    const void *k_block, *v_block;       /* device [batch * n_cand][kv_heads][block][head_dim] or NULL */
+    int64_t block_row, block_head, block_cand;
+    void* o;                             /* device, rows as q                               */
+    int64_t o_ld;
+    float* lse;                          /* device [batch * n_cand * block][heads] or NULL  */
+    void* workspace;                     /* device, 256-byte aligned; not shared by calls that may overlap */
+    size_t ws_bytes;
+    uint32_t* flags;
+} evs_shared_attn_args;
+/* Bytes of workspace for these sizes (pointers may still be null; 0 if invalid). */
+size_t evs_shared_attention_workspace(const evs_shared_attn_args* args);
+evs_status evs_shared_attention(const evs_shared_attn_args* args, void* stream);
+
+/* Short causal convolution of every channel, with bias and SiLU (the FIR mixer of a selective
+ * layer): y_t[c] = act(bias[c] + sum_{j < taps} weight[c][j] x_{t-j}[c]), the inputs before the
+ * first token taken from tail_in. Sequence b has lens[b] tokens (NULL: all have `tokens`; clamped
+ * to [0, tokens]); rows of y past them are left as they were. tail_out gets the last taps - 1
+ * inputs at that point, so state slicing at k is a call with lens k + 1 and y NULL. tail_out may
+ * be tail_in; y must not overlap x. */
+typedef struct {
+    int32_t batch, tokens, width;
+    int32_t taps;                /* 2 .. 16                                                 */
+    int32_t dtype;               /* of x and y                                              */
+    int32_t silu;                /* 1: act = v / (1 + exp(-v)), 0: none                     */
+    const void* x;               /* device [batch][tokens][width], strides x_seq, x_ld      */
+    int64_t x_ld, x_seq;
+    void* y;                     /* likewise, or NULL when only the tail is wanted          */
+    int64_t y_ld, y_seq;
+    const float* weight;         /* device [width][taps]: weight[c][j] multiplies x_{t-j}   */
+    const float* bias;           /* device [width] or NULL                                  */
+    const float* tail_in;        /* device [batch][taps - 1][width], oldest first, or NULL (0) */
+    float* tail_out;             /* likewise, or NULL                                       */
+    const int32_t* lens;         /* device [batch] or NULL                                  */
+    uint32_t* flags;
+} evs_conv_args;
+evs_status evs_causal_conv(const evs_conv_args* args, void* stream);
+
+/* Selective scan (the modal IIR mixer's input-dependent sibling). Per channel c, state n:
+ *   dl_t = softplus(dt_t + dt_bias)  (or dt_t + dt_bias where softplus is 0)
+ *   s_t  = exp(dl_t A[c][n]) s_{t-1} + dl_t x_t B_t[n]
+ *   y_t  = (sum_n C_t[n] s_t[n] + D[c] x_t) * z_t / (1 + exp(-z_t))
+ * A is finite and normally negative. lens, y and the two states as in evs_causal_conv: state_out
+ * is the state after lens[b] tokens and may be state_in; y must not overlap the inputs. States
+ * and A start on 16 bytes. */
+typedef struct {
+    int32_t batch, tokens, width;
+    int32_t states;              /* 4, 8, 16 or 32                                          */
+    int32_t dtype;               /* of x, dt, z, B, C and y                                 */
+    int32_t softplus;
+    const void* x;               /* device [batch][tokens][width]                           */
+    int64_t x_ld, x_seq;
+    const void* dt;              /* device [batch][tokens][width]                           */
+    int64_t dt_ld, dt_seq;
+    const void* z;               /* device [batch][tokens][width] or NULL (no gate)         */
+    int64_t z_ld, z_seq;
+    const void* B;               /* device [batch][tokens][states]                          */
+    int64_t b_ld, b_seq;
+    const void* C;               /* device [batch][tokens][states]                          */
+    int64_t c_ld, c_seq;
+    void* y;                     /* device [batch][tokens][width], or NULL                  */
+    int64_t y_ld, y_seq;
+    const float* A;              /* device [width][states]                                  */
+    const float* D;              /* device [width] or NULL (0)                              */
+    const float* dt_bias;        /* device [width] or NULL (0)                              */
+    const float* state_in;       /* device [batch][width][states] or NULL (0)               */
+    float* state_out;            /* likewise, or NULL                                       */
+    const int32_t* lens;         /* device [batch] or NULL                                  */
+    uint32_t* flags;
+} evs_scan_args;
+evs_status evs_selective_scan(const evs_scan_args* args, void* stream);
 
 /* Static description of a status code. */
 const char* evs_status_str(evs_status s);

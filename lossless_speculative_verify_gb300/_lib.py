@@ -19,6 +19,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 MODE_GREEDY, MODE_SAMPLING = 0, 1
 CAND_RECURSIVE, CAND_MAX_ACCEPT = 0, 1
 FLAG_KV_OVERFLOW, FLAG_BAD_K, FLAG_EMPTY_RESIDUAL, FLAG_BAD_TOKEN, FLAG_TIMEOUT = 1, 2, 4, 8, 16
+FLAG_BAD_LEN, FLAG_EMPTY_ROW = 32, 64
 (BUF_LOGITS, BUF_FIR_STAGE, BUF_IIR_U, BUF_K_CACHE, BUF_V_CACHE, BUF_K_SIDE, BUF_V_SIDE,
  BUF_KV_LEN, BUF_FIR_TAIL, BUF_IIR_STATE, BUF_CAND_K, BUF_CAND_CORR) = range(12)
 
@@ -27,7 +28,8 @@ EXPORTED = (
     "evs_prefill", "evs_verify_block", "evs_slice_state", "evs_replay_state", "evs_decode_step", "evs_import_state",
     "evs_export_state", "evs_debug_buffer", "evs_device_flags", "evs_last_launch_count",
     "evs_status_str", "evs_profile_enable", "evs_profile_read", "evs_debug_projection",
-    "evs_projection_noalloc", "evs_projection_noalloc_flags",
+    "evs_projection_noalloc", "evs_projection_noalloc_flags", "evs_sample", "evs_decode_filtered",
+    "evs_causal_conv", "evs_selective_scan", "evs_shared_attention_workspace", "evs_shared_attention",
 )
 KERNEL_KINDS = ("embed", "norm", "gemm", "fir", "iir", "kv_write", "attn", "attn_combine", "accept",
                 "slice", "advance")
@@ -61,6 +63,36 @@ class StateView(C.Structure):
 
 class BufferInfo(C.Structure):
     _fields_ = [("ptr", C.c_void_p), ("bytes", C.c_size_t)]
+
+
+def _fields(text):
+    """Struct fields from "kind name, name; kind name": i int32, q int64, f float, p pointer, z size_t."""
+    kinds = {"i": C.c_int32, "q": C.c_int64, "f": C.c_float, "p": C.c_void_p, "z": C.c_size_t}
+    return [(name.strip(), kinds[part.split()[0]]) for part in text.split(";")
+            for name in part.strip()[1:].split(",")]
+
+
+class SampleArgs(C.Structure):
+    _fields_ = _fields("i rows, vocab, dtype; q ld; p logits, temperature, top_k, top_p, min_p, uniforms, token, "
+                       "logprob, probs; q probs_ld; p flags")
+
+
+class ConvArgs(C.Structure):
+    _fields_ = _fields("i batch, tokens, width, taps, dtype, silu; p x; q x_ld, x_seq; p y; q y_ld, y_seq; "
+                       "p weight, bias, tail_in, tail_out, lens, flags")
+
+
+class ScanArgs(C.Structure):
+    _fields_ = _fields("i batch, tokens, width, states, dtype, softplus; p x; q x_ld, x_seq; p dt; q dt_ld, dt_seq; "
+                       "p z; q z_ld, z_seq; p B; q b_ld, b_seq; p C; q c_ld, c_seq; p y; q y_ld, y_seq; "
+                       "p A, D, dt_bias, state_in, state_out, lens, flags")
+
+
+class SharedAttnArgs(C.Structure):
+    _fields_ = _fields("i batch, n_cand, block, heads, kv_heads, head_dim, dtype, q_dtype, prefix, own_max, own_skip; "
+                       "f scale; p q; q q_ld; p k_prefix, v_prefix; q prefix_row, prefix_head; p k_own, v_own; "
+                       "q own_row, own_head, own_seq; p own_len, k_block, v_block; "
+                       "q block_row, block_head, block_cand; p o; q o_ld; p lse, workspace; z ws_bytes; p flags")
 
 
 _lib = None
@@ -118,6 +150,15 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.evs_projection_noalloc.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
     lib.evs_projection_noalloc_flags.restype = C.c_int
     lib.evs_projection_noalloc_flags.argtypes = [C.POINTER(C.c_uint32), i32, vp]
+    for name, args in (("evs_sample", SampleArgs), ("evs_causal_conv", ConvArgs),
+                       ("evs_selective_scan", ScanArgs), ("evs_shared_attention", SharedAttnArgs)):
+        fn = getattr(lib, name)
+        fn.restype = C.c_int
+        fn.argtypes = [C.POINTER(args), vp]
+    lib.evs_shared_attention_workspace.restype = C.c_size_t
+    lib.evs_shared_attention_workspace.argtypes = [C.POINTER(SharedAttnArgs)]
+    lib.evs_decode_filtered.restype = C.c_int
+    lib.evs_decode_filtered.argtypes = [vp, vp, C.POINTER(SampleArgs), vp]
     lib.evs_status_str.restype = C.c_char_p
     lib.evs_status_str.argtypes = [C.c_int]
     _lib = lib

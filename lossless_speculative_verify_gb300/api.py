@@ -156,6 +156,25 @@ class Verifier:
         L.check(self.lib.evs_decode_step(self.h, _vp(tokens), _vp(u), _vp(nxt), _vp(tie)), "evs_decode_step")
         return nxt, tie
 
+    def decode_filtered(self, tokens, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None,
+                        logprob=None, probs=None):
+        """One native decode step whose draw is filtered (see ``ops.sample``): consume tokens [B], return next
+        [B]. u, temperature, top_p, min_p [B] fp32 and top_k [B] int32 on the device or None; logprob [B] and
+        probs [B, vocab] fp32 tensors are filled where given."""
+        nxt = self.next if out is None else out
+        B, V = self.cfg.batch, self.cfg.vocab
+        for name, t, dt, shape in (("tokens", tokens, torch.int32, (B,)), ("u", u, torch.float32, (B,)),
+                                   ("temperature", temperature, torch.float32, (B,)), ("out", nxt, torch.int32, (B,)),
+                                   ("top_k", top_k, torch.int32, (B,)), ("top_p", top_p, torch.float32, (B,)),
+                                   ("min_p", min_p, torch.float32, (B,)), ("logprob", logprob, torch.float32, (B,)),
+                                   ("probs", probs, torch.float32, (B, V))):
+            if t is not None and not (t.dtype == dt and tuple(t.shape) == shape and t.is_contiguous() and t.is_cuda):
+                raise ValueError(f"{name}: want contiguous {dt} {shape} on the device")
+        a = L.SampleArgs(temperature=_vp(temperature), top_k=_vp(top_k), top_p=_vp(top_p), min_p=_vp(min_p),
+                         uniforms=_vp(u), logprob=_vp(logprob), probs=_vp(probs), probs_ld=V)
+        L.check(self.lib.evs_decode_filtered(self.h, _vp(tokens), C.byref(a), _vp(nxt)), "evs_decode_filtered")
+        return nxt
+
     def reset(self):
         L.check(self.lib.evs_reset(self.h), "evs_reset")
 

@@ -537,6 +537,32 @@ evs_status evs_decode_step(evs_handle* h, const int32_t* tokens, const float* un
     return after_launch(h);
 }
 
+evs_status evs_decode_filtered(evs_handle* h, const int32_t* tokens, const evs_sample_args* draw, int32_t* next) {
+    if (!h || !tokens || !draw || !next || !draw->uniforms) return EVS_ERR_INVALID_ARG;
+    if (draw->probs && draw->probs_ld < h->cfg.vocab) return EVS_ERR_INVALID_ARG;
+    h->launches = 0;
+    if (h->kv_hi + 1 > h->cfg.t_max) return EVS_ERR_CAPACITY;
+    const int B = h->cfg.batch;
+    evs::Pass p{B, 1, 1, B, 1, 1};
+    run_layers(h, tokens, 1, nullptr, p, true);
+    evs::launch_advance(h, 1);
+    evs_sample_args a = *draw;
+    a.rows = B;
+    a.vocab = h->cfg.vocab;
+    a.dtype = EVS_DTYPE_F32;
+    a.ld = h->cfg.vocab;
+    a.logits = h->logits;
+    a.token = next;
+    a.flags = h->flags;
+    evs::prof_begin(h, EVS_K_ACCEPT);
+    const cudaError_t e = evs::launch_sample(a, h->stream);
+    h->launches++;
+    evs::prof_end(h, EVS_K_ACCEPT);
+    h->kv_hi += 1;
+    h->verified = 0;
+    return e == cudaSuccess ? after_launch(h) : EVS_ERR_CUDA;
+}
+
 evs_status evs_slice_state(evs_handle* h, const int32_t* accepted_len, const int32_t* best_cand) {
     if (!h || !accepted_len) return EVS_ERR_INVALID_ARG;
     if (h->cfg.n_cand > 1 && !best_cand) return EVS_ERR_INVALID_ARG;

@@ -149,5 +149,9 @@ void launch_accept(evs_handle* h, const int32_t* tokens, const float* q, const f
 void launch_slice(evs_handle* h, const int32_t* k, const int32_t* cand);
 void launch_pick(evs_handle* h, const float* u, int32_t* next, uint32_t* tie);
 void launch_advance(evs_handle* h, int T);
+// filtered draw (sample.cu)
+cudaError_t launch_sample(const evs_sample_args& args, cudaStream_t stream);
+// shared-prefix attention (attn_shared.cu), arguments already checked
+cudaError_t launch_shared_attention(const evs_shared_attn_args& args, cudaStream_t stream);
 
 }  // namespace evs

@@ -1,0 +1,731 @@
+// The filtered draw of the next token (evs_sample): temperature, top-k, top-p, min-p and the
+// inverse CDF at a given uniform, one thread-block cluster per row.
+//
+//   w_i = exp((l_i - max l) / T). In the order (l descending, id ascending): the first top_k
+//   tokens, of these the shortest prefix whose mass before the token is below top_p of theirs,
+//   of these the ones with w_i >= min_p. The token is the smallest id whose cumulative kept
+//   mass, over ascending ids, exceeds u times the total.
+//
+// The decisions are comparisons of sums over the whole vocabulary, so weights are computed to
+// about 2^-37 relative and summed as 64-bit fixed point (2^-44): the sums do not depend on their
+// order, every run gives the same token, and it is the one that exact arithmetic gives unless a
+// border falls within about 1e-11 of the total mass. In fp32 the error of one such sum,
+// about 1e-6 of the mass, would move the draw in several percent of rows of 131072 flat logits.
+//
+// The row is read once: the CTAs of the cluster keep their slices in shared memory and search
+// there. The cut (top-k and top-p are both prefixes of the sorted row, so one pair (logit, id)
+// describes what is kept) is found by a histogram over (max - l) / T in steps of 1/64, narrowed
+// by digits of (ordered logit, id) while the bin that holds the cut has more than CAP tokens;
+// those few are then ranked pairwise.
+#include "evs_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace evs {
+namespace {
+
+using bf16 = __nv_bfloat16;
+typedef unsigned long long u64;
+
+constexpr int SMP_MAX_V = 1 << 18;      // ids take 18 bits of the order
+constexpr int SMP_IDBITS = 18;
+constexpr int SMP_ORDER_BITS = 32 + SMP_IDBITS;
+constexpr int SMP_DIGIT = 11;
+constexpr int SMP_BINS = 1 << SMP_DIGIT;
+constexpr int SMP_CAP = 1024;           // tokens ranked pairwise
+constexpr int SMP_FRAC = 44;            // fixed point of weights; 2^18 of them stay below 2^63
+constexpr int SMP_MAX_CS = 8;           // portable cluster size
+
+// 2^(j/32) for j = -16..16, in units of 2^-62
+__constant__ u64 kPow2[33] = {
+    0x2d413cccfe779921ull, 0x2e3eebd1d8bee7baull, 0x2f4228e7d6030db0ull, 0x304b1332999c2516ull,
+    0x3159ca845541b6b7ull, 0x326e6f619b8bc9e9ull, 0x3389230547e12039ull, 0x34aa07647c4ab917ull,
+    0x35d13f32b5a75abdull, 0x36feede5f6bc8dd5ull, 0x383337bb0aa53844ull, 0x396e41b9df20d22aull,
+    0x3ab031b9f7490e4cull, 0x3bf92e66f736bd73ull, 0x3d495f454921b30bull, 0x3ea0ecb6dc8a80cfull,
+    0x4000000000000000ull, 0x4166c34c5615d0ecull, 0x42d561b3e6243d8aull, 0x444c0740496d4294ull,
+    0x45cae0f1f545eb73ull, 0x47521cc5a2e6a9e0ull, 0x48e1e9b9d588e19bull, 0x4a7a77d47f7b84b1ull,
+    0x4c1bf828c6dc54b8ull, 0x4dc69cdceaa72a9cull, 0x4f7a993048d088d7ull, 0x513821818624b40cull,
+    0x52ff6b54d8a89c75ull, 0x54d0ad5a753e077cull, 0x56ac1f752150a563ull, 0x5891fac0e95612c8ull,
+    0x5a827999fcef3242ull
+};
+
+struct SampleArgs {
+    const void* logits;
+    int64_t ld, ldp;
+    int V;
+    const float *temperature, *top_p, *min_p, *uniforms;
+    const int32_t* top_k;
+    int32_t* token;
+    float* logprob;
+    float* probs;
+    uint32_t* flags;
+    int slice;             // slots of shared memory for logits
+};
+
+// ---- cluster helpers --------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void st_peer_u64(uint32_t addr, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t atom_peer_add(uint32_t addr, uint32_t v) {
+    uint32_t o;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(addr), "r"(v) : "memory");
+    return o;
+}
+template <bool CLUSTER> __device__ __forceinline__ void sync_all() {
+    if constexpr (CLUSTER) cluster_sync(); else __syncthreads();
+}
+
+__device__ __forceinline__ float load_logit(float v) { return v != v ? -INFINITY : v; }   // NaN: ruled out
+__device__ __forceinline__ float load_logit(bf16 v) { return load_logit(__bfloat162float(v)); }
+
+// Position in the order: larger is earlier. The logit's bits mapped to an ascending integer,
+// then the id descending.
+__device__ __forceinline__ u64 order_of(float l, int id) {
+    uint32_t k = __float_as_uint(l + 0.f);             // -0 and +0 are one value
+    k = (k & 0x80000000u) ? ~k : (k | 0x80000000u);
+    return ((u64)k << SMP_IDBITS) | (u64)((1 << SMP_IDBITS) - 1 - id);
+}
+
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Exclusive scan over the block, and the total; red holds one word per warp.
+__device__ __forceinline__ u64 block_scan_u64(u64 v, u64* red, u64& total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    u64 x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[w] = x;
+    __syncthreads();
+    u64 before = 0, all = 0;
+    for (int i = 0; i < nw; ++i) {
+        const u64 r = red[i];
+        if (i < w) before += r;
+        all += r;
+    }
+    total = all;
+    return before + x - v;
+}
+
+// p in [0, 1) as 2^-64 fixed point (p >= 1: all ones; p <= 0 or NaN: 0)
+__device__ __forceinline__ u64 unit_fixed(float p) {
+    if (!(p > 0.f)) return 0;
+    if (p >= 1.f) return ~0ull;
+    return (u64)((double)p * 18446744073709551616.0);
+}
+
+// ---- weights ------------------------------------------------------------------------------------
+// exp((l - M) / T) = 2^y, y = (l - M) * c with c = log2(e) / T held as the sum of two floats. The
+// difference and the product are formed exactly (two-sum, fused multiply-add remainders);
+// y = n + j/32 + g, |g| <= 1/64, and 2^g - 1 by its Taylor series, whose first term is kept as a
+// sum of two floats too. Relative error about 2^-37; weights below 2^-45 are 0.
+struct WeightFn {
+    float M, c_hi, c_lo;
+    const u64* tab;       // shared copy of kPow2
+
+    __device__ __forceinline__ bool split(float l, int& n, int& j, float& q, float& lo) const {
+        const float dh = l - M;
+        const float bb = dh - l;
+        const float dl = (l - (dh - bb)) + (-M - bb);
+        const float p = dh * c_hi;
+        if (!(p > -64.f)) return false;
+        const float e = fmaf(dh, c_hi, -p) + fmaf(dh, c_lo, dl * c_hi);
+        const float nf = rintf(p);
+        const float r = (p - nf) + e;
+        const float e1 = ((p - nf) - r) + e;              // what the sum dropped, below 2^-25
+        const float jf = rintf(r * 32.f);
+        const float g = fmaf(jf, -0.03125f, r);
+        const float L_hi = 0.693147182464599609375f, L_lo = -1.904654299957768e-09f;   // ln 2
+        q = g * L_hi;
+        const float q_lo = fmaf(g, L_hi, -q) + g * L_lo;
+        float h = fmaf(q, 1.f / 120.f, 1.f / 24.f);
+        h = fmaf(h, q, 1.f / 6.f);
+        h = fmaf(h, q, 0.5f);
+        lo = fmaf(h * q, q, fmaf(e1 * L_hi, 1.f + q, q_lo));
+        n = (int)nf;
+        j = (int)jf;
+        return true;
+    }
+    __device__ __forceinline__ u64 fixed(float l) const {
+        int n, j;
+        float q, lo;
+        if (l == M) return 1ull << SMP_FRAC;
+        if (!split(l, n, j, q, lo)) return 0;
+        const int E = __float2int_rn(q * 137438953472.f) + __float2int_rn(lo * 137438953472.f);   // 2^37
+        const u64 t = tab[16 + j];
+        const long long v = (long long)t + (((long long)(uint32_t)(t >> 31) * (long long)E) >> 6);
+        const int sh = 62 - SMP_FRAC - n;                 // >= 18
+        return sh > 62 ? 0 : ((u64)v + (1ull << (sh - 1))) >> sh;
+    }
+    __device__ __forceinline__ float real(float l) const {   // fp32, for probabilities
+        int n, j;
+        float q, lo;
+        if (l == M) return 1.f;
+        if (!split(l, n, j, q, lo)) return 0.f;
+        const float t = (float)tab[16 + j] * 2.168404344971009e-19f;   // 2^-62
+        return fmaf(t, q + lo, t) * __int_as_float((n + 127) << 23);   // n >= -64
+    }
+};
+
+// 16 bytes of a row
+template <typename T> union Raw16 {
+    uint4 q;
+    T v[16 / sizeof(T)];
+    __device__ Raw16() {}
+};
+
+// The set of tokens that holds a cut, and what precedes it: level-0 bin bin0, of it the tokens
+// whose order has `prefix` above bit `shift` (shift SMP_ORDER_BITS: all of the bin).
+struct Found {
+    int bin0, shift;
+    uint32_t count, above_count;
+    u64 above_mass, prefix;
+};
+
+// =========================================================================================
+template <typename T, int THREADS, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel(SampleArgs a) {
+    constexpr int VEC = 16 / sizeof(T);
+    constexpr int BPT = SMP_BINS / THREADS;     // bins a thread sums when the CTA is alone
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* l_s = reinterpret_cast<float*>(smem);
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);   // [4][BINS]: count, mass planes
+    u64* list_o = reinterpret_cast<u64*>(hist);                                 // [CAP], after a search
+    u64* list_w = list_o + SMP_CAP;                                             // [CAP]
+    __shared__ u64 tab[33];
+    __shared__ u64 red[THREADS / 32];
+    __shared__ u64 warp_mass[THREADS / 32];
+    __shared__ float x_max[SMP_MAX_CS];
+    __shared__ u64 x_cnt[SMP_MAX_CS], x_mass[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
+    __shared__ u64 f_above_mass, f_cut, pick_before;
+    __shared__ uint32_t f_bin, f_count, f_above_count, list_n;
+    __shared__ int pick_warp;
+
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t cs = CLUSTER ? cluster_size() : 1u, rank = CLUSTER ? cluster_rank() : 0u;
+    const int row = blockIdx.x / cs;
+    if (tid < 33) tab[tid] = kPow2[tid];
+    if (tid == 0) list_n = 0;
+    // peers may write here once every CTA of the cluster runs: arrive now, wait before the first
+    if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    pdl_wait();
+
+    // ---- parameters of the row
+    const float temp = a.temperature ? a.temperature[row] : 1.f;
+    const bool greedy = !(temp > 0.f);
+    const int k_in = a.top_k ? a.top_k[row] : 0;
+    const float p_in = a.top_p ? a.top_p[row] : 1.f;
+    const float mp_in = a.min_p ? a.min_p[row] : 0.f;
+    const bool need_k = !greedy && k_in > 0 && k_in < a.V;
+    const bool need_p = !greedy && p_in < 1.f;
+    WeightFn wf;
+    wf.tab = tab;
+    {
+        const double c = 1.4426950408889634074 / (greedy ? 1.0 : (double)temp);
+        wf.c_hi = (float)c;
+        wf.c_lo = isfinite(wf.c_hi) ? (float)(c - (double)wf.c_hi) : 0.f;
+    }
+    const float bin_scale = 64.f / (greedy ? 1.f : temp);
+
+    // ---- the slice: granules of 16 bytes of the row, the first and last ones partly filled
+    const T* rp = (const T*)a.logits + (size_t)row * a.ld;
+    const int mis = (int)(((uintptr_t)rp % 16) / sizeof(T));
+    const int grans = (mis + a.V + VEC - 1) / VEC;
+    const int g0 = (int)((long long)grans * rank / cs), g1 = (int)((long long)grans * (rank + 1) / cs);
+    const int n = (g1 - g0) * VEC;              // slots; slot s holds id base + s
+    const int base = g0 * VEC - mis;
+    float mx = -INFINITY;
+    for (int gb = 0; gb < g1 - g0; gb += 4 * THREADS) {
+        Raw16<T> r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int g = gb + u * THREADS + tid;
+            if (g < g1 - g0) {
+                const int id0 = base + g * VEC;
+                if (id0 >= 0 && id0 + VEC <= a.V) {
+                    r[u].q = *reinterpret_cast<const uint4*>(rp + id0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        r[u].v[j] = (id0 + j >= 0 && id0 + j < a.V) ? rp[id0 + j] : from_f32<T>(-INFINITY);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int g = gb + u * THREADS + tid;
+            if (g < g1 - g0) {
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4) {
+                    const float4 f = make_float4(load_logit(r[u].v[j]), load_logit(r[u].v[j + 1]),
+                                                 load_logit(r[u].v[j + 2]), load_logit(r[u].v[j + 3]));
+                    mx = fmaxf(mx, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
+                    *reinterpret_cast<float4*>(l_s + g * VEC + j) = f;
+                }
+            }
+        }
+    }
+    mx = block_max(mx, reinterpret_cast<float*>(red));
+    if constexpr (CLUSTER) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (tid < (int)cs) st_peer_f32(map_peer(smem_u32(&x_max[rank]), tid), mx);
+        cluster_sync();
+        mx = x_max[0];
+        for (uint32_t i = 1; i < cs; ++i) mx = fmaxf(mx, x_max[i]);
+    } else {
+        __syncthreads();
+    }
+    wf.M = mx;
+    if (mx == -INFINITY) {                       // every token ruled out: no draw
+        if (rank == 0 && tid == 0) {
+            a.token[row] = -1;
+            if (a.logprob) a.logprob[row] = -INFINITY;
+            if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_EMPTY_ROW);
+        }
+        if (a.probs)
+            for (int s = tid; s < n; s += THREADS)
+                if (base + s >= 0 && base + s < a.V) a.probs[(size_t)row * a.ldp + base + s] = 0.f;
+        if constexpr (CLUSTER) cluster_sync();
+        return;
+    }
+
+    u64 cut = 0;           // tokens with order >= cut are kept (before min-p)
+    auto bin0_of = [&](float l) -> int {
+        const float d = (mx - l) * bin_scale;
+        return l == mx ? 0 : (d < (float)(SMP_BINS - 1) ? (int)d : SMP_BINS - 1);
+    };
+    auto in_found = [&](const Found& f, float l, u64 o) -> bool {
+        return bin0_of(l) == f.bin0 && (f.shift == SMP_ORDER_BITS || (o >> f.shift) == f.prefix);
+    };
+    // The set of at most CAP tokens (or the single one) where the cumulative count reaches k
+    // (k > 0), or the cumulative mass over the tokens with order >= floor_order reaches
+    // x = ceil(p64 * their mass). Level 0 bins by (max - l) / T, later levels by a digit of the
+    // order. bin0 is BINS where fewer than k tokens are left. Uniform over the cluster.
+    auto search = [&](uint32_t k, u64 floor_order, u64 p64, u64& x) -> Found {
+        Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0, 0};
+        for (int level = 0;; ++level) {
+            const int to = max(0, f.shift - SMP_DIGIT), width = f.shift - to;   // this level's digit
+            for (int i = tid; i < (k ? 1 : 4) * SMP_BINS; i += THREADS) hist[i] = 0;
+            __syncthreads();
+            if (tid == 0) f_bin = SMP_BINS;      // read by all before that barrier, written next after another
+            for (int s = tid; s < n; s += THREADS) {
+                const float l = l_s[s];
+                if (l == -INFINITY) continue;
+                int bin;
+                if (level == 0 && floor_order == 0) {
+                    bin = bin0_of(l);
+                } else {
+                    const u64 o = order_of(l, base + s);
+                    if (o < floor_order) continue;
+                    if (level == 0) {
+                        bin = bin0_of(l);
+                    } else {
+                        if (!in_found(f, l, o)) continue;
+                        // digits descend, so that a lower bin is earlier in the order
+                        bin = (1 << width) - 1 - (int)((o >> to) & ((1ull << width) - 1));
+                    }
+                }
+                atomicAdd(&hist[bin], 1u);
+                if (k == 0) {
+                    const u64 w = wf.fixed(l);
+                    const uint32_t w0 = (uint32_t)w & 0xffffu, w1 = (uint32_t)(w >> 16) & 0xffffu,
+                                   w2 = (uint32_t)(w >> 32);
+                    if (w0) atomicAdd(&hist[SMP_BINS + bin], w0);
+                    if (w1) atomicAdd(&hist[2 * SMP_BINS + bin], w1);
+                    if (w2) atomicAdd(&hist[3 * SMP_BINS + bin], w2);
+                }
+            }
+            sync_all<CLUSTER>();
+            // this CTA's share of the bins, summed over the cluster; a thread takes PT in a row
+            const int nb = SMP_BINS / cs, b_lo = nb * rank, PT = (nb + THREADS - 1) / THREADS;
+            uint32_t cnt[BPT];
+            u64 mass[BPT], tc = 0, tm = 0;
+#pragma unroll
+            for (int i = 0; i < BPT; ++i) {
+                cnt[i] = 0;
+                mass[i] = 0;
+                if (i < PT && tid * PT + i < nb) {
+                    const int b = b_lo + tid * PT + i;
+                    for (uint32_t r = 0; r < cs; ++r) {
+                        auto at = [&](int plane) -> u64 {
+                            if constexpr (CLUSTER) return ld_peer_u32(map_peer(smem_u32(&hist[plane * SMP_BINS + b]), r));
+                            else return hist[plane * SMP_BINS + b];
+                        };
+                        cnt[i] += (uint32_t)at(0);
+                        if (k == 0) mass[i] += at(1) + (at(2) << 16) + (at(3) << 32);
+                    }
+                }
+                tc += cnt[i];
+                tm += mass[i];
+            }
+            u64 all_c, all_m;
+            u64 ec = block_scan_u64(tc, red, all_c);
+            u64 em = block_scan_u64(tm, red, all_m);
+            if constexpr (CLUSTER) {
+                if (tid < (int)cs) {
+                    st_peer_u64(map_peer(smem_u32(&x_cnt[rank]), tid), all_c);
+                    st_peer_u64(map_peer(smem_u32(&x_mass[rank]), tid), all_m);
+                }
+                cluster_sync();
+                all_m = 0;
+                for (uint32_t i = 0; i < cs; ++i) {
+                    if (i < rank) {
+                        ec += x_cnt[i];
+                        em += x_mass[i];
+                    }
+                    all_m += x_mass[i];
+                }
+            }
+            if (level == 0 && k == 0) {           // mass before a kept token < p * total
+                x = __umul64hi(p64, all_m) + ((p64 * all_m) != 0 ? 1 : 0);
+                if (x == 0) x = 1;                // the first token is always kept
+            }
+            ec += f.above_count;
+            em += f.above_mass;
+#pragma unroll
+            for (int i = 0; i < BPT; ++i) {
+                const bool hit = k ? (ec < k && ec + cnt[i] >= k) : (em < x && em + mass[i] >= x);
+                if (hit) {
+                    const uint32_t bin = b_lo + tid * PT + i;
+                    for (uint32_t r = 0; r < cs; ++r) {
+                        if constexpr (CLUSTER) {
+                            st_peer_u32(map_peer(smem_u32(&f_bin), r), bin);
+                            st_peer_u32(map_peer(smem_u32(&f_count), r), cnt[i]);
+                            st_peer_u32(map_peer(smem_u32(&f_above_count), r), (uint32_t)ec);
+                            st_peer_u64(map_peer(smem_u32(&f_above_mass), r), em);
+                        } else {
+                            f_bin = bin;
+                            f_count = cnt[i];
+                            f_above_count = (uint32_t)ec;
+                            f_above_mass = em;
+                        }
+                    }
+                }
+                ec += cnt[i];
+                em += mass[i];
+            }
+            sync_all<CLUSTER>();
+            if (f_bin == SMP_BINS) return f;
+            f.count = f_count;
+            f.above_count = f_above_count;
+            f.above_mass = f_above_mass;
+            if (level == 0) {
+                f.bin0 = (int)f_bin;
+            } else {
+                const u64 digit = (u64)((1 << width) - 1 - (int)f_bin);
+                f.prefix = f.shift == SMP_ORDER_BITS ? digit : ((f.prefix << width) | digit);
+                f.shift = to;
+            }
+            if (f.count <= SMP_CAP || f.shift == 0) return f;
+        }
+    };
+    // Ranks the gathered tokens (first CTA) and returns the order of the last one kept: the first
+    // k overall (k > 0), and with do_p of these the nucleus of mass x, or where x is 0 of
+    // ceil(p64 * mass of the k). above_*: what precedes all of them.
+    auto finish = [&](uint32_t above_count, u64 above_mass, uint32_t k, bool do_p, u64 p64, u64 x) -> u64 {
+        sync_all<CLUSTER>();                      // every CTA's entries have arrived
+        if (rank == 0) {
+            const int m = min((int)list_n, SMP_CAP);
+            constexpr int PER = SMP_CAP / THREADS;
+            u64 o[PER], before[PER], w[PER], km = 0;
+            uint32_t rk[PER];
+            bool keep[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = tid + i * THREADS;
+                o[i] = e < m ? list_o[e] : 0;
+                w[i] = e < m ? list_w[e] : 0;
+                before[i] = above_mass;
+                rk[i] = above_count;
+            }
+            for (int j = 0; j < m; ++j) {
+                const u64 oj = list_o[j], wj = list_w[j];
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (oj > o[i]) {
+                        rk[i] += 1;
+                        before[i] += wj;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                keep[i] = tid + i * THREADS < m && (k == 0 || rk[i] < k);
+                km += keep[i] ? w[i] : 0;
+            }
+            if (do_p) {
+                if (x == 0) {
+                    u64 total;
+                    block_scan_u64(km, red, total);
+                    total += above_mass;
+                    x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
+                    if (x == 0) x = 1;
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) keep[i] = keep[i] && before[i] < x;
+            }
+            u64 lowest = ~0ull;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (keep[i] && o[i] < lowest) lowest = o[i];
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                const u64 t = __shfl_xor_sync(0xffffffffu, lowest, s);
+                if (t < lowest) lowest = t;
+            }
+            __syncthreads();
+            if (lane == 0) red[warp] = lowest;
+            __syncthreads();
+            if (tid < (int)cs) {
+                for (int i = 0; i < THREADS / 32; ++i)
+                    if (red[i] < lowest) lowest = red[i];
+                if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), lowest);
+                else f_cut = lowest;
+            }
+        }
+        sync_all<CLUSTER>();
+        const u64 c = f_cut;
+        if (tid == 0) list_n = 0;
+        sync_all<CLUSTER>();
+        return c;
+    };
+    auto push = [&](float l, u64 o) {
+        const u64 w = wf.fixed(l);
+        if constexpr (CLUSTER) {
+            const uint32_t at = atom_peer_add(map_peer(smem_u32(&list_n), 0), 1u);
+            if (at < SMP_CAP) {
+                st_peer_u64(map_peer(smem_u32(&list_o[at]), 0), o);
+                st_peer_u64(map_peer(smem_u32(&list_w[at]), 0), w);
+            }
+        } else {
+            const uint32_t at = atomicAdd(&list_n, 1u);
+            if (at < SMP_CAP) {
+                list_o[at] = o;
+                list_w[at] = w;
+            }
+        }
+    };
+
+    if (greedy) {
+        u64 best = 0;
+        for (int s = tid; s < n; s += THREADS)
+            if (l_s[s] == mx) {
+                const u64 o = order_of(mx, base + s);
+                if (o > best) best = o;
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const u64 t = __shfl_xor_sync(0xffffffffu, best, o);
+            if (t > best) best = t;
+        }
+        __syncthreads();
+        if (lane == 0) red[warp] = best;
+        __syncthreads();
+        for (int i = 0; i < THREADS / 32; ++i)
+            if (red[i] > best) best = red[i];
+        if constexpr (CLUSTER) {
+            if (tid < (int)cs) st_peer_u64(map_peer(smem_u32(&x_arg[rank]), tid), best);
+            cluster_sync();
+            for (uint32_t i = 0; i < cs; ++i)
+                if (x_arg[i] > best) best = x_arg[i];
+        }
+        cut = best;
+    } else if (need_k || need_p) {
+        const u64 p64 = unit_fixed(p_in);
+        u64 x = 0;
+        bool p_left = need_p;
+        if (a.V <= SMP_CAP) {                     // all of them ranked, no search
+            for (int s = tid; s < n; s += THREADS)
+                if (l_s[s] != -INFINITY) push(l_s[s], order_of(l_s[s], base + s));
+            cut = finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0);
+            p_left = false;
+        } else if (need_k) {
+            // the whole top-k as one list where it fits, else only the set that holds its end
+            const Found f = search((uint32_t)k_in, 0, 0, x);
+            if (f.bin0 < SMP_BINS) {
+                const bool all = f.shift == SMP_ORDER_BITS && f.above_count + f.count <= SMP_CAP;
+                for (int s = tid; s < n; s += THREADS) {
+                    const float l = l_s[s];
+                    if (l == -INFINITY) continue;
+                    const u64 o = order_of(l, base + s);
+                    if (all ? bin0_of(l) <= f.bin0 : in_found(f, l, o)) push(l, o);
+                }
+                cut = finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0);
+                if (all) p_left = false;
+            }
+        }
+        if (p_left) {
+            const Found f = search(0, cut, p64, x);
+            for (int s = tid; s < n; s += THREADS) {
+                const float l = l_s[s];
+                if (l == -INFINITY) continue;
+                const u64 o = order_of(l, base + s);
+                if (o >= cut && in_found(f, l, o)) push(l, o);
+            }
+            cut = finish(f.above_count, f.above_mass, 0, true, p64, x);
+        }
+    }
+
+    // ---- the kept mass by ids: a warp owns consecutive slots ------------------------------------
+    const u64 mp = mp_in > 0.f && !greedy ? (u64)ceil((double)fminf(mp_in, 1.f) * (double)(1ull << SMP_FRAC)) : 0;
+    auto kept = [&](int s) -> u64 {
+        const float l = l_s[s];
+        if (l == -INFINITY || order_of(l, base + s) < cut) return 0;
+        const u64 w = wf.fixed(l);
+        return w >= mp ? w : 0;
+    };
+    const int seg = (n + THREADS - 1) / THREADS * 32;
+    {
+        u64 m = 0;
+        const int hi = min(n, (warp + 1) * seg);
+        for (int s = warp * seg + lane; s < hi; s += 32) m += kept(s);
+        m = warp_sum_u64(m);
+        if (lane == 0) warp_mass[warp] = m;
+    }
+    __syncthreads();
+    u64 mine = 0, total, before = 0;
+    for (int i = 0; i < THREADS / 32; ++i) mine += warp_mass[i];
+    total = mine;
+    if constexpr (CLUSTER) {
+        if (tid < (int)cs) st_peer_u64(map_peer(smem_u32(&x_sum[rank]), tid), mine);
+        cluster_sync();
+        total = 0;
+        for (uint32_t i = 0; i < cs; ++i) {
+            if (i < rank) before += x_sum[i];
+            total += x_sum[i];
+        }
+    }
+    // cumulative mass > u * total: integers, so > its floor
+    const u64 thr = __umul64hi(unit_fixed(a.uniforms[row]), total);
+    if (before <= thr && thr < before + mine) {
+        if (tid == 0) {
+            u64 c = before;
+            int w = 0;
+            while (w < THREADS / 32 - 1 && c + warp_mass[w] <= thr) c += warp_mass[w++];
+            pick_warp = w;
+            pick_before = c;
+        }
+        __syncthreads();
+        // the warp's slots, dealt out to the whole CTA in order
+        const int lo = pick_warp * seg, hi = min(n, lo + seg), per = (seg + THREADS - 1) / THREADS;
+        u64 m = 0;
+        for (int i = 0; i < per; ++i)
+            if (lo + tid * per + i < hi) m += kept(lo + tid * per + i);
+        u64 all;
+        u64 c = pick_before + block_scan_u64(m, red, all);
+        if (c <= thr && thr < c + m) {
+            int s = lo + tid * per;
+            for (;; ++s) {
+                const u64 w = kept(s);
+                if (thr < c + w) break;
+                c += w;
+            }
+            a.token[row] = base + s;
+            if (a.logprob) {
+                const double lw = l_s[s] == mx ? 0.0
+                                               : ((double)l_s[s] - (double)mx) / (greedy ? 1.0 : (double)temp);
+                a.logprob[row] = (float)(lw - log((double)total) + SMP_FRAC * 0.69314718055994530942);
+            }
+        }
+    }
+    if (a.probs) {
+        const float inv = (float)((double)(1ull << SMP_FRAC) / (double)total);
+        float* pr = a.probs + (size_t)row * a.ldp;
+        for (int s = tid; s < n; s += THREADS) {
+            const int id = base + s;
+            if (id >= 0 && id < a.V) pr[id] = kept(s) ? wf.real(l_s[s]) * inv : 0.f;
+        }
+    }
+    if constexpr (CLUSTER) cluster_sync();        // peers may still write into this CTA
+}
+
+// Cluster size: slices of at most 16384 slots (64 KiB, so that two CTAs share an SM), then more
+// CTAs a row while the rows alone leave SMs idle and a slice still has 4096 slots.
+int sample_cluster(int rows, int V) {
+    int cs = 1;
+    while (cs < SMP_MAX_CS && V > cs * 16384) cs *= 2;
+    while (cs < SMP_MAX_CS && (long long)rows * cs < 2 * 152 && V > cs * 4096) cs *= 2;
+    return cs;
+}
+
+template <typename T, int THREADS, bool CLUSTER>
+cudaError_t sample_launch(const SampleArgs& a, int rows, int cs, size_t smem, cudaStream_t stream) {
+    auto kernel = sample_kernel<T, THREADS, CLUSTER>;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows * cs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T>
+cudaError_t sample_dispatch(SampleArgs a, int rows, cudaStream_t stream) {
+    constexpr int VEC = 16 / sizeof(T);
+    const int cs = sample_cluster(rows, a.V);
+    const int grans = (VEC - 1 + a.V + VEC - 1) / VEC;
+    a.slice = (grans + cs - 1) / cs * VEC;
+    const size_t smem = (size_t)a.slice * 4 + (a.V <= SMP_CAP ? (size_t)SMP_CAP * 16 : (size_t)SMP_BINS * 16);
+    if (cs > 1) return sample_launch<T, 512, true>(a, rows, cs, smem, stream);
+    if (a.V > 2048) return sample_launch<T, 512, false>(a, rows, 1, smem, stream);
+    return sample_launch<T, 256, false>(a, rows, 1, smem, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const evs_sample_args& c, cudaStream_t stream) {
+    SampleArgs a{c.logits, c.ld, c.probs_ld, c.vocab, c.temperature, c.top_p, c.min_p, c.uniforms, c.top_k,
+                 c.token, c.logprob, c.probs, c.flags, 0};
+    return c.dtype == EVS_DTYPE_BF16 ? sample_dispatch<bf16>(a, c.rows, stream)
+                                     : sample_dispatch<float>(a, c.rows, stream);
+}
+
+}  // namespace evs
+
+extern "C" evs_status evs_sample(const evs_sample_args* c, void* stream) {
+    using namespace evs;
+    if (!c || c->rows < 0 || c->vocab < 1 || c->vocab > SMP_MAX_V || c->ld < c->vocab) return EVS_ERR_INVALID_ARG;
+    if (c->dtype != EVS_DTYPE_F32 && c->dtype != EVS_DTYPE_BF16) return EVS_ERR_INVALID_ARG;
+    if (c->rows == 0) return EVS_OK;
+    if (c->rows > (1 << 24) || !c->logits || !c->token || !c->uniforms) return EVS_ERR_INVALID_ARG;
+    if ((uintptr_t)c->logits % (c->dtype == EVS_DTYPE_BF16 ? 2 : 4)) return EVS_ERR_INVALID_ARG;
+    if (c->probs && c->probs_ld < c->vocab) return EVS_ERR_INVALID_ARG;
+    return launch_sample(*c, (cudaStream_t)stream) == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+}

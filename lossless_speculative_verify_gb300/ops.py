@@ -1,0 +1,254 @@
+"""Stand-alone operators of the library on torch tensors: attention over a shared prefix, the
+filtered draw, the short causal convolution and the selective scan.
+
+Each function checks its arguments, fills the argument struct of one entry point (include/evs.h
+states the mathematics) and enqueues it on the current stream of the tensors' device, like any
+torch operator: outputs and workspaces come from torch's allocator, calls may be captured into
+CUDA graphs, nothing synchronises. Inputs that are not what an operator takes raise ValueError
+before anything is enqueued. ``flags`` is an int32 tensor of one element that collects
+EVS_FLAG_* bits.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _lib as L
+
+_DT = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vec(name, t, dtype, shape, dev):
+    """Address of a contiguous tensor of the given type and shape on dev, or None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and
+            t.is_contiguous() and t.device == dev):
+        raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}")
+    return t.data_ptr()
+
+
+def _rows3(name, t, dtype, shape, dev, written=False):
+    """Strides (row, sequence) of a [batch, tokens, n] tensor whose last dimension is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    b, n, w = shape
+    sq, ld, one = t.stride()
+    ld = ld if n > 1 else w
+    sq = sq if b > 1 else 0
+    _need(one == 1 or w == 1, f"{name}: the last dimension has to be contiguous")
+    _need(ld >= w, f"{name}: rows overlap")
+    _need(not written or b <= 1 or sq >= w, f"{name}: sequences overlap")
+    return ld, sq
+
+
+def _enqueue(fn, where, args, dev):
+    if torch.cuda.current_device() == dev.index:
+        st = fn(C.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(C.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+    L.check(st, where)
+
+
+def _device(name, t):
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: want a CUDA tensor")
+    return t.device
+
+
+def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, *, return_logprob=False,
+           return_probs=False, out=None, flags=None):
+    """Draw one token per row of ``logits`` [rows, vocab] (fp32 or bf16, any row stride).
+
+    uniforms [rows] fp32 in [0, 1); temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, each on the
+    device or None (off). Temperatures that are not above zero take the largest logit. Returns the tokens
+    [rows] int32, or a list [tokens, logprob fp32 [rows] if asked, probabilities fp32 [rows, vocab] if asked];
+    the probabilities are the distribution that was drawn from (what a verify needs as the draft's q). A row
+    with every token ruled out gives -1."""
+    dev = _device("logits", logits)
+    _need(logits.dim() == 2 and logits.dtype in _DT, "logits: want fp32 or bf16 [rows, vocab]")
+    R, V = logits.shape
+    _need(1 <= V <= 1 << 18, "logits: vocabulary of 1 to 262144")
+    _need(logits.stride(1) == 1 or V == 1, "logits: the vocabulary has to be contiguous")
+    ld = logits.stride(0) if R > 1 else V
+    _need(ld >= V, "logits: rows overlap")
+    _need(uniforms is not None, "uniforms: missing")
+    token = torch.empty(R, dtype=torch.int32, device=dev) if out is None else out
+    logprob = torch.empty(R, dtype=torch.float32, device=dev) if return_logprob else None
+    probs = torch.empty(R, V, dtype=torch.float32, device=dev) if return_probs else None
+    f32 = torch.float32
+    a = L.SampleArgs(R, V, _DT[logits.dtype], ld, logits.data_ptr(), _vec("temperature", temperature, f32, (R,), dev),
+                     _vec("top_k", top_k, torch.int32, (R,), dev), _vec("top_p", top_p, f32, (R,), dev),
+                     _vec("min_p", min_p, f32, (R,), dev), _vec("uniforms", uniforms, f32, (R,), dev),
+                     _vec("out", token, torch.int32, (R,), dev), _p(logprob), _p(probs), V,
+                     _vec("flags", flags, torch.int32, (1,), dev))
+    _enqueue(L.load().evs_sample, "evs_sample", a, dev)
+    if logprob is None and probs is None:
+        return token
+    return [t for t in (token, logprob, probs) if t is not None]
+
+
+def causal_conv(x, weight, bias=None, *, tail=None, tail_out=None, lens=None, silu=True, out=None, output=True,
+                flags=None):
+    """Short causal convolution of every channel of x [batch, tokens, width] (fp32 or bf16).
+
+    weight [width, taps] fp32 (2 to 16 taps; weight[c, j] multiplies x[t - j]), bias [width] fp32 or None; tail
+    and tail_out [batch, taps - 1, width] fp32, oldest first: the inputs before the first token, and the last
+    ones after lens[b] tokens (they may be one tensor). lens [batch] int32 or None. Rows past a sequence's
+    length are left as they were in ``out``. Returns out, or None with output=False (only the tail moves on:
+    slicing at position k is lens = k + 1)."""
+    dev = _device("x", x)
+    _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
+    B, T, D = x.shape
+    _need(isinstance(weight, torch.Tensor) and weight.dim() == 2 and 2 <= weight.shape[1] <= 16,
+          "weight: want [width, 2..16]")
+    taps = weight.shape[1]
+    x_ld, x_sq = _rows3("x", x, x.dtype, (B, T, D), dev)
+    y_ld = y_sq = 0
+    y = None
+    if output:
+        y = torch.empty(B, T, D, dtype=x.dtype, device=dev) if out is None else out
+        y_ld, y_sq = _rows3("out", y, x.dtype, (B, T, D), dev, written=True)
+        _need(y.data_ptr() != x.data_ptr() or y.numel() == 0, "out: may not be x")
+    else:
+        _need(out is None and tail_out is not None, "output=False wants tail_out and no out")
+    f32 = torch.float32
+    a = L.ConvArgs(B, T, D, taps, _DT[x.dtype], 1 if silu else 0, x.data_ptr(), x_ld, x_sq, _p(y), y_ld, y_sq,
+                   _vec("weight", weight, f32, (D, taps), dev), _vec("bias", bias, f32, (D,), dev),
+                   _vec("tail", tail, f32, (B, taps - 1, D), dev),
+                   _vec("tail_out", tail_out, f32, (B, taps - 1, D), dev),
+                   _vec("lens", lens, torch.int32, (B,), dev), _vec("flags", flags, torch.int32, (1,), dev))
+    if (T == 0 or B == 0) and tail_out is None:
+        return y
+    _enqueue(L.load().evs_causal_conv, "evs_causal_conv", a, dev)
+    return y
+
+
+def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, state_out=None, lens=None,
+                   softplus=True, out=None, output=True, flags=None):
+    """Selective scan over x [batch, tokens, width] with step sizes dt (same shape), input and output weights B, C
+    [batch, tokens, states] and gate z (like x, or None), all fp32 or all bf16; A [width, states] fp32, states
+    4, 8, 16 or 32; D, dt_bias [width] fp32 or None; state, state_out [batch, width, states] fp32 or None (they
+    may be one tensor); lens [batch] int32 or None. Rows past a sequence's length are left as they were in
+    ``out``. Returns out, or None with output=False (only the state moves on)."""
+    dev = _device("x", x)
+    _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
+    Bn, T, W = x.shape
+    _need(isinstance(A, torch.Tensor) and A.dim() == 2 and A.shape[1] in (4, 8, 16, 32), "A: want [width, 4|8|16|32]")
+    N = A.shape[1]
+    x_ld, x_sq = _rows3("x", x, x.dtype, (Bn, T, W), dev)
+    dt_ld, dt_sq = _rows3("dt", dt, x.dtype, (Bn, T, W), dev)
+    z_ld, z_sq = (0, 0) if z is None else _rows3("z", z, x.dtype, (Bn, T, W), dev)
+    b_ld, b_sq = _rows3("B", B, x.dtype, (Bn, T, N), dev)
+    c_ld, c_sq = _rows3("C", C, x.dtype, (Bn, T, N), dev)
+    y_ld = y_sq = 0
+    y = None
+    if output:
+        y = torch.empty(Bn, T, W, dtype=x.dtype, device=dev) if out is None else out
+        y_ld, y_sq = _rows3("out", y, x.dtype, (Bn, T, W), dev, written=True)
+        for name, t in (("x", x), ("dt", dt), ("z", z)):
+            _need(t is None or y.data_ptr() != t.data_ptr() or y.numel() == 0, f"out: may not be {name}")
+    else:
+        _need(out is None and state_out is not None, "output=False wants state_out and no out")
+    f32 = torch.float32
+    for name, t in (("A", A), ("state", state), ("state_out", state_out)):
+        _need(t is None or t.data_ptr() % 16 == 0, f"{name}: has to start on 16 bytes")
+    a = L.ScanArgs(Bn, T, W, N, _DT[x.dtype], 1 if softplus else 0, x.data_ptr(), x_ld, x_sq, dt.data_ptr(), dt_ld,
+                   dt_sq, _p(z), z_ld, z_sq, B.data_ptr(), b_ld, b_sq, C.data_ptr(), c_ld, c_sq, _p(y), y_ld, y_sq,
+                   _vec("A", A, f32, (W, N), dev), _vec("D", D, f32, (W,), dev),
+                   _vec("dt_bias", dt_bias, f32, (W,), dev), _vec("state", state, f32, (Bn, W, N), dev),
+                   _vec("state_out", state_out, f32, (Bn, W, N), dev),
+                   _vec("lens", lens, torch.int32, (Bn,), dev), _vec("flags", flags, torch.int32, (1,), dev))
+    if (T == 0 or Bn == 0) and state_out is None:
+        return y
+    _enqueue(L.load().evs_selective_scan, "evs_selective_scan", a, dev)
+    return y
+
+
+def _kv(name, t, dtype, shape, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    _need(t.stride(-1) == 1, f"{name}: the head dimension has to be contiguous")
+
+
+def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_block=None, v_block=None, *, scale=None,
+                            out=None, return_lse=False, flags=None):
+    """Attention of q [batch, candidates, block, heads, dh] over rows that the batch shares, k_prefix / v_prefix
+    [kv_heads, P, dh], each sequence's own rows k_own / v_own [batch, kv_heads, capacity, dh] up to own_len [batch]
+    (int32), and the block rows k_block / v_block [batch, candidates, kv_heads, block, dh] up to the query's own
+    position. Without k_block (one candidate) the block rows are own rows own_len[b] + j.
+
+    K and V are fp32 or bf16 with any strides but the last (K and V of a pair alike); q is of their type, or
+    fp32. heads is a multiple of kv_heads; dh 16, 32, 64 or 128. Returns out (the type of K), or [out, lse fp32
+    [batch, candidates, block, heads]]."""
+    dev = _device("q", q)
+    _need(q.dim() == 5 and q.dtype in _DT, "q: want fp32 or bf16 [batch, candidates, block, heads, dh]")
+    B, Cn, T, H, dh = q.shape
+    _need(isinstance(k_prefix, torch.Tensor) and k_prefix.dim() == 3 and k_prefix.dtype in _DT,
+          "k_prefix: want fp32 or bf16 [kv_heads, P, dh]")
+    G, P, _ = k_prefix.shape
+    dt = k_prefix.dtype
+    _need(q.dtype == dt or q.dtype == torch.float32, "q: of the type of K, or fp32")
+    _need(dh in (16, 32, 64, 128) and G > 0 and H > 0 and H % G == 0,
+          "head dimension 16, 32, 64 or 128, heads a multiple of kv_heads")
+    _need(1 <= Cn <= 64 and 1 <= T <= 128 and B <= 1024, "at most 1024 sequences, 64 candidates, 128 block positions")
+    _need(isinstance(k_own, torch.Tensor) and k_own.dim() == 4, "k_own: want [batch, kv_heads, capacity, dh]")
+    S = k_own.shape[2]
+    for name, t, shape in (("k_prefix", k_prefix, (G, P, dh)), ("v_prefix", v_prefix, (G, P, dh)),
+                           ("k_own", k_own, (B, G, S, dh)), ("v_own", v_own, (B, G, S, dh))):
+        _kv(name, t, dt, shape, dev)
+    ps, os_ = k_prefix.stride(), k_own.stride()
+    _need(ps == v_prefix.stride() and os_ == v_own.stride(), "K and V: want equal strides")
+    _need((k_block is None) == (v_block is None), "k_block and v_block go together")
+    if k_block is not None:
+        _kv("k_block", k_block, dt, (B, Cn, G, T, dh), dev)
+        _kv("v_block", v_block, dt, (B, Cn, G, T, dh), dev)
+        bs = k_block.stride()
+        _need(bs == v_block.stride(), "K and V: want equal strides")
+        _need(Cn == 1 or B == 1 or bs[0] == Cn * bs[1], "k_block: sequences and candidates have to be evenly spaced")
+        b_row, b_head, b_cand = (bs[3] if T > 1 else dh), bs[2], bs[1] if Cn > 1 else bs[0]
+    else:
+        _need(Cn == 1 and S > 0, "block rows in k_own want one candidate")
+        b_row = b_head = b_cand = 0
+
+    def flat(name, t, dtype):
+        """Row stride of a [batch, candidates, block, heads, dh] tensor whose rows are evenly spaced."""
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == (B, Cn, T, H, dh) and
+                t.device == dev):
+            raise ValueError(f"{name}: want {dtype} {(B, Cn, T, H, dh)} on {dev}")
+        s = t.stride()
+        _need(s[4] == 1 and (H == 1 or s[3] == dh), f"{name}: heads have to be contiguous")
+        ld = s[2] if T > 1 else s[1] if Cn > 1 else s[0] if B > 1 else H * dh
+        _need(ld >= H * dh and (Cn == 1 or s[1] == T * ld) and (B == 1 or s[0] == Cn * T * ld),
+              f"{name}: rows have to be evenly spaced")
+        return ld
+
+    q_ld = flat("q", q, q.dtype)
+    o = torch.empty(B, Cn, T, H, dh, dtype=dt, device=dev) if out is None else out
+    o_ld = flat("out", o, dt)
+    _need(scale is None or scale > 0.0, "scale: above zero")
+    lse = torch.empty(B, Cn, T, H, dtype=torch.float32, device=dev) if return_lse else None
+    a = L.SharedAttnArgs(B, Cn, T, H, G, dh, _DT[dt], _DT[q.dtype], P, S, 0, 0.0 if scale is None else scale,
+                         q.data_ptr(), q_ld, k_prefix.data_ptr(), v_prefix.data_ptr(), ps[1] if P > 1 else dh, ps[0],
+                         k_own.data_ptr(), v_own.data_ptr(), os_[2] if S > 1 else dh, os_[1], os_[0],
+                         _vec("own_len", own_len, torch.int32, (B,), dev), _p(k_block), _p(v_block), b_row, b_head,
+                         b_cand, o.data_ptr(), o_ld, _p(lse), None, 0, _vec("flags", flags, torch.int32, (1,), dev))
+    _need(own_len is not None, "own_len: missing")
+    if B > 0:
+        lib = L.load()
+        n = int(lib.evs_shared_attention_workspace(C.byref(a)))
+        _need(n > 0, "sizes that the operator does not take")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        a.workspace, a.ws_bytes = ws.data_ptr(), n
+        _enqueue(lib.evs_shared_attention, "evs_shared_attention", a, dev)
+    return o if lse is None else [o, lse]
