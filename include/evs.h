@@ -347,8 +347,8 @@ evs_status evs_projection_noalloc_flags(uint32_t* flags, int32_t clear, void* st
  *   keep the first k; of these the shortest prefix whose mass before a token is below p times
  *   their mass (at least one token); of these the tokens with w_i >= m * max w;
  *   token = the smallest id whose cumulative kept mass over ascending ids exceeds u * total.
- * The weights are summed in 64-bit fixed point: the same inputs give the same token whatever
- * the launch, and the order of equal logits is that of their ids. NaN and -inf logits are ruled
+ * The weights are summed in 64-bit fixed point (2^-44 of the largest; smaller ones are 0): the
+ * same inputs give the same token whatever the launch, and equal logits go by their ids. NaN and -inf logits are ruled
  * out; where the largest logit is +inf, the +inf tokens share the mass. A row with every token
  * ruled out gives token -1, logprob -inf, zero probabilities and EVS_FLAG_EMPTY_ROW. */
 typedef struct {
@@ -383,8 +383,8 @@ evs_status evs_decode_filtered(evs_handle* h, const int32_t* tokens, const evs_s
  * exponentials. The block rows lie in k_block / v_block, or (both NULL, n_cand 1) in the own rows
  * behind the readable ones, row own_len[b] - own_skip + j.
  * Lengths outside [0, own_max] are clamped (EVS_FLAG_BAD_LEN); block rows past own_max are left
- * out (EVS_FLAG_KV_OVERFLOW); a query left without any key gives o = 0 and lse = -inf. Rows that
- * no query reads may hold anything. K, V and o are dtype; q is q_dtype, rounded to bf16 where the
+ * out (EVS_FLAG_KV_OVERFLOW). A query whose every score is -inf gives o = 0 and lse = -inf. Rows
+ * that no query reads may hold anything. K, V and o are dtype; q is q_dtype, rounded to bf16 where the
  * products run on tensor cores (dtype bf16, head_dim 64 or 128, rows on 16 bytes); statistics and
  * accumulators are fp32, softmax weights enter the tensor-core products as bf16. */
 typedef struct {

@@ -7,6 +7,8 @@
 //
 // Two launches: partial sums (o unnormalised, m, l) per run of keys, then a combine that merges
 // a query's partials, adds its block rows and normalises.
+#include <cudaTypedefs.h>
+
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -31,6 +33,10 @@ struct SharedArgs {
     float *sh_o, *own_o;       // [segment][slot][rows][dh]
     float2 *sh_ml, *own_ml;    // [segment][slot][rows] (m, l), natural units
     int sh_rows, sh_tiles, sh_slots, own_rows, own_tiles, own_slots;
+    int tensor;                // the tensor-core kernel's partials: slots by its runs of tiles
+    int sh_pair, own_pair;     // 1: 256-row segments, a row tile per lane; 0: a lane per key tile
+    int* plan;                 // tiles per run, then the running sum of own tiles per sequence
+    int q_vec, stages;
 };
 
 // fp32 problems keep the full precision of the exponential
@@ -161,6 +167,455 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
 }
 
 // =========================================================================================
+// Partials on the tensor cores (bf16, head width 64 or 128).
+//
+// Work: 128-key tiles of every segment (a K/V head of the prefix with up to 256 query rows, or
+// of one sequence's own rows) laid end to end; each of up to 152 persistent CTAs takes an equal
+// run of tiles, so ragged lengths balance on the device. A run may cross segments; each piece of
+// a segment leaves its own partials.
+//
+// Two lanes of work share a CTA, each with its own score, weight and output columns in tensor
+// memory and its own four softmax warps. In a segment of more than 128 rows the lanes are two row
+// tiles and each K/V tile that TMA brings serves both; otherwise they are alternate key tiles of
+// the same rows. While one lane's softmax runs, the tensor core works for the other:
+//   S[q][key] = Q K^T (fp32, 128 columns) -> registers, one thread a row: running maximum, exp2,
+//   sum -> bf16 weights back over the first half of S's columns -> O += P V with P read from
+//   tensor memory, V MN-major from shared memory.
+// The running maximum moves only when it grows by more than 2^8, as few rescales of O as that.
+// A tile that the keys end in takes only the 16-key steps that hold keys, the rows behind them in
+// the last step cleared in shared memory (they may hold anything, NaN included).
+//
+// Tensor memory, columns: S/P of lane 0 and 1 at 0 and 128, O at 256 and 384.
+// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warp 9: MMA.
+// =========================================================================================
+constexpr int ST_KEYS = 128;
+constexpr int ST_THREADS = 320;
+constexpr float ST_RESCALE_LOG2 = 8.f;
+
+__device__ __forceinline__ uint32_t st_sw128(int row, int chunk16) {
+    return (uint32_t)row * 128u + ((uint32_t)(chunk16 ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t st_pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One CTA's share of a segment: tiles t0 .. t0 + n - 1 of `keys` keys.
+struct Piece {
+    int sh, b, g, rt, t0, n, keys, slot, seg;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(ST_THREADS, 1)
+shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
+                 const __grid_constant__ CUtensorMap tmKO, const __grid_constant__ CUtensorMap tmVO, SharedArgs a) {
+    constexpr int HALVES = DH / 64;
+    constexpr int HALF = ST_KEYS * 128;          // 64 columns of a tile
+    constexpr int TILE = HALF * HALVES;
+    constexpr uint32_t O_COL = 256;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t tmem_slot[1];
+    __shared__ volatile int abort_flag[1];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t* sQ = smem;                                        // [2 lanes][halves][128 rows][128 B]
+    uint8_t* ring = sQ + 2 * TILE;                             // [stages]
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)a.stages * TILE);
+    uint64_t* empty = full + a.stages;
+    uint64_t* s_full = empty + a.stages;                       // [2] scores of a tile in tensor memory
+    uint64_t* p_full = s_full + 2;                             // [2] weights of a tile there
+    uint64_t* pv_done = p_full + 2;                            // [2] P V of a tile complete
+    uint64_t* q_ready = pv_done + 2;                           // [2] Q of a piece staged
+    uint64_t* drain = q_ready + 2;
+    int* pre = reinterpret_cast<int*>(drain + 1);              // [B + 1] own tiles before sequence b
+    int* len = pre + a.B + 1;                                  // [B]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_trigger();
+    pdl_wait();
+    for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
+    if (tid == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&q_ready[i], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = b < a.B ? (len[b] + ST_KEYS - 1) / ST_KEYS : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < a.B) pre[b + 1] = run + x;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ntp = (a.P + ST_KEYS - 1) / ST_KEYS;
+    const int sh_total = a.G * a.sh_tiles * ntp, per_b = a.G * a.own_tiles;
+    const int total = sh_total + per_b * pre[a.B];
+    const int W = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const int lo = min(total, W * (int)blockIdx.x), hi = min(lo + W, total);
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= a.B; b += ST_THREADS) a.plan[1 + b] = pre[b];
+        if (tid == 0) a.plan[0] = W;
+    }
+    // the piece that starts at position pos, the same for every role
+    auto piece = [&](int pos) -> Piece {
+        Piece p;
+        int start, nt;
+        if (pos < sh_total) {
+            p.sh = 1;
+            p.b = 0;
+            p.seg = pos / ntp;
+            p.g = p.seg / a.sh_tiles;
+            p.rt = p.seg % a.sh_tiles;
+            start = p.seg * ntp;
+            nt = ntp;
+            p.keys = a.P;
+        } else {
+            const int q = pos - sh_total;
+            int b0 = 0, b1 = a.B - 1;             // the last b with per_b * pre[b] <= q
+            while (b0 < b1) {
+                const int mid = (b0 + b1 + 1) >> 1;
+                if (per_b * pre[mid] <= q) b0 = mid; else b1 = mid - 1;
+            }
+            nt = pre[b0 + 1] - pre[b0];
+            const int r = (q - per_b * pre[b0]) / nt;
+            p.sh = 0;
+            p.b = b0;
+            p.g = r / a.own_tiles;
+            p.rt = r % a.own_tiles;
+            p.seg = b0 * per_b + r;
+            start = sh_total + per_b * pre[b0] + r * nt;
+            p.keys = len[b0];
+        }
+        p.t0 = pos - start;
+        p.n = min(nt - p.t0, hi - pos);
+        p.slot = (int)blockIdx.x - start / W;
+        return p;
+    };
+    // tiles of lane L in a piece
+    auto lane_tiles = [&](const Piece& p, int L) { return (p.sh ? a.sh_pair : a.own_pair) ? p.n : (p.n + 1 - L) / 2; };
+
+    if (warp == 8) {
+        int issued = 0;
+        if (lane == 0) {
+            // ---- TMA, in the order of use. Row lanes: K0 V0 K1 V1 ...; key lanes: K0 K1 V0 K2 V1 K3 ...
+            const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
+            bool ok = true;
+            for (int pos = lo; pos < hi && ok;) {
+                const Piece p = piece(pos);
+                const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
+                auto load = [&](const CUtensorMap* m, int t) {
+                    const int s = issued % a.stages;
+                    if (issued >= a.stages && !mbar_wait(&empty[s], ((uint32_t)(issued / a.stages) & 1u) ^ 1u)) {
+                        ok = false;
+                        return;
+                    }
+                    uint8_t* dst = ring + (size_t)s * TILE;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)TILE);
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf)
+                        tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, &full[s], pol);
+                    ++issued;
+                };
+                const CUtensorMap *mk = p.sh ? &tmKP : &tmKO, *mv = p.sh ? &tmVP : &tmVO;
+                const int ahead = pair ? 1 : 2;
+                for (int t = 0; t < min(ahead, p.n) && ok; ++t) load(mk, t);
+                for (int t = 0; t < p.n && ok; ++t) {
+                    load(mv, t);
+                    if (ok && t + ahead < p.n) load(mk, t + ahead);
+                }
+                pos += p.n;
+            }
+            if (!ok) *abort_flag = 1;
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        if (*abort_flag && lane == 0) {
+            // loads in flight into this CTA's shared memory end before it does (bounded)
+            for (int j = issued > a.stages ? issued - a.stages : 0; j < issued; ++j)
+                mbar_wait(&full[j % a.stages], (uint32_t)(j / a.stages) & 1u);
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+        return;
+    }
+    if (warp == 9) {
+        // ---- MMA: every lane of the warp follows, one issues
+        const uint32_t id_s = idesc_bf16_f32(128, ST_KEYS);
+        const uint32_t id_o = idesc_bf16_f32_bmn(128, DH);
+        const uint32_t q0 = smem_u32(sQ);
+        int base = 0;                  // ring steps of earlier pieces
+        int cnt[2] = {0, 0}, qn[2] = {0, 0};
+        bool ok = true;
+        for (int pos = lo; pos < hi && ok;) {
+            const Piece p = piece(pos);
+            const bool pair = p.sh ? a.sh_pair : a.own_pair;
+            const int n0 = lane_tiles(p, 0), n1 = lane_tiles(p, 1);
+            // ring step of the K and V tile t of the piece
+            auto k_step = [&](int t) { return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1)); };
+            auto v_step = [&](int t) {
+                return base + (pair ? min(2 * t + 1, 2 * p.n - 1) : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
+            };
+            auto wait_full = [&](int step) {
+                const bool r = mbar_wait(&full[step % a.stages], (uint32_t)(step / a.stages) & 1u);
+                return __all_sync(0xffffffffu, r) != 0;
+            };
+            auto score = [&](int L, int t, bool last_use) {
+                const int st = k_step(t);
+                if (!wait_full(st)) { ok = false; return; }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t k0 = smem_u32(ring + (size_t)(st % a.stages) * TILE), qa = q0 + L * TILE;
+#pragma unroll
+                    for (int kk = 0; kk < DH / 16; ++kk) {
+                        const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32u;
+                        tc_mma_f16(tmem + (uint32_t)L * 128u, smem_desc_sw128(qa + off), smem_desc_sw128(k0 + off),
+                                   id_s, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full[L]);
+                    if (last_use) tc_commit(&empty[st % a.stages]);
+                }
+                __syncwarp();
+            };
+            auto weigh = [&](int L, int t, bool first, bool first_use, bool last_use) {   // O += P V
+                const int st = v_step(t);
+                if (!__all_sync(0xffffffffu, mbar_wait(&p_full[L], (uint32_t)cnt[L] & 1u))) { ok = false; return; }
+                ++cnt[L];
+                if (!wait_full(st)) { ok = false; return; }
+                const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+                uint8_t* v = ring + (size_t)(st % a.stages) * TILE;
+                if (first_use && (nv & 15)) {
+                    // rows nv .. of the last 16-key step: clear them
+                    const int rows = 16 - (nv & 15);
+                    for (int e = lane; e < rows * 8 * HALVES; e += 32) {
+                        const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
+                        *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t v0 = smem_u32(v);
+                    const int steps = (nv + 15) / 16;
+                    for (int kk = 0; kk < steps; ++kk)
+                        tc_mma_f16_ta(tmem + O_COL + (uint32_t)L * 128u, tmem + (uint32_t)L * 128u + (uint32_t)kk * 8u,
+                                      smem_desc_sw128_mn(v0 + (uint32_t)kk * 16u * 128u, HALF), id_o,
+                                      (!first || kk > 0) ? 1u : 0u);
+                    tc_commit(&pv_done[L]);
+                    if (last_use) tc_commit(&empty[st % a.stages]);
+                }
+                __syncwarp();
+            };
+            for (int L = 0; L < 2 && ok; ++L) {
+                if ((L ? n1 : n0) == 0) continue;
+                if (!__all_sync(0xffffffffu, mbar_wait(&q_ready[L], (uint32_t)qn[L] & 1u))) { ok = false; break; }
+                ++qn[L];
+                tc_fence_after();
+                score(L, pair ? 0 : L, !pair || L == 1);
+            }
+            for (int s = 0; s < n0 && ok; ++s) {
+                for (int L = 0; L < 2 && ok; ++L) {
+                    const int nl = L ? n1 : n0;
+                    if (s < nl) weigh(L, pair ? s : 2 * s + L, s == 0, !pair || L == 0, !pair || L == 1);
+                    if (ok && s + 1 < nl) score(L, pair ? s + 1 : 2 * (s + 1) + L, !pair || L == 1);
+                }
+            }
+            base += 2 * p.n;
+            pos += p.n;
+        }
+        if (lane == 0) {
+            if (!ok) *abort_flag = 1;
+            tc_commit(drain);                     // nothing of this CTA's in tensor memory in flight
+            mbar_wait(drain, 0);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        return;
+    }
+    // ---- softmax of lane L: thread = row r of the lane's tile
+    const int L = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t s_col = (uint32_t)L * 128u, o_col = O_COL + (uint32_t)L * 128u;
+    const int grp = a.H / a.G;
+    const float sl = a.scale * 1.4426950408889634f;
+    int cnt = 0;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+        const Piece p = piece(pos);
+        const bool pair = p.sh ? a.sh_pair : a.own_pair;
+        const int nl = lane_tiles(p, L);
+        const int all_rows = p.sh ? a.B * a.C * a.T * grp : a.C * a.T * grp;
+        const int seg_rows = p.sh ? a.sh_rows : a.own_rows;
+        const int r_seg = pair ? L * 128 + r : r;                       // row in the segment
+        const int r_all = p.rt * seg_rows + r_seg;                      // and of the head
+        const bool live = r_seg < seg_rows && r_all < all_rows;
+        const bool work = __any_sync(0xffffffffu, live);
+        float m_run = -INFINITY, l = 0.f;
+        if (nl > 0) {
+            if (work) {
+                // Q row -> bf16, K-major, 128-byte swizzle
+                const int64_t m = p.sh ? r_all / grp : (int64_t)p.b * a.C * a.T + r_all / grp;
+                const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all % grp) * DH;
+#pragma unroll
+                for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll 4
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (live) {
+                            const int64_t e = at + hf * 64 + c * 8;
+                            if (a.q_bf16 && a.q_vec) {
+                                u = *reinterpret_cast<const uint4*>((const bf16*)a.q + e);
+                            } else {
+                                float x[8];
+                                if (a.q_vec) {
+                                    const float4 x0 = *reinterpret_cast<const float4*>((const float*)a.q + e);
+                                    const float4 x1 = *reinterpret_cast<const float4*>((const float*)a.q + e + 4);
+                                    x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
+                                    x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
+                                } else {
+                                    for (int j = 0; j < 8; ++j) x[j] = load_q(a, e + j);
+                                }
+                                u = make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]), st_pack(x[4], x[5]),
+                                               st_pack(x[6], x[7]));
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(sQ + L * TILE + hf * HALF + st_sw128(r, c)) = u;
+                    }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[L]);
+        }
+        for (int s = 0; s < nl; ++s) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[L], (uint32_t)cnt & 1u))) { ok = false; break; }
+            if (work) {
+                tc_fence_after();
+                uint32_t x[8][16];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) tmem_ld16_issue(trow + s_col + (uint32_t)(c * 16), x[c]);
+                tmem_wait_ld();
+                const int t = pair ? s : 2 * s + L;
+                const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+                if (nv < ST_KEYS) {               // keys behind the last one: no weight
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c * 16 + j >= nv) x[c][j] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[c][j]));
+                const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl);
+                const bool move = m_new > m_run + ST_RESCALE_LOG2 || (m_run == -INFINITY && m_new > -INFINITY);
+                if (s > 0 && __any_sync(0xffffffffu, move)) {
+                    // rescale the rows of O once P V of the previous tile is in it
+                    if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[L], (uint32_t)(cnt - 1) & 1u))) { ok = false; break; }
+                    tc_fence_after();
+                    const float f = move ? ex2_approx_ftz(m_run - m_new) : 1.f;
+#pragma unroll
+                    for (int c = 0; c < DH / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16_issue(trow + o_col + (uint32_t)(c * 16), o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st16(trow + o_col + (uint32_t)(c * 16), o);
+                    }
+                    l *= f;
+                }
+                if (move) m_run = m_new;
+                const float mb = m_run == -INFINITY ? 0.f : m_run;   // only -inf scores so far: weights 0
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {     // 32 keys: 16 columns of weights
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float e0 = ex2_approx_ftz(fmaf(__uint_as_float(x[2 * c + j / 8][(2 * j) & 15]), sl, -mb));
+                        const float e1 = ex2_approx_ftz(fmaf(__uint_as_float(x[2 * c + j / 8][(2 * j + 1) & 15]), sl, -mb));
+                        ls[j & 1] += e0;
+                        ls[2 + (j & 1)] += e1;
+                        w[j] = st_pack(e0, e1);
+                    }
+                    tmem_st16(trow + s_col + (uint32_t)(c * 16), w);
+                }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[L]);
+            ++cnt;
+        }
+        // ---- the piece's partials: o, then (m, l)
+        if (ok && nl > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[L], (uint32_t)(cnt - 1) & 1u))) ok = false;
+        tc_fence_after();
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
+        }
+        if (work) {
+            const int slot = pair ? p.slot : 2 * p.slot + L, slots = p.sh ? a.sh_slots : a.own_slots;
+            const int64_t row = ((int64_t)p.seg * slots + slot) * seg_rows + r_seg;
+            if (ok && nl > 0) {
+                float* dst = (p.sh ? a.sh_o : a.own_o) + row * DH;
+#pragma unroll
+                for (int c = 0; c < DH / 16; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16_issue(trow + o_col + (uint32_t)(c * 16), o);
+                    tmem_wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4*>(dst + c * 16 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+            }
+            if (live)
+                (p.sh ? a.sh_ml : a.own_ml)[row] =
+                    ok && nl > 0 ? make_float2(m_run * 0.6931471805599453f, l) : make_float2(-INFINITY, 0.f);
+        }
+        tc_fence_before();                        // these reads precede the next piece's products
+        pos += p.n;
+    }
+    tc_fence_before();
+    __syncthreads();
+}
+
+// =========================================================================================
 // Combine: a warp per (query, head); lanes own dh / 32 consecutive columns (dh 16: 16 lanes one).
 // =========================================================================================
 template <typename T, int EPL>
@@ -224,13 +679,23 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
     };
     const int r_sh = (int)(m * grp + hg), r_own = (c * a.T + i) * grp + hg;
     const int own = own_rows_of(a, b, false);
+    const int ntp = (a.P + 127) / 128, W = a.tensor ? a.plan[0] : 1;
+    // the runs of W tiles that a segment of nt tiles starting at position start meets
+    auto runs = [&](int start, int nt, int pair) { return ((start + nt - 1) / W - start / W + 1) * (pair ? 1 : 2); };
     if (a.P > 0) {
-        const int64_t seg = (int64_t)g * a.sh_tiles + r_sh / a.sh_rows;
-        fold(a.sh_o, a.sh_ml, seg * a.sh_slots * a.sh_rows + r_sh % a.sh_rows, a.sh_rows, a.sh_slots);
+        const int seg = g * a.sh_tiles + r_sh / a.sh_rows;
+        fold(a.sh_o, a.sh_ml, (int64_t)seg * a.sh_slots * a.sh_rows + r_sh % a.sh_rows, a.sh_rows,
+             a.tensor ? runs(seg * ntp, ntp, a.sh_pair) : a.sh_slots);
     }
     if (own > 0) {
-        const int64_t seg = ((int64_t)b * a.G + g) * a.own_tiles + r_own / a.own_rows;
-        fold(a.own_o, a.own_ml, seg * a.own_slots * a.own_rows + r_own % a.own_rows, a.own_rows, a.own_slots);
+        const int in_b = g * a.own_tiles + r_own / a.own_rows, per_b = a.G * a.own_tiles;
+        int used = a.own_slots;
+        if (a.tensor) {
+            const int before = a.plan[1 + b], nt = a.plan[2 + b] - before;
+            used = runs(a.G * a.sh_tiles * ntp + per_b * before + in_b * nt, nt, a.own_pair);
+        }
+        fold(a.own_o, a.own_ml, ((int64_t)b * per_b + in_b) * a.own_slots * a.own_rows + r_own % a.own_rows, a.own_rows,
+             used);
     }
     // block rows j <= i: of this candidate, or own rows own + j when the block is in the cache
     const T *kb, *vb;
@@ -289,7 +754,7 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
             for (int u = 0; u < EPL; ++u) O[u] = fmaf(w, vv[j][u], O[u]);
         }
     }
-    // a query without any key: zero output, lse -inf
+    // no key with any weight: zero output, lse -inf
     if (act) {
         const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
         T* dst = (T*)a.o + m * a.o_ld + (int64_t)h * dh + e0;
@@ -330,6 +795,51 @@ void plan_simt(const evs_shared_attn_args& c, SharedArgs& a) {
     a.own_slots = c.own_max > 0 ? slots(own, c.own_max) : 0;
 }
 
+// The tensor-core path: bf16 with heads of 64 or 128, rows that tensor maps describe.
+bool map_ok(const void* p, long long row, long long head, long long seq, bool heads, bool seqs) {
+    return (uintptr_t)p % 16 == 0 && row % 8 == 0 && row < (1LL << 38) &&
+           (!heads || (head % 8 == 0 && head > 0 && head < (1LL << 38))) &&
+           (!seqs || (seq % 8 == 0 && seq > 0 && seq < (1LL << 38)));
+}
+bool tensor_ok(const evs_shared_attn_args& c) {
+    if (c.dtype != EVS_DTYPE_BF16 || (c.head_dim != 64 && c.head_dim != 128)) return false;
+    if (c.prefix == 0 && c.own_max == 0) return false;
+    if (c.prefix > 0 && !(map_ok(c.k_prefix, c.prefix_row, c.prefix_head, 0, c.kv_heads > 1, false) &&
+                          map_ok(c.v_prefix, c.prefix_row, c.prefix_head, 0, c.kv_heads > 1, false)))
+        return false;
+    if (c.own_max > 0 && !(map_ok(c.k_own, c.own_row, c.own_head, c.own_seq, c.kv_heads > 1, c.batch > 1) &&
+                           map_ok(c.v_own, c.own_row, c.own_head, c.own_seq, c.kv_heads > 1, c.batch > 1)))
+        return false;
+    return true;
+}
+
+// Tiles, slots and grid. A segment of nt tiles meets at most (nt - 1) / W + 2 runs of W tiles, and
+// W >= total / grid, with the own lengths known only on the device: the bound at their capacity
+// is the largest. false: sizes past the kernel's 32-bit tile positions.
+bool plan_tensor(const evs_shared_attn_args& c, SharedArgs& a, int& grid) {
+    const int grp = c.heads / c.kv_heads;
+    const long long sh = (long long)c.batch * c.n_cand * c.block * grp, own = (long long)c.n_cand * c.block * grp;
+    const long long ntp = (c.prefix + ST_KEYS - 1) / ST_KEYS, nto = (c.own_max + ST_KEYS - 1) / ST_KEYS;
+    a.sh_pair = sh > 128;
+    a.own_pair = own > 128;
+    a.sh_rows = (int)(sh < 256 ? sh : 256);
+    a.own_rows = (int)(own < 256 ? own : 256);
+    a.sh_tiles = (int)((sh + 255) / 256);
+    a.own_tiles = (int)((own + 255) / 256);
+    const long long sh_total = c.kv_heads * (long long)a.sh_tiles * ntp;
+    const long long per_b = (long long)c.kv_heads * a.own_tiles, most = sh_total + c.batch * per_b * nto;
+    if (most >= (1LL << 30)) return false;
+    grid = (int)(most < kAttnGrid ? most : kAttnGrid);
+    auto bound = [&](long long nt, long long total) {
+        const long long s = nt * grid / (total > 0 ? total : 1) + 2;
+        return (int)(s < nt ? s : nt);
+    };
+    a.sh_slots = ntp ? bound(ntp, sh_total) * (a.sh_pair ? 1 : 2) : 0;
+    a.own_slots = nto ? bound(nto, sh_total + per_b * nto) * (a.own_pair ? 1 : 2) : 0;
+    a.tensor = 1;
+    return true;
+}
+
 // Lays the partials out from base (or sizes them).
 size_t carve_partials(const evs_shared_attn_args& c, SharedArgs& a, char* base) {
     size_t off = 0;
@@ -344,7 +854,66 @@ size_t carve_partials(const evs_shared_attn_args& c, SharedArgs& a, char* base) 
     a.own_o = (float*)take(own * c.head_dim * 4);
     a.sh_ml = (float2*)take(sh * 8);
     a.own_ml = (float2*)take(own * 8);
+    a.plan = (int*)take(((size_t)c.batch + 2) * 4);
     return off;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// [seqs][heads][rows][dh] bf16, boxes of 128 rows x 64 columns. The stride of a dimension of one
+// is not used; it only has to be a legal one.
+bool make_rows_map(CUtensorMap* m, const void* base, int dh, int rows, int heads, int seqs, int64_t row, int64_t head,
+                   int64_t seq) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)seqs};
+    const cuuint64_t r2 = rows > 1 ? (cuuint64_t)row * 2 : (cuuint64_t)dh * 2;
+    const cuuint64_t h2 = heads > 1 ? (cuuint64_t)head * 2 : r2, s2 = seqs > 1 ? (cuuint64_t)seq * 2 : h2;
+    const cuuint64_t strides[3] = {r2, h2, s2};
+    const cuuint32_t box[4] = {64, ST_KEYS, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+cudaError_t launch_tensor(const evs_shared_attn_args& c, SharedArgs& a, int grid, cudaStream_t stream) {
+    CUtensorMap kp, vp, ko, vo;
+    bool ok = true;
+    if (c.prefix > 0)
+        ok = make_rows_map(&kp, c.k_prefix, DH, c.prefix, c.kv_heads, 1, c.prefix_row, c.prefix_head, 0) &&
+             make_rows_map(&vp, c.v_prefix, DH, c.prefix, c.kv_heads, 1, c.prefix_row, c.prefix_head, 0);
+    if (ok && c.own_max > 0)
+        ok = make_rows_map(&ko, c.k_own, DH, c.own_max, c.kv_heads, c.batch, c.own_row, c.own_head, c.own_seq) &&
+             make_rows_map(&vo, c.v_own, DH, c.own_max, c.kv_heads, c.batch, c.own_row, c.own_head, c.own_seq);
+    if (!ok) return cudaErrorInvalidValue;
+    if (c.prefix == 0) { kp = ko; vp = vo; }
+    if (c.own_max == 0) { ko = kp; vo = vp; }
+    constexpr int TILE = ST_KEYS * DH * 2;
+    const int es = c.q_dtype == EVS_DTYPE_BF16 ? 2 : 4;
+    a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld * es % 16 == 0;
+    int dev = 0, optin = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e != cudaSuccess) return e;
+    // alignment, two Q tiles, 9 barriers beside the ring's, lengths and their running sums
+    const int fixed = 1024 + 2 * TILE + 9 * 8 + (2 * c.batch + 1) * 4 + 64;
+    a.stages = (optin - 256 - fixed) / (TILE + 16);   // 256: the static part
+    if (a.stages > 12) a.stages = 12;
+    const int smem = fixed + a.stages * (TILE + 16);
+    e = cudaFuncSetAttribute(shared_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_s(stream, shared_tc_kernel<DH>, dim3(grid), dim3(ST_THREADS), (size_t)smem, kp, vp, ko, vo, a);
 }
 
 }  // namespace
@@ -359,13 +928,17 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     a.B = c.batch; a.C = c.n_cand; a.T = c.block; a.H = c.heads; a.G = c.kv_heads; a.dh = c.head_dim;
     a.P = c.prefix; a.own_max = c.own_max; a.own_skip = c.own_skip; a.q_bf16 = c.q_dtype == EVS_DTYPE_BF16;
     a.scale = c.scale != 0.f ? c.scale : 1.f / sqrtf((float)c.head_dim);
-    plan_simt(c, a);
-    carve_partials(c, a, (char*)c.workspace);
     const bool half = c.dtype == EVS_DTYPE_BF16;
+    int grid_tc = 0;
+    const bool tensor = tensor_ok(c) && plan_tensor(c, a, grid_tc);
+    if (!tensor) plan_simt(c, a);
+    carve_partials(c, a, (char*)c.workspace);
     const int sh_items = c.kv_heads * a.sh_slots * ((a.sh_rows + SA_Q - 1) / SA_Q);
     const int own_items = c.batch * c.kv_heads * a.own_slots * ((a.own_rows + SA_Q - 1) / SA_Q);
     cudaError_t e = cudaSuccess;
-    if (sh_items + own_items > 0)
+    if (tensor)
+        e = c.head_dim == 128 ? launch_tensor<128>(c, a, grid_tc, stream) : launch_tensor<64>(c, a, grid_tc, stream);
+    else if (sh_items + own_items > 0)
         e = half ? launch_s(stream, shared_simt_kernel<bf16>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items)
                  : launch_s(stream, shared_simt_kernel<float>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items);
     if (e != cudaSuccess) return e;
@@ -387,9 +960,15 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
 extern "C" size_t evs_shared_attention_workspace(const evs_shared_attn_args* c) {
     using namespace evs;
     if (!valid_shape(c)) return 0;
-    SharedArgs a{};
+    // the larger of the two paths: which one runs depends on addresses too
+    SharedArgs a{}, t{};
+    int grid = 0;
     plan_simt(*c, a);
-    const size_t n = carve_partials(*c, a, nullptr);
+    size_t n = carve_partials(*c, a, nullptr);
+    if (c->dtype == EVS_DTYPE_BF16 && (c->head_dim == 64 || c->head_dim == 128) && plan_tensor(*c, t, grid)) {
+        const size_t m = carve_partials(*c, t, nullptr);
+        n = m > n ? m : n;
+    }
     return n ? n : 256;
 }
 
