@@ -186,10 +186,12 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
 // the last step cleared in shared memory (they may hold anything, NaN included).
 //
 // Tensor memory, columns: S/P of lane 0 and 1 at 0 and 128, O at 256 and 384.
-// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warp 9: MMA.
+// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warp 9: MMA (one thread, its
+// products unrolled: issuing them from a loop took 1650 cycles for eight of 64); warp 10 clears
+// the rows behind the last key of a piece.
 // =========================================================================================
 constexpr int ST_KEYS = 128;
-constexpr int ST_THREADS = 320;
+constexpr int ST_THREADS = 352;
 constexpr float ST_RESCALE_LOG2 = 8.f;
 
 __device__ __forceinline__ uint32_t st_sw128(int row, int chunk16) {
@@ -200,9 +202,14 @@ __device__ __forceinline__ uint32_t st_pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One CTA's share of a segment: tiles t0 .. t0 + n - 1 of `keys` keys.
+__device__ __forceinline__ void st_cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One CTA's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys. `seg` numbers
+// the prefix's segments or the own rows' ones.
 struct Piece {
-    int sh, b, g, rt, t0, n, keys, slot, seg;
+    int sh, b, g, rt, t0, n, nt, keys, slot, seg;
 };
 
 template <int DH>
@@ -226,7 +233,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     uint64_t* p_full = s_full + 2;                             // [2] weights of a tile there
     uint64_t* pv_done = p_full + 2;                            // [2] P V of a tile complete
     uint64_t* q_ready = pv_done + 2;                           // [2] Q of a piece staged
-    uint64_t* drain = q_ready + 2;
+    uint64_t* cleared = q_ready + 2;                           // the rows behind a piece's last key
+    uint64_t* want = cleared + 1;                              // that tile is in the ring
+    uint64_t* drain = want + 1;
     int* pre = reinterpret_cast<int*>(drain + 1);              // [B + 1] own tiles before sequence b
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -245,6 +254,8 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_ready[i], 4);
         }
+        mbar_init(cleared, 1);
+        mbar_init(want, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -282,39 +293,60 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         for (int b = tid; b <= a.B; b += ST_THREADS) a.plan[1 + b] = pre[b];
         if (tid == 0) a.plan[0] = W;
     }
-    // the piece that starts at position pos, the same for every role
-    auto piece = [&](int pos) -> Piece {
+    // the CTA's first piece, and the one behind p (pos: where it starts), the same for every role
+    auto first_piece = [&]() -> Piece {
         Piece p;
-        int start, nt;
-        if (pos < sh_total) {
+        int start;
+        if (lo < sh_total) {
             p.sh = 1;
             p.b = 0;
-            p.seg = pos / ntp;
+            p.seg = lo / ntp;
             p.g = p.seg / a.sh_tiles;
             p.rt = p.seg % a.sh_tiles;
             start = p.seg * ntp;
-            nt = ntp;
+            p.nt = ntp;
             p.keys = a.P;
         } else {
-            const int q = pos - sh_total;
+            const int q = lo - sh_total;
             int b0 = 0, b1 = a.B - 1;             // the last b with per_b * pre[b] <= q
             while (b0 < b1) {
                 const int mid = (b0 + b1 + 1) >> 1;
                 if (per_b * pre[mid] <= q) b0 = mid; else b1 = mid - 1;
             }
-            nt = pre[b0 + 1] - pre[b0];
-            const int r = (q - per_b * pre[b0]) / nt;
+            p.nt = pre[b0 + 1] - pre[b0];
+            const int r = (q - per_b * pre[b0]) / p.nt;
             p.sh = 0;
             p.b = b0;
             p.g = r / a.own_tiles;
             p.rt = r % a.own_tiles;
             p.seg = b0 * per_b + r;
-            start = sh_total + per_b * pre[b0] + r * nt;
+            start = sh_total + per_b * pre[b0] + r * p.nt;
             p.keys = len[b0];
         }
-        p.t0 = pos - start;
-        p.n = min(nt - p.t0, hi - pos);
+        p.t0 = lo - start;
+        p.n = min(p.nt - p.t0, hi - lo);
         p.slot = (int)blockIdx.x - start / W;
+        return p;
+    };
+    auto next_piece = [&](const Piece& c, int pos) -> Piece {
+        Piece p = c;
+        p.t0 = 0;
+        p.slot = 0;                               // the first run that meets its segment
+        ++p.seg;
+        const int tiles = c.sh ? a.sh_tiles : a.own_tiles;
+        if (++p.rt == tiles) {
+            p.rt = 0;
+            if (++p.g == a.G) {                   // on to the next sequence that has rows
+                p.g = 0;
+                p.b = c.sh ? 0 : c.b + 1;
+                while (p.b < a.B - 1 && pre[p.b + 1] == pre[p.b]) ++p.b;
+                p.sh = 0;
+                p.seg = p.b * per_b;
+                p.nt = pre[p.b + 1] - pre[p.b];
+                p.keys = len[p.b];
+            }
+        }
+        p.n = min(p.nt, hi - pos);
         return p;
     };
     // tiles of lane L in a piece
@@ -326,8 +358,8 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             // ---- TMA, in the order of use. Row lanes: K0 V0 K1 V1 ...; key lanes: K0 K1 V0 K2 V1 K3 ...
             const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
             bool ok = true;
-            for (int pos = lo; pos < hi && ok;) {
-                const Piece p = piece(pos);
+            Piece p = first_piece();
+            for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
                 const bool pair = p.sh ? a.sh_pair : a.own_pair;
                 const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
                 auto load = [&](const CUtensorMap* m, int t) {
@@ -350,7 +382,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                     load(mv, t);
                     if (ok && t + ahead < p.n) load(mk, t + ahead);
                 }
-                pos += p.n;
             }
             if (!ok) *abort_flag = 1;
         }
@@ -367,92 +398,92 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         tmem_dealloc(tmem, 512);
         return;
     }
+    // ring step of the K and V tile t of a piece whose first step is base
+    auto k_step = [&](const Piece& p, bool pair, int base, int t) {
+        return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1));
+    };
+    auto v_step = [&](const Piece& p, bool pair, int base, int t) {
+        return base + (pair ? 2 * t + 1 : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
+    };
+    // keys of the piece's last tile, in whole 16-key steps or not
+    auto ragged = [&](const Piece& p) { return p.t0 + p.n == p.nt && (p.keys & 15) != 0; };
     if (warp == 9) {
-        // ---- MMA: every lane of the warp follows, one issues
-        const uint32_t id_s = idesc_bf16_f32(128, ST_KEYS);
-        const uint32_t id_o = idesc_bf16_f32_bmn(128, DH);
-        const uint32_t q0 = smem_u32(sQ);
-        int base = 0;                  // ring steps of earlier pieces
-        int cnt[2] = {0, 0}, qn[2] = {0, 0};
-        bool ok = true;
-        for (int pos = lo; pos < hi && ok;) {
-            const Piece p = piece(pos);
-            const bool pair = p.sh ? a.sh_pair : a.own_pair;
-            const int n0 = lane_tiles(p, 0), n1 = lane_tiles(p, 1);
-            // ring step of the K and V tile t of the piece
-            auto k_step = [&](int t) { return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1)); };
-            auto v_step = [&](int t) {
-                return base + (pair ? min(2 * t + 1, 2 * p.n - 1) : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
-            };
-            auto wait_full = [&](int step) {
-                const bool r = mbar_wait(&full[step % a.stages], (uint32_t)(step / a.stages) & 1u);
-                return __all_sync(0xffffffffu, r) != 0;
-            };
-            auto score = [&](int L, int t, bool last_use) {
-                const int st = k_step(t);
-                if (!wait_full(st)) { ok = false; return; }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t k0 = smem_u32(ring + (size_t)(st % a.stages) * TILE), qa = q0 + L * TILE;
+        if (lane == 0) {
+            // ---- MMA
+            constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
+            const uint64_t dq = smem_desc_sw128(smem_u32(sQ)), dk = smem_desc_sw128(smem_u32(ring)),
+                           dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
+            int base = 0;                  // ring steps of earlier pieces
+            int cnt[2] = {0, 0}, qn[2] = {0, 0}, cleans = 0;
+            bool ok = true;
+            Piece p = first_piece();
+            for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
+                const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                const int n0 = lane_tiles(p, 0), n1 = lane_tiles(p, 1);
+                auto wait_full = [&](int step) {
+                    if (mbar_wait(&full[step % a.stages], (uint32_t)(step / a.stages) & 1u)) return true;
+                    ok = false;
+                    return false;
+                };
+                auto score = [&](int L, int t, bool last_use) {
+                    const int st = k_step(p, pair, base, t), slot = st % a.stages;
+                    if (!wait_full(st)) return;
+                    tc_fence_after();
+                    const uint64_t qd = dq + (uint64_t)((uint32_t)(L * TILE) >> 4);
+                    const uint64_t kd = dk + (uint64_t)((uint32_t)(slot * TILE) >> 4);
+                    const uint32_t d = tmem + (uint32_t)L * 128u;
 #pragma unroll
                     for (int kk = 0; kk < DH / 16; ++kk) {
-                        const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32u;
-                        tc_mma_f16(tmem + (uint32_t)L * 128u, smem_desc_sw128(qa + off), smem_desc_sw128(k0 + off),
-                                   id_s, kk > 0 ? 1u : 0u);
+                        const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                        tc_mma_f16(d, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
                     }
                     tc_commit(&s_full[L]);
-                    if (last_use) tc_commit(&empty[st % a.stages]);
-                }
-                __syncwarp();
-            };
-            auto weigh = [&](int L, int t, bool first, bool first_use, bool last_use) {   // O += P V
-                const int st = v_step(t);
-                if (!__all_sync(0xffffffffu, mbar_wait(&p_full[L], (uint32_t)cnt[L] & 1u))) { ok = false; return; }
-                ++cnt[L];
-                if (!wait_full(st)) { ok = false; return; }
-                const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
-                uint8_t* v = ring + (size_t)(st % a.stages) * TILE;
-                if (first_use && (nv & 15)) {
-                    // rows nv .. of the last 16-key step: clear them
-                    const int rows = 16 - (nv & 15);
-                    for (int e = lane; e < rows * 8 * HALVES; e += 32) {
-                        const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
-                        *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    if (last_use) tc_commit(&empty[slot]);
+                };
+                auto weigh = [&](int L, int t, bool first, bool last_use) {   // O += P V
+                    const int st = v_step(p, pair, base, t), slot = st % a.stages;
+                    if (!wait_full(st)) return;
+                    const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+                    // cleared while the softmax runs; of two row lanes the first one asks
+                    const bool clean = (nv & 15) && (!pair || L == 0);
+                    if (clean) mbar_arrive(want);
+                    if (!mbar_wait(&p_full[L], (uint32_t)cnt[L] & 1u)) { ok = false; return; }
+                    ++cnt[L];
+                    if (clean) {
+                        if (!mbar_wait(cleared, (uint32_t)cleans & 1u)) { ok = false; return; }
+                        ++cleans;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t v0 = smem_u32(v);
-                    const int steps = (nv + 15) / 16;
-                    for (int kk = 0; kk < steps; ++kk)
-                        tc_mma_f16_ta(tmem + O_COL + (uint32_t)L * 128u, tmem + (uint32_t)L * 128u + (uint32_t)kk * 8u,
-                                      smem_desc_sw128_mn(v0 + (uint32_t)kk * 16u * 128u, HALF), id_o,
-                                      (!first || kk > 0) ? 1u : 0u);
+                    tc_fence_after();
+                    const uint64_t vd = dv + (uint64_t)((uint32_t)(slot * TILE) >> 4);
+                    const uint32_t d = tmem + O_COL + (uint32_t)L * 128u, w = tmem + (uint32_t)L * 128u;
+                    if (nv > ST_KEYS - 16) {
+#pragma unroll
+                        for (int kk = 0; kk < ST_KEYS / 16; ++kk)
+                            tc_mma_f16_ta(d, w + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                          (kk > 0 || !first) ? 1u : 0u);
+                    } else {
+                        for (int kk = 0; kk < (nv + 15) / 16; ++kk)
+                            tc_mma_f16_ta(d, w + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                          (kk > 0 || !first) ? 1u : 0u);
+                    }
                     tc_commit(&pv_done[L]);
-                    if (last_use) tc_commit(&empty[st % a.stages]);
-                }
-                __syncwarp();
-            };
-            for (int L = 0; L < 2 && ok; ++L) {
-                if ((L ? n1 : n0) == 0) continue;
-                if (!__all_sync(0xffffffffu, mbar_wait(&q_ready[L], (uint32_t)qn[L] & 1u))) { ok = false; break; }
-                ++qn[L];
-                tc_fence_after();
-                score(L, pair ? 0 : L, !pair || L == 1);
-            }
-            for (int s = 0; s < n0 && ok; ++s) {
+                    if (last_use) tc_commit(&empty[slot]);
+                };
                 for (int L = 0; L < 2 && ok; ++L) {
-                    const int nl = L ? n1 : n0;
-                    if (s < nl) weigh(L, pair ? s : 2 * s + L, s == 0, !pair || L == 0, !pair || L == 1);
-                    if (ok && s + 1 < nl) score(L, pair ? s + 1 : 2 * (s + 1) + L, !pair || L == 1);
+                    if ((L ? n1 : n0) == 0) continue;
+                    if (!mbar_wait(&q_ready[L], (uint32_t)qn[L] & 1u)) { ok = false; break; }
+                    ++qn[L];
+                    score(L, pair ? 0 : L, !pair || L == 1);
                 }
+                for (int s = 0; s < n0 && ok; ++s) {
+                    for (int L = 0; L < 2 && ok; ++L) {
+                        const int nl = L ? n1 : n0;
+                        if (s < nl) weigh(L, pair ? s : 2 * s + L, s == 0, !pair || L == 1);
+                        if (ok && s + 1 < nl) score(L, pair ? s + 1 : 2 * (s + 1) + L, !pair || L == 1);
+                    }
+                }
+                base += 2 * p.n;
             }
-            base += 2 * p.n;
-            pos += p.n;
-        }
-        if (lane == 0) {
             if (!ok) *abort_flag = 1;
             tc_commit(drain);                     // nothing of this CTA's in tensor memory in flight
             mbar_wait(drain, 0);
@@ -462,62 +493,109 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         __syncthreads();
         return;
     }
+    if (warp == 10) {
+        // ---- clear the V rows behind the last key, up to the end of its 16-key step
+        int base = 0, cleans = 0;
+        bool ok = true;
+        Piece p = first_piece();
+        for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
+            if (ragged(p)) {
+                const int st = v_step(p, p.sh ? a.sh_pair : a.own_pair, base, p.n - 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(want, (uint32_t)cleans & 1u)) != 0;
+                if (!ok) break;
+                ++cleans;
+                uint8_t* v = ring + (size_t)(st % a.stages) * TILE;
+                const int nv = p.keys - (p.nt - 1) * ST_KEYS, rows = 16 - (nv & 15);
+                for (int e = lane; e < rows * 8 * HALVES; e += 32) {
+                    const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
+                    *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cleared);
+            }
+            base += 2 * p.n;
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+        __syncthreads();
+        return;
+    }
     // ---- softmax of lane L: thread = row r of the lane's tile
     const int L = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t s_col = (uint32_t)L * 128u, o_col = O_COL + (uint32_t)L * 128u;
     const int grp = a.H / a.G;
     const float sl = a.scale * 1.4426950408889634f;
-    int cnt = 0;
-    bool ok = true;
-    for (int pos = lo; pos < hi && ok;) {
-        const Piece p = piece(pos);
+    // where this thread's row of a piece lies: in its segment, and of the head
+    auto rows_of = [&](const Piece& p, int& r_seg, int& r_all) -> bool {
         const bool pair = p.sh ? a.sh_pair : a.own_pair;
-        const int nl = lane_tiles(p, L);
         const int all_rows = p.sh ? a.B * a.C * a.T * grp : a.C * a.T * grp;
         const int seg_rows = p.sh ? a.sh_rows : a.own_rows;
-        const int r_seg = pair ? L * 128 + r : r;                       // row in the segment
-        const int r_all = p.rt * seg_rows + r_seg;                      // and of the head
-        const bool live = r_seg < seg_rows && r_all < all_rows;
-        const bool work = __any_sync(0xffffffffu, live);
-        float m_run = -INFINITY, l = 0.f;
-        if (nl > 0) {
-            if (work) {
-                // Q row -> bf16, K-major, 128-byte swizzle
-                const int64_t m = p.sh ? r_all / grp : (int64_t)p.b * a.C * a.T + r_all / grp;
-                const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all % grp) * DH;
-#pragma unroll
-                for (int hf = 0; hf < HALVES; ++hf)
+        r_seg = pair ? L * 128 + r : r;
+        r_all = p.rt * seg_rows + r_seg;
+        return r_seg < seg_rows && r_all < all_rows;
+    };
+    // Q row -> bf16, K-major, 128-byte swizzle. bf16 rows on 16 bytes are copied asynchronously, so
+    // that the next piece's come while this one's last tile is worked on; staged() ends a staging.
+    auto stage = [&](const Piece& p) {
+        int r_seg, r_all;
+        const bool live = rows_of(p, r_seg, r_all);
+        if (!__any_sync(0xffffffffu, live)) return;
+        const int64_t m = p.sh ? r_all / grp : (int64_t)p.b * a.C * a.T + r_all / grp;
+        const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all % grp) * DH;
+        uint8_t* dst = sQ + L * TILE;
+#pragma unroll 1
+        for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll 4
-                    for (int c = 0; c < 8; ++c) {
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (live) {
-                            const int64_t e = at + hf * 64 + c * 8;
-                            if (a.q_bf16 && a.q_vec) {
-                                u = *reinterpret_cast<const uint4*>((const bf16*)a.q + e);
-                            } else {
-                                float x[8];
-                                if (a.q_vec) {
-                                    const float4 x0 = *reinterpret_cast<const float4*>((const float*)a.q + e);
-                                    const float4 x1 = *reinterpret_cast<const float4*>((const float*)a.q + e + 4);
-                                    x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
-                                    x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
-                                } else {
-                                    for (int j = 0; j < 8; ++j) x[j] = load_q(a, e + j);
-                                }
-                                u = make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]), st_pack(x[4], x[5]),
-                                               st_pack(x[6], x[7]));
-                            }
-                        }
-                        *reinterpret_cast<uint4*>(sQ + L * TILE + hf * HALF + st_sw128(r, c)) = u;
+            for (int c = 0; c < 8; ++c) {
+                uint8_t* to = dst + hf * HALF + st_sw128(r, c);
+                const int64_t e = at + hf * 64 + c * 8;
+                if (!live) {
+                    *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
+                } else if (a.q_bf16 && a.q_vec) {
+                    st_cp_async16(smem_u32(to), (const bf16*)a.q + e);
+                } else {
+                    float x[8];
+                    if (a.q_vec) {
+                        const float4 x0 = *reinterpret_cast<const float4*>((const float*)a.q + e);
+                        const float4 x1 = *reinterpret_cast<const float4*>((const float*)a.q + e + 4);
+                        x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
+                        x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = load_q(a, e + j);
                     }
-                fence_proxy_async_smem();
+                    *reinterpret_cast<uint4*>(to) = make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]),
+                                                               st_pack(x[4], x[5]), st_pack(x[6], x[7]));
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_ready[L]);
-        }
+    };
+    auto staged = [&]() {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready[L]);
+    };
+    int cnt = 0;
+    bool ok = true;
+    Piece p = first_piece();
+    if (lo < hi && lane_tiles(p, L) > 0) {
+        stage(p);
+        staged();
+    }
+    for (int pos = lo; pos < hi && ok;) {
+        const bool pair = p.sh ? a.sh_pair : a.own_pair;
+        const int nl = lane_tiles(p, L), seg_rows = p.sh ? a.sh_rows : a.own_rows;
+        int r_seg, r_all;
+        const bool live = rows_of(p, r_seg, r_all), work = __any_sync(0xffffffffu, live);
+        const bool more = pos + p.n < hi;
+        const Piece nx = more ? next_piece(p, pos + p.n) : p;
+        const bool feed = more && lane_tiles(nx, L) > 0;
+        float m_run = -INFINITY, l = 0.f;
+        if (nl == 0 && feed) stage(nx);
         for (int s = 0; s < nl; ++s) {
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[L], (uint32_t)cnt & 1u))) { ok = false; break; }
+            if (s == nl - 1 && feed) stage(nx);   // this piece's last scores are out: Q's place is free
             if (work) {
                 tc_fence_after();
                 uint32_t x[8][16];
@@ -580,6 +658,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             if (lane == 0) mbar_arrive(&p_full[L]);
             ++cnt;
         }
+        if (ok && feed) staged();                 // the next scores need not wait for the rest
         // ---- the piece's partials: o, then (m, l)
         if (ok && nl > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[L], (uint32_t)(cnt - 1) & 1u))) ok = false;
         tc_fence_after();
@@ -610,6 +689,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         }
         tc_fence_before();                        // these reads precede the next piece's products
         pos += p.n;
+        p = nx;
     }
     tc_fence_before();
     __syncthreads();
@@ -623,12 +703,11 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 4 + warp;
     const int dh = a.dh, grp = a.H / a.G;
-    if (id >= (int64_t)a.B * a.C * a.T * a.H) return;
-    // id -> (b, c, g, i, head in group), so that the four warps of a CTA share block rows
-    const int hg = (int)(id % grp), i = (int)(id / grp % a.T), g = (int)(id / grp / a.T % a.G);
-    const int bc = (int)(id / grp / a.T / a.G), b = bc / a.C, c = bc % a.C;
+    // CTA (b and c, g, four of the queries and heads there): its warps share block rows
+    const int bc = blockIdx.x, g = blockIdx.y, at = blockIdx.z * 4 + warp;
+    const int i = at / grp, hg = at % grp, b = bc / a.C, c = bc % a.C;
+    if (i >= a.T) return;
     const int64_t m = (int64_t)bc * a.T + i;
     const int h = g * grp + hg;
     const int e0 = lane * EPL;
@@ -906,8 +985,8 @@ cudaError_t launch_tensor(const evs_shared_attn_args& c, SharedArgs& a, int grid
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return e;
-    // alignment, two Q tiles, 9 barriers beside the ring's, lengths and their running sums
-    const int fixed = 1024 + 2 * TILE + 9 * 8 + (2 * c.batch + 1) * 4 + 64;
+    // alignment, two Q tiles, 11 barriers beside the ring's, lengths and their running sums
+    const int fixed = 1024 + 2 * TILE + 11 * 8 + (2 * c.batch + 1) * 4 + 64;
     a.stages = (optin - 256 - fixed) / (TILE + 16);   // 256: the static part
     if (a.stages > 12) a.stages = 12;
     const int smem = fixed + a.stages * (TILE + 16);
@@ -942,8 +1021,7 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
         e = half ? launch_s(stream, shared_simt_kernel<bf16>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items)
                  : launch_s(stream, shared_simt_kernel<float>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items);
     if (e != cudaSuccess) return e;
-    const long long queries = (long long)c.batch * c.n_cand * c.block * c.heads;
-    const dim3 grid((unsigned)((queries + 3) / 4));
+    const dim3 grid(c.batch * c.n_cand, c.kv_heads, (c.block * (c.heads / c.kv_heads) + 3) / 4);
     if (half)
         e = c.head_dim == 128  ? launch_s(stream, shared_combine_kernel<bf16, 4>, grid, dim3(128), 0, a)
             : c.head_dim == 64 ? launch_s(stream, shared_combine_kernel<bf16, 2>, grid, dim3(128), 0, a)
