@@ -36,7 +36,7 @@ struct SharedArgs {
     int tensor;                // the tensor-core kernel's partials: slots by its runs of tiles
     int sh_pair, own_pair;     // 1: 256-row segments, a row tile per lane; 0: a lane per key tile
     int* plan;                 // tiles per run, then the running sum of own tiles per sequence
-    int q_vec, stages;
+    int q_vec;
 };
 
 // fp32 problems keep the full precision of the exponential
@@ -186,12 +186,13 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
 // the last step cleared in shared memory (they may hold anything, NaN included).
 //
 // Tensor memory, columns: S/P of lane 0 and 1 at 0 and 128, O at 256 and 384.
-// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warp 9: MMA (one thread, its
-// products unrolled: issuing them from a loop took 1650 cycles for eight of 64); warp 10 clears
-// the rows behind the last key of a piece.
+// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warps 9 and 11: one thread each
+// issues a lane's products. Issuing eight of them takes as long as they run (512 cycles), and the
+// waits and commits between two groups about 1600 more; with one thread for both lanes those
+// left the tensor core idle half of the time. Warp 10 clears the rows behind a piece's last key.
 // =========================================================================================
 constexpr int ST_KEYS = 128;
-constexpr int ST_THREADS = 352;
+constexpr int ST_THREADS = 384;
 constexpr float ST_RESCALE_LOG2 = 8.f;
 
 __device__ __forceinline__ uint32_t st_sw128(int row, int chunk16) {
@@ -206,13 +207,32 @@ __device__ __forceinline__ void st_cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ uint64_t st_pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void st_split(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t st_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t st_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // One CTA's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys. `seg` numbers
 // the prefix's segments or the own rows' ones.
 struct Piece {
     int sh, b, g, rt, t0, n, nt, keys, slot, seg;
 };
 
-template <int DH>
+template <int DH, int NST>
 __global__ void __launch_bounds__(ST_THREADS, 1)
 shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
                  const __grid_constant__ CUtensorMap tmKO, const __grid_constant__ CUtensorMap tmVO, SharedArgs a) {
@@ -227,16 +247,19 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* sQ = smem;                                        // [2 lanes][halves][128 rows][128 B]
     uint8_t* ring = sQ + 2 * TILE;                             // [stages]
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)a.stages * TILE);
-    uint64_t* empty = full + a.stages;
-    uint64_t* s_full = empty + a.stages;                       // [2] scores of a tile in tensor memory
+    // A ring slot has three "full" barriers, for a tile that both lanes use and for one of lane 0
+    // or 1 alone: whoever waits on one of them has waited on all its earlier phases, so a phase's
+    // parity is enough.
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)NST * TILE);   // [3][NST]
+    uint64_t* empty = full + 3 * NST;                          // [NST], two arrivals
+    uint64_t* s_full = empty + NST;                            // [2] scores of a tile in tensor memory
     uint64_t* p_full = s_full + 2;                             // [2] weights of a tile there
     uint64_t* pv_done = p_full + 2;                            // [2] P V of a tile complete
     uint64_t* q_ready = pv_done + 2;                           // [2] Q of a piece staged
-    uint64_t* cleared = q_ready + 2;                           // the rows behind a piece's last key
-    uint64_t* want = cleared + 1;                              // that tile is in the ring
-    uint64_t* drain = want + 1;
-    int* pre = reinterpret_cast<int*>(drain + 1);              // [B + 1] own tiles before sequence b
+    uint64_t* want = q_ready + 2;                              // [2] a tile to clear is in the ring
+    uint64_t* cleared = want + 2;                              // [2]
+    uint64_t* drain = cleared + 2;                             // [2]
+    int* pre = reinterpret_cast<int*>(drain + 2);              // [B + 1] own tiles before sequence b
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -244,19 +267,17 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     pdl_wait();
     for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
     if (tid == 0) {
-        for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
+        for (int s = 0; s < 3 * NST; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < NST; ++s) mbar_init(&empty[s], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_ready[i], 4);
+            mbar_init(&want[i], 1);
+            mbar_init(&cleared[i], 1);
+            mbar_init(&drain[i], 1);
         }
-        mbar_init(cleared, 1);
-        mbar_init(want, 1);
-        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -352,27 +373,41 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     // tiles of lane L in a piece
     auto lane_tiles = [&](const Piece& p, int L) { return (p.sh ? a.sh_pair : a.own_pair) ? p.n : (p.n + 1 - L) / 2; };
 
+    // Ring steps: row lanes take K0 V0 K1 V1 ..., key lanes K0 K1 V0 K2 V1 K3 ... V(n-1), the order of
+    // use. The step of the K and V tile t of a piece whose first step is base:
+    auto k_step = [&](bool pair, int base, int t) { return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1)); };
+    auto v_step = [&](const Piece& p, bool pair, int base, int t) {
+        return base + (pair ? 2 * t + 1 : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
+    };
     if (warp == 8) {
-        int issued = 0;
         if (lane == 0) {
-            // ---- TMA, in the order of use. Row lanes: K0 V0 K1 V1 ...; key lanes: K0 K1 V0 K2 V1 K3 ...
+            // ---- TMA
             const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
+            int issued = 0;
+            uint32_t par[3] = {0, 0, 0}, kind0 = 0, kind1 = 0;   // bit s: slot s
             bool ok = true;
             Piece p = first_piece();
             for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
                 const bool pair = p.sh ? a.sh_pair : a.own_pair;
                 const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
                 auto load = [&](const CUtensorMap* m, int t) {
-                    const int s = issued % a.stages;
-                    if (issued >= a.stages && !mbar_wait(&empty[s], ((uint32_t)(issued / a.stages) & 1u) ^ 1u)) {
+                    const int s = issued % NST;
+                    if (issued >= NST && !mbar_wait(&empty[s], ((uint32_t)(issued / NST) & 1u) ^ 1u)) {
                         ok = false;
                         return;
                     }
+                    const int kd = pair ? 0 : 1 + (t & 1);
+                    uint64_t* bar = &full[kd * NST + s];
                     uint8_t* dst = ring + (size_t)s * TILE;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)TILE);
+                    mbar_arrive_expect_tx(bar, (uint32_t)TILE);
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, &full[s], pol);
+                        tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, bar, pol);
+                    par[0] ^= kd == 0 ? 1u << s : 0u;
+                    par[1] ^= kd == 1 ? 1u << s : 0u;
+                    par[2] ^= kd == 2 ? 1u << s : 0u;
+                    kind0 = (kind0 & ~(1u << s)) | (uint32_t)(kd & 1) << s;
+                    kind1 = (kind1 & ~(1u << s)) | (uint32_t)(kd >> 1) << s;
                     ++issued;
                 };
                 const CUtensorMap *mk = p.sh ? &tmKP : &tmKO, *mv = p.sh ? &tmVP : &tmVO;
@@ -383,110 +418,103 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                     if (ok && t + ahead < p.n) load(mk, t + ahead);
                 }
             }
-            if (!ok) *abort_flag = 1;
+            // loads in flight into this CTA's shared memory end before it does (bounded): only
+            // where the pipeline gave up are there any
+            if (!ok) {
+                *abort_flag = 1;
+                for (int s = 0; s < min(issued, NST); ++s) {
+                    const int kd = (int)((kind0 >> s) & 1u) + 2 * (int)((kind1 >> s) & 1u);
+                    const uint32_t bits = kd == 0 ? par[0] : (kd == 1 ? par[1] : par[2]);
+                    mbar_wait(&full[kd * NST + s], ((bits >> s) & 1u) ^ 1u);
+                }
+            }
         }
         __syncwarp();
         tc_fence_before();
         __syncthreads();
-        if (*abort_flag && lane == 0) {
-            // loads in flight into this CTA's shared memory end before it does (bounded)
-            for (int j = issued > a.stages ? issued - a.stages : 0; j < issued; ++j)
-                mbar_wait(&full[j % a.stages], (uint32_t)(j / a.stages) & 1u);
-        }
-        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
         return;
     }
-    // ring step of the K and V tile t of a piece whose first step is base
-    auto k_step = [&](const Piece& p, bool pair, int base, int t) {
-        return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1));
-    };
-    auto v_step = [&](const Piece& p, bool pair, int base, int t) {
-        return base + (pair ? 2 * t + 1 : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
-    };
-    // keys of the piece's last tile, in whole 16-key steps or not
-    auto ragged = [&](const Piece& p) { return p.t0 + p.n == p.nt && (p.keys & 15) != 0; };
-    if (warp == 9) {
+    if (warp == 9 || warp == 11) {
         if (lane == 0) {
-            // ---- MMA
+            // ---- MMA of lane L
+            const int L = warp == 9 ? 0 : 1;
             constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
-            const uint64_t dq = smem_desc_sw128(smem_u32(sQ)), dk = smem_desc_sw128(smem_u32(ring)),
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
                            dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
+            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + O_COL + (uint32_t)L * 128u;
             int base = 0;                  // ring steps of earlier pieces
-            int cnt[2] = {0, 0}, qn[2] = {0, 0}, cleans = 0;
+            uint32_t cnt = 0, qn = 0, cleans = 0, both = 0, alone = 0;   // phases; of a slot's barriers: bit s
             bool ok = true;
             Piece p = first_piece();
             for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
                 const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                const int n0 = lane_tiles(p, 0), n1 = lane_tiles(p, 1);
-                auto wait_full = [&](int step) {
-                    if (mbar_wait(&full[step % a.stages], (uint32_t)(step / a.stages) & 1u)) return true;
-                    ok = false;
-                    return false;
+                const int nl = lane_tiles(p, L);
+                auto wait_full = [&](int slot) {
+                    uint64_t* bar = &full[(pair ? 0 : 1 + L) * NST + slot];
+                    const uint32_t ph = ((pair ? both : alone) >> slot) & 1u;
+                    if (pair) both ^= 1u << slot; else alone ^= 1u << slot;
+                    if (!mbar_wait(bar, ph)) ok = false;
+                    return ok;
                 };
-                auto score = [&](int L, int t, bool last_use) {
-                    const int st = k_step(p, pair, base, t), slot = st % a.stages;
-                    if (!wait_full(st)) return;
+                auto release = [&](int slot) {    // once the products so far are complete
+                    if (!pair) mbar_arrive(&empty[slot]);
+                    tc_commit(&empty[slot]);
+                };
+                auto score = [&](int t) {
+                    const int slot = k_step(pair, base, t) % NST;
+                    if (!wait_full(slot)) return;
                     tc_fence_after();
-                    const uint64_t qd = dq + (uint64_t)((uint32_t)(L * TILE) >> 4);
                     const uint64_t kd = dk + (uint64_t)((uint32_t)(slot * TILE) >> 4);
-                    const uint32_t d = tmem + (uint32_t)L * 128u;
 #pragma unroll
                     for (int kk = 0; kk < DH / 16; ++kk) {
                         const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                        tc_mma_f16(d, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+                        tc_mma_f16(s_at, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
                     }
                     tc_commit(&s_full[L]);
-                    if (last_use) tc_commit(&empty[slot]);
+                    release(slot);
                 };
-                auto weigh = [&](int L, int t, bool first, bool last_use) {   // O += P V
-                    const int st = v_step(p, pair, base, t), slot = st % a.stages;
-                    if (!wait_full(st)) return;
+                auto weigh = [&](int t, bool first) {   // O += P V
+                    const int slot = v_step(p, pair, base, t) % NST;
+                    if (!wait_full(slot)) return;
                     const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
-                    // cleared while the softmax runs; of two row lanes the first one asks
-                    const bool clean = (nv & 15) && (!pair || L == 0);
-                    if (clean) mbar_arrive(want);
-                    if (!mbar_wait(&p_full[L], (uint32_t)cnt[L] & 1u)) { ok = false; return; }
-                    ++cnt[L];
-                    if (clean) {
-                        if (!mbar_wait(cleared, (uint32_t)cleans & 1u)) { ok = false; return; }
+                    if (nv & 15) mbar_arrive(&want[L]);  // cleared while the softmax runs
+                    if (!mbar_wait(&p_full[L], cnt & 1u)) { ok = false; return; }
+                    ++cnt;
+                    if (nv & 15) {
+                        if (!mbar_wait(&cleared[L], cleans & 1u)) { ok = false; return; }
                         ++cleans;
                     }
                     tc_fence_after();
                     const uint64_t vd = dv + (uint64_t)((uint32_t)(slot * TILE) >> 4);
-                    const uint32_t d = tmem + O_COL + (uint32_t)L * 128u, w = tmem + (uint32_t)L * 128u;
                     if (nv > ST_KEYS - 16) {
 #pragma unroll
                         for (int kk = 0; kk < ST_KEYS / 16; ++kk)
-                            tc_mma_f16_ta(d, w + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
                                           (kk > 0 || !first) ? 1u : 0u);
                     } else {
                         for (int kk = 0; kk < (nv + 15) / 16; ++kk)
-                            tc_mma_f16_ta(d, w + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
                                           (kk > 0 || !first) ? 1u : 0u);
                     }
                     tc_commit(&pv_done[L]);
-                    if (last_use) tc_commit(&empty[slot]);
+                    release(slot);
                 };
-                for (int L = 0; L < 2 && ok; ++L) {
-                    if ((L ? n1 : n0) == 0) continue;
-                    if (!mbar_wait(&q_ready[L], (uint32_t)qn[L] & 1u)) { ok = false; break; }
-                    ++qn[L];
-                    score(L, pair ? 0 : L, !pair || L == 1);
-                }
-                for (int s = 0; s < n0 && ok; ++s) {
-                    for (int L = 0; L < 2 && ok; ++L) {
-                        const int nl = L ? n1 : n0;
-                        if (s < nl) weigh(L, pair ? s : 2 * s + L, s == 0, !pair || L == 1);
-                        if (ok && s + 1 < nl) score(L, pair ? s + 1 : 2 * (s + 1) + L, !pair || L == 1);
+                if (nl > 0) {
+                    if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
+                    ++qn;
+                    score(pair ? 0 : L);
+                    for (int s = 0; s < nl && ok; ++s) {
+                        weigh(pair ? s : 2 * s + L, s == 0);
+                        if (ok && s + 1 < nl) score(pair ? s + 1 : 2 * (s + 1) + L);
                     }
                 }
                 base += 2 * p.n;
             }
             if (!ok) *abort_flag = 1;
-            tc_commit(drain);                     // nothing of this CTA's in tensor memory in flight
-            mbar_wait(drain, 0);
+            tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
+            mbar_wait(&drain[L], 0);
         }
         __syncwarp();
         tc_fence_before();
@@ -495,16 +523,21 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     }
     if (warp == 10) {
         // ---- clear the V rows behind the last key, up to the end of its 16-key step
-        int base = 0, cleans = 0;
+        int base = 0;
+        uint32_t cleans[2] = {0, 0};
         bool ok = true;
         Piece p = first_piece();
         for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-            if (ragged(p)) {
-                const int st = v_step(p, p.sh ? a.sh_pair : a.own_pair, base, p.n - 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(want, (uint32_t)cleans & 1u)) != 0;
+            if (p.t0 + p.n == p.nt && (p.keys & 15) != 0) {
+                const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                const int st = v_step(p, pair, base, p.n - 1);
+                for (int L = 0; L < 2 && ok; ++L) {   // both of two row lanes, or the key lane that has it
+                    if (!pair && L != ((p.n - 1) & 1)) continue;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&want[L], cleans[L] & 1u)) != 0;
+                    ++cleans[L];
+                }
                 if (!ok) break;
-                ++cleans;
-                uint8_t* v = ring + (size_t)(st % a.stages) * TILE;
+                uint8_t* v = ring + (size_t)(st % NST) * TILE;
                 const int nv = p.keys - (p.nt - 1) * ST_KEYS, rows = 16 - (nv & 15);
                 for (int e = lane; e < rows * 8 * HALVES; e += 32) {
                     const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
@@ -512,7 +545,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(cleared);
+                if (lane < 2 && (pair || lane == ((p.n - 1) & 1))) mbar_arrive(&cleared[lane]);
             }
             base += 2 * p.n;
         }
@@ -636,21 +669,27 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 }
                 if (move) m_run = m_new;
                 const float mb = m_run == -INFINITY ? 0.f : m_run;   // only -inf scores so far: weights 0
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sl2 = st_pair(sl, sl), mb2 = st_pair(-mb, -mb);
+                uint64_t sum0 = 0, sum1 = 0;      // two fp32 each
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {     // 32 keys: 16 columns of weights
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float e0 = ex2_approx_ftz(fmaf(__uint_as_float(x[2 * c + j / 8][(2 * j) & 15]), sl, -mb));
-                        const float e1 = ex2_approx_ftz(fmaf(__uint_as_float(x[2 * c + j / 8][(2 * j + 1) & 15]), sl, -mb));
-                        ls[j & 1] += e0;
-                        ls[2 + (j & 1)] += e1;
+                        const uint32_t* at = &x[2 * c + j / 8][(2 * j) & 15];
+                        float e0, e1;
+                        st_split(st_fma2(st_pair(__uint_as_float(at[0]), __uint_as_float(at[1])), sl2, mb2), e0, e1);
+                        e0 = ex2_approx_ftz(e0);
+                        e1 = ex2_approx_ftz(e1);
+                        if (j & 1) sum1 = st_add2(sum1, st_pair(e0, e1));
+                        else sum0 = st_add2(sum0, st_pair(e0, e1));
                         w[j] = st_pack(e0, e1);
                     }
                     tmem_st16(trow + s_col + (uint32_t)(c * 16), w);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                float l0, l1;
+                st_split(st_add2(sum0, sum1), l0, l1);
+                l += l0 + l1;
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -965,8 +1004,13 @@ bool make_rows_map(CUtensorMap* m, const void* base, int dh, int rows, int heads
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DH>
-cudaError_t launch_tensor(const evs_shared_attn_args& c, SharedArgs& a, int grid, cudaStream_t stream) {
+// alignment, two Q tiles, the barriers, lengths and their running sums, the ring
+constexpr int tc_smem(int dh, int stages, int batch) {
+    return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (4 * stages + 14) * 8 + (2 * batch + 1) * 4 + 16;
+}
+
+template <int DH, int NST>
+cudaError_t launch_tensor(const evs_shared_attn_args& c, const SharedArgs& a, int grid, cudaStream_t stream) {
     CUtensorMap kp, vp, ko, vo;
     bool ok = true;
     if (c.prefix > 0)
@@ -978,21 +1022,11 @@ cudaError_t launch_tensor(const evs_shared_attn_args& c, SharedArgs& a, int grid
     if (!ok) return cudaErrorInvalidValue;
     if (c.prefix == 0) { kp = ko; vp = vo; }
     if (c.own_max == 0) { ko = kp; vo = vp; }
-    constexpr int TILE = ST_KEYS * DH * 2;
-    const int es = c.q_dtype == EVS_DTYPE_BF16 ? 2 : 4;
-    a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld * es % 16 == 0;
-    int dev = 0, optin = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    const int smem = tc_smem(DH, NST, c.batch);
+    const cudaError_t e =
+        cudaFuncSetAttribute(shared_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // alignment, two Q tiles, 11 barriers beside the ring's, lengths and their running sums
-    const int fixed = 1024 + 2 * TILE + 11 * 8 + (2 * c.batch + 1) * 4 + 64;
-    a.stages = (optin - 256 - fixed) / (TILE + 16);   // 256: the static part
-    if (a.stages > 12) a.stages = 12;
-    const int smem = fixed + a.stages * (TILE + 16);
-    e = cudaFuncSetAttribute(shared_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return launch_s(stream, shared_tc_kernel<DH>, dim3(grid), dim3(ST_THREADS), (size_t)smem, kp, vp, ko, vo, a);
+    return launch_s(stream, shared_tc_kernel<DH, NST>, dim3(grid), dim3(ST_THREADS), (size_t)smem, kp, vp, ko, vo, a);
 }
 
 }  // namespace
@@ -1011,12 +1045,16 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     int grid_tc = 0;
     const bool tensor = tensor_ok(c) && plan_tensor(c, a, grid_tc);
     if (!tensor) plan_simt(c, a);
+    a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld * (a.q_bf16 ? 2 : 4) % 16 == 0;
     carve_partials(c, a, (char*)c.workspace);
     const int sh_items = c.kv_heads * a.sh_slots * ((a.sh_rows + SA_Q - 1) / SA_Q);
     const int own_items = c.batch * c.kv_heads * a.own_slots * ((a.own_rows + SA_Q - 1) / SA_Q);
     cudaError_t e = cudaSuccess;
     if (tensor)
-        e = c.head_dim == 128 ? launch_tensor<128>(c, a, grid_tc, stream) : launch_tensor<64>(c, a, grid_tc, stream);
+        // the ring takes what 227 KB leave: five tiles of 32 KB, four where the lengths need their place
+        e = c.head_dim == 64                                 ? launch_tensor<64, 8>(c, a, grid_tc, stream)
+            : tc_smem(128, 5, c.batch) <= 227 * 1024 - 256 ? launch_tensor<128, 5>(c, a, grid_tc, stream)
+                                                             : launch_tensor<128, 4>(c, a, grid_tc, stream);
     else if (sh_items + own_items > 0)
         e = half ? launch_s(stream, shared_simt_kernel<bf16>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items)
                  : launch_s(stream, shared_simt_kernel<float>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items);
