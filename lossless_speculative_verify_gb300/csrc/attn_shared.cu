@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
 //   S[q][key] = Q K^T (fp32, 128 columns) -> registers, one thread a row: running maximum, exp2,
 //   sum -> bf16 weights back over the first half of S's columns -> O += P V with P read from
 //   tensor memory, V MN-major from shared memory.
+// The lanes' softmaxes take turns: left alone the two fall into step, both in the softmax and then
+// both waiting for the tensor core (5550 cycles for two tiles, 3100 of them softmax).
 // The running maximum moves only when it grows by more than 2^8, as few rescales of O as that.
 // A tile that the keys end in takes only the 16-key steps that hold keys, the rows behind them in
 // the last step cleared in shared memory (they may hold anything, NaN included).
@@ -226,6 +228,12 @@ __device__ __forceinline__ uint64_t st_add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ float st_max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // One CTA's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys. `seg` numbers
 // the prefix's segments or the own rows' ones.
 struct Piece {
@@ -258,7 +266,8 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     uint64_t* q_ready = pv_done + 2;                           // [2] Q of a piece staged
     uint64_t* want = q_ready + 2;                              // [2] a tile to clear is in the ring
     uint64_t* cleared = want + 2;                              // [2]
-    uint64_t* drain = cleared + 2;                             // [2]
+    uint64_t* turn = cleared + 2;                              // [2] the other lane's softmax is through
+    uint64_t* drain = turn + 2;                                // [2]
     int* pre = reinterpret_cast<int*>(drain + 2);              // [B + 1] own tiles before sequence b
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -276,6 +285,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             mbar_init(&q_ready[i], 4);
             mbar_init(&want[i], 1);
             mbar_init(&cleared[i], 1);
+            mbar_init(&turn[i], 4);
             mbar_init(&drain[i], 1);
         }
         *abort_flag = 0;
@@ -379,180 +389,192 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     auto v_step = [&](const Piece& p, bool pair, int base, int t) {
         return base + (pair ? 2 * t + 1 : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
     };
-    if (warp == 8) {
-        if (lane == 0) {
-            // ---- TMA
-            const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
-            int issued = 0;
-            uint32_t par[3] = {0, 0, 0}, kind0 = 0, kind1 = 0;   // bit s: slot s
-            bool ok = true;
-            Piece p = first_piece();
-            for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-                const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
-                auto load = [&](const CUtensorMap* m, int t) {
-                    const int s = issued % NST;
-                    if (issued >= NST && !mbar_wait(&empty[s], ((uint32_t)(issued / NST) & 1u) ^ 1u)) {
-                        ok = false;
-                        return;
+    // The softmax threads hold a row of scores each: they take registers that the other warps leave
+    // (of the launch's 384 x 168: 256 x 208 + 128 x 80).
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 8) {
+            if (lane == 0) {
+                // ---- TMA
+                const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
+                int issued = 0;
+                uint32_t par[3] = {0, 0, 0}, kind0 = 0, kind1 = 0;   // bit s: slot s
+                bool ok = true;
+                Piece p = first_piece();
+                for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
+                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                    const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
+                    auto load = [&](const CUtensorMap* m, int t) {
+                        const int s = issued % NST;
+                        if (issued >= NST && !mbar_wait(&empty[s], ((uint32_t)(issued / NST) & 1u) ^ 1u)) {
+                            ok = false;
+                            return;
+                        }
+                        const int kd = pair ? 0 : 1 + (t & 1);
+                        uint64_t* bar = &full[kd * NST + s];
+                        uint8_t* dst = ring + (size_t)s * TILE;
+                        mbar_arrive_expect_tx(bar, (uint32_t)TILE);
+    #pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, bar, pol);
+                        par[0] ^= kd == 0 ? 1u << s : 0u;
+                        par[1] ^= kd == 1 ? 1u << s : 0u;
+                        par[2] ^= kd == 2 ? 1u << s : 0u;
+                        kind0 = (kind0 & ~(1u << s)) | (uint32_t)(kd & 1) << s;
+                        kind1 = (kind1 & ~(1u << s)) | (uint32_t)(kd >> 1) << s;
+                        ++issued;
+                    };
+                    const CUtensorMap *mk = p.sh ? &tmKP : &tmKO, *mv = p.sh ? &tmVP : &tmVO;
+                    const int ahead = pair ? 1 : 2;
+                    for (int t = 0; t < min(ahead, p.n) && ok; ++t) load(mk, t);
+                    for (int t = 0; t < p.n && ok; ++t) {
+                        load(mv, t);
+                        if (ok && t + ahead < p.n) load(mk, t + ahead);
                     }
-                    const int kd = pair ? 0 : 1 + (t & 1);
-                    uint64_t* bar = &full[kd * NST + s];
-                    uint8_t* dst = ring + (size_t)s * TILE;
-                    mbar_arrive_expect_tx(bar, (uint32_t)TILE);
-#pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, bar, pol);
-                    par[0] ^= kd == 0 ? 1u << s : 0u;
-                    par[1] ^= kd == 1 ? 1u << s : 0u;
-                    par[2] ^= kd == 2 ? 1u << s : 0u;
-                    kind0 = (kind0 & ~(1u << s)) | (uint32_t)(kd & 1) << s;
-                    kind1 = (kind1 & ~(1u << s)) | (uint32_t)(kd >> 1) << s;
-                    ++issued;
-                };
-                const CUtensorMap *mk = p.sh ? &tmKP : &tmKO, *mv = p.sh ? &tmVP : &tmVO;
-                const int ahead = pair ? 1 : 2;
-                for (int t = 0; t < min(ahead, p.n) && ok; ++t) load(mk, t);
-                for (int t = 0; t < p.n && ok; ++t) {
-                    load(mv, t);
-                    if (ok && t + ahead < p.n) load(mk, t + ahead);
+                }
+                // loads in flight into this CTA's shared memory end before it does (bounded): only
+                // where the pipeline gave up are there any
+                if (!ok) {
+                    *abort_flag = 1;
+                    for (int s = 0; s < min(issued, NST); ++s) {
+                        const int kd = (int)((kind0 >> s) & 1u) + 2 * (int)((kind1 >> s) & 1u);
+                        const uint32_t bits = kd == 0 ? par[0] : (kd == 1 ? par[1] : par[2]);
+                        mbar_wait(&full[kd * NST + s], ((bits >> s) & 1u) ^ 1u);
+                    }
                 }
             }
-            // loads in flight into this CTA's shared memory end before it does (bounded): only
-            // where the pipeline gave up are there any
-            if (!ok) {
-                *abort_flag = 1;
-                for (int s = 0; s < min(issued, NST); ++s) {
-                    const int kd = (int)((kind0 >> s) & 1u) + 2 * (int)((kind1 >> s) & 1u);
-                    const uint32_t bits = kd == 0 ? par[0] : (kd == 1 ? par[1] : par[2]);
-                    mbar_wait(&full[kd * NST + s], ((bits >> s) & 1u) ^ 1u);
-                }
-            }
+            __syncwarp();
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            tmem_dealloc(tmem, 512);
+            return;
         }
-        __syncwarp();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-        return;
-    }
-    if (warp == 9 || warp == 11) {
-        if (lane == 0) {
-            // ---- MMA of lane L
-            const int L = warp == 9 ? 0 : 1;
-            constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
-            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
-                           dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
-            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + O_COL + (uint32_t)L * 128u;
-            int base = 0;                  // ring steps of earlier pieces
-            uint32_t cnt = 0, qn = 0, cleans = 0, both = 0, alone = 0;   // phases; of a slot's barriers: bit s
+        if (warp == 9 || warp == 11) {
+            if (lane == 0) {
+                // ---- MMA of lane L
+                const int L = warp == 9 ? 0 : 1;
+                constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
+                const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
+                               dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
+                const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + O_COL + (uint32_t)L * 128u;
+                int base = 0;                  // ring steps of earlier pieces
+                uint32_t cnt = 0, qn = 0, cleans = 0, both = 0, alone = 0;   // phases; of a slot's barriers: bit s
+                bool ok = true;
+                Piece p = first_piece();
+                for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
+                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                    const int nl = lane_tiles(p, L);
+                    auto wait_full = [&](int slot) {
+                        uint64_t* bar = &full[(pair ? 0 : 1 + L) * NST + slot];
+                        const uint32_t ph = ((pair ? both : alone) >> slot) & 1u;
+                        if (pair) both ^= 1u << slot; else alone ^= 1u << slot;
+                        if (!mbar_wait(bar, ph)) ok = false;
+                        return ok;
+                    };
+                    auto release = [&](int slot) {    // once the products so far are complete
+                        if (!pair) mbar_arrive(&empty[slot]);
+                        tc_commit(&empty[slot]);
+                    };
+                    auto score = [&](int slot) {      // S = Q K^T
+                        const uint64_t kd = dk + (uint64_t)((uint32_t)(slot * TILE) >> 4);
+    #pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk) {
+                            const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            tc_mma_f16(s_at, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+                        }
+                    };
+                    if (nl > 0) {
+                        if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
+                        ++qn;
+                        int ks = k_step(pair, base, pair ? 0 : L) % NST;
+                        if (!wait_full(ks)) break;
+                        tc_fence_after();
+                        score(ks);
+                        tc_commit(&s_full[L]);
+                        release(ks);
+                    }
+                    for (int s = 0; s < nl; ++s) {
+                        // O += P V of this tile, then the next one's scores before any of the commits
+                        const int t = pair ? s : 2 * s + L, vs = v_step(p, pair, base, t) % NST;
+                        const bool next = s + 1 < nl;
+                        if (!wait_full(vs)) break;
+                        const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+                        if (nv & 15) mbar_arrive(&want[L]);  // cleared while the softmax runs
+                        const int ks = next ? k_step(pair, base, t + (pair ? 1 : 2)) % NST : 0;
+                        if (next && !wait_full(ks)) break;
+                        if (!mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
+                        ++cnt;
+                        if (nv & 15) {
+                            if (!mbar_wait(&cleared[L], cleans & 1u)) { ok = false; break; }
+                            ++cleans;
+                        }
+                        tc_fence_after();
+                        const uint64_t vd = dv + (uint64_t)((uint32_t)(vs * TILE) >> 4);
+                        if (nv > ST_KEYS - 16) {
+    #pragma unroll
+                            for (int kk = 0; kk < ST_KEYS / 16; ++kk)
+                                tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                              (kk > 0 || s > 0) ? 1u : 0u);
+                        } else {
+                            for (int kk = 0; kk < (nv + 15) / 16; ++kk)
+                                tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                              (kk > 0 || s > 0) ? 1u : 0u);
+                        }
+                        if (next) {
+                            score(ks);
+                            tc_commit(&s_full[L]);
+                            release(ks);
+                        }
+                        release(vs);
+                        tc_commit(&pv_done[L]);
+                    }
+                    base += 2 * p.n;
+                }
+                if (!ok) *abort_flag = 1;
+                tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
+                mbar_wait(&drain[L], 0);
+            }
+            __syncwarp();
+            tc_fence_before();
+            __syncthreads();
+            return;
+        }
+        if (warp == 10) {
+            // ---- clear the V rows behind the last key, up to the end of its 16-key step
+            int base = 0;
+            uint32_t cleans[2] = {0, 0};
             bool ok = true;
             Piece p = first_piece();
             for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-                const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                const int nl = lane_tiles(p, L);
-                auto wait_full = [&](int slot) {
-                    uint64_t* bar = &full[(pair ? 0 : 1 + L) * NST + slot];
-                    const uint32_t ph = ((pair ? both : alone) >> slot) & 1u;
-                    if (pair) both ^= 1u << slot; else alone ^= 1u << slot;
-                    if (!mbar_wait(bar, ph)) ok = false;
-                    return ok;
-                };
-                auto release = [&](int slot) {    // once the products so far are complete
-                    if (!pair) mbar_arrive(&empty[slot]);
-                    tc_commit(&empty[slot]);
-                };
-                auto score = [&](int t) {
-                    const int slot = k_step(pair, base, t) % NST;
-                    if (!wait_full(slot)) return;
-                    tc_fence_after();
-                    const uint64_t kd = dk + (uint64_t)((uint32_t)(slot * TILE) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < DH / 16; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                        tc_mma_f16(s_at, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+                if (p.t0 + p.n == p.nt && (p.keys & 15) != 0) {
+                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                    const int st = v_step(p, pair, base, p.n - 1);
+                    for (int L = 0; L < 2 && ok; ++L) {   // both of two row lanes, or the key lane that has it
+                        if (!pair && L != ((p.n - 1) & 1)) continue;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&want[L], cleans[L] & 1u)) != 0;
+                        ++cleans[L];
                     }
-                    tc_commit(&s_full[L]);
-                    release(slot);
-                };
-                auto weigh = [&](int t, bool first) {   // O += P V
-                    const int slot = v_step(p, pair, base, t) % NST;
-                    if (!wait_full(slot)) return;
-                    const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
-                    if (nv & 15) mbar_arrive(&want[L]);  // cleared while the softmax runs
-                    if (!mbar_wait(&p_full[L], cnt & 1u)) { ok = false; return; }
-                    ++cnt;
-                    if (nv & 15) {
-                        if (!mbar_wait(&cleared[L], cleans & 1u)) { ok = false; return; }
-                        ++cleans;
+                    if (!ok) break;
+                    uint8_t* v = ring + (size_t)(st % NST) * TILE;
+                    const int nv = p.keys - (p.nt - 1) * ST_KEYS, rows = 16 - (nv & 15);
+                    for (int e = lane; e < rows * 8 * HALVES; e += 32) {
+                        const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
+                        *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    tc_fence_after();
-                    const uint64_t vd = dv + (uint64_t)((uint32_t)(slot * TILE) >> 4);
-                    if (nv > ST_KEYS - 16) {
-#pragma unroll
-                        for (int kk = 0; kk < ST_KEYS / 16; ++kk)
-                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
-                                          (kk > 0 || !first) ? 1u : 0u);
-                    } else {
-                        for (int kk = 0; kk < (nv + 15) / 16; ++kk)
-                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
-                                          (kk > 0 || !first) ? 1u : 0u);
-                    }
-                    tc_commit(&pv_done[L]);
-                    release(slot);
-                };
-                if (nl > 0) {
-                    if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
-                    ++qn;
-                    score(pair ? 0 : L);
-                    for (int s = 0; s < nl && ok; ++s) {
-                        weigh(pair ? s : 2 * s + L, s == 0);
-                        if (ok && s + 1 < nl) score(pair ? s + 1 : 2 * (s + 1) + L);
-                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane < 2 && (pair || lane == ((p.n - 1) & 1))) mbar_arrive(&cleared[lane]);
                 }
                 base += 2 * p.n;
             }
-            if (!ok) *abort_flag = 1;
-            tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
-            mbar_wait(&drain[L], 0);
+            if (!ok && lane == 0) *abort_flag = 1;
+            __syncthreads();
+            return;
         }
-        __syncwarp();
-        tc_fence_before();
-        __syncthreads();
         return;
     }
-    if (warp == 10) {
-        // ---- clear the V rows behind the last key, up to the end of its 16-key step
-        int base = 0;
-        uint32_t cleans[2] = {0, 0};
-        bool ok = true;
-        Piece p = first_piece();
-        for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-            if (p.t0 + p.n == p.nt && (p.keys & 15) != 0) {
-                const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                const int st = v_step(p, pair, base, p.n - 1);
-                for (int L = 0; L < 2 && ok; ++L) {   // both of two row lanes, or the key lane that has it
-                    if (!pair && L != ((p.n - 1) & 1)) continue;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&want[L], cleans[L] & 1u)) != 0;
-                    ++cleans[L];
-                }
-                if (!ok) break;
-                uint8_t* v = ring + (size_t)(st % NST) * TILE;
-                const int nv = p.keys - (p.nt - 1) * ST_KEYS, rows = 16 - (nv & 15);
-                for (int e = lane; e < rows * 8 * HALVES; e += 32) {
-                    const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
-                    *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane < 2 && (pair || lane == ((p.n - 1) & 1))) mbar_arrive(&cleared[lane]);
-            }
-            base += 2 * p.n;
-        }
-        if (!ok && lane == 0) *abort_flag = 1;
-        __syncthreads();
-        return;
-    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax of lane L: thread = row r of the lane's tile
     const int L = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
@@ -610,6 +632,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         if (lane == 0) mbar_arrive(&q_ready[L]);
     };
     int cnt = 0;
+    uint32_t took = 0;
     bool ok = true;
     Piece p = first_piece();
     if (lo < hi && lane_tiles(p, L) > 0) {
@@ -626,15 +649,28 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         const bool feed = more && lane_tiles(nx, L) > 0;
         float m_run = -INFINITY, l = 0.f;
         if (nl == 0 && feed) stage(nx);
-        for (int s = 0; s < nl; ++s) {
+        const int turns = lane_tiles(p, 0);       // lane 1 may have a tile less: it still passes its turn on
+        for (int s = 0; s < turns; ++s) {
+            // lane 1's turn s follows lane 0's, lane 0's turn s + 1 lane 1's
+            const uint32_t phase = L ? took & 1u : (took & 1u) ^ 1u;
+            const bool wait_turn = L == 1 || took > 0;
+            ++took;
+            if (s >= nl) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&turn[L], phase))) { ok = false; break; }
+                if (lane == 0) mbar_arrive(&turn[L ^ 1]);
+                continue;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[L], (uint32_t)cnt & 1u))) { ok = false; break; }
             if (s == nl - 1 && feed) stage(nx);   // this piece's last scores are out: Q's place is free
+            uint32_t x[8][16];
             if (work) {
                 tc_fence_after();
-                uint32_t x[8][16];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) tmem_ld16_issue(trow + s_col + (uint32_t)(c * 16), x[c]);
                 tmem_wait_ld();
+            }
+            if (wait_turn && !__all_sync(0xffffffffu, mbar_wait(&turn[L], phase))) { ok = false; break; }
+            if (work) {
                 const int t = pair ? s : 2 * s + L;
                 const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
                 if (nv < ST_KEYS) {               // keys behind the last one: no weight
@@ -648,7 +684,8 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[c][j]));
+                    for (int j = 0; j < 16; j += 2)
+                        mx[(j >> 1) & 3] = st_max3(mx[(j >> 1) & 3], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
                 const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl);
                 const bool move = m_new > m_run + ST_RESCALE_LOG2 || (m_run == -INFINITY && m_new > -INFINITY);
                 if (s > 0 && __any_sync(0xffffffffu, move)) {
@@ -690,6 +727,10 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 float l0, l1;
                 st_split(st_add2(sum0, sum1), l0, l1);
                 l += l0 + l1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&turn[L ^ 1]);
+            if (work) {
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -1006,7 +1047,7 @@ bool make_rows_map(CUtensorMap* m, const void* base, int dh, int rows, int heads
 
 // alignment, two Q tiles, the barriers, lengths and their running sums, the ring
 constexpr int tc_smem(int dh, int stages, int batch) {
-    return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (4 * stages + 14) * 8 + (2 * batch + 1) * 4 + 16;
+    return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (4 * stages + 16) * 8 + (2 * batch + 1) * 4 + 16;
 }
 
 template <int DH, int NST>
