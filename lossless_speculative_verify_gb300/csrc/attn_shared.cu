@@ -20,7 +20,9 @@ using bf16 = __nv_bfloat16;
 // What both launches know. A partial of a shared row r of K/V head g (r = m * group + head in the
 // group, m = (b * C + c) * T + i) lies in segment g * sh_tiles + r / sh_rows, row r % sh_rows; of
 // an own row r = (c * T + i) * group + head in segment (b * G + g) * own_tiles + r / own_rows.
-// Segments have `slots` partials of `rows` rows each.
+// Segments have `slots` partials. o is stored four columns at a time, [dh / 4][rows to a multiple
+// of four][4], so that both the threads that write it (one a row) and those that read it (four
+// columns each) touch consecutive addresses.
 struct SharedArgs {
     const void *q, *kp, *vp, *ko, *vo, *kb, *vb;
     void* o;
@@ -30,14 +32,16 @@ struct SharedArgs {
     int64_t q_ld, o_ld, p_row, p_head, o_row, o_head, o_seq, b_row, b_head, b_cand;
     int B, C, T, H, G, dh, P, own_max, own_skip, q_bf16;
     float scale;
-    float *sh_o, *own_o;       // [segment][slot][rows][dh]
+    float *sh_o, *own_o;       // [segment][slot][dh / 4][rows4][4]
     float2 *sh_ml, *own_ml;    // [segment][slot][rows] (m, l), natural units
     int sh_rows, sh_tiles, sh_slots, own_rows, own_tiles, own_slots;
     int tensor;                // the tensor-core kernel's partials: slots by its runs of tiles
-    int sh_pair, own_pair;     // 1: 256-row segments, a row tile per lane; 0: a lane per key tile
-    int* plan;                 // tiles per run, then the running sum of own tiles per sequence
-    int q_vec;
+    int sh_pair, own_pair;     // 1: segments of up to 256 rows, a row tile a lane; 0: a lane of its own
+    int* plan;                 // run lengths (shared, own), where own runs start, own costs before sequence b
+    int q_vec, b_vec;          // q and block rows on 16 (8) bytes
 };
+
+__host__ __device__ inline int rows4(int rows) { return (rows + 3) & ~3; }
 
 // fp32 problems keep the full precision of the exponential
 template <typename T> __device__ __forceinline__ float exp_of(float x);
@@ -157,42 +161,45 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
     }
     const int r = r0 + orow;
     if (r < rows) {
-        const int64_t at = ((int64_t)seg * slots + slot) * rows + r;
-        float* dst = (sh ? a.sh_o : a.own_o) + at * dh;
+        const int64_t at = (int64_t)seg * slots + slot;
+        float* dst = (sh ? a.sh_o : a.own_o) + at * rows4(rows) * dh + r * 4;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (ocol + 16 * u < dh) dst[ocol + 16 * u] = o[u];
-        if (ocol == 0) (sh ? a.sh_ml : a.own_ml)[at] = make_float2(row_m[orow], row_l[orow]);
+        for (int u = 0; u < 8; ++u) {
+            const int c = ocol + 16 * u;
+            if (c < dh) dst[(int64_t)(c >> 2) * rows4(rows) * 4 + (c & 3)] = o[u];
+        }
+        if (ocol == 0) (sh ? a.sh_ml : a.own_ml)[at * rows + r] = make_float2(row_m[orow], row_l[orow]);
     }
 }
 
 // =========================================================================================
 // Partials on the tensor cores (bf16, head width 64 or 128).
 //
-// Work: 128-key tiles of every segment (a K/V head of the prefix with up to 256 query rows, or
-// of one sequence's own rows) laid end to end; each of up to 152 persistent CTAs takes an equal
-// run of tiles, so ragged lengths balance on the device. A run may cross segments; each piece of
-// a segment leaves its own partials.
+// Work: the 128-key tiles of every segment (a K/V head of the prefix with up to 256 query rows, or
+// of one sequence's own rows) laid end to end, a segment's first tile behind ST_OVER tiles' worth of
+// its own cost; workers take equal runs of that axis, so ragged lengths balance on the device. A
+// run may cross segments; each piece of a segment leaves its own partials.
 //
-// Two lanes of work share a CTA, each with its own score, weight and output columns in tensor
-// memory and its own four softmax warps. In a segment of more than 128 rows the lanes are two row
-// tiles and each K/V tile that TMA brings serves both; otherwise they are alternate key tiles of
-// the same rows. While one lane's softmax runs, the tensor core works for the other:
+// A CTA has two lanes, each with its own score, weight and output columns in tensor memory, four
+// softmax warps and a thread that issues its products. In segments of more than 128 rows the CTA is
+// the worker: its lanes are two row tiles, and each K/V tile that TMA brings serves both. Otherwise
+// each lane is a worker of its own, with half of the ring. Where the prefix is of the one kind and
+// the own rows of the other, the CTAs are divided by cost.
 //   S[q][key] = Q K^T (fp32, 128 columns) -> registers, one thread a row: running maximum, exp2,
 //   sum -> bf16 weights back over the first half of S's columns -> O += P V with P read from
 //   tensor memory, V MN-major from shared memory.
-// The lanes' softmaxes take turns: left alone the two fall into step, both in the softmax and then
-// both waiting for the tensor core (5550 cycles for two tiles, 3100 of them softmax).
+// Two row lanes take turns at the softmax: left alone they fall into step, both in it and then both
+// waiting for the tensor core (5550 cycles for two tiles instead of 4150).
 // The running maximum moves only when it grows by more than 2^8, as few rescales of O as that.
 // A tile that the keys end in takes only the 16-key steps that hold keys, the rows behind them in
 // the last step cleared in shared memory (they may hold anything, NaN included).
 //
 // Tensor memory, columns: S/P of lane 0 and 1 at 0 and 128, O at 256 and 384.
-// Warps 0-3 and 4-7: the lanes' softmax and epilogue; warp 8: TMA; warps 9 and 11: one thread each
-// issues a lane's products. Issuing eight of them takes as long as they run (512 cycles), and the
-// waits and commits between two groups about 1600 more; with one thread for both lanes those
-// left the tensor core idle half of the time. Warp 10 clears the rows behind a piece's last key.
+// Warps 0-3 and 4-7: the lanes' softmax and epilogue; 8 and 10: TMA; 9 and 11: products. Issuing
+// eight products takes as long as they run (512 cycles), the waits and commits between two groups
+// about 1600 more: one thread for both lanes left the tensor core idle half of the time.
 // =========================================================================================
+constexpr int ST_OVER = 1;
 constexpr int ST_KEYS = 128;
 constexpr int ST_THREADS = 384;
 constexpr float ST_RESCALE_LOG2 = 8.f;
@@ -234,10 +241,10 @@ __device__ __forceinline__ float st_max3(float a, float b, float c) {
     return r;
 }
 
-// One CTA's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys. `seg` numbers
-// the prefix's segments or the own rows' ones.
+// A worker's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys; start: where
+// the segment lies on the axis; seg numbers the prefix's segments or the own rows' ones.
 struct Piece {
-    int sh, b, g, rt, t0, n, nt, keys, slot, seg;
+    int sh, b, g, rt, t0, n, nt, keys, slot, seg, start;
 };
 
 template <int DH, int NST>
@@ -254,49 +261,32 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* sQ = smem;                                        // [2 lanes][halves][128 rows][128 B]
-    uint8_t* ring = sQ + 2 * TILE;                             // [stages]
-    // A ring slot has three "full" barriers, for a tile that both lanes use and for one of lane 0
-    // or 1 alone: whoever waits on one of them has waited on all its earlier phases, so a phase's
-    // parity is enough.
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)NST * TILE);   // [3][NST]
-    uint64_t* empty = full + 3 * NST;                          // [NST], two arrivals
+    uint8_t* ring = sQ + 2 * TILE;                             // [NST]
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)NST * TILE);   // [NST]
+    uint64_t* empty = full + NST;                              // [NST]
     uint64_t* s_full = empty + NST;                            // [2] scores of a tile in tensor memory
     uint64_t* p_full = s_full + 2;                             // [2] weights of a tile there
     uint64_t* pv_done = p_full + 2;                            // [2] P V of a tile complete
     uint64_t* q_ready = pv_done + 2;                           // [2] Q of a piece staged
-    uint64_t* want = q_ready + 2;                              // [2] a tile to clear is in the ring
-    uint64_t* cleared = want + 2;                              // [2]
-    uint64_t* turn = cleared + 2;                              // [2] the other lane's softmax is through
+    uint64_t* turn = q_ready + 2;                              // [2] the other lane's softmax is through
     uint64_t* drain = turn + 2;                                // [2]
-    int* pre = reinterpret_cast<int*>(drain + 2);              // [B + 1] own tiles before sequence b
+    int* pre = reinterpret_cast<int*>(drain + 2);              // [B + 1] cost of one head's own rows before b
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_trigger();
     pdl_wait();
     for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
-    if (tid == 0) {
-        for (int s = 0; s < 3 * NST; ++s) mbar_init(&full[s], 1);
-        for (int s = 0; s < NST; ++s) mbar_init(&empty[s], 2);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&pv_done[i], 1);
-            mbar_init(&q_ready[i], 4);
-            mbar_init(&want[i], 1);
-            mbar_init(&cleared[i], 1);
-            mbar_init(&turn[i], 4);
-            mbar_init(&drain[i], 1);
-        }
-        *abort_flag = 0;
-        fence_barrier_init();
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
     }
     __syncthreads();
     if (warp == 0) {
         int run = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            int x = b < a.B ? (len[b] + ST_KEYS - 1) / ST_KEYS : 0;
+            int x = b < a.B && len[b] > 0 ? (len[b] + ST_KEYS - 1) / ST_KEYS + ST_OVER : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -307,65 +297,102 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         }
         if (lane == 0) pre[0] = 0;
     }
-    if (warp == 8) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
+    __syncthreads();
+    // ---- this CTA's axis: the prefix's tiles and then the own ones, or one of the two
+    const int ntp = (a.P + ST_KEYS - 1) / ST_KEYS, per_b = a.G * a.own_tiles;
+    const int sh_cost = ntp ? a.G * a.sh_tiles * (ntp + ST_OVER) : 0, own_cost = per_b * pre[a.B];
+    const int grid = gridDim.x;
+    const bool split = a.sh_pair != a.own_pair && sh_cost > 0 && own_cost > 0;
+    const int n_sh = split ? min(grid - 1, max(1, (int)(((long long)grid * sh_cost + (sh_cost + own_cost) / 2) /
+                                                        (sh_cost + own_cost))))
+                           : grid;
+    const bool on_sh = split ? (int)blockIdx.x < n_sh : sh_cost > 0;      // axis starts with the prefix
+    const bool rows2 = (on_sh ? a.sh_pair : a.own_pair) != 0;             // lanes are two row tiles
+    auto run_of = [&](int cost, int ctas, int pair) { return max(1, (cost + ctas * (2 - pair) - 1) / (ctas * (2 - pair))); };
+    const int sh_run = run_of(split ? sh_cost : sh_cost + own_cost, n_sh, sh_cost > 0 ? a.sh_pair : a.own_pair);
+    const int own_run = split ? run_of(own_cost, grid - n_sh, a.own_pair) : sh_run;
+    const int own_at = split ? 0 : sh_cost;                               // where the own tiles start
+    const int total = split ? (on_sh ? sh_cost : own_cost) : sh_cost + own_cost;
+    const int W = on_sh ? sh_run : own_run;
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= a.B; b += ST_THREADS) a.plan[3 + b] = pre[b];
+        if (tid == 0) {
+            a.plan[0] = sh_run;
+            a.plan[1] = own_run;
+            a.plan[2] = own_at;
+        }
+    }
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], rows2 ? 2 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&q_ready[i], 4);
+            mbar_init(&turn[i], 4);
+            mbar_init(&drain[i], 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int ntp = (a.P + ST_KEYS - 1) / ST_KEYS;
-    const int sh_total = a.G * a.sh_tiles * ntp, per_b = a.G * a.own_tiles;
-    const int total = sh_total + per_b * pre[a.B];
-    const int W = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-    const int lo = min(total, W * (int)blockIdx.x), hi = min(lo + W, total);
-    if (blockIdx.x == 0) {
-        for (int b = tid; b <= a.B; b += ST_THREADS) a.plan[1 + b] = pre[b];
-        if (tid == 0) a.plan[0] = W;
-    }
-    // the CTA's first piece, and the one behind p (pos: where it starts), the same for every role
+
+    // Lane L's run of the axis and slots of the ring
+    const int L = warp < 8 ? warp >> 2 : (warp < 10 ? 0 : 1);
+    const int cta = (int)blockIdx.x - (split && !on_sh ? n_sh : 0), worker = rows2 ? cta : 2 * cta + L;
+    const int lo = min(total, W * worker), hi = min(lo + W, total);
+    const int slot0 = rows2 || L == 0 ? 0 : NST / 2, nslots = rows2 ? NST : NST / 2;
+    // the run's first piece, and the one behind p; n = 0: none
     auto first_piece = [&]() -> Piece {
         Piece p;
-        int start;
-        if (lo < sh_total) {
+        p.n = 0;
+        if (lo >= hi) return p;
+        if (on_sh && lo < sh_cost) {
             p.sh = 1;
             p.b = 0;
-            p.seg = lo / ntp;
+            p.seg = lo / (ntp + ST_OVER);
             p.g = p.seg / a.sh_tiles;
-            p.rt = p.seg % a.sh_tiles;
-            start = p.seg * ntp;
+            p.rt = p.seg - p.g * a.sh_tiles;
+            p.start = p.seg * (ntp + ST_OVER);
             p.nt = ntp;
             p.keys = a.P;
         } else {
-            const int q = lo - sh_total;
+            const int q = lo - own_at;
             int b0 = 0, b1 = a.B - 1;             // the last b with per_b * pre[b] <= q
             while (b0 < b1) {
                 const int mid = (b0 + b1 + 1) >> 1;
                 if (per_b * pre[mid] <= q) b0 = mid; else b1 = mid - 1;
             }
-            p.nt = pre[b0 + 1] - pre[b0];
-            const int r = (q - per_b * pre[b0]) / p.nt;
+            const int cost = pre[b0 + 1] - pre[b0], r = (q - per_b * pre[b0]) / cost;
+            p.nt = cost - ST_OVER;
             p.sh = 0;
             p.b = b0;
             p.g = r / a.own_tiles;
-            p.rt = r % a.own_tiles;
+            p.rt = r - p.g * a.own_tiles;
             p.seg = b0 * per_b + r;
-            start = sh_total + per_b * pre[b0] + r * p.nt;
+            p.start = own_at + per_b * pre[b0] + r * cost;
             p.keys = len[b0];
         }
-        p.t0 = lo - start;
-        p.n = min(p.nt - p.t0, hi - lo);
-        p.slot = (int)blockIdx.x - start / W;
+        p.t0 = max(0, lo - p.start - ST_OVER);
+        p.n = max(0, min(p.nt, hi - p.start - ST_OVER) - p.t0);
+        p.slot = worker - (p.start + ST_OVER) / W;
         return p;
     };
-    auto next_piece = [&](const Piece& c, int pos) -> Piece {
+    auto next_piece = [&](const Piece& c) -> Piece {
         Piece p = c;
+        p.start = c.start + c.nt + ST_OVER;
+        p.n = 0;
+        if (p.start >= hi) return p;
         p.t0 = 0;
         p.slot = 0;                               // the first run that meets its segment
         ++p.seg;
-        const int tiles = c.sh ? a.sh_tiles : a.own_tiles;
-        if (++p.rt == tiles) {
+        if (++p.rt == (c.sh ? a.sh_tiles : a.own_tiles)) {
             p.rt = 0;
             if (++p.g == a.G) {                   // on to the next sequence that has rows
                 p.g = 0;
@@ -373,220 +400,146 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 while (p.b < a.B - 1 && pre[p.b + 1] == pre[p.b]) ++p.b;
                 p.sh = 0;
                 p.seg = p.b * per_b;
-                p.nt = pre[p.b + 1] - pre[p.b];
+                p.nt = pre[p.b + 1] - pre[p.b] - ST_OVER;
                 p.keys = len[p.b];
             }
         }
-        p.n = min(p.nt, hi - pos);
+        p.n = max(0, min(p.nt, hi - p.start - ST_OVER));
         return p;
     };
-    // tiles of lane L in a piece
-    auto lane_tiles = [&](const Piece& p, int L) { return (p.sh ? a.sh_pair : a.own_pair) ? p.n : (p.n + 1 - L) / 2; };
 
-    // Ring steps: row lanes take K0 V0 K1 V1 ..., key lanes K0 K1 V0 K2 V1 K3 ... V(n-1), the order of
-    // use. The step of the K and V tile t of a piece whose first step is base:
-    auto k_step = [&](bool pair, int base, int t) { return base + (pair ? 2 * t : (t < 2 ? t : 2 * t - 1)); };
-    auto v_step = [&](const Piece& p, bool pair, int base, int t) {
-        return base + (pair ? 2 * t + 1 : min(2, p.n) + t + min(t, max(p.n - 2, 0)));
-    };
+    // Ring steps of a worker: K0 V0 K1 V1 ... over all its pieces, in the order of use.
     // The softmax threads hold a row of scores each: they take registers that the other warps leave
     // (of the launch's 384 x 168: 256 x 208 + 128 x 80).
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 8) {
-            if (lane == 0) {
+        if ((warp & 1) == 0) {
+            if (lane == 0 && (L == 0 || !rows2)) {
                 // ---- TMA
                 const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
-                int issued = 0;
-                uint32_t par[3] = {0, 0, 0}, kind0 = 0, kind1 = 0;   // bit s: slot s
+                int s = 0;
+                uint32_t ph = 1, used = 0;        // parity that a free slot has; slots in use so far
                 bool ok = true;
-                Piece p = first_piece();
-                for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
+                for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
                     const uint64_t pol = p.sh && a.sh_tiles > 1 ? keep : stream;
-                    auto load = [&](const CUtensorMap* m, int t) {
-                        const int s = issued % NST;
-                        if (issued >= NST && !mbar_wait(&empty[s], ((uint32_t)(issued / NST) & 1u) ^ 1u)) {
-                            ok = false;
-                            return;
-                        }
-                        const int kd = pair ? 0 : 1 + (t & 1);
-                        uint64_t* bar = &full[kd * NST + s];
-                        uint8_t* dst = ring + (size_t)s * TILE;
-                        mbar_arrive_expect_tx(bar, (uint32_t)TILE);
-    #pragma unroll
+                    for (int j = 0; j < 2 * p.n; ++j) {
+                        const int at = slot0 + s;
+                        if ((used >> s & 1u) && !mbar_wait(&empty[at], ph)) { ok = false; break; }
+                        used |= 1u << s;
+                        const CUtensorMap* m = p.sh ? (j & 1 ? &tmVP : &tmKP) : (j & 1 ? &tmVO : &tmKO);
+                        uint8_t* dst = ring + (size_t)at * TILE;
+                        mbar_arrive_expect_tx(&full[at], (uint32_t)TILE);
+#pragma unroll
                         for (int hf = 0; hf < HALVES; ++hf)
-                            tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + t) * ST_KEYS, p.g, p.b, bar, pol);
-                        par[0] ^= kd == 0 ? 1u << s : 0u;
-                        par[1] ^= kd == 1 ? 1u << s : 0u;
-                        par[2] ^= kd == 2 ? 1u << s : 0u;
-                        kind0 = (kind0 & ~(1u << s)) | (uint32_t)(kd & 1) << s;
-                        kind1 = (kind1 & ~(1u << s)) | (uint32_t)(kd >> 1) << s;
-                        ++issued;
-                    };
-                    const CUtensorMap *mk = p.sh ? &tmKP : &tmKO, *mv = p.sh ? &tmVP : &tmVO;
-                    const int ahead = pair ? 1 : 2;
-                    for (int t = 0; t < min(ahead, p.n) && ok; ++t) load(mk, t);
-                    for (int t = 0; t < p.n && ok; ++t) {
-                        load(mv, t);
-                        if (ok && t + ahead < p.n) load(mk, t + ahead);
+                            tma_load_4d(dst + hf * HALF, m, hf * 64, (p.t0 + (j >> 1)) * ST_KEYS, p.g, p.b, &full[at], pol);
+                        if (++s == nslots) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
-                // loads in flight into this CTA's shared memory end before it does (bounded): only
-                // where the pipeline gave up are there any
                 if (!ok) {
+                    // loads in flight into this CTA's shared memory end before it does (bounded)
                     *abort_flag = 1;
-                    for (int s = 0; s < min(issued, NST); ++s) {
-                        const int kd = (int)((kind0 >> s) & 1u) + 2 * (int)((kind1 >> s) & 1u);
-                        const uint32_t bits = kd == 0 ? par[0] : (kd == 1 ? par[1] : par[2]);
-                        mbar_wait(&full[kd * NST + s], ((bits >> s) & 1u) ^ 1u);
-                    }
+                    for (int i = 0; i < nslots; ++i)
+                        if (used >> i & 1u) mbar_wait(&full[slot0 + i], i < s ? ph ^ 1u : ph);
                 }
             }
             __syncwarp();
             tc_fence_before();
             __syncthreads();
-            tc_fence_after();
-            tmem_dealloc(tmem, 512);
-            return;
-        }
-        if (warp == 9 || warp == 11) {
-            if (lane == 0) {
-                // ---- MMA of lane L
-                const int L = warp == 9 ? 0 : 1;
-                constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
-                const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
-                               dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
-                const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + O_COL + (uint32_t)L * 128u;
-                int base = 0;                  // ring steps of earlier pieces
-                uint32_t cnt = 0, qn = 0, cleans = 0, both = 0, alone = 0;   // phases; of a slot's barriers: bit s
-                bool ok = true;
-                Piece p = first_piece();
-                for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                    const int nl = lane_tiles(p, L);
-                    auto wait_full = [&](int slot) {
-                        uint64_t* bar = &full[(pair ? 0 : 1 + L) * NST + slot];
-                        const uint32_t ph = ((pair ? both : alone) >> slot) & 1u;
-                        if (pair) both ^= 1u << slot; else alone ^= 1u << slot;
-                        if (!mbar_wait(bar, ph)) ok = false;
-                        return ok;
-                    };
-                    auto release = [&](int slot) {    // once the products so far are complete
-                        if (!pair) mbar_arrive(&empty[slot]);
-                        tc_commit(&empty[slot]);
-                    };
-                    auto score = [&](int slot) {      // S = Q K^T
-                        const uint64_t kd = dk + (uint64_t)((uint32_t)(slot * TILE) >> 4);
-    #pragma unroll
-                        for (int kk = 0; kk < DH / 16; ++kk) {
-                            const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            tc_mma_f16(s_at, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
-                        }
-                    };
-                    if (nl > 0) {
-                        if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
-                        ++qn;
-                        int ks = k_step(pair, base, pair ? 0 : L) % NST;
-                        if (!wait_full(ks)) break;
-                        tc_fence_after();
-                        score(ks);
-                        tc_commit(&s_full[L]);
-                        release(ks);
-                    }
-                    for (int s = 0; s < nl; ++s) {
-                        // O += P V of this tile, then the next one's scores before any of the commits
-                        const int t = pair ? s : 2 * s + L, vs = v_step(p, pair, base, t) % NST;
-                        const bool next = s + 1 < nl;
-                        if (!wait_full(vs)) break;
-                        const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
-                        if (nv & 15) mbar_arrive(&want[L]);  // cleared while the softmax runs
-                        const int ks = next ? k_step(pair, base, t + (pair ? 1 : 2)) % NST : 0;
-                        if (next && !wait_full(ks)) break;
-                        if (!mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
-                        ++cnt;
-                        if (nv & 15) {
-                            if (!mbar_wait(&cleared[L], cleans & 1u)) { ok = false; break; }
-                            ++cleans;
-                        }
-                        tc_fence_after();
-                        const uint64_t vd = dv + (uint64_t)((uint32_t)(vs * TILE) >> 4);
-                        if (nv > ST_KEYS - 16) {
-    #pragma unroll
-                            for (int kk = 0; kk < ST_KEYS / 16; ++kk)
-                                tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
-                                              (kk > 0 || s > 0) ? 1u : 0u);
-                        } else {
-                            for (int kk = 0; kk < (nv + 15) / 16; ++kk)
-                                tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
-                                              (kk > 0 || s > 0) ? 1u : 0u);
-                        }
-                        if (next) {
-                            score(ks);
-                            tc_commit(&s_full[L]);
-                            release(ks);
-                        }
-                        release(vs);
-                        tc_commit(&pv_done[L]);
-                    }
-                    base += 2 * p.n;
-                }
-                if (!ok) *abort_flag = 1;
-                tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
-                mbar_wait(&drain[L], 0);
+            if (warp == 8) {
+                tc_fence_after();
+                tmem_dealloc(tmem, 512);
             }
-            __syncwarp();
-            tc_fence_before();
-            __syncthreads();
             return;
         }
-        if (warp == 10) {
-            // ---- clear the V rows behind the last key, up to the end of its 16-key step
-            int base = 0;
-            uint32_t cleans[2] = {0, 0};
+        if (lane == 0) {
+            // ---- products of lane L
+            constexpr uint32_t id_s = idesc_bf16_f32(128, ST_KEYS), id_o = idesc_bf16_f32_bmn(128, DH);
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)),
+                           dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE)),
+                           dv = smem_desc_sw128_mn(smem_u32(ring + slot0 * TILE), HALF);
+            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + O_COL + (uint32_t)L * 128u;
+            int s = 0;                            // next slot, its phase
+            uint32_t ph = 0, cnt = 0, qn = 0;
             bool ok = true;
-            Piece p = first_piece();
-            for (int pos = lo; pos < hi && ok; pos += p.n, p = pos < hi ? next_piece(p, pos) : p) {
-                if (p.t0 + p.n == p.nt && (p.keys & 15) != 0) {
-                    const bool pair = p.sh ? a.sh_pair : a.own_pair;
-                    const int st = v_step(p, pair, base, p.n - 1);
-                    for (int L = 0; L < 2 && ok; ++L) {   // both of two row lanes, or the key lane that has it
-                        if (!pair && L != ((p.n - 1) & 1)) continue;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&want[L], cleans[L] & 1u)) != 0;
-                        ++cleans[L];
-                    }
-                    if (!ok) break;
-                    uint8_t* v = ring + (size_t)(st % NST) * TILE;
-                    const int nv = p.keys - (p.nt - 1) * ST_KEYS, rows = 16 - (nv & 15);
-                    for (int e = lane; e < rows * 8 * HALVES; e += 32) {
-                        const int hf = e / (rows * 8), r = nv + e % (rows * 8) / 8;
-                        *reinterpret_cast<uint4*>(v + hf * HALF + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane < 2 && (pair || lane == ((p.n - 1) & 1))) mbar_arrive(&cleared[lane]);
+            auto take = [&]() -> int {            // wait for the next step's tile
+                const int at = s;
+                if (!mbar_wait(&full[slot0 + at], ph)) ok = false;
+                if (++s == nslots) {
+                    s = 0;
+                    ph ^= 1u;
                 }
-                base += 2 * p.n;
+                return at;
+            };
+            auto score = [&](int at) {            // S = Q K^T
+                const uint64_t kd = dk + (uint64_t)((uint32_t)(at * TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                    tc_mma_f16(s_at, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+                }
+            };
+            for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
+                if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
+                ++qn;
+                int k = take();
+                if (!ok) break;
+                tc_fence_after();
+                score(k);
+                tc_commit(&s_full[L]);
+                tc_commit(&empty[slot0 + k]);
+                for (int t = 0; t < p.n; ++t) {
+                    // O += P V of this tile, then the next one's scores before any of the commits
+                    const bool next = t + 1 < p.n;
+                    const int v = take();
+                    if (next) k = take();
+                    if (!ok || !mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
+                    ++cnt;
+                    tc_fence_after();
+                    const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+                    const uint64_t vd = dv + (uint64_t)((uint32_t)(v * TILE) >> 4);
+                    if (nv > ST_KEYS - 16) {
+#pragma unroll
+                        for (int kk = 0; kk < ST_KEYS / 16; ++kk)
+                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                          (kk > 0 || t > 0) ? 1u : 0u);
+                    } else {
+                        for (int kk = 0; kk < (nv + 15) / 16; ++kk)
+                            tc_mma_f16_ta(o_at, s_at + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), id_o,
+                                          (kk > 0 || t > 0) ? 1u : 0u);
+                    }
+                    if (next) {
+                        score(k);
+                        tc_commit(&s_full[L]);
+                        tc_commit(&empty[slot0 + k]);
+                    }
+                    tc_commit(&empty[slot0 + v]);
+                    tc_commit(&pv_done[L]);
+                }
             }
-            if (!ok && lane == 0) *abort_flag = 1;
-            __syncthreads();
-            return;
+            if (!ok) *abort_flag = 1;
+            tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
+            mbar_wait(&drain[L], 0);
         }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax of lane L: thread = row r of the lane's tile
-    const int L = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const int q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t s_col = (uint32_t)L * 128u, o_col = O_COL + (uint32_t)L * 128u;
     const int grp = a.H / a.G;
     const float sl = a.scale * 1.4426950408889634f;
     // where this thread's row of a piece lies: in its segment, and of the head
     auto rows_of = [&](const Piece& p, int& r_seg, int& r_all) -> bool {
-        const bool pair = p.sh ? a.sh_pair : a.own_pair;
         const int all_rows = p.sh ? a.B * a.C * a.T * grp : a.C * a.T * grp;
         const int seg_rows = p.sh ? a.sh_rows : a.own_rows;
-        r_seg = pair ? L * 128 + r : r;
+        r_seg = rows2 ? L * 128 + r : r;
         r_all = p.rt * seg_rows + r_seg;
         return r_seg < seg_rows && r_all < all_rows;
     };
@@ -596,8 +549,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         int r_seg, r_all;
         const bool live = rows_of(p, r_seg, r_all);
         if (!__any_sync(0xffffffffu, live)) return;
-        const int64_t m = p.sh ? r_all / grp : (int64_t)p.b * a.C * a.T + r_all / grp;
-        const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all % grp) * DH;
+        const int m_in = r_all / grp;
+        const int64_t m = p.sh ? m_in : (int64_t)p.b * a.C * a.T + m_in;
+        const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all - m_in * grp) * DH;
         uint8_t* dst = sQ + L * TILE;
 #pragma unroll 1
         for (int hf = 0; hf < HALVES; ++hf)
@@ -631,37 +585,23 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_ready[L]);
     };
-    int cnt = 0;
-    uint32_t took = 0;
+    auto wait_all = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0; };
+    uint32_t cnt = 0;                             // tiles so far
     bool ok = true;
     Piece p = first_piece();
-    if (lo < hi && lane_tiles(p, L) > 0) {
+    if (p.n > 0) {
         stage(p);
         staged();
     }
-    for (int pos = lo; pos < hi && ok;) {
-        const bool pair = p.sh ? a.sh_pair : a.own_pair;
-        const int nl = lane_tiles(p, L), seg_rows = p.sh ? a.sh_rows : a.own_rows;
+    while (p.n > 0 && ok) {
+        const int seg_rows = p.sh ? a.sh_rows : a.own_rows;
         int r_seg, r_all;
         const bool live = rows_of(p, r_seg, r_all), work = __any_sync(0xffffffffu, live);
-        const bool more = pos + p.n < hi;
-        const Piece nx = more ? next_piece(p, pos + p.n) : p;
-        const bool feed = more && lane_tiles(nx, L) > 0;
+        const Piece nx = next_piece(p);
         float m_run = -INFINITY, l = 0.f;
-        if (nl == 0 && feed) stage(nx);
-        const int turns = lane_tiles(p, 0);       // lane 1 may have a tile less: it still passes its turn on
-        for (int s = 0; s < turns; ++s) {
-            // lane 1's turn s follows lane 0's, lane 0's turn s + 1 lane 1's
-            const uint32_t phase = L ? took & 1u : (took & 1u) ^ 1u;
-            const bool wait_turn = L == 1 || took > 0;
-            ++took;
-            if (s >= nl) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&turn[L], phase))) { ok = false; break; }
-                if (lane == 0) mbar_arrive(&turn[L ^ 1]);
-                continue;
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[L], (uint32_t)cnt & 1u))) { ok = false; break; }
-            if (s == nl - 1 && feed) stage(nx);   // this piece's last scores are out: Q's place is free
+        for (int t = 0; t < p.n; ++t) {
+            if (!wait_all(&s_full[L], cnt & 1u)) { ok = false; break; }
+            if (t == p.n - 1 && nx.n > 0) stage(nx);   // the last scores are out: Q's place is free
             uint32_t x[8][16];
             if (work) {
                 tc_fence_after();
@@ -669,10 +609,24 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 for (int c = 0; c < 8; ++c) tmem_ld16_issue(trow + s_col + (uint32_t)(c * 16), x[c]);
                 tmem_wait_ld();
             }
-            if (wait_turn && !__all_sync(0xffffffffu, mbar_wait(&turn[L], phase))) { ok = false; break; }
+            const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
+            // row lanes: lane 1's turn follows lane 0's of the same tile, lane 0's the one before of lane 1
+            if (rows2 && (L == 1 || cnt > 0) && !wait_all(&turn[L], (cnt & 1u) ^ (uint32_t)(L ^ 1))) { ok = false; break; }
+            if ((nv & 15) && (!rows2 || L == 0)) {
+                // clear the V rows behind the last key, up to the end of its 16-key step (for both of
+                // two row lanes: lane 1's weights come after this turn)
+                const uint32_t st = 2 * cnt + 1;
+                const int at = slot0 + (int)(st % (uint32_t)nslots);
+                if (!wait_all(&full[at], st / (uint32_t)nslots & 1u)) { ok = false; break; }
+                const int rows = 16 - (nv & 15);
+                for (int e = r; e < rows * 8 * HALVES; e += 128) {
+                    const int hf = e / (rows * 8), k = nv + (e - hf * rows * 8) / 8;
+                    *reinterpret_cast<uint4*>(ring + (size_t)at * TILE + hf * HALF + k * 128 + e % 8 * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
             if (work) {
-                const int t = pair ? s : 2 * s + L;
-                const int nv = min(ST_KEYS, p.keys - (p.t0 + t) * ST_KEYS);
                 if (nv < ST_KEYS) {               // keys behind the last one: no weight
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
@@ -688,9 +642,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                         mx[(j >> 1) & 3] = st_max3(mx[(j >> 1) & 3], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
                 const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl);
                 const bool move = m_new > m_run + ST_RESCALE_LOG2 || (m_run == -INFINITY && m_new > -INFINITY);
-                if (s > 0 && __any_sync(0xffffffffu, move)) {
+                if (t > 0 && __any_sync(0xffffffffu, move)) {
                     // rescale the rows of O once P V of the previous tile is in it
-                    if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[L], (uint32_t)(cnt - 1) & 1u))) { ok = false; break; }
+                    if (!wait_all(&pv_done[L], (cnt - 1) & 1u)) { ok = false; break; }
                     tc_fence_after();
                     const float f = move ? ex2_approx_ftz(m_run - m_new) : 1.f;
 #pragma unroll
@@ -729,7 +683,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 l += l0 + l1;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&turn[L ^ 1]);
+            if (rows2 && lane == 0) mbar_arrive(&turn[L ^ 1]);
             if (work) {
                 tmem_wait_st();
                 tc_fence_before();
@@ -738,37 +692,39 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             if (lane == 0) mbar_arrive(&p_full[L]);
             ++cnt;
         }
-        if (ok && feed) staged();                 // the next scores need not wait for the rest
+        if (ok && nx.n > 0) staged();             // the next scores need not wait for the rest
         // ---- the piece's partials: o, then (m, l)
-        if (ok && nl > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[L], (uint32_t)(cnt - 1) & 1u))) ok = false;
+        if (ok && !wait_all(&pv_done[L], (cnt - 1) & 1u)) ok = false;
         tc_fence_after();
         if (!ok && lane == 0) {
             *abort_flag = 1;
             if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
         }
         if (work) {
-            const int slot = pair ? p.slot : 2 * p.slot + L, slots = p.sh ? a.sh_slots : a.own_slots;
-            const int64_t row = ((int64_t)p.seg * slots + slot) * seg_rows + r_seg;
-            if (ok && nl > 0) {
-                float* dst = (p.sh ? a.sh_o : a.own_o) + row * DH;
+            const int64_t at = (int64_t)p.seg * (p.sh ? a.sh_slots : a.own_slots) + p.slot;
+            const int ld = rows4(seg_rows) * 4;
+            float* dst = (p.sh ? a.sh_o : a.own_o) + at * rows4(seg_rows) * DH + r_seg * 4;
+            if (ok) {
 #pragma unroll
-                for (int c = 0; c < DH / 16; ++c) {
-                    uint32_t o[16];
-                    tmem_ld16_issue(trow + o_col + (uint32_t)(c * 16), o);
+                for (int c = 0; c < DH / 32; ++c) {
+                    uint32_t o[2][16];
+                    tmem_ld16_issue(trow + o_col + (uint32_t)(c * 32), o[0]);
+                    tmem_ld16_issue(trow + o_col + (uint32_t)(c * 32 + 16), o[1]);
                     tmem_wait_ld();
                     if (live) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<uint4*>(dst + c * 16 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(dst + (c * 8 + j) * ld) =
+                                make_uint4(o[j >> 2][4 * (j & 3)], o[j >> 2][4 * (j & 3) + 1], o[j >> 2][4 * (j & 3) + 2],
+                                           o[j >> 2][4 * (j & 3) + 3]);
                     }
                 }
             }
             if (live)
-                (p.sh ? a.sh_ml : a.own_ml)[row] =
-                    ok && nl > 0 ? make_float2(m_run * 0.6931471805599453f, l) : make_float2(-INFINITY, 0.f);
+                (p.sh ? a.sh_ml : a.own_ml)[at * seg_rows + r_seg] =
+                    ok ? make_float2(m_run * 0.6931471805599453f, l) : make_float2(-INFINITY, 0.f);
         }
         tc_fence_before();                        // these reads precede the next piece's products
-        pos += p.n;
         p = nx;
     }
     tc_fence_before();
@@ -776,50 +732,55 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
 }
 
 // =========================================================================================
-// Combine: a warp per (query, head); lanes own dh / 32 consecutive columns (dh 16: 16 lanes one).
+// Combine. A CTA takes 512 / dh consecutive (candidate, position, head) rows of a sequence and K/V
+// head, a thread four columns of one row: it folds the row's partials, then the block rows j <= i
+// (scores by a dot product over the row's threads, 16 keys at a time), and normalises.
 // =========================================================================================
-template <typename T, int EPL>
+template <typename T, int DH>
 __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
+    constexpr int RW = 512 / DH, KB = 16;
+    __shared__ float part[4][KB][RW];             // a warp's share of the dot products
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int dh = a.dh, grp = a.H / a.G;
-    // CTA (b and c, g, four of the queries and heads there): its warps share block rows
-    const int bc = blockIdx.x, g = blockIdx.y, at = blockIdx.z * 4 + warp;
-    const int i = at / grp, hg = at % grp, b = bc / a.C, c = bc % a.C;
-    if (i >= a.T) return;
-    const int64_t m = (int64_t)bc * a.T + i;
+    const int warp = threadIdx.x >> 5;
+    const int grp = a.H / a.G, rows = a.C * a.T * grp;
+    const int b = blockIdx.x, g = blockIdx.y, row = threadIdx.x % RW, c4 = threadIdx.x / RW;
+    const int r_own = blockIdx.z * RW + row;
+    const bool live = r_own < rows;
+    const int ci = (live ? r_own : rows - 1) / grp, hg = (live ? r_own : rows - 1) - ci * grp;   // (c, i), head
+    const int c = ci / a.T, i = ci - c * a.T;
+    const int64_t m = (int64_t)b * a.C * a.T + ci;
     const int h = g * grp + hg;
-    const int e0 = lane * EPL;
-    const bool act = e0 < dh;
-    float M = -INFINITY, L = 0.f, O[EPL];
-#pragma unroll
-    for (int u = 0; u < EPL; ++u) O[u] = 0.f;
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     auto rebase = [&](float mb) {
         if (mb > M) {
             const float f = M == -INFINITY ? 0.f : exp_of<T>(M - mb);
             L *= f;
-#pragma unroll
-            for (int u = 0; u < EPL; ++u) O[u] *= f;
+            O.x *= f; O.y *= f; O.z *= f; O.w *= f;
             M = mb;
         }
     };
-    auto fold = [&](const float* po, const float2* pml, int64_t row, int64_t stride, int used) {
-        constexpr int PB = 8;                      // partials in flight
+    auto add = [&](float w, float4 v) {
+        O.x = fmaf(w, v.x, O.x);
+        O.y = fmaf(w, v.y, O.y);
+        O.z = fmaf(w, v.z, O.z);
+        O.w = fmaf(w, v.w, O.w);
+    };
+    // the partials of row r of segment seg
+    auto fold = [&](const float* po, const float2* pml, int64_t seg, int slots, int seg_rows, int r, int used) {
+        constexpr int PB = 8;                      // in flight
+        const float2* ml_at = pml + seg * slots * seg_rows + r;
+        const float* o_at = po + (seg * slots * DH + (int64_t)c4 * 4) * rows4(seg_rows) + r * 4;
+        const int64_t o_step = (int64_t)DH * rows4(seg_rows);
         for (int s0 = 0; s0 < used; s0 += PB) {
             float2 ml[PB];
-            float os[PB][EPL];
+            float4 os[PB];
 #pragma unroll
             for (int j = 0; j < PB; ++j) {
                 const bool on = s0 + j < used;
-                ml[j] = on ? pml[row + (s0 + j) * stride] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int u = 0; u < EPL; ++u) os[j][u] = 0.f;
-                if (on && act) {
-                    const float* src = po + (row + (s0 + j) * stride) * dh + e0;
-#pragma unroll
-                    for (int u = 0; u < EPL; ++u) os[j][u] = src[u];
-                }
+                ml[j] = on ? ml_at[(int64_t)(s0 + j) * seg_rows] : make_float2(-INFINITY, 0.f);
+                os[j] = on ? *reinterpret_cast<const float4*>(o_at + (s0 + j) * o_step) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float mb = -INFINITY;
 #pragma unroll
@@ -831,96 +792,107 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
                 if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
                 const float w = exp_of<T>(ml[j].x - M);
                 L = fmaf(ml[j].y, w, L);
-#pragma unroll
-                for (int u = 0; u < EPL; ++u) O[u] = fmaf(os[j][u], w, O[u]);
+                add(w, os[j]);
             }
         }
     };
-    const int r_sh = (int)(m * grp + hg), r_own = (c * a.T + i) * grp + hg;
     const int own = own_rows_of(a, b, false);
-    const int ntp = (a.P + 127) / 128, W = a.tensor ? a.plan[0] : 1;
-    // the runs of W tiles that a segment of nt tiles starting at position start meets
-    auto runs = [&](int start, int nt, int pair) { return ((start + nt - 1) / W - start / W + 1) * (pair ? 1 : 2); };
-    if (a.P > 0) {
-        const int seg = g * a.sh_tiles + r_sh / a.sh_rows;
-        fold(a.sh_o, a.sh_ml, (int64_t)seg * a.sh_slots * a.sh_rows + r_sh % a.sh_rows, a.sh_rows,
-             a.tensor ? runs(seg * ntp, ntp, a.sh_pair) : a.sh_slots);
+    // the runs that a segment's nt tiles from position at on meet
+    auto runs = [&](int at, int nt, int W) { return (at + nt - 1) / W - at / W + 1; };
+    if (live && a.P > 0) {
+        const int r = (int)(m * grp + hg), t = r / a.sh_rows, seg = g * a.sh_tiles + t, nt = (a.P + 127) / 128;
+        fold(a.sh_o, a.sh_ml, seg, a.sh_slots, a.sh_rows, r - t * a.sh_rows,
+             a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots);
     }
-    if (own > 0) {
-        const int in_b = g * a.own_tiles + r_own / a.own_rows, per_b = a.G * a.own_tiles;
+    if (live && own > 0) {
+        const int t = r_own / a.own_rows, in_b = g * a.own_tiles + t, per_b = a.G * a.own_tiles;
         int used = a.own_slots;
         if (a.tensor) {
-            const int before = a.plan[1 + b], nt = a.plan[2 + b] - before;
-            used = runs(a.G * a.sh_tiles * ntp + per_b * before + in_b * nt, nt, a.own_pair);
+            const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
+            used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
         }
-        fold(a.own_o, a.own_ml, ((int64_t)b * per_b + in_b) * a.own_slots * a.own_rows + r_own % a.own_rows, a.own_rows,
-             used);
+        fold(a.own_o, a.own_ml, (int64_t)b * per_b + in_b, a.own_slots, a.own_rows, r_own - t * a.own_rows, used);
     }
     // block rows j <= i: of this candidate, or own rows own + j when the block is in the cache
     const T *kb, *vb;
     int64_t ld;
     int last = i;
     if (a.kb) {
-        kb = (const T*)a.kb + bc * a.b_cand + g * a.b_head;
-        vb = (const T*)a.vb + bc * a.b_cand + g * a.b_head;
+        const int64_t at = ((int64_t)b * a.C + c) * a.b_cand + g * a.b_head + c4 * 4;
+        kb = (const T*)a.kb + at;
+        vb = (const T*)a.vb + at;
         ld = a.b_row;
     } else {
-        kb = (const T*)a.ko + b * a.o_seq + g * a.o_head + own * a.o_row;
-        vb = (const T*)a.vo + b * a.o_seq + g * a.o_head + own * a.o_row;
+        const int64_t at = b * a.o_seq + g * a.o_head + own * a.o_row + c4 * 4;
+        kb = (const T*)a.ko + at;
+        vb = (const T*)a.vo + at;
         ld = a.o_row;
         if (own + i >= a.own_max) {                // rows past the capacity do not exist
             last = a.own_max - 1 - own;
-            if (a.flags && lane == 0) atomicOr(a.flags, (uint32_t)EVS_FLAG_KV_OVERFLOW);
+            if (a.flags && live && c4 == 0) atomicOr(a.flags, (uint32_t)EVS_FLAG_KV_OVERFLOW);
         }
     }
-    float qv[EPL];
-#pragma unroll
-    for (int u = 0; u < EPL; ++u)
-        qv[u] = act ? load_q(a, m * a.q_ld + (int64_t)h * dh + e0 + u) * a.scale : 0.f;
-    for (int j0 = 0; j0 <= last; j0 += 4) {
-        float kv[4][EPL], vv[4][EPL], s[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int u = 0; u < EPL; ++u) {
-                const bool on = j0 + j <= last && act;
-                kv[j][u] = on ? to_f32(kb[(int64_t)(j0 + j) * ld + e0 + u]) : 0.f;
-                vv[j][u] = on ? to_f32(vb[(int64_t)(j0 + j) * ld + e0 + u]) : 0.f;
+    auto load4 = [&](const T* p) -> float4 {
+        if (a.b_vec) {
+            if constexpr (sizeof(T) == 4) {
+                return *reinterpret_cast<const float4*>(p);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(p);
+                const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+                const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+                return make_float4(lo.x, lo.y, hi.x, hi.y);
             }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s[j] = 0.f;
-#pragma unroll
-            for (int u = 0; u < EPL; ++u) s[j] = fmaf(qv[u], kv[j][u], s[j]);
         }
+        return make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+    };
+    float q[4];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
+    for (int u = 0; u < 4; ++u) q[u] = load_q(a, m * a.q_ld + (int64_t)h * DH + c4 * 4 + u) * a.scale;
+    for (int j0 = 0; j0 < a.T; j0 += KB) {         // the same count for every row of the CTA
+        const int n = min(KB, a.T - j0);
+        float4 v[KB];
+        if (j0 > 0) __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], x);
-        float mb = -INFINITY;
+        for (int j = 0; j < KB; ++j) {
+            if (j >= n) break;
+            const bool on = live && j0 + j <= last;
+            float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j] = k;
+            if (on) {
+                k = load4(kb + (j0 + j) * ld);
+                v[j] = load4(vb + (j0 + j) * ld);
+            }
+            float s = fmaf(q[0], k.x, fmaf(q[1], k.y, fmaf(q[2], k.z, q[3] * k.w)));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j0 + j > last) s[j] = -INFINITY;
+            for (int o = RW; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if ((threadIdx.x & 31) < RW) part[warp][j][row] = s;
+        }
+        __syncthreads();
+        float s[KB], mb = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            s[j] = -INFINITY;
+            if (j < n && j0 + j <= last) s[j] = (part[0][j][row] + part[1][j][row]) + (part[2][j][row] + part[3][j][row]);
             mb = fmaxf(mb, s[j]);
         }
         rebase(mb);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (s[j] == -INFINITY) continue;
+        for (int j = 0; j < KB; ++j) {
+            if (j >= n || s[j] == -INFINITY) continue;
             const float w = exp_of<T>(s[j] - M);
             L += w;
-#pragma unroll
-            for (int u = 0; u < EPL; ++u) O[u] = fmaf(w, vv[j][u], O[u]);
+            add(w, v[j]);
         }
     }
+    if (!live) return;
     // no key with any weight: zero output, lse -inf
-    if (act) {
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-        T* dst = (T*)a.o + m * a.o_ld + (int64_t)h * dh + e0;
-#pragma unroll
-        for (int u = 0; u < EPL; ++u) dst[u] = from_f32<T>(O[u] * inv);
-    }
-    if (a.lse && lane == 0) a.lse[m * a.H + h] = L == 0.f ? -INFINITY : M + logf(L);
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    T* dst = (T*)a.o + m * a.o_ld + (int64_t)h * DH + c4 * 4;
+    dst[0] = from_f32<T>(O.x * inv);
+    dst[1] = from_f32<T>(O.y * inv);
+    dst[2] = from_f32<T>(O.z * inv);
+    dst[3] = from_f32<T>(O.w * inv);
+    if (a.lse && c4 == 0) a.lse[m * a.H + h] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
 // ---- host side ----------------------------------------------------------------------------------
@@ -972,9 +944,9 @@ bool tensor_ok(const evs_shared_attn_args& c) {
     return true;
 }
 
-// Tiles, slots and grid. A segment of nt tiles meets at most (nt - 1) / W + 2 runs of W tiles, and
-// W >= total / grid, with the own lengths known only on the device: the bound at their capacity
-// is the largest. false: sizes past the kernel's 32-bit tile positions.
+// Tiles, slots and grid. A segment of nt tiles meets at most (nt - 1) / W + 2 runs, and a run is at
+// least the segments' cost over the workers; the own lengths are known only on the device, the
+// bound at their capacity is the largest. false: sizes past the kernel's 32-bit positions.
 bool plan_tensor(const evs_shared_attn_args& c, SharedArgs& a, int& grid) {
     const int grp = c.heads / c.kv_heads;
     const long long sh = (long long)c.batch * c.n_cand * c.block * grp, own = (long long)c.n_cand * c.block * grp;
@@ -985,16 +957,16 @@ bool plan_tensor(const evs_shared_attn_args& c, SharedArgs& a, int& grid) {
     a.own_rows = (int)(own < 256 ? own : 256);
     a.sh_tiles = (int)((sh + 255) / 256);
     a.own_tiles = (int)((own + 255) / 256);
-    const long long sh_total = c.kv_heads * (long long)a.sh_tiles * ntp;
-    const long long per_b = (long long)c.kv_heads * a.own_tiles, most = sh_total + c.batch * per_b * nto;
-    if (most >= (1LL << 30)) return false;
-    grid = (int)(most < kAttnGrid ? most : kAttnGrid);
-    auto bound = [&](long long nt, long long total) {
-        const long long s = nt * grid / (total > 0 ? total : 1) + 2;
+    const long long shs = c.kv_heads * (long long)a.sh_tiles, owns = c.kv_heads * (long long)a.own_tiles;
+    const long long tiles = shs * ntp + c.batch * owns * nto;
+    if (tiles + shs * ST_OVER + c.batch * owns * ST_OVER >= (1LL << 30)) return false;
+    grid = (int)(tiles < kAttnGrid ? tiles : kAttnGrid);
+    auto bound = [&](long long nt, long long segs, int pair) {
+        const long long s = nt ? nt * grid * (2 - pair) / (segs * (nt + ST_OVER)) + 2 : 0;
         return (int)(s < nt ? s : nt);
     };
-    a.sh_slots = ntp ? bound(ntp, sh_total) * (a.sh_pair ? 1 : 2) : 0;
-    a.own_slots = nto ? bound(nto, sh_total + per_b * nto) * (a.own_pair ? 1 : 2) : 0;
+    a.sh_slots = bound(ntp, shs, a.sh_pair);
+    a.own_slots = bound(nto, owns, a.own_pair);
     a.tensor = 1;
     return true;
 }
@@ -1007,13 +979,13 @@ size_t carve_partials(const evs_shared_attn_args& c, SharedArgs& a, char* base) 
         off = round256(off + bytes);
         return p;
     };
-    const size_t sh = (size_t)c.kv_heads * a.sh_tiles * a.sh_slots * a.sh_rows;
-    const size_t own = (size_t)c.batch * c.kv_heads * a.own_tiles * a.own_slots * a.own_rows;
-    a.sh_o = (float*)take(sh * c.head_dim * 4);
-    a.own_o = (float*)take(own * c.head_dim * 4);
-    a.sh_ml = (float2*)take(sh * 8);
-    a.own_ml = (float2*)take(own * 8);
-    a.plan = (int*)take(((size_t)c.batch + 2) * 4);
+    const size_t sh = (size_t)c.kv_heads * a.sh_tiles * a.sh_slots;
+    const size_t own = (size_t)c.batch * c.kv_heads * a.own_tiles * a.own_slots;
+    a.sh_o = (float*)take(sh * rows4(a.sh_rows) * c.head_dim * 4);
+    a.own_o = (float*)take(own * rows4(a.own_rows) * c.head_dim * 4);
+    a.sh_ml = (float2*)take(sh * a.sh_rows * 8);
+    a.own_ml = (float2*)take(own * a.own_rows * 8);
+    a.plan = (int*)take(((size_t)c.batch + 4) * 4);
     return off;
 }
 
@@ -1047,7 +1019,7 @@ bool make_rows_map(CUtensorMap* m, const void* base, int dh, int rows, int heads
 
 // alignment, two Q tiles, the barriers, lengths and their running sums, the ring
 constexpr int tc_smem(int dh, int stages, int batch) {
-    return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (4 * stages + 16) * 8 + (2 * batch + 1) * 4 + 16;
+    return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (2 * stages + 12) * 8 + (2 * batch + 1) * 4 + 16;
 }
 
 template <int DH, int NST>
@@ -1086,6 +1058,12 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     int grid_tc = 0;
     const bool tensor = tensor_ok(c) && plan_tensor(c, a, grid_tc);
     if (!tensor) plan_simt(c, a);
+    const int es = half ? 2 : 4;
+    const bool in_cache = !c.k_block;
+    const int64_t b0 = in_cache ? c.own_row : c.block_row, b1 = in_cache ? c.own_head : c.block_head,
+                  b2 = in_cache ? c.own_seq : c.block_cand;
+    a.b_vec = ((uintptr_t)(in_cache ? c.k_own : c.k_block) | (uintptr_t)(in_cache ? c.v_own : c.v_block)) % (4 * es) == 0 &&
+              b0 % 4 == 0 && b1 % 4 == 0 && b2 % 4 == 0;
     a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld * (a.q_bf16 ? 2 : 4) % 16 == 0;
     carve_partials(c, a, (char*)c.workspace);
     const int sh_items = c.kv_heads * a.sh_slots * ((a.sh_rows + SA_Q - 1) / SA_Q);
@@ -1100,16 +1078,15 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
         e = half ? launch_s(stream, shared_simt_kernel<bf16>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items)
                  : launch_s(stream, shared_simt_kernel<float>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items);
     if (e != cudaSuccess) return e;
-    const dim3 grid(c.batch * c.n_cand, c.kv_heads, (c.block * (c.heads / c.kv_heads) + 3) / 4);
-    if (half)
-        e = c.head_dim == 128  ? launch_s(stream, shared_combine_kernel<bf16, 4>, grid, dim3(128), 0, a)
-            : c.head_dim == 64 ? launch_s(stream, shared_combine_kernel<bf16, 2>, grid, dim3(128), 0, a)
-                               : launch_s(stream, shared_combine_kernel<bf16, 1>, grid, dim3(128), 0, a);
-    else
-        e = c.head_dim == 128  ? launch_s(stream, shared_combine_kernel<float, 4>, grid, dim3(128), 0, a)
-            : c.head_dim == 64 ? launch_s(stream, shared_combine_kernel<float, 2>, grid, dim3(128), 0, a)
-                               : launch_s(stream, shared_combine_kernel<float, 1>, grid, dim3(128), 0, a);
-    return e;
+    const int rw = 512 / c.head_dim;
+    const dim3 grid(c.batch, c.kv_heads, (c.n_cand * c.block * (c.heads / c.kv_heads) + rw - 1) / rw);
+    auto combine = [&](auto kernel) { return launch_s(stream, kernel, grid, dim3(128), 0, a); };
+    switch (c.head_dim) {
+        case 128: return half ? combine(shared_combine_kernel<bf16, 128>) : combine(shared_combine_kernel<float, 128>);
+        case 64: return half ? combine(shared_combine_kernel<bf16, 64>) : combine(shared_combine_kernel<float, 64>);
+        case 32: return half ? combine(shared_combine_kernel<bf16, 32>) : combine(shared_combine_kernel<float, 32>);
+        default: return half ? combine(shared_combine_kernel<bf16, 16>) : combine(shared_combine_kernel<float, 16>);
+    }
 }
 
 }  // namespace evs
