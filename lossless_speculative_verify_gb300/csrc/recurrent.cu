@@ -44,12 +44,12 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T, uint32
 // =========================================================================================
 // Short causal convolution, y_t[c] = act(bias[c] + sum_{j<L} w[c][j] x_{t-j}[c]).
 //
-// A thread owns VEC consecutive channels and CONV_RUN consecutive positions: the window slides
-// through registers, so x is read once but for the L - 1 rows before a run. Eight rows are
-// requested before any is used. The thread of the first run also writes the tail (after it has
-// read the old one), so the two may be the same buffer. HBM-bound: x read + y written.
+// A thread owns VEC consecutive channels and a run of consecutive positions: the window slides
+// through registers, so x is read once but for the L - 1 rows before a run, and the weights once a
+// run. The next eight rows are requested before the last eight are used. The thread of the first
+// run also writes the tail (after it has read the old one), so the two may be the same buffer.
+// HBM-bound: x read + y written.
 // =========================================================================================
-constexpr int CONV_RUN = 32;
 constexpr int CONV_THREADS = 128;
 
 struct ConvArgs {
@@ -60,16 +60,15 @@ struct ConvArgs {
     const int32_t* lens;
     uint32_t* flags;
     int64_t x_ld, x_seq, y_ld, y_seq;
-    int T, D, L, act;
+    int T, D, L, act, run;
 };
 
 template <typename T, int LMAX, int VEC>
 __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
-    pdl_trigger();
     pdl_wait();
     const int L = a.L;
     const int ch = (blockIdx.x * CONV_THREADS + threadIdx.x) * VEC;
-    const int b = blockIdx.z, t0 = blockIdx.y * CONV_RUN;
+    const int b = blockIdx.z, t0 = blockIdx.y * a.run;
     if (ch >= a.D) return;
     const int len = seq_len(a.lens, b, a.T, a.flags, ch == 0 && t0 == 0);
     if (t0 >= len && t0 > 0) return;
@@ -80,10 +79,21 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
     float w[LMAX][VEC], hist[LMAX - 1][VEC], bias[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[ch + i] : 0.f;
+    if constexpr (VEC * LMAX % 4 == 0 && LMAX <= 4) {   // instances of one length, rows on 16 bytes
+        float4 v[VEC * LMAX / 4];
 #pragma unroll
-    for (int j = 0; j < LMAX; ++j)
+        for (int i = 0; i < VEC * LMAX / 4; ++i) v[i] = reinterpret_cast<const float4*>(a.w + (size_t)ch * LMAX)[i];
+        const float* f = reinterpret_cast<const float*>(v);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = j < L ? a.w[(size_t)(ch + i) * L + j] : 0.f;
+        for (int j = 0; j < LMAX; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[j][i] = f[i * LMAX + j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < LMAX; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[j][i] = j < L ? a.w[(size_t)(ch + i) * L + j] : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < LMAX - 1; ++j) {
 #pragma unroll
@@ -116,12 +126,16 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
         }
     }
     if (!y) return;
-    const int t1 = min(t0 + CONV_RUN, len);
-    for (int s = t0; s < t1; s += 8) {
-        Chunk<T, VEC> in[8];
+    const int t1 = min(t0 + a.run, len);
+    Chunk<T, VEC> in[8], nx[8];
+    auto fetch = [&](int s, Chunk<T, VEC> (&c)[8]) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (s + u < t1) in[u] = *reinterpret_cast<const Chunk<T, VEC>*>(x + (size_t)(s + u) * a.x_ld);
+            if (s + u < t1) c[u] = *reinterpret_cast<const Chunk<T, VEC>*>(x + (size_t)(s + u) * a.x_ld);
+    };
+    fetch(t0, in);
+    for (int s = t0; s < t1; s += 8) {
+        fetch(s + 8, nx);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if (s + u >= t1) break;
@@ -140,14 +154,27 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
             }
             store_vec<T, VEC>(y + (size_t)(s + u) * a.y_ld, out);
         }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) in[u] = nx[u];
     }
+    pdl_trigger();
 }
 
+// Runs: about three CTAs an SM over all sequences, at least 16 positions each.
 template <typename T, int LMAX, int VEC>
-void conv_launch(const ConvArgs& a, int B, cudaStream_t s) {
+void conv_launch(ConvArgs a, int B, cudaStream_t s) {
     const int cols = (a.D + VEC * CONV_THREADS - 1) / (VEC * CONV_THREADS);
-    const int runs = a.y ? (a.T + CONV_RUN - 1) / CONV_RUN : 1;
-    launch_s(s, conv_kernel<T, LMAX, VEC>, dim3(cols, runs < 1 ? 1 : runs, B), dim3(CONV_THREADS), 0, a);
+    int runs = 1;
+    if (a.y) {
+        const long long want = (3 * 152 + (long long)cols * B - 1) / ((long long)cols * B);
+        const long long most = (a.T + 15) / 16;
+        runs = (int)(want < most ? want : most);
+        a.run = ((a.T + runs - 1) / runs + 7) / 8 * 8;
+        runs = (a.T + a.run - 1) / a.run;
+    } else {
+        a.run = a.T > 0 ? a.T : 1;
+    }
+    launch_s(s, conv_kernel<T, LMAX, VEC>, dim3(cols, runs, B), dim3(CONV_THREADS), 0, a);
 }
 
 template <typename T>
@@ -191,11 +218,50 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266175e-8f;   // log2 e and its rest
+
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|): the exponential's argument with its rounding
+// carried along, and log(1 + e) = 2 atanh(z), z = e / (2 + e) <= 1/3, by its series (the terms left
+// out are below 2e-8 of it), so that it stays relatively exact where e is small.
 __device__ __forceinline__ float step_size(float v, int softplus) {
-    return softplus ? (v > 20.f ? v : log1pf(expf(v))) : v;
+    if (!softplus) return v;
+    const float t = fmaxf(-fabsf(v), -100.f);
+    const float hi = t * kLog2e;
+    const float lo = fmaf(t, kLog2eLo, fmaf(t, kLog2e, -hi));
+    float e = ex2(hi);
+    e = fmaf(e, lo * 0.69314718f, e);
+    const float z = __fdividef(e, 2.f + e), w = z * z;
+    float p = fmaf(w, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(p, w, 1.f / 9.f);
+    p = fmaf(p, w, 1.f / 7.f);
+    p = fmaf(p, w, 1.f / 5.f);
+    p = fmaf(p, w, 1.f / 3.f);
+    p = fmaf(p, w, 1.f);
+    const float r = fmaf(2.f * z, p, fmaxf(v, 0.f));
+    return v != v ? v : r;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// ---- pairs of fp32 ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
 // A few tokens (single tokens, verify blocks): lanes of a channel hold NPL states each, straight
 // from global memory; HBM-bound on the state read and written.
@@ -252,27 +318,29 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
 
 // Prompts. A CTA owns CH channels of one sequence and walks its tokens SCAN_TC at a time: the
 // chunk's dl and dl x are formed once per (t, channel) into shared memory together with B_t and
-// C_t, then LPC lanes of each channel run the recurrence over it, then the outputs leave with
-// coalesced stores. The next chunk's raw values are requested before the recurrence of this one
-// starts. The recurrence's own chain is one multiply-add a step: the exponentials of later steps
-// do not depend on it, so they fill the pipe.
+// C_t, then LPC lanes of each channel run the recurrence over it, two states to an instruction, then
+// the outputs leave with coalesced stores. The next chunk's raw values are requested before the
+// recurrence of this one starts. The recurrence's own chain is one multiply-add a step: the
+// exponentials of later steps do not depend on it, so they fill the pipe. Bound by issue: one
+// exponential, half of four packed operations and its share of the staging per (t, c, n).
 constexpr int SCAN_TC = 32;
 
-template <typename T, int N, int LPC>
+template <typename T, int N, int LPC, bool V2>
 __global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
     constexpr int NPL = N / LPC;
     constexpr int CH = 256 / LPC;
-    constexpr int PER = SCAN_TC * CH / 256;          // (t, channel) items a thread stages
-    constexpr int PBC = SCAN_TC * N / 256 > 0 ? SCAN_TC * N / 256 : 1;
-    __shared__ float2 du_s[SCAN_TC][CH];             // dl, dl * x
-    __shared__ float y_s[SCAN_TC][CH + 1];
+    constexpr int RP = 512 / CH;                     // rows that one pass of the threads stages
+    constexpr int PER = SCAN_TC / RP;
+    constexpr int PBC = (SCAN_TC * N / 2 + 255) / 256;
+    constexpr int YS = CH + 4;                       // eight steps of a channel's lanes in different banks
+    __shared__ __align__(16) float2 du_s[SCAN_TC][CH];   // dl, dl * x
+    __shared__ __align__(16) float y_s[SCAN_TC][YS];
     __shared__ __align__(16) float b_s[SCAN_TC][N], c_s[SCAN_TC][N];
-    pdl_trigger();
     pdl_wait();
     const int b = blockIdx.y, tid = threadIdx.x;
     const int ch0 = blockIdx.x * CH;
     const int len = seq_len(a.lens, b, a.T, a.flags, blockIdx.x == 0 && tid == 0);
-    const int lch = tid / LPC, k0 = (tid % LPC) * NPL;
+    const int lch = tid / LPC, sub = tid % LPC, k0 = sub * NPL;
     const int ch = min(ch0 + lch, a.D - 1);
     const bool on = ch0 + lch < a.D;
     float A2[NPL], s[NPL];
@@ -286,57 +354,67 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < NPL; ++k) A2[k] *= kLog2e;
-    // staging: thread -> channel tid % CH, positions tid / CH + i * (256 / CH)
-    const int sc = tid % CH, sr = tid / CH;
-    const int gch = min(ch0 + sc, a.D - 1);
-    const bool son = ch0 + sc < a.D;
-    const float bias = a.dt_bias ? a.dt_bias[gch] : 0.f, Ds = a.Dskip ? a.Dskip[gch] : 0.f;
+    // staging: thread -> channels 2 (tid % (CH / 2)) and the next, positions tid / (CH / 2) + i RP
+    const int sc = tid % (CH / 2) * 2, sr = tid / (CH / 2);
+    const bool s1 = ch0 + sc < a.D, s2 = ch0 + sc + 1 < a.D;
+    const int gch = min(ch0 + sc, a.D - 1), gch2 = min(ch0 + sc + 1, a.D - 1);
+    const float2 bias = a.dt_bias ? make_float2(a.dt_bias[gch], a.dt_bias[gch2]) : make_float2(0.f, 0.f);
+    const float2 Ds = a.Dskip ? make_float2(a.Dskip[gch], a.Dskip[gch2]) : make_float2(0.f, 0.f);
     const T* x = (const T*)a.x + (size_t)b * a.x_seq + gch;
     const T* dt = (const T*)a.dt + (size_t)b * a.dt_seq + gch;
     const T* z = a.z ? (const T*)a.z + (size_t)b * a.z_seq + gch : nullptr;
     const T* Bm = (const T*)a.Bm + (size_t)b * a.b_seq;
     const T* Cm = (const T*)a.Cm + (size_t)b * a.c_seq;
     T* y = a.y ? (T*)a.y + (size_t)b * a.y_seq + gch : nullptr;
-    T xr[PER], dr[PER], zr[PER], br[PBC], cr[PBC];
+    Chunk<T, 2> xr[PER], dr[PER], zr[PER], br[PBC], cr[PBC];
+    auto two = [&](const T* p, bool f1, bool f2) -> Chunk<T, 2> {
+        Chunk<T, 2> r;
+        r.v[0] = r.v[1] = from_f32<T>(0.f);
+        if (V2) {
+            if (f1) r = *reinterpret_cast<const Chunk<T, 2>*>(p);
+        } else {
+            if (f1) r.v[0] = p[0];
+            if (f2) r.v[1] = p[1];
+        }
+        return r;
+    };
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = t0 + sr + i * (256 / CH);
-            xr[i] = dr[i] = zr[i] = from_f32<T>(0.f);
-            if (t < len) {
-                xr[i] = x[(size_t)t * a.x_ld];
-                dr[i] = dt[(size_t)t * a.dt_ld];
-                if (z) zr[i] = z[(size_t)t * a.z_ld];
-            }
+            const int t = t0 + sr + i * RP;
+            const bool in = t < len;
+            xr[i] = two(x + (int64_t)t * a.x_ld, in && s1, in && s2);
+            dr[i] = two(dt + (int64_t)t * a.dt_ld, in && s1, in && s2);
+            if (z) zr[i] = two(z + (int64_t)t * a.z_ld, in && s1, in && s2);
         }
 #pragma unroll
         for (int i = 0; i < PBC; ++i) {
-            const int e = tid + i * 256, t = t0 + e / N;
-            br[i] = cr[i] = from_f32<T>(0.f);
-            if (e < SCAN_TC * N && t < len) {
-                br[i] = Bm[(size_t)t * a.b_ld + e % N];
-                cr[i] = Cm[(size_t)t * a.c_ld + e % N];
-            }
+            const int e = (tid + i * 256) * 2, t = t0 + e / N;
+            const bool in = e < SCAN_TC * N && t < len;
+            br[i] = two(Bm + (int64_t)t * a.b_ld + e % N, in, in);
+            cr[i] = two(Cm + (int64_t)t * a.c_ld + e % N, in, in);
         }
     };
     if (len > 0) fetch(0);
     for (int t0 = 0; t0 < len; t0 += SCAN_TC) {
-        float skip[PER], gate[PER];
+        Chunk<T, 2> xc[PER], zc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const float xv = to_f32(xr[i]);
             // positions past the end keep the state: dl = 0 gives a decay of one and no input
-            const float dl = t0 + sr + i * (256 / CH) < len ? step_size(to_f32(dr[i]) + bias, a.softplus) : 0.f;
-            du_s[sr + i * (256 / CH)][sc] = make_float2(dl, dl * xv);
-            skip[i] = Ds * xv;
-            gate[i] = z ? silu(to_f32(zr[i])) : 1.f;
+            const bool in = t0 + sr + i * RP < len;
+            const float d0 = in ? step_size(to_f32(dr[i].v[0]) + bias.x, a.softplus) : 0.f;
+            const float d1 = in ? step_size(to_f32(dr[i].v[1]) + bias.y, a.softplus) : 0.f;
+            *reinterpret_cast<float4*>(&du_s[sr + i * RP][sc]) =
+                make_float4(d0, d0 * to_f32(xr[i].v[0]), d1, d1 * to_f32(xr[i].v[1]));
+            xc[i] = xr[i];
+            zc[i] = zr[i];
         }
 #pragma unroll
         for (int i = 0; i < PBC; ++i) {
-            const int e = tid + i * 256;
+            const int e = (tid + i * 256) * 2;
             if (e < SCAN_TC * N) {
-                b_s[e / N][e % N] = to_f32(br[i]);
-                c_s[e / N][e % N] = to_f32(cr[i]);
+                *reinterpret_cast<float2*>(&b_s[e / N][e % N]) = make_float2(to_f32(br[i].v[0]), to_f32(br[i].v[1]));
+                *reinterpret_cast<float2*>(&c_s[e / N][e % N]) = make_float2(to_f32(cr[i].v[0]), to_f32(cr[i].v[1]));
             }
         }
         __syncthreads();
@@ -350,44 +428,94 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
                 float bv[NPL], cv[NPL];
                 load_vec<float, NPL>(&b_s[i0 + u][k0], bv);
                 load_vec<float, NPL>(&c_s[i0 + u][k0], cv);
-                float acc = 0.f;
+                if constexpr (NPL % 2 == 0) {
+                    const uint64_t dl2 = pair_of(du.x, du.x), u2 = pair_of(du.y, du.y);
+                    uint64_t acc = 0;
 #pragma unroll
-                for (int k = 0; k < NPL; ++k) {
-                    s[k] = fmaf(ex2(du.x * A2[k]), s[k], du.y * bv[k]);
-                    acc = fmaf(s[k], cv[k], acc);
+                    for (int k = 0; k < NPL; k += 2) {
+                        const float2 r = unpair(mul2(dl2, pair_of(A2[k], A2[k + 1])));
+                        const uint64_t ns = fma2(pair_of(ex2(r.x), ex2(r.y)), pair_of(s[k], s[k + 1]),
+                                                 mul2(u2, pair_of(bv[k], bv[k + 1])));
+                        acc = fma2(ns, pair_of(cv[k], cv[k + 1]), acc);
+                        const float2 sv = unpair(ns);
+                        s[k] = sv.x;
+                        s[k + 1] = sv.y;
+                    }
+                    const float2 v = unpair(acc);
+                    q[u] = v.x + v.y;
+                } else {
+                    float acc = 0.f;
+#pragma unroll
+                    for (int k = 0; k < NPL; ++k) {
+                        s[k] = fmaf(ex2(du.x * A2[k]), s[k], du.y * bv[k]);
+                        acc = fmaf(s[k], cv[k], acc);
+                    }
+                    q[u] = acc;
                 }
-                q[u] = acc;
+            }
+            // sum the eight steps over the channel's lanes; each lane is left with 8 / LPC of them
+            int first = 0;
+#pragma unroll
+            for (int o = LPC / 2, n = 4; o > 0; o >>= 1, n >>= 1) {
+                const bool up = (sub & o) != 0;
+#pragma unroll
+                for (int u = 0; u < n; ++u) {
+                    const float give = up ? q[u] : q[u + n], keep = up ? q[u + n] : q[u];
+                    q[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+                first += up ? n : 0;
             }
 #pragma unroll
-            for (int o = LPC / 2; o > 0; o >>= 1)
-#pragma unroll
-                for (int u = 0; u < 8; ++u) q[u] += __shfl_xor_sync(0xffffffffu, q[u], o);
-            if (k0 == 0) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) y_s[i0 + u][lch] = q[u];
-            }
+            for (int u = 0; u < 8 / LPC; ++u) y_s[i0 + first + u][lch] = q[u];
         }
         __syncthreads();
-        if (y && son) {
+        if (y) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int r = sr + i * (256 / CH), t = t0 + r;
-                if (t < len) y[(size_t)t * a.y_ld] = from_f32<T>((y_s[r][sc] + skip[i]) * gate[i]);
+                const int r = sr + i * RP, t = t0 + r;
+                if (t >= len) break;
+                const float2 v = *reinterpret_cast<const float2*>(&y_s[r][sc]);
+                float o[2] = {fmaf(Ds.x, to_f32(xc[i].v[0]), v.x), fmaf(Ds.y, to_f32(xc[i].v[1]), v.y)};
+                if (z) {
+                    o[0] *= silu(to_f32(zc[i].v[0]));
+                    o[1] *= silu(to_f32(zc[i].v[1]));
+                }
+                T* to = y + (int64_t)t * a.y_ld;
+                if (V2) {
+                    if (s1) store_vec<T, 2>(to, o);
+                } else {
+                    if (s1) to[0] = from_f32<T>(o[0]);
+                    if (s2) to[1] = from_f32<T>(o[1]);
+                }
             }
         }
         // the next chunk's y_s writes come after its own barrier, which follows these reads
     }
     if (a.state_out && on) store_vec<float, NPL>(a.state_out + so, s);
+    // not before: CTAs of a successor placed early would share SMs that this grid keeps busy
+    pdl_trigger();
 }
 
 constexpr int SCAN_STEP_MAX = 16;   // up to this many tokens the staging is not worth its barriers
 
+// Pairs of channels load and store as one where every row starts on a pair.
+bool pairs_ok(const ScanArgs& a, size_t es) {
+    auto ok = [&](const void* p, int64_t ld, int64_t seq) {
+        return !p || ((uintptr_t)p % (2 * es) == 0 && ld % 2 == 0 && seq % 2 == 0);
+    };
+    return a.D % 2 == 0 && ok(a.x, a.x_ld, a.x_seq) && ok(a.dt, a.dt_ld, a.dt_seq) && ok(a.z, a.z_ld, a.z_seq) &&
+           ok(a.Bm, a.b_ld, a.b_seq) && ok(a.Cm, a.c_ld, a.c_seq) && ok(a.y, a.y_ld, a.y_seq);
+}
+
 template <typename T, int N, int LPC>
 void scan_launch(const ScanArgs& a, int B, cudaStream_t s) {
+    const dim3 grid((a.D * LPC + 255) / 256, B);
     if (a.T <= SCAN_STEP_MAX)
-        launch_s(s, scan_step_kernel<T, N, LPC>, dim3((a.D * LPC + 255) / 256, B), dim3(256), 0, a);
+        launch_s(s, scan_step_kernel<T, N, LPC>, grid, dim3(256), 0, a);
+    else if (pairs_ok(a, sizeof(T)))
+        launch_s(s, scan_kernel<T, N, LPC, true>, grid, dim3(256), 0, a);
     else
-        launch_s(s, scan_kernel<T, N, LPC>, dim3((a.D * LPC + 255) / 256, B), dim3(256), 0, a);
+        launch_s(s, scan_kernel<T, N, LPC, false>, grid, dim3(256), 0, a);
 }
 
 template <typename T>
@@ -410,18 +538,18 @@ extern "C" evs_status evs_causal_conv(const evs_conv_args* c, void* stream) {
     using namespace evs;
     if (!c || c->batch < 0 || c->tokens < 0 || c->width < 1 || c->taps < 2 || c->taps > 16) return EVS_ERR_INVALID_ARG;
     if (c->dtype != EVS_DTYPE_F32 && c->dtype != EVS_DTYPE_BF16) return EVS_ERR_INVALID_ARG;
-    if (c->batch > 65535 || (long long)c->tokens > 65535LL * CONV_RUN || c->width > (1 << 24)) return EVS_ERR_INVALID_ARG;
+    if (c->batch > 65535 || c->tokens > (1 << 30) || c->width > (1 << 24)) return EVS_ERR_INVALID_ARG;
     if (c->batch == 0) return EVS_OK;
     if (!c->weight || (c->tokens > 0 && !c->x) || (!c->y && !c->tail_out)) return EVS_ERR_INVALID_ARG;
     if (c->x_ld < c->width || (c->y && c->y_ld < c->width)) return EVS_ERR_INVALID_ARG;
     if (c->tokens == 0 && !c->tail_out) return EVS_OK;
     ConvArgs a{c->x, c->tokens > 0 ? c->y : nullptr, c->weight, c->bias, c->tail_in, c->tail_out, c->lens, c->flags,
-               c->x_ld, c->x_seq, c->y_ld, c->y_seq, c->tokens, c->width, c->taps, c->silu ? 1 : 0};
+               c->x_ld, c->x_seq, c->y_ld, c->y_seq, c->tokens, c->width, c->taps, c->silu ? 1 : 0, 0};
     const int es = c->dtype == EVS_DTYPE_BF16 ? 2 : 4, v = 16 / es;
     // 16-byte accesses when every row starts on 16 bytes and the width is a whole number of them
     const bool wide = c->width % v == 0 && c->x_ld % v == 0 && c->x_seq % v == 0 && aligned(c->x, 16) &&
                       (!c->y || (c->y_ld % v == 0 && c->y_seq % v == 0 && aligned(c->y, 16))) &&
-                      (!c->tail_in || aligned(c->tail_in, 16)) && (!c->tail_out || aligned(c->tail_out, 16));
+                      aligned(c->weight, 16) && (!c->tail_in || aligned(c->tail_in, 16)) && (!c->tail_out || aligned(c->tail_out, 16));
     if (es == 2) conv_dispatch<bf16>(a, c->batch, wide, (cudaStream_t)stream);
     else conv_dispatch<float>(a, c->batch, wide, (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;

@@ -16,7 +16,8 @@
 // there. The cut (top-k and top-p are both prefixes of the sorted row, so one pair (logit, id)
 // describes what is kept) is found by a histogram over (max - l) / T in steps of 1/64, narrowed
 // by digits of (ordered logit, id) while the bin that holds the cut has more than CAP tokens;
-// those few are then ranked pairwise.
+// those few are then sorted. (Ranking them pairwise took 15 us for the 461 tokens left of a
+// 512-entry row, and one CTA's 17 us held the other seven of a large row's cluster.)
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -31,7 +32,7 @@ constexpr int SMP_IDBITS = 18;
 constexpr int SMP_ORDER_BITS = 32 + SMP_IDBITS;
 constexpr int SMP_DIGIT = 11;
 constexpr int SMP_BINS = 1 << SMP_DIGIT;
-constexpr int SMP_CAP = 1024;           // tokens ranked pairwise
+constexpr int SMP_CAP = 1024;           // tokens sorted
 constexpr int SMP_FRAC = 44;            // fixed point of weights; 2^18 of them stay below 2^63
 constexpr int SMP_MAX_CS = 8;           // portable cluster size
 
@@ -223,7 +224,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     __shared__ u64 x_cnt[SMP_MAX_CS], x_mass[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
     __shared__ u64 f_above_mass, f_cut, pick_before;
     __shared__ uint32_t f_bin, f_count, f_above_count, list_n;
-    __shared__ int pick_warp;
+    __shared__ int pick_warp, last_kept;
+    __shared__ float inv_total;
+    __shared__ struct {
+        u64 p64, u64_, mp;
+        float c_hi, c_lo, bin_scale, temp;
+        int k, greedy, need_p;
+    } par;
 
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -235,22 +242,24 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
 
-    // ---- parameters of the row
-    const float temp = a.temperature ? a.temperature[row] : 1.f;
-    const bool greedy = !(temp > 0.f);
-    const int k_in = a.top_k ? a.top_k[row] : 0;
-    const float p_in = a.top_p ? a.top_p[row] : 1.f;
-    const float mp_in = a.min_p ? a.min_p[row] : 0.f;
-    const bool need_k = !greedy && k_in > 0 && k_in < a.V;
-    const bool need_p = !greedy && p_in < 1.f;
-    WeightFn wf;
-    wf.tab = tab;
-    {
+    // ---- parameters of the row: one thread's few fp64 operations (their rate is 1/64 of fp32's)
+    if (tid == 0) {
+        const float temp = a.temperature ? a.temperature[row] : 1.f;
+        const int k = a.top_k ? a.top_k[row] : 0;
+        const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
+        const bool greedy = !(temp > 0.f);
         const double c = 1.4426950408889634074 / (greedy ? 1.0 : (double)temp);
-        wf.c_hi = (float)c;
-        wf.c_lo = isfinite(wf.c_hi) ? (float)(c - (double)wf.c_hi) : 0.f;
+        par.c_hi = (float)c;
+        par.c_lo = isfinite(par.c_hi) ? (float)(c - (double)par.c_hi) : 0.f;
+        par.bin_scale = 64.f / (greedy ? 1.f : temp);
+        par.temp = greedy ? 1.f : temp;
+        par.greedy = greedy;
+        par.k = !greedy && k > 0 && k < a.V ? k : 0;
+        par.need_p = !greedy && p < 1.f;
+        par.p64 = unit_fixed(p);
+        par.u64_ = unit_fixed(a.uniforms[row]);
+        par.mp = mp > 0.f && !greedy ? (u64)ceil((double)fminf(mp, 1.f) * (double)(1ull << SMP_FRAC)) : 0;
     }
-    const float bin_scale = 64.f / (greedy ? 1.f : temp);
 
     // ---- the slice: granules of 16 bytes of the row, the first and last ones partly filled
     const T* rp = (const T*)a.logits + (size_t)row * a.ld;
@@ -300,7 +309,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     } else {
         __syncthreads();
     }
-    wf.M = mx;
+    WeightFn wf{mx, par.c_hi, par.c_lo, tab};      // written before the barriers of the maximum
+    const float bin_scale = par.bin_scale;
+    const bool greedy = par.greedy, need_p = par.need_p;
+    const int k_in = par.k;
+    const bool need_k = k_in > 0;
     if (mx == -INFINITY) {                       // every token ruled out: no draw
         if (rank == 0 && tid == 0) {
             a.token[row] = -1;
@@ -444,65 +457,64 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             if (f.count <= SMP_CAP || f.shift == 0) return f;
         }
     };
-    // Ranks the gathered tokens (first CTA) and returns the order of the last one kept: the first
+    // Sorts the gathered tokens (first CTA) and returns the order of the last one kept: the first
     // k overall (k > 0), and with do_p of these the nucleus of mass x, or where x is 0 of
     // ceil(p64 * mass of the k). above_*: what precedes all of them.
     auto finish = [&](uint32_t above_count, u64 above_mass, uint32_t k, bool do_p, u64 p64, u64 x) -> u64 {
         sync_all<CLUSTER>();                      // every CTA's entries have arrived
         if (rank == 0) {
             const int m = min((int)list_n, SMP_CAP);
-            constexpr int PER = SMP_CAP / THREADS;
-            u64 o[PER], before[PER], w[PER], km = 0;
-            uint32_t rk[PER];
-            bool keep[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid + i * THREADS;
-                o[i] = e < m ? list_o[e] : 0;
-                w[i] = e < m ? list_w[e] : 0;
-                before[i] = above_mass;
-                rk[i] = above_count;
-            }
-            for (int j = 0; j < m; ++j) {
-                const u64 oj = list_o[j], wj = list_w[j];
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (oj > o[i]) {
-                        rk[i] += 1;
-                        before[i] += wj;
+            int n2 = 2;
+            while (n2 < m) n2 *= 2;
+            for (int e = m + tid; e < n2; e += THREADS) list_o[e] = list_w[e] = 0;
+            if (tid == 0) last_kept = 0;
+            __syncthreads();
+            // bitonic, descending; up to 64 entries by one warp
+            if (n2 > 64 || warp == 0) {
+                const int workers = n2 > 64 ? THREADS : 32;
+                for (int k2 = 2; k2 <= n2; k2 *= 2)
+                    for (int j = k2 / 2; j > 0; j /= 2) {
+                        for (int t = tid; t < n2 / 2; t += workers) {
+                            const int i = 2 * t - (t & (j - 1)), i2 = i + j;
+                            const u64 x0 = list_o[i], x1 = list_o[i2];
+                            if ((x0 < x1) == ((i & k2) == 0)) {
+                                const u64 w0 = list_w[i], w1 = list_w[i2];
+                                list_o[i] = x1;
+                                list_o[i2] = x0;
+                                list_w[i] = w1;
+                                list_w[i2] = w0;
+                            }
+                        }
+                        if (n2 > 64) __syncthreads(); else __syncwarp();
                     }
             }
+            __syncthreads();
+            constexpr int PER = SMP_CAP / THREADS;
+            u64 w[PER], mine = 0, total;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                keep[i] = tid + i * THREADS < m && (k == 0 || rk[i] < k);
-                km += keep[i] ? w[i] : 0;
+                const int e = tid * PER + i;
+                w[i] = e < m && (k == 0 || above_count + e < k) ? list_w[e] : 0;
+                mine += w[i];
             }
-            if (do_p) {
-                if (x == 0) {
-                    u64 total;
-                    block_scan_u64(km, red, total);
-                    total += above_mass;
-                    x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
-                    if (x == 0) x = 1;
-                }
-#pragma unroll
-                for (int i = 0; i < PER; ++i) keep[i] = keep[i] && before[i] < x;
+            u64 before = block_scan_u64(mine, red, total) + above_mass;
+            total += above_mass;
+            if (do_p && x == 0) {
+                x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
+                if (x == 0) x = 1;
             }
-            u64 lowest = ~0ull;
+            int kept_to = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (keep[i] && o[i] < lowest) lowest = o[i];
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) {
-                const u64 t = __shfl_xor_sync(0xffffffffu, lowest, s);
-                if (t < lowest) lowest = t;
+            for (int i = 0; i < PER; ++i) {
+                const int e = tid * PER + i;
+                if (e < m && (k == 0 || above_count + e < k) && (!do_p || before < x)) kept_to = e;
+                before += w[i];
             }
-            __syncthreads();
-            if (lane == 0) red[warp] = lowest;
+            kept_to = __reduce_max_sync(0xffffffffu, kept_to);
+            if (lane == 0 && kept_to > 0) atomicMax(&last_kept, kept_to);
             __syncthreads();
             if (tid < (int)cs) {
-                for (int i = 0; i < THREADS / 32; ++i)
-                    if (red[i] < lowest) lowest = red[i];
+                const u64 lowest = list_o[last_kept];
                 if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), lowest);
                 else f_cut = lowest;
             }
@@ -555,10 +567,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         }
         cut = best;
     } else if (need_k || need_p) {
-        const u64 p64 = unit_fixed(p_in);
+        const u64 p64 = par.p64;
         u64 x = 0;
         bool p_left = need_p;
-        if (a.V <= SMP_CAP) {                     // all of them ranked, no search
+        if (a.V <= SMP_CAP) {                     // all of them sorted, no search
             for (int s = tid; s < n; s += THREADS)
                 if (l_s[s] != -INFINITY) push(l_s[s], order_of(l_s[s], base + s));
             cut = finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0);
@@ -591,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     }
 
     // ---- the kept mass by ids: a warp owns consecutive slots ------------------------------------
-    const u64 mp = mp_in > 0.f && !greedy ? (u64)ceil((double)fminf(mp_in, 1.f) * (double)(1ull << SMP_FRAC)) : 0;
+    const u64 mp = par.mp;
     auto kept = [&](int s) -> u64 {
         const float l = l_s[s];
         if (l == -INFINITY || order_of(l, base + s) < cut) return 0;
@@ -620,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         }
     }
     // cumulative mass > u * total: integers, so > its floor
-    const u64 thr = __umul64hi(unit_fixed(a.uniforms[row]), total);
+    const u64 thr = __umul64hi(par.u64_, total);
     if (before <= thr && thr < before + mine) {
         if (tid == 0) {
             u64 c = before;
@@ -647,13 +659,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             a.token[row] = base + s;
             if (a.logprob) {
                 const double lw = l_s[s] == mx ? 0.0
-                                               : ((double)l_s[s] - (double)mx) / (greedy ? 1.0 : (double)temp);
+                                               : ((double)l_s[s] - (double)mx) / (double)par.temp;
                 a.logprob[row] = (float)(lw - log((double)total) + SMP_FRAC * 0.69314718055994530942);
             }
         }
     }
     if (a.probs) {
-        const float inv = (float)((double)(1ull << SMP_FRAC) / (double)total);
+        if (tid == 0) inv_total = (float)((double)(1ull << SMP_FRAC) / (double)total);
+        __syncthreads();
+        const float inv = inv_total;
         float* pr = a.probs + (size_t)row * a.ldp;
         for (int s = tid; s < n; s += THREADS) {
             const int id = base + s;

@@ -112,9 +112,10 @@ def conv(x, w, bias, tail, lens, silu=True):
 def scan(x, dt, A, B, C, D, z, dt_bias, state, lens, softplus=True):
     """y, state, and bounds of their fp32 errors; fp64 torch, lens a list.
 
-    Errors, with u = 2^-24: softplus to 8u relative (expf, log1pf and the sum before them); A log2(e) and its
-    product with the step 2u, ex2.approx 4u: so a decay exp(-r) is off by (8 + 2) u r + 4u relative, the input
-    term by 12u, and each step's multiply-add rounds once more (2u of the magnitudes)."""
+    Errors, with u = 2^-24: softplus to 12u relative (the exponential 5u, its quotient 4u and a half, the series,
+    the product and the sum one each; its own argument's rounding apart); A log2(e) and its product with the
+    step 2u, ex2.approx 4u: so a decay exp(-r) is off by (12 + 2) u r + 4u relative, the input term by 16u, and
+    each step's multiply-add rounds once more (2u of the magnitudes)."""
     Bn, T, W = x.shape
     N = A.shape[1]
     u = 2.0 ** -24
@@ -135,8 +136,8 @@ def scan(x, dt, A, B, C, D, z, dt_bias, state, lens, softplus=True):
             a = torch.exp(r)
             inp = (dl * x[b, t])[:, None] * B[b, t]
             # v rounds by u |v| before the softplus, whose slope there is at most dl
-            err = a * err + a * mag * u * (10.0 * r.abs() + v.abs()[:, None] * r.abs() + 6.0) + \
-                inp.abs() * u * (14.0 + v.abs()[:, None])
+            err = a * err + a * mag * u * (14.0 * r.abs() + v.abs()[:, None] * r.abs() + 6.0) + \
+                inp.abs() * u * (18.0 + v.abs()[:, None])
             mag = a * mag + inp.abs()
             h = a * h + inp
             s = (h * C[b, t]).sum(-1)

@@ -59,7 +59,7 @@ def _conv(L, **kw):
 
 @pytest.mark.parametrize("bad", [dict(batch=-1), dict(tokens=-1), dict(width=0), dict(taps=1), dict(taps=17),
                                  dict(dtype=3), dict(weight=None), dict(x=None), dict(y=None), dict(x_ld=63),
-                                 dict(y_ld=63), dict(batch=65536), dict(tokens=65535 * 32 + 1),
+                                 dict(y_ld=63), dict(batch=65536), dict(tokens=(1 << 30) + 1),
                                  dict(width=1 << 25, x_ld=1 << 25, y_ld=1 << 25)])
 def test_conv_refuses(L, bad):
     assert _conv(L, **bad) == INV
