@@ -12,11 +12,30 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // ---- vectors of consecutive channels --------------------------------------------------------
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Chunk { T v[VEC]; };
-
+// Raw words, so that a vector is one load, and loads are never conditional: out of range they take
+// a valid neighbour. (Loads under a condition each wait for the one before: 14 of them, at 700
+// cycles apiece, made a chunk of the scan take 10400 cycles.)
+template <int BYTES> struct Word;
+template <> struct Word<2> { using type = unsigned short; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<16> { using type = uint4; };
+struct TwoWords { uint4 a, b; };
+template <> struct Word<32> { using type = TwoWords; };
+template <typename T, int VEC> union Chunk {
+    typename Word<sizeof(T) * VEC>::type raw;
+    T v[VEC];
+    __device__ Chunk() {}
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Chunk<T, VEC> load_chunk(const T* p) {
+    Chunk<T, VEC> c;
+    c.raw = *reinterpret_cast<const typename Word<sizeof(T) * VEC>::type*>(p);
+    return c;
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
-    const Chunk<T, VEC> c = *reinterpret_cast<const Chunk<T, VEC>*>(p);
+    const Chunk<T, VEC> c = load_chunk<T, VEC>(p);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = to_f32(c.v[i]);
 }
@@ -25,7 +44,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
     Chunk<T, VEC> c;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) c.v[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<Chunk<T, VEC>*>(p) = c;
+    *reinterpret_cast<typename Word<sizeof(T) * VEC>::type*>(p) = c.raw;
 }
 
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
@@ -46,7 +65,7 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T, uint32
 //
 // A thread owns VEC consecutive channels and a run of consecutive positions: the window slides
 // through registers, so x is read once but for the L - 1 rows before a run, and the weights once a
-// run. The next eight rows are requested before the last eight are used. The thread of the first
+// run. The next four rows are requested before the last four are used. The thread of the first
 // run also writes the tail (after it has read the old one), so the two may be the same buffer.
 // HBM-bound: x read + y written.
 // =========================================================================================
@@ -127,18 +146,17 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
     }
     if (!y) return;
     const int t1 = min(t0 + a.run, len);
-    Chunk<T, VEC> in[8], nx[8];
-    auto fetch = [&](int s, Chunk<T, VEC> (&c)[8]) {
+    if (t0 >= t1) return;
+    constexpr int AHEAD = 4;                       // rows requested while as many are worked on
+    Chunk<T, VEC> buf[2][AHEAD];
+    auto fetch = [&](int s, Chunk<T, VEC> (&c)[AHEAD]) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (s + u < t1) c[u] = *reinterpret_cast<const Chunk<T, VEC>*>(x + (size_t)(s + u) * a.x_ld);
+        for (int u = 0; u < AHEAD; ++u) c[u] = load_chunk<T, VEC>(x + (int64_t)min(s + u, t1 - 1) * a.x_ld);
     };
-    fetch(t0, in);
-    for (int s = t0; s < t1; s += 8) {
-        fetch(s + 8, nx);
+    auto work = [&](int s, const Chunk<T, VEC> (&in)[AHEAD]) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (s + u >= t1) break;
+        for (int u = 0; u < AHEAD; ++u) {
+            if (s + u >= t1) return;
             float out[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -152,10 +170,15 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
                 hist[0][i] = v;
                 out[i] = a.act ? silu(acc) : acc;
             }
-            store_vec<T, VEC>(y + (size_t)(s + u) * a.y_ld, out);
+            store_vec<T, VEC>(y + (int64_t)(s + u) * a.y_ld, out);
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) in[u] = nx[u];
+    };
+    fetch(t0, buf[0]);
+    for (int s = t0; s < t1; s += 2 * AHEAD) {
+        fetch(s + AHEAD, buf[1]);
+        work(s, buf[0]);
+        fetch(s + 2 * AHEAD, buf[0]);
+        work(s + AHEAD, buf[1]);
     }
     pdl_trigger();
 }
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
     // staging: thread -> channels 2 (tid % (CH / 2)) and the next, positions tid / (CH / 2) + i RP
     const int sc = tid % (CH / 2) * 2, sr = tid / (CH / 2);
     const bool s1 = ch0 + sc < a.D, s2 = ch0 + sc + 1 < a.D;
-    const int gch = min(ch0 + sc, a.D - 1), gch2 = min(ch0 + sc + 1, a.D - 1);
+    const int gch = min(ch0 + sc, a.D - (V2 ? 2 : 1)), gch2 = min(gch + 1, a.D - 1);
     const float2 bias = a.dt_bias ? make_float2(a.dt_bias[gch], a.dt_bias[gch2]) : make_float2(0.f, 0.f);
     const float2 Ds = a.Dskip ? make_float2(a.Dskip[gch], a.Dskip[gch2]) : make_float2(0.f, 0.f);
     const T* x = (const T*)a.x + (size_t)b * a.x_seq + gch;
@@ -367,32 +390,27 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
     const T* Cm = (const T*)a.Cm + (size_t)b * a.c_seq;
     T* y = a.y ? (T*)a.y + (size_t)b * a.y_seq + gch : nullptr;
     Chunk<T, 2> xr[PER], dr[PER], zr[PER], br[PBC], cr[PBC];
-    auto two = [&](const T* p, bool f1, bool f2) -> Chunk<T, 2> {
+    const int other = gch2 - gch;                 // the second channel's place; 0: there is none
+    auto two = [&](const T* p, int second) -> Chunk<T, 2> {
+        if (V2) return load_chunk<T, 2>(p);
         Chunk<T, 2> r;
-        r.v[0] = r.v[1] = from_f32<T>(0.f);
-        if (V2) {
-            if (f1) r = *reinterpret_cast<const Chunk<T, 2>*>(p);
-        } else {
-            if (f1) r.v[0] = p[0];
-            if (f2) r.v[1] = p[1];
-        }
+        r.v[0] = p[0];
+        r.v[1] = p[second];
         return r;
     };
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = t0 + sr + i * RP;
-            const bool in = t < len;
-            xr[i] = two(x + (int64_t)t * a.x_ld, in && s1, in && s2);
-            dr[i] = two(dt + (int64_t)t * a.dt_ld, in && s1, in && s2);
-            if (z) zr[i] = two(z + (int64_t)t * a.z_ld, in && s1, in && s2);
+            const int t = min(t0 + sr + i * RP, len - 1);
+            xr[i] = two(x + (int64_t)t * a.x_ld, other);
+            dr[i] = two(dt + (int64_t)t * a.dt_ld, other);
+            if (z) zr[i] = two(z + (int64_t)t * a.z_ld, other);
         }
 #pragma unroll
         for (int i = 0; i < PBC; ++i) {
-            const int e = (tid + i * 256) * 2, t = t0 + e / N;
-            const bool in = e < SCAN_TC * N && t < len;
-            br[i] = two(Bm + (int64_t)t * a.b_ld + e % N, in, in);
-            cr[i] = two(Cm + (int64_t)t * a.c_ld + e % N, in, in);
+            const int e = (tid + i * 256) * 2 % (SCAN_TC * N), t = min(t0 + e / N, len - 1);
+            br[i] = two(Bm + (int64_t)t * a.b_ld + e % N, 1);
+            cr[i] = two(Cm + (int64_t)t * a.c_ld + e % N, 1);
         }
     };
     if (len > 0) fetch(0);
