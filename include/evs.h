@@ -469,7 +469,12 @@ typedef struct {
     float* state_out;            /* likewise, or NULL                                       */
     const int32_t* lens;         /* device [batch] or NULL                                  */
     uint32_t* flags;
+    void* workspace;             /* device, 16-byte aligned, or NULL where none is needed; not shared
+                                    by calls that may overlap                               */
+    size_t ws_bytes;
 } evs_scan_args;
+/* Bytes of workspace for these sizes (0: none; prompts of few sequences are run in segments). */
+size_t evs_selective_scan_workspace(int32_t batch, int32_t tokens, int32_t width, int32_t states);
 evs_status evs_selective_scan(const evs_scan_args* args, void* stream);
 
 /* Static description of a status code. */

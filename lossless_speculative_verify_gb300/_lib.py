@@ -29,7 +29,7 @@ EXPORTED = (
     "evs_export_state", "evs_debug_buffer", "evs_device_flags", "evs_last_launch_count",
     "evs_status_str", "evs_profile_enable", "evs_profile_read", "evs_debug_projection",
     "evs_projection_noalloc", "evs_projection_noalloc_flags", "evs_sample", "evs_decode_filtered",
-    "evs_causal_conv", "evs_selective_scan", "evs_shared_attention_workspace", "evs_shared_attention",
+    "evs_causal_conv", "evs_selective_scan", "evs_selective_scan_workspace", "evs_shared_attention_workspace", "evs_shared_attention",
 )
 KERNEL_KINDS = ("embed", "norm", "gemm", "fir", "iir", "kv_write", "attn", "attn_combine", "accept",
                 "slice", "advance")
@@ -85,7 +85,7 @@ class ConvArgs(C.Structure):
 class ScanArgs(C.Structure):
     _fields_ = _fields("i batch, tokens, width, states, dtype, softplus; p x; q x_ld, x_seq; p dt; q dt_ld, dt_seq; "
                        "p z; q z_ld, z_seq; p B; q b_ld, b_seq; p C; q c_ld, c_seq; p y; q y_ld, y_seq; "
-                       "p A, D, dt_bias, state_in, state_out, lens, flags")
+                       "p A, D, dt_bias, state_in, state_out, lens, flags, workspace; z ws_bytes")
 
 
 class SharedAttnArgs(C.Structure):
@@ -157,6 +157,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         fn.argtypes = [C.POINTER(args), vp]
     lib.evs_shared_attention_workspace.restype = C.c_size_t
     lib.evs_shared_attention_workspace.argtypes = [C.POINTER(SharedAttnArgs)]
+    lib.evs_selective_scan_workspace.restype = C.c_size_t
+    lib.evs_selective_scan_workspace.argtypes = [i32, i32, i32, i32]
     lib.evs_decode_filtered.restype = C.c_int
     lib.evs_decode_filtered.argtypes = [vp, vp, C.POINTER(SampleArgs), vp]
     lib.evs_status_str.restype = C.c_char_p

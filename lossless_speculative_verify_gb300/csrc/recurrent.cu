@@ -20,8 +20,9 @@ template <> struct Word<2> { using type = unsigned short; };
 template <> struct Word<4> { using type = uint32_t; };
 template <> struct Word<8> { using type = uint2; };
 template <> struct Word<16> { using type = uint4; };
-struct TwoWords { uint4 a, b; };
-template <> struct Word<32> { using type = TwoWords; };
+template <int N> struct Words { uint4 w[N]; };
+template <> struct Word<32> { using type = Words<2>; };
+template <> struct Word<64> { using type = Words<4>; };
 template <typename T, int VEC> union Chunk {
     typename Word<sizeof(T) * VEC>::type raw;
     T v[VEC];
@@ -45,6 +46,28 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) c.v[i] = from_f32<T>(f[i]);
     *reinterpret_cast<typename Word<sizeof(T) * VEC>::type*>(p) = c.raw;
+}
+
+// ---- pairs of fp32 ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
@@ -158,6 +181,27 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
         for (int u = 0; u < AHEAD; ++u) {
             if (s + u >= t1) return;
             float out[VEC];
+            if constexpr (VEC % 2 == 0 && LMAX <= 4) {
+                // pairs of channels: the taps and the activation in packed fp32
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2) {
+                    const float v0 = to_f32(in[u].v[i]), v1 = to_f32(in[u].v[i + 1]);
+                    uint64_t acc = fma2(pair_of(w[0][i], w[0][i + 1]), pair_of(v0, v1), pair_of(bias[i], bias[i + 1]));
+#pragma unroll
+                    for (int j = 1; j < LMAX; ++j)
+                        acc = fma2(pair_of(w[j][i], w[j][i + 1]), pair_of(hist[j - 1][i], hist[j - 1][i + 1]), acc);
+#pragma unroll
+                    for (int j = LMAX - 2; j > 0; --j) {
+                        hist[j][i] = hist[j - 1][i];
+                        hist[j][i + 1] = hist[j - 1][i + 1];
+                    }
+                    hist[0][i] = v0;
+                    hist[0][i + 1] = v1;
+                    const float2 r = unpair(acc);
+                    out[i] = a.act ? silu(r.x) : r.x;
+                    out[i + 1] = a.act ? silu(r.y) : r.y;
+                }
+            } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const float v = to_f32(in[u].v[i]);
@@ -169,6 +213,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
                 for (int j = LMAX - 2; j > 0; --j) hist[j][i] = hist[j - 1][i];
                 hist[0][i] = v;
                 out[i] = a.act ? silu(acc) : acc;
+            }
             }
             store_vec<T, VEC>(y + (int64_t)(s + u) * a.y_ld, out);
         }
@@ -264,28 +309,6 @@ __device__ __forceinline__ float step_size(float v, int softplus) {
     return v != v ? v : r;
 }
 
-// ---- pairs of fp32 ---------------------------------------------------------------------------
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // A few tokens (single tokens, verify blocks): lanes of a channel hold NPL states each, straight
 // from global memory; HBM-bound on the state read and written.
 template <typename T, int N, int LPC>
@@ -339,211 +362,300 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
     if (a.state_out && on) store_vec<float, NPL>(a.state_out + so, s);
 }
 
-// Prompts. A CTA owns CH channels of one sequence and walks its tokens SCAN_TC at a time: the
-// chunk's dl and dl x are formed once per (t, channel) into shared memory together with B_t and
-// C_t, then LPC lanes of each channel run the recurrence over it, two states to an instruction, then
-// the outputs leave with coalesced stores. The next chunk's raw values are requested before the
-// recurrence of this one starts. The recurrence's own chain is one multiply-add a step: the
-// exponentials of later steps do not depend on it, so they fill the pipe. Bound by issue: one
-// exponential, half of four packed operations and its share of the staging per (t, c, n).
-constexpr int SCAN_TC = 32;
+// Prompts. A lane owns a channel (LPC lanes where it has 32 states) with its states in registers, a
+// warp 32 / LPC neighbouring channels. x, dt and z come asynchronously into the warp's own ring of
+// SCAN_RING groups of eight positions, B_t and C_t into shared memory for the CTA, 32 positions at a
+// time, which all lanes read as one address. Nothing is exchanged between lanes.
+//
+// That leaves few warps for few sequences, so the tokens are cut into segments: a first pass runs
+// each segment from a zero state (the first from state_in) and leaves its last state and the sum of
+// its step sizes; the second starts every segment from
+//   s(j) = exp(A sum dl(j-1)) s(j-1) + last(j-1),
+// folded over the segments before it, and writes the outputs. The first pass costs the
+// exponentials once more: segments are taken only where warps are short.
+constexpr int SCAN_TC = 32, SCAN_WARPS = 4, SCAN_RING = 6;
 
-template <typename T, int N, int LPC, bool V2>
-__global__ void __launch_bounds__(256) scan_kernel(ScanArgs a) {
-    constexpr int NPL = N / LPC;
-    constexpr int CH = 256 / LPC;
-    constexpr int RP = 512 / CH;                     // rows that one pass of the threads stages
-    constexpr int PER = SCAN_TC / RP;
-    constexpr int PBC = (SCAN_TC * N / 2 + 255) / 256;
-    constexpr int YS = CH + 4;                       // eight steps of a channel's lanes in different banks
-    __shared__ __align__(16) float2 du_s[SCAN_TC][CH];   // dl, dl * x
-    __shared__ __align__(16) float y_s[SCAN_TC][YS];
-    __shared__ __align__(16) float b_s[SCAN_TC][N], c_s[SCAN_TC][N];
+template <int BYTES> __device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+
+struct ScanSeg {
+    float* ws;          // [b][segment][N + 1][D]: last states and the sum of dl; then [b][N][D] state_in
+    int segs, len;      // segments of a sequence, positions of one
+};
+
+// V2: rows of channel pairs that can be copied asynchronously (they start on two elements).
+template <typename T, int N, int LPC, bool FIRST, bool V2>
+__global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanSeg sg) {
+    constexpr int NPL = N / LPC, THREADS = 32 * SCAN_WARPS, CPW = 32 / LPC, PAIRS = CPW / 2;
+    constexpr int PXL = 8 * PAIRS / 32;              // pairs of a group that a lane copies
+    constexpr int GROUP = 8 * CPW;                   // values of one array in a ring slot
+    extern __shared__ __align__(16) uint8_t ring_raw[];
+    constexpr int PBC = (SCAN_TC * N / 2 + THREADS - 1) / THREADS;
+    __shared__ __align__(16) float b_s[2][SCAN_TC][N], c_s[2][SCAN_TC][N];
     pdl_wait();
-    const int b = blockIdx.y, tid = threadIdx.x;
-    const int ch0 = blockIdx.x * CH;
-    const int len = seq_len(a.lens, b, a.T, a.flags, blockIdx.x == 0 && tid == 0);
-    const int lch = tid / LPC, sub = tid % LPC, k0 = sub * NPL;
-    const int ch = min(ch0 + lch, a.D - 1);
-    const bool on = ch0 + lch < a.D;
-    float A2[NPL], s[NPL];
-    load_vec<float, NPL>(a.A + (size_t)ch * N + k0, A2);
-    const size_t so = ((size_t)b * a.D + ch) * N + k0;
-    if (a.state_in) {
-        load_vec<float, NPL>(a.state_in + so, s);
-    } else {
-#pragma unroll
-        for (int k = 0; k < NPL; ++k) s[k] = 0.f;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.y, j = blockIdx.z, t0 = j * sg.len;
+    const int len = seq_len(a.lens, b, a.T, a.flags, FIRST == (sg.segs > 1) && blockIdx.x == 0 && j == 0 && tid == 0);
+    const int t1 = min(t0 + sg.len, len);
+    const bool last = t1 == len && (t0 < len || j == 0);   // the sequence ends here
+    const int raw = (blockIdx.x * SCAN_WARPS + warp) * CPW + lane / LPC, k0 = lane % LPC * NPL;
+    const bool on = raw < a.D;
+    const int ch = on ? raw : a.D - 1;
+    // a first pass serves segments that another one follows; a second one without outputs the last
+    if (FIRST ? t0 + sg.len >= len : (t0 >= len && j > 0) || (!a.y && !last)) {
+        pdl_trigger();
+        return;
     }
+    uint64_t A2[NPL / 2], s[NPL / 2];                // pairs of states
+    auto of_state = [&](const float* p, int64_t step, int k) { return on ? p[(k0 + k) * step] : 0.f; };
+    {
+        float v[NPL];
+        load_vec<float, NPL>(a.A + (size_t)ch * N + k0, v);
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) A2[k] *= kLog2e;
-    // staging: thread -> channels 2 (tid % (CH / 2)) and the next, positions tid / (CH / 2) + i RP
-    const int sc = tid % (CH / 2) * 2, sr = tid / (CH / 2);
-    const bool s1 = ch0 + sc < a.D, s2 = ch0 + sc + 1 < a.D;
-    const int gch = min(ch0 + sc, a.D - (V2 ? 2 : 1)), gch2 = min(gch + 1, a.D - 1);
-    const float2 bias = a.dt_bias ? make_float2(a.dt_bias[gch], a.dt_bias[gch2]) : make_float2(0.f, 0.f);
-    const float2 Ds = a.Dskip ? make_float2(a.Dskip[gch], a.Dskip[gch2]) : make_float2(0.f, 0.f);
-    const T* x = (const T*)a.x + (size_t)b * a.x_seq + gch;
-    const T* dt = (const T*)a.dt + (size_t)b * a.dt_seq + gch;
-    const T* z = a.z ? (const T*)a.z + (size_t)b * a.z_seq + gch : nullptr;
+        for (int k = 0; k < NPL; k += 2) A2[k / 2] = pair_of(v[k] * kLog2e, v[k + 1] * kLog2e);
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) v[k] = 0.f;
+        float* keep = sg.ws + (size_t)gridDim.y * sg.segs * (N + 1) * a.D + (size_t)b * N * a.D + ch;
+        if (j == 0 && a.state_in) {
+            if (!FIRST && sg.segs > 1) {          // state_out may be state_in: the first pass kept a copy
+#pragma unroll
+                for (int k = 0; k < NPL; ++k) v[k] = of_state(keep, a.D, k);
+            } else {
+                load_vec<float, NPL>(a.state_in + ((size_t)b * a.D + ch) * N + k0, v);
+            }
+        }
+        if (FIRST && j == 0 && a.state_in && on) {
+#pragma unroll
+            for (int k = 0; k < NPL; ++k) keep[(int64_t)(k0 + k) * a.D] = v[k];
+        }
+        if (!FIRST) {
+            const float* w = sg.ws + (size_t)b * sg.segs * (N + 1) * a.D + ch;
+            for (int i = 0; i < j; ++i, w += (size_t)(N + 1) * a.D) {
+                const float sum = w[(int64_t)N * a.D];
+#pragma unroll
+                for (int k = 0; k < NPL; k += 2) {
+                    const float2 r = unpair(mul2(pair_of(sum, sum), A2[k / 2]));
+                    v[k] = fmaf(ex2(r.x), v[k], w[(int64_t)(k0 + k) * a.D]);
+                    v[k + 1] = fmaf(ex2(r.y), v[k + 1], w[(int64_t)(k0 + k + 1) * a.D]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NPL; k += 2) s[k / 2] = pair_of(v[k], v[k + 1]);
+    }
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, Ds = a.Dskip ? a.Dskip[ch] : 0.f;
+    const T* xb = (const T*)a.x + (size_t)b * a.x_seq;
+    const T* db = (const T*)a.dt + (size_t)b * a.dt_seq;
+    const bool out = !FIRST && a.y != nullptr, gated = out && a.z != nullptr;
+    const T* zb = gated ? (const T*)a.z + (size_t)b * a.z_seq : xb;
     const T* Bm = (const T*)a.Bm + (size_t)b * a.b_seq;
     const T* Cm = (const T*)a.Cm + (size_t)b * a.c_seq;
-    T* y = a.y ? (T*)a.y + (size_t)b * a.y_seq + gch : nullptr;
-    Chunk<T, 2> xr[PER], dr[PER], zr[PER], br[PBC], cr[PBC];
-    const int other = gch2 - gch;                 // the second channel's place; 0: there is none
-    auto two = [&](const T* p, int second) -> Chunk<T, 2> {
-        if (V2) return load_chunk<T, 2>(p);
-        Chunk<T, 2> r;
-        r.v[0] = p[0];
-        r.v[1] = p[second];
-        return r;
-    };
-    auto fetch = [&](int t0) {
+    T* y = out ? (T*)a.y + (size_t)b * a.y_seq + ch : nullptr;
+    float sum = 0.f;
+    T* ring = reinterpret_cast<T*>(ring_raw) + (size_t)warp * SCAN_RING * 3 * GROUP;
+    const int c0 = (blockIdx.x * SCAN_WARPS + warp) * CPW;    // the warp's first channel
+    const int groups = (max(t1 - t0, 0) + 7) / 8;
+    // Positions t0 + 8 g .. + 7 into the ring; past the end the last row again, past the width the
+    // last channels. A pair that straddles neither is copied as it lies.
+    auto request = [&](int g) {
+        if (g < groups) {
+            T* to = ring + g % SCAN_RING * (3 * GROUP);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = min(t0 + sr + i * RP, len - 1);
-            xr[i] = two(x + (int64_t)t * a.x_ld, other);
-            dr[i] = two(dt + (int64_t)t * a.dt_ld, other);
-            if (z) zr[i] = two(z + (int64_t)t * a.z_ld, other);
-        }
+            for (int i = 0; i < PXL; ++i) {
+                const int e = lane + 32 * i, c = min(c0 + e % PAIRS * 2, a.D - (V2 ? 2 : 1)), o = V2 ? 0 : min(c + 1, a.D - 1) - c;
+                const int64_t t = min(t0 + 8 * g + e / PAIRS, t1 - 1);
+                const T *px = xb + t * a.x_ld + c, *pd = db + t * a.dt_ld + c, *pz = gated ? zb + t * a.z_ld + c : px;
+                if (V2) {
+                    cp_async<2 * sizeof(T)>(to + 2 * e, px);
+                    cp_async<2 * sizeof(T)>(to + GROUP + 2 * e, pd);
+                    if (gated) cp_async<2 * sizeof(T)>(to + 2 * GROUP + 2 * e, pz);
+                } else {
+                    const T v[6] = {px[0], px[o], pd[0], pd[o], pz[0], pz[o]};
 #pragma unroll
-        for (int i = 0; i < PBC; ++i) {
-            const int e = (tid + i * 256) * 2 % (SCAN_TC * N), t = min(t0 + e / N, len - 1);
-            br[i] = two(Bm + (int64_t)t * a.b_ld + e % N, 1);
-            cr[i] = two(Cm + (int64_t)t * a.c_ld + e % N, 1);
-        }
-    };
-    if (len > 0) fetch(0);
-    for (int t0 = 0; t0 < len; t0 += SCAN_TC) {
-        Chunk<T, 2> xc[PER], zc[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            // positions past the end keep the state: dl = 0 gives a decay of one and no input
-            const bool in = t0 + sr + i * RP < len;
-            const float d0 = in ? step_size(to_f32(dr[i].v[0]) + bias.x, a.softplus) : 0.f;
-            const float d1 = in ? step_size(to_f32(dr[i].v[1]) + bias.y, a.softplus) : 0.f;
-            *reinterpret_cast<float4*>(&du_s[sr + i * RP][sc]) =
-                make_float4(d0, d0 * to_f32(xr[i].v[0]), d1, d1 * to_f32(xr[i].v[1]));
-            xc[i] = xr[i];
-            zc[i] = zr[i];
-        }
-#pragma unroll
-        for (int i = 0; i < PBC; ++i) {
-            const int e = (tid + i * 256) * 2;
-            if (e < SCAN_TC * N) {
-                *reinterpret_cast<float2*>(&b_s[e / N][e % N]) = make_float2(to_f32(br[i].v[0]), to_f32(br[i].v[1]));
-                *reinterpret_cast<float2*>(&c_s[e / N][e % N]) = make_float2(to_f32(cr[i].v[0]), to_f32(cr[i].v[1]));
+                    for (int k = 0; k < 6; ++k) to[k / 2 * GROUP + 2 * e + k % 2] = v[k];
+                }
             }
         }
-        __syncthreads();
-        if (t0 + SCAN_TC < len) fetch(t0 + SCAN_TC);
-#pragma unroll 1
-        for (int i0 = 0; i0 < SCAN_TC; i0 += 8) {
-            float q[8];
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    T br[PBC][2], cr[PBC][2];
+    auto fetch_bc = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PBC; ++i) {
+            const int e = (tid + i * THREADS) * 2 % (SCAN_TC * N);
+            const int64_t at = min(t + e / N, t1 - 1);
+            br[i][0] = Bm[at * a.b_ld + e % N];
+            br[i][1] = Bm[at * a.b_ld + e % N + 1];
+            if (!FIRST) {
+                cr[i][0] = Cm[at * a.c_ld + e % N];
+                cr[i][1] = Cm[at * a.c_ld + e % N + 1];
+            }
+        }
+    };
+    auto place_bc = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < PBC; ++i) {
+            const int e = (tid + i * THREADS) * 2;
+            if (e < SCAN_TC * N) {
+                *reinterpret_cast<float2*>(&b_s[buf][0][0] + e) = make_float2(to_f32(br[i][0]), to_f32(br[i][1]));
+                if (!FIRST)
+                    *reinterpret_cast<float2*>(&c_s[buf][0][0] + e) = make_float2(to_f32(cr[i][0]), to_f32(cr[i][1]));
+            }
+        }
+    };
+    const int my = min(ch - c0, CPW - 1);            // this lane's channel in a ring row
+    auto steps = [&](int g, int row, int buf) {
+        // the three parts apart, each eight positions wide, so that their chains fill one another
+        const T* from = ring + g % SCAN_RING * (3 * GROUP) + my;
+        const int t = t0 + 8 * g;
+        float xv[8], dl[8], q[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            xv[u] = to_f32(from[u * CPW]);
+            dl[u] = step_size(to_f32(from[GROUP + u * CPW]) + bias, a.softplus);
+            // positions past the end keep the state: dl = 0 gives a decay of one, and no input
+            if (t + u >= t1) dl[u] = xv[u] = 0.f;
+            if (FIRST) sum += dl[u];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float ux = dl[u] * xv[u];
+            const uint64_t dl2 = pair_of(dl[u], dl[u]), u2 = pair_of(ux, ux);
+            uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+            for (int k = 0; k < NPL / 2; k += 2) {
+                // four states' B and C, one address for all lanes of a part
+                const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&b_s[buf][row + u][k0 + 2 * k]);
+                const float2 r0 = unpair(mul2(dl2, A2[k])), r1 = unpair(mul2(dl2, A2[k + 1]));
+                s[k] = fma2(pair_of(ex2(r0.x), ex2(r0.y)), s[k], mul2(u2, bv.x));
+                s[k + 1] = fma2(pair_of(ex2(r1.x), ex2(r1.y)), s[k + 1], mul2(u2, bv.y));
+                if (!FIRST) {
+                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&c_s[buf][row + u][k0 + 2 * k]);
+                    acc0 = k == 0 ? mul2(s[k], cv.x) : fma2(s[k], cv.x, acc0);
+                    acc1 = k == 0 ? mul2(s[k + 1], cv.y) : fma2(s[k + 1], cv.y, acc1);
+                }
+            }
+            const float2 v0 = unpair(acc0), v1 = unpair(acc1);
+            q[u] = (v0.x + v0.y) + (v1.x + v1.y);
+        }
+        if (out) {
+#pragma unroll
+            for (int o = LPC / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) q[u] += __shfl_xor_sync(0xffffffffu, q[u], o);
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float2 du = du_s[i0 + u][lch];
-                float bv[NPL], cv[NPL];
-                load_vec<float, NPL>(&b_s[i0 + u][k0], bv);
-                load_vec<float, NPL>(&c_s[i0 + u][k0], cv);
-                if constexpr (NPL % 2 == 0) {
-                    const uint64_t dl2 = pair_of(du.x, du.x), u2 = pair_of(du.y, du.y);
-                    uint64_t acc = 0;
-#pragma unroll
-                    for (int k = 0; k < NPL; k += 2) {
-                        const float2 r = unpair(mul2(dl2, pair_of(A2[k], A2[k + 1])));
-                        const uint64_t ns = fma2(pair_of(ex2(r.x), ex2(r.y)), pair_of(s[k], s[k + 1]),
-                                                 mul2(u2, pair_of(bv[k], bv[k + 1])));
-                        acc = fma2(ns, pair_of(cv[k], cv[k + 1]), acc);
-                        const float2 sv = unpair(ns);
-                        s[k] = sv.x;
-                        s[k + 1] = sv.y;
-                    }
-                    const float2 v = unpair(acc);
-                    q[u] = v.x + v.y;
-                } else {
-                    float acc = 0.f;
-#pragma unroll
-                    for (int k = 0; k < NPL; ++k) {
-                        s[k] = fmaf(ex2(du.x * A2[k]), s[k], du.y * bv[k]);
-                        acc = fmaf(s[k], cv[k], acc);
-                    }
-                    q[u] = acc;
-                }
-            }
-            // sum the eight steps over the channel's lanes; each lane is left with 8 / LPC of them
-            int first = 0;
-#pragma unroll
-            for (int o = LPC / 2, n = 4; o > 0; o >>= 1, n >>= 1) {
-                const bool up = (sub & o) != 0;
-#pragma unroll
-                for (int u = 0; u < n; ++u) {
-                    const float give = up ? q[u] : q[u + n], keep = up ? q[u + n] : q[u];
-                    q[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-                first += up ? n : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < 8 / LPC; ++u) y_s[i0 + first + u][lch] = q[u];
-        }
-        __syncthreads();
-        if (y) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int r = sr + i * RP, t = t0 + r;
-                if (t >= len) break;
-                const float2 v = *reinterpret_cast<const float2*>(&y_s[r][sc]);
-                float o[2] = {fmaf(Ds.x, to_f32(xc[i].v[0]), v.x), fmaf(Ds.y, to_f32(xc[i].v[1]), v.y)};
-                if (z) {
-                    o[0] *= silu(to_f32(zc[i].v[0]));
-                    o[1] *= silu(to_f32(zc[i].v[1]));
-                }
-                T* to = y + (int64_t)t * a.y_ld;
-                if (V2) {
-                    if (s1) store_vec<T, 2>(to, o);
-                } else {
-                    if (s1) to[0] = from_f32<T>(o[0]);
-                    if (s2) to[1] = from_f32<T>(o[1]);
-                }
+                q[u] = fmaf(Ds, xv[u], q[u]);
+                if (gated) q[u] *= silu(to_f32(from[2 * GROUP + u * CPW]));
+                if (t + u < t1 && on && k0 == 0) y[(int64_t)(t + u) * a.y_ld] = from_f32<T>(q[u]);
             }
         }
-        // the next chunk's y_s writes come after its own barrier, which follows these reads
+    };
+    if (t0 < t1) {
+        fetch_bc(t0);
+        for (int g = 0; g < SCAN_RING - 1; ++g) request(g);
+        int buf = 0, g = 0;
+        for (int tc = t0; tc < t1; tc += SCAN_TC, buf ^= 1) {
+            place_bc(buf);
+            __syncthreads();                       // the other buffer's readers passed the one before
+            fetch_bc(tc + SCAN_TC);
+#pragma unroll 1
+            for (int row = 0; row < SCAN_TC; row += 8, ++g) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(SCAN_RING - 2) : "memory");
+                __syncwarp();
+                steps(g, row, buf);                // a group past the end changes nothing
+                __syncwarp();
+                request(g + SCAN_RING - 1);        // into the slot of group g - 1
+            }
+        }
     }
-    if (a.state_out && on) store_vec<float, NPL>(a.state_out + so, s);
+    if (on && (FIRST || (last && a.state_out))) {
+        float v[NPL];
+#pragma unroll
+        for (int k = 0; k < NPL; k += 2) {
+            const float2 p = unpair(s[k / 2]);
+            v[k] = p.x;
+            v[k + 1] = p.y;
+        }
+        if (FIRST) {
+            float* w = sg.ws + ((size_t)b * sg.segs + j) * (N + 1) * a.D + ch;
+#pragma unroll
+            for (int k = 0; k < NPL; ++k) w[(int64_t)(k0 + k) * a.D] = v[k];
+            if (k0 == 0) w[(int64_t)N * a.D] = sum;
+        } else {
+            store_vec<float, NPL>(a.state_out + ((size_t)b * a.D + ch) * N + k0, v);
+        }
+    }
     // not before: CTAs of a successor placed early would share SMs that this grid keeps busy
     pdl_trigger();
 }
 
 constexpr int SCAN_STEP_MAX = 16;   // up to this many tokens the staging is not worth its barriers
 
-// Pairs of channels load and store as one where every row starts on a pair.
+// Segments of a prompt: enough that about SCAN_FILL warps run, of at least 128 positions (a multiple
+// of the staged 32), and none where the channels alone give a third of them.
+constexpr int SCAN_FILL = 152 * 12, SCAN_MAX_SEGS = 64;
+ScanSeg scan_segments(int B, int T, int D, int N) {
+    const long long warps = (long long)B * ((D * (N == 32 ? 2 : 1) + 31) / 32);
+    long long segs = 1;
+    if (T > SCAN_STEP_MAX && warps * 3 < SCAN_FILL) {
+        segs = (SCAN_FILL + warps - 1) / warps;
+        if (segs > T / 128) segs = T / 128;
+        if (segs > SCAN_MAX_SEGS) segs = SCAN_MAX_SEGS;
+        if (segs < 3) segs = 1;                    // two segments pay twice and gain at most that
+    }
+    ScanSeg sg{nullptr, 1, T};
+    if (segs > 1) {
+        sg.len = (int)(((T + segs - 1) / segs + SCAN_TC - 1) / SCAN_TC * SCAN_TC);
+        sg.segs = (T + sg.len - 1) / sg.len;
+    }
+    return sg;
+}
+size_t scan_ws_bytes(const ScanSeg& sg, int B, int D, int N) {
+    return sg.segs > 1 ? ((size_t)B * sg.segs * (N + 1) + (size_t)B * N) * D * 4 : 0;
+}
+
+template <typename T, int N, int LPC, bool V2>
+cudaError_t scan_prompt(const ScanArgs& a, const ScanSeg& sg, int B, cudaStream_t s) {
+    const int cols = (a.D * LPC + 32 * SCAN_WARPS - 1) / (32 * SCAN_WARPS);
+    constexpr size_t smem = SCAN_WARPS * SCAN_RING * 3 * 8 * (32 / LPC) * sizeof(T);
+    const dim3 block(32 * SCAN_WARPS);
+    cudaError_t e = cudaSuccess;
+    if (sg.segs > 1) {
+        if (smem > 24 * 1024)   // with the static part above 48 KB
+            e = cudaFuncSetAttribute(scan_kernel<T, N, LPC, true, V2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = launch_s(s, scan_kernel<T, N, LPC, true, V2>, dim3(cols, B, sg.segs - 1), block, smem, a, sg);
+    }
+    if (smem > 24 * 1024 && e == cudaSuccess)
+        e = cudaFuncSetAttribute(scan_kernel<T, N, LPC, false, V2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch_s(s, scan_kernel<T, N, LPC, false, V2>, dim3(cols, B, sg.segs), block, smem, a, sg);
+}
+
+// Channel pairs are copied as they lie where every row starts on one.
 bool pairs_ok(const ScanArgs& a, size_t es) {
     auto ok = [&](const void* p, int64_t ld, int64_t seq) {
         return !p || ((uintptr_t)p % (2 * es) == 0 && ld % 2 == 0 && seq % 2 == 0);
     };
-    return a.D % 2 == 0 && ok(a.x, a.x_ld, a.x_seq) && ok(a.dt, a.dt_ld, a.dt_seq) && ok(a.z, a.z_ld, a.z_seq) &&
-           ok(a.Bm, a.b_ld, a.b_seq) && ok(a.Cm, a.c_ld, a.c_seq) && ok(a.y, a.y_ld, a.y_seq);
+    return a.D % 2 == 0 && ok(a.x, a.x_ld, a.x_seq) && ok(a.dt, a.dt_ld, a.dt_seq) && ok(a.z, a.z_ld, a.z_seq);
 }
 
-template <typename T, int N, int LPC>
-void scan_launch(const ScanArgs& a, int B, cudaStream_t s) {
-    const dim3 grid((a.D * LPC + 255) / 256, B);
+template <typename T, int N, int SLPC, int LPC>
+cudaError_t scan_launch(const ScanArgs& a, const ScanSeg& sg, int B, cudaStream_t s) {
     if (a.T <= SCAN_STEP_MAX)
-        launch_s(s, scan_step_kernel<T, N, LPC>, grid, dim3(256), 0, a);
-    else if (pairs_ok(a, sizeof(T)))
-        launch_s(s, scan_kernel<T, N, LPC, true>, grid, dim3(256), 0, a);
-    else
-        launch_s(s, scan_kernel<T, N, LPC, false>, grid, dim3(256), 0, a);
+        return launch_s(s, scan_step_kernel<T, N, SLPC>, dim3((a.D * SLPC + 255) / 256, B), dim3(256), 0, a);
+    return pairs_ok(a, sizeof(T)) ? scan_prompt<T, N, LPC, true>(a, sg, B, s) : scan_prompt<T, N, LPC, false>(a, sg, B, s);
 }
 
 template <typename T>
-bool scan_dispatch(const ScanArgs& a, int B, int N, cudaStream_t s) {
+cudaError_t scan_dispatch(const ScanArgs& a, const ScanSeg& sg, int B, int N, cudaStream_t s) {
     switch (N) {
-        case 4: scan_launch<T, 4, 4>(a, B, s); return true;
-        case 8: scan_launch<T, 8, 4>(a, B, s); return true;
-        case 16: scan_launch<T, 16, 4>(a, B, s); return true;
-        case 32: scan_launch<T, 32, 8>(a, B, s); return true;
-        default: return false;
+        case 4: return scan_launch<T, 4, 4, 1>(a, sg, B, s);
+        case 8: return scan_launch<T, 8, 4, 1>(a, sg, B, s);
+        case 16: return scan_launch<T, 16, 4, 1>(a, sg, B, s);
+        default: return scan_launch<T, 32, 8, 2>(a, sg, B, s);
     }
 }
 
@@ -592,8 +704,20 @@ extern "C" evs_status evs_selective_scan(const evs_scan_args* c, void* stream) {
     ScanArgs a{c->x, c->dt, c->z, c->B, c->C, c->y, c->A, c->D, c->dt_bias, c->state_in, c->state_out, c->lens,
                c->flags, c->x_ld, c->x_seq, c->dt_ld, c->dt_seq, c->z_ld, c->z_seq, c->b_ld, c->b_seq, c->c_ld,
                c->c_seq, c->y_ld, c->y_seq, c->tokens, c->width, c->softplus ? 1 : 0};
-    const bool ok = c->dtype == EVS_DTYPE_BF16 ? scan_dispatch<bf16>(a, c->batch, c->states, (cudaStream_t)stream)
-                                               : scan_dispatch<float>(a, c->batch, c->states, (cudaStream_t)stream);
-    if (!ok) return EVS_ERR_INVALID_ARG;
-    return cudaGetLastError() == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    ScanSeg sg = scan_segments(c->batch, c->tokens, c->width, c->states);
+    if (sg.segs > 1) {
+        if (!c->workspace || !aligned(c->workspace, 16)) return EVS_ERR_INVALID_ARG;
+        if (c->ws_bytes < scan_ws_bytes(sg, c->batch, c->width, c->states)) return EVS_ERR_CAPACITY;
+        sg.ws = (float*)c->workspace;
+    }
+    const cudaError_t e = c->dtype == EVS_DTYPE_BF16 ? scan_dispatch<bf16>(a, sg, c->batch, c->states, (cudaStream_t)stream)
+                                                     : scan_dispatch<float>(a, sg, c->batch, c->states, (cudaStream_t)stream);
+    return e == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+}
+
+extern "C" size_t evs_selective_scan_workspace(int32_t batch, int32_t tokens, int32_t width, int32_t states) {
+    using namespace evs;
+    if (batch < 1 || tokens < 1 || width < 1 || batch > 65535 || width > (1 << 24) || tokens > (1 << 30)) return 0;
+    if (states != 4 && states != 8 && states != 16 && states != 32) return 0;
+    return scan_ws_bytes(scan_segments(batch, tokens, width, states), batch, width, states);
 }

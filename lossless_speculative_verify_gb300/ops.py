@@ -171,7 +171,12 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
                    _vec("lens", lens, torch.int32, (Bn,), dev), _vec("flags", flags, torch.int32, (1,), dev))
     if (T == 0 or Bn == 0) and state_out is None:
         return y
-    _enqueue(L.load().evs_selective_scan, "evs_selective_scan", a, dev)
+    lib = L.load()
+    n = int(lib.evs_selective_scan_workspace(Bn, T, W, N))
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        a.workspace, a.ws_bytes = ws.data_ptr(), n
+    _enqueue(lib.evs_selective_scan, "evs_selective_scan", a, dev)
     return y
 
 
