@@ -596,12 +596,13 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
 constexpr int SCAN_STEP_MAX = 16;   // up to this many tokens the staging is not worth its barriers
 
 // Segments of a prompt: enough that about SCAN_FILL warps run, of at least 128 positions (a multiple
-// of the staged 32), and none where the channels alone give a third of them.
-constexpr int SCAN_FILL = 152 * 12, SCAN_MAX_SEGS = 64;
+// of the staged 32). 2 x 4096 x 4096 tokens x channels: 274 us with 30 warps an SM asked for, 322
+// with 12; 8 x 1024 x 4096: 244 us, 265 in one piece.
+constexpr int SCAN_FILL = 152 * 30, SCAN_MAX_SEGS = 64;
 ScanSeg scan_segments(int B, int T, int D, int N) {
     const long long warps = (long long)B * ((D * (N == 32 ? 2 : 1) + 31) / 32);
     long long segs = 1;
-    if (T > SCAN_STEP_MAX && warps * 3 < SCAN_FILL) {
+    if (T > SCAN_STEP_MAX && warps < SCAN_FILL) {
         segs = (SCAN_FILL + warps - 1) / warps;
         if (segs > T / 128) segs = T / 128;
         if (segs > SCAN_MAX_SEGS) segs = SCAN_MAX_SEGS;

@@ -36,17 +36,19 @@ constexpr int SMP_CAP = 1024;           // tokens sorted
 constexpr int SMP_FRAC = 44;            // fixed point of weights; 2^18 of them stay below 2^63
 constexpr int SMP_MAX_CS = 8;           // portable cluster size
 
-// 2^(j/32) for j = -16..16, in units of 2^-62
-__constant__ u64 kPow2[33] = {
-    0x2d413cccfe779921ull, 0x2e3eebd1d8bee7baull, 0x2f4228e7d6030db0ull, 0x304b1332999c2516ull,
-    0x3159ca845541b6b7ull, 0x326e6f619b8bc9e9ull, 0x3389230547e12039ull, 0x34aa07647c4ab917ull,
-    0x35d13f32b5a75abdull, 0x36feede5f6bc8dd5ull, 0x383337bb0aa53844ull, 0x396e41b9df20d22aull,
-    0x3ab031b9f7490e4cull, 0x3bf92e66f736bd73ull, 0x3d495f454921b30bull, 0x3ea0ecb6dc8a80cfull,
-    0x4000000000000000ull, 0x4166c34c5615d0ecull, 0x42d561b3e6243d8aull, 0x444c0740496d4294ull,
-    0x45cae0f1f545eb73ull, 0x47521cc5a2e6a9e0ull, 0x48e1e9b9d588e19bull, 0x4a7a77d47f7b84b1ull,
-    0x4c1bf828c6dc54b8ull, 0x4dc69cdceaa72a9cull, 0x4f7a993048d088d7ull, 0x513821818624b40cull,
-    0x52ff6b54d8a89c75ull, 0x54d0ad5a753e077cull, 0x56ac1f752150a563ull, 0x5891fac0e95612c8ull,
-    0x5a827999fcef3242ull
+// 2^(j/32) for j = -16..16, each the sum of two floats
+__constant__ float2 kPow2[33] = {
+    {0.7071067690849304f, 1.2101617485882343e-08f}, {0.7225903868675232f, 1.662099968768871e-08f}, {0.7384130954742432f, -2.250449426810519e-08f},
+    {0.7545822262763977f, -1.2479686617439256e-08f}, {0.7711054086685181f, 4.035452416673024e-09f}, {0.7879904508590698f, -2.830512713103417e-08f},
+    {0.8052451610565186f, 4.918108587048664e-09f}, {0.8228777647018433f, -2.5624860455764065e-08f}, {0.8408964276313782f, -1.2377663338725142e-08f},
+    {0.8593096733093262f, -2.4248087981959543e-08f}, {0.8781260848045349f, -4.617885185353998e-09f}, {0.8973545432090759f, -5.707522454656555e-09f},
+    {0.9170040488243103f, -5.619638976384067e-09f}, {0.9370838403701782f, -2.331502813035513e-08f}, {0.9576032757759094f, 4.922664054163306e-09f},
+    {0.9785720705986023f, -8.510902205216553e-09f}, {1.0f, 0.0f}, {1.0218971967697144f, -4.811559861650494e-08f},
+    {1.0442737340927124f, 4.8334701574503924e-08f}, {1.0671404600143433f, -5.9337519786595294e-08f}, {1.0905077457427979f, -1.3077539939843064e-08f},
+    {1.114386796951294f, -5.435540018083884e-08f}, {1.1387885808944702f, 5.386222312608879e-08f}, {1.1637248992919922f, -4.051441493402308e-08f},
+    {1.1892070770263672f, 3.797635272917432e-08f}, {1.215247392654419f, -3.267394887984665e-08f}, {1.2418577671051025f, 4.496838101886169e-08f},
+    {1.2690509557724f, 1.419333317542737e-09f}, {1.2968395948410034f, -4.018999533172973e-08f}, {1.3252366781234741f, -3.496373324196611e-08f},
+    {1.3542555570602417f, -1.0123349269974824e-08f}, {1.3839099407196045f, -5.875577357983275e-08f}, {1.4142135381698608f, 2.4203234971764687e-08f}
 };
 
 struct SampleArgs {
@@ -132,63 +134,75 @@ __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* red, u64& total) {
     return before + x - v;
 }
 
-// p in [0, 1) as 2^-64 fixed point (p >= 1: all ones; p <= 0 or NaN: 0)
-__device__ __forceinline__ u64 unit_fixed(float p) {
+// p in [0, 1) as 2^-bits fixed point, rounded down or up (p >= 1: `one`; p <= 0 or NaN: 0). By its
+// bits: fp64 runs at 1/64 of fp32's rate.
+__device__ __forceinline__ u64 unit_fixed(float p, int bits, bool up, u64 one) {
     if (!(p > 0.f)) return 0;
-    if (p >= 1.f) return ~0ull;
-    return (u64)((double)p * 18446744073709551616.0);
+    if (p >= 1.f) return one;
+    const uint32_t u = __float_as_uint(p), e = u >> 23;
+    const u64 m = e ? (u & 0x7fffffu) | 0x800000u : u & 0x7fffffu;
+    const int sh = (int)(e ? e : 1) - 150 + bits;          // p = m 2^(sh - bits)
+    if (sh >= 0) return m << sh;
+    if (sh <= -24) return up ? 1 : 0;
+    return (m >> -sh) + (up && (m & ((1ull << -sh) - 1)) ? 1 : 0);
 }
 
 // ---- weights ------------------------------------------------------------------------------------
 // exp((l - M) / T) = 2^y, y = (l - M) * c with c = log2(e) / T held as the sum of two floats. The
 // difference and the product are formed exactly (two-sum, fused multiply-add remainders);
 // y = n + j/32 + g, |g| <= 1/64, and 2^g - 1 by its Taylor series, whose first term is kept as a
-// sum of two floats too. Relative error about 2^-37; weights below 2^-45 are 0.
+// sum of two floats too. Relative error about 2^-37; weights below 2^-45 are 0. Integers are taken
+// from the low bits of sums with 1.5 * 2^23: conversions run at an eighth of the rate.
+constexpr float kRound = 12582912.f;      // 1.5 * 2^23
 struct WeightFn {
     float M, c_hi, c_lo;
-    const u64* tab;       // shared copy of kPow2
+    const float2* tab;    // shared copy of kPow2
 
-    __device__ __forceinline__ bool split(float l, int& n, int& j, float& q, float& lo) const {
+    // the weight times 2^22, as the sum of two floats; false: 0 (or l is not below M)
+    __device__ __forceinline__ bool scaled(float l, float& hi, float& lo) const {
         const float dh = l - M;
         const float bb = dh - l;
         const float dl = (l - (dh - bb)) + (-M - bb);
         const float p = dh * c_hi;
         if (!(p > -64.f)) return false;
         const float e = fmaf(dh, c_hi, -p) + fmaf(dh, c_lo, dl * c_hi);
-        const float nf = rintf(p);
-        const float r = (p - nf) + e;
-        const float e1 = ((p - nf) - r) + e;              // what the sum dropped, below 2^-25
-        const float jf = rintf(r * 32.f);
-        const float g = fmaf(jf, -0.03125f, r);
+        const float tn = p + kRound;
+        const float r0 = p - (tn - kRound);
+        const float r = r0 + e;
+        const float e1 = (r0 - r) + e;                    // what the sum dropped, below 2^-25
+        const float tj = fmaf(r, 32.f, kRound);
+        const float g = fmaf(tj - kRound, -0.03125f, r);
         const float L_hi = 0.693147182464599609375f, L_lo = -1.904654299957768e-09f;   // ln 2
-        q = g * L_hi;
-        const float q_lo = fmaf(g, L_hi, -q) + g * L_lo;
+        const float q = g * L_hi;
+        const float q_lo = fmaf(g, L_lo, fmaf(g, L_hi, -q));
         float h = fmaf(q, 1.f / 120.f, 1.f / 24.f);
         h = fmaf(h, q, 1.f / 6.f);
         h = fmaf(h, q, 0.5f);
-        lo = fmaf(h * q, q, fmaf(e1 * L_hi, 1.f + q, q_lo));
-        n = (int)nf;
-        j = (int)jf;
+        const float rest = fmaf(h * q, q, fmaf(e1 * L_hi, 1.f + q, q_lo));
+        const float2 t = tab[16 + (__float_as_int(tj) - __float_as_int(kRound))];
+        const float m = t.x * q;
+        const float s = t.x + m;
+        const float s_lo = ((t.x - s) + m) + (fmaf(t.x, q, -m) + fmaf(t.x, rest, t.y));
+        const float w = s + s_lo, w_lo = (s - w) + s_lo;  // w_lo within half a step of w
+        const float two_n = __int_as_float((__float_as_int(tn) - __float_as_int(kRound) + 127 + 22) << 23);
+        hi = w * two_n;
+        lo = w_lo * two_n;
         return true;
     }
     __device__ __forceinline__ u64 fixed(float l) const {
-        int n, j;
-        float q, lo;
+        float hi, lo;
         if (l == M) return 1ull << SMP_FRAC;
-        if (!split(l, n, j, q, lo)) return 0;
-        const int E = __float2int_rn(q * 137438953472.f) + __float2int_rn(lo * 137438953472.f);   // 2^37
-        const u64 t = tab[16 + j];
-        const long long v = (long long)t + (((long long)(uint32_t)(t >> 31) * (long long)E) >> 6);
-        const int sh = 62 - SMP_FRAC - n;                 // >= 18
-        return sh > 62 ? 0 : ((u64)v + (1ull << (sh - 1))) >> sh;
+        if (!scaled(l, hi, lo)) return 0;
+        const float t = hi + kRound;
+        const float rest = (hi - (t - kRound)) + lo;      // exact, then rounded once
+        const float t2 = fmaf(rest, 4194304.f, kRound);
+        const int a = __float_as_int(t) - __float_as_int(kRound), b = __float_as_int(t2) - __float_as_int(kRound);
+        return (u64)((long long)a * (1ll << (SMP_FRAC - 22)) + b);
     }
     __device__ __forceinline__ float real(float l) const {   // fp32, for probabilities
-        int n, j;
-        float q, lo;
+        float hi, lo;
         if (l == M) return 1.f;
-        if (!split(l, n, j, q, lo)) return 0.f;
-        const float t = (float)tab[16 + j] * 2.168404344971009e-19f;   // 2^-62
-        return fmaf(t, q + lo, t) * __int_as_float((n + 127) << 23);   // n >= -64
+        return scaled(l, hi, lo) ? (hi + lo) * 2.384185791015625e-7f : 0.f;   // 2^-22
     }
 };
 
@@ -217,13 +231,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);   // [4][BINS]: count, mass planes
     u64* list_o = reinterpret_cast<u64*>(hist);                                 // [CAP], after a search
     u64* list_w = list_o + SMP_CAP;                                             // [CAP]
-    __shared__ u64 tab[33];
+    __shared__ float2 tab[33];
     __shared__ u64 red[THREADS / 32];
     __shared__ u64 warp_mass[THREADS / 32];
     __shared__ float x_max[SMP_MAX_CS];
     __shared__ u64 x_cnt[SMP_MAX_CS], x_mass[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
     __shared__ u64 f_above_mass, f_cut, pick_before;
-    __shared__ uint32_t f_bin, f_count, f_above_count, list_n;
+    __shared__ uint32_t f_bin, f_count, f_above_count, list_n[2];
     __shared__ int pick_warp, last_kept;
     __shared__ float inv_total;
     __shared__ struct {
@@ -237,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     const uint32_t cs = CLUSTER ? cluster_size() : 1u, rank = CLUSTER ? cluster_rank() : 0u;
     const int row = blockIdx.x / cs;
     if (tid < 33) tab[tid] = kPow2[tid];
-    if (tid == 0) list_n = 0;
+    if (tid < 2) list_n[tid] = 0;
     // peers may write here once every CTA of the cluster runs: arrive now, wait before the first
     if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
@@ -248,17 +262,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         const int k = a.top_k ? a.top_k[row] : 0;
         const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
         const bool greedy = !(temp > 0.f);
-        const double c = 1.4426950408889634074 / (greedy ? 1.0 : (double)temp);
-        par.c_hi = (float)c;
-        par.c_lo = isfinite(par.c_hi) ? (float)(c - (double)par.c_hi) : 0.f;
+        // log2(e) / T, the quotient's remainder by a fused multiply-add
+        const float L2E = 1.44269502162933349609375f, L2E_lo = 1.9259629911266175e-8f, t = greedy ? 1.f : temp;
+        par.c_hi = L2E / t;
+        const float rest = fmaf(-par.c_hi, t, L2E) + L2E_lo;
+        par.c_lo = isfinite(par.c_hi) && isfinite(rest) ? rest / t : 0.f;
         par.bin_scale = 64.f / (greedy ? 1.f : temp);
         par.temp = greedy ? 1.f : temp;
         par.greedy = greedy;
         par.k = !greedy && k > 0 && k < a.V ? k : 0;
         par.need_p = !greedy && p < 1.f;
-        par.p64 = unit_fixed(p);
-        par.u64_ = unit_fixed(a.uniforms[row]);
-        par.mp = mp > 0.f && !greedy ? (u64)ceil((double)fminf(mp, 1.f) * (double)(1ull << SMP_FRAC)) : 0;
+        par.p64 = unit_fixed(p, 64, false, ~0ull);
+        par.u64_ = unit_fixed(a.uniforms[row], 64, false, ~0ull);
+        par.mp = greedy ? 0 : unit_fixed(mp, SMP_FRAC, true, 1ull << SMP_FRAC);
     }
 
     // ---- the slice: granules of 16 bytes of the row, the first and last ones partly filled
@@ -327,7 +343,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         return;
     }
 
-    u64 cut = 0;           // tokens with order >= cut are kept (before min-p)
+    u64 cut = 0;           // tokens with order >= cut are kept (before min-p): logits above cut_l,
+    float cut_l = -INFINITY;   // and of that value ids up to cut_id
+    int cut_id = 0;
+    auto set_cut = [&](u64 c) {
+        cut = c;
+        const uint32_t k = (uint32_t)(c >> SMP_IDBITS);
+        cut_l = __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+        cut_id = (1 << SMP_IDBITS) - 1 - (int)(c & ((1ull << SMP_IDBITS) - 1));
+    };
+    auto above_cut = [&](float l, int id) -> bool { return l > cut_l || (l == cut_l && id <= cut_id && cut != 0); };
     auto bin0_of = [&](float l) -> int {
         const float d = (mx - l) * bin_scale;
         return l == mx ? 0 : (d < (float)(SMP_BINS - 1) ? (int)d : SMP_BINS - 1);
@@ -336,10 +361,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         return bin0_of(l) == f.bin0 && (f.shift == SMP_ORDER_BITS || (o >> f.shift) == f.prefix);
     };
     // The set of at most CAP tokens (or the single one) where the cumulative count reaches k
-    // (k > 0), or the cumulative mass over the tokens with order >= floor_order reaches
+    // (k > 0), or the cumulative mass of the tokens above the cut so far reaches
     // x = ceil(p64 * their mass). Level 0 bins by (max - l) / T, later levels by a digit of the
     // order. bin0 is BINS where fewer than k tokens are left. Uniform over the cluster.
-    auto search = [&](uint32_t k, u64 floor_order, u64 p64, u64& x) -> Found {
+    auto search = [&](uint32_t k, u64 p64, u64& x) -> Found {
         Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0, 0};
         for (int level = 0;; ++level) {
             const int to = max(0, f.shift - SMP_DIGIT), width = f.shift - to;   // this level's digit
@@ -348,20 +373,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             if (tid == 0) f_bin = SMP_BINS;      // read by all before that barrier, written next after another
             for (int s = tid; s < n; s += THREADS) {
                 const float l = l_s[s];
-                if (l == -INFINITY) continue;
+                if (!above_cut(l, base + s)) continue;
                 int bin;
-                if (level == 0 && floor_order == 0) {
+                if (level == 0) {
                     bin = bin0_of(l);
                 } else {
                     const u64 o = order_of(l, base + s);
-                    if (o < floor_order) continue;
-                    if (level == 0) {
-                        bin = bin0_of(l);
-                    } else {
-                        if (!in_found(f, l, o)) continue;
-                        // digits descend, so that a lower bin is earlier in the order
-                        bin = (1 << width) - 1 - (int)((o >> to) & ((1ull << width) - 1));
-                    }
+                    if (!in_found(f, l, o)) continue;
+                    // digits descend, so that a lower bin is earlier in the order
+                    bin = (1 << width) - 1 - (int)((o >> to) & ((1ull << width) - 1));
                 }
                 atomicAdd(&hist[bin], 1u);
                 if (k == 0) {
@@ -457,13 +477,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             if (f.count <= SMP_CAP || f.shift == 0) return f;
         }
     };
+    int list_at = 0;
     // Sorts the gathered tokens (first CTA) and returns the order of the last one kept: the first
     // k overall (k > 0), and with do_p of these the nucleus of mass x, or where x is 0 of
     // ceil(p64 * mass of the k). above_*: what precedes all of them.
     auto finish = [&](uint32_t above_count, u64 above_mass, uint32_t k, bool do_p, u64 p64, u64 x) -> u64 {
         sync_all<CLUSTER>();                      // every CTA's entries have arrived
         if (rank == 0) {
-            const int m = min((int)list_n, SMP_CAP);
+            const int m = min((int)list_n[list_at], SMP_CAP);
             int n2 = 2;
             while (n2 < m) n2 *= 2;
             for (int e = m + tid; e < n2; e += THREADS) list_o[e] = list_w[e] = 0;
@@ -520,21 +541,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             }
         }
         sync_all<CLUSTER>();
-        const u64 c = f_cut;
-        if (tid == 0) list_n = 0;
-        sync_all<CLUSTER>();
-        return c;
+        ++list_at;                                // a second list counts anew
+        return f_cut;
     };
     auto push = [&](float l, u64 o) {
         const u64 w = wf.fixed(l);
         if constexpr (CLUSTER) {
-            const uint32_t at = atom_peer_add(map_peer(smem_u32(&list_n), 0), 1u);
+            const uint32_t at = atom_peer_add(map_peer(smem_u32(&list_n[list_at]), 0), 1u);
             if (at < SMP_CAP) {
                 st_peer_u64(map_peer(smem_u32(&list_o[at]), 0), o);
                 st_peer_u64(map_peer(smem_u32(&list_w[at]), 0), w);
             }
         } else {
-            const uint32_t at = atomicAdd(&list_n, 1u);
+            const uint32_t at = atomicAdd(&list_n[list_at], 1u);
             if (at < SMP_CAP) {
                 list_o[at] = o;
                 list_w[at] = w;
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             for (uint32_t i = 0; i < cs; ++i)
                 if (x_arg[i] > best) best = x_arg[i];
         }
-        cut = best;
+        set_cut(best);
     } else if (need_k || need_p) {
         const u64 p64 = par.p64;
         u64 x = 0;
@@ -573,11 +592,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         if (a.V <= SMP_CAP) {                     // all of them sorted, no search
             for (int s = tid; s < n; s += THREADS)
                 if (l_s[s] != -INFINITY) push(l_s[s], order_of(l_s[s], base + s));
-            cut = finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0);
+            set_cut(finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0));
             p_left = false;
         } else if (need_k) {
             // the whole top-k as one list where it fits, else only the set that holds its end
-            const Found f = search((uint32_t)k_in, 0, 0, x);
+            const Found f = search((uint32_t)k_in, 0, x);
             if (f.bin0 < SMP_BINS) {
                 const bool all = f.shift == SMP_ORDER_BITS && f.above_count + f.count <= SMP_CAP;
                 for (int s = tid; s < n; s += THREADS) {
@@ -586,19 +605,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                     const u64 o = order_of(l, base + s);
                     if (all ? bin0_of(l) <= f.bin0 : in_found(f, l, o)) push(l, o);
                 }
-                cut = finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0);
+                set_cut(finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0));
                 if (all) p_left = false;
             }
         }
         if (p_left) {
-            const Found f = search(0, cut, p64, x);
+            const Found f = search(0, p64, x);
             for (int s = tid; s < n; s += THREADS) {
                 const float l = l_s[s];
-                if (l == -INFINITY) continue;
+                if (!above_cut(l, base + s)) continue;
                 const u64 o = order_of(l, base + s);
-                if (o >= cut && in_found(f, l, o)) push(l, o);
+                if (in_found(f, l, o)) push(l, o);
             }
-            cut = finish(f.above_count, f.above_mass, 0, true, p64, x);
+            set_cut(finish(f.above_count, f.above_mass, 0, true, p64, x));
         }
     }
 
@@ -606,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     const u64 mp = par.mp;
     auto kept = [&](int s) -> u64 {
         const float l = l_s[s];
-        if (l == -INFINITY || order_of(l, base + s) < cut) return 0;
+        if (!above_cut(l, base + s)) return 0;
         const u64 w = wf.fixed(l);
         return w >= mp ? w : 0;
     };
