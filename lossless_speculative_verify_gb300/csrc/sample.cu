@@ -113,8 +113,9 @@ __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 }
 
 // Exclusive scan over the block, and the total; red holds one word per warp.
+template <int THREADS>
 __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* red, u64& total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     u64 x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -125,9 +126,10 @@ __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* red, u64& total) {
     if (lane == 31) red[w] = x;
     __syncthreads();
     u64 before = 0, all = 0;
-    for (int i = 0; i < nw; ++i) {
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
         const u64 r = red[i];
-        if (i < w) before += r;
+        before += i < w ? r : 0;
         all += r;
     }
     total = all;
@@ -417,8 +419,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                 tm += mass[i];
             }
             u64 all_c, all_m;
-            u64 ec = block_scan_u64(tc, red, all_c);
-            u64 em = block_scan_u64(tm, red, all_m);
+            u64 ec = block_scan_u64<THREADS>(tc, red, all_c);
+            u64 em = 0;
+            all_m = 0;
+            if (k == 0) em = block_scan_u64<THREADS>(tm, red, all_m);
             if constexpr (CLUSTER) {
                 if (tid < (int)cs) {
                     st_peer_u64(map_peer(smem_u32(&x_cnt[rank]), tid), all_c);
@@ -485,40 +489,61 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         sync_all<CLUSTER>();                      // every CTA's entries have arrived
         if (rank == 0) {
             const int m = min((int)list_n[list_at], SMP_CAP);
+            // Bitonic, descending, an element a thread (and every THREADS further): neighbours closer
+            // than a warp through shuffles, others through shared memory. The place in the list
+            // rides in the low bits.
+            constexpr int PER = SMP_CAP / THREADS, PLACE = 10;
+            u64 v[PER];
             int n2 = 2;
             while (n2 < m) n2 *= 2;
-            for (int e = m + tid; e < n2; e += THREADS) list_o[e] = list_w[e] = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = tid + i * THREADS;
+                v[i] = e < m ? (list_o[e] << PLACE) | (u64)e : 0;
+            }
+            for (int k2 = 2; k2 <= n2; k2 *= 2)
+                for (int j = k2 / 2; j > 0; j /= 2) {
+                    u64 o[PER];
+                    if (j < 32) {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) o[i] = __shfl_xor_sync(0xffffffffu, v[i], j);
+                    } else if (j < THREADS) {
+                        __syncthreads();
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
+                        __syncthreads();
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) o[i] = list_o[(tid ^ j) + i * THREADS];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            o[i] = v[i];
+#pragma unroll
+                            for (int x = 0; x < PER; ++x)
+                                if (x == (i ^ (j / THREADS))) o[i] = v[x];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int e = tid + i * THREADS;
+                        const bool larger = ((e & k2) == 0) == ((e & j) == 0);
+                        if ((o[i] > v[i]) == larger) v[i] = o[i];
+                    }
+                }
+            // consecutive entries to a thread again
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
             if (tid == 0) last_kept = 0;
             __syncthreads();
-            // bitonic, descending; up to 64 entries by one warp
-            if (n2 > 64 || warp == 0) {
-                const int workers = n2 > 64 ? THREADS : 32;
-                for (int k2 = 2; k2 <= n2; k2 *= 2)
-                    for (int j = k2 / 2; j > 0; j /= 2) {
-                        for (int t = tid; t < n2 / 2; t += workers) {
-                            const int i = 2 * t - (t & (j - 1)), i2 = i + j;
-                            const u64 x0 = list_o[i], x1 = list_o[i2];
-                            if ((x0 < x1) == ((i & k2) == 0)) {
-                                const u64 w0 = list_w[i], w1 = list_w[i2];
-                                list_o[i] = x1;
-                                list_o[i2] = x0;
-                                list_w[i] = w1;
-                                list_w[i2] = w0;
-                            }
-                        }
-                        if (n2 > 64) __syncthreads(); else __syncwarp();
-                    }
-            }
-            __syncthreads();
-            constexpr int PER = SMP_CAP / THREADS;
             u64 w[PER], mine = 0, total;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = tid * PER + i;
-                w[i] = e < m && (k == 0 || above_count + e < k) ? list_w[e] : 0;
+                w[i] = e < m && (k == 0 || above_count + e < k) ? list_w[list_o[e] & ((1 << PLACE) - 1)] : 0;
                 mine += w[i];
             }
-            u64 before = block_scan_u64(mine, red, total) + above_mass;
+            u64 before = block_scan_u64<THREADS>(mine, red, total) + above_mass;
             total += above_mass;
             if (do_p && x == 0) {
                 x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             if (lane == 0 && kept_to > 0) atomicMax(&last_kept, kept_to);
             __syncthreads();
             if (tid < (int)cs) {
-                const u64 lowest = list_o[last_kept];
+                const u64 lowest = list_o[last_kept] >> PLACE;
                 if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), lowest);
                 else f_cut = lowest;
             }
@@ -544,19 +569,30 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         ++list_at;                                // a second list counts anew
         return f_cut;
     };
-    auto push = [&](float l, u64 o) {
-        const u64 w = wf.fixed(l);
-        if constexpr (CLUSTER) {
-            const uint32_t at = atom_peer_add(map_peer(smem_u32(&list_n[list_at]), 0), 1u);
-            if (at < SMP_CAP) {
-                st_peer_u64(map_peer(smem_u32(&list_o[at]), 0), o);
-                st_peer_u64(map_peer(smem_u32(&list_w[at]), 0), w);
+    // Appends the tokens that `take` names to the first CTA's list; a warp's share by one counter update.
+    auto gather = [&](auto take) {
+        for (int s0 = 0; s0 < n; s0 += THREADS) {
+            const int s = s0 + tid;
+            const float l = s < n ? l_s[s] : -INFINITY;
+            u64 o = 0;
+            const bool yes = l > -INFINITY && take(l, s, o);
+            const unsigned who = __ballot_sync(0xffffffffu, yes);
+            if (who == 0) continue;
+            uint32_t at = 0;
+            if (lane == 0) {
+                if constexpr (CLUSTER) at = atom_peer_add(map_peer(smem_u32(&list_n[list_at]), 0), __popc(who));
+                else at = atomicAdd(&list_n[list_at], __popc(who));
             }
-        } else {
-            const uint32_t at = atomicAdd(&list_n[list_at], 1u);
-            if (at < SMP_CAP) {
-                list_o[at] = o;
-                list_w[at] = w;
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+            if (yes && at < SMP_CAP) {
+                const u64 w = wf.fixed(l);
+                if constexpr (CLUSTER) {
+                    st_peer_u64(map_peer(smem_u32(&list_o[at]), 0), o);
+                    st_peer_u64(map_peer(smem_u32(&list_w[at]), 0), w);
+                } else {
+                    list_o[at] = o;
+                    list_w[at] = w;
+                }
             }
         }
     };
@@ -590,8 +626,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         u64 x = 0;
         bool p_left = need_p;
         if (a.V <= SMP_CAP) {                     // all of them sorted, no search
-            for (int s = tid; s < n; s += THREADS)
-                if (l_s[s] != -INFINITY) push(l_s[s], order_of(l_s[s], base + s));
+            gather([&](float l, int s, u64& o) {
+                o = order_of(l, base + s);
+                return true;
+            });
             set_cut(finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0));
             p_left = false;
         } else if (need_k) {
@@ -599,24 +637,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             const Found f = search((uint32_t)k_in, 0, x);
             if (f.bin0 < SMP_BINS) {
                 const bool all = f.shift == SMP_ORDER_BITS && f.above_count + f.count <= SMP_CAP;
-                for (int s = tid; s < n; s += THREADS) {
-                    const float l = l_s[s];
-                    if (l == -INFINITY) continue;
-                    const u64 o = order_of(l, base + s);
-                    if (all ? bin0_of(l) <= f.bin0 : in_found(f, l, o)) push(l, o);
-                }
+                gather([&](float l, int s, u64& o) {
+                    if (all ? bin0_of(l) > f.bin0 : bin0_of(l) != f.bin0) return false;
+                    o = order_of(l, base + s);
+                    return all || in_found(f, l, o);
+                });
                 set_cut(finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0));
                 if (all) p_left = false;
             }
         }
         if (p_left) {
             const Found f = search(0, p64, x);
-            for (int s = tid; s < n; s += THREADS) {
-                const float l = l_s[s];
-                if (!above_cut(l, base + s)) continue;
-                const u64 o = order_of(l, base + s);
-                if (in_found(f, l, o)) push(l, o);
-            }
+            gather([&](float l, int s, u64& o) {
+                if (bin0_of(l) != f.bin0 || !above_cut(l, base + s)) return false;
+                o = order_of(l, base + s);
+                return in_found(f, l, o);
+            });
             set_cut(finish(f.above_count, f.above_mass, 0, true, p64, x));
         }
     }
@@ -667,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         for (int i = 0; i < per; ++i)
             if (lo + tid * per + i < hi) m += kept(lo + tid * per + i);
         u64 all;
-        u64 c = pick_before + block_scan_u64(m, red, all);
+        u64 c = pick_before + block_scan_u64<THREADS>(m, red, all);
         if (c <= thr && thr < c + m) {
             int s = lo + tid * per;
             for (;; ++s) {
@@ -677,9 +713,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             }
             a.token[row] = base + s;
             if (a.logprob) {
-                const double lw = l_s[s] == mx ? 0.0
-                                               : ((double)l_s[s] - (double)mx) / (double)par.temp;
-                a.logprob[row] = (float)(lw - log((double)total) + SMP_FRAC * 0.69314718055994530942);
+                // log(w / total): the logit's distance less the log of the total over the largest weight,
+                // which is at least 1 and relative to it where it is near
+                const float lw = l_s[s] == mx ? 0.f : (l_s[s] - mx) / par.temp;
+                const u64 one = 1ull << SMP_FRAC;
+                const float lt = total < 2 * one ? log1pf((float)(total - one) * 5.684341886080802e-14f)   // 2^-44
+                                                 : logf((float)total * 5.684341886080802e-14f);
+                a.logprob[row] = lw - lt;
             }
         }
     }
