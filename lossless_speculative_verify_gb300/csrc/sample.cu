@@ -7,19 +7,22 @@
 //   mass, over ascending ids, exceeds u times the total.
 //
 // The decisions are comparisons of sums over the whole vocabulary, so weights are computed to
-// about 2^-37 relative and summed as 64-bit fixed point (2^-44): the sums do not depend on their
+// about 2^-33 relative and summed as 64-bit fixed point (2^-45): the sums do not depend on their
 // order, every run gives the same token, and it is the one that exact arithmetic gives unless a
-// border falls within about 1e-11 of the total mass. In fp32 the error of one such sum,
+// border falls within about 1e-10 of the total mass. In fp32 the error of one such sum,
 // about 1e-6 of the mass, would move the draw in several percent of rows of 131072 flat logits.
 //
 // The row is read once: the CTAs of the cluster keep their slices in shared memory and search
 // there. The cut (top-k and top-p are both prefixes of the sorted row, so one pair (logit, id)
-// describes what is kept) is found by a histogram over (max - l) / T in steps of 1/64, narrowed
-// by digits of (ordered logit, id) while the bin that holds the cut has more than CAP tokens;
-// those few are then sorted. (Ranking them pairwise took 15 us for the 461 tokens left of a
-// 512-entry row, and one CTA's 17 us held the other seven of a large row's cluster.)
+// describes what is kept) is found by a histogram over the weight's exponent in steps of 1/32,
+// narrowed by digits of (ordered logit, id) while the bin that holds the cut has more than CAP
+// tokens; those few are then ranked. A bin's mass follows from its count and the sum of its
+// tokens' mantissas above its lower end, so three 32-bit counters a bin are exact.
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
+
+#include <cfloat>
+#include <climits>
 
 namespace evs {
 namespace {
@@ -32,23 +35,25 @@ constexpr int SMP_IDBITS = 18;
 constexpr int SMP_ORDER_BITS = 32 + SMP_IDBITS;
 constexpr int SMP_DIGIT = 11;
 constexpr int SMP_BINS = 1 << SMP_DIGIT;
-constexpr int SMP_CAP = 1024;           // tokens sorted
-constexpr int SMP_FRAC = 44;            // fixed point of weights; 2^18 of them stay below 2^63
+constexpr int SMP_CAP = 1024;           // tokens ranked at once
+constexpr int SMP_FEW = 128;            // of them by counting instead of sorting
+constexpr int SMP_FRAC = 45;            // fixed point of weights; 2^18 of them reach 2^63
+constexpr int SMP_ZERO = SMP_FRAC + 1;  // weights of 2^-46 and less are 0
 constexpr int SMP_MAX_CS = 8;           // portable cluster size
 
-// 2^(j/32) for j = -16..16, each the sum of two floats
-__constant__ float2 kPow2[33] = {
-    {0.7071067690849304f, 1.2101617485882343e-08f}, {0.7225903868675232f, 1.662099968768871e-08f}, {0.7384130954742432f, -2.250449426810519e-08f},
-    {0.7545822262763977f, -1.2479686617439256e-08f}, {0.7711054086685181f, 4.035452416673024e-09f}, {0.7879904508590698f, -2.830512713103417e-08f},
-    {0.8052451610565186f, 4.918108587048664e-09f}, {0.8228777647018433f, -2.5624860455764065e-08f}, {0.8408964276313782f, -1.2377663338725142e-08f},
-    {0.8593096733093262f, -2.4248087981959543e-08f}, {0.8781260848045349f, -4.617885185353998e-09f}, {0.8973545432090759f, -5.707522454656555e-09f},
-    {0.9170040488243103f, -5.619638976384067e-09f}, {0.9370838403701782f, -2.331502813035513e-08f}, {0.9576032757759094f, 4.922664054163306e-09f},
-    {0.9785720705986023f, -8.510902205216553e-09f}, {1.0f, 0.0f}, {1.0218971967697144f, -4.811559861650494e-08f},
-    {1.0442737340927124f, 4.8334701574503924e-08f}, {1.0671404600143433f, -5.9337519786595294e-08f}, {1.0905077457427979f, -1.3077539939843064e-08f},
-    {1.114386796951294f, -5.435540018083884e-08f}, {1.1387885808944702f, 5.386222312608879e-08f}, {1.1637248992919922f, -4.051441493402308e-08f},
-    {1.1892070770263672f, 3.797635272917432e-08f}, {1.215247392654419f, -3.267394887984665e-08f}, {1.2418577671051025f, 4.496838101886169e-08f},
-    {1.2690509557724f, 1.419333317542737e-09f}, {1.2968395948410034f, -4.018999533172973e-08f}, {1.3252366781234741f, -3.496373324196611e-08f},
-    {1.3542555570602417f, -1.0123349269974824e-08f}, {1.3839099407196045f, -5.875577357983275e-08f}, {1.4142135381698608f, 2.4203234971764687e-08f}
+// 2^(j/32) for j = 0..31, each the sum of two floats
+__constant__ float2 kPow2[32] = {
+    {1.0f, 0.0f}, {1.0218971967697144f, -4.811559861650494e-08f}, {1.0442737340927124f, 4.8334701574503924e-08f},
+    {1.0671404600143433f, -5.9337519786595294e-08f}, {1.0905077457427979f, -1.3077539939843064e-08f}, {1.1143867969512939f, -5.4355400180838842e-08f},
+    {1.1387885808944702f, 5.3862223126088793e-08f}, {1.1637248992919922f, -4.051441493402308e-08f}, {1.1892070770263672f, 3.7976352729174323e-08f},
+    {1.2152473926544189f, -3.2673948879846648e-08f}, {1.2418577671051025f, 4.4968381018861692e-08f}, {1.2690509557723999f, 1.4193333175427369e-09f},
+    {1.2968395948410034f, -4.0189995331729733e-08f}, {1.3252366781234741f, -3.4963733241966111e-08f}, {1.3542555570602417f, -1.0123349269974824e-08f},
+    {1.3839099407196045f, -5.8755773579832749e-08f}, {1.4142135381698608f, 2.4203234971764687e-08f}, {1.4451807737350464f, 3.3241999375377418e-08f},
+    {1.4768261909484863f, -4.5008988536210381e-08f}, {1.5091644525527954f, -2.4959373234878512e-08f}, {1.5422108173370361f, 8.0709048333460487e-09f},
+    {1.5759809017181396f, -5.6610254262068338e-08f}, {1.6104903221130371f, 9.8362171740973281e-09f}, {1.6457555294036865f, -5.1249720911528129e-08f},
+    {1.6817928552627563f, -2.4755326677450284e-08f}, {1.7186193466186523f, -4.8496175963919086e-08f}, {1.7562521696090698f, -9.2357703707079963e-09f},
+    {1.7947090864181519f, -1.141504490931311e-08f}, {1.8340080976486206f, -1.1239277952768134e-08f}, {1.8741676807403564f, -4.6630056260710262e-08f},
+    {1.9152065515518188f, 9.845328108326612e-09f}, {1.9571441411972046f, -1.7021804410433106e-08f},
 };
 
 struct SampleArgs {
@@ -106,6 +111,11 @@ __device__ __forceinline__ u64 order_of(float l, int id) {
     return ((u64)k << SMP_IDBITS) | (u64)((1 << SMP_IDBITS) - 1 - id);
 }
 
+__device__ __forceinline__ float logit_of(u64 order) {
+    const uint32_t k = (uint32_t)(order >> SMP_IDBITS);
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -151,62 +161,110 @@ __device__ __forceinline__ u64 unit_fixed(float p, int bits, bool up, u64 one) {
 
 // ---- weights ------------------------------------------------------------------------------------
 // exp((l - M) / T) = 2^y, y = (l - M) * c with c = log2(e) / T held as the sum of two floats. The
-// difference and the product are formed exactly (two-sum, fused multiply-add remainders);
-// y = n + j/32 + g, |g| <= 1/64, and 2^g - 1 by its Taylor series, whose first term is kept as a
-// sum of two floats too. Relative error about 2^-37; weights below 2^-45 are 0. Integers are taken
-// from the low bits of sums with 1.5 * 2^23: conversions run at an eighth of the rate.
-constexpr float kRound = 12582912.f;      // 1.5 * 2^23
+// difference and the product are formed exactly (two-sum, fused multiply-add remainders), so that
+// y = p + e; p = i/32 + r, |r| <= 1/64, i taken from the low bits of p + 1.5 * 2^18; and
+// 2^(r + e) - 1 = q + rest with q = r ln 2 rounded and rest its tail, q^2/2 + q^3/6 + q^4/24 and
+// e ln 2 * exp(q). In fixed point of 2^-34 the sum of the two is off by 2^-34 at most; times
+// 2^(i/32), a weight is within about 2^-33 of its value. Two logits at a time: 26 packed
+// instructions for both, where one by one in the same arithmetic takes 51 for each.
+constexpr float kRound = 393216.f;        // 1.5 * 2^18: its last bit is 1/32
+
+__device__ __forceinline__ u64 pk(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ u64 pk(float a) { return pk(a, a); }
+__device__ __forceinline__ float2 unpk(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b) { return fma2(b, pk(-1.f), a); }
+
+struct Parts {
+    int i0, i1;           // the weight is 2^(i/32) (1 + q + rest) where p > -SMP_ZERO; else 0
+    float2 p, q, rest;
+};
 struct WeightFn {
     float M, c_hi, c_lo;
-    const float2* tab;    // shared copy of kPow2
+    const u64* tab;       // 2^(j/32) * 2^62
 
-    // the weight times 2^22, as the sum of two floats; false: 0 (or l is not below M)
-    __device__ __forceinline__ bool scaled(float l, float& hi, float& lo) const {
-        const float dh = l - M;
-        const float bb = dh - l;
-        const float dl = (l - (dh - bb)) + (-M - bb);
-        const float p = dh * c_hi;
-        if (!(p > -64.f)) return false;
-        const float e = fmaf(dh, c_hi, -p) + fmaf(dh, c_lo, dl * c_hi);
-        const float tn = p + kRound;
-        const float r0 = p - (tn - kRound);
-        const float r = r0 + e;
-        const float e1 = (r0 - r) + e;                    // what the sum dropped, below 2^-25
-        const float tj = fmaf(r, 32.f, kRound);
-        const float g = fmaf(tj - kRound, -0.03125f, r);
+    __device__ __forceinline__ Parts parts(float l0, float l1) const {
+        const u64 l = pk(l0, l1), nM = pk(-M), ch = pk(c_hi);
+        const u64 dh = add2(l, nM);
+        const u64 bb = sub2(dh, l);
+        const u64 dl = add2(sub2(l, sub2(dh, bb)), sub2(nM, bb));
+        const u64 p = mul2(dh, ch);
+        const u64 e = fma2(dl, ch, fma2(dh, pk(c_lo), fma2(dh, ch, mul2(dh, pk(-c_hi)))));
+        const u64 tn = add2(p, pk(kRound));
+        const u64 r = sub2(p, add2(tn, pk(-kRound)));
         const float L_hi = 0.693147182464599609375f, L_lo = -1.904654299957768e-09f;   // ln 2
-        const float q = g * L_hi;
-        const float q_lo = fmaf(g, L_lo, fmaf(g, L_hi, -q));
-        float h = fmaf(q, 1.f / 120.f, 1.f / 24.f);
-        h = fmaf(h, q, 1.f / 6.f);
-        h = fmaf(h, q, 0.5f);
-        const float rest = fmaf(h * q, q, fmaf(e1 * L_hi, 1.f + q, q_lo));
-        const float2 t = tab[16 + (__float_as_int(tj) - __float_as_int(kRound))];
-        const float m = t.x * q;
-        const float s = t.x + m;
-        const float s_lo = ((t.x - s) + m) + (fmaf(t.x, q, -m) + fmaf(t.x, rest, t.y));
-        const float w = s + s_lo, w_lo = (s - w) + s_lo;  // w_lo within half a step of w
-        const float two_n = __int_as_float((__float_as_int(tn) - __float_as_int(kRound) + 127 + 22) << 23);
-        hi = w * two_n;
-        lo = w_lo * two_n;
-        return true;
+        const u64 q = mul2(r, pk(L_hi));
+        const u64 q_lo = fma2(r, pk(L_lo), fma2(r, pk(L_hi), mul2(r, pk(-L_hi))));
+        const u64 d = fma2(e, pk(L_hi), q_lo);
+        const u64 h = fma2(fma2(q, pk(1.f / 24.f), pk(1.f / 6.f)), q, pk(0.5f));
+        const u64 ex = fma2(fma2(q, pk(0.5f), pk(1.f)), q, pk(1.f));
+        const u64 rest = fma2(mul2(h, q), q, mul2(d, ex));
+        const float2 t = unpk(tn);
+        return {__float_as_int(t.x) - __float_as_int(kRound), __float_as_int(t.y) - __float_as_int(kRound), unpk(p),
+                unpk(q), unpk(rest)};
+    }
+    // q + rest in steps of 2^-34
+    static __device__ __forceinline__ int frac(float q, float rest) {
+        return __float2int_rn(q * 17179869184.f) + __float2int_rn(rest * 17179869184.f);
+    }
+    __device__ __forceinline__ u64 scaled(int i, float p, float q, float rest) const {
+        const u64 t = tab[i & 31];
+        const u64 w = t + (u64)((long long)(int)(t >> 34) * frac(q, rest));
+        return p > (float)-SMP_ZERO ? w >> ((62 - SMP_FRAC - (i >> 5)) & 63) : 0;
+    }
+    __device__ __forceinline__ void fixed2(float l0, float l1, u64& w0, u64& w1) const {
+        const Parts a = parts(l0, l1);
+        w0 = scaled(a.i0, a.p.x, a.q.x, a.rest.x);
+        w1 = scaled(a.i1, a.p.y, a.q.y, a.rest.y);
     }
     __device__ __forceinline__ u64 fixed(float l) const {
-        float hi, lo;
-        if (l == M) return 1ull << SMP_FRAC;
-        if (!scaled(l, hi, lo)) return 0;
-        const float t = hi + kRound;
-        const float rest = (hi - (t - kRound)) + lo;      // exact, then rounded once
-        const float t2 = fmaf(rest, 4194304.f, kRound);
-        const int a = __float_as_int(t) - __float_as_int(kRound), b = __float_as_int(t2) - __float_as_int(kRound);
-        return (u64)((long long)a * (1ll << (SMP_FRAC - 22)) + b);
+        u64 w0, w1;
+        fixed2(l, l, w0, w1);
+        return w0;
     }
-    __device__ __forceinline__ float real(float l) const {   // fp32, for probabilities
-        float hi, lo;
-        if (l == M) return 1.f;
-        return scaled(l, hi, lo) ? (hi + lo) * 2.384185791015625e-7f : 0.f;   // 2^-22
+    // Which step of 1/32 of the exponent: bins that ascend as the logit falls
+    __device__ __forceinline__ int bin(int i, float p) const { return p > -63.9f ? -i : SMP_BINS - 1; }
+    __device__ __forceinline__ int bin(float l) const {
+        const float p = (l - M) * c_hi;
+        return bin(__float_as_int(p + kRound) - __float_as_int(kRound), p);
+    }
+    // The mass of `count` tokens of one bin whose q + rest sum to frac_sum
+    __device__ __forceinline__ u64 mass(int b, u64 count, long long frac_sum) const {
+        if (b > 32 * SMP_ZERO) return 0;
+        const u64 t = tab[-b & 31];
+        const int n = (b + 31) >> 5;
+        const u64 m = count * (t >> (63 - SMP_FRAC)) + (u64)__mul64hi((long long)t, frac_sum << (SMP_FRAC - 33));
+        return n ? m >> (n - 1) : m << 1;
     }
 };
+// fp32 of it, for probabilities
+__device__ __forceinline__ float real_weight(int i, float p, float q, float rest, const float2* pow2) {
+    const float2 t = pow2[i & 31];
+    const float w = t.x + fmaf(t.x, q + rest, t.y);
+    return p > (float)-SMP_ZERO ? w * __int_as_float((127 + (i >> 5)) << 23) : 0.f;
+}
 
 // 16 bytes of a row
 template <typename T> union Raw16 {
@@ -230,21 +288,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     constexpr int BPT = SMP_BINS / THREADS;     // bins a thread sums when the CTA is alone
     extern __shared__ __align__(16) uint8_t smem[];
     float* l_s = reinterpret_cast<float*>(smem);
-    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);   // [4][BINS]: count, mass planes
-    u64* list_o = reinterpret_cast<u64*>(hist);                                 // [CAP], after a search
-    u64* list_w = list_o + SMP_CAP;                                             // [CAP]
-    __shared__ float2 tab[33];
+    // [3][BINS]: count, sum of q + rest (low 16 bits, the rest)
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);
+    // after a search: what the row's first CTA ranks, and what each CTA found of it
+    u64* list_o = reinterpret_cast<u64*>(hist);                                 // [CAP]
+    u64* list_w = list_o + SMP_CAP;                                             // [FEW]
+    u64* own_o = CLUSTER ? list_w + SMP_FEW : list_o;                           // [CAP]
+    // after the cut: 192 kept logits a warp
+    float* queue = reinterpret_cast<float*>(hist) + (threadIdx.x >> 5) * 192;
+    __shared__ float2 pow2[32];
+    __shared__ u64 tab[32];
     __shared__ u64 red[THREADS / 32];
     __shared__ u64 warp_mass[THREADS / 32];
     __shared__ float x_max[SMP_MAX_CS];
     __shared__ u64 x_cnt[SMP_MAX_CS], x_mass[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
     __shared__ u64 f_above_mass, f_cut, pick_before;
-    __shared__ uint32_t f_bin, f_count, f_above_count, list_n[2];
+    __shared__ uint32_t f_bin, f_count, f_above_count, list_n[2], own_n[2], own_at;
     __shared__ int pick_warp, last_kept;
-    __shared__ float inv_total;
     __shared__ struct {
         u64 p64, u64_, mp;
-        float c_hi, c_lo, bin_scale, temp;
+        float c_hi, c_lo, temp;
         int k, greedy, need_p;
     } par;
 
@@ -252,31 +315,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t cs = CLUSTER ? cluster_size() : 1u, rank = CLUSTER ? cluster_rank() : 0u;
     const int row = blockIdx.x / cs;
-    if (tid < 33) tab[tid] = kPow2[tid];
-    if (tid < 2) list_n[tid] = 0;
+    if (tid < 32) {
+        const float2 t = kPow2[tid];
+        pow2[tid] = t;
+        tab[tid] = (u64)(__float2ll_rn(t.x * 4611686018427387904.f) + __float2ll_rn(t.y * 4611686018427387904.f));
+    }
+    if (tid < 2) list_n[tid] = own_n[tid] = 0;
     // peers may write here once every CTA of the cluster runs: arrive now, wait before the first
     if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
 
-    // ---- parameters of the row: one thread's few fp64 operations (their rate is 1/64 of fp32's)
+    // ---- parameters of the row, by one thread: loaded here, worked out while the row arrives
+    float temp = 1.f, p_in = 1.f, mp_in = 0.f, u_in = 0.f;
+    int top_k = 0;
     if (tid == 0) {
-        const float temp = a.temperature ? a.temperature[row] : 1.f;
-        const int k = a.top_k ? a.top_k[row] : 0;
-        const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
-        const bool greedy = !(temp > 0.f);
-        // log2(e) / T, the quotient's remainder by a fused multiply-add
-        const float L2E = 1.44269502162933349609375f, L2E_lo = 1.9259629911266175e-8f, t = greedy ? 1.f : temp;
-        par.c_hi = L2E / t;
-        const float rest = fmaf(-par.c_hi, t, L2E) + L2E_lo;
-        par.c_lo = isfinite(par.c_hi) && isfinite(rest) ? rest / t : 0.f;
-        par.bin_scale = 64.f / (greedy ? 1.f : temp);
-        par.temp = greedy ? 1.f : temp;
-        par.greedy = greedy;
-        par.k = !greedy && k > 0 && k < a.V ? k : 0;
-        par.need_p = !greedy && p < 1.f;
-        par.p64 = unit_fixed(p, 64, false, ~0ull);
-        par.u64_ = unit_fixed(a.uniforms[row], 64, false, ~0ull);
-        par.mp = greedy ? 0 : unit_fixed(mp, SMP_FRAC, true, 1ull << SMP_FRAC);
+        if (a.temperature) temp = a.temperature[row];
+        if (a.top_k) top_k = a.top_k[row];
+        if (a.top_p) p_in = a.top_p[row];
+        if (a.min_p) mp_in = a.min_p[row];
+        u_in = a.uniforms[row];
     }
 
     // ---- the slice: granules of 16 bytes of the row, the first and last ones partly filled
@@ -317,6 +374,21 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             }
         }
     }
+    if (tid == 0) {
+        const bool greedy = !(temp > 0.f);
+        // log2(e) / T, the quotient's remainder by a fused multiply-add
+        const float L2E = 1.44269502162933349609375f, L2E_lo = 1.9259629911266175e-8f, t = greedy ? 1.f : temp;
+        const float c = L2E / t, left = fmaf(-c, t, L2E) + L2E_lo;
+        par.c_hi = fminf(c, FLT_MAX);         // where 1 / T overflows
+        par.c_lo = c <= FLT_MAX && isfinite(left) ? left / t : 0.f;
+        par.temp = t;
+        par.greedy = greedy;
+        par.k = !greedy && top_k > 0 && top_k < a.V ? top_k : 0;
+        par.need_p = !greedy && p_in < 1.f;
+        par.p64 = unit_fixed(p_in, 64, false, ~0ull);
+        par.u64_ = unit_fixed(u_in, 64, false, ~0ull);
+        par.mp = greedy ? 0 : unit_fixed(mp_in, SMP_FRAC, true, 1ull << SMP_FRAC);
+    }
     mx = block_max(mx, reinterpret_cast<float*>(red));
     if constexpr (CLUSTER) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -327,8 +399,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     } else {
         __syncthreads();
     }
-    WeightFn wf{mx, par.c_hi, par.c_lo, tab};      // written before the barriers of the maximum
-    const float bin_scale = par.bin_scale;
+    if (mx == INFINITY) {                        // the infinite ones share the mass
+        for (int s = tid; s < n; s += THREADS) l_s[s] = l_s[s] == INFINITY ? 0.f : -INFINITY;
+        mx = 0.f;
+        __syncthreads();
+    }
+    const WeightFn wf{mx, par.c_hi, par.c_lo, tab};      // written before the barriers of the maximum
     const bool greedy = par.greedy, need_p = par.need_p;
     const int k_in = par.k;
     const bool need_k = k_in > 0;
@@ -345,54 +421,61 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         return;
     }
 
-    u64 cut = 0;           // tokens with order >= cut are kept (before min-p): logits above cut_l,
-    float cut_l = -INFINITY;   // and of that value ids up to cut_id
-    int cut_id = 0;
+    // Kept (before min-p): logits above cut_l, and of that value ids up to cut_id
+    float cut_l = -INFINITY;
+    int cut_id = INT_MIN;
     auto set_cut = [&](u64 c) {
-        cut = c;
-        const uint32_t k = (uint32_t)(c >> SMP_IDBITS);
-        cut_l = __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+        cut_l = logit_of(c);
         cut_id = (1 << SMP_IDBITS) - 1 - (int)(c & ((1ull << SMP_IDBITS) - 1));
     };
-    auto above_cut = [&](float l, int id) -> bool { return l > cut_l || (l == cut_l && id <= cut_id && cut != 0); };
-    auto bin0_of = [&](float l) -> int {
-        const float d = (mx - l) * bin_scale;
-        return l == mx ? 0 : (d < (float)(SMP_BINS - 1) ? (int)d : SMP_BINS - 1);
-    };
-    auto in_found = [&](const Found& f, float l, u64 o) -> bool {
-        return bin0_of(l) == f.bin0 && (f.shift == SMP_ORDER_BITS || (o >> f.shift) == f.prefix);
+    auto above_cut = [&](float l, int id) -> bool { return l > cut_l || (l == cut_l && id <= cut_id); };
+    auto in_found = [&](const Found& f, int bin, u64 o) -> bool {
+        return bin == f.bin0 && (f.shift == SMP_ORDER_BITS || (o >> f.shift) == f.prefix);
     };
     // The set of at most CAP tokens (or the single one) where the cumulative count reaches k
     // (k > 0), or the cumulative mass of the tokens above the cut so far reaches
-    // x = ceil(p64 * their mass). Level 0 bins by (max - l) / T, later levels by a digit of the
+    // x = ceil(p64 * their mass). Level 0 bins by the weight's exponent, later levels by a digit of the
     // order. bin0 is BINS where fewer than k tokens are left. Uniform over the cluster.
     auto search = [&](uint32_t k, u64 p64, u64& x) -> Found {
         Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0, 0};
         for (int level = 0;; ++level) {
             const int to = max(0, f.shift - SMP_DIGIT), width = f.shift - to;   // this level's digit
-            for (int i = tid; i < (k ? 1 : 4) * SMP_BINS; i += THREADS) hist[i] = 0;
+            for (int i = tid; i < (k ? 1 : 3) * SMP_BINS; i += THREADS) hist[i] = 0;
             __syncthreads();
             if (tid == 0) f_bin = SMP_BINS;      // read by all before that barrier, written next after another
-            for (int s = tid; s < n; s += THREADS) {
-                const float l = l_s[s];
-                if (!above_cut(l, base + s)) continue;
-                int bin;
-                if (level == 0) {
-                    bin = bin0_of(l);
-                } else {
-                    const u64 o = order_of(l, base + s);
-                    if (!in_found(f, l, o)) continue;
-                    // digits descend, so that a lower bin is earlier in the order
-                    bin = (1 << width) - 1 - (int)((o >> to) & ((1ull << width) - 1));
-                }
-                atomicAdd(&hist[bin], 1u);
-                if (k == 0) {
-                    const u64 w = wf.fixed(l);
-                    const uint32_t w0 = (uint32_t)w & 0xffffu, w1 = (uint32_t)(w >> 16) & 0xffffu,
-                                   w2 = (uint32_t)(w >> 32);
-                    if (w0) atomicAdd(&hist[SMP_BINS + bin], w0);
-                    if (w1) atomicAdd(&hist[2 * SMP_BINS + bin], w1);
-                    if (w2) atomicAdd(&hist[3 * SMP_BINS + bin], w2);
+            for (int s = 4 * tid; s < n; s += 4 * THREADS) {
+                const float4 l4 = *reinterpret_cast<const float4*>(l_s + s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float l0 = h ? l4.z : l4.x, l1 = h ? l4.w : l4.y;
+                    const bool in0 = above_cut(l0, base + s + 2 * h), in1 = above_cut(l1, base + s + 2 * h + 1);
+                    if (!in0 && !in1) continue;
+                    auto place = [&](float l, int id, int bin) -> int {       // -1: not in the set
+                        if (level == 0) return bin;
+                        const u64 o = order_of(l, id);
+                        if (!in_found(f, bin, o)) return -1;
+                        // digits descend, so that a lower bin is earlier in the order
+                        return (1 << width) - 1 - (int)((o >> to) & ((1ull << width) - 1));
+                    };
+                    if (k) {
+                        const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(l0)) : -1;
+                        const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(l1)) : -1;
+                        if (b0 >= 0) atomicAdd(&hist[b0], 1u);
+                        if (b1 >= 0) atomicAdd(&hist[b1], 1u);
+                    } else {
+                        const Parts w = wf.parts(l0, l1);
+                        auto add = [&](int b, float p, float q, float rest) {
+                            atomicAdd(&hist[b], 1u);
+                            if (!(p > (float)-SMP_ZERO)) return;
+                            const int x = WeightFn::frac(q, rest);
+                            atomicAdd(&hist[SMP_BINS + b], (uint32_t)x & 0xffffu);
+                            atomicAdd(&hist[2 * SMP_BINS + b], (uint32_t)(x >> 16));
+                        };
+                        const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(w.i0, w.p.x)) : -1;
+                        const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(w.i1, w.p.y)) : -1;
+                        if (b0 >= 0) add(b0, w.p.x, w.q.x, w.rest.x);
+                        if (b1 >= 0) add(b1, w.p.y, w.q.y, w.rest.y);
+                    }
                 }
             }
             sync_all<CLUSTER>();
@@ -406,14 +489,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                 mass[i] = 0;
                 if (i < PT && tid * PT + i < nb) {
                     const int b = b_lo + tid * PT + i;
+                    long long frac = 0;
                     for (uint32_t r = 0; r < cs; ++r) {
-                        auto at = [&](int plane) -> u64 {
+                        auto at = [&](int plane) -> uint32_t {
                             if constexpr (CLUSTER) return ld_peer_u32(map_peer(smem_u32(&hist[plane * SMP_BINS + b]), r));
                             else return hist[plane * SMP_BINS + b];
                         };
-                        cnt[i] += (uint32_t)at(0);
-                        if (k == 0) mass[i] += at(1) + (at(2) << 16) + (at(3) << 32);
+                        cnt[i] += at(0);
+                        if (k == 0) frac += (long long)at(1) + ((long long)(int)at(2) << 16);
                     }
+                    if (k == 0) mass[i] = wf.mass(level ? f.bin0 : b, cnt[i], frac);
                 }
                 tc += cnt[i];
                 tm += mass[i];
@@ -482,118 +567,173 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         }
     };
     int list_at = 0;
-    // Sorts the gathered tokens (first CTA) and returns the order of the last one kept: the first
+    // Ranks the gathered tokens (first CTA) and returns the order of the last one kept: the first
     // k overall (k > 0), and with do_p of these the nucleus of mass x, or where x is 0 of
     // ceil(p64 * mass of the k). above_*: what precedes all of them.
     auto finish = [&](uint32_t above_count, u64 above_mass, uint32_t k, bool do_p, u64 p64, u64 x) -> u64 {
         sync_all<CLUSTER>();                      // every CTA's entries have arrived
         if (rank == 0) {
             const int m = min((int)list_n[list_at], SMP_CAP);
-            // Bitonic, descending, an element a thread (and every THREADS further): neighbours closer
-            // than a warp through shuffles, others through shared memory. The place in the list
-            // rides in the low bits.
-            constexpr int PER = SMP_CAP / THREADS, PLACE = 10;
-            u64 v[PER];
-            int n2 = 2;
-            while (n2 < m) n2 *= 2;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid + i * THREADS;
-                v[i] = e < m ? (list_o[e] << PLACE) | (u64)e : 0;
-            }
-            for (int k2 = 2; k2 <= n2; k2 *= 2)
-                for (int j = k2 / 2; j > 0; j /= 2) {
-                    u64 o[PER];
-                    if (j < 32) {
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) o[i] = __shfl_xor_sync(0xffffffffu, v[i], j);
-                    } else if (j < THREADS) {
-                        __syncthreads();
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
-                        __syncthreads();
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) o[i] = list_o[(tid ^ j) + i * THREADS];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            o[i] = v[i];
-#pragma unroll
-                            for (int x = 0; x < PER; ++x)
-                                if (x == (i ^ (j / THREADS))) o[i] = v[x];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int e = tid + i * THREADS;
-                        const bool larger = ((e & k2) == 0) == ((e & j) == 0);
-                        if ((o[i] > v[i]) == larger) v[i] = o[i];
-                    }
-                }
-            // consecutive entries to a thread again
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
             if (tid == 0) last_kept = 0;
-            __syncthreads();
-            u64 w[PER], mine = 0, total;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid * PER + i;
-                w[i] = e < m && (k == 0 || above_count + e < k) ? list_w[list_o[e] & ((1 << PLACE) - 1)] : 0;
-                mine += w[i];
-            }
-            u64 before = block_scan_u64<THREADS>(mine, red, total) + above_mass;
-            total += above_mass;
-            if (do_p && x == 0) {
+            auto nucleus = [&](u64 mine) {        // x where it is not known yet; uniform
+                if (!do_p || x != 0) return;
+                u64 total;
+                block_scan_u64<THREADS>(mine, red, total);
+                total += above_mass;
                 x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
                 if (x == 0) x = 1;
-            }
-            int kept_to = 0;
+            };
+            if (m <= SMP_FEW) {
+                // G lanes compare an entry with all others
+                constexpr int G = THREADS / SMP_FEW;
+                if (tid < m) list_w[tid] = wf.fixed(logit_of(list_o[tid]));
+                __syncthreads();
+                const int at = tid / G;
+                const u64 o = at < m ? list_o[at] : ~0ull;
+                u64 before = 0;
+                int place = 0;
+#pragma unroll 4
+                for (int j = tid % G; j < m; j += G) {
+                    const bool earlier = list_o[j] > o;
+                    place += earlier;
+                    before += earlier ? list_w[j] : 0;
+                }
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid * PER + i;
-                if (e < m && (k == 0 || above_count + e < k) && (!do_p || before < x)) kept_to = e;
-                before += w[i];
-            }
-            kept_to = __reduce_max_sync(0xffffffffu, kept_to);
-            if (lane == 0 && kept_to > 0) atomicMax(&last_kept, kept_to);
-            __syncthreads();
-            if (tid < (int)cs) {
-                const u64 lowest = list_o[last_kept] >> PLACE;
-                if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), lowest);
-                else f_cut = lowest;
+                for (int d = 1; d < G; d *= 2) {
+                    place += __shfl_xor_sync(0xffffffffu, place, d);
+                    before += __shfl_xor_sync(0xffffffffu, before, d);
+                }
+                const bool in_k = at < m && (k == 0 || above_count + place < k);
+                nucleus(in_k && tid % G == 0 ? list_w[at] : 0);
+                const bool stays = in_k && (!do_p || above_mass + before < x);
+                const int to = __reduce_max_sync(0xffffffffu, stays ? place : 0);
+                if (lane == 0 && to > 0) atomicMax(&last_kept, to);
+                __syncthreads();
+                if (at < m && place == last_kept)
+                    for (int c = tid % G; c < (int)cs; c += G) {
+                        if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), c), o);
+                        else f_cut = o;
+                    }
+            } else {
+                // Bitonic, descending, an element a thread (and every THREADS further): neighbours
+                // closer than a warp through shuffles, others through shared memory.
+                constexpr int PER = SMP_CAP / THREADS;
+                u64 v[PER];
+                int n2 = SMP_FEW;
+                while (n2 < m) n2 *= 2;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = tid + i * THREADS;
+                    v[i] = e < m ? list_o[e] : 0;
+                }
+                for (int k2 = 2; k2 <= n2; k2 *= 2)
+                    for (int j = k2 / 2; j > 0; j /= 2) {
+                        u64 o[PER];
+                        if (j < 32) {
+#pragma unroll
+                            for (int i = 0; i < PER; ++i) o[i] = __shfl_xor_sync(0xffffffffu, v[i], j);
+                        } else if (j < THREADS) {
+                            __syncthreads();
+#pragma unroll
+                            for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
+                            __syncthreads();
+#pragma unroll
+                            for (int i = 0; i < PER; ++i) o[i] = list_o[(tid ^ j) + i * THREADS];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < PER; ++i) {
+                                o[i] = v[i];
+#pragma unroll
+                                for (int y = 0; y < PER; ++y)
+                                    if (y == (i ^ (j / THREADS))) o[i] = v[y];
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const int e = tid + i * THREADS;
+                            const bool larger = ((e & k2) == 0) == ((e & j) == 0);
+                            if ((o[i] > v[i]) == larger) v[i] = o[i];
+                        }
+                    }
+                // consecutive entries to a thread
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
+                __syncthreads();
+                u64 w[PER], mine = 0, total;
+#pragma unroll
+                for (int i = 0; i < PER; i += 2) {
+                    const int e = tid * PER + i;
+                    wf.fixed2(logit_of(list_o[e]), logit_of(list_o[e + 1]), w[i], w[i + 1]);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        if (!(e + y < m && (k == 0 || above_count + e + y < k))) w[i + y] = 0;
+                        mine += w[i + y];
+                    }
+                }
+                nucleus(mine);
+                u64 before = block_scan_u64<THREADS>(mine, red, total) + above_mass;
+                int to = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = tid * PER + i;
+                    if (e < m && (k == 0 || above_count + e < k) && (!do_p || before < x)) to = e;
+                    before += w[i];
+                }
+                to = __reduce_max_sync(0xffffffffu, to);
+                if (lane == 0 && to > 0) atomicMax(&last_kept, to);
+                __syncthreads();
+                if (tid < (int)cs) {
+                    if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), list_o[last_kept]);
+                    else f_cut = list_o[last_kept];
+                }
             }
         }
         sync_all<CLUSTER>();
         ++list_at;                                // a second list counts anew
         return f_cut;
     };
-    // Appends the tokens that `take` names to the first CTA's list; a warp's share by one counter update.
+    // Collects the orders of the tokens that `take` names, a warp's share by one counter update, and
+    // in a cluster a CTA's share by one more.
     auto gather = [&](auto take) {
-        for (int s0 = 0; s0 < n; s0 += THREADS) {
-            const int s = s0 + tid;
-            const float l = s < n ? l_s[s] : -INFINITY;
-            u64 o = 0;
-            const bool yes = l > -INFINITY && take(l, s, o);
-            const unsigned who = __ballot_sync(0xffffffffu, yes);
-            if (who == 0) continue;
+        uint32_t* count = CLUSTER ? &own_n[list_at] : &list_n[list_at];
+        for (int s0 = 0; s0 < n; s0 += 4 * THREADS) {
+            const int s = s0 + 4 * tid;
+            const float4 l4 = s < n ? *reinterpret_cast<const float4*>(l_s + s)
+                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+            bool yes[4];
+            int mine = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                yes[j] = l[j] > -INFINITY && take(l[j], base + s + j);
+                mine += yes[j];
+            }
+            if (!__any_sync(0xffffffffu, mine != 0)) continue;
+            int upto = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += y;
+            }
             uint32_t at = 0;
-            if (lane == 0) {
-                if constexpr (CLUSTER) at = atom_peer_add(map_peer(smem_u32(&list_n[list_at]), 0), __popc(who));
-                else at = atomicAdd(&list_n[list_at], __popc(who));
-            }
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-            if (yes && at < SMP_CAP) {
-                const u64 w = wf.fixed(l);
-                if constexpr (CLUSTER) {
-                    st_peer_u64(map_peer(smem_u32(&list_o[at]), 0), o);
-                    st_peer_u64(map_peer(smem_u32(&list_w[at]), 0), w);
-                } else {
-                    list_o[at] = o;
-                    list_w[at] = w;
+            if (lane == 31) at = atomicAdd(count, (uint32_t)upto);
+            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (yes[j]) {
+                    if (at < SMP_CAP) own_o[at] = order_of(l[j], base + s + j);
+                    ++at;
                 }
-            }
+        }
+        if constexpr (CLUSTER) {
+            __syncthreads();
+            const int m = min((int)*count, SMP_CAP);
+            if (tid == 0) own_at = m ? atom_peer_add(map_peer(smem_u32(&list_n[list_at]), 0), m) : 0;
+            __syncthreads();
+            const uint32_t at = own_at;
+            for (int e = tid; e < m; e += THREADS)
+                if (at + e < SMP_CAP) st_peer_u64(map_peer(smem_u32(&list_o[at + e]), 0), own_o[e]);
         }
     };
 
@@ -625,22 +765,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         const u64 p64 = par.p64;
         u64 x = 0;
         bool p_left = need_p;
-        if (a.V <= SMP_CAP) {                     // all of them sorted, no search
-            gather([&](float l, int s, u64& o) {
-                o = order_of(l, base + s);
-                return true;
-            });
-            set_cut(finish(0, 0, need_k ? (uint32_t)k_in : 0u, need_p, p64, 0));
-            p_left = false;
-        } else if (need_k) {
+        if (need_k) {
             // the whole top-k as one list where it fits, else only the set that holds its end
             const Found f = search((uint32_t)k_in, 0, x);
             if (f.bin0 < SMP_BINS) {
                 const bool all = f.shift == SMP_ORDER_BITS && f.above_count + f.count <= SMP_CAP;
-                gather([&](float l, int s, u64& o) {
-                    if (all ? bin0_of(l) > f.bin0 : bin0_of(l) != f.bin0) return false;
-                    o = order_of(l, base + s);
-                    return all || in_found(f, l, o);
+                gather([&](float l, int id) {
+                    const int b = wf.bin(l);
+                    return all ? b <= f.bin0 : b == f.bin0 && in_found(f, b, order_of(l, id));
                 });
                 set_cut(finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0));
                 if (all) p_left = false;
@@ -648,10 +780,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         }
         if (p_left) {
             const Found f = search(0, p64, x);
-            gather([&](float l, int s, u64& o) {
-                if (bin0_of(l) != f.bin0 || !above_cut(l, base + s)) return false;
-                o = order_of(l, base + s);
-                return in_found(f, l, o);
+            gather([&](float l, int id) {
+                const int b = wf.bin(l);
+                return b == f.bin0 && above_cut(l, id) && in_found(f, b, order_of(l, id));
             });
             set_cut(finish(f.above_count, f.above_mass, 0, true, p64, x));
         }
@@ -665,11 +796,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         const u64 w = wf.fixed(l);
         return w >= mp ? w : 0;
     };
-    const int seg = (n + THREADS - 1) / THREADS * 32;
+    const int seg = (n + 4 * THREADS - 1) / (4 * THREADS) * 128;
     {
+        // Few tokens stay of many and they lie apart: a warp queues them and weighs 64 at a time
         u64 m = 0;
+        int held = 0;
+        auto weigh = [&](int first) {
+            __syncwarp();
+            const int e = first + lane;
+            u64 w0, w1;
+            wf.fixed2(e < held ? queue[e] : -INFINITY, e + 32 < held ? queue[e + 32] : -INFINITY, w0, w1);
+            m += (w0 >= mp ? w0 : 0) + (w1 >= mp ? w1 : 0);
+            __syncwarp();
+        };
         const int hi = min(n, (warp + 1) * seg);
-        for (int s = warp * seg + lane; s < hi; s += 32) m += kept(s);
+        for (int s0 = warp * seg; s0 < hi; s0 += 128) {
+            const int s = s0 + 4 * lane;
+            const float4 l4 = s < hi ? *reinterpret_cast<const float4*>(l_s + s)
+                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool yes = above_cut(l[j], base + s + j);
+                const unsigned who = __ballot_sync(0xffffffffu, yes);
+                if (yes) queue[held + __popc(who & ((1u << lane) - 1))] = l[j];
+                held += __popc(who);
+            }
+            for (; held >= 64; held -= 64) weigh(held - 64);
+        }
+        if (held > 0) weigh(0);
         m = warp_sum_u64(m);
         if (lane == 0) warp_mass[warp] = m;
     }
@@ -717,20 +872,30 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                 // which is at least 1 and relative to it where it is near
                 const float lw = l_s[s] == mx ? 0.f : (l_s[s] - mx) / par.temp;
                 const u64 one = 1ull << SMP_FRAC;
-                const float lt = total < 2 * one ? log1pf((float)(total - one) * 5.684341886080802e-14f)   // 2^-44
-                                                 : logf((float)total * 5.684341886080802e-14f);
+                const float lt = total < 2 * one ? log1pf((float)(total - one) * 2.842170943040401e-14f)   // 2^-45
+                                                 : logf((float)total * 2.842170943040401e-14f);
                 a.logprob[row] = lw - lt;
             }
         }
     }
     if (a.probs) {
-        if (tid == 0) inv_total = (float)((double)(1ull << SMP_FRAC) / (double)total);
-        __syncthreads();
-        const float inv = inv_total;
+        const float inv = (float)(1ull << SMP_FRAC) / (float)total;
         float* pr = a.probs + (size_t)row * a.ldp;
-        for (int s = tid; s < n; s += THREADS) {
-            const int id = base + s;
-            if (id >= 0 && id < a.V) pr[id] = kept(s) ? wf.real(l_s[s]) * inv : 0.f;
+        for (int s = tid; s < n; s += 2 * THREADS) {
+            const int s1 = s + THREADS;
+            const float l0 = l_s[s], l1 = s1 < n ? l_s[s1] : -INFINITY;
+            const bool in0 = above_cut(l0, base + s), in1 = above_cut(l1, base + s1);
+            float p0 = 0.f, p1 = 0.f;
+            if (in0 || in1) {
+                const Parts w = wf.parts(l0, l1);
+                if (in0 && (mp == 0 || wf.scaled(w.i0, w.p.x, w.q.x, w.rest.x) >= mp))
+                    p0 = real_weight(w.i0, w.p.x, w.q.x, w.rest.x, pow2) * inv;
+                if (in1 && (mp == 0 || wf.scaled(w.i1, w.p.y, w.q.y, w.rest.y) >= mp))
+                    p1 = real_weight(w.i1, w.p.y, w.q.y, w.rest.y, pow2) * inv;
+            }
+            const int id = base + s, id1 = base + s1;
+            if (id >= 0 && id < a.V) pr[id] = p0;
+            if (s1 < n && id1 < a.V) pr[id1] = p1;
         }
     }
     if constexpr (CLUSTER) cluster_sync();        // peers may still write into this CTA
@@ -775,7 +940,7 @@ cudaError_t sample_dispatch(SampleArgs a, int rows, cudaStream_t stream) {
     const int cs = sample_cluster(rows, a.V);
     const int grans = (VEC - 1 + a.V + VEC - 1) / VEC;
     a.slice = (grans + cs - 1) / cs * VEC;
-    const size_t smem = (size_t)a.slice * 4 + (a.V <= SMP_CAP ? (size_t)SMP_CAP * 16 : (size_t)SMP_BINS * 16);
+    const size_t smem = (size_t)a.slice * 4 + (size_t)SMP_BINS * 12;
     if (cs > 1) return sample_launch<T, 512, true>(a, rows, cs, smem, stream);
     if (a.V > 2048) return sample_launch<T, 512, false>(a, rows, 1, smem, stream);
     return sample_launch<T, 256, false>(a, rows, 1, smem, stream);

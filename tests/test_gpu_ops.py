@@ -293,7 +293,7 @@ def test_attention_refusals(evs):
 
 # ---- the draw ------------------------------------------------------------------------------------
 def check_draw(evs, logits, u, probs=True, **kw):
-    """Tokens equal the definition's; logprob and probabilities to fp32 (their sums are exact to 1e-11)."""
+    """Tokens equal the definition's; logprob and probabilities to fp32 (their sums are exact to 1e-10)."""
     R, V = logits.shape
     out = evs.sample(logits, u, return_logprob=True, return_probs=probs, **kw)
     host = logits.float().cpu().numpy()
@@ -311,7 +311,7 @@ def check_draw(evs, logits, u, probs=True, **kw):
             # negative); weights below 2^-45 of the largest are left out of the total
             assert abs(lp[r] - wl) <= 5 * U * abs(wl) + 1e-9
         if probs:
-            # four roundings (a table entry, the multiply-add with it, 1 / total, the product) and one of a term
+            # four roundings (the sum of a table entry and its tail, the total, 1 over it, the product) and one of a term
             # of at most 0.011; weights below 2^-45 of the largest are none
             assert np.all(np.abs(pr[r] - wp) <= 4.05 * U * wp + 2.0 ** -44), r
     return out
