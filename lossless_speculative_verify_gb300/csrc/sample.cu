@@ -16,8 +16,8 @@
 // there. The cut (top-k and top-p are both prefixes of the sorted row, so one pair (logit, id)
 // describes what is kept) is found by a histogram over the weight's exponent in steps of 1/32,
 // narrowed by digits of (ordered logit, id) while the bin that holds the cut has more than CAP
-// tokens; those few are then ranked. A bin's mass follows from its count and the sum of its
-// tokens' mantissas above its lower end, so three 32-bit counters a bin are exact.
+// tokens; those few are then ranked. A bin's mass is the sum of its tokens' mantissas, of 34 bits,
+// in two 32-bit counters: the shared-memory atomics are what bounds the histogram of a large row.
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -225,9 +225,9 @@ struct WeightFn {
         return {__float_as_int(t.x) - __float_as_int(kRound), __float_as_int(t.y) - __float_as_int(kRound), unpk(p),
                 unpk(q), unpk(rest)};
     }
-    // q + rest in steps of 2^-34
-    static __device__ __forceinline__ int frac(float q, float rest) {
-        return __float2int_rn(q * 17179869184.f) + __float2int_rn(rest * 17179869184.f);
+    // q + rest in steps of 2^-34, or of 2^-33
+    static __device__ __forceinline__ int frac(float q, float rest, float steps = 17179869184.f) {
+        return __float2int_rn(q * steps) + __float2int_rn(rest * steps);
     }
     __device__ __forceinline__ u64 scaled(int i, float p, float q, float rest) const {
         const u64 t = tab[i & 31];
@@ -250,13 +250,11 @@ struct WeightFn {
         const float p = (l - M) * c_hi;
         return bin(__float_as_int(p + kRound) - __float_as_int(kRound), p);
     }
-    // The mass of `count` tokens of one bin whose q + rest sum to frac_sum
-    __device__ __forceinline__ u64 mass(int b, u64 count, long long frac_sum) const {
+    // The mass of a bin whose tokens' 1 + q + rest sum to s 2^-33
+    __device__ __forceinline__ u64 mass(int b, u64 s) const {
         if (b > 32 * SMP_ZERO) return 0;
-        const u64 t = tab[-b & 31];
-        const int n = (b + 31) >> 5;
-        const u64 m = count * (t >> (63 - SMP_FRAC)) + (u64)__mul64hi((long long)t, frac_sum << (SMP_FRAC - 33));
-        return n ? m >> (n - 1) : m << 1;
+        const u64 t = tab[-b & 31], hi = __umul64hi(t, s << 12), lo = t * (s << 12);   // in 2^-43, 2^-107
+        return (hi << (SMP_FRAC - 43) | lo >> (64 - (SMP_FRAC - 43))) >> ((b + 31) >> 5);
     }
 };
 // fp32 of it, for probabilities
@@ -277,8 +275,8 @@ template <typename T> union Raw16 {
 // whose order has `prefix` above bit `shift` (shift SMP_ORDER_BITS: all of the bin).
 struct Found {
     int bin0, shift;
-    uint32_t count, above_count;
-    u64 above_mass, prefix;
+    uint32_t count;        // at most so many
+    u64 above, prefix;     // above: count or mass of what precedes
 };
 
 // =========================================================================================
@@ -288,12 +286,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     constexpr int BPT = SMP_BINS / THREADS;     // bins a thread sums when the CTA is alone
     extern __shared__ __align__(16) uint8_t smem[];
     float* l_s = reinterpret_cast<float*>(smem);
-    // [3][BINS]: count, sum of q + rest (low 16 bits, the rest)
+    // [2][BINS]: count, or sum of mantissas (low 17 bits, high 17 bits)
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);
-    // after a search: what the row's first CTA ranks, and what each CTA found of it
+    // after a search: what the row's first CTA ranks, with its weights; and before these are
+    // worked out, what each CTA found of it, after that two lists of places
     u64* list_o = reinterpret_cast<u64*>(hist);                                 // [CAP]
-    u64* list_w = list_o + SMP_CAP;                                             // [FEW]
-    u64* own_o = CLUSTER ? list_w + SMP_FEW : list_o;                           // [CAP]
+    u64* list_w = list_o + SMP_CAP;                                             // [CAP]
+    u64* own_o = CLUSTER ? list_w : list_o;                                     // [CAP]
+    uint16_t* places = reinterpret_cast<uint16_t*>(list_w + SMP_CAP);           // [2][CAP]
     // after the cut: 192 kept logits a warp
     float* queue = reinterpret_cast<float*>(hist) + (threadIdx.x >> 5) * 192;
     __shared__ float2 pow2[32];
@@ -301,9 +301,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     __shared__ u64 red[THREADS / 32];
     __shared__ u64 warp_mass[THREADS / 32];
     __shared__ float x_max[SMP_MAX_CS];
-    __shared__ u64 x_cnt[SMP_MAX_CS], x_mass[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
-    __shared__ u64 f_above_mass, f_cut, pick_before;
-    __shared__ uint32_t f_bin, f_count, f_above_count, list_n[2], own_n[2], own_at;
+    __shared__ u64 x_cnt[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
+    __shared__ u64 f_above, f_cut, last_o, pick_before;
+    __shared__ u64 piv_o[THREADS / 32], piv_w[THREADS / 32];
+    __shared__ int piv_c[THREADS / 32];
+    __shared__ uint32_t piv_n;
+    __shared__ uint32_t f_bin, f_count, list_n[2], own_n[2], own_at;
     __shared__ int pick_warp, last_kept;
     __shared__ struct {
         u64 p64, u64_, mp;
@@ -417,7 +420,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         if (a.probs)
             for (int s = tid; s < n; s += THREADS)
                 if (base + s >= 0 && base + s < a.V) a.probs[(size_t)row * a.ldp + base + s] = 0.f;
-        if constexpr (CLUSTER) cluster_sync();
         return;
     }
 
@@ -437,10 +439,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     // x = ceil(p64 * their mass). Level 0 bins by the weight's exponent, later levels by a digit of the
     // order. bin0 is BINS where fewer than k tokens are left. Uniform over the cluster.
     auto search = [&](uint32_t k, u64 p64, u64& x) -> Found {
-        Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0, 0};
+        Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0};
         for (int level = 0;; ++level) {
             const int to = max(0, f.shift - SMP_DIGIT), width = f.shift - to;   // this level's digit
-            for (int i = tid; i < (k ? 1 : 3) * SMP_BINS; i += THREADS) hist[i] = 0;
+            for (int i = tid; i < (k ? 1 : 2) * SMP_BINS; i += THREADS) hist[i] = 0;
             __syncthreads();
             if (tid == 0) f_bin = SMP_BINS;      // read by all before that barrier, written next after another
             for (int s = 4 * tid; s < n; s += 4 * THREADS) {
@@ -465,11 +467,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                     } else {
                         const Parts w = wf.parts(l0, l1);
                         auto add = [&](int b, float p, float q, float rest) {
-                            atomicAdd(&hist[b], 1u);
                             if (!(p > (float)-SMP_ZERO)) return;
-                            const int x = WeightFn::frac(q, rest);
-                            atomicAdd(&hist[SMP_BINS + b], (uint32_t)x & 0xffffu);
-                            atomicAdd(&hist[2 * SMP_BINS + b], (uint32_t)(x >> 16));
+                            const int x = WeightFn::frac(q, rest, 8589934592.f);
+                            atomicAdd(&hist[b], (uint32_t)x & 0x1ffffu);
+                            atomicAdd(&hist[SMP_BINS + b], (uint32_t)((x >> 17) + 65536));
                         };
                         const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(w.i0, w.p.x)) : -1;
                         const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(w.i1, w.p.y)) : -1;
@@ -481,81 +482,68 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             sync_all<CLUSTER>();
             // this CTA's share of the bins, summed over the cluster; a thread takes PT in a row
             const int nb = SMP_BINS / cs, b_lo = nb * rank, PT = (nb + THREADS - 1) / THREADS;
-            uint32_t cnt[BPT];
-            u64 mass[BPT], tc = 0, tm = 0;
+            u64 sum[BPT], cnt[BPT], tc = 0;       // of counts or of masses
 #pragma unroll
             for (int i = 0; i < BPT; ++i) {
-                cnt[i] = 0;
-                mass[i] = 0;
+                cnt[i] = sum[i] = 0;
                 if (i < PT && tid * PT + i < nb) {
                     const int b = b_lo + tid * PT + i;
-                    long long frac = 0;
                     for (uint32_t r = 0; r < cs; ++r) {
                         auto at = [&](int plane) -> uint32_t {
                             if constexpr (CLUSTER) return ld_peer_u32(map_peer(smem_u32(&hist[plane * SMP_BINS + b]), r));
                             else return hist[plane * SMP_BINS + b];
                         };
-                        cnt[i] += at(0);
-                        if (k == 0) frac += (long long)at(1) + ((long long)(int)at(2) << 16);
+                        sum[i] += at(0);
+                        if (k == 0) sum[i] += (u64)at(1) << 17;
                     }
-                    if (k == 0) mass[i] = wf.mass(level ? f.bin0 : b, cnt[i], frac);
+                    cnt[i] = sum[i];
+                    if (k == 0) {
+                        // |q + rest| < 0.011: at most this many tokens
+                        cnt[i] = (sum[i] >> 33) + (sum[i] >> 39) + 1;
+                        sum[i] = wf.mass(level ? f.bin0 : b, sum[i]);
+                    }
                 }
-                tc += cnt[i];
-                tm += mass[i];
+                tc += sum[i];
             }
-            u64 all_c, all_m;
-            u64 ec = block_scan_u64<THREADS>(tc, red, all_c);
-            u64 em = 0;
-            all_m = 0;
-            if (k == 0) em = block_scan_u64<THREADS>(tm, red, all_m);
+            u64 all;
+            u64 before = block_scan_u64<THREADS>(tc, red, all);
             if constexpr (CLUSTER) {
-                if (tid < (int)cs) {
-                    st_peer_u64(map_peer(smem_u32(&x_cnt[rank]), tid), all_c);
-                    st_peer_u64(map_peer(smem_u32(&x_mass[rank]), tid), all_m);
-                }
+                if (tid < (int)cs) st_peer_u64(map_peer(smem_u32(&x_cnt[rank]), tid), all);
                 cluster_sync();
-                all_m = 0;
+                all = 0;
                 for (uint32_t i = 0; i < cs; ++i) {
-                    if (i < rank) {
-                        ec += x_cnt[i];
-                        em += x_mass[i];
-                    }
-                    all_m += x_mass[i];
+                    if (i < rank) before += x_cnt[i];
+                    all += x_cnt[i];
                 }
             }
             if (level == 0 && k == 0) {           // mass before a kept token < p * total
-                x = __umul64hi(p64, all_m) + ((p64 * all_m) != 0 ? 1 : 0);
+                x = __umul64hi(p64, all) + ((p64 * all) != 0 ? 1 : 0);
                 if (x == 0) x = 1;                // the first token is always kept
             }
-            ec += f.above_count;
-            em += f.above_mass;
+            before += f.above;
+            const u64 goal = k ? k : x;
 #pragma unroll
             for (int i = 0; i < BPT; ++i) {
-                const bool hit = k ? (ec < k && ec + cnt[i] >= k) : (em < x && em + mass[i] >= x);
-                if (hit) {
+                if (before < goal && before + sum[i] >= goal) {
                     const uint32_t bin = b_lo + tid * PT + i;
                     for (uint32_t r = 0; r < cs; ++r) {
                         if constexpr (CLUSTER) {
                             st_peer_u32(map_peer(smem_u32(&f_bin), r), bin);
-                            st_peer_u32(map_peer(smem_u32(&f_count), r), cnt[i]);
-                            st_peer_u32(map_peer(smem_u32(&f_above_count), r), (uint32_t)ec);
-                            st_peer_u64(map_peer(smem_u32(&f_above_mass), r), em);
+                            st_peer_u32(map_peer(smem_u32(&f_count), r), (uint32_t)cnt[i]);
+                            st_peer_u64(map_peer(smem_u32(&f_above), r), before);
                         } else {
                             f_bin = bin;
-                            f_count = cnt[i];
-                            f_above_count = (uint32_t)ec;
-                            f_above_mass = em;
+                            f_count = (uint32_t)cnt[i];
+                            f_above = before;
                         }
                     }
                 }
-                ec += cnt[i];
-                em += mass[i];
+                before += sum[i];
             }
             sync_all<CLUSTER>();
             if (f_bin == SMP_BINS) return f;
             f.count = f_count;
-            f.above_count = f_above_count;
-            f.above_mass = f_above_mass;
+            f.above = f_above;
             if (level == 0) {
                 f.bin0 = (int)f_bin;
             } else {
@@ -570,123 +558,124 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     // Ranks the gathered tokens (first CTA) and returns the order of the last one kept: the first
     // k overall (k > 0), and with do_p of these the nucleus of mass x, or where x is 0 of
     // ceil(p64 * mass of the k). above_*: what precedes all of them.
-    auto finish = [&](uint32_t above_count, u64 above_mass, uint32_t k, bool do_p, u64 p64, u64 x) -> u64 {
+    auto finish = [&](u64 above_count, u64 above_mass, u64 k, bool do_p, u64 p64, u64 x) -> u64 {
         sync_all<CLUSTER>();                      // every CTA's entries have arrived
         if (rank == 0) {
             const int m = min((int)list_n[list_at], SMP_CAP);
-            if (tid == 0) last_kept = 0;
-            auto nucleus = [&](u64 mine) {        // x where it is not known yet; uniform
-                if (!do_p || x != 0) return;
+            for (int e = tid; e < m; e += THREADS) list_w[e] = wf.fixed(logit_of(list_o[e]));
+            auto nucleus = [&](u64 mine) {        // mass wanted of these and what precedes them
                 u64 total;
                 block_scan_u64<THREADS>(mine, red, total);
                 total += above_mass;
                 x = __umul64hi(p64, total) + ((p64 * total) != 0 ? 1 : 0);
                 if (x == 0) x = 1;
             };
-            if (m <= SMP_FEW) {
-                // G lanes compare an entry with all others
-                constexpr int G = THREADS / SMP_FEW;
-                if (tid < m) list_w[tid] = wf.fixed(logit_of(list_o[tid]));
+            // The last entry that has fewer than k - above_count before it (k > 0) and less mass than
+            // x - above_mass (with_p). While more than FEW may be it, each warp weighs one of them
+            // against the others, and what lies between two of those goes on.
+            auto last = [&](u64 k, bool with_p) -> u64 {
+                u64 before_c = above_count, before_m = above_mass;
+                int left = m, at = 0;
+                for (int e = tid; e < m; e += THREADS) places[e] = (uint16_t)e;
                 __syncthreads();
-                const int at = tid / G;
-                const u64 o = at < m ? list_o[at] : ~0ull;
-                u64 before = 0;
-                int place = 0;
+                while (left > SMP_FEW) {
+                    const uint16_t* from = places + at * SMP_CAP;
+                    uint16_t* onto = places + (at ^ 1) * SMP_CAP;
+                    const int pivot = from[(int)((long long)left * warp / (THREADS / 32))];
+                    const u64 o = list_o[pivot];
+                    int c = 0;
+                    u64 w = 0;
 #pragma unroll 4
-                for (int j = tid % G; j < m; j += G) {
-                    const bool earlier = list_o[j] > o;
-                    place += earlier;
-                    before += earlier ? list_w[j] : 0;
+                    for (int e = lane; e < left; e += 32) {
+                        const int i = from[e];
+                        const u64 y = list_w[i];
+                        const bool earlier = list_o[i] > o;
+                        c += earlier;
+                        w += earlier ? y : 0;
+                    }
+                    c = __reduce_add_sync(0xffffffffu, c);
+                    w = warp_sum_u64(w);
+                    if (lane == 0) {
+                        piv_o[warp] = o;
+                        piv_c[warp] = c;
+                        piv_w[warp] = w;
+                    }
+                    if (tid == 0) piv_n = 0;
+                    __syncthreads();
+                    // the last one known to stay, the first one known to go
+                    const int y = lane % (THREADS / 32);
+                    const u64 py = piv_o[y], wy = piv_w[y];
+                    const int cy = piv_c[y];
+                    const bool stays = (k == 0 || before_c + cy < k) && (!with_p || before_m + wy < x);
+                    const int hi_c = __reduce_max_sync(0xffffffffu, stays ? cy : -1);
+                    const int lo_c = __reduce_min_sync(0xffffffffu, stays ? INT_MAX : cy);
+                    const unsigned is_hi = __ballot_sync(0xffffffffu, cy == hi_c), is_lo = __ballot_sync(0xffffffffu, cy == lo_c);
+                    u64 hi = ~0ull, lo = 0;
+                    if (is_lo) lo = __shfl_sync(0xffffffffu, py, __ffs(is_lo) - 1);
+                    if (is_hi) {
+                        hi = __shfl_sync(0xffffffffu, py, __ffs(is_hi) - 1);
+                        before_c += hi_c;
+                        before_m += __shfl_sync(0xffffffffu, wy, __ffs(is_hi) - 1);
+                    }
+                    for (int e0 = 0; e0 < left; e0 += THREADS) {
+                        const int e = e0 + tid;
+                        const int i = e < left ? from[e] : 0;
+                        const bool goes_on = e < left && list_o[i] > lo && list_o[i] <= hi;
+                        const unsigned who = __ballot_sync(0xffffffffu, goes_on);
+                        uint32_t to = 0;
+                        if (lane == 0 && who) to = atomicAdd(&piv_n, (uint32_t)__popc(who));
+                        to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1));
+                        if (goes_on) onto[to] = (uint16_t)i;
+                    }
+                    __syncthreads();
+                    left = piv_n;
+                    at ^= 1;
+                    __syncthreads();
                 }
-#pragma unroll
+                // 2^g lanes compare an entry with all others
+                const int g = min(5, __clz(max(left - 1, 1)) - __clz(THREADS) - 1), G = 1 << g;
+                const uint16_t* from = places + at * SMP_CAP;
+                const int e = tid >> g, sub = tid & (G - 1);
+                const int own = e < left ? from[e] : 0;
+                const u64 own_w = list_w[own];
+                const u64 o = e < left ? list_o[own] : ~0ull;
+                int c = 0;
+                u64 w = 0;
+#pragma unroll 4
+                for (int j = sub; j < left; j += G) {
+                    const int i = from[j];
+                    const u64 y = list_w[i];
+                    const bool earlier = list_o[i] > o;
+                    c += earlier;
+                    w += earlier ? y : 0;
+                }
                 for (int d = 1; d < G; d *= 2) {
-                    place += __shfl_xor_sync(0xffffffffu, place, d);
-                    before += __shfl_xor_sync(0xffffffffu, before, d);
+                    c += __shfl_xor_sync(0xffffffffu, c, d);
+                    w += __shfl_xor_sync(0xffffffffu, w, d);
                 }
-                const bool in_k = at < m && (k == 0 || above_count + place < k);
-                nucleus(in_k && tid % G == 0 ? list_w[at] : 0);
-                const bool stays = in_k && (!do_p || above_mass + before < x);
-                const int to = __reduce_max_sync(0xffffffffu, stays ? place : 0);
+                const bool in_k = e < left && (k == 0 || before_c + c < k);
+                if (with_p && x == 0) nucleus(in_k && sub == 0 ? own_w : 0);
+                if (tid == 0) last_kept = 0;
+                __syncthreads();
+                const bool stays = in_k && (!with_p || before_m + w < x);
+                const int to = __reduce_max_sync(0xffffffffu, stays ? c : 0);
                 if (lane == 0 && to > 0) atomicMax(&last_kept, to);
                 __syncthreads();
-                if (at < m && place == last_kept)
-                    for (int c = tid % G; c < (int)cs; c += G) {
-                        if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), c), o);
-                        else f_cut = o;
-                    }
-            } else {
-                // Bitonic, descending, an element a thread (and every THREADS further): neighbours
-                // closer than a warp through shuffles, others through shared memory.
-                constexpr int PER = SMP_CAP / THREADS;
-                u64 v[PER];
-                int n2 = SMP_FEW;
-                while (n2 < m) n2 *= 2;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = tid + i * THREADS;
-                    v[i] = e < m ? list_o[e] : 0;
-                }
-                for (int k2 = 2; k2 <= n2; k2 *= 2)
-                    for (int j = k2 / 2; j > 0; j /= 2) {
-                        u64 o[PER];
-                        if (j < 32) {
-#pragma unroll
-                            for (int i = 0; i < PER; ++i) o[i] = __shfl_xor_sync(0xffffffffu, v[i], j);
-                        } else if (j < THREADS) {
-                            __syncthreads();
-#pragma unroll
-                            for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
-                            __syncthreads();
-#pragma unroll
-                            for (int i = 0; i < PER; ++i) o[i] = list_o[(tid ^ j) + i * THREADS];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < PER; ++i) {
-                                o[i] = v[i];
-#pragma unroll
-                                for (int y = 0; y < PER; ++y)
-                                    if (y == (i ^ (j / THREADS))) o[i] = v[y];
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const int e = tid + i * THREADS;
-                            const bool larger = ((e & k2) == 0) == ((e & j) == 0);
-                            if ((o[i] > v[i]) == larger) v[i] = o[i];
-                        }
-                    }
-                // consecutive entries to a thread
+                if (e < left && c == last_kept && sub == 0) last_o = o;
                 __syncthreads();
-#pragma unroll
-                for (int i = 0; i < PER; ++i) list_o[tid + i * THREADS] = v[i];
-                __syncthreads();
-                u64 w[PER], mine = 0, total;
-#pragma unroll
-                for (int i = 0; i < PER; i += 2) {
-                    const int e = tid * PER + i;
-                    wf.fixed2(logit_of(list_o[e]), logit_of(list_o[e + 1]), w[i], w[i + 1]);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if (!(e + y < m && (k == 0 || above_count + e + y < k))) w[i + y] = 0;
-                        mine += w[i + y];
-                    }
-                }
+                return last_o;
+            };
+            if (do_p && x == 0 && m > SMP_FEW) {
+                const u64 c = last(k, false);
+                u64 mine = 0;
+                for (int e = tid; e < m; e += THREADS) mine += list_o[e] >= c ? list_w[e] : 0;
                 nucleus(mine);
-                u64 before = block_scan_u64<THREADS>(mine, red, total) + above_mass;
-                int to = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = tid * PER + i;
-                    if (e < m && (k == 0 || above_count + e < k) && (!do_p || before < x)) to = e;
-                    before += w[i];
-                }
-                to = __reduce_max_sync(0xffffffffu, to);
-                if (lane == 0 && to > 0) atomicMax(&last_kept, to);
-                __syncthreads();
-                if (tid < (int)cs) {
-                    if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), list_o[last_kept]);
-                    else f_cut = list_o[last_kept];
-                }
+                k = 0;                            // what follows the k-th has x or more before it
+            }
+            const u64 c = last(k, do_p);
+            if (tid < (int)cs) {
+                if constexpr (CLUSTER) st_peer_u64(map_peer(smem_u32(&f_cut), tid), c);
+                else f_cut = c;
             }
         }
         sync_all<CLUSTER>();
@@ -702,29 +691,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             const float4 l4 = s < n ? *reinterpret_cast<const float4*>(l_s + s)
                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-            bool yes[4];
-            int mine = 0;
+            bool yes[4], mine = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 yes[j] = l[j] > -INFINITY && take(l[j], base + s + j);
-                mine += yes[j];
+                mine |= yes[j];
             }
-            if (!__any_sync(0xffffffffu, mine != 0)) continue;
-            int upto = mine;
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            uint32_t off[4], all = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += y;
+            for (int j = 0; j < 4; ++j) {
+                const unsigned who = __ballot_sync(0xffffffffu, yes[j]);
+                off[j] = all + __popc(who & ((1u << lane) - 1));
+                all += __popc(who);
             }
             uint32_t at = 0;
-            if (lane == 31) at = atomicAdd(count, (uint32_t)upto);
-            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+            if (lane == 0) at = atomicAdd(count, all);
+            at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (yes[j]) {
-                    if (at < SMP_CAP) own_o[at] = order_of(l[j], base + s + j);
-                    ++at;
-                }
+                if (yes[j] && at + off[j] < SMP_CAP) own_o[at + off[j]] = order_of(l[j], base + s + j);
         }
         if constexpr (CLUSTER) {
             __syncthreads();
@@ -769,12 +755,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             // the whole top-k as one list where it fits, else only the set that holds its end
             const Found f = search((uint32_t)k_in, 0, x);
             if (f.bin0 < SMP_BINS) {
-                const bool all = f.shift == SMP_ORDER_BITS && f.above_count + f.count <= SMP_CAP;
+                const bool all = f.shift == SMP_ORDER_BITS && f.above + f.count <= SMP_CAP;
                 gather([&](float l, int id) {
                     const int b = wf.bin(l);
                     return all ? b <= f.bin0 : b == f.bin0 && in_found(f, b, order_of(l, id));
                 });
-                set_cut(finish(all ? 0 : f.above_count, 0, (uint32_t)k_in, need_p && all, p64, 0));
+                set_cut(finish(all ? 0 : f.above, 0, (uint32_t)k_in, need_p && all, p64, 0));
                 if (all) p_left = false;
             }
         }
@@ -784,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                 const int b = wf.bin(l);
                 return b == f.bin0 && above_cut(l, id) && in_found(f, b, order_of(l, id));
             });
-            set_cut(finish(f.above_count, f.above_mass, 0, true, p64, x));
+            set_cut(finish(0, f.above, 0, true, p64, x));
         }
     }
 
@@ -898,7 +884,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             if (s1 < n && id1 < a.V) pr[id1] = p1;
         }
     }
-    if constexpr (CLUSTER) cluster_sync();        // peers may still write into this CTA
 }
 
 // Cluster size: slices of at most 16384 slots (64 KiB, so that two CTAs share an SM), then more
@@ -940,7 +925,7 @@ cudaError_t sample_dispatch(SampleArgs a, int rows, cudaStream_t stream) {
     const int cs = sample_cluster(rows, a.V);
     const int grans = (VEC - 1 + a.V + VEC - 1) / VEC;
     a.slice = (grans + cs - 1) / cs * VEC;
-    const size_t smem = (size_t)a.slice * 4 + (size_t)SMP_BINS * 12;
+    const size_t smem = (size_t)a.slice * 4 + (size_t)SMP_CAP * 20;
     if (cs > 1) return sample_launch<T, 512, true>(a, rows, cs, smem, stream);
     if (a.V > 2048) return sample_launch<T, 512, false>(a, rows, 1, smem, stream);
     return sample_launch<T, 256, false>(a, rows, 1, smem, stream);
