@@ -32,33 +32,39 @@ def _vec(name, t, dtype, shape, dev):
     """Address of a contiguous tensor of the given type and shape on dev, or None."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and
-            t.is_contiguous() and t.device == dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+            t.device == dev):
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}")
     return t.data_ptr()
 
 
 def _rows3(name, t, dtype, shape, dev, written=False):
     """Strides (row, sequence) of a [batch, tokens, n] tensor whose last dimension is contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
     b, n, w = shape
     sq, ld, one = t.stride()
     ld = ld if n > 1 else w
     sq = sq if b > 1 else 0
-    _need(one == 1 or w == 1, f"{name}: the last dimension has to be contiguous")
-    _need(ld >= w, f"{name}: rows overlap")
-    _need(not written or b <= 1 or sq >= w, f"{name}: sequences overlap")
+    if not (one == 1 or w == 1):
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
+    if ld < w:
+        raise ValueError(f"{name}: rows overlap")
+    if written and b > 1 and sq < w:
+        raise ValueError(f"{name}: sequences overlap")
     return ld, sq
 
 
 def _enqueue(fn, where, args, dev):
+    # (the stream object that torch.cuda.current_stream builds costs 2 us a call)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        st = fn(C.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(C.byref(args), stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(C.byref(args), torch.cuda.current_stream(dev).cuda_stream)
-    L.check(st, where)
+            st = fn(C.byref(args), stream)
+    if st:
+        L.check(st, where)
 
 
 def _device(name, t):
@@ -181,9 +187,26 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
 
 
 def _kv(name, t, dtype, shape, dev):
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
-    _need(t.stride(-1) == 1, f"{name}: the head dimension has to be contiguous")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the head dimension has to be contiguous")
+    return st
+
+
+def _flat(name, t, dtype, shape, dev):
+    """Row stride of a [batch, candidates, block, heads, dh] tensor whose rows are evenly spaced."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    B, Cn, T, H, dh = shape
+    s0, s1, s2, s3, s4 = t.stride()
+    if not (s4 == 1 and (H == 1 or s3 == dh)):
+        raise ValueError(f"{name}: heads have to be contiguous")
+    ld = s2 if T > 1 else s1 if Cn > 1 else s0 if B > 1 else H * dh
+    if not (ld >= H * dh and (Cn == 1 or s1 == T * ld) and (B == 1 or s0 == Cn * T * ld)):
+        raise ValueError(f"{name}: rows have to be evenly spaced")
+    return ld
 
 
 def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_block=None, v_block=None, *, scale=None,
@@ -209,38 +232,23 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     _need(1 <= Cn <= 64 and 1 <= T <= 128 and B <= 1024, "at most 1024 sequences, 64 candidates, 128 block positions")
     _need(isinstance(k_own, torch.Tensor) and k_own.dim() == 4, "k_own: want [batch, kv_heads, capacity, dh]")
     S = k_own.shape[2]
-    for name, t, shape in (("k_prefix", k_prefix, (G, P, dh)), ("v_prefix", v_prefix, (G, P, dh)),
-                           ("k_own", k_own, (B, G, S, dh)), ("v_own", v_own, (B, G, S, dh))):
-        _kv(name, t, dt, shape, dev)
-    ps, os_ = k_prefix.stride(), k_own.stride()
-    _need(ps == v_prefix.stride() and os_ == v_own.stride(), "K and V: want equal strides")
+    ps = _kv("k_prefix", k_prefix, dt, (G, P, dh), dev)
+    os_ = _kv("k_own", k_own, dt, (B, G, S, dh), dev)
+    _need(ps == _kv("v_prefix", v_prefix, dt, (G, P, dh), dev) and os_ == _kv("v_own", v_own, dt, (B, G, S, dh), dev),
+          "K and V: want equal strides")
     _need((k_block is None) == (v_block is None), "k_block and v_block go together")
     if k_block is not None:
-        _kv("k_block", k_block, dt, (B, Cn, G, T, dh), dev)
-        _kv("v_block", v_block, dt, (B, Cn, G, T, dh), dev)
-        bs = k_block.stride()
-        _need(bs == v_block.stride(), "K and V: want equal strides")
+        bs = _kv("k_block", k_block, dt, (B, Cn, G, T, dh), dev)
+        _need(bs == _kv("v_block", v_block, dt, (B, Cn, G, T, dh), dev), "K and V: want equal strides")
         _need(Cn == 1 or B == 1 or bs[0] == Cn * bs[1], "k_block: sequences and candidates have to be evenly spaced")
         b_row, b_head, b_cand = (bs[3] if T > 1 else dh), bs[2], bs[1] if Cn > 1 else bs[0]
     else:
         _need(Cn == 1 and S > 0, "block rows in k_own want one candidate")
         b_row = b_head = b_cand = 0
 
-    def flat(name, t, dtype):
-        """Row stride of a [batch, candidates, block, heads, dh] tensor whose rows are evenly spaced."""
-        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == (B, Cn, T, H, dh) and
-                t.device == dev):
-            raise ValueError(f"{name}: want {dtype} {(B, Cn, T, H, dh)} on {dev}")
-        s = t.stride()
-        _need(s[4] == 1 and (H == 1 or s[3] == dh), f"{name}: heads have to be contiguous")
-        ld = s[2] if T > 1 else s[1] if Cn > 1 else s[0] if B > 1 else H * dh
-        _need(ld >= H * dh and (Cn == 1 or s[1] == T * ld) and (B == 1 or s[0] == Cn * T * ld),
-              f"{name}: rows have to be evenly spaced")
-        return ld
-
-    q_ld = flat("q", q, q.dtype)
+    q_ld = _flat("q", q, q.dtype, (B, Cn, T, H, dh), dev)
     o = torch.empty(B, Cn, T, H, dh, dtype=dt, device=dev) if out is None else out
-    o_ld = flat("out", o, dt)
+    o_ld = _flat("out", o, dt, (B, Cn, T, H, dh), dev)
     _need(scale is None or scale > 0.0, "scale: above zero")
     lse = torch.empty(B, Cn, T, H, dtype=torch.float32, device=dev) if return_lse else None
     a = L.SharedAttnArgs(B, Cn, T, H, G, dh, _DT[dt], _DT[q.dtype], P, S, 0, 0.0 if scale is None else scale,
