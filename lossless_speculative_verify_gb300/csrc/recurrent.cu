@@ -309,6 +309,44 @@ __device__ __forceinline__ float step_size(float v, int softplus) {
     return v != v ? v : r;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
+
+// The same for two at a time: 25 instructions where the scalar one takes 28 for each
+__device__ __forceinline__ float2 step_sizes(float v0, float v1) {
+    const uint64_t t = pair_of(fmaxf(-fabsf(v0), -100.f), fmaxf(-fabsf(v1), -100.f));
+    const uint64_t hi = mul2(t, both(kLog2e));
+    const uint64_t lo = fma2(t, both(kLog2eLo), fma2(t, both(kLog2e), mul2(t, both(-kLog2e))));
+    const float2 h = unpair(hi);
+    uint64_t e = pair_of(ex2(h.x), ex2(h.y));
+    e = fma2(e, mul2(lo, both(0.69314718f)), e);
+    const float2 d = unpair(fma2(e, both(1.f), both(2.f)));
+    const uint64_t z = mul2(e, pair_of(rcp(d.x), rcp(d.y))), w = mul2(z, z);
+    uint64_t p = fma2(w, both(1.f / 13.f), both(1.f / 11.f));
+    p = fma2(p, w, both(1.f / 9.f));
+    p = fma2(p, w, both(1.f / 7.f));
+    p = fma2(p, w, both(1.f / 5.f));
+    p = fma2(p, w, both(1.f / 3.f));
+    p = fma2(p, w, both(1.f));
+    return unpair(fma2(fma2(z, both(1.f), z), p, pair_of(max_nan(v0, 0.f), max_nan(v1, 0.f))));
+}
+// q * silu(z) for two
+__device__ __forceinline__ uint64_t gate(uint64_t q, float z0, float z1) {
+    const uint64_t z = pair_of(z0, z1);
+    const float2 t = unpair(mul2(z, both(-kLog2e)));
+    const float2 d = unpair(fma2(pair_of(ex2(t.x), ex2(t.y)), both(1.f), both(1.f)));
+    return mul2(q, mul2(z, pair_of(rcp(d.x), rcp(d.y))));
+}
+
 // A few tokens (single tokens, verify blocks): lanes of a channel hold NPL states each, straight
 // from global memory; HBM-bound on the state read and written.
 template <typename T, int N, int LPC>
@@ -362,10 +400,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
     if (a.state_out && on) store_vec<float, NPL>(a.state_out + so, s);
 }
 
-// Prompts. A lane owns a channel (LPC lanes where it has 32 states) with its states in registers, a
-// warp 32 / LPC neighbouring channels. x, dt and z come asynchronously into the warp's own ring of
-// SCAN_RING groups of eight positions, B_t and C_t into shared memory for the CTA, 32 positions at a
-// time, which all lanes read as one address. Nothing is exchanged between lanes.
+// Prompts. A lane owns a channel (LPC lanes do, with N / LPC states each, where that would leave few
+// warps) with its states in registers, a warp 32 / LPC neighbouring channels. x, dt and z come
+// asynchronously into the warp's own ring of SCAN_RING groups of eight positions, B_t and C_t into
+// shared memory for the CTA, 32 positions at a time, which all lanes read as one address. What is
+// per position and channel (softplus, gate) one of its lanes works out for the others, two
+// positions at a time in packed arithmetic. Bound by instructions: 16 sequences of 2048 x 4096 take
+// 720 us, 104 ns for a warp's step of about 125 instructions on a quarter of an SM.
 //
 // That leaves few warps for few sequences, so the tokens are cut into segments: a first pass runs
 // each segment from a zero state (the first from state_in) and leaves its last state and the sum of
@@ -384,13 +425,15 @@ template <int BYTES> __device__ __forceinline__ void cp_async(void* dst, const v
 struct ScanSeg {
     float* ws;          // [b][segment][N + 1][D]: last states and the sum of dl; then [b][N][D] state_in
     int segs, len;      // segments of a sequence, positions of one
+    int lanes;          // of a channel
 };
 
-// V2: rows of channel pairs that can be copied asynchronously (they start on two elements).
-template <typename T, int N, int LPC, bool FIRST, bool V2>
+// COPY: bytes of an asynchronous copy, 16 where rows start on 16 bytes, else 4 (bf16: where they
+// start on two channels), else 0: element by element.
+template <typename T, int N, int LPC, bool FIRST, int COPY>
 __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanSeg sg) {
-    constexpr int NPL = N / LPC, THREADS = 32 * SCAN_WARPS, CPW = 32 / LPC, PAIRS = CPW / 2;
-    constexpr int PXL = 8 * PAIRS / 32;              // pairs of a group that a lane copies
+    constexpr int NPL = N / LPC, THREADS = 32 * SCAN_WARPS, CPW = 32 / LPC;
+    constexpr int EL = COPY ? COPY / (int)sizeof(T) : 1, PER_ROW = CPW / EL;   // channels of a copy, copies of a row
     constexpr int GROUP = 8 * CPW;                   // values of one array in a ring slot
     extern __shared__ __align__(16) uint8_t ring_raw[];
     constexpr int PBC = (SCAN_TC * N / 2 + THREADS - 1) / THREADS;
@@ -451,6 +494,7 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
     const T* db = (const T*)a.dt + (size_t)b * a.dt_seq;
     const bool out = !FIRST && a.y != nullptr, gated = out && a.z != nullptr;
     const T* zb = gated ? (const T*)a.z + (size_t)b * a.z_seq : xb;
+    const int64_t z_ld = gated ? a.z_ld : a.x_ld;
     const T* Bm = (const T*)a.Bm + (size_t)b * a.b_seq;
     const T* Cm = (const T*)a.Cm + (size_t)b * a.c_seq;
     T* y = out ? (T*)a.y + (size_t)b * a.y_seq + ch : nullptr;
@@ -459,23 +503,25 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
     const int c0 = (blockIdx.x * SCAN_WARPS + warp) * CPW;    // the warp's first channel
     const int groups = (max(t1 - t0, 0) + 7) / 8;
     // Positions t0 + 8 g .. + 7 into the ring; past the end the last row again, past the width the
-    // last channels. A pair that straddles neither is copied as it lies.
+    // last channels.
     auto request = [&](int g) {
         if (g < groups) {
             T* to = ring + g % SCAN_RING * (3 * GROUP);
 #pragma unroll
-            for (int i = 0; i < PXL; ++i) {
-                const int e = lane + 32 * i, c = min(c0 + e % PAIRS * 2, a.D - (V2 ? 2 : 1)), o = V2 ? 0 : min(c + 1, a.D - 1) - c;
-                const int64_t t = min(t0 + 8 * g + e / PAIRS, t1 - 1);
-                const T *px = xb + t * a.x_ld + c, *pd = db + t * a.dt_ld + c, *pz = gated ? zb + t * a.z_ld + c : px;
-                if (V2) {
-                    cp_async<2 * sizeof(T)>(to + 2 * e, px);
-                    cp_async<2 * sizeof(T)>(to + GROUP + 2 * e, pd);
-                    if (gated) cp_async<2 * sizeof(T)>(to + 2 * GROUP + 2 * e, pz);
+            for (int i = 0; i < (8 * PER_ROW + 31) / 32; ++i) {
+                const int e = lane + 32 * i, c = min(c0 + e % PER_ROW * EL, a.D - EL);
+                if (8 * PER_ROW % 32 && e >= 8 * PER_ROW) break;
+                const int64_t t = min(t0 + 8 * g + e / PER_ROW, t1 - 1);
+                const T *px = xb + t * a.x_ld + c, *pd = db + t * a.dt_ld + c, *pz = zb + t * z_ld + c;
+                if constexpr (COPY > 0) {
+                    cp_async<COPY>(to + EL * e, px);
+                    cp_async<COPY>(to + GROUP + EL * e, pd);
+                    if (gated) cp_async<COPY>(to + 2 * GROUP + EL * e, pz);
                 } else {
-                    const T v[6] = {px[0], px[o], pd[0], pd[o], pz[0], pz[o]};
-#pragma unroll
-                    for (int k = 0; k < 6; ++k) to[k / 2 * GROUP + 2 * e + k % 2] = v[k];
+                    const T vx = *px, vd = *pd, vz = *pz;
+                    to[e] = vx;
+                    to[GROUP + e] = vd;
+                    to[2 * GROUP + e] = vz;
                 }
             }
         }
@@ -506,24 +552,45 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
             }
         }
     };
-    const int my = min(ch - c0, CPW - 1);            // this lane's channel in a ring row
+    constexpr int PER = 8 / LPC;
+    const int part = lane % LPC;
+    const int my = max(0, min(ch - c0, CPW - 1));    // this lane's channel in a ring row
     auto steps = [&](int g, int row, int buf) {
-        // the three parts apart, each eight positions wide, so that their chains fill one another
+        // the three parts apart, each eight positions wide, so that their chains fill one another;
+        // what belongs to a position alone is worked out by one of a channel's lanes for all
         const T* from = ring + g % SCAN_RING * (3 * GROUP) + my;
-        const int t = t0 + 8 * g;
-        float xv[8], dl[8], q[8];
+        const int t = t0 + 8 * g, u0 = part * PER;
+        float xv[PER], dl[PER], ux[PER], q[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            xv[u] = to_f32(from[u * CPW]);
-            dl[u] = step_size(to_f32(from[GROUP + u * CPW]) + bias, a.softplus);
+        for (int i = 0; i < PER; ++i) {
+            xv[i] = to_f32(from[(u0 + i) * CPW]);
+            dl[i] = to_f32(from[GROUP + (u0 + i) * CPW]) + bias;
+        }
+        if (a.softplus) {
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                const float2 d = step_sizes(dl[i], dl[i + 1]);
+                dl[i] = d.x;
+                dl[i + 1] = d.y;
+            }
+        }
+        const bool whole = t + 8 <= t1;
+        if (!whole) {
             // positions past the end keep the state: dl = 0 gives a decay of one, and no input
-            if (t + u >= t1) dl[u] = xv[u] = 0.f;
-            if (FIRST) sum += dl[u];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (t + u0 + i >= t1) dl[i] = xv[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (FIRST) sum += dl[i];
+            ux[i] = dl[i] * xv[i];
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float ux = dl[u] * xv[u];
-            const uint64_t dl2 = pair_of(dl[u], dl[u]), u2 = pair_of(ux, ux);
+            const float dlu = LPC == 1 ? dl[u % PER] : __shfl_sync(0xffffffffu, dl[u % PER], u / PER, LPC);
+            const float uxu = LPC == 1 ? ux[u % PER] : __shfl_sync(0xffffffffu, ux[u % PER], u / PER, LPC);
+            const uint64_t dl2 = pair_of(dlu, dlu), u2 = pair_of(uxu, uxu);
             uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
             for (int k = 0; k < NPL / 2; k += 2) {
@@ -542,15 +609,31 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
             q[u] = (v0.x + v0.y) + (v1.x + v1.y);
         }
         if (out) {
+            // the lanes' sums, each keeping half of the positions
 #pragma unroll
-            for (int o = LPC / 2; o > 0; o >>= 1)
+            for (int o = LPC / 2, n = 4; o > 0; o >>= 1, n >>= 1)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) q[u] += __shfl_xor_sync(0xffffffffu, q[u], o);
+                for (int i = 0; i < n; ++i) {
+                    const bool up = part & o;
+                    const float other = __shfl_xor_sync(0xffffffffu, up ? q[i] : q[i + n], o);
+                    q[i] = (up ? q[i + n] : q[i]) + other;
+                }
+            T* yt = y + (int64_t)(t + u0) * a.y_ld;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                q[u] = fmaf(Ds, xv[u], q[u]);
-                if (gated) q[u] *= silu(to_f32(from[2 * GROUP + u * CPW]));
-                if (t + u < t1 && on && k0 == 0) y[(int64_t)(t + u) * a.y_ld] = from_f32<T>(q[u]);
+            for (int i = 0; i < PER; i += 2) {
+                uint64_t v = fma2(both(Ds), pair_of(xv[i], xv[i + 1]), pair_of(q[i], q[i + 1]));
+                if (gated) v = gate(v, to_f32(from[2 * GROUP + (u0 + i) * CPW]), to_f32(from[2 * GROUP + (u0 + i + 1) * CPW]));
+                const float2 w = unpair(v);
+                q[i] = w.x;
+                q[i + 1] = w.y;
+            }
+            if (on && whole) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i, yt += a.y_ld) *yt = from_f32<T>(q[i]);
+            } else if (on) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i, yt += a.y_ld)
+                    if (t + u0 + i < t1) *yt = from_f32<T>(q[i]);
             }
         }
     };
@@ -571,6 +654,10 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
                 request(g + SCAN_RING - 1);        // into the slot of group g - 1
             }
         }
+    }
+    if (FIRST) {
+#pragma unroll
+        for (int o = LPC / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     if (on && (FIRST || (last && a.state_out))) {
         float v[NPL];
@@ -595,68 +682,86 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
 
 constexpr int SCAN_STEP_MAX = 16;   // up to this many tokens the staging is not worth its barriers
 
-// Segments of a prompt: enough that about SCAN_FILL warps run, of at least 128 positions (a multiple
-// of the staged 32). 2 x 4096 x 4096 tokens x channels: 274 us with 30 warps an SM asked for, 322
-// with 12; 8 x 1024 x 4096: 244 us, 265 in one piece.
-constexpr int SCAN_FILL = 152 * 30, SCAN_MAX_SEGS = 64;
+// Lanes and segments of a prompt. One lane a channel, unless that leaves schedulers without a warp
+// even with segments (512 x 2048 positions x channels of 16 states: 27 us with four lanes, 44 with
+// one). Segments where fewer than a warp for each scheduler would run, of at least 128 positions
+// (a multiple of the staged 32), enough for about 32 warps an SM: 2 x 4096 x 4096 takes 242 us so,
+// 293 with half of that and 731 in one piece; 8 x 1024 x 4096, with 1024 warps in one piece, 230 us,
+// 261 with segments.
+constexpr int SCAN_FEW = 152 * 4, SCAN_FILL = 152 * 32, SCAN_MAX_SEGS = 64;
 ScanSeg scan_segments(int B, int T, int D, int N) {
-    const long long warps = (long long)B * ((D * (N == 32 ? 2 : 1) + 31) / 32);
-    long long segs = 1;
-    if (T > SCAN_STEP_MAX && warps < SCAN_FILL) {
-        segs = (SCAN_FILL + warps - 1) / warps;
-        if (segs > T / 128) segs = T / 128;
-        if (segs > SCAN_MAX_SEGS) segs = SCAN_MAX_SEGS;
-        if (segs < 3) segs = 1;                    // two segments pay twice and gain at most that
+    ScanSeg sg{nullptr, 1, T, 1};
+    if (T <= SCAN_STEP_MAX) return sg;
+    for (int lanes = N == 32 ? 2 : 1;; lanes = N == 32 ? 4 : N / 4) {
+        const long long warps = (long long)B * ((D * (long long)lanes + 31) / 32);
+        long long segs = 1;
+        if (warps < SCAN_FEW) {
+            segs = SCAN_FILL / warps;
+            if (segs > T / 128) segs = T / 128;
+            if (segs > SCAN_MAX_SEGS) segs = SCAN_MAX_SEGS;
+            if (segs < 3) segs = 1;                // two segments pay twice and gain at most that
+        }
+        const bool most = lanes >= (N == 32 ? 4 : N / 4);
+        if (warps * segs >= SCAN_FEW || most) {
+            sg.lanes = lanes;
+            if (segs > 1) {
+                sg.len = (int)(((T + segs - 1) / segs + SCAN_TC - 1) / SCAN_TC * SCAN_TC);
+                sg.segs = (T + sg.len - 1) / sg.len;
+            }
+            return sg;
+        }
     }
-    ScanSeg sg{nullptr, 1, T};
-    if (segs > 1) {
-        sg.len = (int)(((T + segs - 1) / segs + SCAN_TC - 1) / SCAN_TC * SCAN_TC);
-        sg.segs = (T + sg.len - 1) / sg.len;
-    }
-    return sg;
 }
 size_t scan_ws_bytes(const ScanSeg& sg, int B, int D, int N) {
     return sg.segs > 1 ? ((size_t)B * sg.segs * (N + 1) + (size_t)B * N) * D * 4 : 0;
 }
 
-template <typename T, int N, int LPC, bool V2>
+template <typename T, int N, int LPC, int COPY>
 cudaError_t scan_prompt(const ScanArgs& a, const ScanSeg& sg, int B, cudaStream_t s) {
     const int cols = (a.D * LPC + 32 * SCAN_WARPS - 1) / (32 * SCAN_WARPS);
     constexpr size_t smem = SCAN_WARPS * SCAN_RING * 3 * 8 * (32 / LPC) * sizeof(T);
     const dim3 block(32 * SCAN_WARPS);
+    auto first = scan_kernel<T, N, LPC, true, COPY>;
+    auto second = scan_kernel<T, N, LPC, false, COPY>;
     cudaError_t e = cudaSuccess;
-    if (sg.segs > 1) {
-        if (smem > 24 * 1024)   // with the static part above 48 KB
-            e = cudaFuncSetAttribute(scan_kernel<T, N, LPC, true, V2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) e = launch_s(s, scan_kernel<T, N, LPC, true, V2>, dim3(cols, B, sg.segs - 1), block, smem, a, sg);
+    if (smem > 24 * 1024) {   // with the static part above 48 KB
+        if (sg.segs > 1) e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(second, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     }
-    if (smem > 24 * 1024 && e == cudaSuccess)
-        e = cudaFuncSetAttribute(scan_kernel<T, N, LPC, false, V2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e != cudaSuccess ? e : launch_s(s, scan_kernel<T, N, LPC, false, V2>, dim3(cols, B, sg.segs), block, smem, a, sg);
+    if (sg.segs > 1 && e == cudaSuccess) e = launch_s(s, first, dim3(cols, B, sg.segs - 1), block, smem, a, sg);
+    return e != cudaSuccess ? e : launch_s(s, second, dim3(cols, B, sg.segs), block, smem, a, sg);
 }
 
-// Channel pairs are copied as they lie where every row starts on one.
-bool pairs_ok(const ScanArgs& a, size_t es) {
+// Every row of x, dt and z starts on n channels.
+bool rows_on(const ScanArgs& a, size_t es, int n) {
     auto ok = [&](const void* p, int64_t ld, int64_t seq) {
-        return !p || ((uintptr_t)p % (2 * es) == 0 && ld % 2 == 0 && seq % 2 == 0);
+        return !p || ((uintptr_t)p % (n * es) == 0 && ld % n == 0 && seq % n == 0);
     };
-    return a.D % 2 == 0 && ok(a.x, a.x_ld, a.x_seq) && ok(a.dt, a.dt_ld, a.dt_seq) && ok(a.z, a.z_ld, a.z_seq);
+    return a.D % n == 0 && ok(a.x, a.x_ld, a.x_seq) && ok(a.dt, a.dt_ld, a.dt_seq) && ok(a.z, a.z_ld, a.z_seq);
 }
 
-template <typename T, int N, int SLPC, int LPC>
+template <typename T, int N, int LPC>
+cudaError_t scan_copies(const ScanArgs& a, const ScanSeg& sg, int B, cudaStream_t s) {
+    constexpr int es = sizeof(T);
+    if (rows_on(a, es, 16 / es)) return scan_prompt<T, N, LPC, 16>(a, sg, B, s);
+    if (es == 4 || rows_on(a, es, 4 / es)) return scan_prompt<T, N, LPC, 4>(a, sg, B, s);
+    if constexpr (es < 4) return scan_prompt<T, N, LPC, 0>(a, sg, B, s);
+    return cudaSuccess;
+}
+template <typename T, int N, int SLPC, int FEW, int MANY>
 cudaError_t scan_launch(const ScanArgs& a, const ScanSeg& sg, int B, cudaStream_t s) {
     if (a.T <= SCAN_STEP_MAX)
         return launch_s(s, scan_step_kernel<T, N, SLPC>, dim3((a.D * SLPC + 255) / 256, B), dim3(256), 0, a);
-    return pairs_ok(a, sizeof(T)) ? scan_prompt<T, N, LPC, true>(a, sg, B, s) : scan_prompt<T, N, LPC, false>(a, sg, B, s);
+    return sg.lanes == MANY ? scan_copies<T, N, MANY>(a, sg, B, s) : scan_copies<T, N, FEW>(a, sg, B, s);
 }
 
 template <typename T>
 cudaError_t scan_dispatch(const ScanArgs& a, const ScanSeg& sg, int B, int N, cudaStream_t s) {
     switch (N) {
-        case 4: return scan_launch<T, 4, 4, 1>(a, sg, B, s);
-        case 8: return scan_launch<T, 8, 4, 1>(a, sg, B, s);
-        case 16: return scan_launch<T, 16, 4, 1>(a, sg, B, s);
-        default: return scan_launch<T, 32, 8, 2>(a, sg, B, s);
+        case 4: return scan_launch<T, 4, 4, 1, 1>(a, sg, B, s);
+        case 8: return scan_launch<T, 8, 4, 1, 2>(a, sg, B, s);
+        case 16: return scan_launch<T, 16, 4, 1, 4>(a, sg, B, s);
+        default: return scan_launch<T, 32, 8, 2, 4>(a, sg, B, s);
     }
 }
 

@@ -608,7 +608,9 @@ def make_scan(seed, B, T, D, N, dtype):
 
 
 SCAN = [(1, 1, 1, 4), (2, 1, 64, 16), (3, 3, 33, 8), (2, 16, 40, 32), (2, 17, 64, 16), (3, 32, 65, 16), (2, 33, 100, 4),
-        (1, 100, 130, 32), (2, 300, 64, 8), (64, 1, 256, 16), (1, 600, 32, 16)]
+        (1, 100, 130, 32), (2, 300, 64, 8), (64, 1, 256, 16), (1, 600, 32, 16),
+        # enough channels for a lane each, in one piece and in segments; rows on 16, 4 and 2 bytes
+        (40, 40, 512, 16), (40, 33, 514, 16), (40, 33, 513, 16), (2, 700, 2048, 16), (40, 40, 488, 8), (24, 40, 420, 32)]
 
 
 @pytest.mark.parametrize("shape", SCAN, ids=str)
