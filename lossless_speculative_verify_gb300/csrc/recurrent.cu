@@ -70,6 +70,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266175e-8f;   // log2 e and its rest
+
+// v / (1 + exp(-v)) for two: 8 instructions, where the scalar one takes about 11 for each
+__device__ __forceinline__ uint64_t silu2(uint64_t v) {
+    const float2 t = unpair(mul2(v, both(-kLog2e)));
+    const float2 d = unpair(fma2(pair_of(ex2(t.x), ex2(t.y)), both(1.f), both(1.f)));
+    return mul2(v, pair_of(rcp(d.x), rcp(d.y)));
+}
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
 // A sequence's length: lens[b] clamped to [0, T], flagged if it lay outside.
@@ -197,9 +219,10 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
                     }
                     hist[0][i] = v0;
                     hist[0][i + 1] = v1;
+                    if (a.act) acc = silu2(acc);
                     const float2 r = unpair(acc);
-                    out[i] = a.act ? silu(r.x) : r.x;
-                    out[i + 1] = a.act ? silu(r.y) : r.y;
+                    out[i] = r.x;
+                    out[i + 1] = r.y;
                 }
             } else {
 #pragma unroll
@@ -280,14 +303,6 @@ struct ScanArgs {
     int T, D, softplus;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266175e-8f;   // log2 e and its rest
-
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|): the exponential's argument with its rounding
 // carried along, and log(1 + e) = 2 atanh(z), z = e / (2 + e) <= 1/3, by its series (the terms left
 // out are below 2e-8 of it), so that it stays relatively exact where e is small.
@@ -309,18 +324,11 @@ __device__ __forceinline__ float step_size(float v, int softplus) {
     return v != v ? v : r;
 }
 
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-__device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
-
 // The same for two at a time: 25 instructions where the scalar one takes 28 for each
 __device__ __forceinline__ float2 step_sizes(float v0, float v1) {
     const uint64_t t = pair_of(fmaxf(-fabsf(v0), -100.f), fmaxf(-fabsf(v1), -100.f));
@@ -339,14 +347,6 @@ __device__ __forceinline__ float2 step_sizes(float v0, float v1) {
     p = fma2(p, w, both(1.f));
     return unpair(fma2(fma2(z, both(1.f), z), p, pair_of(max_nan(v0, 0.f), max_nan(v1, 0.f))));
 }
-// q * silu(z) for two
-__device__ __forceinline__ uint64_t gate(uint64_t q, float z0, float z1) {
-    const uint64_t z = pair_of(z0, z1);
-    const float2 t = unpair(mul2(z, both(-kLog2e)));
-    const float2 d = unpair(fma2(pair_of(ex2(t.x), ex2(t.y)), both(1.f), both(1.f)));
-    return mul2(q, mul2(z, pair_of(rcp(d.x), rcp(d.y))));
-}
-
 // A few tokens (single tokens, verify blocks): lanes of a channel hold NPL states each, straight
 // from global memory; HBM-bound on the state read and written.
 template <typename T, int N, int LPC>
@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanS
 #pragma unroll
             for (int i = 0; i < PER; i += 2) {
                 uint64_t v = fma2(both(Ds), pair_of(xv[i], xv[i + 1]), pair_of(q[i], q[i + 1]));
-                if (gated) v = gate(v, to_f32(from[2 * GROUP + (u0 + i) * CPW]), to_f32(from[2 * GROUP + (u0 + i + 1) * CPW]));
+                if (gated)
+                    v = mul2(v, silu2(pair_of(to_f32(from[2 * GROUP + (u0 + i) * CPW]), to_f32(from[2 * GROUP + (u0 + i + 1) * CPW]))));
                 const float2 w = unpair(v);
                 q[i] = w.x;
                 q[i + 1] = w.y;
