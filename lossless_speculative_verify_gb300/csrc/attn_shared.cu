@@ -35,6 +35,7 @@ struct SharedArgs {
     float *sh_o, *own_o;       // [segment][slot][dh / 4][rows4][4]
     float2 *sh_ml, *own_ml;    // [segment][slot][rows] (m, l), natural units
     int sh_rows, sh_tiles, sh_slots, own_rows, own_tiles, own_slots;
+    int partials;              // a partial kernel runs
     int tensor;                // the tensor-core kernel's partials: slots by its runs of tiles
     int sh_pair, own_pair;     // 1: segments of up to 256 rows, a row tile a lane; 0: a lane of its own
     int* plan;                 // run lengths (shared, own), where own runs start, own costs before sequence b
@@ -72,8 +73,8 @@ constexpr int SA_Q = 16, SA_K = 64;
 
 template <typename T>
 __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_items) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                // the combine may begin: all before this kernel is done
     __shared__ float qs[SA_Q][128];
     __shared__ float kvs[SA_K][129];
     __shared__ float ps[SA_Q][SA_K];
@@ -274,13 +275,13 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    pdl_trigger();
-    pdl_wait();
-    for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
     if (warp == 8) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    pdl_wait();
+    pdl_trigger();                // the combine may begin: all before this kernel is done
+    for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
     __syncthreads();
     if (warp == 0) {
         int run = 0;
@@ -303,9 +304,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     const int sh_cost = ntp ? a.G * a.sh_tiles * (ntp + ST_OVER) : 0, own_cost = per_b * pre[a.B];
     const int grid = gridDim.x;
     const bool split = a.sh_pair != a.own_pair && sh_cost > 0 && own_cost > 0;
-    const int n_sh = split ? min(grid - 1, max(1, (int)(((long long)grid * sh_cost + (sh_cost + own_cost) / 2) /
-                                                        (sh_cost + own_cost))))
-                           : grid;
+    // a tile takes a pair of lanes 1.76 us (measured with 208 rows), a lane of its own 2.3, its CTA half of that
+    const long long sh_ctas = (2 + a.sh_pair) * (long long)sh_cost, ctas = sh_ctas + (2 + a.own_pair) * (long long)own_cost;
+    const int n_sh = split ? min(grid - 1, max(1, (int)((grid * sh_ctas + ctas / 2) / ctas))) : grid;
     const bool on_sh = split ? (int)blockIdx.x < n_sh : sh_cost > 0;      // axis starts with the prefix
     const bool rows2 = (on_sh ? a.sh_pair : a.own_pair) != 0;             // lanes are two row tiles
     auto run_of = [&](int cost, int ctas, int pair) { return max(1, (cost + ctas * (2 - pair) - 1) / (ctas * (2 - pair))); };
@@ -733,18 +734,26 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
 
 // =========================================================================================
 // Combine. A CTA takes 512 / dh consecutive (candidate, position, head) rows of a sequence and K/V
-// head, a thread four columns of one row: it folds the row's partials, then the block rows j <= i
-// (scores by a dot product over the row's threads, 16 keys at a time), and normalises.
+// head, 128 threads for them, four columns of one row each, and up to four such groups, which deal
+// the row's partials and the chunks of its block rows among them. First the block rows j <= i
+// (scores by a dot product over the row's threads, 16 keys at a time), which need nothing of the
+// partial kernel and are done while that runs out; then the partials; then the groups' sums.
 // =========================================================================================
+constexpr int SC_GROUPS = 4;
 template <typename T, int DH>
-__global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
+__global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedArgs a) {
     constexpr int RW = 512 / DH, KB = 16;
-    __shared__ float part[4][KB][RW];             // a warp's share of the dot products
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5;
+    __shared__ float part[SC_GROUPS][4][KB][RW];  // a warp's share of the dot products
+    __shared__ float4 sum_o[SC_GROUPS - 1][128];
+    __shared__ float2 sum_ml[SC_GROUPS - 1][128];
+    // The partial kernel starts its dependents when all before it is done; without one, wait for that.
+    if (!a.partials) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    const int tid = threadIdx.x & 127, part_of = threadIdx.x >> 7, parts = blockDim.x >> 7, warp = tid >> 5;
     const int grp = a.H / a.G, rows = a.C * a.T * grp;
-    const int b = blockIdx.x, g = blockIdx.y, row = threadIdx.x % RW, c4 = threadIdx.x / RW;
+    const int b = blockIdx.x, g = blockIdx.y, row = tid % RW, c4 = tid / RW;
     const int r_own = blockIdx.z * RW + row;
     const bool live = r_own < rows;
     const int ci = (live ? r_own : rows - 1) / grp, hg = (live ? r_own : rows - 1) - ci * grp;   // (c, i), head
@@ -767,52 +776,7 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
         O.z = fmaf(w, v.z, O.z);
         O.w = fmaf(w, v.w, O.w);
     };
-    // the partials of row r of segment seg
-    auto fold = [&](const float* po, const float2* pml, int64_t seg, int slots, int seg_rows, int r, int used) {
-        constexpr int PB = 8;                      // in flight
-        const float2* ml_at = pml + seg * slots * seg_rows + r;
-        const float* o_at = po + (seg * slots * DH + (int64_t)c4 * 4) * rows4(seg_rows) + r * 4;
-        const int64_t o_step = (int64_t)DH * rows4(seg_rows);
-        for (int s0 = 0; s0 < used; s0 += PB) {
-            float2 ml[PB];
-            float4 os[PB];
-#pragma unroll
-            for (int j = 0; j < PB; ++j) {
-                const bool on = s0 + j < used;
-                ml[j] = on ? ml_at[(int64_t)(s0 + j) * seg_rows] : make_float2(-INFINITY, 0.f);
-                os[j] = on ? *reinterpret_cast<const float4*>(o_at + (s0 + j) * o_step) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float mb = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < PB; ++j) mb = fmaxf(mb, ml[j].x);
-            rebase(mb);
-#pragma unroll
-            for (int j = 0; j < PB; ++j) {
-                // an empty partial leaves its o unwritten (one of NaN scores has l = NaN)
-                if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
-                const float w = exp_of<T>(ml[j].x - M);
-                L = fmaf(ml[j].y, w, L);
-                add(w, os[j]);
-            }
-        }
-    };
     const int own = own_rows_of(a, b, false);
-    // the runs that a segment's nt tiles from position at on meet
-    auto runs = [&](int at, int nt, int W) { return (at + nt - 1) / W - at / W + 1; };
-    if (live && a.P > 0) {
-        const int r = (int)(m * grp + hg), t = r / a.sh_rows, seg = g * a.sh_tiles + t, nt = (a.P + 127) / 128;
-        fold(a.sh_o, a.sh_ml, seg, a.sh_slots, a.sh_rows, r - t * a.sh_rows,
-             a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots);
-    }
-    if (live && own > 0) {
-        const int t = r_own / a.own_rows, in_b = g * a.own_tiles + t, per_b = a.G * a.own_tiles;
-        int used = a.own_slots;
-        if (a.tensor) {
-            const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
-            used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
-        }
-        fold(a.own_o, a.own_ml, (int64_t)b * per_b + in_b, a.own_slots, a.own_rows, r_own - t * a.own_rows, used);
-    }
     // block rows j <= i: of this candidate, or own rows own + j when the block is in the cache
     const T *kb, *vb;
     int64_t ld;
@@ -829,7 +793,7 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
         ld = a.o_row;
         if (own + i >= a.own_max) {                // rows past the capacity do not exist
             last = a.own_max - 1 - own;
-            if (a.flags && live && c4 == 0) atomicOr(a.flags, (uint32_t)EVS_FLAG_KV_OVERFLOW);
+            if (a.flags && live && c4 == 0 && part_of == 0) atomicOr(a.flags, (uint32_t)EVS_FLAG_KV_OVERFLOW);
         }
     }
     auto load4 = [&](const T* p) -> float4 {
@@ -848,10 +812,10 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
     float q[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) q[u] = load_q(a, m * a.q_ld + (int64_t)h * DH + c4 * 4 + u) * a.scale;
-    for (int j0 = 0; j0 < a.T; j0 += KB) {         // the same count for every row of the CTA
-        const int n = min(KB, a.T - j0);
+    for (int j1 = 0; j1 < a.T; j1 += KB * parts) {  // the same count for every thread of the CTA
+        const int j0 = j1 + part_of * KB, n = min(KB, a.T - j0);
         float4 v[KB];
-        if (j0 > 0) __syncthreads();
+        if (j1 > 0) __syncthreads();
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
             if (j >= n) break;
@@ -865,14 +829,15 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
             float s = fmaf(q[0], k.x, fmaf(q[1], k.y, fmaf(q[2], k.z, q[3] * k.w)));
 #pragma unroll
             for (int o = RW; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((threadIdx.x & 31) < RW) part[warp][j][row] = s;
+            if ((tid & 31) < RW) part[part_of][warp][j][row] = s;
         }
         __syncthreads();
         float s[KB], mb = -INFINITY;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
             s[j] = -INFINITY;
-            if (j < n && j0 + j <= last) s[j] = (part[0][j][row] + part[1][j][row]) + (part[2][j][row] + part[3][j][row]);
+            if (j < n && j0 + j <= last)
+                s[j] = (part[part_of][0][j][row] + part[part_of][1][j][row]) + (part[part_of][2][j][row] + part[part_of][3][j][row]);
             mb = fmaxf(mb, s[j]);
         }
         rebase(mb);
@@ -882,6 +847,79 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(SharedArgs a) {
             const float w = exp_of<T>(s[j] - M);
             L += w;
             add(w, v[j]);
+        }
+    }
+    if (a.partials) {
+        pdl_wait();
+        pdl_trigger();
+        // the runs that a segment's nt tiles from position at on meet
+        auto runs = [&](int at, int nt, int W) { return (at + nt - 1) / W - at / W + 1; };
+        // the row's partials: those of the prefix, then those of the own rows
+        const float *sh_o = nullptr, *own_o = nullptr;
+        const float2 *sh_ml = nullptr, *own_ml = nullptr;
+        int sh_used = 0, own_used = 0;
+        if (live && a.P > 0) {
+            const int r = (int)(m * grp + hg), t = r / a.sh_rows, in = r - t * a.sh_rows;
+            const int seg = g * a.sh_tiles + t, nt = (a.P + 127) / 128;
+            sh_ml = a.sh_ml + (int64_t)seg * a.sh_slots * a.sh_rows + in;
+            sh_o = a.sh_o + ((int64_t)seg * a.sh_slots * DH + c4 * 4) * rows4(a.sh_rows) + in * 4;
+            sh_used = a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots;
+        }
+        if (live && own > 0) {
+            const int t = r_own / a.own_rows, in = r_own - t * a.own_rows, in_b = g * a.own_tiles + t, per_b = a.G * a.own_tiles;
+            const int64_t seg = (int64_t)b * per_b + in_b;
+            own_ml = a.own_ml + seg * a.own_slots * a.own_rows + in;
+            own_o = a.own_o + (seg * a.own_slots * DH + c4 * 4) * rows4(a.own_rows) + in * 4;
+            own_used = a.own_slots;
+            if (a.tensor) {
+                const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
+                own_used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
+            }
+        }
+        constexpr int PB = 8;                      // in flight
+        for (int s0 = part_of; s0 < sh_used + own_used; s0 += PB * parts) {
+            float2 ml[PB];
+            float4 os[PB];
+#pragma unroll
+            for (int j = 0; j < PB; ++j) {
+                const int s = s0 + j * parts, so = s - sh_used;
+                const bool sh = so < 0;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                os[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < sh_used + own_used) {
+                    ml[j] = sh ? sh_ml[(int64_t)s * a.sh_rows] : own_ml[(int64_t)so * a.own_rows];
+                    os[j] = *reinterpret_cast<const float4*>(sh ? sh_o + (int64_t)s * DH * rows4(a.sh_rows)
+                                                                : own_o + (int64_t)so * DH * rows4(a.own_rows));
+                }
+            }
+            float mb = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < PB; ++j) mb = fmaxf(mb, ml[j].x);
+            rebase(mb);
+#pragma unroll
+            for (int j = 0; j < PB; ++j) {
+                // an empty partial leaves its o unwritten (one of NaN scores has l = NaN)
+                if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
+                const float w = exp_of<T>(ml[j].x - M);
+                L = fmaf(ml[j].y, w, L);
+                add(w, os[j]);
+            }
+        }
+    }
+    if (parts > 1) {
+        if (part_of > 0) {
+            sum_o[part_of - 1][tid] = O;
+            sum_ml[part_of - 1][tid] = make_float2(M, L);
+        }
+        __syncthreads();
+        if (part_of > 0) return;
+        for (int p = 0; p < parts - 1; ++p) {
+            const float2 ml = sum_ml[p][tid];
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;
+            rebase(ml.x);
+            const float w = exp_of<T>(ml.x - M);
+            L = fmaf(ml.y, w, L);
+            add(w, sum_o[p][tid]);
         }
     }
     if (!live) return;
@@ -1068,6 +1106,7 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     carve_partials(c, a, (char*)c.workspace);
     const int sh_items = c.kv_heads * a.sh_slots * ((a.sh_rows + SA_Q - 1) / SA_Q);
     const int own_items = c.batch * c.kv_heads * a.own_slots * ((a.own_rows + SA_Q - 1) / SA_Q);
+    a.partials = tensor || sh_items + own_items > 0;
     cudaError_t e = cudaSuccess;
     if (tensor)
         // the ring takes what 227 KB leave: five tiles of 32 KB, four where the lengths need their place
@@ -1080,7 +1119,12 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     if (e != cudaSuccess) return e;
     const int rw = 512 / c.head_dim;
     const dim3 grid(c.batch, c.kv_heads, (c.n_cand * c.block * (c.heads / c.kv_heads) + rw - 1) / rw);
-    auto combine = [&](auto kernel) { return launch_s(stream, kernel, grid, dim3(128), 0, a); };
+    // groups: one for eight partials of a row, which it loads at once, while all of them run at once
+    const long long most = 4 * 152 / ((long long)grid.x * grid.y * grid.z);
+    int groups = ((a.P > 0 ? a.sh_slots : 0) + (a.own_max > 0 ? a.own_slots : 0) + 7) / 8;
+    groups = groups < most ? groups : (int)most;
+    groups = groups < 1 ? 1 : groups > SC_GROUPS ? SC_GROUPS : groups;
+    auto combine = [&](auto kernel) { return launch_s(stream, kernel, grid, dim3(128 * groups), 0, a); };
     switch (c.head_dim) {
         case 128: return half ? combine(shared_combine_kernel<bf16, 128>) : combine(shared_combine_kernel<float, 128>);
         case 64: return half ? combine(shared_combine_kernel<bf16, 64>) : combine(shared_combine_kernel<float, 64>);
