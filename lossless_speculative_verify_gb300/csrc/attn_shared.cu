@@ -213,8 +213,9 @@ __device__ __forceinline__ uint32_t st_pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void st_cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or as many zeros
+__device__ __forceinline__ void st_cp_async16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ uint64_t st_pair(float a, float b) {
@@ -305,8 +306,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     const int grid = gridDim.x;
     const bool split = a.sh_pair != a.own_pair && sh_cost > 0 && own_cost > 0;
     // a tile takes a pair of lanes 1.76 us (measured with 208 rows), a lane of its own 2.3, its CTA half of that
-    const long long sh_ctas = (2 + a.sh_pair) * (long long)sh_cost, ctas = sh_ctas + (2 + a.own_pair) * (long long)own_cost;
-    const int n_sh = split ? min(grid - 1, max(1, (int)((grid * sh_ctas + ctas / 2) / ctas))) : grid;
+    // (in fp32, the same for every CTA)
+    const float sh_ctas = (float)(2 + a.sh_pair) * (float)sh_cost, own_ctas = (float)(2 + a.own_pair) * (float)own_cost;
+    const int n_sh = split ? min(grid - 1, max(1, (int)((float)grid * __fdividef(sh_ctas, sh_ctas + own_ctas) + 0.5f))) : grid;
     const bool on_sh = split ? (int)blockIdx.x < n_sh : sh_cost > 0;      // axis starts with the prefix
     const bool rows2 = (on_sh ? a.sh_pair : a.own_pair) != 0;             // lanes are two row tiles
     auto run_of = [&](int cost, int ctas, int pair) { return max(1, (cost + ctas * (2 - pair) - 1) / (ctas * (2 - pair))); };
@@ -553,32 +555,34 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         const int m_in = r_all / grp;
         const int64_t m = p.sh ? m_in : (int64_t)p.b * a.C * a.T + m_in;
         const int64_t at = m * a.q_ld + (int64_t)(p.g * grp + r_all - m_in * grp) * DH;
-        uint8_t* dst = sQ + L * TILE;
+        uint8_t* dst = sQ + L * TILE + r * 128;
+        if (a.q_bf16 && a.q_vec) {
+            const bf16* src = (const bf16*)a.q + (live ? at : 0);
+            const uint32_t to = smem_u32(dst);
 #pragma unroll 1
-        for (int hf = 0; hf < HALVES; ++hf)
-#pragma unroll 4
-            for (int c = 0; c < 8; ++c) {
-                uint8_t* to = dst + hf * HALF + st_sw128(r, c);
-                const int64_t e = at + hf * 64 + c * 8;
-                if (!live) {
-                    *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
-                } else if (a.q_bf16 && a.q_vec) {
-                    st_cp_async16(smem_u32(to), (const bf16*)a.q + e);
-                } else {
-                    float x[8];
-                    if (a.q_vec) {
-                        const float4 x0 = *reinterpret_cast<const float4*>((const float*)a.q + e);
-                        const float4 x1 = *reinterpret_cast<const float4*>((const float*)a.q + e + 4);
-                        x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
-                        x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
-                    } else {
+            for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = load_q(a, e + j);
-                    }
-                    *reinterpret_cast<uint4*>(to) = make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]),
-                                                               st_pack(x[4], x[5]), st_pack(x[6], x[7]));
-                }
+                for (int c = 0; c < 8; ++c)
+                    st_cp_async16(to + hf * HALF + (uint32_t)((c ^ (r & 7)) << 4), src + hf * 64 + c * 8, live);
+            return;
+        }
+#pragma unroll 1
+        for (int e = 0; e < DH; e += 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+            if (live && a.q_vec) {
+                const float4 x0 = *reinterpret_cast<const float4*>((const float*)a.q + at + e);
+                const float4 x1 = *reinterpret_cast<const float4*>((const float*)a.q + at + e + 4);
+                x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
+                x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
+            } else if (live) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = load_q(a, at + e + j);
             }
+            *reinterpret_cast<uint4*>(dst + (e >> 6) * HALF + (((e >> 3 & 7) ^ (r & 7)) << 4)) =
+                make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]), st_pack(x[4], x[5]), st_pack(x[6], x[7]));
+        }
     };
     auto staged = [&]() {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -854,55 +858,69 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
         pdl_trigger();
         // the runs that a segment's nt tiles from position at on meet
         auto runs = [&](int at, int nt, int W) { return (at + nt - 1) / W - at / W + 1; };
-        // the row's partials: those of the prefix, then those of the own rows
-        const float *sh_o = nullptr, *own_o = nullptr;
-        const float2 *sh_ml = nullptr, *own_ml = nullptr;
-        int sh_used = 0, own_used = 0;
-        if (live && a.P > 0) {
-            const int r = (int)(m * grp + hg), t = r / a.sh_rows, in = r - t * a.sh_rows;
-            const int seg = g * a.sh_tiles + t, nt = (a.P + 127) / 128;
-            sh_ml = a.sh_ml + (int64_t)seg * a.sh_slots * a.sh_rows + in;
-            sh_o = a.sh_o + ((int64_t)seg * a.sh_slots * DH + c4 * 4) * rows4(a.sh_rows) + in * 4;
-            sh_used = a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots;
-        }
-        if (live && own > 0) {
-            const int t = r_own / a.own_rows, in = r_own - t * a.own_rows, in_b = g * a.own_tiles + t, per_b = a.G * a.own_tiles;
-            const int64_t seg = (int64_t)b * per_b + in_b;
-            own_ml = a.own_ml + seg * a.own_slots * a.own_rows + in;
-            own_o = a.own_o + (seg * a.own_slots * DH + c4 * 4) * rows4(a.own_rows) + in * 4;
-            own_used = a.own_slots;
-            if (a.tensor) {
-                const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
-                own_used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
-            }
-        }
+        // The row's partials: those of the prefix, dealt among the groups but the last, and those of
+        // the own rows, the last group's
         constexpr int PB = 8;                      // in flight
-        for (int s0 = part_of; s0 < sh_used + own_used; s0 += PB * parts) {
-            float2 ml[PB];
-            float4 os[PB];
-#pragma unroll
-            for (int j = 0; j < PB; ++j) {
-                const int s = s0 + j * parts, so = s - sh_used;
-                const bool sh = so < 0;
-                ml[j] = make_float2(-INFINITY, 0.f);
-                os[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (s < sh_used + own_used) {
-                    ml[j] = sh ? sh_ml[(int64_t)s * a.sh_rows] : own_ml[(int64_t)so * a.own_rows];
-                    os[j] = *reinterpret_cast<const float4*>(sh ? sh_o + (int64_t)s * DH * rows4(a.sh_rows)
-                                                                : own_o + (int64_t)so * DH * rows4(a.own_rows));
+        const int dealt = max(1, parts - 1);
+#pragma unroll 1
+        for (int kind = part_of < dealt ? 0 : 1; kind < (part_of == parts - 1 ? 2 : 1); ++kind) {
+            const float* o_at;
+            const float2* ml_at;
+            int rows_seg, s = 0, step = 1, used = 0;
+            if (kind == 0) {
+                if (!live || a.P == 0) continue;
+                const int r = (int)(m * grp + hg), t = r / a.sh_rows, in = r - t * a.sh_rows;
+                const int seg = g * a.sh_tiles + t, nt = (a.P + 127) / 128;
+                rows_seg = a.sh_rows;
+                s = part_of;
+                step = dealt;
+                ml_at = a.sh_ml + (int64_t)seg * a.sh_slots * rows_seg + in;
+                o_at = a.sh_o + ((int64_t)seg * a.sh_slots * DH + c4 * 4) * rows4(rows_seg) + in * 4;
+                used = a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots;
+            } else {
+                if (!live || own == 0) continue;
+                const int t = r_own / a.own_rows, in = r_own - t * a.own_rows, in_b = g * a.own_tiles + t;
+                const int per_b = a.G * a.own_tiles;
+                const int64_t seg = (int64_t)b * per_b + in_b;
+                rows_seg = a.own_rows;
+                ml_at = a.own_ml + seg * a.own_slots * rows_seg + in;
+                o_at = a.own_o + (seg * a.own_slots * DH + c4 * 4) * rows4(rows_seg) + in * 4;
+                used = a.own_slots;
+                if (a.tensor) {
+                    const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
+                    used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
                 }
             }
-            float mb = -INFINITY;
+            const int64_t ml_step = (int64_t)step * rows_seg, o_step = (int64_t)step * DH * rows4(rows_seg);
+            ml_at += (int64_t)s * rows_seg;
+            o_at += (int64_t)s * DH * rows4(rows_seg);
+#pragma unroll 1
+            for (; s < used; s += PB * step) {
+                float2 ml[PB];
+                float4 os[PB];
 #pragma unroll
-            for (int j = 0; j < PB; ++j) mb = fmaxf(mb, ml[j].x);
-            rebase(mb);
+                for (int j = 0; j < PB; ++j) {
+                    ml[j] = make_float2(-INFINITY, 0.f);
+                    os[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (s + j * step < used) {
+                        ml[j] = *ml_at;
+                        os[j] = *reinterpret_cast<const float4*>(o_at);
+                    }
+                    ml_at += ml_step;
+                    o_at += o_step;
+                }
+                float mb = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < PB; ++j) {
-                // an empty partial leaves its o unwritten (one of NaN scores has l = NaN)
-                if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
-                const float w = exp_of<T>(ml[j].x - M);
-                L = fmaf(ml[j].y, w, L);
-                add(w, os[j]);
+                for (int j = 0; j < PB; ++j) mb = fmaxf(mb, ml[j].x);
+                rebase(mb);
+#pragma unroll
+                for (int j = 0; j < PB; ++j) {
+                    // an empty partial leaves its o unwritten (one of NaN scores has l = NaN)
+                    if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
+                    const float w = exp_of<T>(ml[j].x - M);
+                    L = fmaf(ml[j].y, w, L);
+                    add(w, os[j]);
+                }
             }
         }
     }
@@ -1119,9 +1137,10 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     if (e != cudaSuccess) return e;
     const int rw = 512 / c.head_dim;
     const dim3 grid(c.batch, c.kv_heads, (c.n_cand * c.block * (c.heads / c.kv_heads) + rw - 1) / rw);
-    // groups: one for eight partials of a row, which it loads at once, while all of them run at once
+    // groups: one for eight partials of a row's prefix, which it loads at once, and one for its own, as
+    // many as all run at once
     const long long most = 4 * 152 / ((long long)grid.x * grid.y * grid.z);
-    int groups = ((a.P > 0 ? a.sh_slots : 0) + (a.own_max > 0 ? a.own_slots : 0) + 7) / 8;
+    int groups = ((a.P > 0 ? a.sh_slots : 0) + 7) / 8 + (a.own_max > 0);
     groups = groups < most ? groups : (int)most;
     groups = groups < 1 ? 1 : groups > SC_GROUPS ? SC_GROUPS : groups;
     auto combine = [&](auto kernel) { return launch_s(stream, kernel, grid, dim3(128 * groups), 0, a); };
