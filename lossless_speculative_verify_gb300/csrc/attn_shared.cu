@@ -276,12 +276,13 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     int* len = pre + a.B + 1;                                  // [B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    pdl_wait();
+    pdl_trigger();                // the combine may begin: all before this kernel is done
+    // not before the wait: a predecessor's CTA on this SM may have yet to allocate
     if (warp == 8) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    pdl_wait();
-    pdl_trigger();                // the combine may begin: all before this kernel is done
     for (int b = tid; b < a.B; b += ST_THREADS) len[b] = own_rows_of(a, b, blockIdx.x == 0);
     __syncthreads();
     if (warp == 0) {

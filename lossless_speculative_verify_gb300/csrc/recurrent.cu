@@ -253,14 +253,15 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
     pdl_trigger();
 }
 
-// Runs: as many as run at once, seven CTAs an SM over all sequences, at least 16 positions each.
+// Runs: as many as run at once, seven CTAs an SM over all sequences, at least 16
+// positions each: only the first run then reads the old tail, which its thread may overwrite.
 template <typename T, int LMAX, int VEC>
 void conv_launch(ConvArgs a, int B, cudaStream_t s) {
     const int cols = (a.D + VEC * CONV_THREADS - 1) / (VEC * CONV_THREADS);
     int runs = 1;
     if (a.y) {
         const long long want = 7 * 152 / ((long long)cols * B);
-        const long long most = (a.T + 15) / 16;
+        const long long most = a.T / 16;
         runs = want < 1 || most < 1 ? 1 : (int)(want < most ? want : most);
         a.run = (a.T + runs - 1) / runs;
         runs = (a.T + a.run - 1) / a.run;

@@ -569,6 +569,18 @@ def test_conv_in_pieces_is_the_same(evs):
     assert torch.equal(pre[0], x[0, 48:51].float()) and torch.equal(pre[1], x[1, 53:56].float())
 
 
+@pytest.mark.parametrize("T", [17, 29, 31, 33, 47, 200])
+def test_conv_tail_in_place_with_long_taps(evs, T):
+    """A run of positions may reach no further back than the one before it: the old tail is overwritten meanwhile."""
+    g = gen(T)
+    x, w, tail = randn(g, 2, T, 4096, dtype=BF16), randn(g, 4096, 16), randn(g, 2, 15, 4096)
+    apart = torch.empty_like(tail)
+    want = evs.causal_conv(x, w, tail=tail, tail_out=apart)
+    for _ in range(5):
+        carried = tail.clone()
+        assert torch.equal(evs.causal_conv(x, w, tail=carried, tail_out=carried), want) and torch.equal(carried, apart)
+
+
 def test_conv_strides_and_lengths(evs):
     g = gen(32)
     B, T, D = 3, 50, 96
