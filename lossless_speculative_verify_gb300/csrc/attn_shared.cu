@@ -758,8 +758,8 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
     }
     const int tid = threadIdx.x & 127, part_of = threadIdx.x >> 7, parts = blockDim.x >> 7, warp = tid >> 5;
     const int grp = a.H / a.G, rows = a.C * a.T * grp;
-    const int b = blockIdx.x, g = blockIdx.y, row = tid % RW, c4 = tid / RW;
-    const int r_own = blockIdx.z * RW + row;
+    const int b = blockIdx.z, g = blockIdx.y, row = tid % RW, c4 = tid / RW;
+    const int r_own = blockIdx.x * RW + row;
     const bool live = r_own < rows;
     const int ci = (live ? r_own : rows - 1) / grp, hg = (live ? r_own : rows - 1) - ci * grp;   // (c, i), head
     const int c = ci / a.T, i = ci - c * a.T;
@@ -1137,7 +1137,7 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
                  : launch_s(stream, shared_simt_kernel<float>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items);
     if (e != cudaSuccess) return e;
     const int rw = 512 / c.head_dim;
-    const dim3 grid(c.batch, c.kv_heads, (c.n_cand * c.block * (c.heads / c.kv_heads) + rw - 1) / rw);
+    const dim3 grid((c.n_cand * c.block * (c.heads / c.kv_heads) + rw - 1) / rw, c.kv_heads, c.batch);   // y and z end at 65535
     // groups: one for eight partials of a row's prefix, which it loads at once, and one for its own, as
     // many as all run at once
     const long long most = 4 * 152 / ((long long)grid.x * grid.y * grid.z);

@@ -277,6 +277,29 @@ def test_attention_captured_and_on_another_stream(evs):
     check_attn(big, outs[0], BF16)
 
 
+def test_attention_many_rows_of_a_head(evs):
+    """64 candidates x 128 positions x 32 heads of one K/V head: 65536 groups of four rows to combine."""
+    g = gen(77)
+    C, T, H, dh = 64, 128, 32, 128
+    q = randn(g, 1, C, T, H, dh, dtype=BF16)
+    kp, vp = (randn(g, 1, 200, dh, dtype=BF16) for _ in range(2))
+    ko, vo = (randn(g, 1, 1, 8, dh, dtype=BF16) for _ in range(2))
+    kb, vb = (randn(g, 1, C, 1, T, dh, dtype=BF16) for _ in range(2))
+    own = torch.tensor([5], dtype=torch.int32, device="cuda")
+    out, lse = evs.shared_prefix_attention(q, kp, vp, ko, vo, own, kb, vb, return_lse=True)
+    for c, t, h in ((0, 0, 0), (0, 127, 31), (31, 64, 7), (63, 0, 31), (63, 127, 31)):
+        k = torch.cat([kp[0], ko[0, 0, :5], kb[0, c, 0, :t + 1]]).double()
+        v = torch.cat([vp[0], vo[0, 0, :5], vb[0, c, 0, :t + 1]]).double()
+        s = (k @ q[0, c, t, h].double()) / math.sqrt(dh)
+        p = torch.softmax(s, 0)
+        # as in check_attn
+        qk = float((k.abs() @ q[0, c, t, h].double().abs()).max()) / math.sqrt(dh)
+        soft = U * ((dh + 4) * qk + len(k) + 128)
+        tol = (2 * soft + BF) * (p @ v.abs()) + BF * (p @ v).abs()
+        assert torch.all((out[0, c, t, h].double() - p @ v).abs() <= tol)
+        assert abs(float(lse[0, c, t, h]) - float(torch.logsumexp(s, 0))) <= 2 * soft + 4 * U * 16
+
+
 def test_attention_refusals(evs):
     d = make_attn(15, BF16, 2, 1, 2, 4, 2, 64, 20, 10, [1, 2])
     for bad in (dict(q=d["q"].half()), dict(q=d["q"][..., :32]), dict(kp=d["kp"].float()), dict(vp=d["vp"][:, :10]),
