@@ -186,12 +186,16 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
     return y
 
 
-def _kv(name, t, dtype, shape, dev):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
-        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
-    st = t.stride()
+def _kv(name, k, v, dtype, shape, dev):
+    """Strides of K and V of one kind, which are alike."""
+    for which, t in (("k_", k), ("v_", v)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+            raise ValueError(f"{which}{name}: want {dtype} {tuple(shape)} on {dev}")
+    st = k.stride()
     if st[-1] != 1:
-        raise ValueError(f"{name}: the head dimension has to be contiguous")
+        raise ValueError(f"k_{name}: the head dimension has to be contiguous")
+    if v.stride() != st:
+        raise ValueError(f"k_{name} and v_{name}: want equal strides")
     return st
 
 
@@ -232,14 +236,11 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     _need(1 <= Cn <= 64 and 1 <= T <= 128 and B <= 1024, "at most 1024 sequences, 64 candidates, 128 block positions")
     _need(isinstance(k_own, torch.Tensor) and k_own.dim() == 4, "k_own: want [batch, kv_heads, capacity, dh]")
     S = k_own.shape[2]
-    ps = _kv("k_prefix", k_prefix, dt, (G, P, dh), dev)
-    os_ = _kv("k_own", k_own, dt, (B, G, S, dh), dev)
-    _need(ps == _kv("v_prefix", v_prefix, dt, (G, P, dh), dev) and os_ == _kv("v_own", v_own, dt, (B, G, S, dh), dev),
-          "K and V: want equal strides")
+    ps = _kv("prefix", k_prefix, v_prefix, dt, (G, P, dh), dev)
+    os_ = _kv("own", k_own, v_own, dt, (B, G, S, dh), dev)
     _need((k_block is None) == (v_block is None), "k_block and v_block go together")
     if k_block is not None:
-        bs = _kv("k_block", k_block, dt, (B, Cn, G, T, dh), dev)
-        _need(bs == _kv("v_block", v_block, dt, (B, Cn, G, T, dh), dev), "K and V: want equal strides")
+        bs = _kv("block", k_block, v_block, dt, (B, Cn, G, T, dh), dev)
         _need(Cn == 1 or B == 1 or bs[0] == Cn * bs[1], "k_block: sequences and candidates have to be evenly spaced")
         b_row, b_head, b_cand = (bs[3] if T > 1 else dh), bs[2], bs[1] if Cn > 1 else bs[0]
     else:
@@ -247,8 +248,10 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
         b_row = b_head = b_cand = 0
 
     q_ld = _flat("q", q, q.dtype, (B, Cn, T, H, dh), dev)
-    o = torch.empty(B, Cn, T, H, dh, dtype=dt, device=dev) if out is None else out
-    o_ld = _flat("out", o, dt, (B, Cn, T, H, dh), dev)
+    if out is not None:
+        o, o_ld = out, _flat("out", out, dt, (B, Cn, T, H, dh), dev)
+    else:
+        o, o_ld = torch.empty(B, Cn, T, H, dh, dtype=dt, device=dev), H * dh
     _need(scale is None or scale > 0.0, "scale: above zero")
     lse = torch.empty(B, Cn, T, H, dtype=torch.float32, device=dev) if return_lse else None
     a = L.SharedAttnArgs(B, Cn, T, H, G, dh, _DT[dt], _DT[q.dtype], P, S, 0, 0.0 if scale is None else scale,
