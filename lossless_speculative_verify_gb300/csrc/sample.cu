@@ -302,12 +302,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     __shared__ u64 warp_mass[THREADS / 32];
     __shared__ float x_max[SMP_MAX_CS];
     __shared__ u64 x_cnt[SMP_MAX_CS], x_sum[SMP_MAX_CS], x_arg[SMP_MAX_CS];
-    __shared__ u64 f_above, f_cut, last_o, pick_before;
+    __shared__ u64 f_above, f_cut, last_o;
     __shared__ u64 piv_o[THREADS / 32], piv_w[THREADS / 32];
     __shared__ int piv_c[THREADS / 32];
     __shared__ uint32_t piv_n;
     __shared__ uint32_t f_bin, f_count, list_n[2], own_n[2], own_at;
-    __shared__ int pick_warp, last_kept;
+    __shared__ int last_kept;
     __shared__ struct {
         u64 p64, u64_, mp;
         float c_hi, c_lo, temp;
@@ -830,14 +830,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     // cumulative mass > u * total: integers, so > its floor
     const u64 thr = __umul64hi(par.u64_, total);
     if (before <= thr && thr < before + mine) {
-        if (tid == 0) {
-            u64 c = before;
-            int w = 0;
-            while (w < THREADS / 32 - 1 && c + warp_mass[w] <= thr) c += warp_mass[w++];
-            pick_warp = w;
-            pick_before = c;
+        // the first warp whose tokens reach past it
+        const u64 in_warp = lane < THREADS / 32 ? warp_mass[lane] : 0;
+        u64 upto = in_warp;
+#pragma unroll
+        for (int o = 1; o < THREADS / 32; o *= 2) {
+            const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        __syncthreads();
+        const int pick_warp = __ffs(__ballot_sync(0xffffffffu, lane < THREADS / 32 && before + upto > thr)) - 1;
+        const u64 pick_before = before + __shfl_sync(0xffffffffu, upto - in_warp, pick_warp);
         // the warp's slots, dealt out to the whole CTA in order
         const int lo = pick_warp * seg, hi = min(n, lo + seg), per = (seg + THREADS - 1) / THREADS;
         u64 m = 0;
@@ -867,21 +869,32 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     if (a.probs) {
         const float inv = (float)(1ull << SMP_FRAC) / (float)total;
         float* pr = a.probs + (size_t)row * a.ldp;
-        for (int s = tid; s < n; s += 2 * THREADS) {
-            const int s1 = s + THREADS;
-            const float l0 = l_s[s], l1 = s1 < n ? l_s[s1] : -INFINITY;
-            const bool in0 = above_cut(l0, base + s), in1 = above_cut(l1, base + s1);
-            float p0 = 0.f, p1 = 0.f;
-            if (in0 || in1) {
-                const Parts w = wf.parts(l0, l1);
-                if (in0 && (mp == 0 || wf.scaled(w.i0, w.p.x, w.q.x, w.rest.x) >= mp))
-                    p0 = real_weight(w.i0, w.p.x, w.q.x, w.rest.x, pow2) * inv;
-                if (in1 && (mp == 0 || wf.scaled(w.i1, w.p.y, w.q.y, w.rest.y) >= mp))
-                    p1 = real_weight(w.i1, w.p.y, w.q.y, w.rest.y, pow2) * inv;
+        const bool wide = (uintptr_t)(pr + base) % 16 == 0;
+        for (int s = 4 * tid; s < n; s += 4 * THREADS) {
+            const float4 l4 = *reinterpret_cast<const float4*>(l_s + s);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+            const int id = base + s;
+            bool in[4];
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) in[j] = above_cut(l[j], id + j);
+            if (in[0] || in[1] || in[2] || in[3]) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    const Parts w = wf.parts(l[j], l[j + 1]);
+                    if (in[j] && (mp == 0 || wf.scaled(w.i0, w.p.x, w.q.x, w.rest.x) >= mp))
+                        p[j] = real_weight(w.i0, w.p.x, w.q.x, w.rest.x, pow2) * inv;
+                    if (in[j + 1] && (mp == 0 || wf.scaled(w.i1, w.p.y, w.q.y, w.rest.y) >= mp))
+                        p[j + 1] = real_weight(w.i1, w.p.y, w.q.y, w.rest.y, pow2) * inv;
+                }
             }
-            const int id = base + s, id1 = base + s1;
-            if (id >= 0 && id < a.V) pr[id] = p0;
-            if (s1 < n && id1 < a.V) pr[id1] = p1;
+            if (wide && id >= 0 && id + 4 <= a.V) {
+                *reinterpret_cast<float4*>(pr + id) = make_float4(p[0], p[1], p[2], p[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (id + j >= 0 && id + j < a.V) pr[id + j] = p[j];
+            }
         }
     }
 }

@@ -5,8 +5,9 @@ Each function checks its arguments, fills the argument struct of one entry point
 states the mathematics) and enqueues it on the current stream of the tensors' device, like any
 torch operator: outputs and workspaces come from torch's allocator, calls may be captured into
 CUDA graphs, nothing synchronises. Inputs that are not what an operator takes raise ValueError
-before anything is enqueued. ``flags`` is an int32 tensor of one element that collects
-EVS_FLAG_* bits.
+before anything is enqueued. Outputs share no memory with inputs, but for the state or tail that
+is carried in place. There are no gradients: a first argument that asks for one is refused.
+``flags`` is an int32 tensor of one element that collects EVS_FLAG_* bits.
 """
 from __future__ import annotations
 
@@ -68,7 +69,10 @@ def _enqueue(fn, where, args, dev):
 
 
 def _device(name, t):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: want a CUDA tensor")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name}: want a CUDA tensor")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: this operator has no gradient")
     return t.device
 
 

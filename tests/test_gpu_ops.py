@@ -498,6 +498,17 @@ def test_sample_refusals(evs):
             evs.sample(*a, **kw)
 
 
+def test_no_gradients(evs):
+    l, u = make_logits(25, 2, 100)
+    x, w = torch.zeros(1, 4, 8, device="cuda", requires_grad=True), torch.zeros(8, 4, device="cuda")
+    with pytest.raises(ValueError, match="gradient"):
+        evs.sample(l.requires_grad_(), u)
+    with pytest.raises(ValueError, match="gradient"):
+        evs.causal_conv(x, w)
+    with torch.no_grad():
+        assert evs.sample(l, u).shape == (2,) and evs.causal_conv(x, w).shape == (1, 4, 8)
+
+
 def test_decode_filtered(evs):
     """The decode step's own path: its logits, drawn with filters; the state as after a plain step."""
     from gpu_harness import Pair
