@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 MAX_LAYERS = 64
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +73,12 @@ def _fields(text):
             for name in part.strip()[1:].split(",")]
 
 
+def _packer(fields):
+    """struct.Struct of the same layout: packing one costs a quarter of filling a ctypes structure."""
+    code = {C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_void_p: "Q", C.c_size_t: "Q"}
+    return struct.Struct("@" + "".join(code[kind] for _, kind in fields))
+
+
 class SampleArgs(C.Structure):
     _fields_ = _fields("i rows, vocab, dtype; q ld; p logits, temperature, top_k, top_p, min_p, uniforms, token, "
                        "logprob, probs; q probs_ld; p flags")
@@ -94,6 +101,14 @@ class SharedAttnArgs(C.Structure):
                        "q own_row, own_head, own_seq; p own_len, k_block, v_block; "
                        "q block_row, block_head, block_cand; p o; q o_ld; p lse, workspace; z ws_bytes; p flags")
 
+
+pack_sample = _packer(SampleArgs._fields_).pack
+pack_conv = _packer(ConvArgs._fields_).pack
+pack_scan = _packer(ScanArgs._fields_).pack
+# the shapes, which the workspace's size needs, and the rest
+pack_attn_shapes = _packer(SharedAttnArgs._fields_[:12]).pack
+pack_attn_rest = _packer(SharedAttnArgs._fields_[12:]).pack
+NO_REST = bytes(C.sizeof(SharedAttnArgs) - _packer(SharedAttnArgs._fields_[:12]).size)
 
 _lib = None
 
@@ -150,13 +165,12 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.evs_projection_noalloc.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
     lib.evs_projection_noalloc_flags.restype = C.c_int
     lib.evs_projection_noalloc_flags.argtypes = [C.POINTER(C.c_uint32), i32, vp]
-    for name, args in (("evs_sample", SampleArgs), ("evs_causal_conv", ConvArgs),
-                       ("evs_selective_scan", ScanArgs), ("evs_shared_attention", SharedAttnArgs)):
+    for name in ("evs_sample", "evs_causal_conv", "evs_selective_scan", "evs_shared_attention"):
         fn = getattr(lib, name)
         fn.restype = C.c_int
-        fn.argtypes = [C.POINTER(args), vp]
+        fn.argtypes = [vp, vp]                   # a structure by reference, or one packed into bytes
     lib.evs_shared_attention_workspace.restype = C.c_size_t
-    lib.evs_shared_attention_workspace.argtypes = [C.POINTER(SharedAttnArgs)]
+    lib.evs_shared_attention_workspace.argtypes = [vp]
     lib.evs_selective_scan_workspace.restype = C.c_size_t
     lib.evs_selective_scan_workspace.argtypes = [i32, i32, i32, i32]
     lib.evs_decode_filtered.restype = C.c_int

@@ -11,8 +11,6 @@ is carried in place. There are no gradients: a first argument that asks for one 
 """
 from __future__ import annotations
 
-import ctypes as C
-
 import torch
 
 from . import _lib as L
@@ -26,13 +24,13 @@ def _need(ok, what):
 
 
 def _p(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _vec(name, t, dtype, shape, dev):
-    """Address of a contiguous tensor of the given type and shape on dev, or None."""
+    """Address of a contiguous tensor of the given type and shape on dev, or 0."""
     if t is None:
-        return None
+        return 0
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
             t.device == dev):
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}")
@@ -60,10 +58,10 @@ def _enqueue(fn, where, args, dev):
     # (the stream object that torch.cuda.current_stream builds costs 2 us a call)
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        st = fn(C.byref(args), stream)
+        st = fn(args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(C.byref(args), stream)
+            st = fn(args, stream)
     if st:
         L.check(st, where)
 
@@ -88,7 +86,7 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
     dev = _device("logits", logits)
     _need(logits.dim() == 2 and logits.dtype in _DT, "logits: want fp32 or bf16 [rows, vocab]")
     R, V = logits.shape
-    _need(1 <= V <= 1 << 18, "logits: vocabulary of 1 to 262144")
+    _need(1 <= V <= 1 << 18 and R <= 1 << 24, "logits: vocabulary of 1 to 262144, at most 2**24 rows")
     _need(logits.stride(1) == 1 or V == 1, "logits: the vocabulary has to be contiguous")
     ld = logits.stride(0) if R > 1 else V
     _need(ld >= V, "logits: rows overlap")
@@ -97,7 +95,7 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
     logprob = torch.empty(R, dtype=torch.float32, device=dev) if return_logprob else None
     probs = torch.empty(R, V, dtype=torch.float32, device=dev) if return_probs else None
     f32 = torch.float32
-    a = L.SampleArgs(R, V, _DT[logits.dtype], ld, logits.data_ptr(), _vec("temperature", temperature, f32, (R,), dev),
+    a = L.pack_sample(R, V, _DT[logits.dtype], ld, logits.data_ptr(), _vec("temperature", temperature, f32, (R,), dev),
                      _vec("top_k", top_k, torch.int32, (R,), dev), _vec("top_p", top_p, f32, (R,), dev),
                      _vec("min_p", min_p, f32, (R,), dev), _vec("uniforms", uniforms, f32, (R,), dev),
                      _vec("out", token, torch.int32, (R,), dev), _p(logprob), _p(probs), V,
@@ -120,6 +118,7 @@ def causal_conv(x, weight, bias=None, *, tail=None, tail_out=None, lens=None, si
     dev = _device("x", x)
     _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
     B, T, D = x.shape
+    _need(B <= 65535 and T <= 1 << 30 and D <= 1 << 24, "x: at most 65535 x 2**30 x 2**24")
     _need(isinstance(weight, torch.Tensor) and weight.dim() == 2 and 2 <= weight.shape[1] <= 16,
           "weight: want [width, 2..16]")
     taps = weight.shape[1]
@@ -133,7 +132,7 @@ def causal_conv(x, weight, bias=None, *, tail=None, tail_out=None, lens=None, si
     else:
         _need(out is None and tail_out is not None, "output=False wants tail_out and no out")
     f32 = torch.float32
-    a = L.ConvArgs(B, T, D, taps, _DT[x.dtype], 1 if silu else 0, x.data_ptr(), x_ld, x_sq, _p(y), y_ld, y_sq,
+    a = L.pack_conv(B, T, D, taps, _DT[x.dtype], 1 if silu else 0, x.data_ptr(), x_ld, x_sq, _p(y), y_ld, y_sq,
                    _vec("weight", weight, f32, (D, taps), dev), _vec("bias", bias, f32, (D,), dev),
                    _vec("tail", tail, f32, (B, taps - 1, D), dev),
                    _vec("tail_out", tail_out, f32, (B, taps - 1, D), dev),
@@ -154,6 +153,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
     dev = _device("x", x)
     _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
     Bn, T, W = x.shape
+    _need(Bn <= 65535 and T <= 1 << 30 and W <= 1 << 24, "x: at most 65535 x 2**30 x 2**24")
     _need(isinstance(A, torch.Tensor) and A.dim() == 2 and A.shape[1] in (4, 8, 16, 32), "A: want [width, 4|8|16|32]")
     N = A.shape[1]
     x_ld, x_sq = _rows3("x", x, x.dtype, (Bn, T, W), dev)
@@ -166,26 +166,24 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
     if output:
         y = torch.empty(Bn, T, W, dtype=x.dtype, device=dev) if out is None else out
         y_ld, y_sq = _rows3("out", y, x.dtype, (Bn, T, W), dev, written=True)
-        for name, t in (("x", x), ("dt", dt), ("z", z)):
-            _need(t is None or y.data_ptr() != t.data_ptr() or y.numel() == 0, f"out: may not be {name}")
+        if y.data_ptr() in (x.data_ptr(), dt.data_ptr(), _p(z)) and y.numel() > 0:
+            raise ValueError("out: may not be x, dt or z")
     else:
         _need(out is None and state_out is not None, "output=False wants state_out and no out")
     f32 = torch.float32
-    for name, t in (("A", A), ("state", state), ("state_out", state_out)):
-        _need(t is None or t.data_ptr() % 16 == 0, f"{name}: has to start on 16 bytes")
-    a = L.ScanArgs(Bn, T, W, N, _DT[x.dtype], 1 if softplus else 0, x.data_ptr(), x_ld, x_sq, dt.data_ptr(), dt_ld,
-                   dt_sq, _p(z), z_ld, z_sq, B.data_ptr(), b_ld, b_sq, C.data_ptr(), c_ld, c_sq, _p(y), y_ld, y_sq,
-                   _vec("A", A, f32, (W, N), dev), _vec("D", D, f32, (W,), dev),
-                   _vec("dt_bias", dt_bias, f32, (W,), dev), _vec("state", state, f32, (Bn, W, N), dev),
-                   _vec("state_out", state_out, f32, (Bn, W, N), dev),
-                   _vec("lens", lens, torch.int32, (Bn,), dev), _vec("flags", flags, torch.int32, (1,), dev))
+    if (A.data_ptr() | _p(state) | _p(state_out)) % 16:
+        raise ValueError("A, state and state_out have to start on 16 bytes")
+    lib = L.load()
+    n = lib.evs_selective_scan_workspace(Bn, T, W, N)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    a = L.pack_scan(Bn, T, W, N, _DT[x.dtype], 1 if softplus else 0, x.data_ptr(), x_ld, x_sq, dt.data_ptr(), dt_ld,
+                    dt_sq, _p(z), z_ld, z_sq, B.data_ptr(), b_ld, b_sq, C.data_ptr(), c_ld, c_sq, _p(y), y_ld, y_sq,
+                    _vec("A", A, f32, (W, N), dev), _vec("D", D, f32, (W,), dev),
+                    _vec("dt_bias", dt_bias, f32, (W,), dev), _vec("state", state, f32, (Bn, W, N), dev),
+                    _vec("state_out", state_out, f32, (Bn, W, N), dev), _vec("lens", lens, torch.int32, (Bn,), dev),
+                    _vec("flags", flags, torch.int32, (1,), dev), _p(ws), n)
     if (T == 0 or Bn == 0) and state_out is None:
         return y
-    lib = L.load()
-    n = int(lib.evs_selective_scan_workspace(Bn, T, W, N))
-    if n:
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        a.workspace, a.ws_bytes = ws.data_ptr(), n
     _enqueue(lib.evs_selective_scan, "evs_selective_scan", a, dev)
     return y
 
@@ -240,6 +238,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     _need(1 <= Cn <= 64 and 1 <= T <= 128 and B <= 1024, "at most 1024 sequences, 64 candidates, 128 block positions")
     _need(isinstance(k_own, torch.Tensor) and k_own.dim() == 4, "k_own: want [batch, kv_heads, capacity, dh]")
     S = k_own.shape[2]
+    _need(H <= 1024 and P <= 1 << 30 and S <= 1 << 30, "at most 1024 heads and 2**30 rows")
     ps = _kv("prefix", k_prefix, v_prefix, dt, (G, P, dh), dev)
     os_ = _kv("own", k_own, v_own, dt, (B, G, S, dh), dev)
     _need((k_block is None) == (v_block is None), "k_block and v_block go together")
@@ -257,18 +256,19 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     else:
         o, o_ld = torch.empty(B, Cn, T, H, dh, dtype=dt, device=dev), H * dh
     _need(scale is None or scale > 0.0, "scale: above zero")
-    lse = torch.empty(B, Cn, T, H, dtype=torch.float32, device=dev) if return_lse else None
-    a = L.SharedAttnArgs(B, Cn, T, H, G, dh, _DT[dt], _DT[q.dtype], P, S, 0, 0.0 if scale is None else scale,
-                         q.data_ptr(), q_ld, k_prefix.data_ptr(), v_prefix.data_ptr(), ps[1] if P > 1 else dh, ps[0],
-                         k_own.data_ptr(), v_own.data_ptr(), os_[2] if S > 1 else dh, os_[1], os_[0],
-                         _vec("own_len", own_len, torch.int32, (B,), dev), _p(k_block), _p(v_block), b_row, b_head,
-                         b_cand, o.data_ptr(), o_ld, _p(lse), None, 0, _vec("flags", flags, torch.int32, (1,), dev))
     _need(own_len is not None, "own_len: missing")
+    lengths = _vec("own_len", own_len, torch.int32, (B,), dev)
+    flag = _vec("flags", flags, torch.int32, (1,), dev)
+    lse = torch.empty(B, Cn, T, H, dtype=torch.float32, device=dev) if return_lse else None
     if B > 0:
         lib = L.load()
-        n = int(lib.evs_shared_attention_workspace(C.byref(a)))
+        shapes = L.pack_attn_shapes(B, Cn, T, H, G, dh, _DT[dt], _DT[q.dtype], P, S, 0, 0.0 if scale is None else scale)
+        n = lib.evs_shared_attention_workspace(shapes + L.NO_REST)
         _need(n > 0, "sizes that the operator does not take")
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        a.workspace, a.ws_bytes = ws.data_ptr(), n
+        a = shapes + L.pack_attn_rest(
+            q.data_ptr(), q_ld, k_prefix.data_ptr(), v_prefix.data_ptr(), ps[1] if P > 1 else dh, ps[0],
+            k_own.data_ptr(), v_own.data_ptr(), os_[2] if S > 1 else dh, os_[1], os_[0], lengths, _p(k_block),
+            _p(v_block), b_row, b_head, b_cand, o.data_ptr(), o_ld, _p(lse), ws.data_ptr(), n, flag)
         _enqueue(lib.evs_shared_attention, "evs_shared_attention", a, dev)
     return o if lse is None else [o, lse]
