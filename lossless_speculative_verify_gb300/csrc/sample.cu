@@ -244,11 +244,15 @@ struct WeightFn {
         fixed2(l, l, w0, w1);
         return w0;
     }
+    // p + 1.5 * 2^18 for two
+    __device__ __forceinline__ u64 step(float l0, float l1) const {
+        return add2(mul2(add2(pk(l0, l1), pk(-M)), pk(c_hi)), pk(kRound));
+    }
     // Which step of 1/32 of the exponent: bins that ascend as the logit falls
-    __device__ __forceinline__ int bin(int i, float p) const { return p > -63.9f ? -i : SMP_BINS - 1; }
-    __device__ __forceinline__ int bin(float l) const {
-        const float p = (l - M) * c_hi;
-        return bin(__float_as_int(p + kRound) - __float_as_int(kRound), p);
+    // (far from M the integer is no multiple of anything, but larger all the same)
+    static __device__ __forceinline__ int bin(int i) { return (int)min((unsigned)-i, (unsigned)SMP_BINS - 1u); }
+    __device__ __forceinline__ int bin(float l) const {   // the product rounded before the sum, as there
+        return bin(__float_as_int(__fadd_rn(__fmul_rn(l - M, c_hi), kRound)) - __float_as_int(kRound));
     }
     // The mass of a bin whose tokens' 1 + q + rest sum to s 2^-33
     __device__ __forceinline__ u64 mass(int b, u64 s) const {
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
         // log2(e) / T, the quotient's remainder by a fused multiply-add
         const float L2E = 1.44269502162933349609375f, L2E_lo = 1.9259629911266175e-8f, t = greedy ? 1.f : temp;
         const float c = L2E / t, left = fmaf(-c, t, L2E) + L2E_lo;
-        par.c_hi = fminf(c, FLT_MAX);         // where 1 / T overflows
+        par.c_hi = fminf(fmaxf(c, 1.4e-45f), FLT_MAX);   // finite, and no 0 to meet an infinite difference
         par.c_lo = c <= FLT_MAX && isfinite(left) ? left / t : 0.f;
         par.temp = t;
         par.greedy = greedy;
@@ -472,8 +476,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                             atomicAdd(&hist[b], (uint32_t)x & 0x1ffffu);
                             atomicAdd(&hist[SMP_BINS + b], (uint32_t)((x >> 17) + 65536));
                         };
-                        const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(w.i0, w.p.x)) : -1;
-                        const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(w.i1, w.p.y)) : -1;
+                        const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(w.i0)) : -1;
+                        const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(w.i1)) : -1;
                         if (b0 >= 0) add(b0, w.p.x, w.q.x, w.rest.x);
                         if (b1 >= 0) add(b1, w.p.y, w.q.y, w.rest.y);
                     }
@@ -684,17 +688,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     };
     // Collects the orders of the tokens that `take` names, a warp's share by one counter update, and
     // in a cluster a CTA's share by one more.
-    auto gather = [&](auto take) {
+    auto gather = [&](int first_bin, int last_bin, auto take) {
+        const float highest = kRound - (float)first_bin * 0.03125f;
+        const float lowest = last_bin < SMP_BINS - 1 ? kRound - (float)last_bin * 0.03125f : -INFINITY;
         uint32_t* count = CLUSTER ? &own_n[list_at] : &list_n[list_at];
         for (int s0 = 0; s0 < n; s0 += 4 * THREADS) {
             const int s = s0 + 4 * tid;
             const float4 l4 = s < n ? *reinterpret_cast<const float4*>(l_s + s)
                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+            // the rounding that WeightFn::bin does, two at a time
+            const float2 a01 = unpk(wf.step(l4.x, l4.y)), a23 = unpk(wf.step(l4.z, l4.w));
+            const float at_step[4] = {a01.x, a01.y, a23.x, a23.y};
             bool yes[4], mine = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                yes[j] = l[j] > -INFINITY && take(l[j], base + s + j);
+                yes[j] = at_step[j] >= lowest && at_step[j] <= highest && l[j] > -INFINITY && take(l[j], base + s + j);
                 mine |= yes[j];
             }
             if (!__any_sync(0xffffffffu, mine)) continue;
@@ -756,20 +765,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             const Found f = search((uint32_t)k_in, 0, x);
             if (f.bin0 < SMP_BINS) {
                 const bool all = f.shift == SMP_ORDER_BITS && f.above + f.count <= SMP_CAP;
-                gather([&](float l, int id) {
-                    const int b = wf.bin(l);
-                    return all ? b <= f.bin0 : b == f.bin0 && in_found(f, b, order_of(l, id));
-                });
+                gather(all ? 0 : f.bin0, f.bin0, [&](float l, int id) { return all || in_found(f, f.bin0, order_of(l, id)); });
                 set_cut(finish(all ? 0 : f.above, 0, (uint32_t)k_in, need_p && all, p64, 0));
                 if (all) p_left = false;
             }
         }
         if (p_left) {
             const Found f = search(0, p64, x);
-            gather([&](float l, int id) {
-                const int b = wf.bin(l);
-                return b == f.bin0 && above_cut(l, id) && in_found(f, b, order_of(l, id));
-            });
+            gather(f.bin0, f.bin0, [&](float l, int id) { return above_cut(l, id) && in_found(f, f.bin0, order_of(l, id)); });
             set_cut(finish(0, f.above, 0, true, p64, x));
         }
     }

@@ -377,6 +377,15 @@ def test_sample_rows(evs, R):
         check_draw(evs, l, u, probs=False, top_p=col(R, 0.95), top_k=col(R, 100, torch.int32))
 
 
+def test_sample_cut_among_close_logits(evs):
+    """Every row of many: the mass above a bin and the tokens in it have to belong to the same bins."""
+    for V, R, spread in ((60000, 96, 2.0), (200000, 24, 1.0), (5000, 200, 0.3)):
+        l, u = make_logits(V + 5, R, V, spread=spread)
+        t = col(R, [0.5 + 0.01 * i for i in range(R)])
+        check_draw(evs, l, u, temperature=t, top_p=col(R, [0.05 + 0.9 * i / R for i in range(R)]))
+        check_draw(evs, l, u, probs=False, temperature=t, top_k=col(R, 2000, torch.int32), top_p=col(R, 0.6))
+
+
 def test_sample_ties(evs):
     """Equal logits go by their ids: cuts inside one value shared by many more tokens than are ranked at once."""
     for V, levels in ((3000, 1), (50021, 1), (50021, 3), (131072, 2), (131072, 40)):
