@@ -347,9 +347,9 @@ evs_status evs_projection_noalloc_flags(uint32_t* flags, int32_t clear, void* st
  *   keep the first k; of these the shortest prefix whose mass before a token is below p times
  *   their mass (at least one token); of these the tokens with w_i >= m * max w;
  *   token = the smallest id whose cumulative kept mass over ascending ids exceeds u * total.
- * The weights are summed in 64-bit fixed point (2^-44 of the largest; smaller ones are 0): the
- * same inputs give the same token whatever the launch, and equal logits go by their ids. NaN and -inf logits are ruled
- * out; where the largest logit is +inf, the +inf tokens share the mass. A row with every token
+ * The weights are summed in 64-bit fixed point (2^-45 of the largest; smaller ones are 0): the
+ * same inputs give the same token whatever the launch, and equal logits go by their ids. NaN and
+ * -inf logits are ruled out; where the largest logit is +inf, the +inf tokens share the mass. A row with every token
  * ruled out gives token -1, logprob -inf, zero probabilities and EVS_FLAG_EMPTY_ROW. */
 typedef struct {
     int32_t rows, vocab;         /* vocab 1 .. 262144                                       */

@@ -17,7 +17,12 @@
 // describes what is kept) is found by a histogram over the weight's exponent in steps of 1/32,
 // narrowed by digits of (ordered logit, id) while the bin that holds the cut has more than CAP
 // tokens; those few are then ranked. A bin's mass is the sum of its tokens' mantissas, of 34 bits,
-// in two 32-bit counters: the shared-memory atomics are what bounds the histogram of a large row.
+// in two 32-bit counters (three took 13.5 thousand cycles of a large row's histogram, two 12.9).
+//
+// A chain of dependent phases with a barrier each bounds the small rows, instructions (two
+// evaluations of every weight) the large ones. 4 x 512 fp32 with every filter 6.9 us, 208 x 4096
+// with probabilities 17, 64 x 50021 bf16 23, 256 x 131072 fp32 with top-p and min-p 261 (2048 CTAs,
+// seven waves of two an SM; its 134 MB alone are 20).
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
