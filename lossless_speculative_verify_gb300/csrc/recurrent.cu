@@ -408,8 +408,10 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
 // asynchronously into the warp's own ring of SCAN_RING groups of eight positions, B_t and C_t into
 // shared memory for the CTA, 32 positions at a time, which all lanes read as one address. What is
 // per position and channel (softplus, gate) one of its lanes works out for the others, two
-// positions at a time in packed arithmetic. Bound by instructions: 16 sequences of 2048 x 4096 take
-// 720 us, 104 ns for a warp's step of about 125 instructions on a quarter of an SM.
+// positions at a time in packed arithmetic. Bound by instructions, 107 for a warp's step: 16
+// sequences of 2048 x 4096 take 669 us, 97 ns a step on a quarter of an SM. The compiler is left all
+// the registers (156): three CTAs an SM with more of the eight positions under way beat four (720
+// us, 110 registers), five (737) and six (785).
 //
 // That leaves few warps for few sequences, so the tokens are cut into segments: a first pass runs
 // each segment from a zero state (the first from state_in) and leaves its last state and the sum of
@@ -434,7 +436,7 @@ struct ScanSeg {
 // COPY: bytes of an asynchronous copy, 16 where rows start on 16 bytes, else 4 (bf16: where they
 // start on two channels), else 0: element by element.
 template <typename T, int N, int LPC, bool FIRST, int COPY>
-__global__ void __launch_bounds__(32 * SCAN_WARPS) scan_kernel(ScanArgs a, ScanSeg sg) {
+__global__ void __launch_bounds__(32 * SCAN_WARPS, 1) scan_kernel(ScanArgs a, ScanSeg sg) {
     constexpr int NPL = N / LPC, THREADS = 32 * SCAN_WARPS, CPW = 32 / LPC;
     constexpr int EL = COPY ? COPY / (int)sizeof(T) : 1, PER_ROW = CPW / EL;   // channels of a copy, copies of a row
     constexpr int GROUP = 8 * CPW;                   // values of one array in a ring slot
@@ -689,10 +691,9 @@ constexpr int SCAN_STEP_MAX = 16;   // up to this many tokens the staging is not
 // Lanes and segments of a prompt. One lane a channel, unless that leaves schedulers without a warp
 // even with segments (512 x 2048 positions x channels of 16 states: 27 us with four lanes, 44 with
 // one). Segments where fewer than a warp for each scheduler would run, of at least 128 positions
-// (a multiple of the staged 32), enough for about 32 warps an SM: 2 x 4096 x 4096 takes 242 us so,
-// 293 with half of that and 731 in one piece; 8 x 1024 x 4096, with 1024 warps in one piece, 230 us,
-// 261 with segments.
-constexpr int SCAN_FEW = 152 * 4, SCAN_FILL = 152 * 32, SCAN_MAX_SEGS = 64;
+// (a multiple of the staged 32), enough for about three times the 12 warps that an SM holds:
+// 2 x 4096 x 4096 takes 224 us so, 257 with a third of that and 731 in one piece.
+constexpr int SCAN_FEW = 152 * 4, SCAN_FILL = 152 * 36, SCAN_MAX_SEGS = 64;
 ScanSeg scan_segments(int B, int T, int D, int N) {
     ScanSeg sg{nullptr, 1, T, 1};
     if (T <= SCAN_STEP_MAX) return sg;
