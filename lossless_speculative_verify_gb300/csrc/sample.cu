@@ -7,16 +7,16 @@
 //   mass, over ascending ids, exceeds u times the total.
 //
 // The decisions are comparisons of sums over the whole vocabulary, so weights are computed to
-// about 2^-33 relative and summed as 64-bit fixed point (2^-45): the sums do not depend on their
+// about 2^-32 relative and summed as 64-bit fixed point (2^-45): the sums do not depend on their
 // order, every run gives the same token, and it is the one that exact arithmetic gives unless a
-// border falls within about 1e-10 of the total mass. In fp32 the error of one such sum,
+// border falls within about 2e-10 of the total mass. In fp32 the error of one such sum,
 // about 1e-6 of the mass, would move the draw in several percent of rows of 131072 flat logits.
 //
 // The row is read once: the CTAs of the cluster keep their slices in shared memory and search
 // there. The cut (top-k and top-p are both prefixes of the sorted row, so one pair (logit, id)
 // describes what is kept) is found by a histogram over the weight's exponent in steps of 1/32,
 // narrowed by digits of (ordered logit, id) while the bin that holds the cut has more than CAP
-// tokens; those few are then ranked. A bin's mass is the sum of its tokens' mantissas, of 34 bits,
+// tokens; those few are then ranked. A bin's mass is the sum of its tokens' mantissas, of 33 bits,
 // in two 32-bit counters (three took 13.5 thousand cycles of a large row's histogram, two 12.9).
 //
 // A chain of dependent phases with a barrier each bounds the small rows, instructions (two
@@ -230,7 +230,7 @@ struct WeightFn {
         return {__float_as_int(t.x) - __float_as_int(kRound), __float_as_int(t.y) - __float_as_int(kRound), unpk(p),
                 unpk(q), unpk(rest)};
     }
-    // q + rest in steps of 2^-34, or of 2^-33
+    // q + rest in steps of 2^-34, or of 2^-32
     static __device__ __forceinline__ int frac(float q, float rest, float steps = 17179869184.f) {
         return __float2int_rn(q * steps) + __float2int_rn(rest * steps);
     }
@@ -259,10 +259,10 @@ struct WeightFn {
     __device__ __forceinline__ int bin(float l) const {   // the product rounded before the sum, as there
         return bin(__float_as_int(__fadd_rn(__fmul_rn(l - M, c_hi), kRound)) - __float_as_int(kRound));
     }
-    // The mass of a bin whose tokens' 1 + q + rest sum to s 2^-33
+    // The mass of a bin whose tokens' 1 + q + rest sum to s 2^-32
     __device__ __forceinline__ u64 mass(int b, u64 s) const {
         if (b > 32 * SMP_ZERO) return 0;
-        const u64 t = tab[-b & 31], hi = __umul64hi(t, s << 12), lo = t * (s << 12);   // in 2^-43, 2^-107
+        const u64 t = tab[-b & 31], hi = __umul64hi(t, s << 13), lo = t * (s << 13);   // in 2^-43, 2^-107
         return (hi << (SMP_FRAC - 43) | lo >> (64 - (SMP_FRAC - 43))) >> ((b + 31) >> 5);
     }
 };
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     constexpr int BPT = SMP_BINS / THREADS;     // bins a thread sums when the CTA is alone
     extern __shared__ __align__(16) uint8_t smem[];
     float* l_s = reinterpret_cast<float*>(smem);
-    // [2][BINS]: count, or sum of mantissas (low 17 bits, high 17 bits)
+    // [2][BINS]: count, or sum of mantissas (low 16 bits, high 17 bits: 32776 slots stay below 2^32)
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (size_t)a.slice * 4);
     // after a search: what the row's first CTA ranks, with its weights; and before these are
     // worked out, what each CTA found of it, after that two lists of places
@@ -477,9 +477,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                         const Parts w = wf.parts(l0, l1);
                         auto add = [&](int b, float p, float q, float rest) {
                             if (!(p > (float)-SMP_ZERO)) return;
-                            const int x = WeightFn::frac(q, rest, 8589934592.f);
-                            atomicAdd(&hist[b], (uint32_t)x & 0x1ffffu);
-                            atomicAdd(&hist[SMP_BINS + b], (uint32_t)((x >> 17) + 65536));
+                            const int x = WeightFn::frac(q, rest, 4294967296.f);
+                            atomicAdd(&hist[b], (uint32_t)x & 0xffffu);
+                            atomicAdd(&hist[SMP_BINS + b], (uint32_t)((x >> 16) + 65536));
                         };
                         const int b0 = in0 ? place(l0, base + s + 2 * h, wf.bin(w.i0)) : -1;
                         const int b1 = in1 ? place(l1, base + s + 2 * h + 1, wf.bin(w.i1)) : -1;
@@ -503,12 +503,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                             else return hist[plane * SMP_BINS + b];
                         };
                         sum[i] += at(0);
-                        if (k == 0) sum[i] += (u64)at(1) << 17;
+                        if (k == 0) sum[i] += (u64)at(1) << 16;
                     }
                     cnt[i] = sum[i];
                     if (k == 0) {
                         // |q + rest| < 0.011: at most this many tokens
-                        cnt[i] = (sum[i] >> 33) + (sum[i] >> 39) + 1;
+                        cnt[i] = (sum[i] >> 32) + (sum[i] >> 38) + 1;
                         sum[i] = wf.mass(level ? f.bin0 : b, sum[i]);
                     }
                 }

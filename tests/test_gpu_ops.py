@@ -316,7 +316,7 @@ def test_attention_refusals(evs):
 
 # ---- the draw ------------------------------------------------------------------------------------
 def check_draw(evs, logits, u, probs=True, **kw):
-    """Tokens equal the definition's; logprob and probabilities to fp32 (their sums are exact to 1e-10)."""
+    """Tokens equal the definition's; logprob and probabilities to fp32 (their sums are exact to 2e-10)."""
     R, V = logits.shape
     out = evs.sample(logits, u, return_logprob=True, return_probs=probs, **kw)
     host = logits.float().cpu().numpy()
@@ -384,6 +384,17 @@ def test_sample_cut_among_close_logits(evs):
         t = col(R, [0.5 + 0.01 * i for i in range(R)])
         check_draw(evs, l, u, temperature=t, top_p=col(R, [0.05 + 0.9 * i / R for i in range(R)]))
         check_draw(evs, l, u, probs=False, temperature=t, top_k=col(R, 2000, torch.int32), top_p=col(R, 0.6))
+
+
+def test_sample_equal_but_for_a_last_bit(evs):
+    """The largest vocabulary off the 16-byte grid, all weights of a bin one step below the largest."""
+    V = 1 << 18
+    wide = torch.full((2, V + 3), 1.0 - 2.0 ** -24, device="cuda")
+    l = wide[:, 1:V + 1]
+    l[:, 1000] = 1.0
+    u = torch.tensor([0.3, 0.999], device="cuda")
+    for t in (600.0, 300.0, 40.0):
+        check_draw(evs, l, u, probs=False, temperature=col(2, t), top_p=col(2, [0.3, 0.7]))
 
 
 def test_sample_ties(evs):
