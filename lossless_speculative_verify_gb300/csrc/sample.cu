@@ -44,6 +44,7 @@ constexpr int SMP_CAP = 1024;           // tokens ranked at once
 constexpr int SMP_FEW = 128;            // of them by counting instead of sorting
 constexpr int SMP_FRAC = 45;            // fixed point of weights; 2^18 of them reach 2^63
 constexpr int SMP_ZERO = SMP_FRAC + 1;  // weights of 2^-46 and less are 0
+constexpr int SMP_AREA = SMP_CAP * 20;   // bytes of shared memory behind the logits: two lists of 8 bytes, two of 2
 constexpr int SMP_MAX_CS = 8;           // portable cluster size
 
 // 2^(j/32) for j = 0..31, each the sum of two floats
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     uint16_t* places = reinterpret_cast<uint16_t*>(list_w + SMP_CAP);           // [2][CAP]
     // after the cut: 192 kept logits a warp
     float* queue = reinterpret_cast<float*>(hist) + (threadIdx.x >> 5) * 192;
+    static_assert(THREADS / 32 * 192 * 4 <= SMP_AREA && SMP_BINS * 8 <= SMP_AREA, "shared memory behind the logits");
     __shared__ float2 pow2[32];
     __shared__ u64 tab[32];
     __shared__ u64 red[THREADS / 32];
@@ -949,7 +951,7 @@ cudaError_t sample_dispatch(SampleArgs a, int rows, cudaStream_t stream) {
     const int cs = sample_cluster(rows, a.V);
     const int grans = (VEC - 1 + a.V + VEC - 1) / VEC;
     a.slice = (grans + cs - 1) / cs * VEC;
-    const size_t smem = (size_t)a.slice * 4 + (size_t)SMP_CAP * 20;
+    const size_t smem = (size_t)a.slice * 4 + SMP_AREA;
     if (cs > 1) return sample_launch<T, 512, true>(a, rows, cs, smem, stream);
     if (a.V > 2048) return sample_launch<T, 512, false>(a, rows, 1, smem, stream);
     return sample_launch<T, 256, false>(a, rows, 1, smem, stream);
