@@ -58,7 +58,7 @@ template <> __device__ __forceinline__ float exp_of<bf16>(float x) { return __ex
 // Own rows of sequence b, clamped to [0, own_max].
 __device__ __forceinline__ int own_rows_of(const SharedArgs& a, int b, bool report) {
     if (!a.own_len) return 0;
-    const int n = a.own_len[b] - a.own_skip;
+    const int n = __ldcg(a.own_len + b) - a.own_skip;
     if (n < 0 || n > a.own_max) {
         if (report && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_BAD_LEN);
         return n < 0 ? 0 : a.own_max;
@@ -68,6 +68,12 @@ __device__ __forceinline__ int own_rows_of(const SharedArgs& a, int b, bool repo
 
 __device__ __forceinline__ float load_q(const SharedArgs& a, int64_t at) {
     return a.q_bf16 ? __bfloat162float(((const bf16*)a.q)[at]) : ((const float*)a.q)[at];
+}
+
+// Past L1, which may hold what an earlier kernel read: for loads ahead of the dependency wait.
+__device__ __forceinline__ float load_l2(const float* p) { return __ldcg(p); }
+__device__ __forceinline__ float load_l2(const bf16* p) {
+    return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p)) << 16);
 }
 
 // =========================================================================================
@@ -757,7 +763,8 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
     __shared__ float part[SC_GROUPS][4][KB][RW];  // a warp's share of the dot products
     __shared__ float4 sum_o[SC_GROUPS - 1][128];
     __shared__ float2 sum_ml[SC_GROUPS - 1][128];
-    // The partial kernel starts its dependents when all before it is done; without one, wait for that.
+    // The partial kernel starts its dependents when all before it is done, so the inputs are there (in
+    // L2); without one, wait for that.
     if (!a.partials) {
         pdl_wait();
         pdl_trigger();
@@ -810,19 +817,22 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
     auto load4 = [&](const T* p) -> float4 {
         if (a.b_vec) {
             if constexpr (sizeof(T) == 4) {
-                return *reinterpret_cast<const float4*>(p);
+                return __ldcg(reinterpret_cast<const float4*>(p));
             } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(p);
+                const uint2 u = __ldcg(reinterpret_cast<const uint2*>(p));
                 const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
                 const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
                 return make_float4(lo.x, lo.y, hi.x, hi.y);
             }
         }
-        return make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+        return make_float4(load_l2(p), load_l2(p + 1), load_l2(p + 2), load_l2(p + 3));
     };
     float q[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) q[u] = load_q(a, m * a.q_ld + (int64_t)h * DH + c4 * 4 + u) * a.scale;
+    for (int u = 0; u < 4; ++u) {
+        const int64_t at = m * a.q_ld + (int64_t)h * DH + c4 * 4 + u;
+        q[u] = (a.q_bf16 ? load_l2((const bf16*)a.q + at) : load_l2((const float*)a.q + at)) * a.scale;
+    }
     for (int j1 = 0; j1 < a.T; j1 += KB * parts) {  // the same count for every thread of the CTA
         const int j0 = j1 + part_of * KB, n = min(KB, a.T - j0);
         float4 v[KB];

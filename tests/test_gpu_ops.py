@@ -518,6 +518,50 @@ def test_sample_refusals(evs):
             evs.sample(*a, **kw)
 
 
+def test_inputs_written_just_before(evs):
+    """Each operator right behind the kernels that write its inputs, over and over, eagerly and in a graph."""
+    n = 12
+    ds = [make_attn(900 + i, BF16, 4, 2, 5, 4, 2, 128, 300, 40, [0, 40, 17, 3]) for i in range(n)]
+    ls = [make_logits(950 + i, 6, 9000) for i in range(n)]
+    ss = [make_scan(970 + i, 2, 24, 96, 16, BF16) for i in range(n)]
+    w = randn(gen(1), 96, 4)
+    p = col(6, 0.9)
+
+    def run(d, l, s):
+        y = evs.causal_conv(s["x"], w)
+        z = evs.selective_scan(y, s["dt"], s["A"], s["B"], s["C"])
+        return [*run_attn(evs, d), evs.sample(*l, top_p=p), y, z]
+
+    want = []
+    for d, l, s in zip(ds, ls, ss):
+        want.append(run(d, l, s))
+        torch.cuda.synchronize()
+    d, l, s = ({k: v.clone() for k, v in ds[0].items()}, [v.clone() for v in ls[0]], {k: v.clone() for k, v in ss[0].items()})
+
+    def chain():
+        out = []
+        for dn, ln, sn in zip(ds, ls, ss):
+            for k, v in dn.items():
+                d[k].copy_(v)
+            for a, b in zip(l, ln):
+                a.copy_(b)
+            for k, v in sn.items():
+                s[k].copy_(v)
+            out.append(run(d, l, s))
+        return out
+
+    eager = chain()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        captured = chain()
+    gr.replay()
+    gr.replay()
+    torch.cuda.synchronize()
+    for got in (eager, captured):
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_no_gradients(evs):
     l, u = make_logits(25, 2, 100)
     x, w = torch.zeros(1, 4, 8, device="cuda", requires_grad=True), torch.zeros(8, 4, device="cuda")
