@@ -428,7 +428,8 @@ template <int BYTES> __device__ __forceinline__ void cp_async(void* dst, const v
 }
 
 struct ScanSeg {
-    float* ws;          // [b][segment][N + 1][D]: last states and the sum of dl; then [b][N][D] state_in
+    float* ws;          // [b][segment][N + 1][D]: last states and the sum of dl; then [b][N][D] state_in of
+                        // the sequences of more than one segment
     int segs, len;      // segments of a sequence, positions of one
     int lanes;          // of a channel
 };
@@ -468,7 +469,9 @@ __global__ void __launch_bounds__(32 * SCAN_WARPS, 1) scan_kernel(ScanArgs a, Sc
         for (int k = 0; k < NPL; ++k) v[k] = 0.f;
         float* keep = sg.ws + (size_t)gridDim.y * sg.segs * (N + 1) * a.D + (size_t)b * N * a.D + ch;
         if (j == 0 && a.state_in) {
-            if (!FIRST && sg.segs > 1) {          // state_out may be state_in: the first pass kept a copy
+            // Where a later segment writes state_out, which may be state_in, the first pass kept a copy. A
+            // sequence that ends in this segment has none, and no other writer than this lane.
+            if (!FIRST && !last) {
 #pragma unroll
                 for (int k = 0; k < NPL; ++k) v[k] = of_state(keep, a.D, k);
             } else {

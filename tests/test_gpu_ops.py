@@ -770,6 +770,62 @@ def test_scan_in_pieces_and_sliced(evs):
     assert torch.equal(whole, run(0, 90, state=s["state"]))
 
 
+def poison(*sizes):
+    """Freed memory of these sizes, which the next allocations of them get, holds NaN."""
+    torch.cuda.synchronize()
+    for n in sizes:
+        if n:
+            t = torch.full((n // 4,), float("nan"), device="cuda")
+            del t
+
+
+# (width, states, tokens, lengths) of prompts that run in segments of 96 to 224 positions
+SEGMENTED = [(4096, 16, 4096, [4096, 100]), (1024, 16, 700, [0, 1, 127, 128, 129, 159, 160, 161, 319, 320, 321, 700]),
+             (96, 4, 513, [513, 0, 128, 129, 31]), (256, 8, 600, [600, 128, 1]), (64, 32, 900, [1, 900, 127, 257]),
+             (33, 16, 400, [400, 128, 2, 399])]
+
+
+@pytest.mark.parametrize("case", SEGMENTED, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_scan_segments_and_short_sequences(evs, case, dtype):
+    """Prompts cut into segments beside sequences that end in the first segment, at its end or have no token:
+    the carried state apart and in place, with and without outputs, in memory that held NaN."""
+    W, N, T, lens = case
+    Bn = len(lens)
+    s = make_scan(W + T, Bn, T, W, N, dtype)
+    n_ws = evs.load().evs_selective_scan_workspace(Bn, T, W, N)
+    assert n_ws > 0                                                  # it does run in segments
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    args = (s["x"], s["dt"], s["A"], s["B"], s["C"])
+    kw = {k: s[k] for k in ("D", "z", "dt_bias")}
+    long = lens.index(max(lens))
+    ry, ye, rs, se = ref.scan(*args, kw["D"], kw["z"], kw["dt_bias"], s["state"],
+                              [0 if T > 2000 and b == long else n for b, n in enumerate(lens)])
+    for place in (False, True):
+        for output in (True, False):
+            st = s["state"].clone()
+            so = st if place else torch.full_like(st, 5.0)
+            out = torch.full((Bn, T, W), 9.0, device="cuda", dtype=dtype) if output else None
+            poison(n_ws)
+            y = evs.selective_scan(*args, **kw, state=st, state_out=so, lens=lt, out=out, output=output)
+            for b, n in enumerate(lens):
+                if T > 2000 and b == long:                           # its definition takes long and has a test
+                    assert torch.isfinite(so[b]).all()
+                    continue
+                assert torch.all((so[b].double() - rs[b]).abs() <= se[b] + 1e-30), (b, n)
+                if output:
+                    tol = ye[b] + (BF * (1 + 1e-3) * ry[b].abs() if dtype == BF16 else 0.0) + 1e-30
+                    assert torch.all((y[b].double() - ry[b]).abs()[:n] <= tol[:n]), (b, n)
+                    assert torch.all(y[b, n:] == 9.0)
+            if not place:
+                assert torch.equal(st, s["state"])
+    # a length below zero is one of zero: the state stays
+    so = torch.empty_like(s["state"])
+    poison(n_ws)
+    evs.selective_scan(*args, **kw, state=s["state"], state_out=so, lens=torch.full_like(lt, -3))
+    assert torch.equal(so, s["state"])
+
+
 def test_scan_extremes(evs):
     """Step sizes from none to huge: a decay of exactly one, and of zero."""
     for T in (4, 40):
