@@ -449,8 +449,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
     // (k > 0), or the cumulative mass of the tokens above the cut so far reaches
     // x = ceil(p64 * their mass). Level 0 bins by the weight's exponent, later levels by a digit of the
     // order. bin0 is BINS where fewer than k tokens are left. Uniform over the cluster.
+    // Masses are rounded down, so those of a bin's digits may fall short of the bin's own, and a cut
+    // in between would have no digit. Digits are therefore summed as mantissas, which add exactly, and
+    // a mass is formed of all of the bin up to a digit: the last digit reaches what the bin does.
     auto search = [&](uint32_t k, u64 p64, u64& x) -> Found {
         Found f{SMP_BINS, SMP_ORDER_BITS, 0, 0, 0};
+        u64 bin_above = 0, part = 0;              // mass before bin0; mantissas of bin0 before the digit
         for (int level = 0;; ++level) {
             const int to = max(0, f.shift - SMP_DIGIT), width = f.shift - to;   // this level's digit
             for (int i = tid; i < (k ? 1 : 2) * SMP_BINS; i += THREADS) hist[i] = 0;
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             sync_all<CLUSTER>();
             // this CTA's share of the bins, summed over the cluster; a thread takes PT in a row
             const int nb = SMP_BINS / cs, b_lo = nb * rank, PT = (nb + THREADS - 1) / THREADS;
-            u64 sum[BPT], cnt[BPT], tc = 0;       // of counts or of masses
+            u64 sum[BPT], cnt[BPT], tc = 0;       // of counts, masses or mantissas
 #pragma unroll
             for (int i = 0; i < BPT; ++i) {
                 cnt[i] = sum[i] = 0;
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                     if (k == 0) {
                         // |q + rest| < 0.011: at most this many tokens
                         cnt[i] = (sum[i] >> 32) + (sum[i] >> 38) + 1;
-                        sum[i] = wf.mass(level ? f.bin0 : b, sum[i]);
+                        if (level == 0) sum[i] = wf.mass(b, sum[i]);
                     }
                 }
                 tc += sum[i];
@@ -531,11 +535,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
                 x = __umul64hi(p64, all) + ((p64 * all) != 0 ? 1 : 0);
                 if (x == 0) x = 1;                // the first token is always kept
             }
-            before += f.above;
+            const bool parts = k == 0 && level > 0;
+            before += parts ? part : f.above;
             const u64 goal = k ? k : x;
+            auto reach = [&](u64 v) -> u64 { return parts ? bin_above + wf.mass(f.bin0, v) : v; };
 #pragma unroll
             for (int i = 0; i < BPT; ++i) {
-                if (before < goal && before + sum[i] >= goal) {
+                if (sum[i] && reach(before) < goal && reach(before + sum[i]) >= goal) {
                     const uint32_t bin = b_lo + tid * PT + i;
                     for (uint32_t r = 0; r < cs; ++r) {
                         if constexpr (CLUSTER) {
@@ -554,8 +560,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             sync_all<CLUSTER>();
             if (f_bin == SMP_BINS) return f;
             f.count = f_count;
-            f.above = f_above;
+            part = parts ? f_above : 0;
+            f.above = reach(f_above);
             if (level == 0) {
+                bin_above = f.above;
                 f.bin0 = (int)f_bin;
             } else {
                 const u64 digit = (u64)((1 << width) - 1 - (int)f_bin);

@@ -397,6 +397,54 @@ def test_sample_equal_but_for_a_last_bit(evs):
         check_draw(evs, l, u, probs=False, temperature=col(2, t), top_p=col(2, [0.3, 0.7]))
 
 
+def test_sample_border_at_the_end_of_a_crowded_bin(evs):
+    """top-p's border on the last units of 2^-45 of a step of 1/32 in the exponent that holds 3360 tokens whose
+    logits spread over 1120 binary orders and quarters: what each of these rounds off must not lose the border.
+
+    Row: one token of weight 1; the crowd A; B of as much mass as both, two of its tokens tuned
+    row by row; top_p = 1/2. The tuned mass at which the kernel first keeps one of B is found by refinement; below
+    it, in steps of 40 units over the 1120 that could be lost, every row keeps exactly the first token and A."""
+    T, p, unit = 64.0, 0.5, 2.0 ** -45
+    step = math.log(2.0) / 32.0 * T
+    top = np.float32(33 * step)                                      # A, around 0, is in step 33 below the largest
+    mags = np.array([2.0 ** -e * (1.0 + q / 4.0 + 0.03 * j) for e in range(2, 142) for q in range(4) for j in range(3)],
+                    np.float32)
+    a = np.sort(np.concatenate([mags, -mags]))[::-1]
+    assert np.all(np.abs(a) < 0.45 * step) and a.size == 3360
+    weight = lambda l: np.exp((np.asarray(l, np.float64) - float(top)) / T)  # noqa: E731
+    want = 1.0 + weight(a).sum()
+    b, left = [], want - 2.0 ** -18 * 1.5
+    for depth in range(40, 19 * 32, 8):                              # 2^-1.25 .. 2^-19 of the largest
+        l = np.float32(float(top) - depth * step)
+        n = min(int(left / weight(l)), 4000)
+        b += [l] * n
+        left -= n * float(weight(l))
+    assert 0 <= left < 2.0 ** -18
+    fixed = np.concatenate([[top], a, np.array(b, np.float32)])
+
+    def kept(extra):
+        """Kept tokens where B has `extra` (an array) more than `left` + 2^-18, as two tokens each."""
+        mass = extra + left + 2.0 ** -18 * 1.5
+        coarse = (float(top) + T * np.log(mass * (1.0 - 2.0 ** -12))).astype(np.float32)
+        fine = (float(top) + T * np.log(mass - weight(coarse))).astype(np.float32)
+        rows = np.tile(fixed, (len(extra), 1))
+        l = torch.from_numpy(np.concatenate([rows, coarse[:, None], fine[:, None]], 1)).cuda()
+        n = len(extra)
+        _, probs = evs.sample(l, torch.full((n,), 0.5, device="cuda"), temperature=col(n, T), top_p=col(n, p),
+                              return_probs=True)
+        return (probs > 0).sum(1).cpu().numpy()
+
+    first = 1 + a.size
+    lo, hi = -2.0 ** -19, 2.0 ** -19
+    while hi - lo > 16 * unit:                                       # kept(lo) <= first < kept(hi)
+        grid = np.linspace(lo, hi, 66)
+        over = np.flatnonzero(kept(grid) > first)
+        assert over.size and over[0] > 0
+        lo, hi = grid[over[0] - 1], grid[over[0]]
+    below = kept(lo - 2.0 * unit * np.arange(0, 1200, 40))
+    assert np.all(below == first), below
+
+
 def test_sample_ties(evs):
     """Equal logits go by their ids: cuts inside one value shared by many more tokens than are ranked at once."""
     for V, levels in ((3000, 1), (50021, 1), (50021, 3), (131072, 2), (131072, 40)):
