@@ -66,8 +66,13 @@ __device__ __forceinline__ int own_rows_of(const SharedArgs& a, int b, bool repo
     return n;
 }
 
-__device__ __forceinline__ float load_q(const SharedArgs& a, int64_t at) {
-    return a.q_bf16 ? __bfloat162float(((const bf16*)a.q)[at]) : ((const float*)a.q)[at];
+// A query enters its products in the type of K: fp32 queries of a bf16 cache are rounded to bf16 in
+// every product, the block rows' and those on CUDA cores too, so that the result is that of the rounded
+// queries whichever kernel the strides lead to. (The tensor cores multiply bf16 by bf16 only; the
+// query's remainder as a second product would double the staged queries, 64 of the 227 KB.)
+template <typename T> __device__ __forceinline__ float as_product(float q) { return to_f32(from_f32<T>(q)); }
+template <typename T> __device__ __forceinline__ float load_q(const SharedArgs& a, int64_t at) {
+    return a.q_bf16 ? __bfloat162float(((const bf16*)a.q)[at]) : as_product<T>(((const float*)a.q)[at]);
 }
 
 // Past L1, which may hold what an earlier kernel read: for loads ahead of the dependency wait.
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
         float v = 0.f;
         if (r < rows) {
             const int64_t m = sh ? r / grp : (int64_t)b * a.C * a.T + r / grp;
-            v = load_q(a, m * a.q_ld + (int64_t)(g * grp + r % grp) * dh + c) * a.scale;
+            v = load_q<T>(a, m * a.q_ld + (int64_t)(g * grp + r % grp) * dh + c) * a.scale;
         }
         qs[e / dh][c] = v;
     }
@@ -591,7 +596,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
             } else if (live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = load_q(a, at + e + j);
+                for (int j = 0; j < 8; ++j) x[j] = load_q<bf16>(a, at + e + j);
             }
             *reinterpret_cast<uint4*>(dst + (e >> 6) * HALF + (((e >> 3 & 7) ^ (r & 7)) << 4)) =
                 make_uint4(st_pack(x[0], x[1]), st_pack(x[2], x[3]), st_pack(x[4], x[5]), st_pack(x[6], x[7]));
@@ -831,7 +836,7 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int64_t at = m * a.q_ld + (int64_t)h * DH + c4 * 4 + u;
-        q[u] = (a.q_bf16 ? load_l2((const bf16*)a.q + at) : load_l2((const float*)a.q + at)) * a.scale;
+        q[u] = (a.q_bf16 ? load_l2((const bf16*)a.q + at) : as_product<T>(load_l2((const float*)a.q + at))) * a.scale;
     }
     for (int j1 = 0; j1 < a.T; j1 += KB * parts) {  // the same count for every thread of the CTA
         const int j0 = j1 + part_of * KB, n = min(KB, a.T - j0);

@@ -223,7 +223,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     position. Without k_block (one candidate) the block rows are own rows own_len[b] + j.
 
     K and V are fp32 or bf16 with any strides but the last (K and V of a pair alike); q is of their type, or
-    fp32. heads is a multiple of kv_heads; dh 16, 32, 64 or 128. Returns out (the type of K), or [out, lse fp32
+    fp32 and rounded to it. heads is a multiple of kv_heads; dh 16, 32, 64 or 128. Returns out (the type of K), or [out, lse fp32
     [batch, candidates, block, heads]]."""
     dev = _device("q", q)
     _need(q.dim() == 5 and q.dtype in _DT, "q: want fp32 or bf16 [batch, candidates, block, heads, dh]")

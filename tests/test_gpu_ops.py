@@ -219,6 +219,24 @@ def test_attention_fp32_queries(evs):
     check_attn(d, run_attn(evs, d, scale=0.25), BF16, scale=0.25)
 
 
+@pytest.mark.parametrize("dh", [16, 32, 64, 128])
+def test_attention_fp32_queries_are_rounded_to_the_cache(evs, dh):
+    """fp32 queries that are no bf16 values give what the rounded ones give, bit for bit: of prefix, own and block
+    rows, block rows in the cache, rows on 16 bytes and off them."""
+    for block in (True, False):
+        d = make_attn(16, BF16, 3, 1, 4, 8, 2, dh, 300, 100, [0, 90, 50], block=block)
+        q = randn(gen(17), 3, 1, 4, 8, dh) * 1.5
+        odd = dict(d)
+        for k in ("kp", "vp"):
+            wide = torch.zeros(d[k].numel() + 1, dtype=BF16, device="cuda")
+            wide[1:] = d[k].flatten()
+            odd[k] = wide[1:].view(d[k].shape)
+        for e in (d, odd):
+            got, want = run_attn(evs, dict(e, q=q)), run_attn(evs, dict(e, q=q.to(BF16)))
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            check_attn(dict(e, q=q.to(BF16)), got, BF16)
+
+
 def test_attention_lengths_out_of_range(evs):
     for dtype, dh in ((BF16, 128), (F32, 16)):
         d = make_attn(11, dtype, 3, 1, 2, 2, 2, dh, 140, 60, [0, 60, 7])
