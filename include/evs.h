@@ -383,8 +383,9 @@ evs_status evs_decode_filtered(evs_handle* h, const int32_t* tokens, const evs_s
  * exponentials. The block rows lie in k_block / v_block, or (both NULL, n_cand 1) in the own rows
  * behind the readable ones, row own_len[b] - own_skip + j.
  * Lengths outside [0, own_max] are clamped (EVS_FLAG_BAD_LEN); block rows past own_max are left
- * out (EVS_FLAG_KV_OVERFLOW). A query whose every score is -inf gives o = 0 and lse = -inf. Rows
- * that no query reads may hold anything. K, V and o are dtype; q is q_dtype and enters every product as
+ * out (EVS_FLAG_KV_OVERFLOW). A query whose every score is -inf gives o = 0 and lse = -inf; one whose
+ * kernel gave up a bounded wait gives NaN for both (EVS_FLAG_TIMEOUT). Rows that no query reads may hold
+ * anything. K, V and o are dtype; q is q_dtype and enters every product as
  * dtype: fp32 queries of a bf16 cache are rounded to bf16. Statistics and accumulators are fp32; softmax
  * weights enter the products as bf16 on the tensor cores (dtype bf16, head_dim 64 or 128, rows on 16
  * bytes) and as fp32 elsewhere. */

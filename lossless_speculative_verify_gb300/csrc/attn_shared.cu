@@ -616,13 +616,13 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         stage(p);
         staged();
     }
-    while (p.n > 0 && ok) {
+    while (p.n > 0) {
         const int seg_rows = p.sh ? a.sh_rows : a.own_rows;
         int r_seg, r_all;
         const bool live = rows_of(p, r_seg, r_all), work = __any_sync(0xffffffffu, live);
         const Piece nx = next_piece(p);
         float m_run = -INFINITY, l = 0.f;
-        for (int t = 0; t < p.n; ++t) {
+        for (int t = 0; ok && t < p.n; ++t) {
             if (!wait_all(&s_full[L], cnt & 1u)) { ok = false; break; }
             if (t == p.n - 1 && nx.n > 0) stage(nx);   // the last scores are out: Q's place is free
             uint32_t x[8][16];
@@ -716,7 +716,9 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             ++cnt;
         }
         if (ok && nx.n > 0) staged();             // the next scores need not wait for the rest
-        // ---- the piece's partials: o, then (m, l)
+        // ---- the piece's partials: o, then (m, l). Once a wait has run out, this piece's and those of the
+        // worker's later ones are void: l = NaN makes the rows' outputs NaN, whether or not the caller
+        // looks at the flag (a row of NaN scores leaves the same pair).
         if (ok && !wait_all(&pv_done[L], (cnt - 1) & 1u)) ok = false;
         tc_fence_after();
         if (!ok && lane == 0) {
@@ -745,7 +747,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             }
             if (live)
                 (p.sh ? a.sh_ml : a.own_ml)[at * seg_rows + r_seg] =
-                    ok ? make_float2(m_run * 0.6931471805599453f, l) : make_float2(-INFINITY, 0.f);
+                    ok ? make_float2(m_run * 0.6931471805599453f, l) : make_float2(-INFINITY, __int_as_float(0x7fc00000));
         }
         tc_fence_before();                        // these reads precede the next piece's products
         p = nx;
@@ -937,7 +939,7 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
                 rebase(mb);
 #pragma unroll
                 for (int j = 0; j < PB; ++j) {
-                    // an empty partial leaves its o unwritten (one of NaN scores has l = NaN)
+                    // an empty partial leaves its o unwritten (one of NaN scores, or void, has l = NaN)
                     if (ml[j].x == -INFINITY && ml[j].y == 0.f) continue;
                     const float w = exp_of<T>(ml[j].x - M);
                     L = fmaf(ml[j].y, w, L);

@@ -165,6 +165,26 @@ def test_attention_reads_nothing_behind_the_lengths(evs, dh, dtype):
     assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
 
 
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_partials_without_a_value(evs, dh):
+    """A partial (m, l) = (-inf, NaN), which a row of NaN scores leaves and a kernel that gave up a wait writes,
+    makes its row NaN among any number of sound partials, first, last or between them; the other rows stay sound."""
+    P, S = 40000, 300                                                # partials of many runs
+    d = make_attn(18, BF16, 3, 2, 2, 4, 2, dh, P, S, [300, 0, 129])
+    clean = run_attn(evs, d)
+    for at in (0, 20000, P - 1):
+        e = dict(d, kp=d["kp"].clone())
+        e["kp"][0, at] = float("nan")                                # one K/V head of two
+        o, lse = run_attn(evs, e)
+        assert torch.isnan(o[:, :, :, :2].float()).all() and torch.isnan(lse[:, :, :, :2]).all()
+        assert torch.equal(o[:, :, :, 2:], clean[0][:, :, :, 2:]) and torch.equal(lse[:, :, :, 2:], clean[1][:, :, :, 2:])
+    e = dict(d, ko=d["ko"].clone())
+    e["ko"][2, 1, 128] = float("nan")                                # the last own row of one sequence
+    o, lse = run_attn(evs, e)
+    assert torch.isnan(o[2, :, :, 2:].float()).all() and torch.isnan(lse[2, :, :, 2:]).all()
+    assert torch.equal(o[:2], clean[0][:2]) and torch.equal(o[2, :, :, :2], clean[0][2, :, :, :2])
+
+
 def test_attention_values_that_propagate(evs):
     """A NaN or infinity in a readable row does reach the queries that read it, and no others."""
     for dtype, dh in ((BF16, 128), (F32, 32)):
