@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(ConvArgs a) {
 // Runs: as many as run at once, seven CTAs an SM over all sequences, at least 16
 // positions each: only the first run then reads the old tail, which its thread may overwrite.
 template <typename T, int LMAX, int VEC>
-void conv_launch(ConvArgs a, int B, cudaStream_t s) {
+cudaError_t conv_launch(ConvArgs a, int B, cudaStream_t s) {
     const int cols = (a.D + VEC * CONV_THREADS - 1) / (VEC * CONV_THREADS);
     int runs = 1;
     if (a.y) {
@@ -268,25 +268,18 @@ void conv_launch(ConvArgs a, int B, cudaStream_t s) {
     } else {
         a.run = a.T > 0 ? a.T : 1;
     }
-    launch_s(s, conv_kernel<T, LMAX, VEC>, dim3(cols, runs, B), dim3(CONV_THREADS), 0, a);
+    return launch_s(s, conv_kernel<T, LMAX, VEC>, dim3(cols, runs, B), dim3(CONV_THREADS), 0, a);
 }
 
 template <typename T>
-void conv_dispatch(const ConvArgs& a, int B, bool wide, cudaStream_t s) {
+cudaError_t conv_dispatch(const ConvArgs& a, int B, bool wide, cudaStream_t s) {
     constexpr int V = 4;
-    if (!wide) {
-        conv_launch<T, 16, 1>(a, B, s);
-    } else if (a.L == 2) {
-        conv_launch<T, 2, V>(a, B, s);
-    } else if (a.L == 3) {
-        conv_launch<T, 3, V>(a, B, s);
-    } else if (a.L == 4) {
-        conv_launch<T, 4, V>(a, B, s);
-    } else if (a.L <= 8) {
-        conv_launch<T, 8, V / 2>(a, B, s);
-    } else {
-        conv_launch<T, 16, 2>(a, B, s);
-    }
+    if (!wide) return conv_launch<T, 16, 1>(a, B, s);
+    if (a.L == 2) return conv_launch<T, 2, V>(a, B, s);
+    if (a.L == 3) return conv_launch<T, 3, V>(a, B, s);
+    if (a.L == 4) return conv_launch<T, 4, V>(a, B, s);
+    if (a.L <= 8) return conv_launch<T, 8, V / 2>(a, B, s);
+    return conv_launch<T, 16, 2>(a, B, s);
 }
 
 // =========================================================================================
@@ -794,9 +787,9 @@ extern "C" evs_status evs_causal_conv(const evs_conv_args* c, void* stream) {
     const bool wide = c->width % v == 0 && c->x_ld % v == 0 && c->x_seq % v == 0 && aligned(c->x, v * es) &&
                       (!c->y || (c->y_ld % v == 0 && c->y_seq % v == 0 && aligned(c->y, v * es))) &&
                       aligned(c->weight, 16) && (!c->tail_in || aligned(c->tail_in, 16)) && (!c->tail_out || aligned(c->tail_out, 16));
-    if (es == 2) conv_dispatch<bf16>(a, c->batch, wide, (cudaStream_t)stream);
-    else conv_dispatch<float>(a, c->batch, wide, (cudaStream_t)stream);
-    return cudaGetLastError() == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    const cudaError_t e = es == 2 ? conv_dispatch<bf16>(a, c->batch, wide, (cudaStream_t)stream)
+                                  : conv_dispatch<float>(a, c->batch, wide, (cudaStream_t)stream);
+    return e == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
 }
 
 extern "C" evs_status evs_selective_scan(const evs_scan_args* c, void* stream) {

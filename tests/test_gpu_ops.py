@@ -794,6 +794,38 @@ def test_conv_strides_and_lengths(evs):
     assert torch.equal(t0, t1)
 
 
+def test_an_earlier_call_that_failed_is_not_reported_again(evs):
+    """A draw on a stream whose capture has become invalid fails, on the host; the calls after it on a sound stream
+    succeed. (The runtime that the library links keeps the last error of a thread until somebody asks for it.)"""
+    import ctypes
+    g = gen(33)
+    x, w, tail = randn(g, 2, 9, 64), randn(g, 64, 4), randn(g, 2, 3, 64)
+    want = evs.causal_conv(x, w, tail=tail)
+    l, u = make_logits(34, 2, 100)
+    tok = torch.empty(2, dtype=torch.int32, device="cuda")
+    lib = evs.load()
+    from lossless_speculative_verify_gb300 import _lib
+    a = _lib.SampleArgs(rows=2, vocab=100, dtype=0, ld=100, logits=l.data_ptr(), uniforms=u.data_ptr(),
+                        token=tok.data_ptr())
+    torch.cuda.synchronize()
+    # torch's runtime, as loaded into this process
+    path = next(p for p in open("/proc/self/maps").read().split() if "libcudart.so" in p)
+    rt = ctypes.CDLL(path)
+    rt.cudaStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    rt.cudaStreamSynchronize.argtypes = rt.cudaStreamDestroy.argtypes = [ctypes.c_void_p]
+    rt.cudaStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    assert rt.cudaStreamBeginCapture(stream, 2) == 0                 # relaxed: other streams of the thread as ever
+    assert rt.cudaStreamSynchronize(stream) != 0                     # not permitted: the capture is invalid now
+    assert lib.evs_sample(ctypes.byref(a), stream) == 4              # EVS_ERR_CUDA
+    assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    rt.cudaGetLastError()
+    assert rt.cudaStreamDestroy(stream) == 0
+    assert torch.equal(evs.causal_conv(x, w, tail=tail), want)
+    assert torch.equal(evs.sample(l, u), evs.sample(l, u))
+
+
 def make_scan(seed, B, T, D, N, dtype):
     g = gen(seed)
     step = torch.exp(torch.rand(D, device="cuda", generator=g) * math.log(100.0) + math.log(1e-3))
