@@ -1207,5 +1207,5 @@ extern "C" evs_status evs_shared_attention(const evs_shared_attn_args* c, void* 
     if (!(c->scale >= 0.f) || isinf(c->scale)) return EVS_ERR_INVALID_ARG;
     if (!c->workspace || (uintptr_t)c->workspace % 256) return EVS_ERR_INVALID_ARG;
     if (c->ws_bytes < evs_shared_attention_workspace(c)) return EVS_ERR_CAPACITY;
-    return launch_shared_attention(*c, (cudaStream_t)stream) == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    return status_of(launch_shared_attention(*c, (cudaStream_t)stream));
 }

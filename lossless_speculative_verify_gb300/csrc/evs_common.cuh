@@ -75,6 +75,14 @@ inline cudaError_t launch_k(evs_handle* h, void (*kernel)(KArgs...), dim3 grid, 
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Status of an entry point that reports its launches' own errors: one that failed is reported here
+// and not left behind for a later call that asks for the thread's last error.
+inline evs_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return EVS_OK;
+    cudaGetLastError();
+    return EVS_ERR_CUDA;
+}
+
 // The same launch on a plain stream, for entry points without a handle.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_s(cudaStream_t stream, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,

@@ -789,7 +789,7 @@ extern "C" evs_status evs_causal_conv(const evs_conv_args* c, void* stream) {
                       aligned(c->weight, 16) && (!c->tail_in || aligned(c->tail_in, 16)) && (!c->tail_out || aligned(c->tail_out, 16));
     const cudaError_t e = es == 2 ? conv_dispatch<bf16>(a, c->batch, wide, (cudaStream_t)stream)
                                   : conv_dispatch<float>(a, c->batch, wide, (cudaStream_t)stream);
-    return e == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    return status_of(e);
 }
 
 extern "C" evs_status evs_selective_scan(const evs_scan_args* c, void* stream) {
@@ -819,7 +819,7 @@ extern "C" evs_status evs_selective_scan(const evs_scan_args* c, void* stream) {
     }
     const cudaError_t e = c->dtype == EVS_DTYPE_BF16 ? scan_dispatch<bf16>(a, sg, c->batch, c->states, (cudaStream_t)stream)
                                                      : scan_dispatch<float>(a, sg, c->batch, c->states, (cudaStream_t)stream);
-    return e == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    return status_of(e);
 }
 
 extern "C" size_t evs_selective_scan_workspace(int32_t batch, int32_t tokens, int32_t width, int32_t states) {

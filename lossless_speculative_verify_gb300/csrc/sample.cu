@@ -984,5 +984,5 @@ extern "C" evs_status evs_sample(const evs_sample_args* c, void* stream) {
     if (c->rows > (1 << 24) || !c->logits || !c->token || !c->uniforms) return EVS_ERR_INVALID_ARG;
     if ((uintptr_t)c->logits % (c->dtype == EVS_DTYPE_BF16 ? 2 : 4)) return EVS_ERR_INVALID_ARG;
     if (c->probs && c->probs_ld < c->vocab) return EVS_ERR_INVALID_ARG;
-    return launch_sample(*c, (cudaStream_t)stream) == cudaSuccess ? EVS_OK : EVS_ERR_CUDA;
+    return status_of(launch_sample(*c, (cudaStream_t)stream));
 }

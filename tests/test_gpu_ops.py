@@ -3,6 +3,7 @@ tile and page edges, ragged and empty lengths, ties, masks, infinities and NaN w
 read them, strides, streams, captured graphs, and a run of all four as a decode step uses them.
 
 Tolerances count roundings: half a step of bf16 is 2^-8 of the value, of fp32 u = 2^-24."""
+import contextlib
 import math
 
 import numpy as np
@@ -794,6 +795,25 @@ def test_conv_strides_and_lengths(evs):
     assert torch.equal(t0, t1)
 
 
+@contextlib.contextmanager
+def invalid_capture():
+    """A stream in a capture that has become invalid: the host's runtime refuses every launch on it."""
+    import ctypes
+    # torch's runtime, as loaded into this process
+    rt = ctypes.CDLL(next(p for p in open("/proc/self/maps").read().split() if "libcudart.so" in p))
+    rt.cudaStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    rt.cudaStreamSynchronize.argtypes = rt.cudaStreamDestroy.argtypes = [ctypes.c_void_p]
+    rt.cudaStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    assert rt.cudaStreamBeginCapture(stream, 2) == 0                 # relaxed: other streams of the thread as ever
+    assert rt.cudaStreamSynchronize(stream) != 0                     # not permitted: the capture is invalid now
+    yield stream
+    assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    rt.cudaGetLastError()
+    assert rt.cudaStreamDestroy(stream) == 0
+
+
 def test_an_earlier_call_that_failed_is_not_reported_again(evs):
     """A draw on a stream whose capture has become invalid fails, on the host; the calls after it on a sound stream
     succeed. (The runtime that the library links keeps the last error of a thread until somebody asks for it.)"""
@@ -808,22 +828,48 @@ def test_an_earlier_call_that_failed_is_not_reported_again(evs):
     a = _lib.SampleArgs(rows=2, vocab=100, dtype=0, ld=100, logits=l.data_ptr(), uniforms=u.data_ptr(),
                         token=tok.data_ptr())
     torch.cuda.synchronize()
-    # torch's runtime, as loaded into this process
-    path = next(p for p in open("/proc/self/maps").read().split() if "libcudart.so" in p)
-    rt = ctypes.CDLL(path)
-    rt.cudaStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
-    rt.cudaStreamSynchronize.argtypes = rt.cudaStreamDestroy.argtypes = [ctypes.c_void_p]
-    rt.cudaStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
-    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
-    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
-    assert rt.cudaStreamBeginCapture(stream, 2) == 0                 # relaxed: other streams of the thread as ever
-    assert rt.cudaStreamSynchronize(stream) != 0                     # not permitted: the capture is invalid now
-    assert lib.evs_sample(ctypes.byref(a), stream) == 4              # EVS_ERR_CUDA
-    assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0
-    rt.cudaGetLastError()
-    assert rt.cudaStreamDestroy(stream) == 0
+    with invalid_capture() as stream:
+        assert lib.evs_sample(ctypes.byref(a), stream) == 4          # EVS_ERR_CUDA
     assert torch.equal(evs.causal_conv(x, w, tail=tail), want)
     assert torch.equal(evs.sample(l, u), evs.sample(l, u))
+
+
+def test_a_failed_operator_leaves_no_error_to_a_handle(evs):
+    """Each operator fails on a stream whose capture has become invalid; a Verifier's next decode step is sound."""
+    import ctypes
+    from gpu_harness import Pair
+    from synth import get_workload
+    from lossless_speculative_verify_gb300 import _lib
+    pair = Pair(get_workload("tiny_d64_fp32"), t_max=100)
+    pair.ver.prefill(torch.randint(65, 85, (1, 9), dtype=torch.int32, device="cuda"))
+    tok = col(1, 67, torch.int32)
+    u = col(1, 0.5)
+    d, s = make_attn(35, BF16, 1, 1, 1, 2, 2, 64, 20, 10, [3]), make_scan(36, 1, 3, 64, 16, F32)
+    y, w = torch.empty_like(s["x"]), torch.ones(64, 4, device="cuda")
+    o, ws = torch.empty_like(d["q"]), torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    l = torch.zeros(1, 100, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    calls = [("evs_sample", _lib.SampleArgs(rows=1, vocab=100, dtype=0, ld=100, logits=p(l), uniforms=p(u), token=p(tok))),
+             ("evs_causal_conv", _lib.ConvArgs(batch=1, tokens=3, width=64, taps=4, dtype=0, x=p(s["x"]), x_ld=64,
+                                               x_seq=192, y=p(y), y_ld=64, y_seq=192, weight=p(w))),
+             ("evs_selective_scan", _lib.ScanArgs(
+                 batch=1, tokens=3, width=64, states=16, dtype=0, x=p(s["x"]), x_ld=64, x_seq=192, dt=p(s["dt"]), dt_ld=64,
+                 dt_seq=192, B=p(s["B"]), b_ld=16, b_seq=48, C=p(s["C"]), c_ld=16, c_seq=48, y=p(y), y_ld=64, y_seq=192,
+                 A=p(s["A"]))),
+             ("evs_shared_attention", _lib.SharedAttnArgs(
+                 batch=1, n_cand=1, block=1, heads=2, kv_heads=2, head_dim=64, dtype=1, q_dtype=1, prefix=20, own_max=10,
+                 q=p(d["q"]), q_ld=128, k_prefix=p(d["kp"]), v_prefix=p(d["vp"]), prefix_row=64, prefix_head=1280,
+                 k_own=p(d["ko"]), v_own=p(d["vo"]), own_row=64, own_head=640, own_seq=1280, own_len=p(d["own"]),
+                 k_block=p(d["kb"]), v_block=p(d["vb"]), block_row=64, block_head=64, block_cand=128, o=p(o), o_ld=128,
+                 workspace=p(ws), ws_bytes=1 << 22))]
+    torch.cuda.synchronize()
+    with invalid_capture() as stream:
+        status = [getattr(evs.load(), name)(ctypes.byref(a), stream) for name, a in calls]
+    assert status == [4] * 4                                         # EVS_ERR_CUDA
+    pair.ver.decode_filtered(tok, u)
+    assert pair.ver.flags() == 0
+    assert [getattr(evs.load(), name)(ctypes.byref(a), None) for name, a in calls] == [0] * 4
+    torch.cuda.synchronize()
 
 
 def make_scan(seed, B, T, D, N, dtype):
