@@ -6,7 +6,8 @@ states the mathematics) and enqueues it on the current stream of the tensors' de
 torch operator: outputs and workspaces come from torch's allocator, calls may be captured into
 CUDA graphs, nothing synchronises. Inputs that are not what an operator takes raise ValueError
 before anything is enqueued. Outputs share no memory with inputs, but for the state or tail that
-is carried in place. There are no gradients: a first argument that asks for one is refused.
+is carried in place. There are no gradients: while they are enabled, a tensor that asks for one is
+refused, whichever argument it is (``torch.no_grad()`` or ``detach()`` lets it in).
 ``flags`` is an int32 tensor of one element that collects EVS_FLAG_* bits.
 """
 from __future__ import annotations
@@ -27,6 +28,11 @@ def _p(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _no_grad(name, t):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: this operator has no gradient")
+
+
 def _vec(name, t, dtype, shape, dev):
     """Address of a contiguous tensor of the given type and shape on dev, or 0."""
     if t is None:
@@ -34,6 +40,7 @@ def _vec(name, t, dtype, shape, dev):
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
             t.device == dev):
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}")
+    _no_grad(name, t)
     return t.data_ptr()
 
 
@@ -41,6 +48,7 @@ def _rows3(name, t, dtype, shape, dev, written=False):
     """Strides (row, sequence) of a [batch, tokens, n] tensor whose last dimension is contiguous."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    _no_grad(name, t)
     b, n, w = shape
     sq, ld, one = t.stride()
     ld = ld if n > 1 else w
@@ -69,8 +77,7 @@ def _enqueue(fn, where, args, dev):
 def _device(name, t):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise ValueError(f"{name}: want a CUDA tensor")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name}: this operator has no gradient")
+    _no_grad(name, t)
     return t.device
 
 
@@ -193,6 +200,7 @@ def _kv(name, k, v, dtype, shape, dev):
     for which, t in (("k_", k), ("v_", v)):
         if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
             raise ValueError(f"{which}{name}: want {dtype} {tuple(shape)} on {dev}")
+        _no_grad(which + name, t)
     st = k.stride()
     if st[-1] != 1:
         raise ValueError(f"k_{name}: the head dimension has to be contiguous")
@@ -205,6 +213,7 @@ def _flat(name, t, dtype, shape, dev):
     """Row stride of a [batch, candidates, block, heads, dh] tensor whose rows are evenly spaced."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    _no_grad(name, t)
     B, Cn, T, H, dh = shape
     s0, s1, s2, s3, s4 = t.stride()
     if not (s4 == 1 and (H == 1 or s3 == dh)):

@@ -660,6 +660,31 @@ def test_no_gradients(evs):
         assert evs.sample(l, u).shape == (2,) and evs.causal_conv(x, w).shape == (1, 4, 8)
 
 
+def test_no_gradients_of_any_argument(evs):
+    """Weights, states and caches that ask for a gradient are refused like the first argument, not detached."""
+    l, u = make_logits(26, 2, 100)
+    s, d = make_scan(27, 2, 5, 64, 16, F32), make_attn(28, F32, 2, 1, 3, 4, 2, 16, 20, 10, [3, 10])
+    x, w, bias, tail = s["x"], torch.ones(64, 4, device="cuda"), torch.zeros(64, device="cuda"), torch.zeros(2, 3, 64, device="cuda")
+    t, p, m = col(2, 0.9), col(2, 0.8), col(2, 0.1)
+    out, so, to = torch.empty_like(x), torch.empty_like(s["state"]), torch.empty_like(tail)
+    o = torch.empty_like(d["q"])
+    draw = lambda: evs.sample(l, u, temperature=t, top_p=p, min_p=m)  # noqa: E731
+    conv = lambda: evs.causal_conv(x, w, bias, tail=tail, tail_out=to, out=out)  # noqa: E731
+    scan = lambda: evs.selective_scan(x, s["dt"], s["A"], s["B"], s["C"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"],  # noqa: E731
+                                      state=s["state"], state_out=so, out=out)
+    attn = lambda: run_attn(evs, d, out=o)  # noqa: E731
+    for call, tensors in ((draw, (l, u, t, p, m)), (conv, (x, w, bias, tail, to, out)),
+                          (scan, (*s.values(), so, out)), (attn, (*(v for k, v in d.items() if k != "own"), o))):
+        call()
+        for leaf in tensors:
+            leaf.requires_grad_()
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+            with torch.no_grad():
+                call()
+            leaf.requires_grad_(False)
+
+
 def test_decode_filtered(evs):
     """The decode step's own path: its logits, drawn with filters; the state as after a plain step."""
     from gpu_harness import Pair
