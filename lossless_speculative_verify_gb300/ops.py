@@ -62,6 +62,12 @@ def _rows3(name, t, dtype, shape, dev, written=False):
     return ld, sq
 
 
+def _fresh(b, n, w, x, lens):
+    """An output like x; with lengths the operator leaves rows unwritten, which are zero then."""
+    make = torch.empty if lens is None else torch.zeros
+    return make(b, n, w, dtype=x.dtype, device=x.device)
+
+
 def _enqueue(fn, where, args, dev):
     # (the stream object that torch.cuda.current_stream builds costs 2 us a call)
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
@@ -120,7 +126,7 @@ def causal_conv(x, weight, bias=None, *, tail=None, tail_out=None, lens=None, si
     weight [width, taps] fp32 (2 to 16 taps; weight[c, j] multiplies x[t - j]), bias [width] fp32 or None; tail
     and tail_out [batch, taps - 1, width] fp32, oldest first: the inputs before the first token, and the last
     ones after lens[b] tokens (they may be one tensor). lens [batch] int32 or None. Rows past a sequence's
-    length are left as they were in ``out``. Returns out, or None with output=False (only the tail moves on:
+    length are left as they were in ``out``, and zero where none is given. Returns out, or None with output=False (only the tail moves on:
     slicing at position k is lens = k + 1)."""
     dev = _device("x", x)
     _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
@@ -133,7 +139,7 @@ def causal_conv(x, weight, bias=None, *, tail=None, tail_out=None, lens=None, si
     y_ld = y_sq = 0
     y = None
     if output:
-        y = torch.empty(B, T, D, dtype=x.dtype, device=dev) if out is None else out
+        y = _fresh(B, T, D, x, lens) if out is None else out
         y_ld, y_sq = _rows3("out", y, x.dtype, (B, T, D), dev, written=True)
         _need(y.data_ptr() != x.data_ptr() or y.numel() == 0, "out: may not be x")
     else:
@@ -156,7 +162,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
     [batch, tokens, states] and gate z (like x, or None), all fp32 or all bf16; A [width, states] fp32, states
     4, 8, 16 or 32; D, dt_bias [width] fp32 or None; state, state_out [batch, width, states] fp32 or None (they
     may be one tensor); lens [batch] int32 or None. Rows past a sequence's length are left as they were in
-    ``out``. Returns out, or None with output=False (only the state moves on)."""
+    ``out``, and zero where none is given. Returns out, or None with output=False (only the state moves on)."""
     dev = _device("x", x)
     _need(x.dim() == 3 and x.dtype in _DT and x.shape[2] > 0, "x: want fp32 or bf16 [batch, tokens, width]")
     Bn, T, W = x.shape
@@ -171,7 +177,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
     y_ld = y_sq = 0
     y = None
     if output:
-        y = torch.empty(Bn, T, W, dtype=x.dtype, device=dev) if out is None else out
+        y = _fresh(Bn, T, W, x, lens) if out is None else out
         y_ld, y_sq = _rows3("out", y, x.dtype, (Bn, T, W), dev, written=True)
         if y.data_ptr() in (x.data_ptr(), dt.data_ptr(), _p(z)) and y.numel() > 0:
             raise ValueError("out: may not be x, dt or z")

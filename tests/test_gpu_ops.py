@@ -1055,6 +1055,23 @@ def test_scan_strides_lengths_refusals(evs):
             evs.selective_scan(**{**args, **bad})
 
 
+@pytest.mark.parametrize("T", [1, 7, 40, 600])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_rows_past_the_lengths_of_an_own_output(evs, T, dtype):
+    """Without an output tensor the rows behind a sequence's length are zero, in memory that held NaN."""
+    lens = [T, 0, T // 2]
+    s = make_scan(46, 3, T, 64, 16, dtype)
+    w = randn(gen(47), 64, 4)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for run in (lambda o: evs.causal_conv(s["x"], w, lens=lt, out=o),
+                lambda o: evs.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], lens=lt, out=o)):
+        want = run(torch.zeros_like(s["x"]))
+        poison(s["x"].numel() * s["x"].element_size())
+        got = run(None)
+        assert torch.equal(got, want)
+        assert all(torch.all(got[b, n:] == 0.0) for b, n in enumerate(lens))
+
+
 def test_recurrent_captured(evs):
     s = make_scan(44, 2, 50, 64, 16, BF16)
     w = randn(gen(45), 64, 4)
