@@ -26,8 +26,10 @@ using bf16 = __nv_bfloat16;
 // What both launches know. A partial of a shared row r of K/V head g (r = m * group + head in the
 // group, m = (b * C + c) * T + i) lies in segment g * sh_tiles + r / sh_rows, row r % sh_rows; of
 // an own row r = (c * T + i) * group + head in segment (b * G + g) * own_tiles + r / own_rows.
-// Segments have `slots` partials. o is stored four columns at a time, [dh / 4][rows to a multiple
-// of four][4], so that both the threads that write it (one a row) and those that read it (four
+// On CUDA cores a segment has `slots` partials, slot s of segment g is partial g * slots + s. On the
+// tensor cores worker w's of segment g is partial w + g: the pieces of the axis in order step on to the
+// next worker, the next segment or both, so no two share a number, and workers + segments are enough
+// whatever the lengths. o is stored four columns at a time, [dh / 4][rows to a multiple of four][4], so that both the threads that write it (one a row) and those that read it (four
 // columns each) touch consecutive addresses.
 struct SharedArgs {
     const void *q, *kp, *vp, *ko, *vo, *kb, *vb;
@@ -38,11 +40,11 @@ struct SharedArgs {
     int64_t q_ld, o_ld, p_row, p_head, o_row, o_head, o_seq, b_row, b_head, b_cand;
     int B, C, T, H, G, dh, P, own_max, own_skip, q_bf16;
     float scale;
-    float *sh_o, *own_o;       // [segment][slot][dh / 4][rows4][4]
-    float2 *sh_ml, *own_ml;    // [segment][slot][rows] (m, l), natural units
+    float *sh_o, *own_o;       // [partial][dh / 4][rows4][4]
+    float2 *sh_ml, *own_ml;    // [partial][rows] (m, l), natural units
     int sh_rows, sh_tiles, sh_slots, own_rows, own_tiles, own_slots;
     int partials;              // a partial kernel runs
-    int tensor;                // the tensor-core kernel's partials: slots by its runs of tiles
+    int tensor;                // the tensor-core kernel's partials (sh_slots: at most so many of a segment)
     int sh_pair, own_pair;     // 1: segments of up to 256 rows, a row tile a lane; 0: a lane of its own
     int* plan;                 // run lengths (shared, own), where own runs start, own costs before sequence b
     int q_vec, b_vec;          // q and block rows on 16 (8) bytes
@@ -263,7 +265,7 @@ __device__ __forceinline__ float st_max3(float a, float b, float c) {
 // A worker's share of a segment: tiles t0 .. t0 + n - 1 of its nt, over `keys` keys; start: where
 // the segment lies on the axis; seg numbers the prefix's segments or the own rows' ones.
 struct Piece {
-    int sh, b, g, rt, t0, n, nt, keys, slot, seg, start;
+    int sh, b, g, rt, t0, n, nt, keys, seg, start;
 };
 
 template <int DH, int NST>
@@ -402,7 +404,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         }
         p.t0 = max(0, lo - p.start - ST_OVER);
         p.n = max(0, min(p.nt, hi - p.start - ST_OVER) - p.t0);
-        p.slot = worker - (p.start + ST_OVER) / W;
         return p;
     };
     auto next_piece = [&](const Piece& c) -> Piece {
@@ -411,7 +412,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         p.n = 0;
         if (p.start >= hi) return p;
         p.t0 = 0;
-        p.slot = 0;                               // the first run that meets its segment
         ++p.seg;
         if (++p.rt == (c.sh ? a.sh_tiles : a.own_tiles)) {
             p.rt = 0;
@@ -726,7 +726,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
         }
         if (work) {
-            const int64_t at = (int64_t)p.seg * (p.sh ? a.sh_slots : a.own_slots) + p.slot;
+            const int64_t at = worker + p.seg;
             const int ld = rows4(seg_rows) * 4;
             float* dst = (p.sh ? a.sh_o : a.own_o) + at * rows4(seg_rows) * DH + r_seg * 4;
             if (ok) {
@@ -880,8 +880,6 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
     if (a.partials) {
         pdl_wait();
         pdl_trigger();
-        // the runs that a segment's nt tiles from position at on meet
-        auto runs = [&](int at, int nt, int W) { return (at + nt - 1) / W - at / W + 1; };
         // The row's partials: those of the prefix, dealt among the groups but the last, and those of
         // the own rows, the last group's
         constexpr int PB = 8;                      // in flight
@@ -891,6 +889,12 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
             const float* o_at;
             const float2* ml_at;
             int rows_seg, s = 0, step = 1, used = 0;
+            int64_t first;                         // partial
+            // the runs that a segment's nt tiles from position at on meet
+            auto runs = [&](int at, int nt, int W) {
+                first = at / W;
+                used = (at + nt - 1) / W - at / W + 1;
+            };
             if (kind == 0) {
                 if (!live || a.P == 0) continue;
                 const int r = (int)(m * grp + hg), t = r / a.sh_rows, in = r - t * a.sh_rows;
@@ -898,22 +902,31 @@ __global__ void __launch_bounds__(128 * SC_GROUPS) shared_combine_kernel(SharedA
                 rows_seg = a.sh_rows;
                 s = part_of;
                 step = dealt;
-                ml_at = a.sh_ml + (int64_t)seg * a.sh_slots * rows_seg + in;
-                o_at = a.sh_o + ((int64_t)seg * a.sh_slots * DH + c4 * 4) * rows4(rows_seg) + in * 4;
-                used = a.tensor ? runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]) : a.sh_slots;
+                if (a.tensor) {
+                    runs(seg * (nt + ST_OVER) + ST_OVER, nt, a.plan[0]);
+                    first += seg;
+                } else {
+                    first = (int64_t)seg * a.sh_slots;
+                    used = a.sh_slots;
+                }
+                ml_at = a.sh_ml + first * rows_seg + in;
+                o_at = a.sh_o + (first * DH + c4 * 4) * rows4(rows_seg) + in * 4;
             } else {
                 if (!live || own == 0) continue;
                 const int t = r_own / a.own_rows, in = r_own - t * a.own_rows, in_b = g * a.own_tiles + t;
                 const int per_b = a.G * a.own_tiles;
                 const int64_t seg = (int64_t)b * per_b + in_b;
                 rows_seg = a.own_rows;
-                ml_at = a.own_ml + seg * a.own_slots * rows_seg + in;
-                o_at = a.own_o + (seg * a.own_slots * DH + c4 * 4) * rows4(rows_seg) + in * 4;
-                used = a.own_slots;
                 if (a.tensor) {
                     const int before = a.plan[3 + b], cost = a.plan[4 + b] - before;
-                    used = runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
+                    runs(a.plan[2] + per_b * before + in_b * cost + ST_OVER, cost - ST_OVER, a.plan[1]);
+                    first += seg;
+                } else {
+                    first = seg * a.own_slots;
+                    used = a.own_slots;
                 }
+                ml_at = a.own_ml + first * rows_seg + in;
+                o_at = a.own_o + (first * DH + c4 * 4) * rows4(rows_seg) + in * 4;
             }
             const int64_t ml_step = (int64_t)step * rows_seg, o_step = (int64_t)step * DH * rows4(rows_seg);
             ml_at += (int64_t)s * rows_seg;
@@ -1024,9 +1037,8 @@ bool tensor_ok(const evs_shared_attn_args& c) {
     return true;
 }
 
-// Tiles, slots and grid. A segment of nt tiles meets at most (nt - 1) / W + 2 runs, and a run is at
-// least the segments' cost over the workers; the own lengths are known only on the device, the
-// bound at their capacity is the largest. false: sizes past the kernel's 32-bit positions.
+// Tiles, slots and grid. A prefix segment of nt tiles meets at most (nt - 1) / W + 2 runs, and a run is
+// at least the segments' cost over the workers. false: sizes past the kernel's 32-bit positions.
 bool plan_tensor(const evs_shared_attn_args& c, SharedArgs& a, int& grid) {
     const int grp = c.heads / c.kv_heads;
     const long long sh = (long long)c.batch * c.n_cand * c.block * grp, own = (long long)c.n_cand * c.block * grp;
@@ -1041,26 +1053,23 @@ bool plan_tensor(const evs_shared_attn_args& c, SharedArgs& a, int& grid) {
     const long long tiles = shs * ntp + c.batch * owns * nto;
     if (tiles + shs * ST_OVER + c.batch * owns * ST_OVER >= (1LL << 30)) return false;
     grid = (int)(tiles < kAttnGrid ? tiles : kAttnGrid);
-    auto bound = [&](long long nt, long long segs, int pair) {
-        const long long s = nt ? nt * grid * (2 - pair) / (segs * (nt + ST_OVER)) + 2 : 0;
-        return (int)(s < nt ? s : nt);
-    };
-    a.sh_slots = bound(ntp, shs, a.sh_pair);
-    a.own_slots = bound(nto, owns, a.own_pair);
+    const long long s = ntp ? ntp * grid * (2 - a.sh_pair) / (shs * (ntp + ST_OVER)) + 2 : 0;
+    a.sh_slots = (int)(s < ntp ? s : ntp);
     a.tensor = 1;
     return true;
 }
 
 // Lays the partials out from base (or sizes them).
-size_t carve_partials(const evs_shared_attn_args& c, SharedArgs& a, char* base) {
+size_t carve_partials(const evs_shared_attn_args& c, SharedArgs& a, int grid_tc, char* base) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         char* p = base ? base + off : nullptr;
         off = round256(off + bytes);
         return p;
     };
-    const size_t sh = (size_t)c.kv_heads * a.sh_tiles * a.sh_slots;
-    const size_t own = (size_t)c.batch * c.kv_heads * a.own_tiles * a.own_slots;
+    size_t sh = (size_t)c.kv_heads * a.sh_tiles, own = (size_t)c.batch * c.kv_heads * a.own_tiles;   // segments
+    sh = c.prefix == 0 ? 0 : a.tensor ? sh + (size_t)grid_tc * (2 - a.sh_pair) : sh * a.sh_slots;
+    own = c.own_max == 0 ? 0 : a.tensor ? own + (size_t)grid_tc * (2 - a.own_pair) : own * a.own_slots;
     a.sh_o = (float*)take(sh * rows4(a.sh_rows) * c.head_dim * 4);
     a.own_o = (float*)take(own * rows4(a.own_rows) * c.head_dim * 4);
     a.sh_ml = (float2*)take(sh * a.sh_rows * 8);
@@ -1145,7 +1154,7 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     a.b_vec = ((uintptr_t)(in_cache ? c.k_own : c.k_block) | (uintptr_t)(in_cache ? c.v_own : c.v_block)) % (4 * es) == 0 &&
               b0 % 4 == 0 && b1 % 4 == 0 && b2 % 4 == 0;
     a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld * (a.q_bf16 ? 2 : 4) % 16 == 0;
-    carve_partials(c, a, (char*)c.workspace);
+    carve_partials(c, a, grid_tc, (char*)c.workspace);
     const int sh_items = c.kv_heads * a.sh_slots * ((a.sh_rows + SA_Q - 1) / SA_Q);
     const int own_items = c.batch * c.kv_heads * a.own_slots * ((a.own_rows + SA_Q - 1) / SA_Q);
     a.partials = tensor || sh_items + own_items > 0;
@@ -1185,9 +1194,9 @@ extern "C" size_t evs_shared_attention_workspace(const evs_shared_attn_args* c) 
     SharedArgs a{}, t{};
     int grid = 0;
     plan_simt(*c, a);
-    size_t n = carve_partials(*c, a, nullptr);
+    size_t n = carve_partials(*c, a, 0, nullptr);
     if (c->dtype == EVS_DTYPE_BF16 && (c->head_dim == 64 || c->head_dim == 128) && plan_tensor(*c, t, grid)) {
-        const size_t m = carve_partials(*c, t, nullptr);
+        const size_t m = carve_partials(*c, t, grid, nullptr);
         n = m > n ? m : n;
     }
     return n ? n : 256;

@@ -113,6 +113,42 @@ def test_attention_matches_definition(evs, case):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])       # no order left to chance
 
 
+def attn_args(L, d, **kw):
+    """The C entry point's arguments for contiguous tensors; the caller keeps o, lse and the workspace."""
+    B, C, T, H, dh = d["q"].shape
+    (G, P, _), S = d["kp"].shape, d["ko"].shape[2]
+    dt = {BF16: 1, F32: 0}
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    base = dict(batch=B, n_cand=C, block=T, heads=H, kv_heads=G, head_dim=dh, dtype=dt[d["kp"].dtype],
+                q_dtype=dt[d["q"].dtype], prefix=P, own_max=S, q=p(d["q"]), q_ld=H * dh, k_prefix=p(d["kp"]),
+                v_prefix=p(d["vp"]), prefix_row=dh, prefix_head=P * dh, k_own=p(d["ko"]), v_own=p(d["vo"]), own_row=dh,
+                own_head=S * dh, own_seq=G * S * dh, own_len=p(d["own"]), k_block=p(d["kb"]), v_block=p(d["vb"]),
+                block_row=dh, block_head=T * dh, block_cand=G * T * dh, o_ld=H * dh)
+    base.update(kw)
+    return L.SharedAttnArgs(**base)
+
+
+@pytest.mark.parametrize("case", ATTN, ids=lambda c: "-".join(str(x) for x in c[1:9]) + ("b" if c[0] == BF16 else "f"))
+def test_attention_keeps_to_its_workspace(evs, case):
+    """The bytes asked for and no others, from lengths of nothing to all of the capacity."""
+    import ctypes
+    from lossless_speculative_verify_gb300 import _lib
+    dtype, B, C, T, H, G, dh, P, S, own = case
+    d = make_attn(B * 1000 + P, dtype, B, C, T, H, G, dh, P, S, own)
+    o, lse = torch.empty_like(d["q"]), torch.empty(B, C, T, H, device="cuda")
+    n = evs.load().evs_shared_attention_workspace(ctypes.byref(attn_args(_lib, d)))
+    ws = torch.empty(n + 65536, dtype=torch.uint8, device="cuda")
+    args = attn_args(_lib, d, o=o.data_ptr(), lse=lse.data_ptr(), workspace=ws.data_ptr(), ws_bytes=n)
+    for lens in (own, [0] * B, [S] * B, [S if b % 3 else 1 for b in range(B)]):
+        d["own"].copy_(torch.tensor(lens, dtype=torch.int32))
+        ws.fill_(0xff)                                               # NaN, where a partial was not written
+        assert evs.load().evs_shared_attention(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.all(ws[n:] == 0xff)
+        want = run_attn(evs, d)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.isfinite(o.float()).all() or S == 0 and P == 0
+
+
 @pytest.mark.parametrize("dh,dtype", [(128, BF16), (64, BF16), (32, BF16), (16, F32)])
 def test_attention_block_rows_in_the_cache(evs, dh, dtype):
     """Without block tensors the block is own rows own_len + j; past the capacity they are left out."""

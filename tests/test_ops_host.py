@@ -125,6 +125,37 @@ def test_attention_workspace(L):
     assert lib.evs_shared_attention_workspace(C.byref(_attn(L, prefix=100000))) >= n
 
 
+def _bytes(L, **kw):
+    return L.load().evs_shared_attention_workspace(C.byref(_attn(L, **kw)))
+
+
+@pytest.mark.parametrize("shape", [
+    dict(batch=64, heads=64, kv_heads=8, head_dim=128, block=16, prefix=8192),
+    dict(batch=1024, heads=64, kv_heads=8, head_dim=128, block=1, prefix=0),
+    dict(batch=256, heads=32, kv_heads=32, head_dim=64, block=13, n_cand=4, prefix=1000),
+    dict(batch=3, heads=8, kv_heads=1, head_dim=128, block=128, n_cand=4, prefix=100)], ids=str)
+def test_attention_workspace_is_what_the_kernels_can_fill(L, shape):
+    """Partials number at most the workers (two on each of 152 SMs) and the segments, of the prefix and of the own
+    rows, each of up to 256 query rows; the CUDA-core kernel's, which share the memory, at most four waves of CTAs
+    of 16 rows besides one for each. However long the own rows may get, no more is asked for."""
+    c = dict(n_cand=1)
+    c.update(shape)
+    grp, per = c["heads"] // c["kv_heads"], c["n_cand"] * c["block"]
+
+    def partial_rows(rows, segs):
+        tensor = (segs * ((rows + 255) // 256) + 2 * 152) * min(rows + 3, 256)
+        simt = (segs * ((rows + 15) // 16) + 4 * 152) * 16
+        return max(tensor, simt)
+
+    rows = partial_rows(per * grp, c["batch"] * c["kv_heads"])
+    if c["prefix"]:
+        rows += partial_rows(c["batch"] * per * grp, c["kv_heads"])
+    most = rows * (c["head_dim"] + 2) * 4 + 8192
+    for own_max in (4096, 32768, 1 << 20):
+        n = _bytes(L, own_max=own_max, **shape)
+        assert 0 < n <= most, (n, most)
+
+
 def test_decode_filtered_refuses(L):
     lib = L.load()
     assert lib.evs_decode_filtered(None, None, None, None) == INV
