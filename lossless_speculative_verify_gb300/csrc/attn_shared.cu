@@ -224,9 +224,6 @@ constexpr int ST_KEYS = 128;
 constexpr int ST_THREADS = 384;
 constexpr float ST_RESCALE_LOG2 = 8.f;
 
-__device__ __forceinline__ uint32_t st_sw128(int row, int chunk16) {
-    return (uint32_t)row * 128u + ((uint32_t)(chunk16 ^ (row & 7)) << 4);
-}
 __device__ __forceinline__ uint32_t st_pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -278,7 +275,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
     constexpr uint32_t O_COL = 256;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot[1];
-    __shared__ volatile int abort_flag[1];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* sQ = smem;                                        // [2 lanes][halves][128 rows][128 B]
@@ -358,7 +354,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
             mbar_init(&turn[i], 4);
             mbar_init(&drain[i], 1);
         }
-        *abort_flag = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -461,7 +456,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                 }
                 if (!ok) {
                     // loads in flight into this CTA's shared memory end before it does (bounded)
-                    *abort_flag = 1;
                     for (int i = 0; i < nslots; ++i)
                         if (used >> i & 1u) mbar_wait(&full[slot0 + i], i < s ? ph ^ 1u : ph);
                 }
@@ -540,7 +534,6 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
                     tc_commit(&pv_done[L]);
                 }
             }
-            if (!ok) *abort_flag = 1;
             tc_commit(&drain[L]);                 // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
         }
@@ -721,10 +714,7 @@ shared_tc_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant
         // looks at the flag (a row of NaN scores leaves the same pair).
         if (ok && !wait_all(&pv_done[L], (cnt - 1) & 1u)) ok = false;
         tc_fence_after();
-        if (!ok && lane == 0) {
-            *abort_flag = 1;
-            if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
-        }
+        if (!ok && lane == 0 && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
         if (work) {
             const int64_t at = worker + p.seg;
             const int ld = rows4(seg_rows) * 4;
