@@ -60,12 +60,12 @@ template <> __device__ __forceinline__ float exp_of<bf16>(float x) { return __ex
 // Own rows of sequence b, clamped to [0, own_max].
 __device__ __forceinline__ int own_rows_of(const SharedArgs& a, int b, bool report) {
     if (!a.own_len) return 0;
-    const int n = __ldcg(a.own_len + b) - a.own_skip;
+    const int64_t n = (int64_t)__ldcg(a.own_len + b) - a.own_skip;   // any two 32-bit values
     if (n < 0 || n > a.own_max) {
         if (report && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_BAD_LEN);
         return n < 0 ? 0 : a.own_max;
     }
-    return n;
+    return (int)n;
 }
 
 // A query enters its products in the type of K: fp32 queries of a bf16 cache are rounded to bf16 in

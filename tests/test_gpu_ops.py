@@ -149,6 +149,33 @@ def test_attention_keeps_to_its_workspace(evs, case):
         assert torch.isfinite(o.float()).all() or S == 0 and P == 0
 
 
+@pytest.mark.parametrize("dh,dtype", [(128, BF16), (16, F32)])
+@pytest.mark.parametrize("block", [True, False], ids=["block", "cache"])
+def test_attention_lengths_that_count_other_rows(evs, dh, dtype, block):
+    """own_skip of a length are rows elsewhere; differences that pass 32 bits are clamped to their own side."""
+    import ctypes
+    from lossless_speculative_verify_gb300 import _lib
+    own, S = [0, 100, 37], 120
+    d = make_attn(19, dtype, 3, 1, 4, 4, 2, dh, 300, S, own, block=block)
+    big = 2 ** 31 - 1
+    behind = 0 if block else 1                                       # EVS_FLAG_KV_OVERFLOW: no block rows behind the last
+    for skip, lens, plain, flag in ((200, [n + 200 for n in own], own, 0), (-3, [n - 3 for n in own], own, 0),
+                                    (5, [-big - 1, 4, 50], [0, 0, 45], 32),
+                                    (-5, [big, 40, 0], [S, 45, 5], 32 | behind)):
+        want = run_attn(evs, dict(d, own=torch.tensor(plain, dtype=torch.int32, device="cuda")))
+        e = dict(d, own=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        o, lse, flags = torch.empty_like(d["q"]), torch.empty(3, 1, 4, 4, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        extra = {} if block else dict(block_row=0, block_head=0, block_cand=0)
+        args = attn_args(_lib, dict(e, kb=d["kb"], vb=d["vb"]), own_skip=skip, o=o.data_ptr(), lse=lse.data_ptr(),
+                         flags=flags.data_ptr(), **extra)
+        n = evs.load().evs_shared_attention_workspace(ctypes.byref(args))
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        args.workspace, args.ws_bytes = ws.data_ptr(), n
+        assert evs.load().evs_shared_attention(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), (skip, lens)
+        assert int(flags) == flag
+
+
 @pytest.mark.parametrize("dh,dtype", [(128, BF16), (64, BF16), (32, BF16), (16, F32)])
 def test_attention_block_rows_in_the_cache(evs, dh, dtype):
     """Without block tensors the block is own rows own_len + j; past the capacity they are left out."""
