@@ -57,7 +57,8 @@ def _rows3(name, t, dtype, shape, dev, written=False):
         raise ValueError(f"{name}: the last dimension has to be contiguous")
     if ld < w:
         raise ValueError(f"{name}: rows overlap")
-    if written and b > 1 and sq < w:
+    # one sequence behind the other, or all of them within the distance of two rows
+    if written and b > 1 and n > 0 and sq < (n - 1) * ld + w and not (sq >= w and ld >= (b - 1) * sq + w):
         raise ValueError(f"{name}: sequences overlap")
     return ld, sq
 

@@ -960,6 +960,26 @@ def test_a_failed_operator_leaves_no_error_to_a_handle(evs):
     torch.cuda.synchronize()
 
 
+def test_outputs_whose_sequences_overlap(evs):
+    """An output whose rows lie on one another is refused; sequence-major, token-major and padded ones are not."""
+    B, T, D = 3, 5, 32
+    s = make_scan(48, B, T, D, 8, F32)
+    w = randn(gen(49), D, 4)
+    conv = lambda o: evs.causal_conv(s["x"], w, out=o)  # noqa: E731
+    scan = lambda o: evs.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], out=o)  # noqa: E731
+    buf = torch.zeros(4096, device="cuda")
+    for run in (conv, scan):
+        want = run(None)
+        for seq, row in ((0, D), (D, D), (2 * D, D), (T * D - 1, D), (D - 1, 3 * D), (D, 3 * D - 1), (D, 2 * D), (4 * D + 3, D)):
+            with pytest.raises(ValueError, match="overlap"):
+                run(buf.as_strided((B, T, D), (seq, row, 1)))
+        for seq, row in ((T * D, D), (D, B * D), (T * D + 7, D), (D + 4, 3 * D + 8), (4 * D + D, D)):
+            buf.fill_(7.0)
+            got = run(buf.as_strided((B, T, D), (seq, row, 1)))
+            assert torch.allclose(got, want, rtol=1e-5, atol=1e-5)     # unaligned rows take another instance
+            assert int((buf != 7.0).sum()) <= B * T * D
+
+
 def make_scan(seed, B, T, D, N, dtype):
     g = gen(seed)
     step = torch.exp(torch.rand(D, device="cuda", generator=g) * math.log(100.0) + math.log(1e-3))
