@@ -168,7 +168,7 @@ __device__ __forceinline__ u64 unit_fixed(float p, int bits, bool up, u64 one) {
 // ---- weights ------------------------------------------------------------------------------------
 // exp((l - M) / T) = 2^y, y = (l - M) * c with c = log2(e) / T held as the sum of two floats. The
 // difference and the product are formed exactly (two-sum, fused multiply-add remainders), so that
-// y = p + e; p = i/32 + r, |r| <= 1/64, i taken from the low bits of p + 1.5 * 2^18; and
+// y = p + e; p = i/32 + r, |r| <= 1/64, i taken from the low bits of p + 1.5 * 2^18 (one fused operation); and
 // 2^(r + e) - 1 = q + rest with q = r ln 2 rounded and rest its tail, q^2/2 + q^3/6 + q^4/24 and
 // e ln 2 * exp(q). In fixed point of 2^-34 the sum of the two is off by 2^-34 at most; times
 // 2^(i/32), a weight is within about 2^-33 of its value. Two logits at a time: 26 packed
@@ -218,7 +218,7 @@ struct WeightFn {
         const u64 dl = add2(sub2(l, sub2(dh, bb)), sub2(nM, bb));
         const u64 p = mul2(dh, ch);
         const u64 e = fma2(dl, ch, fma2(dh, pk(c_lo), fma2(dh, ch, mul2(dh, pk(-c_hi)))));
-        const u64 tn = add2(p, pk(kRound));
+        const u64 tn = fma2(dh, ch, pk(kRound));
         const u64 r = sub2(p, add2(tn, pk(-kRound)));
         const float L_hi = 0.693147182464599609375f, L_lo = -1.904654299957768e-09f;   // ln 2
         const u64 q = mul2(r, pk(L_hi));
@@ -250,15 +250,17 @@ struct WeightFn {
         fixed2(l, l, w0, w1);
         return w0;
     }
-    // p + 1.5 * 2^18 for two
+    // The step of 1/32 that parts() takes, of two. One fused operation wherever a bin is worked out, so
+    // that a token counted in a bin is ranked in it: a rounded product and a sum are one operation or two
+    // as the compiler finds in each place, and a token within 2^-23 of a border fell into two bins.
     __device__ __forceinline__ u64 step(float l0, float l1) const {
-        return add2(mul2(add2(pk(l0, l1), pk(-M)), pk(c_hi)), pk(kRound));
+        return fma2(add2(pk(l0, l1), pk(-M)), pk(c_hi), pk(kRound));
     }
     // Which step of 1/32 of the exponent: bins that ascend as the logit falls
     // (far from M the integer is no multiple of anything, but larger all the same)
     static __device__ __forceinline__ int bin(int i) { return (int)min((unsigned)-i, (unsigned)SMP_BINS - 1u); }
-    __device__ __forceinline__ int bin(float l) const {   // the product rounded before the sum, as there
-        return bin(__float_as_int(__fadd_rn(__fmul_rn(l - M, c_hi), kRound)) - __float_as_int(kRound));
+    __device__ __forceinline__ int bin(float l) const {
+        return bin(__float_as_int(__fmaf_rn(__fadd_rn(l, -M), c_hi, kRound)) - __float_as_int(kRound));
     }
     // The mass of a bin whose tokens' 1 + q + rest sum to s 2^-32
     __device__ __forceinline__ u64 mass(int b, u64 s) const {
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1) sample_kernel
             const float4 l4 = s < n ? *reinterpret_cast<const float4*>(l_s + s)
                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-            // the rounding that WeightFn::bin does, two at a time
+            // what WeightFn::bin rounds, two at a time
             const float2 a01 = unpk(wf.step(l4.x, l4.y)), a23 = unpk(wf.step(l4.z, l4.w));
             const float at_step[4] = {a01.x, a01.y, a23.x, a23.y};
             bool yes[4], mine = false;

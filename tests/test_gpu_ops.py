@@ -547,6 +547,33 @@ def test_sample_border_at_the_end_of_a_crowded_bin(evs):
     assert np.all(below == first), below
 
 
+@pytest.mark.parametrize("V,R", [(301, 512), (3000, 512), (20000, 64)])
+def test_sample_tokens_on_the_border_of_a_bin(evs, V, R):
+    """300 neighbouring floats around a border between two steps of 1/32 in the exponent, top-p's cut among the
+    later ones: whichever step a token is counted in has to be the one that it is ranked in."""
+    rng = np.random.default_rng(V)
+    n, cut = 300, 225
+    rows = np.full((R, V), -np.inf, np.float32)
+    t = (0.6 + 0.8 * rng.random(R)).astype(np.float32)
+    p = np.empty(R, np.float32)
+    for r in range(R):
+        top = np.float32(3.0 + 5.0 * rng.random())
+        per = math.log(2.0) / 32.0 * float(t[r])                     # logits of a step
+        mid = np.float32(float(top) - (rng.integers(20, 200) + 0.5) * per)
+        l = (mid.view(np.int32) + np.arange(n, dtype=np.int32) - n // 2).view(np.float32)
+        assert np.all(np.abs(l - mid) < per / 4) and len(set(l.tolist())) == n
+        l = np.sort(l)[::-1]
+        w = np.exp((l.astype(np.float64) - float(top)) / float(t[r]))
+        # in the middle of token `cut`: half a token's mass, 1 / 800 of all at least, is 10^4 roundings of p
+        p[r] = (1.0 + w[:cut].sum() + 0.5 * w[cut]) / (1.0 + w.sum())
+        at = rng.permutation(V)[:n + 1]
+        rows[r, at[0]], rows[r, at[1:]] = top, l
+    _, probs = evs.sample(torch.from_numpy(rows).cuda(), torch.full((R,), 0.5, device="cuda"),
+                          temperature=torch.from_numpy(t).cuda(), top_p=torch.from_numpy(p).cuda(), return_probs=True)
+    kept = (probs > 0).sum(1).cpu().numpy()
+    assert np.all(kept == 1 + cut + 1), np.bincount(kept)[cut:]
+
+
 def test_sample_ties(evs):
     """Equal logits go by their ids: cuts inside one value shared by many more tokens than are ranked at once."""
     for V, levels in ((3000, 1), (50021, 1), (50021, 3), (131072, 2), (131072, 40)):
