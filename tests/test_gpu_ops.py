@@ -685,6 +685,32 @@ def test_sample_strides_and_streams(evs):
     assert evs.sample(l[:0], u[:0]).shape == (0,)
 
 
+FIRST_CALL = """
+import torch, lossless_speculative_verify_gb300 as evs
+g = torch.Generator(device="cuda").manual_seed(1)
+for dtype in (torch.float32, torch.bfloat16):
+    for rows, vocab in ((200, 7000), (30, 14000)):
+        l = torch.randn(rows, vocab, device="cuda", generator=g).to(dtype)
+        u = torch.rand(rows, device="cuda", generator=g)
+        got = evs.sample(l, u, top_p=torch.full((rows,), 0.9, device="cuda"))
+        wide = torch.full((rows, 40000), -float("inf"), device="cuda", dtype=dtype)
+        wide[:, :vocab] = l
+        assert torch.equal(evs.sample(wide, u, top_p=torch.full((rows,), 0.9, device="cuda")), got), (dtype, vocab)
+print("done")
+"""
+
+
+def test_sample_first_call_of_a_process(evs):
+    """Slices of 7000 logits need 48 KB of shared memory with the kernel's own: the first call of each instance in a
+    process, before a larger one has raised its limit (then alike rows in a wider vocabulary)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=180)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-1500:]
+
+
 def test_sample_refusals(evs):
     l, u = make_logits(24, 4, 100)
     for a, kw in (((l.half(), u), {}), ((l.t(), u), {}), ((l, u[:3]), {}), ((l, u.double()), {}), ((l, None), {}),
