@@ -210,6 +210,9 @@ __global__ void __launch_bounds__(256) shared_simt_kernel(SharedArgs a, int sh_i
 //   tensor memory, V MN-major from shared memory.
 // Two row lanes take turns at the softmax: left alone they fall into step, both in it and then both
 // waiting for the tensor core (155 us instead of 131 behind 32768 rows of 32 heads with 208 queries).
+// The weights enter P V as bf16, the type that the products with V want: off by 2^-8 at most each,
+// of both signs, while their sum l stays fp32. Against 64 bits outputs are 2.3e-3 off where the
+// rounding of the output alone is 1.7e-3 (root mean square, relative); lse is not touched by it.
 // The running maximum moves only when it grows by more than 2^8, as few rescales of O as that.
 // A tile that the keys end in takes only the 16-key steps that hold keys, the rows behind them in
 // the last step cleared in shared memory (they may hold anything, NaN included).

@@ -19,10 +19,12 @@
 // tokens; those few are then ranked. A bin's mass is the sum of its tokens' mantissas, of 33 bits,
 // in two 32-bit counters (three took 13.5 thousand cycles of a large row's histogram, two 12.9).
 //
-// A chain of dependent phases with a barrier each bounds the small rows, instructions (two
-// evaluations of every weight) the large ones. 4 x 512 fp32 with every filter 6.9 us, 208 x 4096
-// with probabilities 17, 64 x 50021 bf16 23, 256 x 131072 fp32 with top-p and min-p 261 (2048 CTAs,
-// seven waves of two an SM; its 134 MB alone are 20).
+// A chain of dependent phases, each with a barrier, bounds small and large rows alike. 4 x 512 fp32
+// with every filter 6.8 us, 208 x 4096 with probabilities 17, 64 x 50021 bf16 23, 256 x 131072 fp32
+// with top-p and min-p 261: 2048 CTAs, two an SM, of 33 us each, in thousands of cycles launch and loads
+// 7, maximum 4, histogram 13 and the wait for the cluster 3, its scan 8, gathering the bin 8, ranking it
+// 11 (one CTA of the eight works), the kept mass 11, its total 3, the rest 1. Two of four issue slots are
+// used; the row is read once (134 MB, 20 us).
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
