@@ -1106,6 +1106,12 @@ constexpr int tc_smem(int dh, int stages, int batch) {
 
 template <int DH, int NST>
 cudaError_t launch_tensor(const evs_shared_attn_args& c, const SharedArgs& a, int grid, cudaStream_t stream) {
+    // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
+    // maps does not and wants to find.
+    const int smem = tc_smem(DH, NST, c.batch);
+    const cudaError_t e =
+        cudaFuncSetAttribute(shared_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     CUtensorMap kp, vp, ko, vo;
     bool ok = true;
     if (c.prefix > 0)
@@ -1117,10 +1123,6 @@ cudaError_t launch_tensor(const evs_shared_attn_args& c, const SharedArgs& a, in
     if (!ok) return cudaErrorInvalidValue;
     if (c.prefix == 0) { kp = ko; vp = vo; }
     if (c.own_max == 0) { ko = kp; vo = vp; }
-    const int smem = tc_smem(DH, NST, c.batch);
-    const cudaError_t e =
-        cudaFuncSetAttribute(shared_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     return launch_s(stream, shared_tc_kernel<DH, NST>, dim3(grid), dim3(ST_THREADS), (size_t)smem, kp, vp, ko, vo, a);
 }
 

@@ -765,6 +765,40 @@ def test_inputs_written_just_before(evs):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_first_call_of_a_thread(evs):
+    """Each operator as the first use of the device that a host thread makes, through its C entry point."""
+    import ctypes
+    import threading
+    from lossless_speculative_verify_gb300 import _lib
+    lib, p = evs.load(), lambda t: t.data_ptr()  # noqa: E731
+    d, s = make_attn(65, BF16, 2, 1, 2, 2, 2, 128, 300, 40, [40, 3]), make_scan(66, 1, 3, 64, 16, F32)
+    l, u = make_logits(67, 2, 9000)
+    o, y, z, w = torch.empty_like(d["q"]), torch.empty_like(s["x"]), torch.empty_like(s["x"]), randn(gen(68), 64, 4)
+    tok = torch.empty(2, dtype=torch.int32, device="cuda")
+    n = lib.evs_shared_attention_workspace(ctypes.byref(attn_args(_lib, d)))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    calls = [("evs_shared_attention", attn_args(_lib, d, o=p(o), workspace=p(ws), ws_bytes=n)),
+             ("evs_sample", _lib.SampleArgs(rows=2, vocab=9000, dtype=0, ld=9000, logits=p(l), uniforms=p(u), token=p(tok))),
+             ("evs_causal_conv", _lib.ConvArgs(batch=1, tokens=3, width=64, taps=4, dtype=0, silu=1, x=p(s["x"]), x_ld=64,
+                                               x_seq=192, y=p(y), y_ld=64, y_seq=192, weight=p(w))),
+             ("evs_selective_scan", _lib.ScanArgs(
+                 batch=1, tokens=3, width=64, states=16, dtype=0, softplus=1, x=p(s["x"]), x_ld=64, x_seq=192, dt=p(s["dt"]),
+                 dt_ld=64, dt_seq=192, B=p(s["B"]), b_ld=16, b_seq=48, C=p(s["C"]), c_ld=16, c_seq=48, y=p(z), y_ld=64,
+                 y_seq=192, A=p(s["A"])))]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for name, args in calls:
+        status = []
+        t = threading.Thread(target=lambda: status.append(getattr(lib, name)(ctypes.byref(args), stream.cuda_stream)))
+        t.start()
+        t.join()
+        assert status == [0], name
+    torch.cuda.synchronize()
+    assert torch.equal(o, run_attn(evs, d)[0]) and torch.equal(tok, evs.sample(l, u))
+    assert torch.equal(y, evs.causal_conv(s["x"], w))
+    assert torch.equal(z, evs.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"]))
+
+
 def test_no_gradients(evs):
     l, u = make_logits(25, 2, 100)
     x, w = torch.zeros(1, 4, 8, device="cuda", requires_grad=True), torch.zeros(8, 4, device="cuda")
