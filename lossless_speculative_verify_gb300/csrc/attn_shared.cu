@@ -1104,13 +1104,16 @@ constexpr int tc_smem(int dh, int stages, int batch) {
     return 1024 + (2 + stages) * ST_KEYS * dh * 2 + (2 * stages + 12) * 8 + (2 * batch + 1) * 4 + 16;
 }
 
+constexpr int TC_SMEM_MAX = 227 * 1024 - 256;   // the kernel's own variables beside it
 template <int DH, int NST>
 cudaError_t launch_tensor(const evs_shared_attn_args& c, const SharedArgs& a, int grid, cudaStream_t stream) {
     // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
-    // maps does not and wants to find.
+    // maps does not and wants to find. The limit is that of any batch: this call's own would be lowered by
+    // another thread's smaller call before the launch.
     const int smem = tc_smem(DH, NST, c.batch);
+    constexpr int most = tc_smem(DH, NST, 1024) < TC_SMEM_MAX ? tc_smem(DH, NST, 1024) : TC_SMEM_MAX;
     const cudaError_t e =
-        cudaFuncSetAttribute(shared_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(shared_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     CUtensorMap kp, vp, ko, vo;
     bool ok = true;
@@ -1157,7 +1160,7 @@ cudaError_t launch_shared_attention(const evs_shared_attn_args& c, cudaStream_t 
     if (tensor)
         // the ring takes what 227 KB leave: five tiles of 32 KB, four where the lengths need their place
         e = c.head_dim == 64                                 ? launch_tensor<64, 8>(c, a, grid_tc, stream)
-            : tc_smem(128, 5, c.batch) <= 227 * 1024 - 256 ? launch_tensor<128, 5>(c, a, grid_tc, stream)
+            : tc_smem(128, 5, c.batch) <= TC_SMEM_MAX ? launch_tensor<128, 5>(c, a, grid_tc, stream)
                                                              : launch_tensor<128, 4>(c, a, grid_tc, stream);
     else if (sh_items + own_items > 0)
         e = half ? launch_s(stream, shared_simt_kernel<bf16>, dim3(sh_items + own_items), dim3(256), 0, a, sh_items)

@@ -48,6 +48,7 @@ constexpr int SMP_FRAC = 45;            // fixed point of weights; 2^18 of them 
 constexpr int SMP_ZERO = SMP_FRAC + 1;  // weights of 2^-46 and less are 0
 constexpr int SMP_AREA = SMP_CAP * 20;   // bytes of shared memory behind the logits: two lists of 8 bytes, two of 2
 constexpr int SMP_MAX_CS = 8;           // portable cluster size
+constexpr int SMP_MAX_SMEM = (SMP_MAX_V / SMP_MAX_CS + 16) * 4 + SMP_AREA;   // of the largest slice, its ends off the grid
 
 // 2^(j/32) for j = 0..31, each the sum of two floats
 __constant__ float2 kPow2[32] = {
@@ -936,8 +937,11 @@ int sample_cluster(int rows, int V) {
 template <typename T, int THREADS, bool CLUSTER>
 cudaError_t sample_launch(const SampleArgs& a, int rows, int cs, size_t smem, cudaStream_t stream) {
     auto kernel = sample_kernel<T, THREADS, CLUSTER>;
+    if (smem > SMP_MAX_SMEM) return cudaErrorInvalidValue;
     if (smem > 40 * 1024) {   // with the kernel's own 2 KB above the 48 KB that need no asking
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the same limit in every call: one of this call's own would be lowered by another thread's smaller
+        // call between here and the launch
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMP_MAX_SMEM);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -799,6 +799,58 @@ def test_first_call_of_a_thread(evs):
     assert torch.equal(z, evs.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"]))
 
 
+def test_calls_of_several_threads(evs):
+    """Threads with a stream each call one kernel instance with little and with much shared memory at once: no call
+    takes from another what it asked for. And a captured large call replays after small ones."""
+    import ctypes
+    import threading
+    from lossless_speculative_verify_gb300 import _lib
+    lib, jobs, keep = evs.load(), [], []
+    for rows, vocab in ((30, 14000), (1, 131072), (2, 262144)):
+        l, u = make_logits(vocab, rows, vocab)
+        p, tok = col(rows, 0.9), torch.empty(rows, dtype=torch.int32, device="cuda")
+        want = evs.sample(l, u, top_p=p)
+        jobs.append((lib.evs_sample, _lib.SampleArgs(
+            rows=rows, vocab=vocab, dtype=0, ld=vocab, logits=l.data_ptr(), uniforms=u.data_ptr(), top_p=p.data_ptr(),
+            token=tok.data_ptr()), tok, want))
+        keep.append((l, u, p))
+    for B in (1, 40, 300):
+        d = make_attn(64, BF16, B, 1, 1, 2, 2, 128, 300, 40, [i % 41 for i in range(B)])
+        o = torch.empty_like(d["q"])
+        n = lib.evs_shared_attention_workspace(ctypes.byref(attn_args(_lib, d)))
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        jobs.append((lib.evs_shared_attention, attn_args(_lib, d, o=o.data_ptr(), workspace=ws.data_ptr(), ws_bytes=n), o,
+                     run_attn(evs, d)[0]))
+        keep.append((d, ws))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    failed = [0] * len(jobs)
+
+    def work(k):
+        fn, args, _, _ = jobs[k]
+        for i in range(6000):
+            failed[k] += fn(ctypes.byref(args), streams[k].cuda_stream) != 0
+            if i % 100 == 0:
+                streams[k].synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(jobs)
+    assert all(torch.equal(got, want) for _, _, got, want in jobs)
+    (l1, u1, p1), (l2, u2, p2) = keep[0], keep[2]
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = evs.sample(l2, u2, top_p=p2)
+    evs.sample(l1, u1, top_p=p1)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, jobs[2][3])
+
+
 def test_no_gradients(evs):
     l, u = make_logits(25, 2, 100)
     x, w = torch.zeros(1, 4, 8, device="cuda", requires_grad=True), torch.zeros(8, 4, device="cuda")
