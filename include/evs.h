@@ -78,10 +78,12 @@ enum {
     EVS_FLAG_KV_OVERFLOW = 1u,    /* a write past t_max was skipped                     */
     EVS_FLAG_BAD_K = 2u,          /* slice saw k outside [0, gamma] or a bad candidate  */
     EVS_FLAG_EMPTY_RESIDUAL = 4u, /* max(0, p - q) summed to 0 in fp32; p was used      */
-    EVS_FLAG_BAD_TOKEN = 8u,      /* a token id outside [0, vocab) was clamped          */
+    EVS_FLAG_BAD_TOKEN = 8u,      /* a token id outside [0, vocab) was clamped (or, among
+                                     given tokens, has the log probability -inf)       */
     EVS_FLAG_TIMEOUT = 16u,       /* a kernel gave up a bounded wait; its output is void */
     EVS_FLAG_BAD_LEN = 32u,       /* a sequence length outside its range was clamped     */
-    EVS_FLAG_EMPTY_ROW = 64u      /* a row whose tokens are all ruled out: no draw (-1)  */
+    EVS_FLAG_EMPTY_ROW = 64u,     /* a row whose tokens are all ruled out: no draw (-1)  */
+    EVS_FLAG_BAD_PARENT = 128u    /* a parent that is no earlier node was read as -1     */
 };
 
 #define EVS_MAX_LAYERS 64
@@ -478,6 +480,100 @@ typedef struct {
 /* Bytes of workspace for these sizes (0: none; prompts of few sequences are run in segments). */
 size_t evs_selective_scan_workspace(int32_t batch, int32_t tokens, int32_t width, int32_t states);
 evs_status evs_selective_scan(const evs_scan_args* args, void* stream);
+
+/* Log probabilities of given tokens, the row's entropy and its largest tokens. Per row r, with T its
+ * temperature: y_i = (l_i - max l) / T, Z = sum exp(y_i);
+ *   logprob[r][j] = y_t - log Z for t = tokens[r][j],  entropy[r] = -sum p_i log p_i (natural logarithms),
+ *   top_token[r][0 .. top) the largest logits' ids in the order (logit descending, id ascending), and
+ *   top_logprob their log probabilities.
+ * NaN and -inf logits are ruled out (-inf); where the largest logit is +inf, the +inf tokens share the
+ * mass. A temperature that is not above zero puts all mass on the first largest token; one above 1e30 is
+ * taken as 1e30. Places of top behind the last token that is not ruled out hold id -1 and -inf. A given id
+ * outside [0, vocab) has -inf (EVS_FLAG_BAD_TOKEN); a row with every token ruled out has -inf, entropy 0,
+ * ids -1 (EVS_FLAG_EMPTY_ROW). Sums are fp32 over a running maximum; the ids are exact. */
+typedef struct {
+    int32_t rows, vocab;         /* at most 2^24 each                                       */
+    int32_t n_tokens, top;       /* given tokens a row; largest ones, at most 64 and vocab  */
+    int32_t dtype;               /* EVS_DTYPE_* of the logits                               */
+    int64_t ld;                  /* row stride of logits (>= vocab)                         */
+    const void* logits;          /* device [rows][vocab]                                    */
+    const float* temperature;    /* device [rows] or NULL (1)                               */
+    const int32_t* tokens;       /* device [rows][n_tokens]                                 */
+    float* logprob;              /* device [rows][n_tokens]                                 */
+    float* entropy;              /* device [rows] or NULL                                   */
+    float* top_logprob;          /* device [rows][top]                                      */
+    int32_t* top_token;          /* device [rows][top]                                      */
+    uint32_t* flags;
+} evs_logprob_args;
+evs_status evs_token_logprobs(const evs_logprob_args* args, void* stream);
+
+/* Causal attention over whole prompts packed behind each other. Sequence b has rows starts[b] ..
+ * starts[b + 1] - 1 of q, k, v and o; its query row i of head h reads its rows j <= i with the K/V head
+ * g = h / (heads / kv_heads): o = softmax(scale q k^T) v, lse = log of the sum of exponentials. Rows of no
+ * sequence (before starts[0], behind starts[batch]) may hold anything; o is left as it was there, or with
+ * zero_rest is zero, and lse is -inf. Starts are made to ascend within [0, tokens] (EVS_FLAG_BAD_LEN where
+ * they did not). A query whose every score is -inf gives o = 0 and lse = -inf; one whose kernel gave up a
+ * bounded wait gives NaN for both (EVS_FLAG_TIMEOUT). Types, statistics and weights as in
+ * evs_shared_attention. */
+typedef struct {
+    int32_t tokens, batch;               /* rows of the buffers, sequences (<= 1024)        */
+    int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
+    int32_t dtype;                       /* EVS_DTYPE_* of all                              */
+    int32_t zero_rest;
+    float scale;                         /* 0: 1 / sqrt(head_dim)                           */
+    const void* q;                       /* device [tokens][heads][head_dim]                */
+    int64_t q_row, q_head;
+    const void *k, *v;                   /* device [tokens][kv_heads][head_dim]             */
+    int64_t kv_row, kv_head;             /* strides of both                                 */
+    const int32_t* starts;               /* device [batch + 1]                              */
+    void* o;                             /* device [tokens][heads][head_dim], heads contiguous */
+    int64_t o_row;
+    float* lse;                          /* device [tokens][heads] or NULL                  */
+    void* workspace;                     /* device, 256-byte aligned; not shared by calls that may overlap */
+    size_t ws_bytes;
+    uint32_t* flags;
+} evs_prompt_attn_args;
+/* Bytes of workspace for these sizes (pointers may still be null; 0 if invalid). */
+size_t evs_prompt_attention_workspace(const evs_prompt_attn_args* args);
+evs_status evs_prompt_attention(const evs_prompt_attn_args* args, void* stream);
+
+/* Attention of a tree of drafted tokens over each sequence's cache. Node i of sequence b reads the cached
+ * rows [0, cache_len[b]) and the nodes on its path to the root: itself, parent[b][i], that one's parent,
+ * and so on to a parent of -1 (a node below the last cached token). A parent comes before its children;
+ * one that does not is read as -1 (EVS_FLAG_BAD_PARENT). Sequence b has lens[b] nodes (NULL: all have
+ * `nodes`; clamped to [0, nodes], EVS_FLAG_BAD_LEN); o of the rest is left as it was, or with zero_rest is
+ * zero, and their lse is -inf. A tree of one node is a decode step, a chain a verify block.
+ * The nodes' K/V lie in k_nodes / v_nodes, or (both NULL) in the cache behind the readable rows, row
+ * cache_len[b] + j; rows past the capacity are left out (EVS_FLAG_KV_OVERFLOW). Lengths outside [0,
+ * capacity] are clamped (EVS_FLAG_BAD_LEN). Rows that no query reads may hold anything, but the nodes of a
+ * tree are read together: a node's V that is not finite shows in all nodes of its tree. Everything else as
+ * in evs_shared_attention. */
+typedef struct {
+    int32_t batch, nodes;                /* 1 .. 1024 sequences, 1 .. 128 nodes             */
+    int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
+    int32_t dtype;                       /* EVS_DTYPE_* of all                              */
+    int32_t capacity;                    /* rows of one sequence's cache                    */
+    int32_t zero_rest;
+    float scale;                         /* 0: 1 / sqrt(head_dim)                           */
+    const void* q;                       /* device, row b * nodes + i: heads x head_dim     */
+    int64_t q_ld;
+    const void *k_cache, *v_cache;       /* device [batch][kv_heads][capacity][head_dim]    */
+    int64_t cache_row, cache_head, cache_seq;
+    const int32_t* cache_len;            /* device [batch]                                  */
+    const int32_t* parents;              /* device [batch][nodes], stride parents_seq (0: one tree for all) */
+    int64_t parents_seq;
+    const void *k_nodes, *v_nodes;       /* device [batch][kv_heads][nodes][head_dim] or NULL */
+    int64_t node_row, node_head, node_seq;
+    const int32_t* lens;                 /* device [batch] or NULL                          */
+    void* o;                             /* device, rows as q                               */
+    int64_t o_ld;
+    float* lse;                          /* device [batch][nodes][heads] or NULL            */
+    void* workspace;                     /* device, 256-byte aligned; not shared by calls that may overlap */
+    size_t ws_bytes;
+    uint32_t* flags;
+} evs_tree_attn_args;
+size_t evs_tree_attention_workspace(const evs_tree_attn_args* args);
+evs_status evs_tree_attention(const evs_tree_attn_args* args, void* stream);
 
 /* Static description of a status code. */
 const char* evs_status_str(evs_status s);

@@ -20,7 +20,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 MODE_GREEDY, MODE_SAMPLING = 0, 1
 CAND_RECURSIVE, CAND_MAX_ACCEPT = 0, 1
 FLAG_KV_OVERFLOW, FLAG_BAD_K, FLAG_EMPTY_RESIDUAL, FLAG_BAD_TOKEN, FLAG_TIMEOUT = 1, 2, 4, 8, 16
-FLAG_BAD_LEN, FLAG_EMPTY_ROW = 32, 64
+FLAG_BAD_LEN, FLAG_EMPTY_ROW, FLAG_BAD_PARENT = 32, 64, 128
 (BUF_LOGITS, BUF_FIR_STAGE, BUF_IIR_U, BUF_K_CACHE, BUF_V_CACHE, BUF_K_SIDE, BUF_V_SIDE,
  BUF_KV_LEN, BUF_FIR_TAIL, BUF_IIR_STATE, BUF_CAND_K, BUF_CAND_CORR) = range(12)
 
@@ -31,6 +31,8 @@ EXPORTED = (
     "evs_status_str", "evs_profile_enable", "evs_profile_read", "evs_debug_projection",
     "evs_projection_noalloc", "evs_projection_noalloc_flags", "evs_sample", "evs_decode_filtered",
     "evs_causal_conv", "evs_selective_scan", "evs_selective_scan_workspace", "evs_shared_attention_workspace", "evs_shared_attention",
+    "evs_token_logprobs", "evs_prompt_attention_workspace", "evs_prompt_attention", "evs_tree_attention_workspace",
+    "evs_tree_attention",
 )
 KERNEL_KINDS = ("embed", "norm", "gemm", "fir", "iir", "kv_write", "attn", "attn_combine", "accept",
                 "slice", "advance")
@@ -102,12 +104,44 @@ class SharedAttnArgs(C.Structure):
                        "q block_row, block_head, block_cand; p o; q o_ld; p lse, workspace; z ws_bytes; p flags")
 
 
+class LogprobArgs(C.Structure):
+    _fields_ = _fields("i rows, vocab, n_tokens, top, dtype; q ld; p logits, temperature, tokens, logprob, entropy, "
+                       "top_logprob, top_token, flags")
+
+
+class PromptAttnArgs(C.Structure):
+    _fields_ = _fields("i tokens, batch, heads, kv_heads, head_dim, dtype, zero_rest; f scale; p q; q q_row, q_head; "
+                       "p k, v; q kv_row, kv_head; p starts, o; q o_row; p lse, workspace; z ws_bytes; p flags")
+
+
+class TreeAttnArgs(C.Structure):
+    _fields_ = _fields("i batch, nodes, heads, kv_heads, head_dim, dtype, capacity, zero_rest; f scale; p q; q q_ld; "
+                       "p k_cache, v_cache; q cache_row, cache_head, cache_seq; p cache_len, parents; q parents_seq; "
+                       "p k_nodes, v_nodes; q node_row, node_head, node_seq; p lens, o; q o_ld; p lse, workspace; "
+                       "z ws_bytes; p flags")
+
+
 pack_sample = _packer(SampleArgs._fields_).pack
 pack_conv = _packer(ConvArgs._fields_).pack
 pack_scan = _packer(ScanArgs._fields_).pack
 # the shapes, which the workspace's size needs, and the rest
 pack_attn_shapes = _packer(SharedAttnArgs._fields_[:12]).pack
 pack_attn_rest = _packer(SharedAttnArgs._fields_[12:]).pack
+pack_logprob = _packer(LogprobArgs._fields_).pack
+pack_prompt_shapes = _packer(PromptAttnArgs._fields_[:8]).pack
+pack_prompt_rest = _packer(PromptAttnArgs._fields_[8:]).pack
+PROMPT_NO_REST = bytes(C.sizeof(PromptAttnArgs) - _packer(PromptAttnArgs._fields_[:8]).size)
+# (the struct's ninth member ends off the eight bytes that its tenth begins on)
+_tree_shapes = _packer(TreeAttnArgs._fields_[:9])
+_TREE_PAD = bytes(-_tree_shapes.size % 8)
+
+
+def pack_tree_shapes(*args):
+    return _tree_shapes.pack(*args) + _TREE_PAD
+
+
+pack_tree_rest = _packer(TreeAttnArgs._fields_[9:]).pack
+TREE_NO_REST = bytes(C.sizeof(TreeAttnArgs) - _tree_shapes.size - len(_TREE_PAD))
 NO_REST = bytes(C.sizeof(SharedAttnArgs) - _packer(SharedAttnArgs._fields_[:12]).size)
 
 _lib = None
@@ -165,12 +199,15 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.evs_projection_noalloc.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
     lib.evs_projection_noalloc_flags.restype = C.c_int
     lib.evs_projection_noalloc_flags.argtypes = [C.POINTER(C.c_uint32), i32, vp]
-    for name in ("evs_sample", "evs_causal_conv", "evs_selective_scan", "evs_shared_attention"):
+    for name in ("evs_sample", "evs_causal_conv", "evs_selective_scan", "evs_shared_attention", "evs_token_logprobs",
+                 "evs_prompt_attention", "evs_tree_attention"):
         fn = getattr(lib, name)
         fn.restype = C.c_int
         fn.argtypes = [vp, vp]                   # a structure by reference, or one packed into bytes
-    lib.evs_shared_attention_workspace.restype = C.c_size_t
-    lib.evs_shared_attention_workspace.argtypes = [vp]
+    for name in ("evs_shared_attention_workspace", "evs_prompt_attention_workspace", "evs_tree_attention_workspace"):
+        fn = getattr(lib, name)
+        fn.restype = C.c_size_t
+        fn.argtypes = [vp]
     lib.evs_selective_scan_workspace.restype = C.c_size_t
     lib.evs_selective_scan_workspace.argtypes = [i32, i32, i32, i32]
     lib.evs_decode_filtered.restype = C.c_int

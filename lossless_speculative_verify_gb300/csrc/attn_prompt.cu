@@ -1,0 +1,513 @@
+// Causal attention over whole prompts packed behind each other (evs_prompt_attention).
+//
+//   o_i = sum_{j <= i} exp(scale q_i.k_j - m) v_j / l,  lse_i = m + log l, within each sequence.
+//
+// On the tensor cores an item is 256 query rows of one head of one sequence, 128 for each lane (see
+// attn_tiles.cuh), and the K/V tiles up to its diagonal, which TMA brings once for both. A persistent grid
+// takes the items in the order of their length, longest first, forwards and backwards in turn, so that the
+// CTAs end together: lengths are on the device, and each role of a CTA walks the same order by itself.
+#include "attn_simt.cuh"
+#include "attn_tiles.cuh"
+
+namespace evs {
+namespace {
+
+using namespace attn;
+
+struct PromptArgs {
+    const void *q, *k, *v;
+    void* o;
+    float* lse;
+    const int32_t* starts;
+    uint32_t* flags;
+    int64_t q_row, q_head, kv_row, kv_head, o_row;
+    int N, B, H, G, zero_rest, o_vec;
+    float scale;
+};
+
+// Row where sequence b starts, in ascending order within [0, N] whatever starts holds; st: [B + 1] in
+// shared memory. All threads of the CTA; a warp scans.
+__device__ __forceinline__ void load_starts(const PromptArgs& a, int* st) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int run = 0;
+        bool bad = false;
+        for (int b0 = 0; b0 <= a.B; b0 += 32) {
+            const int b = b0 + lane;
+            const int raw = b <= a.B ? __ldcg(a.starts + b) : 0;
+            int x = min(max(raw, 0), a.N);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x = max(x, y);
+            }
+            x = max(x, run);
+            if (b <= a.B) {
+                st[b] = x;
+                bad |= x != raw;
+            }
+            run = __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (bad && a.flags && blockIdx.x == 0) atomicOr(a.flags, (uint32_t)EVS_FLAG_BAD_LEN);
+    }
+    __syncthreads();
+}
+
+// Rows of no sequence, dealt among `parts` CTAs of `threads`
+template <typename T>
+__device__ __forceinline__ void rest_rows(const PromptArgs& a, int s0, int s1, int dh, int part, int parts, int t, int threads) {
+    const int rest = s0 + (a.N - s1);
+    for (int i = part; i < rest; i += parts) {
+        const int64_t row = i < s0 ? i : s1 + (i - s0);
+        if (a.zero_rest)
+            for (int c = t; c < a.H * dh; c += threads) ((T*)a.o)[row * a.o_row + c] = from_f32<T>(0.f);
+        if (a.lse)
+            for (int h = t; h < a.H; h += threads) a.lse[row * a.H + h] = -INFINITY;
+    }
+}
+
+// The CTA's items. Level v holds the items of v x 256 rows and their keys: one for each head of each
+// sequence that is as long (order: sequences by length, longest first).
+struct Items {
+    const int *st, *order;
+    int B, H, grid, round, base, level, count;
+    int first, len, head, tile;          // the item: its sequence's first row and length, its head and 256 rows
+
+    __device__ __forceinline__ int tiles(int i) const {
+        const int s = order[i];
+        return (st[s + 1] - st[s] + 255) >> 8;
+    }
+    __device__ __forceinline__ void init(const int* s, const int* ord, int b, int h) {
+        st = s;
+        order = ord;
+        B = b;
+        H = h;
+        grid = gridDim.x;
+        round = 0;
+        base = 0;
+        level = b > 0 ? tiles(0) : 0;
+        count = 0;
+        widen();
+    }
+    __device__ __forceinline__ void widen() {
+        while (count < B && tiles(count) >= level) ++count;
+    }
+    __device__ __forceinline__ bool next() {
+        const int at = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        ++round;
+        while (level > 0 && at >= base + count * H) {
+            base += count * H;
+            --level;
+            widen();
+        }
+        if (level <= 0) return false;
+        const int in = at - base, i = in / H;
+        const int s = order[i];
+        first = st[s];
+        len = st[s + 1] - first;
+        head = in - i * H;
+        tile = level - 1;
+        return true;
+    }
+    // of lane L: rows, key tiles; of the item: key tiles
+    __device__ __forceinline__ int rows(int L) const { return min(128, len - tile * 256 - L * 128); }
+    __device__ __forceinline__ int keys(int L) const { return tile * 2 + L + 1; }
+    __device__ __forceinline__ int keys() const { return keys(rows(1) > 0 ? 1 : 0); }
+};
+
+constexpr int small_smem(int B) { return 1024 + 256 + (2 * B + 1) * 4; }
+constexpr int prompt_smem(int dh, int stages, int B) { return small_smem(B) + 1024 + (2 + stages) * KEYS * dh * 2; }
+constexpr int SMEM_MAX = 227 * 1024;
+
+template <int DH, int NST>
+__global__ void __launch_bounds__(THREADS, 1)
+prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, PromptArgs a) {
+    constexpr int HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
+    extern __shared__ uint8_t smem_raw[];
+    float* exchange = reinterpret_cast<float*>(smem_raw);                  // [2][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + 1024);         // [NST]
+    uint64_t* empty = full + NST;                                          // [NST]
+    uint64_t* s_full = empty + NST;                                        // [2] scores of a tile in tensor memory
+    uint64_t* p_full = s_full + 2;                                         // [2] weights of a tile there
+    uint64_t* pv_done = p_full + 2;                                        // [2] P V of a tile complete
+    uint64_t* q_full = pv_done + 2;                                        // [2] Q of an item there
+    uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
+    uint64_t* drain = q_free + 2;                                          // [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+    int* st = reinterpret_cast<int*>(smem_raw + 1024 + 256);               // [B + 1]
+    int* order = st + a.B + 1;                                             // [B]
+    uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
+    uint8_t* ring = sQ + 2 * TILE;
+    static_assert((2 * NST + 12) * 8 + 4 <= 256, "barriers");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_wait();
+    pdl_trigger();
+    // not before the wait: a predecessor's CTA on this SM may have yet to allocate
+    if (warp == SOFT_WARPS) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 8);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_free[i], 1);
+            mbar_init(&drain[i], 1);
+        }
+        fence_barrier_init();
+    }
+    load_starts(a, st);
+    for (int s = tid; s < a.B; s += THREADS) {           // sequences by tiles, longest first
+        const int n = (st[s + 1] - st[s] + 255) >> 8;
+        int before = 0;
+        for (int o = 0; o < a.B; ++o) {
+            const int m = (st[o + 1] - st[o] + 255) >> 8;
+            before += m > n || (m == n && o < s);
+        }
+        order[before] = s;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Items it;
+    it.init(st, order, a.B, a.H);
+
+    if (warp >= SOFT_WARPS) {
+        asm volatile(EVS_ATTN_AUX_REGS);
+        const int role = warp - SOFT_WARPS;
+        if (role == 0 && lane == 0) {
+            // ---- K and V tiles: K0 V0 K1 V1 ... of all items
+            const uint64_t keep = policy_evict_last();
+            int s = 0;
+            uint32_t ph = 1, used = 0;                   // parity that a free slot has; slots in use so far
+            bool ok = true;
+            while (ok && it.next()) {
+                const int n = 2 * it.keys(), g = it.head / (a.H / a.G);
+                for (int j = 0; j < n; ++j) {
+                    if ((used >> s & 1u) && !mbar_wait(&empty[s], ph)) { ok = false; break; }
+                    used |= 1u << s;
+                    uint8_t* dst = ring + (size_t)s * TILE;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)TILE);
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf)
+                        tma_load_4d(dst + hf * HALF, j & 1 ? &tmV : &tmK, hf * 64, it.first + (j >> 1) * KEYS, g, 0, &full[s], keep);
+                    if (++s == NST) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok)                                     // loads in flight end before this CTA does (bounded)
+                for (int i = 0; i < NST; ++i)
+                    if (used >> i & 1u) mbar_wait(&full[i], i < s ? ph ^ 1u : ph);
+        } else if (role == 2 && lane == 0) {
+            // ---- Q
+            const uint64_t once = policy_evict_first();
+            uint32_t cnt[2] = {0, 0};
+            bool ok = true;
+            while (ok && it.next()) {
+                for (int L = 0; L < 2 && ok; ++L) {
+                    if (it.rows(L) <= 0) continue;
+                    if (cnt[L] > 0 && !mbar_wait(&q_free[L], (cnt[L] - 1) & 1u)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&q_full[L], (uint32_t)TILE);
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf)
+                        tma_load_4d(sQ + L * TILE + hf * HALF, &tmQ, hf * 64, it.first + it.tile * 256 + L * 128, it.head, 0,
+                                    &q_full[L], once);
+                    ++cnt[L];
+                }
+            }
+            if (!ok)
+                for (int L = 0; L < 2; ++L)
+                    if (cnt[L] > 0) mbar_wait(&q_full[L], (cnt[L] - 1) & 1u);
+        } else if ((role & 1) && lane == 0) {
+            // ---- products of lane L
+            const int L = role >> 1;
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
+                           dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
+            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + 256u + (uint32_t)L * 128u;
+            int s = 0;                                   // next slot, its phase
+            uint32_t ph = 0, cnt = 0, qn = 0;
+            bool ok = true;
+            auto take = [&]() -> int {                   // the next step's tile
+                const int at = s;
+                if (ok && !mbar_wait(&full[at], ph)) ok = false;
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                return at;
+            };
+            while (ok && it.next()) {
+                const int rows = it.rows(L), n = rows > 0 ? it.keys(L) : 0, all = it.keys();
+                if (n > 0) {
+                    if (!mbar_wait(&q_full[L], qn & 1u)) { ok = false; break; }
+                    ++qn;
+                    int k = take();
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
+                    tc_commit(&s_full[L]);
+                    tc_commit(&empty[k]);
+                    if (n == 1) tc_commit(&q_free[L]);
+                    for (int t = 0; t < n && ok; ++t) {
+                        // O += P V of this tile, then the next one's scores before any of the commits
+                        const bool next = t + 1 < n;
+                        const int v = take();
+                        if (next) k = take();
+                        if (!ok || !mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
+                        ++cnt;
+                        tc_fence_after();
+                        issue_pv<DH>(o_at, s_at, dv + (uint64_t)((uint32_t)(v * TILE) >> 4), next ? KEYS : rows, t > 0);
+                        if (next) {
+                            issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
+                            tc_commit(&s_full[L]);
+                            tc_commit(&empty[k]);
+                        }
+                        tc_commit(&empty[v]);
+                        tc_commit(&pv_done[L]);
+                        if (t + 2 == n) tc_commit(&q_free[L]);
+                    }
+                }
+                for (int t = n; t < all && ok; ++t)      // tiles that only the other lane reads
+                    for (int j = 0; j < 2; ++j) {
+                        const int at = take();
+                        if (ok) mbar_arrive(&empty[at]);
+                    }
+            }
+            tc_commit(&drain[L]);                        // nothing of this thread's in tensor memory in flight
+            mbar_wait(&drain[L], 0);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == SOFT_WARPS) {
+            tc_fence_after();
+            tmem_dealloc(tmem, 512);
+        }
+        return;
+    }
+
+    // ---- softmax and epilogue
+    asm volatile(EVS_ATTN_SOFT_REGS);
+    SoftThread th;
+    th.init(warp, lane, tmem, exchange, DH);
+    const int L = th.lane;
+    const float sl = a.scale * LOG2E;
+    uint32_t cnt = 0, steps = 0;                         // tiles of this lane, ring steps before this item
+    bool ok = true;                                      // a wait that ran out ends all later ones; barriers go on
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0;
+        return ok;
+    };
+    while (it.next()) {
+        const int rows = it.rows(L), n = it.keys(L);
+        if (rows > 0) {
+            const bool work = (th.row & ~31) < rows;     // of this warp
+            th.begin();
+            for (int t = 0; t < n; ++t) {
+                wait(&s_full[L], cnt & 1u);
+                const bool last = t == n - 1;
+                if (work) {
+                    uint32_t x[4][16];
+                    tc_fence_after();
+                    th.load(x);
+                    if (last) mask_from(x, th.row + 1 - th.half * 64);
+                    th.template tile<DH>(x, sl, t == 0, [&]() { return wait(&pv_done[L], (cnt - 1) & 1u); });
+                }
+                if (last && (rows & 15)) {
+                    const uint32_t at = steps + 2 * (uint32_t)t + 1;
+                    wait(&full[at % NST], at / NST & 1u);
+                    if (ok) clear_rows<DH>(ring + (size_t)(at % NST) * TILE, rows, th.half * 128 + th.row, 256);
+                    fence_proxy_async_smem();
+                }
+                if (work) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[L]);
+                ++cnt;
+            }
+            wait(&pv_done[L], (cnt - 1) & 1u);
+            if (work) {
+                const float l = th.exchange(th.l, [](float x, float y) { return x + y; });
+                tc_fence_after();
+                const bool live = th.row < rows;
+                const int64_t row = it.first + it.tile * 256 + L * 128 + th.row;
+                // no key with any weight: zero output, lse -inf; a void row: NaN
+                const float inv = ok ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : __int_as_float(0x7fc00000);
+                bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)it.head * DH + th.half * (DH / 2);
+#pragma unroll
+                for (int c = 0; c < DH / 32; ++c) {
+                    uint32_t o[16], w[8];
+                    tmem_ld16_issue(th.o_at + (uint32_t)(c * 16), o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = pack2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    if (live && a.o_vec) {
+                        *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(dst + c * 16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (live) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            reinterpret_cast<uint16_t*>(dst)[c * 16 + j] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
+                    }
+                }
+                if (live && th.half == 0 && a.lse)
+                    a.lse[row * a.H + it.head] = !ok ? inv : l == 0.f ? -INFINITY : th.m * LN2 + logf(l);
+                tc_fence_before();                       // these reads precede the next item's products
+            }
+            __syncwarp();
+        }
+        steps += 2 * (uint32_t)it.keys();
+    }
+    if (!ok && lane == 0 && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
+    rest_rows<bf16>(a, st[0], st[a.B], DH, blockIdx.x, gridDim.x, tid, 32 * SOFT_WARPS);
+    tc_fence_before();
+    __syncthreads();
+}
+
+// =========================================================================================
+// On CUDA cores (fp32, narrow heads, strides that tensor maps cannot describe): a CTA takes 64 rows of one
+// head. Tiles are numbered over the sequences as if each began a new 64 rows; a CTA behind the last one
+// takes rows of no sequence.
+// =========================================================================================
+template <typename T, int DH> __global__ void __launch_bounds__(256) prompt_simt_kernel(PromptArgs a) {
+    using S = Simt<T, DH, 4>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    int* st = reinterpret_cast<int*>(smem_raw);
+    typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(smem_raw + ((a.B + 1) * 4 + 15) / 16 * 16);
+    pdl_wait();
+    pdl_trigger();
+    load_starts(a, st);
+    const int h = blockIdx.y;
+    int item = blockIdx.x, s = 0;
+    for (; s < a.B; ++s) {
+        const int n = (st[s + 1] - st[s] + S::ROWS - 1) / S::ROWS;
+        if (item < n) {
+            item = n - 1 - item;                         // the longest rows first
+            break;
+        }
+        item -= n;
+    }
+    if (s == a.B) {
+        if (h == 0) rest_rows<T>(a, st[0], st[a.B], DH, item, gridDim.x - (blockIdx.x - item), threadIdx.x, 256);
+        return;
+    }
+    const int first = st[s], len = st[s + 1] - first, r0 = item * S::ROWS;
+    const int g = h / (a.H / a.G);
+    const T* q = (const T*)a.q + h * a.q_head;
+    const T* k = (const T*)a.k + first * a.kv_row + g * a.kv_head;
+    const T* v = (const T*)a.v + first * a.kv_row + g * a.kv_head;
+    S w(sm);
+    w.stage_q([&](int r) -> const T* { return r0 + r < len ? q + (int64_t)(first + r0 + r) * a.q_row : nullptr; }, a.scale);
+    const int end = min(len, r0 + S::ROWS);
+    for (int j0 = 0; j0 < end; j0 += S::KEYS) {
+        const int nk = min(S::KEYS, end - j0);
+        w.tile([&](int j) { return k + (int64_t)(j0 + j) * a.kv_row; }, [&](int j) { return v + (int64_t)(j0 + j) * a.kv_row; }, nk,
+               [&](int r, int j) { return j0 + j <= r0 + r; });
+    }
+    w.finish([&](int r, int c, float o, float m, float l) {
+        if (r0 + r >= len) return;
+        const int64_t row = first + r0 + r;
+        ((T*)a.o)[row * a.o_row + (int64_t)h * DH + c] = from_f32<T>(l > 0.f ? o / l : (l == 0.f ? 0.f : l));
+        if (c == 0 && a.lse) a.lse[row * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
+    });
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+bool valid_shape(const evs_prompt_attn_args* c) {
+    if (!c || c->tokens < 0 || c->batch < 0 || c->heads < 1 || c->kv_heads < 1) return false;
+    if (c->tokens > (1 << 24) || c->batch > 1024 || c->heads > 1024 || c->heads % c->kv_heads) return false;
+    if (!(c->head_dim == 16 || c->head_dim == 32 || c->head_dim == 64 || c->head_dim == 128)) return false;
+    if (c->batch == 0 && c->tokens > 0) return false;
+    return c->dtype == EVS_DTYPE_F32 || c->dtype == EVS_DTYPE_BF16;
+}
+
+bool tensor_ok(const evs_prompt_attn_args& c) {
+    return c.dtype == EVS_DTYPE_BF16 && (c.head_dim == 64 || c.head_dim == 128) &&
+           map_ok(c.q, c.q_row, c.q_head, 0, c.heads > 1, false) && map_ok(c.k, c.kv_row, c.kv_head, 0, c.kv_heads > 1, false) &&
+           map_ok(c.v, c.kv_row, c.kv_head, 0, c.kv_heads > 1, false);
+}
+
+template <int DH, int NST>
+cudaError_t launch_tensor(const evs_prompt_attn_args& c, const PromptArgs& a, cudaStream_t stream) {
+    // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
+    // maps does not and wants to find. The limit is that of any batch: this call's own would be lowered by
+    // another thread's smaller call before the launch.
+    constexpr int most = prompt_smem(DH, NST, 1024) < SMEM_MAX ? prompt_smem(DH, NST, 1024) : SMEM_MAX;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    CUtensorMap q, k, v;
+    if (!make_rows_map(&q, c.q, DH, c.tokens, c.heads, 1, c.q_row, c.q_head, 0) ||
+        !make_rows_map(&k, c.k, DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0) ||
+        !make_rows_map(&v, c.v, DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0))
+        return cudaErrorInvalidValue;
+    const long long items = ((long long)c.tokens / 256 + c.batch) * c.heads;     // at most
+    const int grid = (int)(items < kAttnGrid ? items : kAttnGrid);
+    return launch_s(stream, prompt_tc_kernel<DH, NST>, dim3(grid), dim3(THREADS), (size_t)prompt_smem(DH, NST, c.batch), q, k, v, a);
+}
+
+template <typename T, int DH>
+cudaError_t launch_simt(const evs_prompt_attn_args& c, const PromptArgs& a, cudaStream_t stream) {
+    using S = Simt<T, DH, 4>;
+    constexpr size_t most = sizeof(typename S::Smem) + (1024 + 1) * 4 + 16;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(typename S::Smem) + ((c.batch + 1) * 4 + 15) / 16 * 16;
+    // one more than the sequences can fill, for the rest
+    const dim3 grid(c.tokens / S::ROWS + c.batch + 1, c.heads);
+    return launch_s(stream, prompt_simt_kernel<T, DH>, grid, dim3(256), smem, a);
+}
+
+cudaError_t launch(const evs_prompt_attn_args& c, cudaStream_t stream) {
+    PromptArgs a{};
+    a.q = c.q; a.k = c.k; a.v = c.v; a.o = c.o; a.lse = c.lse; a.starts = c.starts; a.flags = c.flags;
+    a.q_row = c.q_row; a.q_head = c.q_head; a.kv_row = c.kv_row; a.kv_head = c.kv_head; a.o_row = c.o_row;
+    a.N = c.tokens; a.B = c.batch; a.H = c.heads; a.G = c.kv_heads; a.zero_rest = c.zero_rest != 0;
+    a.scale = c.scale != 0.f ? c.scale : 1.f / sqrtf((float)c.head_dim);
+    a.o_vec = (uintptr_t)c.o % 16 == 0 && c.o_row % 8 == 0;
+    if (tensor_ok(c)) {
+        // the ring takes what 227 KB leave: five tiles of 32 KB, four where the starts need their place
+        if (c.head_dim == 64) return launch_tensor<64, 8>(c, a, stream);
+        return prompt_smem(128, 5, c.batch) <= SMEM_MAX ? launch_tensor<128, 5>(c, a, stream) : launch_tensor<128, 4>(c, a, stream);
+    }
+    const bool half = c.dtype == EVS_DTYPE_BF16;
+    switch (c.head_dim) {
+        case 128: return half ? launch_simt<bf16, 128>(c, a, stream) : launch_simt<float, 128>(c, a, stream);
+        case 64: return half ? launch_simt<bf16, 64>(c, a, stream) : launch_simt<float, 64>(c, a, stream);
+        case 32: return half ? launch_simt<bf16, 32>(c, a, stream) : launch_simt<float, 32>(c, a, stream);
+        default: return half ? launch_simt<bf16, 16>(c, a, stream) : launch_simt<float, 16>(c, a, stream);
+    }
+}
+
+}  // namespace
+}  // namespace evs
+
+extern "C" size_t evs_prompt_attention_workspace(const evs_prompt_attn_args* c) {
+    return 0;
+}
+
+extern "C" evs_status evs_prompt_attention(const evs_prompt_attn_args* c, void* stream) {
+    using namespace evs;
+    if (!valid_shape(c)) return EVS_ERR_INVALID_ARG;
+    if (c->tokens == 0) return EVS_OK;
+    const int es = c->dtype == EVS_DTYPE_F32 ? 4 : 2;
+    if (!c->q || !c->k || !c->v || !c->o || !c->starts) return EVS_ERR_INVALID_ARG;
+    if (((uintptr_t)c->q | (uintptr_t)c->k | (uintptr_t)c->v | (uintptr_t)c->o) % es) return EVS_ERR_INVALID_ARG;
+    if (c->q_row < c->head_dim || c->kv_row < c->head_dim || c->o_row < (long long)c->heads * c->head_dim) return EVS_ERR_INVALID_ARG;
+    if ((c->heads > 1 && c->q_head < c->head_dim) || (c->kv_heads > 1 && c->kv_head < c->head_dim)) return EVS_ERR_INVALID_ARG;
+    if (!(c->scale >= 0.f) || isinf(c->scale) || (c->scale > 0.f && c->scale < 1e-30f)) return EVS_ERR_INVALID_ARG;
+    return status_of(launch(*c, (cudaStream_t)stream));
+}

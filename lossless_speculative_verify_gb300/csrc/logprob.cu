@@ -1,0 +1,440 @@
+// Log probabilities of given tokens, with the row's entropy and its largest tokens
+// (evs_token_logprobs).
+//
+//   y_i = (l_i - max l) / T,  Z = sum e^y_i:  log p(t) = y_t - log Z,
+//   entropy = -sum p log p = log Z - sum (e^y_i y_i) / Z.
+//
+// One pass over the row: each thread keeps the running maximum m of what it has seen, s = sum e^y and
+// w = sum e^y (l - m), rescaled when m grows; a row's threads (and the CTAs of a cluster, where there are
+// too few rows for the GPU) join theirs at the end.
+//
+// The largest K tokens, in the order (logit descending, id ascending), come from the same pass: a thread
+// remembers where it met its maximum. A token among the row's K largest can only be one of a thread whose
+// own largest is among the K largest of all threads', so just those K threads' tokens are read a second
+// time (K / 256 of the row, from L2) and merged by warps that hold sorted lists in registers. No list can
+// overflow, whatever the logits are, and no order of execution shows in the result.
+#include "evs_common.cuh"
+#include "sm100_ptx.cuh"
+
+#include <cfloat>
+
+namespace evs {
+namespace {
+
+using bf16 = __nv_bfloat16;
+typedef unsigned long long u64;
+
+constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
+constexpr int LP_MAX_CS = 8;             // portable cluster size
+constexpr int LP_MAX_TOP = 64;
+constexpr uint32_t FULL = 0xffffffffu;
+
+struct LogprobArgs {
+    const void* logits;
+    int64_t ld;
+    int V, n, K;
+    const float* temperature;
+    const int32_t* tokens;
+    float *logprob, *entropy, *top_logprob;
+    int32_t* top_token;
+    uint32_t* flags;
+};
+
+// Position in the order: larger is earlier, 0 is no token. The logit's bits mapped to an ascending
+// integer, then the id descending.
+__device__ __forceinline__ u64 lp_key(float l, int id) {
+    if (!(l > -INFINITY)) return 0;                    // NaN and -inf: ruled out
+    uint32_t k = __float_as_uint(l + 0.f);             // -0 and +0 are one value
+    k = (k & 0x80000000u) ? ~k : (k | 0x80000000u);
+    return ((u64)k << 32) | (u64)(0xffffffffu - (uint32_t)id);
+}
+__device__ __forceinline__ float lp_value(u64 key) {
+    const uint32_t k = (uint32_t)(key >> 32);
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ int lp_id(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
+
+__device__ __forceinline__ u64 lp_max(u64 a, u64 b) { return a > b ? a : b; }
+__device__ __forceinline__ u64 lp_min(u64 a, u64 b) { return a > b ? b : a; }
+
+// A bitonic sequence over the lanes, sorted descending
+__device__ __forceinline__ u64 lp_merge32(u64 v, int lane) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const u64 o = __shfl_xor_sync(FULL, v, d);
+        v = (lane & d) ? lp_min(v, o) : lp_max(v, o);
+    }
+    return v;
+}
+__device__ __forceinline__ u64 lp_sort32(u64 v, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int d = k >> 1; d > 0; d >>= 1) {
+            const u64 o = __shfl_xor_sync(FULL, v, d);
+            v = (((lane & d) == 0) == ((lane & k) == 0)) ? lp_max(v, o) : lp_min(v, o);
+        }
+    return v;
+}
+
+// A warp's largest 32 L keys, descending: place 32 j + lane.
+template <int L> struct WarpTop {
+    u64 a[L];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < L; ++j) a[j] = 0;
+    }
+    // 32 keys in descending order
+    __device__ __forceinline__ void push_sorted(u64 b, int lane) {
+#pragma unroll
+        for (int j = L - 1; j >= 0; --j) {
+            // the larger half of (a[j], b) stays, and goes on against the places before
+            const u64 r = __shfl_xor_sync(FULL, b, 31);
+            const u64 hi = lp_merge32(lp_max(a[j], r), lane);
+            if (j + 1 < L) a[j + 1] = lp_merge32(lp_min(a[j], r), lane);
+            b = hi;
+        }
+        a[0] = b;
+    }
+    __device__ __forceinline__ void push(u64 b, int lane) { push_sorted(lp_sort32(b, lane), lane); }
+};
+
+// All warps' lists into warp 0's, by halves; lists: [LP_WARPS / 2][32 L]. Ends with a barrier only
+// between its steps: callers synchronise before lists is used again.
+template <int L> __device__ __forceinline__ void join_warps(WarpTop<L>& top, u64* lists, int warp, int lane) {
+#pragma unroll 1
+    for (int half = LP_WARPS / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp >= half && warp < 2 * half) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) lists[(warp - half) * 32 * L + j * 32 + lane] = top.a[j];
+        }
+        __syncthreads();
+        if (warp < half) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) top.push_sorted(lists[warp * 32 * L + j * 32 + lane], lane);
+        }
+    }
+}
+
+// Vectors of 16 bytes on their own grid: vector v holds the ids v E - off .. v E - off + E - 1, of which
+// those outside the row are read as -inf.
+template <typename T> struct Row {
+    static constexpr int E = 16 / (int)sizeof(T);
+    const T* base;                       // id 0
+    int off, V;
+    __device__ __forceinline__ void load(int v, float (&x)[E]) const {
+        const int id0 = v * E - off;
+        if (id0 >= 0 && id0 + E <= V) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(base + id0));
+            if constexpr (sizeof(T) == 4) {
+                x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+                x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+            } else {
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[2 * j] = __uint_as_float(w[j] << 16);
+                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[j] = (id0 + j >= 0 && id0 + j < V) ? to_f32(base[id0 + j]) : -INFINITY;
+        }
+    }
+};
+
+// (m, s, w) of two disjoint parts of a row; c: log2(e) / T in two parts
+struct Stat {
+    float m, s, w;
+};
+__device__ __forceinline__ float lp_exp(float x, float2 c) { return ex2_approx_ftz(fmaf(x, c.y, x * c.x)); }
+__device__ __forceinline__ Stat join(Stat a, Stat b, float2 c) {
+    Stat r;
+    r.m = fmaxf(a.m, b.m);
+    // -FLT_MAX: a part of ruled-out tokens, or one beside +inf, has no weight
+    const float da = a.m == r.m ? 0.f : fmaxf(a.m - r.m, -FLT_MAX), db = b.m == r.m ? 0.f : fmaxf(b.m - r.m, -FLT_MAX);
+    const float fa = lp_exp(da, c), fb = lp_exp(db, c);
+    r.s = a.s * fa + b.s * fb;
+    // a part's w moves by its shift; a part without weight has no shift worth the name
+    r.w = (fa > 0.f ? fmaf(a.s, da, a.w) * fa : 0.f) + (fb > 0.f ? fmaf(b.s, db, b.w) * fb : 0.f);
+    return r;
+}
+
+template <typename T, int L>
+__global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
+    constexpr int E = Row<T>::E, U = 4, LL = L ? L : 1;
+    __shared__ u64 lists[LP_WARPS / 2 * 32 * LL];
+    __shared__ u64 parts[LP_MAX_CS * 32 * LL];           // of the cluster's CTAs, in its first
+    __shared__ Stat part_stat[LP_MAX_CS];
+    __shared__ Stat warp_stat[LP_WARPS];
+    __shared__ u64 winners[32 * LL];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t cs, rank;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    // the first CTA's shared memory is written to below: not before it runs
+    if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int64_t r = blockIdx.x / cs;
+    Row<T> row;
+    row.base = (const T*)a.logits + r * a.ld;
+    row.V = a.V;
+    row.off = (int)(((uintptr_t)row.base & 15) / sizeof(T));
+    const int vectors = (a.V + row.off + E - 1) / E, per = (vectors + (int)cs - 1) / (int)cs;
+    const int lo = min(vectors, per * (int)rank), hi = min(vectors, lo + per);
+
+    const float t_in = a.temperature ? a.temperature[r] : 1.f;
+    const bool greedy = !(t_in > 0.f);
+    const float t = greedy ? 1.f : fminf(t_in, 1e30f);   // above: as 1e30, so that ruled-out tokens stay so
+    // log2(e) / T rounded would move every exponent the same way: its remainder is kept
+    float2 c;
+    {
+        const double cd = 1.4426950408889634 / (double)t;
+        c.x = (float)fmin(cd, (double)FLT_MAX);
+        c.y = cd < (double)FLT_MAX ? (float)(cd - (double)c.x) : 0.f;
+    }
+
+    // ---- the pass
+    float m = -INFINITY, s = 0.f, w = 0.f;
+    int where = -1;                                      // first vector of the chunk that holds m
+    for (int v0 = lo + tid; v0 < hi; v0 += U * LP_THREADS) {
+        float x[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (v0 + u * LP_THREADS < hi) {
+                row.load(v0 + u * LP_THREADS, x[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[u][j] = -INFINITY;
+            }
+        }
+        float cm = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < E; ++j) cm = fmaxf(cm, x[u][j]);
+        if (cm > m) {
+            if (m > -INFINITY) {
+                const float d = fmaxf(m - cm, -FLT_MAX), f = lp_exp(d, c);
+                w = f > 0.f ? fmaf(s, d, w) * f : 0.f;
+                s *= f;
+            }
+            m = cm;
+            where = v0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                // -inf, NaN and what +inf leaves behind: no weight, and no NaN in w
+                const float d = fmaxf(x[u][j] - m, -FLT_MAX), e = lp_exp(d, c);
+                s += e;
+                w = fmaf(e, d, w);
+            }
+    }
+    // ---- the row's statistics
+    Stat st = {m, s, w};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stat b;
+        b.m = __shfl_xor_sync(FULL, st.m, o);
+        b.s = __shfl_xor_sync(FULL, st.s, o);
+        b.w = __shfl_xor_sync(FULL, st.w, o);
+        st = (lane & o) ? join(b, st, c) : join(st, b, c);   // the same operands in the same order on both
+    }
+    if (lane == 0) warp_stat[warp] = st;
+    __syncthreads();
+    st = warp_stat[0];
+#pragma unroll
+    for (int i = 1; i < LP_WARPS; ++i) st = join(st, warp_stat[i], c);
+    if (st.m == INFINITY) {                              // the +inf tokens share the mass: count them
+        float mine = 0.f;
+        for (int v = lo + tid; v < hi; v += LP_THREADS) {
+            float x[E];
+            row.load(v, x);
+#pragma unroll
+            for (int j = 0; j < E; ++j) mine += x[j] == INFINITY ? 1.f : 0.f;
+        }
+        mine = warp_sum(mine);
+        __syncthreads();
+        if (lane == 0) warp_stat[warp].s = mine;
+        __syncthreads();
+        st.s = 0.f;
+        st.w = 0.f;
+        for (int i = 0; i < LP_WARPS; ++i) st.s += warp_stat[i].s;
+    }
+
+    // ---- the largest tokens
+    WarpTop<LL> top;
+    top.clear();
+    const bool keys = L > 0 || greedy;
+    const int K = L > 0 ? a.K : 1;                       // greedy: the argmax
+    if (keys) {
+        u64 mine = 0;
+        if (where >= 0) {
+            // the chunk's first token that is m (a later chunk of this thread has only larger ids)
+#pragma unroll 1
+            for (int u = 0; u < U && mine == 0 && where + u * LP_THREADS < hi; ++u) {
+                float x[E];
+                const int v = where + u * LP_THREADS;
+                row.load(v, x);
+#pragma unroll
+                for (int j = E - 1; j >= 0; --j)
+                    if (x[j] == m) mine = lp_key(x[j], v * E - row.off + j);
+            }
+        }
+        top.push(mine, lane);
+        join_warps<LL>(top, lists, warp, lane);
+        if (warp == 0) {
+#pragma unroll
+            for (int j = 0; j < LL; ++j) winners[j * 32 + lane] = top.a[j];
+        }
+        __syncthreads();
+        if (L > 0) {
+            // all tokens of the winners' threads that are not behind the K-th winner
+            const u64 border = winners[K - 1];
+            top.clear();
+            for (int k = warp; k < K; k += LP_WARPS) {
+                const u64 win = winners[k];
+                if (win == 0) break;
+                const int v = (lp_id(win) + row.off) / E, first = lo + (v - lo) % LP_THREADS;   // its thread's first
+                const int count = (hi - first + LP_THREADS - 1) / LP_THREADS;
+#pragma unroll 1
+                for (int i0 = 0; i0 < count; i0 += 32) {
+                    const int i = i0 + lane, vv = first + i * LP_THREADS;
+                    float x[E];
+                    if (i < count) {
+                        row.load(vv, x);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) x[j] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        u64 key = lp_key(x[j], vv * E - row.off + j);
+                        if (key < border) key = 0;
+                        if (__any_sync(FULL, key != 0)) top.push(key, lane);
+                    }
+                }
+            }
+            join_warps<LL>(top, lists, warp, lane);
+        }
+    }
+
+    // ---- the cluster's parts to its first CTA
+    if (cs > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (warp == 0) {
+            if (keys) {
+#pragma unroll
+                for (int j = 0; j < LL; ++j) {
+                    const uint32_t to = map_peer(smem_u32(&parts[rank * 32 * LL + j * 32 + lane]), 0);
+                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(top.a[j]) : "memory");
+                }
+            }
+            if (lane == 0) {
+                const uint32_t to = map_peer(smem_u32(&part_stat[rank]), 0);
+                st_peer_f32(to, st.m);
+                st_peer_f32(to + 4, st.s);
+                st_peer_f32(to + 8, st.w);
+            }
+        }
+        cluster_sync();
+        if (rank != 0) return;
+        st = part_stat[0];
+        for (int i = 1; i < (int)cs; ++i) st = join(st, part_stat[i], c);
+        if (keys && warp == 0) {
+            for (int i = 1; i < (int)cs; ++i)
+#pragma unroll
+                for (int j = 0; j < LL; ++j) top.push_sorted(parts[i * 32 * LL + j * 32 + lane], lane);
+        }
+    }
+
+    // ---- out
+    const bool empty = st.m == -INFINITY;
+    const float log_z = empty ? 0.f : logf(st.s);
+    auto logprob = [&](float l) -> float {
+        if (empty || !(l > -INFINITY)) return -INFINITY;
+        if (l == st.m) return -log_z;                    // also +inf
+        return st.m == INFINITY ? -INFINITY : (l - st.m) / t - log_z;
+    };
+    if (greedy && warp == 0 && lane == 0) winners[0] = top.a[0];
+    __syncthreads();
+    const int best = greedy ? lp_id(winners[0]) : 0;     // -1 of an empty row is no token's id
+    if (tid == 0) {
+        if (a.entropy) a.entropy[r] = greedy || empty ? 0.f : st.m == INFINITY ? log_z : fmaxf(log_z - st.w / st.s / t, 0.f);
+        if (empty && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_EMPTY_ROW);
+    }
+    for (int i = tid; i < a.n; i += LP_THREADS) {
+        const int id = a.tokens[r * a.n + i];
+        float lp = -INFINITY;
+        if ((uint32_t)id >= (uint32_t)a.V) {
+            if (a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_BAD_TOKEN);
+        } else if (greedy) {
+            lp = id == best && !empty ? 0.f : -INFINITY;
+        } else {
+            lp = logprob(to_f32(row.base[id]));
+        }
+        a.logprob[r * a.n + i] = lp;
+    }
+    if (L > 0 && warp == 0) {
+#pragma unroll
+        for (int j = 0; j < LL; ++j) {
+            const int at = j * 32 + lane;
+            if (at >= a.K) continue;
+            const u64 key = top.a[j];
+            const float lp = key == 0 ? -INFINITY : greedy ? (at == 0 ? 0.f : -INFINITY) : logprob(lp_value(key));
+            a.top_logprob[r * a.K + at] = lp;
+            a.top_token[r * a.K + at] = key == 0 ? -1 : lp_id(key);
+        }
+    }
+}
+
+template <typename T, int L> cudaError_t launch(const evs_logprob_args& c, const LogprobArgs& a, int cs, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c.rows * cs);
+    cfg.blockDim = dim3(LP_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, L>, a);
+}
+
+}  // namespace
+}  // namespace evs
+
+extern "C" evs_status evs_token_logprobs(const evs_logprob_args* c, void* stream) {
+    using namespace evs;
+    if (!c || c->rows < 0 || c->vocab < 1 || c->n_tokens < 0 || c->top < 0) return EVS_ERR_INVALID_ARG;
+    if (c->rows > (1 << 24) || c->vocab > (1 << 24) || c->n_tokens > (1 << 20) || c->top > LP_MAX_TOP || c->top > c->vocab)
+        return EVS_ERR_INVALID_ARG;
+    if (c->dtype != EVS_DTYPE_F32 && c->dtype != EVS_DTYPE_BF16) return EVS_ERR_INVALID_ARG;
+    if (c->rows == 0) return EVS_OK;
+    const int es = c->dtype == EVS_DTYPE_F32 ? 4 : 2;
+    if (!c->logits || (uintptr_t)c->logits % es || (c->rows > 1 && c->ld < c->vocab)) return EVS_ERR_INVALID_ARG;
+    if (c->n_tokens > 0 && (!c->tokens || !c->logprob)) return EVS_ERR_INVALID_ARG;
+    if (c->top > 0 && (!c->top_logprob || !c->top_token)) return EVS_ERR_INVALID_ARG;
+    if (c->n_tokens == 0 && c->top == 0 && !c->entropy) return EVS_ERR_INVALID_ARG;
+    LogprobArgs a{c->logits, c->ld, c->vocab, c->n_tokens, c->top, c->temperature, c->tokens, c->logprob, c->entropy,
+                  c->top_logprob, c->top_token, c->flags};
+    // CTAs of a row: more while the rows leave SMs without any and a CTA's share of the row is some passes long
+    int cs = 1;
+    while (cs < LP_MAX_CS && (long long)c->rows * cs < 304 && c->vocab / (cs * 2) >= 4096) cs *= 2;
+    const int lists = c->top == 0 ? 0 : c->top <= 32 ? 1 : 2;
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (c->dtype == EVS_DTYPE_F32)
+        e = lists == 0 ? launch<float, 0>(*c, a, cs, s) : lists == 1 ? launch<float, 1>(*c, a, cs, s) : launch<float, 2>(*c, a, cs, s);
+    else
+        e = lists == 0 ? launch<bf16, 0>(*c, a, cs, s) : lists == 1 ? launch<bf16, 1>(*c, a, cs, s) : launch<bf16, 2>(*c, a, cs, s);
+    return status_of(e);
+}

@@ -1,5 +1,6 @@
-"""Stand-alone operators of the library on torch tensors: attention over a shared prefix, the
-filtered draw, the short causal convolution and the selective scan.
+"""Stand-alone operators of the library on torch tensors: attention over a shared prefix, over whole
+prompts and of trees of drafts, the filtered draw, log probabilities, the short causal convolution and
+the selective scan.
 
 Each function checks its arguments, fills the argument struct of one entry point (include/evs.h
 states the mathematics) and enqueues it on the current stream of the tensors' device, like any
@@ -11,6 +12,8 @@ refused, whichever argument it is (``torch.no_grad()`` or ``detach()`` lets it i
 ``flags`` is an int32 tensor of one element that collects EVS_FLAG_* bits.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -204,15 +207,16 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, state=None, 
 
 def _kv(name, k, v, dtype, shape, dev):
     """Strides of K and V of one kind, which are alike."""
-    for which, t in (("k_", k), ("v_", v)):
+    of = "_" + name if name else ""
+    for which, t in (("k", k), ("v", v)):
         if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
-            raise ValueError(f"{which}{name}: want {dtype} {tuple(shape)} on {dev}")
-        _no_grad(which + name, t)
+            raise ValueError(f"{which}{of}: want {dtype} {tuple(shape)} on {dev}")
+        _no_grad(which + of, t)
     st = k.stride()
     if st[-1] != 1:
-        raise ValueError(f"k_{name}: the head dimension has to be contiguous")
+        raise ValueError(f"k{of}: the head dimension has to be contiguous")
     if v.stride() != st:
-        raise ValueError(f"k_{name} and v_{name}: want equal strides")
+        raise ValueError(f"k{of} and v{of}: want equal strides")
     return st
 
 
@@ -288,3 +292,147 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
             _p(v_block), b_row, b_head, b_cand, o.data_ptr(), o_ld, _p(lse), ws.data_ptr(), n, flag)
         _enqueue(lib.evs_shared_attention, "evs_shared_attention", a, dev)
     return o if lse is None else [o, lse]
+
+
+def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False, flags=None):
+    """Causal attention over whole prompts packed behind each other: q [tokens, heads, dh], k and v [tokens, kv_heads,
+    dh], all fp32 or all bf16. Sequence b is rows starts[b] up to starts[b + 1] of starts [batch + 1] (int32, on the
+    device, ascending); its row i reads its rows j <= i.
+
+    Any strides but the last (k and v alike), so that q, k and v may be parts of one projection's output. heads is
+    a multiple of kv_heads; dh 16, 32, 64 or 128. Rows of no sequence may hold anything; they are left as they were
+    in ``out``, and zero where none is given. Returns out [tokens, heads, dh], or [out, lse fp32 [tokens, heads]],
+    whose rows of no sequence are -inf."""
+    dev = _device("q", q)
+    _need(q.dim() == 3 and q.dtype in _DT, "q: want fp32 or bf16 [tokens, heads, dh]")
+    N, H, dh = q.shape
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k: want [tokens, kv_heads, dh]")
+    G = k.shape[1]
+    _need(dh in (16, 32, 64, 128) and G > 0 and 0 < H <= 1024 and H % G == 0,
+          "head dimension 16, 32, 64 or 128, at most 1024 heads, a multiple of kv_heads")
+    _need(N <= 1 << 24, "at most 2**24 tokens")
+    qs = q.stride()
+    _need(qs[2] == 1, "q: the head dimension has to be contiguous")
+    q_row, q_head = (qs[0] if N > 1 else H * dh), (qs[1] if H > 1 else dh)
+    _need(q_row >= dh and q_head >= dh, "q: rows overlap")
+    ks = _kv("", k, v, q.dtype, (N, G, dh), dev)
+    kv_row, kv_head = (ks[0] if N > 1 else G * dh), (ks[1] if G > 1 else dh)
+    _need(kv_row >= dh and kv_head >= dh, "k: rows overlap")
+    _need(isinstance(starts, torch.Tensor) and starts.dim() == 1 and 2 <= starts.shape[0] <= 1025,
+          "starts: want [batch + 1], at most 1024 sequences")
+    at = _vec("starts", starts, torch.int32, starts.shape, dev)
+    if out is not None:
+        o = out
+        _need(isinstance(o, torch.Tensor) and o.dtype is q.dtype and o.shape == q.shape and o.device == dev,
+              f"out: want {q.dtype} {tuple(q.shape)} on {dev}")
+        _no_grad("out", o)
+        s0, s1, s2 = o.stride()
+        _need(s2 == 1 and (H == 1 or s1 == dh), "out: heads have to be contiguous")
+        o_row = s0 if N > 1 else H * dh
+        _need(o_row >= H * dh, "out: rows overlap")
+    else:
+        o, o_row = torch.empty(N, H, dh, dtype=q.dtype, device=dev), H * dh
+    _need(scale is None or 1e-30 <= scale < math.inf, "scale: above zero")
+    flag = _vec("flags", flags, torch.int32, (1,), dev)
+    lse = torch.empty(N, H, dtype=torch.float32, device=dev) if return_lse else None
+    if N > 0:
+        a = L.pack_prompt_shapes(N, starts.shape[0] - 1, H, G, dh, _DT[q.dtype], out is None,
+                                 0.0 if scale is None else scale) + \
+            L.pack_prompt_rest(q.data_ptr(), q_row, q_head, k.data_ptr(), v.data_ptr(), kv_row, kv_head, at,
+                               o.data_ptr(), o_row, _p(lse), 0, 0, flag)
+        _enqueue(L.load().evs_prompt_attention, "evs_prompt_attention", a, dev)
+    return o if lse is None else [o, lse]
+
+
+def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_nodes=None, *, lens=None, scale=None,
+                   out=None, return_lse=False, flags=None):
+    """Attention of a tree of drafted tokens over each sequence's cache: q [batch, nodes, heads, dh] (at most 128
+    nodes), k_cache and v_cache [batch, kv_heads, capacity, dh] of which cache_len [batch] (int32) rows are readable.
+    Node i reads those and the nodes on its path to the root, itself included: parents [batch, nodes] or [nodes]
+    (int32, on the device) holds the node above it, which comes before it, or -1 below the last cached token. A tree
+    of one node is a decode step. lens [batch] (int32) or None: nodes of each tree; the rest is left as it was in
+    ``out``, and zero where none is given.
+
+    The nodes' K/V are k_nodes and v_nodes [batch, kv_heads, nodes, dh], or without them the cache's rows
+    cache_len[b] + i. All fp32 or all bf16, with any strides but the last (K and V of a pair alike); heads is a
+    multiple of kv_heads; dh 16, 32, 64 or 128. Returns out [batch, nodes, heads, dh], or [out, lse fp32 [batch,
+    nodes, heads]]."""
+    dev = _device("q", q)
+    _need(q.dim() == 4 and q.dtype in _DT, "q: want fp32 or bf16 [batch, nodes, heads, dh]")
+    B, T, H, dh = q.shape
+    _need(isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4, "k_cache: want [batch, kv_heads, capacity, dh]")
+    G, S = k_cache.shape[1:3]
+    dt = q.dtype
+    _need(dh in (16, 32, 64, 128) and G > 0 and 0 < H <= 1024 and H % G == 0,
+          "head dimension 16, 32, 64 or 128, at most 1024 heads, a multiple of kv_heads")
+    _need(1 <= T <= 128 and B <= 1024 and S <= 1 << 30, "at most 1024 sequences, 1 to 128 nodes, 2**30 rows")
+    cs = _kv("cache", k_cache, v_cache, dt, (B, G, S, dh), dev)
+    _need((k_nodes is None) == (v_nodes is None), "k_nodes and v_nodes go together")
+    n_row = n_head = n_seq = 0
+    if k_nodes is not None:
+        ns = _kv("nodes", k_nodes, v_nodes, dt, (B, G, T, dh), dev)
+        n_row, n_head, n_seq = (ns[2] if T > 1 else dh), ns[1], ns[0]
+    else:
+        _need(S > 0, "nodes in the cache want a capacity")
+    _need(isinstance(parents, torch.Tensor) and parents.shape in ((B, T), (T,)), "parents: want [batch, nodes] or [nodes]")
+    par = _vec("parents", parents, torch.int32, parents.shape, dev)
+    _need(cache_len is not None, "cache_len: missing")
+    cached = _vec("cache_len", cache_len, torch.int32, (B,), dev)
+    sizes = _vec("lens", lens, torch.int32, (B,), dev)
+    q_ld = _flat("q", q.unsqueeze(1), dt, (B, 1, T, H, dh), dev)
+    if out is not None:
+        _need(isinstance(out, torch.Tensor) and out.dim() == 4, f"out: want {dt} {tuple(q.shape)} on {dev}")
+        o, o_ld = out, _flat("out", out.unsqueeze(1), dt, (B, 1, T, H, dh), dev)
+    else:
+        o, o_ld = torch.empty(B, T, H, dh, dtype=dt, device=dev), H * dh
+    _need(scale is None or 1e-30 <= scale < math.inf, "scale: above zero")
+    flag = _vec("flags", flags, torch.int32, (1,), dev)
+    lse = torch.empty(B, T, H, dtype=torch.float32, device=dev) if return_lse else None
+    if B > 0:
+        lib = L.load()
+        shapes = L.pack_tree_shapes(B, T, H, G, dh, _DT[dt], S, out is None, 0.0 if scale is None else scale)
+        n = lib.evs_tree_attention_workspace(shapes + L.TREE_NO_REST)
+        _need(n > 0, "sizes that the operator does not take")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        a = shapes + L.pack_tree_rest(
+            q.data_ptr(), q_ld, k_cache.data_ptr(), v_cache.data_ptr(), cs[2] if S > 1 else dh, cs[1], cs[0], cached,
+            par, T if parents.dim() == 2 else 0, _p(k_nodes), _p(v_nodes), n_row, n_head, n_seq, sizes, o.data_ptr(),
+            o_ld, _p(lse), ws.data_ptr(), n, flag)
+        _enqueue(lib.evs_tree_attention, "evs_tree_attention", a, dev)
+    return o if lse is None else [o, lse]
+
+
+def token_logprobs(logits, tokens, *, temperature=None, top=0, return_entropy=False, flags=None):
+    """Log probabilities of ``tokens`` [rows, n] or [rows] (int32) under softmax(logits / temperature), logits [rows,
+    vocab] (fp32 or bf16, any row stride), temperature [rows] fp32 or None; natural logarithms, fp32.
+
+    Returns them, in the shape of tokens, or a list [logprob, entropy [rows] if asked, top_logprob [rows, top] and
+    top_token int32 [rows, top] if top]: the ``top`` (at most 64) largest logits, equal ones by their ids. Logits
+    that are NaN or -inf are ruled out. A temperature that is not above zero puts all mass on the first largest
+    token. An id outside the vocabulary has -inf; behind the last token that is not ruled out, top_token is -1."""
+    dev = _device("logits", logits)
+    _need(logits.dim() == 2 and logits.dtype in _DT, "logits: want fp32 or bf16 [rows, vocab]")
+    R, V = logits.shape
+    _need(1 <= V <= 1 << 24 and R <= 1 << 24, "logits: vocabulary of 1 to 2**24, at most 2**24 rows")
+    _need(logits.stride(1) == 1 or V == 1, "logits: the vocabulary has to be contiguous")
+    ld = logits.stride(0) if R > 1 else V
+    _need(ld >= V, "logits: rows overlap")
+    _need(isinstance(tokens, torch.Tensor) and tokens.dim() in (1, 2) and tokens.shape[0] == R,
+          "tokens: want int32 [rows] or [rows, n]")
+    n = tokens.shape[1] if tokens.dim() == 2 else 1
+    _need(n <= 1 << 20, "tokens: at most 2**20 a row")
+    _need(0 <= top <= min(64, V), "top: 0 to 64, at most the vocabulary")
+    f32 = torch.float32
+    tok = _vec("tokens", tokens, torch.int32, tokens.shape, dev)
+    logprob = torch.empty(tokens.shape, dtype=f32, device=dev)
+    entropy = torch.empty(R, dtype=f32, device=dev) if return_entropy else None
+    top_lp = torch.empty(R, top, dtype=f32, device=dev) if top else None
+    top_id = torch.empty(R, top, dtype=torch.int32, device=dev) if top else None
+    if R > 0 and (n > 0 or top or return_entropy):
+        a = L.pack_logprob(R, V, n, top, _DT[logits.dtype], ld, logits.data_ptr(),
+                           _vec("temperature", temperature, f32, (R,), dev), tok, logprob.data_ptr(), _p(entropy),
+                           _p(top_lp), _p(top_id), _vec("flags", flags, torch.int32, (1,), dev))
+        _enqueue(L.load().evs_token_logprobs, "evs_token_logprobs", a, dev)
+    if entropy is None and not top:
+        return logprob
+    return [t for t in (logprob, entropy, top_lp, top_id) if t is not None]
