@@ -109,37 +109,45 @@ struct Items {
         tile = level - 1;
         return true;
     }
-    // of lane L: rows, key tiles; of the item: key tiles
-    __device__ __forceinline__ int rows(int L) const { return min(128, len - tile * 256 - L * 128); }
-    __device__ __forceinline__ int keys(int L) const { return tile * 2 + L + 1; }
-    __device__ __forceinline__ int keys() const { return keys(rows(1) > 0 ? 1 : 0); }
+    // of lane L: its first row, rows, keys, tiles of K keys; of the item: tiles
+    __device__ __forceinline__ int row0(int L) const { return tile * 256 + L * 128; }
+    __device__ __forceinline__ int rows(int L) const { return min(128, len - row0(L)); }
+    __device__ __forceinline__ int keys(int L) const { return min(len, row0(L) + 128); }
+    template <int K> __device__ __forceinline__ int key_tiles(int L) const { return rows(L) > 0 ? (keys(L) + K - 1) / K : 0; }
+    template <int K> __device__ __forceinline__ int key_tiles() const { return (keys(1) + K - 1) / K; }
 };
 
-constexpr int small_smem(int B) { return 1024 + 256 + (2 * B + 1) * 4; }
-constexpr int prompt_smem(int dh, int stages, int B) { return small_smem(B) + 1024 + (2 + stages) * KEYS * dh * 2; }
+constexpr int BARRIERS = 288;
+constexpr int small_smem(int B) { return 1024 + BARRIERS + (2 * B + 1) * 4; }
+constexpr int prompt_smem(int dh, int stages, int B) {
+    return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
+}
 constexpr int SMEM_MAX = 227 * 1024;
 
 template <int DH, int NST>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, PromptArgs a) {
-    constexpr int HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
+    constexpr int KEYS = tile_keys(DH), HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
+    constexpr int Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
     extern __shared__ uint8_t smem_raw[];
     float* exchange = reinterpret_cast<float*>(smem_raw);                  // [2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + 1024);         // [NST]
     uint64_t* empty = full + NST;                                          // [NST]
     uint64_t* s_full = empty + NST;                                        // [2] scores of a tile in tensor memory
-    uint64_t* p_full = s_full + 2;                                         // [2] weights of a tile there
+    uint64_t* s_free = s_full + 2;                                         // [2] and in registers
+    uint64_t* p_full = s_free + 2;                                         // [2] weights of a tile in tensor memory
     uint64_t* pv_done = p_full + 2;                                        // [2] P V of a tile complete
     uint64_t* q_full = pv_done + 2;                                        // [2] Q of an item there
     uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
     uint64_t* drain = q_free + 2;                                          // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-    int* st = reinterpret_cast<int*>(smem_raw + 1024 + 256);               // [B + 1]
+    int* st = reinterpret_cast<int*>(smem_raw + 1024 + BARRIERS);          // [B + 1]
     int* order = st + a.B + 1;                                             // [B]
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
-    uint8_t* ring = sQ + 2 * TILE;
-    static_assert((2 * NST + 12) * 8 + 4 <= 256, "barriers");
+    uint8_t* ring = sQ + 2 * Q_TILE;
+    static_assert((2 * NST + 14) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert(TILE == tile_bytes(DH) && HALF % 1024 == 0, "tiles on 1024 bytes");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_wait();
@@ -156,6 +164,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 8);
             mbar_init(&p_full[i], 8);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_full[i], 1);
@@ -191,7 +200,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             uint32_t ph = 1, used = 0;                   // parity that a free slot has; slots in use so far
             bool ok = true;
             while (ok && it.next()) {
-                const int n = 2 * it.keys(), g = it.head / (a.H / a.G);
+                const int n = 2 * it.key_tiles<KEYS>(), g = it.head / (a.H / a.G);
                 for (int j = 0; j < n; ++j) {
                     if ((used >> s & 1u) && !mbar_wait(&empty[s], ph)) { ok = false; break; }
                     used |= 1u << s;
@@ -218,11 +227,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 for (int L = 0; L < 2 && ok; ++L) {
                     if (it.rows(L) <= 0) continue;
                     if (cnt[L] > 0 && !mbar_wait(&q_free[L], (cnt[L] - 1) & 1u)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&q_full[L], (uint32_t)TILE);
+                    mbar_arrive_expect_tx(&q_full[L], (uint32_t)Q_TILE);
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(sQ + L * TILE + hf * HALF, &tmQ, hf * 64, it.first + it.tile * 256 + L * 128, it.head, 0,
-                                    &q_full[L], once);
+                        tma_load_4d(sQ + L * Q_TILE + hf * Q_HALF, &tmQ, hf * 64, it.first + it.row0(L), it.head, 0, &q_full[L], once);
                     ++cnt[L];
                 }
             }
@@ -230,59 +238,52 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 for (int L = 0; L < 2; ++L)
                     if (cnt[L] > 0) mbar_wait(&q_full[L], (cnt[L] - 1) & 1u);
         } else if ((role & 1) && lane == 0) {
-            // ---- products of lane L
+            // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
             const int L = role >> 1;
-            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring)),
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring)),
                            dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
-            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + 256u + (uint32_t)L * 128u;
-            int s = 0;                                   // next slot, its phase
-            uint32_t ph = 0, cnt = 0, qn = 0;
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
+            Cursor k(0, NST), v(1, NST);
+            uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, items
             bool ok = true;
-            auto take = [&]() -> int {                   // the next step's tile
-                const int at = s;
-                if (ok && !mbar_wait(&full[at], ph)) ok = false;
-                if (++s == NST) {
-                    s = 0;
-                    ph ^= 1u;
+            auto scores = [&]() {
+                if (!ok || !mbar_wait(&full[k.slot], k.phase) || (sn > 0 && !mbar_wait(&s_free[L], (sn - 1) & 1u))) {
+                    ok = false;
+                    return;
                 }
-                return at;
+                tc_fence_after();
+                issue_scores<DH>(at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                tc_commit(&s_full[L]);
+                tc_commit(&empty[k.slot]);
+                k.next();
             };
             while (ok && it.next()) {
-                const int rows = it.rows(L), n = rows > 0 ? it.keys(L) : 0, all = it.keys();
+                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>(), keys = it.keys(L);
                 if (n > 0) {
                     if (!mbar_wait(&q_full[L], qn & 1u)) { ok = false; break; }
                     ++qn;
-                    int k = take();
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
-                    tc_commit(&s_full[L]);
-                    tc_commit(&empty[k]);
-                    if (n == 1) tc_commit(&q_free[L]);
+                    scores();
+                    if (ok && n == 1) tc_commit(&q_free[L]);
                     for (int t = 0; t < n && ok; ++t) {
-                        // O += P V of this tile, then the next one's scores before any of the commits
-                        const bool next = t + 1 < n;
-                        const int v = take();
-                        if (next) k = take();
-                        if (!ok || !mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
-                        ++cnt;
-                        tc_fence_after();
-                        issue_pv<DH>(o_at, s_at, dv + (uint64_t)((uint32_t)(v * TILE) >> 4), next ? KEYS : rows, t > 0);
-                        if (next) {
-                            issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
-                            tc_commit(&s_full[L]);
-                            tc_commit(&empty[k]);
+                        if (t + 1 < n) {
+                            scores();
+                            if (ok && t + 2 == n) tc_commit(&q_free[L]);
                         }
-                        tc_commit(&empty[v]);
+                        if (!ok || !mbar_wait(&full[v.slot], v.phase) || !mbar_wait(&p_full[L], pn & 1u)) { ok = false; break; }
+                        tc_fence_after();
+                        issue_pv<DH>(at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), keys - t * KEYS, t > 0);
                         tc_commit(&pv_done[L]);
-                        if (t + 2 == n) tc_commit(&q_free[L]);
+                        tc_commit(&empty[v.slot]);
+                        v.next();
                     }
                 }
-                for (int t = n; t < all && ok; ++t)      // tiles that only the other lane reads
-                    for (int j = 0; j < 2; ++j) {
-                        const int at = take();
-                        if (ok) mbar_arrive(&empty[at]);
-                    }
+                for (int t = n; t < all && ok; ++t) {    // tiles that only the other lane reads
+                    if (!mbar_wait(&full[k.slot], k.phase) || !mbar_wait(&full[v.slot], v.phase)) { ok = false; break; }
+                    mbar_arrive(&empty[k.slot]);
+                    mbar_arrive(&empty[v.slot]);
+                    k.next();
+                    v.next();
+                }
             }
             tc_commit(&drain[L]);                        // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
@@ -299,78 +300,84 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     // ---- softmax and epilogue
     asm volatile(EVS_ATTN_SOFT_REGS);
-    SoftThread th;
-    th.init(warp, lane, tmem, exchange, DH);
+    SoftThread<DH> th;
+    th.init(warp, lane, tmem, exchange);
     const int L = th.lane;
     const float sl = a.scale * LOG2E;
-    uint32_t cnt = 0, steps = 0;                         // tiles of this lane, ring steps before this item
+    uint32_t cnt = 0;                                    // tiles of this lane
+    Cursor v(1, NST);
     bool ok = true;                                      // a wait that ran out ends all later ones; barriers go on
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0;
-        return ok;
+    };
+    auto arrive = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    auto before = [&]() {
+        if (cnt > 0) wait(&pv_done[L], (cnt - 1) & 1u);
     };
     while (it.next()) {
-        const int rows = it.rows(L), n = it.keys(L);
-        if (rows > 0) {
-            const bool work = (th.row & ~31) < rows;     // of this warp
-            th.begin();
-            for (int t = 0; t < n; ++t) {
-                wait(&s_full[L], cnt & 1u);
-                const bool last = t == n - 1;
-                if (work) {
-                    uint32_t x[4][16];
-                    tc_fence_after();
-                    th.load(x);
-                    if (last) mask_from(x, th.row + 1 - th.half * 64);
-                    th.template tile<DH>(x, sl, t == 0, [&]() { return wait(&pv_done[L], (cnt - 1) & 1u); });
-                }
-                if (last && (rows & 15)) {
-                    const uint32_t at = steps + 2 * (uint32_t)t + 1;
-                    wait(&full[at % NST], at / NST & 1u);
-                    if (ok) clear_rows<DH>(ring + (size_t)(at % NST) * TILE, rows, th.half * 128 + th.row, 256);
-                    fence_proxy_async_smem();
-                }
-                if (work) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[L]);
-                ++cnt;
-            }
-            wait(&pv_done[L], (cnt - 1) & 1u);
+        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), keys = it.keys(L), row0 = it.row0(L);
+        const bool work = (th.row & ~31) < rows;         // of this warp
+        th.begin();
+        for (int t = 0; t < n; ++t) {
+            wait(&s_full[L], cnt & 1u);
+            const int nv = keys - t * KEYS;              // keys from this tile on
+            uint32_t x[SoftThread<DH>::N];
             if (work) {
-                const float l = th.exchange(th.l, [](float x, float y) { return x + y; });
                 tc_fence_after();
-                const bool live = th.row < rows;
-                const int64_t row = it.first + it.tile * 256 + L * 128 + th.row;
-                // no key with any weight: zero output, lse -inf; a void row: NaN
-                const float inv = ok ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : __int_as_float(0x7fc00000);
-                bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)it.head * DH + th.half * (DH / 2);
-#pragma unroll
-                for (int c = 0; c < DH / 32; ++c) {
-                    uint32_t o[16], w[8];
-                    tmem_ld16_issue(th.o_at + (uint32_t)(c * 16), o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = pack2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                    if (live && a.o_vec) {
-                        *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(dst + c * 16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else if (live) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            reinterpret_cast<uint16_t*>(dst)[c * 16 + j] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
-                    }
-                }
-                if (live && th.half == 0 && a.lse)
-                    a.lse[row * a.H + it.head] = !ok ? inv : l == 0.f ? -INFINITY : th.m * LN2 + logf(l);
-                tc_fence_before();                       // these reads precede the next item's products
+                th.load(x, cnt);
             }
-            __syncwarp();
+            arrive(&s_free[L]);
+            if (nv < KEYS && (nv & 15)) {
+                wait(&full[v.slot], v.phase);
+                if (ok) clear_rows<DH>(ring + (size_t)v.slot * TILE, nv, th.half * 128 + th.row, 256);
+                fence_proxy_async_smem();
+            }
+            if (work) {
+                if ((t + 1) * KEYS > row0 + 1) th.mask_from(x, row0 + th.row + 1 - t * KEYS - th.half * (KEYS / 2));
+                th.tile(x, sl, cnt, t == 0, before);
+                tmem_wait_st();
+            }
+            before();                                    // p_full's phase before is over, too
+            arrive(&p_full[L]);
+            ++cnt;
+            v.next();
         }
-        steps += 2 * (uint32_t)it.keys();
+        for (int t = n; t < it.key_tiles<KEYS>(); ++t) v.next();
+        if (rows <= 0) continue;
+        before();
+        if (work) {
+            const float l = th.exchange(th.l, [](float x, float y) { return x + y; });
+            tc_fence_after();
+            const bool live = th.row < rows;
+            const int64_t row = it.first + row0 + th.row;
+            // no key with any weight: zero output, lse -inf; a void row: NaN
+            const float inv = ok ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : __int_as_float(0x7fc00000);
+            bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)it.head * DH + th.half * (DH / 2);
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+                uint32_t o[16], w[8];
+                tmem_ld16_issue(th.o_at + (uint32_t)(c * 16), o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                if (live && a.o_vec) {
+                    *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(dst + c * 16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                } else if (live) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        reinterpret_cast<uint16_t*>(dst)[c * 16 + j] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
+                }
+            }
+            if (live && th.half == 0 && a.lse)
+                a.lse[row * a.H + it.head] = !ok ? inv : l == 0.f ? -INFINITY : th.m * LN2 + logf(l);
+            tc_fence_before();                           // these reads precede the next item's products
+        }
+        __syncwarp();
     }
     if (!ok && lane == 0 && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_TIMEOUT);
     rest_rows<bf16>(a, st[0], st[a.B], DH, blockIdx.x, gridDim.x, tid, 32 * SOFT_WARPS);
@@ -450,9 +457,9 @@ cudaError_t launch_tensor(const evs_prompt_attn_args& c, const PromptArgs& a, cu
     const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     CUtensorMap q, k, v;
-    if (!make_rows_map(&q, c.q, DH, c.tokens, c.heads, 1, c.q_row, c.q_head, 0) ||
-        !make_rows_map(&k, c.k, DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0) ||
-        !make_rows_map(&v, c.v, DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0))
+    if (!make_rows_map(&q, c.q, Q_ROWS, DH, c.tokens, c.heads, 1, c.q_row, c.q_head, 0) ||
+        !make_rows_map(&k, c.k, tile_keys(DH), DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0) ||
+        !make_rows_map(&v, c.v, tile_keys(DH), DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0))
         return cudaErrorInvalidValue;
     const long long items = ((long long)c.tokens / 256 + c.batch) * c.heads;     // at most
     const int grid = (int)(items < kAttnGrid ? items : kAttnGrid);
@@ -479,9 +486,9 @@ cudaError_t launch(const evs_prompt_attn_args& c, cudaStream_t stream) {
     a.scale = c.scale != 0.f ? c.scale : 1.f / sqrtf((float)c.head_dim);
     a.o_vec = (uintptr_t)c.o % 16 == 0 && c.o_row % 8 == 0;
     if (tensor_ok(c)) {
-        // the ring takes what 227 KB leave: five tiles of 32 KB, four where the starts need their place
+        // the ring takes what 227 KB leave: eight tiles of 20 KB, seven where the starts need their place
         if (c.head_dim == 64) return launch_tensor<64, 8>(c, a, stream);
-        return prompt_smem(128, 5, c.batch) <= SMEM_MAX ? launch_tensor<128, 5>(c, a, stream) : launch_tensor<128, 4>(c, a, stream);
+        return prompt_smem(128, 8, c.batch) <= SMEM_MAX ? launch_tensor<128, 8>(c, a, stream) : launch_tensor<128, 7>(c, a, stream);
     }
     const bool half = c.dtype == EVS_DTYPE_BF16;
     switch (c.head_dim) {

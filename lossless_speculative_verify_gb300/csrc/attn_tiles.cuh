@@ -3,17 +3,21 @@
 //
 // A CTA has two lanes of 128 query rows, each with its own score, weight and output columns in tensor
 // memory and a thread that issues its products:
-//   S[row][key] = Q K^T (fp32, 128 columns) -> registers: running maximum, exp2, sum -> bf16 weights over
-//   columns 0-31 and 64-95 of S -> O += P V with P read from tensor memory, V MN-major from shared memory.
-// Eight warps serve a lane, two threads a row with 64 scores each: the same instructions as with one
-// thread a row, at half the latency of a tile, and that is what bounds a lane: its next scores wait for
-// this tile's weights, since S and P share their columns. The two threads' maxima meet in a barrier that
-// carries one bit, "the maximum of some row has grown by more than 2^8": only then do they exchange them
-// and rescale O. So weights are at most 2^8, and the sum stays fp32.
+//   S[row][key] = Q K^T (fp32) -> registers: running maximum, exp2, sum -> bf16 weights P in tensor memory
+//   -> O += P V with P read from there, V MN-major from shared memory.
+// A lane waits for neither product: the next tile's scores are computed while this one's weights are, and
+// P V while the next one's are. Beside O a lane has three slots of columns (a, b, c), each as wide as half a
+// tile's scores or all of its weights: S of an even tile lies in a and b and its P in a (its scores are in
+// registers by then), S of an odd tile in b and c and its P in c. So S of a tile does not touch the weights
+// of the one before, and touches those of the one before that only behind their product, in the order of
+// issue. That sets the tile's width: 128 columns for heads of 128 are three slots of 40, 80 keys; 192 for
+// heads of 64 are 128 keys. (With P over S, tiles of 128 keys and turns at the softmax: 1.58 ms for 32768
+// tokens x 8 heads of 128; with a place of its own for P, but one only: 1.63.)
+// Eight warps serve a lane, two threads a row with half of the scores each: their maxima meet in a barrier
+// that carries one bit, "the maximum of some row has grown by more than 2^8": only then do they exchange
+// them and rescale O. So weights are at most 2^8, and the sum stays fp32.
 // The weights enter P V as bf16, the type that products with V want: off by 2^-9 relative on average, of
 // both signs, while their sum is fp32.
-//
-// Tensor memory, columns: S/P of lane 0 and 1 at 0 and 128, O at 256 and 384.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -26,7 +30,14 @@ namespace attn {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int KEYS = 128;                    // of a tile
+// A tile's keys; a lane's columns of tensor memory: where S and P of a tile are (by its parity), and O
+constexpr int tile_keys(int dh) { return dh == 128 ? 80 : 128; }
+constexpr uint32_t LANE_COLS = 256;
+__host__ __device__ constexpr uint32_t s_col(int dh, uint32_t tile) { return (tile & 1u) * (uint32_t)(tile_keys(dh) / 2); }
+__host__ __device__ constexpr uint32_t p_col(int dh, uint32_t tile) { return (tile & 1u) * (uint32_t)tile_keys(dh); }
+constexpr uint32_t o_col(int dh) { return LANE_COLS - (uint32_t)dh; }
+constexpr int tile_bytes(int dh) { return tile_keys(dh) * dh * 2; }
+constexpr int Q_ROWS = 128;
 constexpr int SOFT_WARPS = 16, AUX_WARPS = 4, THREADS = 32 * (SOFT_WARPS + AUX_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float LN2 = 0.6931471805599453f, LOG2E = 1.4426950408889634f;
@@ -75,26 +86,49 @@ __device__ __forceinline__ bool bar_any(int id, bool pred) {
     return r != 0;
 }
 
+// Loads and stores of 32 lanes x 32 bits, N consecutive columns a lane, without the wait.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+}
+
 // A softmax thread: row `row` of lane `lane`, the columns of half `half`.
-struct SoftThread {
+template <int DH> struct SoftThread {
+    static constexpr int N = tile_keys(DH) / 2;   // its scores of a tile
     int lane, half, row, bar;            // bar: named barrier of its 64 threads
-    uint32_t s_at, p_at, o_at;           // its scores, weights and output columns
+    uint32_t s_at, p_at, o_at;           // its scores and weights of an even tile, its output columns
     float* xch;                          // [128] of its lane, for what the two threads of a row exchange
     float m, l;                          // running maximum (log2 units), sum over its columns
 
-    __device__ __forceinline__ void init(int warp, int ln, uint32_t tmem, float* exchange, int dh) {
+    __device__ __forceinline__ void init(int warp, int ln, uint32_t tmem, float* exchange) {
         lane = warp >> 3;
         half = (warp >> 2) & 1;
         const int q4 = warp & 3;
         row = q4 * 32 + ln;
         bar = 1 + lane * 4 + q4;
-        const uint32_t rows = tmem + ((uint32_t)(q4 * 32) << 16) + 0u;
-        s_at = rows + (uint32_t)(lane * 128 + half * 64);
-        p_at = s_at;
-        o_at = rows + 256u + (uint32_t)(lane * 128 + half * (dh / 2));
+        const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)lane * LANE_COLS;
+        s_at = at + (uint32_t)(half * N);
+        p_at = at + (uint32_t)(half * (N / 2));
+        o_at = at + o_col(DH) + (uint32_t)(half * (DH / 2));
         xch = exchange + lane * 128;
     }
-    // One value of both threads of the row, by its first user (half 0) and then its second
+    // One value of both threads of the row
     template <typename F> __device__ __forceinline__ float exchange(float mine, F both) {
         if (half == 1) xch[row] = mine;
         named_bar_sync(bar, 64);
@@ -111,36 +145,44 @@ struct SoftThread {
         m = -INFINITY;
         l = 0.f;
     }
-    // The scores x (64 columns) of a tile become weights in tensor memory. first: O holds nothing yet;
-    // pv_done(): waits until the products of the tile before are in O. false: that wait ran out.
-    template <int DH, typename W>
-    __device__ __forceinline__ bool tile(uint32_t (&x)[4][16], float sl, bool first, W pv_done) {
+    // Scores of tile `tile` of the lane
+    __device__ __forceinline__ void load(uint32_t (&x)[N], uint32_t tile) const {
+        const uint32_t at = s_at + s_col(DH, tile);
+        tmem_ld32(at, x);
+        if constexpr (N == 40) tmem_ld8(at + 32, x + 32);
+        else tmem_ld32(at + 32, x + 32);
+        tmem_wait_ld();
+    }
+    // Scores behind the first n of the thread's: no weight
+    static __device__ __forceinline__ void mask_from(uint32_t (&x)[N], int n) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j >= n) x[j] = 0xff800000u;
+    }
+    // The scores x of tile `at` of the lane become weights in tensor memory. first: O holds nothing yet; before():
+    // waits until the products of the tile before are in O.
+    template <typename W> __device__ __forceinline__ void tile(uint32_t (&x)[N], float sl, uint32_t at, bool first, W before) {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; j += 2)
-                mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
+        for (int j = 0; j < N; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
         float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
         auto grown = [&](float v) { return v > m + RESCALE_LOG2 || (m == -INFINITY && v > -INFINITY); };
-        bool ok = true;
-        if (bar_any(bar, grown(mine))) {
+        if (bar_any(bar, grown(mine))) {                 // (also: both threads of a row have their scores)
             mine = exchange(mine, [](float a, float b) { return fmaxf(a, b); });
             const bool move = grown(mine);
             if (!first) {
-                ok = pv_done();
+                before();
                 tc_fence_after();
                 const float f = move ? ex2_approx_ftz(m - mine) : 1.f;
-                if (ok) {
 #pragma unroll 1
-                    for (int c = 0; c < DH / 32; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16_issue(o_at + (uint32_t)(c * 16), o);
-                        tmem_wait_ld();
+                for (int c = 0; c < DH / 32; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16_issue(o_at + (uint32_t)(c * 16), o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st16(o_at + (uint32_t)(c * 16), o);
-                    }
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st16(o_at + (uint32_t)(c * 16), o);
                 }
                 l *= f;
             }
@@ -149,42 +191,40 @@ struct SoftThread {
         const float mb = m == -INFINITY ? 0.f : m;       // only -inf scores so far: weights 0
         const uint64_t sl2 = pair(sl, sl), mb2 = pair(-mb, -mb);
         uint64_t sum0 = 0, sum1 = 0;                     // two fp32 each
+        uint32_t w[N / 2];
+        const uint32_t to = p_at + p_col(DH, at);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {                    // 32 keys: 16 columns of weights
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t* at = &x[2 * c + j / 8][(2 * j) & 15];
-                float e0, e1;
-                unpair(fma2(pair(__uint_as_float(at[0]), __uint_as_float(at[1])), sl2, mb2), e0, e1);
-                e0 = ex2_approx_ftz(e0);
-                e1 = ex2_approx_ftz(e1);
-                if (j & 1) sum1 = add2(sum1, pair(e0, e1));
-                else sum0 = add2(sum0, pair(e0, e1));
-                w[j] = pack2(e0, e1);
-            }
-            tmem_st16(p_at + (uint32_t)(c * 16), w);
+        for (int j = 0; j < N / 2; ++j) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sl2, mb2), e0, e1);
+            e0 = ex2_approx_ftz(e0);
+            e1 = ex2_approx_ftz(e1);
+            if (j & 1) sum1 = add2(sum1, pair(e0, e1));
+            else sum0 = add2(sum0, pair(e0, e1));
+            w[j] = pack2(e0, e1);
+            if (j == 15) tmem_st16(to, *reinterpret_cast<const uint32_t(*)[16]>(w));
         }
+        if constexpr (N == 40) tmem_st4(to + 16, w + 16);
+        else tmem_st16(to + 16, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
         float l0, l1;
         unpair(add2(sum0, sum1), l0, l1);
         l += l0 + l1;
-        return ok;
-    }
-    __device__ __forceinline__ void load(uint32_t (&x)[4][16]) const {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld16_issue(s_at + (uint32_t)(c * 16), x[c]);
-        tmem_wait_ld();
     }
 };
 
-// Keys behind the first n of a thread's 64: no weight
-__device__ __forceinline__ void mask_from(uint32_t (&x)[4][16], int n) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c * 16 + j >= n) x[c][j] = 0xff800000u;
-}
+// Slots of a ring that holds K0 V0 K1 V1 ..., as one who reads every other one goes through them
+struct Cursor {
+    int slot, slots;
+    uint32_t phase;
+    __device__ __forceinline__ Cursor(int first, int n) : slot(first), slots(n), phase(0) {}
+    __device__ __forceinline__ void next() {
+        slot += 2;
+        if (slot >= slots) {
+            slot -= slots;
+            phase ^= 1u;
+        }
+    }
+};
 
 // Clears the rows nv .. up to the end of its 16-row step of a V tile, by `threads` threads: they may hold
 // anything, and the weight 0 of a key does not silence a NaN.
@@ -192,33 +232,26 @@ template <int DH> __device__ __forceinline__ void clear_rows(uint8_t* tile, int 
     const int rows = 16 - (nv & 15);
     for (int e = t; e < rows * (DH / 8); e += threads) {
         const int hf = e / (rows * 8), k = nv + (e - hf * rows * 8) / 8;
-        *reinterpret_cast<uint4*>(tile + hf * KEYS * 128 + k * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(tile + hf * tile_keys(DH) * 128 + k * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
-// Issue of O += P V over the first nv keys, by one thread. accumulate: O holds earlier tiles.
-template <int DH>
-__device__ __forceinline__ void issue_pv(uint32_t o_at, uint32_t s_at, uint64_t vd, int nv, bool accumulate) {
+// Issue of O += P V of tile `tile` of a lane over the first nv keys, by one thread. accumulate: O holds earlier tiles.
+template <int DH> __device__ __forceinline__ void issue_pv(uint32_t lane, uint32_t tile, uint64_t vd, int nv, bool accumulate) {
     constexpr uint32_t id = idesc_bf16_f32_bmn(128, DH);
-    if (nv > KEYS - 16) {
 #pragma unroll
-        for (int kk = 0; kk < KEYS / 16; ++kk)
-            tc_mma_f16_ta(o_at, s_at + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), vd + (uint64_t)((kk * 16 * 128) >> 4), id,
+    for (int kk = 0; kk < tile_keys(DH) / 16; ++kk)
+        if (kk * 16 < nv)
+            tc_mma_f16_ta(lane + o_col(DH), lane + p_col(DH, tile) + (uint32_t)(kk * 8), vd + (uint64_t)((kk * 16 * 128) >> 4), id,
                           (kk > 0 || accumulate) ? 1u : 0u);
-    } else {
-        for (int kk = 0; kk < (nv + 15) / 16; ++kk)
-            tc_mma_f16_ta(o_at, s_at + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), vd + (uint64_t)((kk * 16 * 128) >> 4), id,
-                          (kk > 0 || accumulate) ? 1u : 0u);
-    }
 }
-// Issue of S = Q K^T.
-template <int DH> __device__ __forceinline__ void issue_scores(uint32_t s_at, uint64_t qd, uint64_t kd) {
-    constexpr uint32_t id = idesc_bf16_f32(128, KEYS);
+// Issue of its S = Q K^T.
+template <int DH> __device__ __forceinline__ void issue_scores(uint32_t lane, uint32_t tile, uint64_t qd, uint64_t kd) {
+    constexpr uint32_t id = idesc_bf16_f32(128, tile_keys(DH));
 #pragma unroll
-    for (int kk = 0; kk < DH / 16; ++kk) {
-        const uint32_t off = (uint32_t)((kk >> 2) * KEYS * 128 + (kk & 3) * 32) >> 4;
-        tc_mma_f16(s_at, qd + off, kd + off, id, kk > 0 ? 1u : 0u);
-    }
+    for (int kk = 0; kk < DH / 16; ++kk)
+        tc_mma_f16(lane + s_col(DH, tile), qd + (uint64_t)(((kk >> 2) * Q_ROWS * 128 + (kk & 3) * 32) >> 4),
+                   kd + (uint64_t)(((kk >> 2) * tile_keys(DH) * 128 + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
 }
 
 // ---- host side ----------------------------------------------------------------------------------
@@ -243,16 +276,16 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [seqs][heads][rows][dh] bf16, boxes of 128 rows x 64 columns; rows outside read as zero.
-inline bool make_rows_map(CUtensorMap* m, const void* base, int dh, int rows, int heads, int seqs, int64_t row, int64_t head,
-                          int64_t seq) {
+// [seqs][heads][rows][dh] bf16, boxes of box_rows rows x 64 columns; rows outside read as zero.
+inline bool make_rows_map(CUtensorMap* m, const void* base, int box_rows, int dh, int rows, int heads, int seqs, int64_t row,
+                          int64_t head, int64_t seq) {
     const auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)seqs};
     const cuuint64_t r2 = rows > 1 ? (cuuint64_t)row * 2 : (cuuint64_t)dh * 2;
     const cuuint64_t h2 = heads > 1 ? (cuuint64_t)head * 2 : r2, s2 = seqs > 1 ? (cuuint64_t)seq * 2 : h2;
     const cuuint64_t strides[3] = {r2, h2, s2};
-    const cuuint32_t box[4] = {64, KEYS, 1, 1}, estr[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

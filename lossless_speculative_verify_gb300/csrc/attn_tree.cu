@@ -5,8 +5,8 @@
 //
 // Two launches: partial sums (o unnormalised, m, l) per run of key tiles, then a combine that merges a
 // row's partials and normalises. A segment is a K/V head of a sequence: its rows are the nodes' queries of
-// the heads that share it (row r = node * group + head in the group), its keys the cached rows in tiles of
-// 128 and then the nodes as one more tile, masked by ancestry. The segments' tiles laid end to end make an
+// the heads that share it (row r = node * group + head in the group), its keys the cached rows in tiles
+// and then the nodes in one or two more, masked by ancestry. The segments' tiles laid end to end make an
 // axis that workers take in equal runs, so ragged lengths balance on the device; a run may cross segments.
 #include "attn_simt.cuh"
 #include "attn_tiles.cuh"
@@ -132,37 +132,45 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(256) tree
 // Otherwise each lane is a worker of its own, with half of the ring.
 // Warps 16 and 18: TMA of the lanes; 17 and 19: their products.
 // =========================================================================================
-// A worker's share of a segment: tiles t0 .. t0 + n - 1 of its nt, the last of which is the nodes'.
+// A worker's share of a segment: tiles t0 .. t0 + n - 1 of its nt, the first ntc of which are of the cache.
 struct Piece {
-    int b, g, rt, t0, n, nt, cached, nodes, keys, seg, start;
+    int b, g, rt, t0, n, nt, ntc, cached, nodes, keys, seg, start;
 };
+// Tiles of a segment
+template <int DH> __device__ __forceinline__ int cache_tiles(int cached) { return (cached + tile_keys(DH) - 1) / tile_keys(DH); }
+template <int DH> __device__ __forceinline__ int node_tiles(int nodes) { return (nodes + tile_keys(DH) - 1) / tile_keys(DH); }
 
-constexpr int small_smem(int B) { return 1024 + 256 + 2 * MAX_NODES + (3 * B + 1) * 4; }
-constexpr int tree_smem(int dh, int stages, int B) { return small_smem(B) + 1024 + (2 + stages) * KEYS * dh * 2; }
+constexpr int BARRIERS = 256;
+constexpr int small_smem(int B) { return 1024 + BARRIERS + 2 * MAX_NODES + (3 * B + 1) * 4; }
+constexpr int tree_smem(int dh, int stages, int B) {
+    return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
+}
 constexpr int SMEM_MAX = 227 * 1024;
 
 template <int DH, int NST>
 __global__ void __launch_bounds__(THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__ CUtensorMap tmVC,
                const __grid_constant__ CUtensorMap tmKN, const __grid_constant__ CUtensorMap tmVN, TreeArgs a) {
-    constexpr int HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
+    constexpr int KEYS = tile_keys(DH), HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
+    constexpr int Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
     extern __shared__ uint8_t smem_raw[];
     float* exchange = reinterpret_cast<float*>(smem_raw);                  // [2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + 1024);         // [NST]
     uint64_t* empty = full + NST;                                          // [NST]
     uint64_t* s_full = empty + NST;                                        // [2] scores of a tile in tensor memory
-    uint64_t* p_full = s_full + 2;                                         // [2] weights of a tile there
+    uint64_t* s_free = s_full + 2;                                         // [2] and in registers
+    uint64_t* p_full = s_free + 2;                                         // [2] weights of a tile in tensor memory
     uint64_t* pv_done = p_full + 2;                                        // [2] P V of a tile complete
     uint64_t* q_ready = pv_done + 2;                                       // [2] Q of a piece staged
     uint64_t* drain = q_ready + 2;                                         // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-    uint8_t* up = smem_raw + 1024 + 256;                                   // [2][MAX_NODES] a lane's tree
+    uint8_t* up = smem_raw + 1024 + BARRIERS;                               // [2][MAX_NODES] a lane's tree
     int* pre = reinterpret_cast<int*>(up + 2 * MAX_NODES);                 // [B + 1] cost of one row tile's axis before b
     int* len = pre + a.B + 1;                                              // [B] cached rows
     int* size = len + a.B;                                                 // [B] nodes
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
-    uint8_t* ring = sQ + 2 * TILE;                                         // sQ: [2 lanes][halves][128 rows][128 B]
-    static_assert((2 * NST + 10) * 8 + 4 <= 256, "barriers");
+    uint8_t* ring = sQ + 2 * Q_TILE;                                       // sQ: [2 lanes][halves][128 rows][128 B]
+    static_assert((2 * NST + 12) * 8 + 4 <= BARRIERS, "barriers");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool pairs = a.pair != 0;
 
@@ -180,6 +188,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 8);
             mbar_init(&p_full[i], 8);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_ready[i], 8);
@@ -197,7 +206,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         int run = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            int x = b < a.B && size[b] > 0 ? (len[b] + KEYS - 1) / KEYS + 1 + OVER : 0;
+            int x = b < a.B && size[b] > 0 ? cache_tiles<DH>(len[b]) + node_tiles<DH>(size[b]) + OVER : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -226,9 +235,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     auto of_sequence = [&](Piece& p) {
         p.cached = len[p.b];
         p.nodes = size[p.b];
-        p.nt = (p.cached + KEYS - 1) / KEYS + 1;
+        p.ntc = cache_tiles<DH>(p.cached);
+        p.nt = p.ntc + node_tiles<DH>(p.nodes);
         p.keys = node_keys(a, p.cached, p.nodes, false);
     };
+    // keys of tile t, at least those
+    auto keys_of = [&](const Piece& p, int t) { return t < p.ntc ? p.cached - t * KEYS : p.keys - (t - p.ntc) * KEYS; };
     // the run's first piece that has tiles, and the one behind p; n = 0: none
     auto fit = [&](Piece& p) {
         p.t0 = max(0, lo - p.start - OVER);
@@ -287,9 +299,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                     const int at = slot0 + s, t = p.t0 + (j >> 1);
                     if ((used >> s & 1u) && !mbar_wait(&empty[at], ph)) { ok = false; break; }
                     used |= 1u << s;
-                    const bool node = t == p.nt - 1;
+                    const bool node = t >= p.ntc;
                     const CUtensorMap* m = node && a.kn ? (j & 1 ? &tmVN : &tmKN) : (j & 1 ? &tmVC : &tmKC);
-                    const int row = !node ? t * KEYS : a.kn ? 0 : p.cached;
+                    const int row = !node ? t * KEYS : (t - p.ntc) * KEYS + (a.kn ? 0 : p.cached);
                     uint8_t* dst = ring + (size_t)at * TILE;
                     mbar_arrive_expect_tx(&full[at], (uint32_t)TILE);
 #pragma unroll
@@ -304,49 +316,37 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                 for (int i = 0; i < nslots; ++i)
                     if (used >> i & 1u) mbar_wait(&full[slot0 + i], i < s ? ph ^ 1u : ph);
         } else if ((warp & 1) && lane == 0) {
-            // ---- products of lane L
-            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * TILE)), dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE)),
+            // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE)),
                            dv = smem_desc_sw128_mn(smem_u32(ring + slot0 * TILE), HALF);
-            const uint32_t s_at = tmem + (uint32_t)L * 128u, o_at = tmem + 256u + (uint32_t)L * 128u;
-            int s = 0;                                   // next slot, its phase
-            uint32_t ph = 0, cnt = 0, qn = 0;
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
+            Cursor k(0, nslots), v(1, nslots);
+            uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, pieces
             bool ok = true;
-            auto take = [&]() -> int {                   // the next step's tile
-                const int at = s;
-                if (ok && !mbar_wait(&full[slot0 + at], ph)) ok = false;
-                if (++s == nslots) {
-                    s = 0;
-                    ph ^= 1u;
+            auto scores = [&]() {
+                if (!ok || !mbar_wait(&full[slot0 + k.slot], k.phase) || (sn > 0 && !mbar_wait(&s_free[L], (sn - 1) & 1u))) {
+                    ok = false;
+                    return;
                 }
-                return at;
+                tc_fence_after();
+                issue_scores<DH>(at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                tc_commit(&s_full[L]);
+                tc_commit(&empty[slot0 + k.slot]);
+                k.next();
             };
             for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
                 if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
                 ++qn;
-                int k = take();
-                if (!ok) break;
-                tc_fence_after();
-                issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
-                tc_commit(&s_full[L]);
-                tc_commit(&empty[slot0 + k]);
-                for (int t = 0; t < p.n; ++t) {
-                    // O += P V of this tile, then the next one's scores before any of the commits
-                    const bool next = t + 1 < p.n;
-                    const int v = take();
-                    if (next) k = take();
-                    if (!ok || !mbar_wait(&p_full[L], cnt & 1u)) { ok = false; break; }
-                    ++cnt;
+                scores();
+                for (int t = 0; t < p.n && ok; ++t) {
+                    if (t + 1 < p.n) scores();
+                    if (!ok || !mbar_wait(&full[slot0 + v.slot], v.phase) || !mbar_wait(&p_full[L], pn & 1u)) { ok = false; break; }
                     tc_fence_after();
-                    const int nv = p.t0 + t == p.nt - 1 ? p.keys : min(KEYS, p.cached - (p.t0 + t) * KEYS);
                     // a tile without keys (nodes past the capacity) still clears O where it is the first
-                    issue_pv<DH>(o_at, s_at, dv + (uint64_t)((uint32_t)(v * TILE) >> 4), max(nv, 1), t > 0);
-                    if (next) {
-                        issue_scores<DH>(s_at, qd, dk + (uint64_t)((uint32_t)(k * TILE) >> 4));
-                        tc_commit(&s_full[L]);
-                        tc_commit(&empty[slot0 + k]);
-                    }
-                    tc_commit(&empty[slot0 + v]);
+                    issue_pv<DH>(at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(keys_of(p, p.t0 + t), 1), t > 0);
                     tc_commit(&pv_done[L]);
+                    tc_commit(&empty[slot0 + v.slot]);
+                    v.next();
                 }
             }
             tc_commit(&drain[L]);                        // nothing of this thread's in tensor memory in flight
@@ -364,8 +364,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
 
     // ---- softmax
     asm volatile(EVS_ATTN_SOFT_REGS);
-    SoftThread th;
-    th.init(warp, lane, tmem, exchange, DH);
+    SoftThread<DH> th;
+    th.init(warp, lane, tmem, exchange);
     const int grp = a.H / a.G, in_lane = th.half * 128 + th.row;
     const float sl = a.scale * LOG2E;
     auto lane_sync = [&]() { named_bar_sync(9 + L, 256); };
@@ -382,11 +382,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         const int node = r / grp;
         const int64_t at = live ? ((int64_t)p.b * a.T + node) * a.q_ld + (int64_t)(p.g * grp + r - node * grp) * DH : 0;
         const bf16* src = (const bf16*)a.q + at;
-        uint8_t* dst = sQ + L * TILE + th.row * 128;
+        uint8_t* dst = sQ + L * Q_TILE + th.row * 128;
 #pragma unroll
         for (int c = 0; c < DH / 16; ++c) {              // pieces of 8 columns
             const int col = th.half * (DH / 2) + c * 8;
-            uint8_t* to = dst + (col >> 6) * HALF + (((col >> 3 & 7) ^ (th.row & 7)) << 4);
+            uint8_t* to = dst + (col >> 6) * Q_HALF + (((col >> 3 & 7) ^ (th.row & 7)) << 4);
             if (a.q_vec) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(src + col), "r"(live ? 16 : 0)
                              : "memory");
@@ -407,10 +407,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         if (lane == 0) mbar_arrive(&q_ready[L]);
     };
     uint32_t cnt = 0;                                    // tiles so far
+    Cursor v(1, nslots);
     bool ok = true;                                      // a wait that ran out ends all later ones; barriers go on
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0;
-        return ok;
+    };
+    auto arrive = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    auto before = [&]() {
+        if (cnt > 0) wait(&pv_done[L], (cnt - 1) & 1u);
     };
     Piece p = first_piece();
     if (p.n > 0) {
@@ -421,55 +429,58 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         const int r = row_of(p);
         const bool live = is_live(p, r), work = __any_sync(0xffffffffu, live);
         const Piece nx = next_piece(p);
-        uint64_t path = 0;                               // nodes that this row reads, of this thread's half
-        if (p.t0 + p.n == p.nt) {
+        // nodes that this row reads: bit j is the thread's j-th key of the first and of the second node tile
+        uint64_t path0 = 0, path1 = 0;
+        if (p.t0 + p.n > p.ntc) {
             if (in_lane < p.nodes) up[L * MAX_NODES + in_lane] = parent_of(a, p.b, in_lane, p.g == 0 && p.rt == 0);
             lane_sync();
             if (live)
-                for (int i = r / grp + 1; i > 0; i = up[L * MAX_NODES + i - 1])
-                    if ((i - 1) >> 6 == th.half) path |= 1ull << ((i - 1) & 63);
+                for (int i = r / grp + 1; i > 0; i = up[L * MAX_NODES + i - 1]) {
+                    const int j = (i - 1) % KEYS - th.half * (KEYS / 2);
+                    const uint64_t bit = j >= 0 && j < KEYS / 2 ? 1ull << j : 0;
+                    path0 |= i > KEYS ? 0 : bit;
+                    path1 |= i > KEYS ? bit : 0;
+                }
             lane_sync();                                 // read before the next piece's
         }
         th.begin();
         for (int t = 0; t < p.n; ++t) {
             wait(&s_full[L], cnt & 1u);
-            if (t == p.n - 1 && nx.n > 0) stage(nx);     // the last scores are out: Q's place is free
-            const bool node = p.t0 + t == p.nt - 1;
-            const int nv = node ? p.keys : min(KEYS, p.cached - (p.t0 + t) * KEYS);
+            const int nv = keys_of(p, p.t0 + t), node = p.t0 + t - p.ntc;
+            uint32_t x[SoftThread<DH>::N];
             if (work) {
-                uint32_t x[4][16];
                 tc_fence_after();
-                th.load(x);
-                if (nv < KEYS) mask_from(x, nv - th.half * 64);
-                if (node) {
-                    const uint32_t lo32 = (uint32_t)path, hi32 = (uint32_t)(path >> 32);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (!((c < 2 ? lo32 : hi32) >> ((c & 1) * 16 + j) & 1u)) x[c][j] = 0xff800000u;
-                }
-                th.template tile<DH>(x, sl, t == 0, [&]() { return wait(&pv_done[L], (cnt - 1) & 1u); });
+                th.load(x, cnt);
             }
-            if ((nv & 15) || nv == 0) {
-                const uint32_t at = 2 * cnt + 1, slot = slot0 + at % (uint32_t)nslots;
-                wait(&full[slot], at / (uint32_t)nslots & 1u);
-                if (ok) clear_rows<DH>(ring + (size_t)slot * TILE, nv, in_lane, 256);
+            arrive(&s_free[L]);
+            if (t == p.n - 1 && nx.n > 0) stage(nx);     // the last scores are out: Q's place is free
+            if (nv < KEYS && ((nv & 15) || nv <= 0)) {
+                wait(&full[slot0 + v.slot], v.phase);
+                if (ok) clear_rows<DH>(ring + (size_t)(slot0 + v.slot) * TILE, max(nv, 0), in_lane, 256);
                 fence_proxy_async_smem();
             }
             if (work) {
+                if (nv < KEYS) th.mask_from(x, nv - th.half * (KEYS / 2));
+                if (node >= 0) {
+                    const uint64_t bits = node == 0 ? path0 : path1;
+                    const uint32_t lo32 = (uint32_t)bits, hi32 = (uint32_t)(bits >> 32);
+#pragma unroll
+                    for (int j = 0; j < SoftThread<DH>::N; ++j)
+                        if (!((j < 32 ? lo32 : hi32) >> (j & 31) & 1u)) x[j] = 0xff800000u;
+                }
+                th.tile(x, sl, cnt, t == 0, before);
                 tmem_wait_st();
-                tc_fence_before();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[L]);
+            before();                                    // p_full's phase before is over, too
+            arrive(&p_full[L]);
             ++cnt;
+            v.next();
         }
         if (nx.n > 0) staged();                          // the next scores need not wait for the rest
         // ---- the piece's partials: o, then (m, l). Once a wait has run out, this piece's and those of the
         // worker's later ones are void: l = NaN makes the rows' outputs NaN, whether or not the caller
         // looks at the flag.
-        wait(&pv_done[L], (cnt - 1) & 1u);
+        before();
         if (work) {
             const float l = th.exchange(th.l, [](float x, float y) { return x + y; });
             tc_fence_after();
@@ -511,7 +522,7 @@ template <typename T, int DH> __global__ void __launch_bounds__(128 * GROUPS) tr
     const int tid = threadIdx.x & 127, part = threadIdx.x >> 7, parts = blockDim.x >> 7;
     const int grp = a.H / a.G, b = blockIdx.z, g = blockIdx.y, c4 = tid / RW, r = blockIdx.x * RW + tid % RW;
     // The partial kernel starts its dependents when all before it is done, so the lengths are there
-    const int nodes = nodes_of(a, b, false), cached = cached_of(a, b, false);
+    const int nodes = nodes_of(a, b, false);
     pdl_wait();
     pdl_trigger();
     const bool row = r < a.T * grp, live = r < nodes * grp;
@@ -542,7 +553,7 @@ template <typename T, int DH> __global__ void __launch_bounds__(128 * GROUPS) tr
         if (a.tensor) {
             // the runs that the segment's tiles meet
             const int per_b = a.G * a.tiles, W = a.plan[0], before = a.plan[1 + b], cost = a.plan[2 + b] - before;
-            const int in_b = g * a.tiles + tile, at = per_b * before + in_b * cost + OVER, nt = (cached + KEYS - 1) / KEYS + 1;
+            const int in_b = g * a.tiles + tile, at = per_b * before + in_b * cost + OVER, nt = cost - OVER;
             first = (int64_t)(at / W) + (int64_t)b * per_b + in_b;
             used = (at + nt - 1) / W - at / W + 1;
         } else {
@@ -631,7 +642,8 @@ bool plan_tensor(const evs_tree_attn_args& c, TreeArgs& a, int& grid) {
     a.pair = rows > 128;
     a.seg_rows = (int)(rows < 256 ? rows : 256);
     a.tiles = (int)((rows + 255) / 256);
-    const long long segs = (long long)c.batch * c.kv_heads * a.tiles, tiles = segs * ((c.capacity + KEYS - 1) / KEYS + 1);
+    const long long segs = (long long)c.batch * c.kv_heads * a.tiles, tiles =
+        segs * (((long long)c.capacity + tile_keys(c.head_dim) - 1) / tile_keys(c.head_dim) + (c.nodes > tile_keys(c.head_dim) ? 2 : 1));
     if (tiles + segs * OVER >= (1LL << 30)) return false;
     grid = (int)(tiles < kAttnGrid ? tiles : kAttnGrid);
     a.tensor = 1;
@@ -665,11 +677,11 @@ cudaError_t launch_tensor(const evs_tree_attn_args& c, const TreeArgs& a, int gr
     CUtensorMap kc, vc, kn, vn;
     bool ok = true;
     if (c.capacity > 0)
-        ok = make_rows_map(&kc, c.k_cache, DH, c.capacity, c.kv_heads, c.batch, c.cache_row, c.cache_head, c.cache_seq) &&
-             make_rows_map(&vc, c.v_cache, DH, c.capacity, c.kv_heads, c.batch, c.cache_row, c.cache_head, c.cache_seq);
+        ok = make_rows_map(&kc, c.k_cache, tile_keys(DH), DH, c.capacity, c.kv_heads, c.batch, c.cache_row, c.cache_head, c.cache_seq) &&
+             make_rows_map(&vc, c.v_cache, tile_keys(DH), DH, c.capacity, c.kv_heads, c.batch, c.cache_row, c.cache_head, c.cache_seq);
     if (ok && c.k_nodes)
-        ok = make_rows_map(&kn, c.k_nodes, DH, c.nodes, c.kv_heads, c.batch, c.node_row, c.node_head, c.node_seq) &&
-             make_rows_map(&vn, c.v_nodes, DH, c.nodes, c.kv_heads, c.batch, c.node_row, c.node_head, c.node_seq);
+        ok = make_rows_map(&kn, c.k_nodes, tile_keys(DH), DH, c.nodes, c.kv_heads, c.batch, c.node_row, c.node_head, c.node_seq) &&
+             make_rows_map(&vn, c.v_nodes, tile_keys(DH), DH, c.nodes, c.kv_heads, c.batch, c.node_row, c.node_head, c.node_seq);
     if (!ok) return cudaErrorInvalidValue;
     if (c.capacity == 0) { kc = kn; vc = vn; }
     if (!c.k_nodes) { kn = kc; vn = vc; }
@@ -705,10 +717,10 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
     carve(c, a, grid, (char*)c.workspace);
     cudaError_t e;
     if (tensor)
-        // the ring takes what 227 KB leave: five tiles of 32 KB, four where the lengths need their place
-        e = c.head_dim == 64                                 ? launch_tensor<64, 8>(c, a, grid, stream)
-            : tree_smem(128, 5, c.batch) <= SMEM_MAX ? launch_tensor<128, 5>(c, a, grid, stream)
-                                                     : launch_tensor<128, 4>(c, a, grid, stream);
+        // the ring takes what 227 KB leave: eight tiles of 20 KB, seven where the lengths need their place
+        e = c.head_dim == 64                         ? launch_tensor<64, 8>(c, a, grid, stream)
+            : tree_smem(128, 8, c.batch) <= SMEM_MAX ? launch_tensor<128, 8>(c, a, grid, stream)
+                                                     : launch_tensor<128, 7>(c, a, grid, stream);
     else
         switch (c.head_dim) {
             case 128: e = half ? launch_simt<bf16, 128>(c, a, stream) : launch_simt<float, 128>(c, a, stream); break;
