@@ -148,7 +148,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint8_t* ring = sQ + 2 * Q_TILE;
     static_assert((2 * NST + 14) * 8 + 4 <= BARRIERS, "barriers");
     static_assert(TILE == tile_bytes(DH) && HALF % 1024 == 0, "tiles on 1024 bytes");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     pdl_wait();
     pdl_trigger();
@@ -237,55 +237,56 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!ok)
                 for (int L = 0; L < 2; ++L)
                     if (cnt[L] > 0) mbar_wait(&q_full[L], (cnt[L] - 1) & 1u);
-        } else if ((role & 1) && lane == 0) {
+        } else if (role & 1) {
             // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
             const int L = role >> 1;
             const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring)),
                            dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
             const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
+            const uint32_t leader = elect_leader();
             Cursor k(0, NST), v(1, NST);
             uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, items
             bool ok = true;
             auto scores = [&]() {
-                if (!ok || !mbar_wait(&full[k.slot], k.phase) || (sn > 0 && !mbar_wait(&s_free[L], (sn - 1) & 1u))) {
+                if (!ok || !all_wait(&full[k.slot], k.phase) || (sn > 0 && !all_wait(&s_free[L], (sn - 1) & 1u))) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
-                issue_scores<DH>(at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
-                tc_commit(&s_full[L]);
-                tc_commit(&empty[k.slot]);
+                issue_scores<DH>(leader, at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                commit(leader, &s_full[L]);
+                commit(leader, &empty[k.slot]);
                 k.next();
             };
             while (ok && it.next()) {
                 const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>(), keys = it.keys(L);
                 if (n > 0) {
-                    if (!mbar_wait(&q_full[L], qn & 1u)) { ok = false; break; }
+                    if (!all_wait(&q_full[L], qn & 1u)) { ok = false; break; }
                     ++qn;
                     scores();
-                    if (ok && n == 1) tc_commit(&q_free[L]);
+                    if (ok && n == 1) commit(leader, &q_free[L]);
                     for (int t = 0; t < n && ok; ++t) {
                         if (t + 1 < n) {
                             scores();
-                            if (ok && t + 2 == n) tc_commit(&q_free[L]);
+                            if (ok && t + 2 == n) commit(leader, &q_free[L]);
                         }
-                        if (!ok || !mbar_wait(&full[v.slot], v.phase) || !mbar_wait(&p_full[L], pn & 1u)) { ok = false; break; }
+                        if (!ok || !all_wait(&full[v.slot], v.phase) || !all_wait(&p_full[L], pn & 1u)) { ok = false; break; }
                         tc_fence_after();
-                        issue_pv<DH>(at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), keys - t * KEYS, t > 0);
-                        tc_commit(&pv_done[L]);
-                        tc_commit(&empty[v.slot]);
+                        issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), keys - t * KEYS, t > 0);
+                        commit(leader, &pv_done[L]);
+                        commit(leader, &empty[v.slot]);
                         v.next();
                     }
                 }
                 for (int t = n; t < all && ok; ++t) {    // tiles that only the other lane reads
-                    if (!mbar_wait(&full[k.slot], k.phase) || !mbar_wait(&full[v.slot], v.phase)) { ok = false; break; }
-                    mbar_arrive(&empty[k.slot]);
-                    mbar_arrive(&empty[v.slot]);
+                    if (!all_wait(&full[k.slot], k.phase) || !all_wait(&full[v.slot], v.phase)) { ok = false; break; }
+                    if (leader) mbar_arrive(&empty[k.slot]);
+                    if (leader) mbar_arrive(&empty[v.slot]);
                     k.next();
                     v.next();
                 }
             }
-            tc_commit(&drain[L]);                        // nothing of this thread's in tensor memory in flight
+            commit(leader, &drain[L]);                        // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
         }
         __syncwarp();

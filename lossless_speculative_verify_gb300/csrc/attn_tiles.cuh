@@ -236,22 +236,60 @@ template <int DH> __device__ __forceinline__ void clear_rows(uint8_t* tile, int 
     }
 }
 
-// Issue of O += P V of tile `tile` of a lane over the first nv keys, by one thread. accumulate: O holds earlier tiles.
-template <int DH> __device__ __forceinline__ void issue_pv(uint32_t lane, uint32_t tile, uint64_t vd, int nv, bool accumulate) {
+// A wait of a whole warp, which agrees on how it ended
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0; }
+// One thread of a warp issues its products, but all of it runs the code around them: descriptors and addresses
+// are the same in every lane then, and stay in the uniform registers that the instruction reads them from.
+__device__ __forceinline__ uint32_t elect_leader() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+
+// Issue of O += P V of tile `tile` of a lane over the first nv keys. accumulate: O holds earlier tiles.
+template <int DH>
+__device__ __forceinline__ void issue_pv(uint32_t leader, uint32_t lane, uint32_t tile, uint64_t vd, int nv, bool accumulate) {
     constexpr uint32_t id = idesc_bf16_f32_bmn(128, DH);
 #pragma unroll
     for (int kk = 0; kk < tile_keys(DH) / 16; ++kk)
         if (kk * 16 < nv)
-            tc_mma_f16_ta(lane + o_col(DH), lane + p_col(DH, tile) + (uint32_t)(kk * 8), vd + (uint64_t)((kk * 16 * 128) >> 4), id,
-                          (kk > 0 || accumulate) ? 1u : 0u);
+            mma_ts(leader, lane + o_col(DH), lane + p_col(DH, tile) + (uint32_t)(kk * 8), vd + (uint64_t)((kk * 16 * 128) >> 4), id,
+                   (kk > 0 || accumulate) ? 1u : 0u);
 }
 // Issue of its S = Q K^T.
-template <int DH> __device__ __forceinline__ void issue_scores(uint32_t lane, uint32_t tile, uint64_t qd, uint64_t kd) {
+template <int DH>
+__device__ __forceinline__ void issue_scores(uint32_t leader, uint32_t lane, uint32_t tile, uint64_t qd, uint64_t kd) {
     constexpr uint32_t id = idesc_bf16_f32(128, tile_keys(DH));
 #pragma unroll
     for (int kk = 0; kk < DH / 16; ++kk)
-        tc_mma_f16(lane + s_col(DH, tile), qd + (uint64_t)(((kk >> 2) * Q_ROWS * 128 + (kk & 3) * 32) >> 4),
-                   kd + (uint64_t)(((kk >> 2) * tile_keys(DH) * 128 + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
+        mma_ss(leader, lane + s_col(DH, tile), qd + (uint64_t)(((kk >> 2) * Q_ROWS * 128 + (kk & 3) * 32) >> 4),
+               kd + (uint64_t)(((kk >> 2) * tile_keys(DH) * 128 + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
 }
 
 // ---- host side ----------------------------------------------------------------------------------

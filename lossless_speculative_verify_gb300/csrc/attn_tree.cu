@@ -171,7 +171,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;                                       // sQ: [2 lanes][halves][128 rows][128 B]
     static_assert((2 * NST + 12) * 8 + 4 <= BARRIERS, "barriers");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool pairs = a.pair != 0;
 
     pdl_wait();
@@ -315,41 +315,42 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             if (!ok)                                     // loads in flight end before this CTA does (bounded)
                 for (int i = 0; i < nslots; ++i)
                     if (used >> i & 1u) mbar_wait(&full[slot0 + i], i < s ? ph ^ 1u : ph);
-        } else if ((warp & 1) && lane == 0) {
+        } else if (warp & 1) {
             // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
             const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE)),
                            dv = smem_desc_sw128_mn(smem_u32(ring + slot0 * TILE), HALF);
             const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
+            const uint32_t leader = elect_leader();
             Cursor k(0, nslots), v(1, nslots);
             uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, pieces
             bool ok = true;
             auto scores = [&]() {
-                if (!ok || !mbar_wait(&full[slot0 + k.slot], k.phase) || (sn > 0 && !mbar_wait(&s_free[L], (sn - 1) & 1u))) {
+                if (!ok || !all_wait(&full[slot0 + k.slot], k.phase) || (sn > 0 && !all_wait(&s_free[L], (sn - 1) & 1u))) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
-                issue_scores<DH>(at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
-                tc_commit(&s_full[L]);
-                tc_commit(&empty[slot0 + k.slot]);
+                issue_scores<DH>(leader, at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                commit(leader, &s_full[L]);
+                commit(leader, &empty[slot0 + k.slot]);
                 k.next();
             };
             for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
-                if (!mbar_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
+                if (!all_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
                 ++qn;
                 scores();
                 for (int t = 0; t < p.n && ok; ++t) {
                     if (t + 1 < p.n) scores();
-                    if (!ok || !mbar_wait(&full[slot0 + v.slot], v.phase) || !mbar_wait(&p_full[L], pn & 1u)) { ok = false; break; }
+                    if (!ok || !all_wait(&full[slot0 + v.slot], v.phase) || !all_wait(&p_full[L], pn & 1u)) { ok = false; break; }
                     tc_fence_after();
                     // a tile without keys (nodes past the capacity) still clears O where it is the first
-                    issue_pv<DH>(at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(keys_of(p, p.t0 + t), 1), t > 0);
-                    tc_commit(&pv_done[L]);
-                    tc_commit(&empty[slot0 + v.slot]);
+                    issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(keys_of(p, p.t0 + t), 1), t > 0);
+                    commit(leader, &pv_done[L]);
+                    commit(leader, &empty[slot0 + v.slot]);
                     v.next();
                 }
             }
-            tc_commit(&drain[L]);                        // nothing of this thread's in tensor memory in flight
+            commit(leader, &drain[L]);                        // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
         }
         __syncwarp();

@@ -265,6 +265,8 @@ TREE = [
     (BF16, 1, 1, 1, 128, 4, [0]), (BF16, 1, 4, 1, 128, 300, [0, 300, 128]), (BF16, 7, 4, 4, 128, 257, [1, 127, 128, 129, 257]),
     (BF16, 13, 8, 2, 64, 1000, [0, 999, 1000, 17]), (BF16, 128, 1, 1, 64, 260, [131, 0]), (BF16, 16, 8, 1, 128, 3000, [2999]),
     (BF16, 1, 32, 8, 128, 700, [(i * 37) % 701 for i in range(33)]),
+    # lengths of so many sequences that the ring is smaller
+    (BF16, 1, 8, 2, 128, 900, [(i * 371) % 901 for i in range(64)]), (BF16, 33, 8, 2, 128, 500, [(i * 137) % 501 for i in range(50)]),
     # a lane per row tile
     (BF16, 33, 8, 2, 128, 777, [777, 0, 131]), (BF16, 60, 8, 2, 64, 500, [500, 3, 16]), (BF16, 128, 2, 1, 128, 400, [400, 255]),
     # several row tiles
