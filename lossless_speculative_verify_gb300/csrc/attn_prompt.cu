@@ -117,7 +117,7 @@ struct Items {
     template <int K> __device__ __forceinline__ int key_tiles() const { return (keys(1) + K - 1) / K; }
 };
 
-constexpr int BARRIERS = 288;
+constexpr int BARRIERS = 304;
 constexpr int small_smem(int B) { return 1024 + BARRIERS + (2 * B + 1) * 4; }
 constexpr int prompt_smem(int dh, int stages, int B) {
     return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
@@ -136,9 +136,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint64_t* empty = full + NST;                                          // [NST]
     uint64_t* s_full = empty + NST;                                        // [2] scores of a tile in tensor memory
     uint64_t* s_free = s_full + 2;                                         // [2] and in registers
-    uint64_t* p_full = s_free + 2;                                         // [2] weights of a tile in tensor memory
-    uint64_t* pv_done = p_full + 2;                                        // [2] P V of a tile complete
-    uint64_t* q_full = pv_done + 2;                                        // [2] Q of an item there
+    uint64_t* p_full = s_free + 2;                                         // [2][2] weights of an even, an odd tile there
+    uint64_t* pv_done = p_full + 4;                                        // [2][2] P V of an even, an odd tile complete
+    uint64_t* q_full = pv_done + 4;                                        // [2] Q of an item there
     uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
     uint64_t* drain = q_free + 2;                                          // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -146,7 +146,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int* order = st + a.B + 1;                                             // [B]
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;
-    static_assert((2 * NST + 14) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((2 * NST + 18) * 8 + 4 <= BARRIERS, "barriers");
     static_assert(TILE == tile_bytes(DH) && HALF % 1024 == 0, "tiles on 1024 bytes");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -165,8 +165,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], 8);
-            mbar_init(&p_full[i], 8);
-            mbar_init(&pv_done[i], 1);
+            mbar_init(&p_full[2 * i], 8);
+            mbar_init(&p_full[2 * i + 1], 8);
+            mbar_init(&pv_done[2 * i], 1);
+            mbar_init(&pv_done[2 * i + 1], 1);
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
             mbar_init(&drain[i], 1);
@@ -270,10 +272,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             scores();
                             if (ok && t + 2 == n) commit(leader, &q_free[L]);
                         }
-                        if (!ok || !all_wait(&full[v.slot], v.phase) || !all_wait(&p_full[L], pn & 1u)) { ok = false; break; }
+                        if (!ok || !all_wait(&full[v.slot], v.phase) || !all_wait(&p_full[2 * L + (pn & 1u)], pn >> 1 & 1u)) { ok = false; break; }
                         tc_fence_after();
                         issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), keys - t * KEYS, t > 0);
-                        commit(leader, &pv_done[L]);
+                        commit(leader, &pv_done[2 * L + ((pn - 1) & 1u)]);
                         commit(leader, &empty[v.slot]);
                         v.next();
                     }
@@ -316,8 +318,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
+    // P V of tile cnt - 1. What came two tiles before a tile whose scores are there is done, since a commit is for
+    // all that its thread has issued: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
     auto before = [&]() {
-        if (cnt > 0) wait(&pv_done[L], (cnt - 1) & 1u);
+        if (cnt > 0) wait(&pv_done[2 * L + ((cnt - 1) & 1u)], (cnt - 1) >> 1 & 1u);
     };
     while (it.next()) {
         const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), keys = it.keys(L), row0 = it.row0(L);
@@ -342,8 +346,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 th.tile(x, sl, cnt, t == 0, before);
                 tmem_wait_st();
             }
-            before();                                    // p_full's phase before is over, too
-            arrive(&p_full[L]);
+            arrive(&p_full[2 * L + (cnt & 1u)]);
             ++cnt;
             v.next();
         }

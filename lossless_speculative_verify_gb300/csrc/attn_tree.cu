@@ -140,7 +140,7 @@ struct Piece {
 template <int DH> __device__ __forceinline__ int cache_tiles(int cached) { return (cached + tile_keys(DH) - 1) / tile_keys(DH); }
 template <int DH> __device__ __forceinline__ int node_tiles(int nodes) { return (nodes + tile_keys(DH) - 1) / tile_keys(DH); }
 
-constexpr int BARRIERS = 256;
+constexpr int BARRIERS = 272;
 constexpr int small_smem(int B) { return 1024 + BARRIERS + 2 * MAX_NODES + (3 * B + 1) * 4; }
 constexpr int tree_smem(int dh, int stages, int B) {
     return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
@@ -159,9 +159,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     uint64_t* empty = full + NST;                                          // [NST]
     uint64_t* s_full = empty + NST;                                        // [2] scores of a tile in tensor memory
     uint64_t* s_free = s_full + 2;                                         // [2] and in registers
-    uint64_t* p_full = s_free + 2;                                         // [2] weights of a tile in tensor memory
-    uint64_t* pv_done = p_full + 2;                                        // [2] P V of a tile complete
-    uint64_t* q_ready = pv_done + 2;                                       // [2] Q of a piece staged
+    uint64_t* p_full = s_free + 2;                                         // [2][2] weights of an even, an odd tile there
+    uint64_t* pv_done = p_full + 4;                                        // [2][2] P V of an even, an odd tile complete
+    uint64_t* q_ready = pv_done + 4;                                       // [2] Q of a piece staged
     uint64_t* drain = q_ready + 2;                                         // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     uint8_t* up = smem_raw + 1024 + BARRIERS;                               // [2][MAX_NODES] a lane's tree
@@ -170,7 +170,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     int* size = len + a.B;                                                 // [B] nodes
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;                                       // sQ: [2 lanes][halves][128 rows][128 B]
-    static_assert((2 * NST + 12) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((2 * NST + 16) * 8 + 4 <= BARRIERS, "barriers");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool pairs = a.pair != 0;
 
@@ -189,8 +189,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], 8);
-            mbar_init(&p_full[i], 8);
-            mbar_init(&pv_done[i], 1);
+            mbar_init(&p_full[2 * i], 8);
+            mbar_init(&p_full[2 * i + 1], 8);
+            mbar_init(&pv_done[2 * i], 1);
+            mbar_init(&pv_done[2 * i + 1], 1);
             mbar_init(&q_ready[i], 8);
             mbar_init(&drain[i], 1);
         }
@@ -341,11 +343,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                 scores();
                 for (int t = 0; t < p.n && ok; ++t) {
                     if (t + 1 < p.n) scores();
-                    if (!ok || !all_wait(&full[slot0 + v.slot], v.phase) || !all_wait(&p_full[L], pn & 1u)) { ok = false; break; }
+                    if (!ok || !all_wait(&full[slot0 + v.slot], v.phase) || !all_wait(&p_full[2 * L + (pn & 1u)], pn >> 1 & 1u)) { ok = false; break; }
                     tc_fence_after();
                     // a tile without keys (nodes past the capacity) still clears O where it is the first
                     issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(keys_of(p, p.t0 + t), 1), t > 0);
-                    commit(leader, &pv_done[L]);
+                    commit(leader, &pv_done[2 * L + ((pn - 1) & 1u)]);
                     commit(leader, &empty[slot0 + v.slot]);
                     v.next();
                 }
@@ -418,8 +420,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
+    // P V of tile cnt - 1. What came two tiles before a tile whose scores are there is done, since a commit is for
+    // all that its thread has issued: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
     auto before = [&]() {
-        if (cnt > 0) wait(&pv_done[L], (cnt - 1) & 1u);
+        if (cnt > 0) wait(&pv_done[2 * L + ((cnt - 1) & 1u)], (cnt - 1) >> 1 & 1u);
     };
     Piece p = first_piece();
     if (p.n > 0) {
@@ -472,8 +476,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                 th.tile(x, sl, cnt, t == 0, before);
                 tmem_wait_st();
             }
-            before();                                    // p_full's phase before is over, too
-            arrive(&p_full[L]);
+            arrive(&p_full[2 * L + (cnt & 1u)]);
             ++cnt;
             v.next();
         }
