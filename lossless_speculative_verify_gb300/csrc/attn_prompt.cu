@@ -117,19 +117,17 @@ struct Items {
     template <int K> __device__ __forceinline__ int key_tiles() const { return (keys(1) + K - 1) / K; }
 };
 
-constexpr int BARRIERS = 304;
+constexpr int BARRIERS = 320;
 constexpr int small_smem(int B) { return 1024 + BARRIERS + (2 * B + 1) * 4; }
-constexpr int prompt_smem(int dh, int stages, int B) {
-    return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
-}
-constexpr int SMEM_MAX = 227 * 1024;
+constexpr int prompt_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
+static_assert(prompt_smem(64, 1024) <= 227 * 1024 && prompt_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
-template <int DH, int NST>
+template <int DH>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, PromptArgs a) {
     constexpr int KEYS = tile_keys(DH), HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
-    constexpr int Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
+    constexpr int NST = ring_slots(DH), Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
     extern __shared__ uint8_t smem_raw[];
     float* exchange = reinterpret_cast<float*>(smem_raw);                  // [2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + 1024);         // [NST]
@@ -140,13 +138,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint64_t* pv_done = p_full + 4;                                        // [2][2] P V of an even, an odd tile complete
     uint64_t* q_full = pv_done + 4;                                        // [2] Q of an item there
     uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
-    uint64_t* drain = q_free + 2;                                          // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+    uint64_t* drain = q_free + 2;                                          // [4]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 4);
     int* st = reinterpret_cast<int*>(smem_raw + 1024 + BARRIERS);          // [B + 1]
     int* order = st + a.B + 1;                                             // [B]
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;
-    static_assert((2 * NST + 18) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((2 * NST + 20) * 8 + 4 <= BARRIERS, "barriers");
+    // an even number: a slot is K's or V's, and each thread that waits for one has seen its phase before
+    static_assert(NST % 2 == 0 && NST >= 4, "ring");
     static_assert(TILE == tile_bytes(DH) && HALF % 1024 == 0, "tiles on 1024 bytes");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -172,6 +172,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
             mbar_init(&drain[i], 1);
+            mbar_init(&drain[2 + i], 1);
         }
         fence_barrier_init();
     }
@@ -220,76 +221,80 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!ok)                                     // loads in flight end before this CTA does (bounded)
                 for (int i = 0; i < NST; ++i)
                     if (used >> i & 1u) mbar_wait(&full[i], i < s ? ph ^ 1u : ph);
-        } else if (role == 2 && lane == 0) {
-            // ---- Q
+        } else if (role == 1 || role == 2) {
+            // ---- Q and the scores of lane L: those of the next tile as soon as this one's are in registers
+            const int L = role - 1;
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring));
             const uint64_t once = policy_evict_first();
-            uint32_t cnt[2] = {0, 0};
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS, leader = elect_leader();
+            Cursor k(0, NST);
+            uint32_t cnt = 0, qn = 0;                    // tiles, items
             bool ok = true;
             while (ok && it.next()) {
-                for (int L = 0; L < 2 && ok; ++L) {
-                    if (it.rows(L) <= 0) continue;
-                    if (cnt[L] > 0 && !mbar_wait(&q_free[L], (cnt[L] - 1) & 1u)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&q_full[L], (uint32_t)Q_TILE);
-#pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(sQ + L * Q_TILE + hf * Q_HALF, &tmQ, hf * 64, it.first + it.row0(L), it.head, 0, &q_full[L], once);
-                    ++cnt[L];
-                }
-            }
-            if (!ok)
-                for (int L = 0; L < 2; ++L)
-                    if (cnt[L] > 0) mbar_wait(&q_full[L], (cnt[L] - 1) & 1u);
-        } else if (role & 1) {
-            // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
-            const int L = role >> 1;
-            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring)),
-                           dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
-            const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
-            const uint32_t leader = elect_leader();
-            Cursor k(0, NST), v(1, NST);
-            uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, items
-            bool ok = true;
-            auto scores = [&]() {
-                if (!ok || !all_wait(&full[k.slot], k.phase) || (sn > 0 && !all_wait(&s_free[L], (sn - 1) & 1u))) {
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                issue_scores<DH>(leader, at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
-                commit(leader, &s_full[L]);
-                commit(leader, &empty[k.slot]);
-                k.next();
-            };
-            while (ok && it.next()) {
-                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>(), keys = it.keys(L);
+                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>();
                 if (n > 0) {
+                    if (qn > 0 && !all_wait(&q_free[L], (qn - 1) & 1u)) { ok = false; break; }
+                    if (leader) {
+                        mbar_arrive_expect_tx(&q_full[L], (uint32_t)Q_TILE);
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            tma_load_4d(sQ + L * Q_TILE + hf * Q_HALF, &tmQ, hf * 64, it.first + it.row0(L), it.head, 0, &q_full[L],
+                                        once);
+                    }
+                    __syncwarp();
                     if (!all_wait(&q_full[L], qn & 1u)) { ok = false; break; }
                     ++qn;
-                    scores();
-                    if (ok && n == 1) commit(leader, &q_free[L]);
-                    for (int t = 0; t < n && ok; ++t) {
-                        if (t + 1 < n) {
-                            scores();
-                            if (ok && t + 2 == n) commit(leader, &q_free[L]);
-                        }
-                        if (!ok || !all_wait(&full[v.slot], v.phase) || !all_wait(&p_full[2 * L + (pn & 1u)], pn >> 1 & 1u)) { ok = false; break; }
-                        tc_fence_after();
-                        issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), keys - t * KEYS, t > 0);
-                        commit(leader, &pv_done[2 * L + ((pn - 1) & 1u)]);
-                        commit(leader, &empty[v.slot]);
-                        v.next();
-                    }
                 }
-                for (int t = n; t < all && ok; ++t) {    // tiles that only the other lane reads
-                    if (!all_wait(&full[k.slot], k.phase) || !all_wait(&full[v.slot], v.phase)) { ok = false; break; }
-                    if (leader) mbar_arrive(&empty[k.slot]);
-                    if (leader) mbar_arrive(&empty[v.slot]);
-                    k.next();
-                    v.next();
+                for (int t = 0; t < all; ++t, k.next()) {
+                    if (t >= n) {                        // only the other lane reads it
+                        if (!all_wait(&full[k.slot], k.phase)) { ok = false; break; }
+                        if (leader) mbar_arrive(&empty[k.slot]);
+                        continue;
+                    }
+                    // S goes over the scores of the tile before and the weights of the one before that
+                    if ((cnt > 0 && !all_wait(&s_free[L], (cnt - 1) & 1u)) ||
+                        (cnt > 1 && !all_wait(&pv_done[2 * L + (cnt & 1u)], (cnt - 2) >> 1 & 1u)) || !all_wait(&full[k.slot], k.phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    issue_scores<DH>(leader, at, cnt, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                    commit(leader, &s_full[L]);
+                    commit(leader, &empty[k.slot]);
+                    if (t == n - 1) commit(leader, &q_free[L]);
+                    ++cnt;
                 }
             }
-            commit(leader, &drain[L]);                        // nothing of this thread's in tensor memory in flight
+            commit(leader, &drain[L]);                   // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
+        } else if (role == 3 || role == 4) {
+            // ---- P V of lane L
+            const int L = role - 3;
+            const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring), HALF);
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS, leader = elect_leader();
+            Cursor v(1, NST);
+            uint32_t cnt = 0;
+            bool ok = true;
+            while (ok && it.next()) {
+                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>(), keys = it.keys(L);
+                for (int t = 0; t < all; ++t, v.next()) {
+                    if (!all_wait(&full[v.slot], v.phase)) { ok = false; break; }
+                    if (t >= n) {
+                        if (leader) mbar_arrive(&empty[v.slot]);
+                        continue;
+                    }
+                    const int nv = keys - t * KEYS;      // keys from this tile on
+                    if (nv < KEYS && (nv & 15)) clear_rows<DH>(ring + (size_t)v.slot * TILE, nv, lane);
+                    if (!all_wait(&p_full[2 * L + (cnt & 1u)], cnt >> 1 & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                    issue_pv<DH>(leader, at, cnt, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), nv, t > 0);
+                    commit(leader, &pv_done[2 * L + (cnt & 1u)]);
+                    commit(leader, &empty[v.slot]);
+                    ++cnt;
+                }
+            }
+            commit(leader, &drain[2 + L]);
+            mbar_wait(&drain[2 + L], 0);
         }
         __syncwarp();
         tc_fence_before();
@@ -308,7 +313,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int L = th.lane;
     const float sl = a.scale * LOG2E;
     uint32_t cnt = 0;                                    // tiles of this lane
-    Cursor v(1, NST);
     bool ok = true;                                      // a wait that ran out ends all later ones; barriers go on
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0;
@@ -318,29 +322,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // P V of tile cnt - 1. What came two tiles before a tile whose scores are there is done, since a commit is for
-    // all that its thread has issued: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
+    // P V of tile cnt - 1. That of two tiles before a tile whose scores are there is done, since S went over its
+    // weights: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
     auto before = [&]() {
         if (cnt > 0) wait(&pv_done[2 * L + ((cnt - 1) & 1u)], (cnt - 1) >> 1 & 1u);
     };
     while (it.next()) {
-        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), keys = it.keys(L), row0 = it.row0(L);
+        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), row0 = it.row0(L);
         const bool work = (th.row & ~31) < rows;         // of this warp
         th.begin();
         for (int t = 0; t < n; ++t) {
             wait(&s_full[L], cnt & 1u);
-            const int nv = keys - t * KEYS;              // keys from this tile on
             uint32_t x[SoftThread<DH>::N];
             if (work) {
                 tc_fence_after();
                 th.load(x, cnt);
             }
             arrive(&s_free[L]);
-            if (nv < KEYS && (nv & 15)) {
-                wait(&full[v.slot], v.phase);
-                if (ok) clear_rows<DH>(ring + (size_t)v.slot * TILE, nv, th.half * 128 + th.row, 256);
-                fence_proxy_async_smem();
-            }
             if (work) {
                 if ((t + 1) * KEYS > row0 + 1) th.mask_from(x, row0 + th.row + 1 - t * KEYS - th.half * (KEYS / 2));
                 th.tile(x, sl, cnt, t == 0, before);
@@ -348,9 +346,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
             arrive(&p_full[2 * L + (cnt & 1u)]);
             ++cnt;
-            v.next();
         }
-        for (int t = n; t < it.key_tiles<KEYS>(); ++t) v.next();
         if (rows <= 0) continue;
         before();
         if (work) {
@@ -452,13 +448,13 @@ bool tensor_ok(const evs_prompt_attn_args& c) {
            map_ok(c.v, c.kv_row, c.kv_head, 0, c.kv_heads > 1, false);
 }
 
-template <int DH, int NST>
+template <int DH>
 cudaError_t launch_tensor(const evs_prompt_attn_args& c, const PromptArgs& a, cudaStream_t stream) {
     // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
     // maps does not and wants to find. The limit is that of any batch: this call's own would be lowered by
     // another thread's smaller call before the launch.
-    constexpr int most = prompt_smem(DH, NST, 1024) < SMEM_MAX ? prompt_smem(DH, NST, 1024) : SMEM_MAX;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const cudaError_t e =
+        cudaFuncSetAttribute(prompt_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(DH, 1024));
     if (e != cudaSuccess) return e;
     CUtensorMap q, k, v;
     if (!make_rows_map(&q, c.q, Q_ROWS, DH, c.tokens, c.heads, 1, c.q_row, c.q_head, 0) ||
@@ -467,7 +463,7 @@ cudaError_t launch_tensor(const evs_prompt_attn_args& c, const PromptArgs& a, cu
         return cudaErrorInvalidValue;
     const long long items = ((long long)c.tokens / 256 + c.batch) * c.heads;     // at most
     const int grid = (int)(items < kAttnGrid ? items : kAttnGrid);
-    return launch_s(stream, prompt_tc_kernel<DH, NST>, dim3(grid), dim3(THREADS), (size_t)prompt_smem(DH, NST, c.batch), q, k, v, a);
+    return launch_s(stream, prompt_tc_kernel<DH>, dim3(grid), dim3(THREADS), (size_t)prompt_smem(DH, c.batch), q, k, v, a);
 }
 
 template <typename T, int DH>
@@ -490,9 +486,7 @@ cudaError_t launch(const evs_prompt_attn_args& c, cudaStream_t stream) {
     a.scale = c.scale != 0.f ? c.scale : 1.f / sqrtf((float)c.head_dim);
     a.o_vec = (uintptr_t)c.o % 16 == 0 && c.o_row % 8 == 0;
     if (tensor_ok(c)) {
-        // the ring takes what 227 KB leave: eight tiles of 20 KB, seven where the starts need their place
-        if (c.head_dim == 64) return launch_tensor<64, 8>(c, a, stream);
-        return prompt_smem(128, 8, c.batch) <= SMEM_MAX ? launch_tensor<128, 8>(c, a, stream) : launch_tensor<128, 7>(c, a, stream);
+        return c.head_dim == 64 ? launch_tensor<64>(c, a, stream) : launch_tensor<128>(c, a, stream);
     }
     const bool half = c.dtype == EVS_DTYPE_BF16;
     switch (c.head_dim) {

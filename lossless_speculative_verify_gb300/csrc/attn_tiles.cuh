@@ -2,17 +2,18 @@
 // tensor-core path, and the tensor maps of rows.
 //
 // A CTA has two lanes of 128 query rows, each with its own score, weight and output columns in tensor
-// memory and a thread that issues its products:
+// memory and two warps that issue its products, one for each kind (waits, issue and commits of both in one
+// warp are as long as a tile takes):
 //   S[row][key] = Q K^T (fp32) -> registers: running maximum, exp2, sum -> bf16 weights P in tensor memory
 //   -> O += P V with P read from there, V MN-major from shared memory.
 // A lane waits for neither product: the next tile's scores are computed while this one's weights are, and
 // P V while the next one's are. Beside O a lane has three slots of columns (a, b, c), each as wide as half a
 // tile's scores or all of its weights: S of an even tile lies in a and b and its P in a (its scores are in
 // registers by then), S of an odd tile in b and c and its P in c. So S of a tile does not touch the weights
-// of the one before, and touches those of the one before that only behind their product, in the order of
-// issue. That sets the tile's width: 128 columns for heads of 128 are three slots of 40, 80 keys; 192 for
-// heads of 64 are 128 keys. (With P over S, tiles of 128 keys and turns at the softmax: 1.58 ms for 32768
-// tokens x 8 heads of 128; with a place of its own for P, but one only: 1.63.)
+// of the one before, and touches those of the one before that only when their product is done. That sets the
+// tile's width: 128 columns for heads of 128 are three slots of 40, 80 keys. For heads of 64, 192 columns would
+// be 128 keys, but 96 is what fits a softmax thread's registers (619 us for 629 with 16384 tokens x 16 heads). (With P over S, tiles of 128 keys and turns at the softmax: 1.58 ms for 32768
+// tokens x 8 heads of 128; with a place of its own for P, but one only: 1.63; this: 1.42.)
 // Eight warps serve a lane, two threads a row with half of the scores each: their maxima meet in a barrier
 // that carries one bit, "the maximum of some row has grown by more than 2^8": only then do they exchange
 // them and rescale O. So weights are at most 2^8, and the sum stays fp32.
@@ -31,19 +32,23 @@ namespace attn {
 using bf16 = __nv_bfloat16;
 
 // A tile's keys; a lane's columns of tensor memory: where S and P of a tile are (by its parity), and O
-constexpr int tile_keys(int dh) { return dh == 128 ? 80 : 128; }
+constexpr int tile_keys(int dh) { return dh == 128 ? 80 : 96; }
 constexpr uint32_t LANE_COLS = 256;
 __host__ __device__ constexpr uint32_t s_col(int dh, uint32_t tile) { return (tile & 1u) * (uint32_t)(tile_keys(dh) / 2); }
 __host__ __device__ constexpr uint32_t p_col(int dh, uint32_t tile) { return (tile & 1u) * (uint32_t)tile_keys(dh); }
 constexpr uint32_t o_col(int dh) { return LANE_COLS - (uint32_t)dh; }
 constexpr int tile_bytes(int dh) { return tile_keys(dh) * dh * 2; }
 constexpr int Q_ROWS = 128;
-constexpr int SOFT_WARPS = 16, AUX_WARPS = 4, THREADS = 32 * (SOFT_WARPS + AUX_WARPS);
+// Slots of the ring of K and V tiles. At least three for each worker: who waits for a slot's next phase has to know
+// that the one before is over (see the waits for full[]). More than six of 20 KB cost time: four a lane 232 us for
+// 202 with three (41 nodes x 32 heads over 4 caches of 32768 rows), eight a pair 228 for 220 (packed prompts).
+constexpr int ring_slots(int dh) { return dh == 128 ? 6 : 8; }
+constexpr int SOFT_WARPS = 16, AUX_WARPS = 8, THREADS = 32 * (SOFT_WARPS + AUX_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float LN2 = 0.6931471805599453f, LOG2E = 1.4426950408889634f;
-// Registers of the launch's 640 x 96: 512 x 104 + 128 x 64
-#define EVS_ATTN_SOFT_REGS "setmaxnreg.inc.sync.aligned.u32 104;"
-#define EVS_ATTN_AUX_REGS "setmaxnreg.dec.sync.aligned.u32 64;"
+// Registers of the launch's 768 x 80: 512 x 96 + 256 x 48
+#define EVS_ATTN_SOFT_REGS "setmaxnreg.inc.sync.aligned.u32 96;"
+#define EVS_ATTN_AUX_REGS "setmaxnreg.dec.sync.aligned.u32 48;"
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -150,6 +155,7 @@ template <int DH> struct SoftThread {
         const uint32_t at = s_at + s_col(DH, tile);
         tmem_ld32(at, x);
         if constexpr (N == 40) tmem_ld8(at + 32, x + 32);
+        else if constexpr (N == 48) tmem_ld16_issue(at + 32, *reinterpret_cast<uint32_t(*)[16]>(x + 32));
         else tmem_ld32(at + 32, x + 32);
         tmem_wait_ld();
     }
@@ -205,6 +211,7 @@ template <int DH> struct SoftThread {
             if (j == 15) tmem_st16(to, *reinterpret_cast<const uint32_t(*)[16]>(w));
         }
         if constexpr (N == 40) tmem_st4(to + 16, w + 16);
+        else if constexpr (N == 48) { tmem_st4(to + 16, w + 16); tmem_st4(to + 20, w + 20); }
         else tmem_st16(to + 16, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
         float l0, l1;
         unpair(add2(sum0, sum1), l0, l1);
@@ -226,14 +233,17 @@ struct Cursor {
     }
 };
 
-// Clears the rows nv .. up to the end of its 16-row step of a V tile, by `threads` threads: they may hold
-// anything, and the weight 0 of a key does not silence a NaN.
-template <int DH> __device__ __forceinline__ void clear_rows(uint8_t* tile, int nv, int t, int threads) {
+// Clears the rows nv .. up to the end of their 16-row step of a V tile, by a warp, ahead of its product: they may
+// hold anything, and the weight 0 of a key does not silence a NaN. (Two lanes may both write these zeros.)
+template <int DH> __device__ __forceinline__ void clear_rows(uint8_t* tile, int nv, int lane) {
     const int rows = 16 - (nv & 15);
-    for (int e = t; e < rows * (DH / 8); e += threads) {
+#pragma unroll 1
+    for (int e = lane; e < rows * (DH / 8); e += 32) {
         const int hf = e / (rows * 8), k = nv + (e - hf * rows * 8) / 8;
         *reinterpret_cast<uint4*>(tile + hf * tile_keys(DH) * 128 + k * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 // A wait of a whole warp, which agrees on how it ended

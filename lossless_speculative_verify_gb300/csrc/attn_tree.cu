@@ -130,7 +130,7 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(256) tree
 // Partials on the tensor cores (bf16, head width 64 or 128; see attn_tiles.cuh). In segments of more than
 // 128 rows a CTA is a worker: its lanes are two row tiles, and each K/V tile that TMA brings serves both.
 // Otherwise each lane is a worker of its own, with half of the ring.
-// Warps 16 and 18: TMA of the lanes; 17 and 19: their products.
+// Warps 16 and 17: TMA of the lanes; 18 and 19: their scores; 20 and 21: P V.
 // =========================================================================================
 // A worker's share of a segment: tiles t0 .. t0 + n - 1 of its nt, the first ntc of which are of the cache.
 struct Piece {
@@ -140,19 +140,17 @@ struct Piece {
 template <int DH> __device__ __forceinline__ int cache_tiles(int cached) { return (cached + tile_keys(DH) - 1) / tile_keys(DH); }
 template <int DH> __device__ __forceinline__ int node_tiles(int nodes) { return (nodes + tile_keys(DH) - 1) / tile_keys(DH); }
 
-constexpr int BARRIERS = 272;
+constexpr int BARRIERS = 288;
 constexpr int small_smem(int B) { return 1024 + BARRIERS + 2 * MAX_NODES + (3 * B + 1) * 4; }
-constexpr int tree_smem(int dh, int stages, int B) {
-    return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + stages * tile_bytes(dh);
-}
-constexpr int SMEM_MAX = 227 * 1024;
+constexpr int tree_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
+static_assert(tree_smem(64, 1024) <= 227 * 1024 && tree_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
-template <int DH, int NST>
+template <int DH>
 __global__ void __launch_bounds__(THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__ CUtensorMap tmVC,
                const __grid_constant__ CUtensorMap tmKN, const __grid_constant__ CUtensorMap tmVN, TreeArgs a) {
     constexpr int KEYS = tile_keys(DH), HALVES = DH / 64, HALF = KEYS * 128, TILE = HALF * HALVES;
-    constexpr int Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
+    constexpr int NST = ring_slots(DH), Q_HALF = Q_ROWS * 128, Q_TILE = Q_HALF * HALVES;
     extern __shared__ uint8_t smem_raw[];
     float* exchange = reinterpret_cast<float*>(smem_raw);                  // [2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + 1024);         // [NST]
@@ -162,15 +160,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     uint64_t* p_full = s_free + 2;                                         // [2][2] weights of an even, an odd tile there
     uint64_t* pv_done = p_full + 4;                                        // [2][2] P V of an even, an odd tile complete
     uint64_t* q_ready = pv_done + 4;                                       // [2] Q of a piece staged
-    uint64_t* drain = q_ready + 2;                                         // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+    uint64_t* drain = q_ready + 2;                                         // [4]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 4);
     uint8_t* up = smem_raw + 1024 + BARRIERS;                               // [2][MAX_NODES] a lane's tree
     int* pre = reinterpret_cast<int*>(up + 2 * MAX_NODES);                 // [B + 1] cost of one row tile's axis before b
     int* len = pre + a.B + 1;                                              // [B] cached rows
     int* size = len + a.B;                                                 // [B] nodes
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;                                       // sQ: [2 lanes][halves][128 rows][128 B]
-    static_assert((2 * NST + 16) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((2 * NST + 18) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert(NST >= 6, "three slots a worker");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool pairs = a.pair != 0;
 
@@ -195,6 +194,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             mbar_init(&pv_done[2 * i + 1], 1);
             mbar_init(&q_ready[i], 8);
             mbar_init(&drain[i], 1);
+            mbar_init(&drain[2 + i], 1);
         }
         fence_barrier_init();
     }
@@ -230,7 +230,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         if (tid == 0) a.plan[0] = W;
     }
     // Lane L's run of the axis and slots of the ring
-    const int L = warp < SOFT_WARPS ? warp >> 3 : (warp - SOFT_WARPS) >> 1;
+    const int L = warp < SOFT_WARPS ? warp >> 3 : warp & 1, role = (warp - SOFT_WARPS) >> 1;
     const int worker = pairs ? (int)blockIdx.x : 2 * (int)blockIdx.x + L;
     const int lo = min(total, W * worker), hi = min(lo + W, total);
     const int slot0 = pairs || L == 0 ? 0 : NST / 2, nslots = pairs ? NST : NST / 2;
@@ -289,7 +289,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     // Ring steps of a worker: K0 V0 K1 V1 ... over all its pieces, in the order of use.
     if (warp >= SOFT_WARPS) {
         asm volatile(EVS_ATTN_AUX_REGS);
-        if ((warp & 1) == 0 && lane == 0 && (L == 0 || !pairs)) {
+        if (role == 0 && lane == 0 && (L == 0 || !pairs)) {
             // ---- TMA
             const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
             int s = 0;
@@ -317,43 +317,59 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             if (!ok)                                     // loads in flight end before this CTA does (bounded)
                 for (int i = 0; i < nslots; ++i)
                     if (used >> i & 1u) mbar_wait(&full[slot0 + i], i < s ? ph ^ 1u : ph);
-        } else if (warp & 1) {
-            // ---- products of lane L: S of the next tile as soon as this one's is in registers, then P V
-            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE)),
-                           dv = smem_desc_sw128_mn(smem_u32(ring + slot0 * TILE), HALF);
-            const uint32_t at = tmem + (uint32_t)L * LANE_COLS;
-            const uint32_t leader = elect_leader();
-            Cursor k(0, nslots), v(1, nslots);
-            uint32_t sn = 0, pn = 0, qn = 0;             // scores issued, weights used, pieces
+        } else if (role == 1) {
+            // ---- scores of lane L: those of the next tile as soon as this one's are in registers
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ + L * Q_TILE)), dk = smem_desc_sw128(smem_u32(ring + slot0 * TILE));
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS, leader = elect_leader();
+            Cursor k(0, nslots);
+            uint32_t cnt = 0, qn = 0;                    // tiles, pieces
             bool ok = true;
-            auto scores = [&]() {
-                if (!ok || !all_wait(&full[slot0 + k.slot], k.phase) || (sn > 0 && !all_wait(&s_free[L], (sn - 1) & 1u))) {
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                issue_scores<DH>(leader, at, sn++, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
-                commit(leader, &s_full[L]);
-                commit(leader, &empty[slot0 + k.slot]);
-                k.next();
-            };
             for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
                 if (!all_wait(&q_ready[L], qn & 1u)) { ok = false; break; }
                 ++qn;
-                scores();
-                for (int t = 0; t < p.n && ok; ++t) {
-                    if (t + 1 < p.n) scores();
-                    if (!ok || !all_wait(&full[slot0 + v.slot], v.phase) || !all_wait(&p_full[2 * L + (pn & 1u)], pn >> 1 & 1u)) { ok = false; break; }
+                for (int t = 0; t < p.n; ++t, k.next()) {
+                    // S goes over the scores of the tile before and the weights of the one before that. The ring's
+                    // slot last: in a ring of three, V of the latter was in it, and a wait for a slot's next phase
+                    // is one for that phase only if the one before is over
+                    if ((cnt > 0 && !all_wait(&s_free[L], (cnt - 1) & 1u)) ||
+                        (cnt > 1 && !all_wait(&pv_done[2 * L + (cnt & 1u)], (cnt - 2) >> 1 & 1u)) ||
+                        !all_wait(&full[slot0 + k.slot], k.phase)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
-                    // a tile without keys (nodes past the capacity) still clears O where it is the first
-                    issue_pv<DH>(leader, at, pn++, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(keys_of(p, p.t0 + t), 1), t > 0);
-                    commit(leader, &pv_done[2 * L + ((pn - 1) & 1u)]);
-                    commit(leader, &empty[slot0 + v.slot]);
-                    v.next();
+                    issue_scores<DH>(leader, at, cnt, qd, dk + (uint64_t)((uint32_t)(k.slot * TILE) >> 4));
+                    commit(leader, &s_full[L]);
+                    commit(leader, &empty[slot0 + k.slot]);
+                    ++cnt;
                 }
             }
-            commit(leader, &drain[L]);                        // nothing of this thread's in tensor memory in flight
+            commit(leader, &drain[L]);                   // nothing of this thread's in tensor memory in flight
             mbar_wait(&drain[L], 0);
+        } else if (role == 2) {
+            // ---- P V of lane L
+            const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + slot0 * TILE), HALF);
+            const uint32_t at = tmem + (uint32_t)L * LANE_COLS, leader = elect_leader();
+            Cursor v(1, nslots);
+            uint32_t cnt = 0;
+            bool ok = true;
+            for (Piece p = first_piece(); p.n > 0 && ok; p = next_piece(p)) {
+                for (int t = 0; t < p.n; ++t, v.next()) {
+                    if (!all_wait(&full[slot0 + v.slot], v.phase)) { ok = false; break; }
+                    // a tile without keys (nodes past the capacity) still clears O where it is the first: one step of
+                    // cleared rows
+                    const int nv = max(keys_of(p, p.t0 + t), 0);
+                    if (nv < KEYS && ((nv & 15) || nv == 0)) clear_rows<DH>(ring + (size_t)(slot0 + v.slot) * TILE, nv, lane);
+                    if (!all_wait(&p_full[2 * L + (cnt & 1u)], cnt >> 1 & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                    issue_pv<DH>(leader, at, cnt, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(nv, 1), t > 0);
+                    commit(leader, &pv_done[2 * L + (cnt & 1u)]);
+                    commit(leader, &empty[slot0 + v.slot]);
+                    ++cnt;
+                }
+            }
+            commit(leader, &drain[2 + L]);
+            mbar_wait(&drain[2 + L], 0);
         }
         __syncwarp();
         tc_fence_before();
@@ -410,7 +426,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         if (lane == 0) mbar_arrive(&q_ready[L]);
     };
     uint32_t cnt = 0;                                    // tiles so far
-    Cursor v(1, nslots);
     bool ok = true;                                      // a wait that ran out ends all later ones; barriers go on
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0;
@@ -420,8 +435,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // P V of tile cnt - 1. What came two tiles before a tile whose scores are there is done, since a commit is for
-    // all that its thread has issued: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
+    // P V of tile cnt - 1. That of two tiles before a tile whose scores are there is done, since S went over its
+    // weights: so a barrier for even and one for odd tiles are never a phase ahead of a wait.
     auto before = [&]() {
         if (cnt > 0) wait(&pv_done[2 * L + ((cnt - 1) & 1u)], (cnt - 1) >> 1 & 1u);
     };
@@ -459,11 +474,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             }
             arrive(&s_free[L]);
             if (t == p.n - 1 && nx.n > 0) stage(nx);     // the last scores are out: Q's place is free
-            if (nv < KEYS && ((nv & 15) || nv <= 0)) {
-                wait(&full[slot0 + v.slot], v.phase);
-                if (ok) clear_rows<DH>(ring + (size_t)(slot0 + v.slot) * TILE, max(nv, 0), in_lane, 256);
-                fence_proxy_async_smem();
-            }
             if (work) {
                 if (nv < KEYS) th.mask_from(x, nv - th.half * (KEYS / 2));
                 if (node >= 0) {
@@ -478,7 +488,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             }
             arrive(&p_full[2 * L + (cnt & 1u)]);
             ++cnt;
-            v.next();
         }
         if (nx.n > 0) staged();                          // the next scores need not wait for the rest
         // ---- the piece's partials: o, then (m, l). Once a wait has run out, this piece's and those of the
@@ -670,13 +679,12 @@ size_t carve(const evs_tree_attn_args& c, TreeArgs& a, int grid, char* base) {
     return off;
 }
 
-template <int DH, int NST>
+template <int DH>
 cudaError_t launch_tensor(const evs_tree_attn_args& c, const TreeArgs& a, int grid, cudaStream_t stream) {
     // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
     // maps does not and wants to find. The limit is that of any batch: this call's own would be lowered by
     // another thread's smaller call before the launch.
-    constexpr int most = tree_smem(DH, NST, 1024) < SMEM_MAX ? tree_smem(DH, NST, 1024) : SMEM_MAX;
-    const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<DH, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem(DH, 1024));
     if (e != cudaSuccess) return e;
     CUtensorMap kc, vc, kn, vn;
     bool ok = true;
@@ -689,7 +697,7 @@ cudaError_t launch_tensor(const evs_tree_attn_args& c, const TreeArgs& a, int gr
     if (!ok) return cudaErrorInvalidValue;
     if (c.capacity == 0) { kc = kn; vc = vn; }
     if (!c.k_nodes) { kn = kc; vn = vc; }
-    return launch_s(stream, tree_tc_kernel<DH, NST>, dim3(grid), dim3(THREADS), (size_t)tree_smem(DH, NST, c.batch), kc, vc, kn, vn, a);
+    return launch_s(stream, tree_tc_kernel<DH>, dim3(grid), dim3(THREADS), (size_t)tree_smem(DH, c.batch), kc, vc, kn, vn, a);
 }
 
 template <typename T, int DH, int R> cudaError_t launch_rows(const evs_tree_attn_args& c, const TreeArgs& a, cudaStream_t stream) {
@@ -721,10 +729,7 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
     carve(c, a, grid, (char*)c.workspace);
     cudaError_t e;
     if (tensor)
-        // the ring takes what 227 KB leave: eight tiles of 20 KB, seven where the lengths need their place
-        e = c.head_dim == 64                         ? launch_tensor<64, 8>(c, a, grid, stream)
-            : tree_smem(128, 8, c.batch) <= SMEM_MAX ? launch_tensor<128, 8>(c, a, grid, stream)
-                                                     : launch_tensor<128, 7>(c, a, grid, stream);
+        e = c.head_dim == 64 ? launch_tensor<64>(c, a, grid, stream) : launch_tensor<128>(c, a, grid, stream);
     else
         switch (c.head_dim) {
             case 128: e = half ? launch_simt<bf16, 128>(c, a, stream) : launch_simt<float, 128>(c, a, stream); break;
