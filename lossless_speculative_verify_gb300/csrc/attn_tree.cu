@@ -17,8 +17,11 @@ namespace {
 using namespace attn;
 
 constexpr int MAX_NODES = 128;
-// What a segment costs beside its tiles, in tiles: Q, the partials
-constexpr int OVER = 1;
+// What a segment costs beside its tiles, in tiles: Q, the partials. About 2.5 us, where a tile takes a pair of lanes
+// 0.95 and a lane of its own 1.8 (heads of 64: half as much). With 1 everywhere the CTA with the segments of a
+// sequence that has just begun ended 20 us behind the others of 60 (60 nodes x 32 heads x 16), and 64 single tokens
+// with heads of 64 took 65 us for 60.
+constexpr int over_tiles(bool pair, int dh) { return pair ? 4 : dh == 64 ? 3 : 1; }
 
 struct TreeArgs {
     const void *q, *kc, *vc, *kn, *vn;
@@ -36,9 +39,9 @@ struct TreeArgs {
     // or both, so no two share a number. On CUDA cores slot i of segment s is s * slots + i.
     float* po;
     float2* pml;
-    int seg_rows, tiles, slots, tensor, pair;
+    int seg_rows, tiles, slots, tensor, pair, over;
     int* plan;                           // run length, then the axis' cost before each sequence, for one K/V head's row tile
-    int q_vec;
+    int q_vec, o_vec;                    // q on 16 bytes, o on four elements
 };
 
 __host__ __device__ inline int rows4(int rows) { return (rows + 3) & ~3; }
@@ -208,7 +211,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         int run = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            int x = b < a.B && size[b] > 0 ? cache_tiles<DH>(len[b]) + node_tiles<DH>(size[b]) + OVER : 0;
+            int x = b < a.B && size[b] > 0 ? cache_tiles<DH>(len[b]) + node_tiles<DH>(size[b]) + a.over : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -245,12 +248,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     auto keys_of = [&](const Piece& p, int t) { return t < p.ntc ? p.cached - t * KEYS : p.keys - (t - p.ntc) * KEYS; };
     // the run's first piece that has tiles, and the one behind p; n = 0: none
     auto fit = [&](Piece& p) {
-        p.t0 = max(0, lo - p.start - OVER);
-        p.n = max(0, min(p.nt, hi - p.start - OVER) - p.t0);
+        p.t0 = max(0, lo - p.start - a.over);
+        p.n = max(0, min(p.nt, hi - p.start - a.over) - p.t0);
     };
     auto next_piece = [&](const Piece& c) -> Piece {
         Piece p = c;
-        p.start = c.start + c.nt + OVER;
+        p.start = c.start + c.nt + a.over;
         p.n = 0;
         if (p.start >= hi) return p;
         ++p.seg;
@@ -524,97 +527,117 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
 }
 
 // =========================================================================================
-// Combine. A CTA takes 512 / dh consecutive (node, head) rows of a sequence and K/V head, 128 threads for
-// them, four columns of one row each, and up to four such groups, which deal the row's partials among them.
+// Combine. 128 threads take 512 / dh (node, head) rows of a sequence and K/V head at a time, four columns of
+// one row each, and R such sets of rows at once, so that the loads of many small rows overlap (240 rows x 128
+// segments of two partials: 23 us with one set, 8 with four). Where rows have many partials, up to four
+// such groups of threads deal them among themselves.
 // =========================================================================================
 constexpr int GROUPS = 4;
-template <typename T, int DH> __global__ void __launch_bounds__(128 * GROUPS) tree_combine_kernel(TreeArgs a) {
-    constexpr int RW = 512 / DH, PB = 8;                 // rows; partials in flight
-    __shared__ float4 sum_o[GROUPS - 1][128];
-    __shared__ float2 sum_ml[GROUPS - 1][128];
+template <typename T, int DH, int R> __global__ void __launch_bounds__(128 * GROUPS) tree_combine_kernel(TreeArgs a) {
+    constexpr int RW = 512 / DH, PB = 8 / R;             // rows of a set; partials of a row in flight
+    __shared__ float4 sum_o[GROUPS - 1][R][128];
+    __shared__ float2 sum_ml[GROUPS - 1][R][128];
     const int tid = threadIdx.x & 127, part = threadIdx.x >> 7, parts = blockDim.x >> 7;
-    const int grp = a.H / a.G, b = blockIdx.z, g = blockIdx.y, c4 = tid / RW, r = blockIdx.x * RW + tid % RW;
+    const int grp = a.H / a.G, b = blockIdx.z, g = blockIdx.y, c4 = tid / RW, r0 = blockIdx.x * RW * R + tid % RW;
     // The partial kernel starts its dependents when all before it is done, so the lengths are there
     const int nodes = nodes_of(a, b, false);
     pdl_wait();
     pdl_trigger();
-    const bool row = r < a.T * grp, live = r < nodes * grp;
-    const int node = r / grp, h = g * grp + r - node * grp;
-    const int64_t m = (int64_t)b * a.T + node;
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 o) {
+    float M[R] = {}, L[R] = {};
+    float4 O[R] = {};
+    auto add = [&](int i, float2 ml, float4 o) {
         // an empty partial may leave its o unwritten (one of NaN scores, or void, has l = NaN)
         if (ml.x == -INFINITY && ml.y == 0.f) return;
-        if (ml.x > M) {
-            const float f = simt_exp<T>(M - ml.x);
-            L *= f;
-            O.x *= f; O.y *= f; O.z *= f; O.w *= f;
-            M = ml.x;
+        if (ml.x > M[i]) {
+            const float f = simt_exp<T>(M[i] - ml.x);
+            L[i] *= f;
+            O[i].x *= f; O[i].y *= f; O[i].z *= f; O[i].w *= f;
+            M[i] = ml.x;
         }
-        const float w = ml.x == M ? 1.f : simt_exp<T>(ml.x - M);
-        L = fmaf(ml.y, w, L);
-        O.x = fmaf(w, o.x, O.x);
-        O.y = fmaf(w, o.y, O.y);
-        O.z = fmaf(w, o.z, O.z);
-        O.w = fmaf(w, o.w, O.w);
+        const float w = ml.x == M[i] ? 1.f : simt_exp<T>(ml.x - M[i]);
+        L[i] = fmaf(ml.y, w, L[i]);
+        O[i].x = fmaf(w, o.x, O[i].x);
+        O[i].y = fmaf(w, o.y, O[i].y);
+        O[i].z = fmaf(w, o.z, O[i].z);
+        O[i].w = fmaf(w, o.w, O[i].w);
     };
-    if (live) {
-        const int tile = r / a.seg_rows, in = r - tile * a.seg_rows;
-        int64_t first;
-        int used;
-        if (a.tensor) {
-            // the runs that the segment's tiles meet
-            const int per_b = a.G * a.tiles, W = a.plan[0], before = a.plan[1 + b], cost = a.plan[2 + b] - before;
-            const int in_b = g * a.tiles + tile, at = per_b * before + in_b * cost + OVER, nt = cost - OVER;
-            first = (int64_t)(at / W) + (int64_t)b * per_b + in_b;
-            used = (at + nt - 1) / W - at / W + 1;
-        } else {
-            first = ((int64_t)b * a.G + g) * a.slots;
-            used = a.slots;
-        }
-        const float2* ml_at = a.pml + first * a.seg_rows + in;
-        const float* o_at = a.po + (first * DH + c4 * 4) * rows4(a.seg_rows) + in * 4;
-#pragma unroll 1
-        for (int s = part; s < used; s += PB * parts) {
-            float2 ml[PB];
-            float4 o[PB];
+    // The CTA's rows are of one row tile (where there are several, they have 256 rows, of which a CTA's are a part):
+    // its partials, from the runs that the segment's tiles meet
+    const int tile = a.tiles > 1 ? blockIdx.x * RW * R / a.seg_rows : 0;
+    int64_t first = ((int64_t)b * a.G + g) * a.slots;
+    int used = a.slots;
+    if (a.tensor) {
+        const int per_b = a.G * a.tiles, W = a.plan[0], before = a.plan[1 + b], cost = a.plan[2 + b] - before;
+        const int in_b = g * a.tiles + tile, at = per_b * before + in_b * cost + a.over, run = at / W;
+        first = run + (int64_t)b * per_b + in_b;
+        used = (at + cost - a.over - 1) / W - run + 1;
+    }
+    const int in = r0 - tile * a.seg_rows, ml_step = a.seg_rows, o_step = DH * rows4(a.seg_rows);
+    const float2* ml_at = a.pml + first * ml_step + in;
+    const float* o_at = a.po + first * o_step + c4 * 4 * rows4(a.seg_rows) + in * 4;
+    const int rows = nodes * grp;
 #pragma unroll
-            for (int j = 0; j < PB; ++j) {
-                const int64_t i = s + j * parts;
-                ml[j] = make_float2(-INFINITY, 0.f);
-                o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < used) {
-                    ml[j] = ml_at[i * a.seg_rows];
-                    o[j] = *reinterpret_cast<const float4*>(o_at + i * DH * rows4(a.seg_rows));
+    for (int i = 0; i < R; ++i) {
+        M[i] = -INFINITY;
+        L[i] = 0.f;
+        O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int s = part; s < used; s += PB * parts) {
+        float2 ml[R][PB];
+        float4 o[R][PB];
+#pragma unroll
+        for (int j = 0; j < PB; ++j) {
+            const int at = s + j * parts;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                ml[i][j] = make_float2(-INFINITY, 0.f);
+                o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at < used && r0 + i * RW < rows) {
+                    ml[i][j] = ml_at[(int64_t)at * ml_step + i * RW];
+                    o[i][j] = *reinterpret_cast<const float4*>(o_at + (int64_t)at * o_step + i * RW * 4);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < PB; ++j) add(ml[j], o[j]);
         }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < PB; ++j) add(i, ml[i][j], o[i][j]);
     }
     if (parts > 1) {
         if (part > 0) {
-            sum_o[part - 1][tid] = O;
-            sum_ml[part - 1][tid] = make_float2(M, L);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                sum_o[part - 1][i][tid] = O[i];
+                sum_ml[part - 1][i][tid] = make_float2(M[i], L[i]);
+            }
         }
         __syncthreads();
         if (part > 0) return;
-        for (int i = 0; i < parts - 1; ++i) add(sum_ml[i][tid], sum_o[i][tid]);
+        for (int p = 0; p < parts - 1; ++p)
+#pragma unroll
+            for (int i = 0; i < R; ++i) add(i, sum_ml[p][i][tid], sum_o[p][i][tid]);
     }
-    if (!row) return;
-    if (!live) {
-        if (a.lse && c4 == 0) a.lse[m * a.H + h] = -INFINITY;
-        if (!a.zero_rest) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = r0 + i * RW, node = r / grp, h = g * grp + r - node * grp;
+        if (r >= a.T * grp) break;
+        const int64_t m = (int64_t)b * a.T + node;
+        const bool live = node < nodes;
+        if (a.lse && c4 == 0) a.lse[m * a.H + h] = !live || L[i] == 0.f ? -INFINITY : M[i] + logf(L[i]);
+        if (!live && !a.zero_rest) continue;
+        // no key with any weight: zero output, lse -inf
+        const float inv = L[i] > 0.f ? 1.f / L[i] : (L[i] == 0.f ? 0.f : L[i]);
+        T* dst = (T*)a.o + m * a.o_ld + (int64_t)h * DH + c4 * 4;
+        const T w[4] = {from_f32<T>(O[i].x * inv), from_f32<T>(O[i].y * inv), from_f32<T>(O[i].z * inv), from_f32<T>(O[i].w * inv)};
+        if (a.o_vec) {
+            struct alignas(4 * sizeof(T)) Four { T x[4]; };
+            *reinterpret_cast<Four*>(dst) = {{w[0], w[1], w[2], w[3]}};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[j] = w[j];
+        }
     }
-    // no key with any weight: zero output, lse -inf
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    T* dst = (T*)a.o + m * a.o_ld + (int64_t)h * DH + c4 * 4;
-    dst[0] = from_f32<T>(O.x * inv);
-    dst[1] = from_f32<T>(O.y * inv);
-    dst[2] = from_f32<T>(O.z * inv);
-    dst[3] = from_f32<T>(O.w * inv);
-    if (live && a.lse && c4 == 0) a.lse[m * a.H + h] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
 // ---- host side ----------------------------------------------------------------------------------
@@ -653,11 +676,12 @@ bool tensor_ok(const evs_tree_attn_args& c) {
 bool plan_tensor(const evs_tree_attn_args& c, TreeArgs& a, int& grid) {
     const long long rows = (long long)c.nodes * (c.heads / c.kv_heads);
     a.pair = rows > 128;
+    a.over = over_tiles(a.pair, c.head_dim);
     a.seg_rows = (int)(rows < 256 ? rows : 256);
     a.tiles = (int)((rows + 255) / 256);
     const long long segs = (long long)c.batch * c.kv_heads * a.tiles, tiles =
         segs * (((long long)c.capacity + tile_keys(c.head_dim) - 1) / tile_keys(c.head_dim) + (c.nodes > tile_keys(c.head_dim) ? 2 : 1));
-    if (tiles + segs * OVER >= (1LL << 30)) return false;
+    if (tiles + segs * a.over >= (1LL << 30)) return false;
     grid = (int)(tiles < kAttnGrid ? tiles : kAttnGrid);
     a.tensor = 1;
     return true;
@@ -712,6 +736,11 @@ template <typename T, int DH> cudaError_t launch_simt(const evs_tree_attn_args& 
     return simt_rows(c) == 64 ? launch_rows<T, DH, 4>(c, a, stream) : launch_rows<T, DH, 1>(c, a, stream);
 }
 
+template <typename T, int DH> cudaError_t combine(const TreeArgs& a, int sets, dim3 grid, dim3 block, cudaStream_t stream) {
+    return sets == 4 ? launch_s(stream, tree_combine_kernel<T, DH, 4>, grid, block, 0, a)
+                     : launch_s(stream, tree_combine_kernel<T, DH, 1>, grid, block, 0, a);
+}
+
 cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
     TreeArgs a{};
     a.q = c.q; a.kc = c.k_cache; a.vc = c.v_cache; a.kn = c.k_nodes; a.vn = c.v_nodes; a.o = c.o; a.lse = c.lse;
@@ -722,6 +751,7 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
     a.zero_rest = c.zero_rest != 0;
     a.scale = c.scale != 0.f ? c.scale : 1.f / sqrtf((float)c.head_dim);
     a.q_vec = (uintptr_t)c.q % 16 == 0 && c.q_ld % 8 == 0;
+    a.o_vec = (uintptr_t)c.o % (c.dtype == EVS_DTYPE_BF16 ? 8 : 16) == 0 && c.o_ld % 4 == 0;
     const bool half = c.dtype == EVS_DTYPE_BF16;
     int grid = 0;
     const bool tensor = tensor_ok(c) && plan_tensor(c, a, grid);
@@ -738,24 +768,21 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
             default: e = half ? launch_simt<bf16, 16>(c, a, stream) : launch_simt<float, 16>(c, a, stream);
         }
     if (e != cudaSuccess) return e;
+    // sets of rows: four where one each would not run at once; groups: one for eight partials of a row, as many as do
     const int rw = 512 / c.head_dim, rows = c.nodes * (c.heads / c.kv_heads);
-    const dim3 cgrid((rows + rw - 1) / rw, c.kv_heads, c.batch);
-    // groups: one for eight partials of a row, as many as all run at once
-    const long long most = 4 * 152 / ((long long)cgrid.x * cgrid.y * cgrid.z);
+    const long long sets = (long long)((rows + rw - 1) / rw) * c.kv_heads * c.batch, room = 152 * 4;
+    const int sets_each = sets > 4 * room ? 4 : 1;
     long long per_row = a.slots;
-    if (tensor) {
-        const long long segs = (long long)c.batch * c.kv_heads * a.tiles;
-        per_row = grid * (a.pair ? 1 : 2) / segs + 2;
-    }
+    if (tensor) per_row = grid * (a.pair ? 1 : 2) / ((long long)c.batch * c.kv_heads * a.tiles) + 2;
     long long groups = (per_row + 7) / 8;
-    groups = groups < most ? groups : most;
+    groups = groups < room / sets ? groups : room / sets;
     groups = groups < 1 ? 1 : groups > GROUPS ? GROUPS : groups;
-    auto combine = [&](auto kernel) { return launch_s(stream, kernel, cgrid, dim3(128 * (unsigned)groups), 0, a); };
+    const dim3 cgrid((rows + rw * sets_each - 1) / (rw * sets_each), c.kv_heads, c.batch), cblock(128 * (unsigned)groups);
     switch (c.head_dim) {
-        case 128: return half ? combine(tree_combine_kernel<bf16, 128>) : combine(tree_combine_kernel<float, 128>);
-        case 64: return half ? combine(tree_combine_kernel<bf16, 64>) : combine(tree_combine_kernel<float, 64>);
-        case 32: return half ? combine(tree_combine_kernel<bf16, 32>) : combine(tree_combine_kernel<float, 32>);
-        default: return half ? combine(tree_combine_kernel<bf16, 16>) : combine(tree_combine_kernel<float, 16>);
+        case 128: return half ? combine<bf16, 128>(a, sets_each, cgrid, cblock, stream) : combine<float, 128>(a, sets_each, cgrid, cblock, stream);
+        case 64: return half ? combine<bf16, 64>(a, sets_each, cgrid, cblock, stream) : combine<float, 64>(a, sets_each, cgrid, cblock, stream);
+        case 32: return half ? combine<bf16, 32>(a, sets_each, cgrid, cblock, stream) : combine<float, 32>(a, sets_each, cgrid, cblock, stream);
+        default: return half ? combine<bf16, 16>(a, sets_each, cgrid, cblock, stream) : combine<float, 16>(a, sets_each, cgrid, cblock, stream);
     }
 }
 
