@@ -66,46 +66,45 @@ __device__ __forceinline__ void rest_rows(const PromptArgs& a, int s0, int s1, i
     }
 }
 
+// Shared memory of the tensor-core kernel: exchange [2][128] floats, barriers, then st [B + 1], order [B] and of [B]
+// (sequences by length, longest first: which, and their items of 256 rows), then Q and the ring on 1024 bytes.
+constexpr int BARRIERS = 320;
+constexpr int small_smem(int B) { return 1024 + BARRIERS + (3 * B + 1) * 4; }
+
 // The CTA's items. Level v holds the items of v x 256 rows and their keys: one for each head of each
-// sequence that is as long (order: sequences by length, longest first).
+// sequence that is as long.
 struct Items {
-    const int *st, *order;
-    int B, H, grid, round, base, level, count;
+    const PromptArgs& a;
+    int round, base, level, count;
     int first, len, head, tile;          // the item: its sequence's first row and length, its head and 256 rows
 
-    __device__ __forceinline__ int tiles(int i) const {
-        const int s = order[i];
-        return (st[s + 1] - st[s] + 255) >> 8;
+    static __device__ __forceinline__ int* starts() {
+        extern __shared__ uint8_t smem_raw[];
+        return reinterpret_cast<int*>(smem_raw + 1024 + BARRIERS);
     }
-    __device__ __forceinline__ void init(const int* s, const int* ord, int b, int h) {
-        st = s;
-        order = ord;
-        B = b;
-        H = h;
-        grid = gridDim.x;
-        round = 0;
-        base = 0;
-        level = b > 0 ? tiles(0) : 0;
-        count = 0;
+    static __device__ __forceinline__ int* order(const PromptArgs& a) { return starts() + a.B + 1; }
+    static __device__ __forceinline__ int* of(const PromptArgs& a) { return starts() + 2 * a.B + 1; }
+
+    __device__ __forceinline__ Items(const PromptArgs& args) : a(args), round(0), base(0), count(0) {
+        level = of(a)[0];
         widen();
     }
     __device__ __forceinline__ void widen() {
-        while (count < B && tiles(count) >= level) ++count;
+        while (count < a.B && of(a)[count] >= level) ++count;
     }
     __device__ __forceinline__ bool next() {
-        const int at = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        const int grid = gridDim.x, at = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
         ++round;
-        while (level > 0 && at >= base + count * H) {
-            base += count * H;
+        while (level > 0 && at >= base + count * a.H) {
+            base += count * a.H;
             --level;
             widen();
         }
         if (level <= 0) return false;
-        const int in = at - base, i = in / H;
-        const int s = order[i];
-        first = st[s];
-        len = st[s + 1] - first;
-        head = in - i * H;
+        const int in = at - base, i = in / a.H, s = order(a)[i];
+        first = starts()[s];
+        len = starts()[s + 1] - first;
+        head = in - i * a.H;
         tile = level - 1;
         return true;
     }
@@ -117,8 +116,6 @@ struct Items {
     template <int K> __device__ __forceinline__ int key_tiles() const { return (keys(1) + K - 1) / K; }
 };
 
-constexpr int BARRIERS = 320;
-constexpr int small_smem(int B) { return 1024 + BARRIERS + (2 * B + 1) * 4; }
 constexpr int prompt_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
 static_assert(prompt_smem(64, 1024) <= 227 * 1024 && prompt_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
@@ -140,8 +137,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
     uint64_t* drain = q_free + 2;                                          // [4]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 4);
-    int* st = reinterpret_cast<int*>(smem_raw + 1024 + BARRIERS);          // [B + 1]
-    int* order = st + a.B + 1;                                             // [B]
+    int* st = Items::starts();
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;
     static_assert((2 * NST + 20) * 8 + 4 <= BARRIERS, "barriers");
@@ -184,14 +180,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const int m = (st[o + 1] - st[o] + 255) >> 8;
             before += m > n || (m == n && o < s);
         }
-        order[before] = s;
+        Items::order(a)[before] = s;
+        Items::of(a)[before] = n;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Items it;
-    it.init(st, order, a.B, a.H);
+    Items it(a);
 
     if (warp >= SOFT_WARPS) {
         asm volatile(EVS_ATTN_AUX_REGS);
@@ -327,8 +323,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     auto before = [&]() {
         if (cnt > 0) wait(&pv_done[2 * L + ((cnt - 1) & 1u)], (cnt - 1) >> 1 & 1u);
     };
-    while (it.next()) {
-        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), row0 = it.row0(L);
+    bool more = it.next();
+    while (more) {
+        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), row0 = it.row0(L), head = it.head;
+        const int row_at = it.first + row0;
         const bool work = (th.row & ~31) < rows;         // of this warp
         th.begin();
         for (int t = 0; t < n; ++t) {
@@ -347,16 +345,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             arrive(&p_full[2 * L + (cnt & 1u)]);
             ++cnt;
         }
+        // what needs nothing of the last product, while that runs
+        float l = 0.f;
+        if (rows > 0 && work) l = th.exchange(th.l, [](float x, float y) { return x + y; });
+        more = it.next();
         if (rows <= 0) continue;
         before();
         if (work) {
-            const float l = th.exchange(th.l, [](float x, float y) { return x + y; });
             tc_fence_after();
             const bool live = th.row < rows;
-            const int64_t row = it.first + row0 + th.row;
+            const int64_t row = row_at + th.row;
             // no key with any weight: zero output, lse -inf; a void row: NaN
             const float inv = ok ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : __int_as_float(0x7fc00000);
-            bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)it.head * DH + th.half * (DH / 2);
+            bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)head * DH + th.half * (DH / 2);
 #pragma unroll
             for (int c = 0; c < DH / 32; ++c) {
                 uint32_t o[16], w[8];
@@ -374,7 +375,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 }
             }
             if (live && th.half == 0 && a.lse)
-                a.lse[row * a.H + it.head] = !ok ? inv : l == 0.f ? -INFINITY : th.m * LN2 + logf(l);
+                a.lse[row * a.H + head] = !ok ? inv : l == 0.f ? -INFINITY : th.m * LN2 + logf(l);
             tc_fence_before();                           // these reads precede the next item's products
         }
         __syncwarp();

@@ -529,15 +529,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
 // =========================================================================================
 // Combine. 128 threads take 512 / dh (node, head) rows of a sequence and K/V head at a time, four columns of
 // one row each, and R such sets of rows at once, so that the loads of many small rows overlap (240 rows x 128
-// segments of two partials: 23 us with one set, 8 with four). Where rows have many partials, up to four
-// such groups of threads deal them among themselves.
+// segments of two or three partials: 18 us with one set, 10 with two, 12 with four). Where rows have many partials
+// (and a CTA one set), up to four such groups of threads deal them among themselves.
 // =========================================================================================
 constexpr int GROUPS = 4;
-template <typename T, int DH, int R> __global__ void __launch_bounds__(128 * GROUPS) tree_combine_kernel(TreeArgs a) {
-    constexpr int RW = 512 / DH, PB = 8 / R;             // rows of a set; partials of a row in flight
-    __shared__ float4 sum_o[GROUPS - 1][R][128];
-    __shared__ float2 sum_ml[GROUPS - 1][R][128];
-    const int tid = threadIdx.x & 127, part = threadIdx.x >> 7, parts = blockDim.x >> 7;
+template <typename T, int DH, int R> __global__ void __launch_bounds__(R == 1 ? 128 * GROUPS : 128) tree_combine_kernel(TreeArgs a) {
+    constexpr int RW = 512 / DH, PB = R == 1 ? 8 : 2;    // rows of a set; partials of a row in flight
+    const int tid = threadIdx.x & 127, part = R == 1 ? threadIdx.x >> 7 : 0, parts = R == 1 ? blockDim.x >> 7 : 1;
     const int grp = a.H / a.G, b = blockIdx.z, g = blockIdx.y, c4 = tid / RW, r0 = blockIdx.x * RW * R + tid % RW;
     // The partial kernel starts its dependents when all before it is done, so the lengths are there
     const int nodes = nodes_of(a, b, false);
@@ -604,19 +602,18 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(128 * GRO
 #pragma unroll
             for (int j = 0; j < PB; ++j) add(i, ml[i][j], o[i][j]);
     }
-    if (parts > 1) {
-        if (part > 0) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                sum_o[part - 1][i][tid] = O[i];
-                sum_ml[part - 1][i][tid] = make_float2(M[i], L[i]);
+    if constexpr (R == 1) {
+        __shared__ float4 sum_o[GROUPS - 1][128];
+        __shared__ float2 sum_ml[GROUPS - 1][128];
+        if (parts > 1) {
+            if (part > 0) {
+                sum_o[part - 1][tid] = O[0];
+                sum_ml[part - 1][tid] = make_float2(M[0], L[0]);
             }
+            __syncthreads();
+            if (part > 0) return;
+            for (int p = 0; p < parts - 1; ++p) add(0, sum_ml[p][tid], sum_o[p][tid]);
         }
-        __syncthreads();
-        if (part > 0) return;
-        for (int p = 0; p < parts - 1; ++p)
-#pragma unroll
-            for (int i = 0; i < R; ++i) add(i, sum_ml[p][i][tid], sum_o[p][i][tid]);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -737,7 +734,7 @@ template <typename T, int DH> cudaError_t launch_simt(const evs_tree_attn_args& 
 }
 
 template <typename T, int DH> cudaError_t combine(const TreeArgs& a, int sets, dim3 grid, dim3 block, cudaStream_t stream) {
-    return sets == 4 ? launch_s(stream, tree_combine_kernel<T, DH, 4>, grid, block, 0, a)
+    return sets == 2 ? launch_s(stream, tree_combine_kernel<T, DH, 2>, grid, block, 0, a)
                      : launch_s(stream, tree_combine_kernel<T, DH, 1>, grid, block, 0, a);
 }
 
@@ -768,10 +765,10 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
             default: e = half ? launch_simt<bf16, 16>(c, a, stream) : launch_simt<float, 16>(c, a, stream);
         }
     if (e != cudaSuccess) return e;
-    // sets of rows: four where one each would not run at once; groups: one for eight partials of a row, as many as do
+    // sets of rows: two where one each would not run at once; groups: one for eight partials of a row, as many as do
     const int rw = 512 / c.head_dim, rows = c.nodes * (c.heads / c.kv_heads);
     const long long sets = (long long)((rows + rw - 1) / rw) * c.kv_heads * c.batch, room = 152 * 4;
-    const int sets_each = sets > 4 * room ? 4 : 1;
+    const int sets_each = sets > 4 * room ? 2 : 1;
     long long per_row = a.slots;
     if (tensor) per_row = grid * (a.pair ? 1 : 2) / ((long long)c.batch * c.kv_heads * a.tiles) + 2;
     long long groups = (per_row + 7) / 8;
