@@ -8,11 +8,15 @@
 // w = sum e^y (l - m), rescaled when m grows; a row's threads (and the CTAs of a cluster, where there are
 // too few rows for the GPU) join theirs at the end.
 //
-// The largest K tokens, in the order (logit descending, id ascending), come from the same pass: a thread
-// remembers where it met its maximum. A token among the row's K largest can only be one of a thread whose
-// own largest is among the K largest of all threads', so just those K threads' tokens are read a second
-// time (K / 256 of the row, from L2) and merged by warps that hold sorted lists in registers. No list can
-// overflow, whatever the logits are, and no order of execution shows in the result.
+// The largest K tokens, in the order (logit descending, id ascending): K threads' own maxima reach a border
+// that the K-th largest token reaches, too, and a token that does is one of a thread whose maximum does. So
+// only those threads' tokens (K / 256 of the row, from L2) are read a second time, and the few that reach the
+// border (its leading bits, found by counting) are ranked by one warp in registers. Where more than 256 do,
+// as among equal logits, every warp keeps a sorted list and the lists are joined. No order of execution shows.
+//
+// Measured (replayed graphs): 13 x 512 fp32 2.6 us, 208 x 4096 with eight alternatives 7.6, 64 x 50021 bf16 with
+// 20 11.6, 512 x 131072 fp32 with five 58 (4.6 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
+// place on an SM a fifth of it, start and ranking about 10).
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -24,10 +28,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 typedef unsigned long long u64;
 
-constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
 constexpr int LP_MAX_CS = 8;             // portable cluster size
 constexpr int LP_MAX_TOP = 64;
 constexpr uint32_t FULL = 0xffffffffu;
+constexpr int LP_FOUND = 256;            // tokens that one warp ranks
+constexpr int LP_BORDER_BIT = 14;        // the border's sign, exponent and nine bits of its mantissa
 
 struct LogprobArgs {
     const void* logits;
@@ -40,18 +45,21 @@ struct LogprobArgs {
     uint32_t* flags;
 };
 
-// Position in the order: larger is earlier, 0 is no token. The logit's bits mapped to an ascending
-// integer, then the id descending.
-__device__ __forceinline__ u64 lp_key(float l, int id) {
-    if (!(l > -INFINITY)) return 0;                    // NaN and -inf: ruled out
-    uint32_t k = __float_as_uint(l + 0.f);             // -0 and +0 are one value
-    k = (k & 0x80000000u) ? ~k : (k | 0x80000000u);
-    return ((u64)k << 32) | (u64)(0xffffffffu - (uint32_t)id);
+// A logit's bits as an ascending integer; NaN and -inf, which are ruled out, are the lowest.
+constexpr uint32_t LP_RULED_OUT = 0x007fffffu;         // of -inf
+__device__ __forceinline__ uint32_t lp_order(float l) {
+    const uint32_t k = __float_as_uint(fmaxf(l, -INFINITY) + 0.f);   // NaN: -inf; -0 and +0 are one value
+    return (k & 0x80000000u) ? ~k : (k | 0x80000000u);
 }
-__device__ __forceinline__ float lp_value(u64 key) {
-    const uint32_t k = (uint32_t)(key >> 32);
+__device__ __forceinline__ float lp_of_order(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+// Position in the order: larger is earlier, 0 is no token.
+__device__ __forceinline__ u64 lp_key(float l, int id) {
+    const uint32_t k = lp_order(l);
+    return k <= LP_RULED_OUT ? 0 : ((u64)k << 32) | (u64)(0xffffffffu - (uint32_t)id);
+}
+__device__ __forceinline__ float lp_value(u64 key) { return lp_of_order((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int lp_id(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
 
 __device__ __forceinline__ u64 lp_max(u64 a, u64 b) { return a > b ? a : b; }
@@ -96,14 +104,16 @@ template <int L> struct WarpTop {
         }
         a[0] = b;
     }
+    // The smallest of them
+    __device__ __forceinline__ u64 last() const { return __shfl_sync(FULL, a[L - 1], 31); }
     __device__ __forceinline__ void push(u64 b, int lane) { push_sorted(lp_sort32(b, lane), lane); }
 };
 
-// All warps' lists into warp 0's, by halves; lists: [LP_WARPS / 2][32 L]. Ends with a barrier only
+// All warps' lists into warp 0's, by halves; lists: [WARPS / 2][32 L]. Ends with a barrier only
 // between its steps: callers synchronise before lists is used again.
-template <int L> __device__ __forceinline__ void join_warps(WarpTop<L>& top, u64* lists, int warp, int lane) {
+template <int L, int WARPS> __device__ __forceinline__ void join_warps(WarpTop<L>& top, u64* lists, int warp, int lane) {
 #pragma unroll 1
-    for (int half = LP_WARPS / 2; half > 0; half >>= 1) {
+    for (int half = WARPS / 2; half > 0; half >>= 1) {
         __syncthreads();
         if (warp >= half && warp < 2 * half) {
 #pragma unroll
@@ -123,26 +133,32 @@ template <typename T> struct Row {
     static constexpr int E = 16 / (int)sizeof(T);
     const T* base;                       // id 0
     int off, V;
-    __device__ __forceinline__ void load(int v, float (&x)[E]) const {
+    // vector v as it lies in memory
+    __device__ __forceinline__ uint4 raw(int v) const {
         const int id0 = v * E - off;
-        if (id0 >= 0 && id0 + E <= V) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(base + id0));
+        if (id0 >= 0 && id0 + E <= V) return __ldg(reinterpret_cast<const uint4*>(base + id0));
+        alignas(16) T x[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] = (id0 + j >= 0 && id0 + j < V) ? base[id0 + j] : from_f32<T>(-INFINITY);
+        return *reinterpret_cast<const uint4*>(x);
+    }
+    static __device__ __forceinline__ uint4 nothing() {
+        const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+        return make_uint4(w, w, w, w);
+    }
+    static __device__ __forceinline__ void values(const uint4& u, float (&x)[E]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             if constexpr (sizeof(T) == 4) {
-                x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-                x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+                x[j] = __uint_as_float(w[j]);
             } else {
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(w[j] << 16);
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                }
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < E; ++j) x[j] = (id0 + j >= 0 && id0 + j < V) ? to_f32(base[id0 + j]) : -INFINITY;
         }
     }
+    __device__ __forceinline__ void load(int v, float (&x)[E]) const { values(raw(v), x); }
 };
 
 // (m, s, w) of two disjoint parts of a row; c: log2(e) / T in two parts
@@ -162,14 +178,16 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float2 c) {
     return r;
 }
 
-template <typename T, int L>
+template <typename T, int L, int LP_THREADS>
 __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
-    constexpr int E = Row<T>::E, U = 4, LL = L ? L : 1;
+    constexpr int E = Row<T>::E, U = 4, LL = L ? L : 1, LP_WARPS = LP_THREADS / 32;
     __shared__ u64 lists[LP_WARPS / 2 * 32 * LL];
     __shared__ u64 parts[LP_MAX_CS * 32 * LL];           // of the cluster's CTAs, in its first
     __shared__ Stat part_stat[LP_MAX_CS];
-    __shared__ Stat warp_stat[LP_WARPS];
-    __shared__ u64 winners[32 * LL];
+    __shared__ uint32_t warp_keys[LP_WARPS], thread_keys[LP_THREADS], border_key;
+    __shared__ float2 warp_sums[LP_WARPS];
+    __shared__ u64 found[LP_FOUND];
+    __shared__ int n_found;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -199,23 +217,26 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
 
     // ---- the pass
     float m = -INFINITY, s = 0.f, w = 0.f;
-    int where = -1;                                      // first vector of the chunk that holds m
+    // U vectors at a time, the next ones on their way while these are worked on
+    uint4 ahead[U];
+    auto fetch = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) ahead[u] = v0 + u * LP_THREADS < hi ? row.raw(v0 + u * LP_THREADS) : Row<T>::nothing();
+    };
+    fetch(lo + tid);
     for (int v0 = lo + tid; v0 < hi; v0 += U * LP_THREADS) {
-        float x[U][E];
+        uint4 now[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (v0 + u * LP_THREADS < hi) {
-                row.load(v0 + u * LP_THREADS, x[u]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) x[u][j] = -INFINITY;
-            }
-        }
+        for (int u = 0; u < U; ++u) now[u] = ahead[u];
+        if (v0 + U * LP_THREADS < hi) fetch(v0 + U * LP_THREADS);
         float cm = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            float x[E];
+            Row<T>::values(now[u], x);
 #pragma unroll
-            for (int j = 0; j < E; ++j) cm = fmaxf(cm, x[u][j]);
+            for (int j = 0; j < E; ++j) cm = fmaxf(cm, x[j]);
+        }
         if (cm > m) {
             if (m > -INFINITY) {
                 const float d = fmaxf(m - cm, -FLT_MAX), f = lp_exp(d, c);
@@ -223,33 +244,42 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
                 s *= f;
             }
             m = cm;
-            where = v0;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            float x[E];
+            Row<T>::values(now[u], x);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 // -inf, NaN and what +inf leaves behind: no weight, and no NaN in w
-                const float d = fmaxf(x[u][j] - m, -FLT_MAX), e = lp_exp(d, c);
+                const float d = fmaxf(x[j] - m, -FLT_MAX), e = lp_exp(d, c);
                 s += e;
                 w = fmaf(e, d, w);
             }
+        }
     }
-    // ---- the row's statistics
-    Stat st = {m, s, w};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stat b;
-        b.m = __shfl_xor_sync(FULL, st.m, o);
-        b.s = __shfl_xor_sync(FULL, st.s, o);
-        b.w = __shfl_xor_sync(FULL, st.w, o);
-        st = (lane & o) ? join(b, st, c) : join(st, b, c);   // the same operands in the same order on both
-    }
-    if (lane == 0) warp_stat[warp] = st;
+    // ---- the row's statistics: the maximum of all, then every thread's sums moved to it once
+    uint32_t key = lp_order(m);
+    const uint32_t warp_key = __reduce_max_sync(FULL, key);
+    if (lane == 0) warp_keys[warp] = warp_key;
     __syncthreads();
-    st = warp_stat[0];
+    uint32_t top_key = warp_keys[0];
 #pragma unroll
-    for (int i = 1; i < LP_WARPS; ++i) st = join(st, warp_stat[i], c);
+    for (int i = 1; i < LP_WARPS; ++i) top_key = max(top_key, warp_keys[i]);
+    Stat st;
+    st.m = lp_of_order(top_key);
+    {
+        const Stat mine = join(Stat{m, s, w}, Stat{st.m, 0.f, 0.f}, c);
+        const float ws = warp_sum(mine.s), ww = warp_sum(mine.w);
+        if (lane == 0) warp_sums[warp] = make_float2(ws, ww);
+    }
+    __syncthreads();
+    st.s = st.w = 0.f;
+#pragma unroll
+    for (int i = 0; i < LP_WARPS; ++i) {
+        st.s += warp_sums[i].x;
+        st.w += warp_sums[i].y;
+    }
     if (st.m == INFINITY) {                              // the +inf tokens share the mass: count them
         float mine = 0.f;
         for (int v = lo + tid; v < hi; v += LP_THREADS) {
@@ -260,11 +290,10 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
         }
         mine = warp_sum(mine);
         __syncthreads();
-        if (lane == 0) warp_stat[warp].s = mine;
+        if (lane == 0) warp_sums[warp].x = mine;
         __syncthreads();
-        st.s = 0.f;
-        st.w = 0.f;
-        for (int i = 0; i < LP_WARPS; ++i) st.s += warp_stat[i].s;
+        st.s = st.w = 0.f;
+        for (int i = 0; i < LP_WARPS; ++i) st.s += warp_sums[i].x;
     }
 
     // ---- the largest tokens
@@ -273,54 +302,60 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
     const bool keys = L > 0 || greedy;
     const int K = L > 0 ? a.K : 1;                       // greedy: the argmax
     if (keys) {
-        u64 mine = 0;
-        if (where >= 0) {
-            // the chunk's first token that is m (a later chunk of this thread has only larger ids)
-#pragma unroll 1
-            for (int u = 0; u < U && mine == 0 && where + u * LP_THREADS < hi; ++u) {
-                float x[E];
-                const int v = where + u * LP_THREADS;
-                row.load(v, x);
-#pragma unroll
-                for (int j = E - 1; j >= 0; --j)
-                    if (x[j] == m) mine = lp_key(x[j], v * E - row.off + j);
-            }
-        }
-        top.push(mine, lane);
-        join_warps<LL>(top, lists, warp, lane);
+        thread_keys[tid] = key;
+        if (tid == 0) n_found = 0;
+        __syncthreads();
         if (warp == 0) {
+            // a border that at least K threads' largest reach (if as many have any): its first bits, which is enough
+            uint32_t mine[LP_WARPS], border = 0;
 #pragma unroll
-            for (int j = 0; j < LL; ++j) winners[j * 32 + lane] = top.a[j];
+            for (int i = 0; i < LP_WARPS; ++i) mine[i] = thread_keys[i * 32 + lane];
+#pragma unroll 1
+            for (uint32_t bit = 1u << 31; bit >= 1u << LP_BORDER_BIT; bit >>= 1) {
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < LP_WARPS; ++i) n += mine[i] >= (border | bit) ? 1 : 0;
+                if (__reduce_add_sync(FULL, n) >= K) border |= bit;
+            }
+            if (lane == 0) border_key = max(border, LP_RULED_OUT + 1);
         }
         __syncthreads();
-        if (L > 0) {
-            // all tokens of the winners' threads that are not behind the K-th winner
-            const u64 border = winners[K - 1];
-            top.clear();
-            for (int k = warp; k < K; k += LP_WARPS) {
-                const u64 win = winners[k];
-                if (win == 0) break;
-                const int v = (lp_id(win) + row.off) / E, first = lo + (v - lo) % LP_THREADS;   // its thread's first
-                const int count = (hi - first + LP_THREADS - 1) / LP_THREADS;
+        const uint32_t border = border_key;
+        // the tokens of the threads that reach it: a warp reads each such thread's vectors again
+        auto each = [&](auto use) {
+            for (uint32_t who = __ballot_sync(FULL, key >= border); who; who &= who - 1) {
+                const int first = lo + warp * 32 + __ffs(who) - 1, count = (hi - first + LP_THREADS - 1) / LP_THREADS;
 #pragma unroll 1
                 for (int i0 = 0; i0 < count; i0 += 32) {
-                    const int i = i0 + lane, vv = first + i * LP_THREADS;
+                    const int i = i0 + lane, v = first + i * LP_THREADS;
                     float x[E];
                     if (i < count) {
-                        row.load(vv, x);
+                        row.load(v, x);
                     } else {
 #pragma unroll
                         for (int j = 0; j < E; ++j) x[j] = -INFINITY;
                     }
 #pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        u64 key = lp_key(x[j], vv * E - row.off + j);
-                        if (key < border) key = 0;
-                        if (__any_sync(FULL, key != 0)) top.push(key, lane);
-                    }
+                    for (int j = 0; j < E; ++j) use(x[j], v * E - row.off + j);
                 }
             }
-            join_warps<LL>(top, lists, warp, lane);
+        };
+        each([&](float x, int id) {
+            if (lp_order(x) < border) return;
+            const int at = atomicAdd(&n_found, 1);
+            if (at < LP_FOUND) found[at] = lp_key(x, id);
+        });
+        __syncthreads();
+        if (n_found <= LP_FOUND) {
+            if (warp == 0)
+                for (int i = 0; i < n_found; i += 32) top.push(i + lane < n_found ? found[i + lane] : 0, lane);
+        } else {
+            // many equal or nearly equal tokens: every warp keeps a list, and they are joined
+            each([&](float x, int id) {
+                const u64 k = lp_order(x) < border ? 0 : lp_key(x, id);
+                if (__any_sync(FULL, k > top.last())) top.push(k, lane);
+            });
+            join_warps<LL, LP_WARPS>(top, lists, warp, lane);
         }
     }
 
@@ -361,9 +396,9 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
         if (l == st.m) return -log_z;                    // also +inf
         return st.m == INFINITY ? -INFINITY : (l - st.m) / t - log_z;
     };
-    if (greedy && warp == 0 && lane == 0) winners[0] = top.a[0];
+    if (greedy && tid == 0) found[0] = top.a[0];
     __syncthreads();
-    const int best = greedy ? lp_id(winners[0]) : 0;     // -1 of an empty row is no token's id
+    const int best = greedy ? lp_id(found[0]) : 0;       // -1 of an empty row is no token's id
     if (tid == 0) {
         if (a.entropy) a.entropy[r] = greedy || empty ? 0.f : st.m == INFINITY ? log_z : fmaxf(log_z - st.w / st.s / t, 0.f);
         if (empty && a.flags) atomicOr(a.flags, (uint32_t)EVS_FLAG_EMPTY_ROW);
@@ -393,10 +428,10 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
     }
 }
 
-template <typename T, int L> cudaError_t launch(const evs_logprob_args& c, const LogprobArgs& a, int cs, cudaStream_t stream) {
+template <typename T, int L, int NT> cudaError_t launch_as(const evs_logprob_args& c, const LogprobArgs& a, int cs, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.rows * cs);
-    cfg.blockDim = dim3(LP_THREADS);
+    cfg.blockDim = dim3(NT);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -406,7 +441,11 @@ template <typename T, int L> cudaError_t launch(const evs_logprob_args& c, const
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, L>, a);
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, L, NT>, a);
+}
+template <typename T, int L>
+cudaError_t launch(const evs_logprob_args& c, const LogprobArgs& a, int nt, int cs, cudaStream_t stream) {
+    return nt == 128 ? launch_as<T, L, 128>(c, a, cs, stream) : launch_as<T, L, 256>(c, a, cs, stream);
 }
 
 }  // namespace
@@ -426,15 +465,21 @@ extern "C" evs_status evs_token_logprobs(const evs_logprob_args* c, void* stream
     if (c->n_tokens == 0 && c->top == 0 && !c->entropy) return EVS_ERR_INVALID_ARG;
     LogprobArgs a{c->logits, c->ld, c->vocab, c->n_tokens, c->top, c->temperature, c->tokens, c->logprob, c->entropy,
                   c->top_logprob, c->top_token, c->flags};
-    // CTAs of a row: more while the rows leave SMs without any and a CTA's share of the row is some passes long
+    // CTAs of a row: two, four or eight where the rows leave SMs without any and a CTA's share stays some passes long,
+    // or where rows of the largest vocabularies would make an uneven wave (64 x 50021 bf16: 11.6 us with two, 12.4
+    // with one, 14 with four; 256 x 131072: 33 with two, 39 with one). A CTA has 128 threads for a short share, whose
+    // time is the ranking's steps (4096 x 4096: 29 us, 256 threads 52), and 256 for a long one (512 x 131072: 58, 67).
+    const long long rows = c->rows;
     int cs = 1;
-    while (cs < LP_MAX_CS && (long long)c->rows * cs < 304 && c->vocab / (cs * 2) >= 4096) cs *= 2;
+    while (cs < LP_MAX_CS && ((2 * rows * cs <= 152 && c->vocab / (2 * cs) >= 8192) || (rows * cs < 304 && c->vocab / (2 * cs) >= 65536)))
+        cs *= 2;
+    const int nt = c->vocab / cs <= 8192 ? 128 : 256;
     const int lists = c->top == 0 ? 0 : c->top <= 32 ? 1 : 2;
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (c->dtype == EVS_DTYPE_F32)
-        e = lists == 0 ? launch<float, 0>(*c, a, cs, s) : lists == 1 ? launch<float, 1>(*c, a, cs, s) : launch<float, 2>(*c, a, cs, s);
+        e = lists == 0 ? launch<float, 0>(*c, a, nt, cs, s) : lists == 1 ? launch<float, 1>(*c, a, nt, cs, s) : launch<float, 2>(*c, a, nt, cs, s);
     else
-        e = lists == 0 ? launch<bf16, 0>(*c, a, cs, s) : lists == 1 ? launch<bf16, 1>(*c, a, cs, s) : launch<bf16, 2>(*c, a, cs, s);
+        e = lists == 0 ? launch<bf16, 0>(*c, a, nt, cs, s) : lists == 1 ? launch<bf16, 1>(*c, a, nt, cs, s) : launch<bf16, 2>(*c, a, nt, cs, s);
     return status_of(e);
 }
