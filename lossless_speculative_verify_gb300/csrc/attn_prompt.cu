@@ -23,6 +23,15 @@ struct PromptArgs {
     int64_t q_row, q_head, kv_row, kv_head, o_row;
     int N, B, H, G, zero_rest, o_vec;
     float scale;
+    // Items in runs (below): of worker w slot 2 w + 1 is for an item that begins in its run, 2 w for one that began
+    // before. o four columns at a time, [slot][dh / 4][256][4]; (m, l) in natural units. jobs[w]: the item that w's
+    // run begins within.
+    float* po;
+    float2* pml;
+    struct Job* jobs;
+};
+struct Job {
+    int valid, first, len, head, tile, start, run, pad;
 };
 
 // Row where sequence b starts, in ascending order within [0, N] whatever starts holds; st: [B + 1] in
@@ -67,21 +76,34 @@ __device__ __forceinline__ void rest_rows(const PromptArgs& a, int s0, int s1, i
 }
 
 // Shared memory of the tensor-core kernel: exchange [2][128] floats, barriers, then st [B + 1], order [B] and of [B]
-// (sequences by length, longest first: which, and their items of 256 rows), then Q and the ring on 1024 bytes.
+// (sequences by length, longest first: which, and their items of 256 rows; or with runs where each begins on the
+// axis), then Q and the ring on 1024 bytes.
 constexpr int BARRIERS = 320;
-constexpr int small_smem(int B) { return 1024 + BARRIERS + (3 * B + 1) * 4; }
+constexpr int small_smem(int B) { return 1024 + BARRIERS + (3 * B + 3) * 4; }
 
-// The CTA's items. Level v holds the items of v x 256 rows and their keys: one for each head of each
-// sequence that is as long.
-struct Items {
-    const PromptArgs& a;
-    int round, base, level, count;
-    int first, len, head, tile;          // the item: its sequence's first row and length, its head and 256 rows
+// The item a CTA is at: its sequence's first row and length, its head and 256 rows.
+struct Item {
+    int first, len, head, tile;
 
     static __device__ __forceinline__ int* starts() {
         extern __shared__ uint8_t smem_raw[];
         return reinterpret_cast<int*>(smem_raw + 1024 + BARRIERS);
     }
+    // of lane L: its first row, rows, keys, tiles of K keys; of the item: tiles
+    __device__ __forceinline__ int row0(int L) const { return tile * 256 + L * 128; }
+    __device__ __forceinline__ int rows(int L) const { return min(128, len - row0(L)); }
+    __device__ __forceinline__ int keys(int L) const { return min(len, row0(L) + 128); }
+    template <int K> __device__ __forceinline__ int lane_tiles(int L) const { return rows(L) > 0 ? (keys(L) + K - 1) / K : 0; }
+    template <int K> __device__ __forceinline__ int item_tiles() const { return (keys(1) + K - 1) / K; }
+};
+
+// Whole items. Level v holds the items of v x 256 rows and their keys: one for each head of each
+// sequence that is as long.
+struct Items : Item {
+    static constexpr bool RUNS = false;
+    const PromptArgs& a;
+    int round, base, level, count;
+
     static __device__ __forceinline__ int* order(const PromptArgs& a) { return starts() + a.B + 1; }
     static __device__ __forceinline__ int* of(const PromptArgs& a) { return starts() + 2 * a.B + 1; }
 
@@ -108,18 +130,118 @@ struct Items {
         tile = level - 1;
         return true;
     }
-    // of lane L: its first row, rows, keys, tiles of K keys; of the item: tiles
-    __device__ __forceinline__ int row0(int L) const { return tile * 256 + L * 128; }
-    __device__ __forceinline__ int rows(int L) const { return min(128, len - row0(L)); }
-    __device__ __forceinline__ int keys(int L) const { return min(len, row0(L) + 128); }
-    template <int K> __device__ __forceinline__ int key_tiles(int L) const { return rows(L) > 0 ? (keys(L) + K - 1) / K : 0; }
-    template <int K> __device__ __forceinline__ int key_tiles() const { return (keys(1) + K - 1) / K; }
+    template <int K> __device__ __forceinline__ int t_lo() const { return 0; }
+    template <int K> __device__ __forceinline__ int tiles() const { return item_tiles<K>(); }
+    template <int K> __device__ __forceinline__ int tiles(int L) const { return lane_tiles<K>(L); }
+    // fills what the kernel's start gives: sequences by length
+    static __device__ __forceinline__ void prepare(const PromptArgs& a) {
+        const int* st = starts();
+        for (int s = threadIdx.x; s < a.B; s += THREADS) {
+            const int n = (st[s + 1] - st[s] + 255) >> 8;
+            int before = 0;
+            for (int o = 0; o < a.B; ++o) {
+                const int m = (st[o + 1] - st[o] + 255) >> 8;
+                before += m > n || (m == n && o < s);
+            }
+            order(a)[before] = s;
+            of(a)[before] = n;
+        }
+    }
+};
+
+// Where there are too few items for that to end evenly, or for every SM to have one: the items of all heads of all
+// sequences lie end to end on an axis in units of 16 keys, each behind RUN_OVER units of its own cost, and worker w
+// takes the tiles that begin in [W w, W (w + 1)). Items that a run ends in leave partials, which a second launch
+// joins.
+constexpr int RUN_OVER = 20;             // Q, first scores, output or partials: about 4 us, a tile of 5 units takes 0.92
+__host__ __device__ inline int item_cost(int tile) { return 16 * (tile + 1) + RUN_OVER; }
+__host__ __device__ inline int items_cost(int n) { return 8 * n * (n + 1) + RUN_OVER * n; }   // of the first n of a head
+// the item's first tile of K keys that begins at unit u of it or behind
+template <int K> __device__ __forceinline__ int run_tile(int u) { return (max(u - RUN_OVER, 0) + K / 16 - 1) / (K / 16); }
+
+struct Runs : Item {
+    static constexpr bool RUNS = true;
+    const PromptArgs& a;
+    int seq, start;                      // the item's sequence, where it begins on the axis (-1: before the first item)
+
+    static __device__ __forceinline__ int* pre(const PromptArgs& a) { return starts() + a.B + 1; }   // [B + 1], then W
+    // (registers are short in the softmax threads: what is needed once an item stays in shared memory)
+    __device__ __forceinline__ int run() const { return pre(a)[a.B + 1]; }
+    __device__ __forceinline__ int lo() const { return min(pre(a)[a.B], run() * (int)blockIdx.x); }
+    __device__ __forceinline__ int hi() const { return min(pre(a)[a.B], run() * ((int)blockIdx.x + 1)); }
+    __device__ __forceinline__ int n_tiles() const { return (len + 255) >> 8; }
+    __device__ __forceinline__ void at_sequence(int s) {
+        seq = s;
+        first = starts()[s];
+        len = starts()[s + 1] - first;
+    }
+    __device__ __forceinline__ Runs(const PromptArgs& args) : a(args), start(-1) {}
+    __device__ __forceinline__ void find(int lo) {
+        int s0 = 0, s1 = a.B - 1;                        // the last sequence that begins at lo or before
+        while (s0 < s1) {
+            const int mid = (s0 + s1 + 1) >> 1;
+            if (pre(a)[mid] <= lo) s0 = mid; else s1 = mid - 1;
+        }
+        at_sequence(s0);
+        const int per_head = items_cost(n_tiles());
+        int in = lo - pre(a)[s0];
+        head = in / per_head;
+        in -= head * per_head;
+        tile = 0;
+        for (int step = 1 << 15; step > 0; step >>= 1)   // the last item that begins at in or before
+            if (tile + step < n_tiles() && items_cost(tile + step) <= in) tile += step;
+        start = lo - in + items_cost(tile);
+    }
+    __device__ __forceinline__ bool next() {
+        if (start < 0) {
+            if (lo() >= hi()) return false;
+            find(lo());
+            return true;
+        }
+        start += item_cost(tile);
+        if (start >= hi()) return false;
+        if (++tile == n_tiles()) {
+            tile = 0;
+            if (++head == a.H) {
+                head = 0;
+                int s = seq + 1;
+                while (pre(a)[s + 1] == pre(a)[s]) ++s;  // (one is behind: the axis goes on)
+                at_sequence(s);
+            }
+        }
+        return true;
+    }
+    template <int K> __device__ __forceinline__ int t_lo() const { return min(run_tile<K>(lo() - start), item_tiles<K>()); }
+    template <int K> __device__ __forceinline__ int t_hi() const { return min(run_tile<K>(hi() - start), item_tiles<K>()); }
+    template <int K> __device__ __forceinline__ int tiles() const { return max(t_hi<K>() - t_lo<K>(), 0); }
+    template <int K> __device__ __forceinline__ int tiles(int L) const { return max(min(t_hi<K>(), lane_tiles<K>(L)) - t_lo<K>(), 0); }
+    static __device__ __forceinline__ void prepare(const PromptArgs& a) {
+        if (threadIdx.x >= 32) return;
+        const int* st = starts();
+        const int lane = threadIdx.x;
+        int run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = b < a.B ? a.H * items_cost((st[b + 1] - st[b] + 255) >> 8) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < a.B) pre(a)[b + 1] = run + x;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            pre(a)[0] = 0;
+            pre(a)[a.B + 1] = max(2 * RUN_OVER, (run + (int)gridDim.x - 1) / (int)gridDim.x);
+        }
+    }
 };
 
 constexpr int prompt_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
 static_assert(prompt_smem(64, 1024) <= 227 * 1024 && prompt_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
-template <int DH>
+template <int DH, class It>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, PromptArgs a) {
@@ -173,21 +295,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         fence_barrier_init();
     }
     load_starts(a, st);
-    for (int s = tid; s < a.B; s += THREADS) {           // sequences by tiles, longest first
-        const int n = (st[s + 1] - st[s] + 255) >> 8;
-        int before = 0;
-        for (int o = 0; o < a.B; ++o) {
-            const int m = (st[o + 1] - st[o] + 255) >> 8;
-            before += m > n || (m == n && o < s);
-        }
-        Items::order(a)[before] = s;
-        Items::of(a)[before] = n;
-    }
+    It::prepare(a);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Items it(a);
+    It it(a);
+    if constexpr (It::RUNS) {
+        if (tid == 0) {
+            Runs r(a);
+            const bool any = r.next();
+            a.jobs[blockIdx.x] = Job{any && r.lo() > r.start, r.first, r.len, r.head, r.tile, r.start, r.run(), 0};
+        }
+    }
 
     if (warp >= SOFT_WARPS) {
         asm volatile(EVS_ATTN_AUX_REGS);
@@ -199,7 +319,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             uint32_t ph = 1, used = 0;                   // parity that a free slot has; slots in use so far
             bool ok = true;
             while (ok && it.next()) {
-                const int n = 2 * it.key_tiles<KEYS>(), g = it.head / (a.H / a.G);
+                const int n = 2 * it.template tiles<KEYS>(), g = it.head / (a.H / a.G), row = it.first + it.template t_lo<KEYS>() * KEYS;
                 for (int j = 0; j < n; ++j) {
                     if ((used >> s & 1u) && !mbar_wait(&empty[s], ph)) { ok = false; break; }
                     used |= 1u << s;
@@ -207,7 +327,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     mbar_arrive_expect_tx(&full[s], (uint32_t)TILE);
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(dst + hf * HALF, j & 1 ? &tmV : &tmK, hf * 64, it.first + (j >> 1) * KEYS, g, 0, &full[s], keep);
+                        tma_load_4d(dst + hf * HALF, j & 1 ? &tmV : &tmK, hf * 64, row + (j >> 1) * KEYS, g, 0, &full[s], keep);
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1u;
@@ -227,7 +347,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             uint32_t cnt = 0, qn = 0;                    // tiles, items
             bool ok = true;
             while (ok && it.next()) {
-                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>();
+                const int n = it.template tiles<KEYS>(L), all = it.template tiles<KEYS>();
                 if (n > 0) {
                     if (qn > 0 && !all_wait(&q_free[L], (qn - 1) & 1u)) { ok = false; break; }
                     if (leader) {
@@ -272,7 +392,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             uint32_t cnt = 0;
             bool ok = true;
             while (ok && it.next()) {
-                const int n = it.key_tiles<KEYS>(L), all = it.key_tiles<KEYS>(), keys = it.keys(L);
+                const int n = it.template tiles<KEYS>(L), all = it.template tiles<KEYS>(), keys = it.keys(L) - it.template t_lo<KEYS>() * KEYS;
                 for (int t = 0; t < all; ++t, v.next()) {
                     if (!all_wait(&full[v.slot], v.phase)) { ok = false; break; }
                     if (t >= n) {
@@ -325,8 +445,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     };
     bool more = it.next();
     while (more) {
-        const int rows = it.rows(L), n = it.key_tiles<KEYS>(L), row0 = it.row0(L), head = it.head;
-        const int row_at = it.first + row0;
+        const int rows = it.rows(L), n = it.template tiles<KEYS>(L), row0 = it.row0(L), head = it.head, row_at = it.first + row0;
+        const int diagonal = row0 - it.template t_lo<KEYS>() * KEYS;   // the first row's own key, from the first tile on
+        int slot = -1;                                   // for partials, where this is not all of the lane's tiles
+        if constexpr (It::RUNS) {
+            if (n < it.template lane_tiles<KEYS>(L)) slot = 2 * blockIdx.x + (it.lo() > it.start ? 0 : 1);
+        }
         const bool work = (th.row & ~31) < rows;         // of this warp
         th.begin();
         for (int t = 0; t < n; ++t) {
@@ -338,7 +462,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
             arrive(&s_free[L]);
             if (work) {
-                if ((t + 1) * KEYS > row0 + 1) th.mask_from(x, row0 + th.row + 1 - t * KEYS - th.half * (KEYS / 2));
+                if ((t + 1) * KEYS > diagonal + 1) th.mask_from(x, diagonal + th.row + 1 - t * KEYS - th.half * (KEYS / 2));
                 th.tile(x, sl, cnt, t == 0, before);
                 tmem_wait_st();
             }
@@ -347,11 +471,28 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         // what needs nothing of the last product, while that runs
         float l = 0.f;
-        if (rows > 0 && work) l = th.exchange(th.l, [](float x, float y) { return x + y; });
+        if (n > 0 && work) l = th.exchange(th.l, [](float x, float y) { return x + y; });
         more = it.next();
-        if (rows <= 0) continue;
+        if (n == 0) continue;
         before();
-        if (work) {
+        if (work && slot >= 0) {
+            tc_fence_after();
+            const int r = L * 128 + th.row;
+            float* dst = a.po + ((int64_t)slot * DH + th.half * (DH / 2)) * 256 + r * 4;
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+                uint32_t o[16];
+                tmem_ld16_issue(th.o_at + (uint32_t)(c * 16), o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(dst + (c * 4 + j) * 1024) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            // once a wait has run out the rest is void: l = NaN makes the rows' outputs NaN
+            if (th.half == 0)
+                a.pml[slot * 256 + r] = ok ? make_float2(th.m * LN2, l) : make_float2(-INFINITY, __int_as_float(0x7fc00000));
+            tc_fence_before();
+        } else if (work) {
             tc_fence_after();
             const bool live = th.row < rows;
             const int64_t row = row_at + th.row;
@@ -384,6 +525,70 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     rest_rows<bf16>(a, st[0], st[a.B], DH, blockIdx.x, gridDim.x, tid, 32 * SOFT_WARPS);
     tc_fence_before();
     __syncthreads();
+}
+
+// =========================================================================================
+// Joins the partials of items that a run ended in: a CTA takes 1024 / dh rows of the item that worker
+// blockIdx.y's run begins within, if that is the first run to do so; four columns of two rows a thread.
+// =========================================================================================
+template <int DH> __global__ void __launch_bounds__(128) prompt_join_kernel(PromptArgs a) {
+    constexpr int KEYS = tile_keys(DH), RW = 512 / DH, R = 2;
+    pdl_wait();
+    pdl_trigger();
+    const int w = blockIdx.y + 1;
+    const Job job = a.jobs[w];
+    if (!job.valid || job.run * (w - 1) > job.start) return;
+    Item it;
+    it.first = job.first;
+    it.len = job.len;
+    it.head = job.head;
+    it.tile = job.tile;
+    const int c4 = threadIdx.x / RW, r0 = blockIdx.x * RW * R, L = r0 >> 7, all = it.lane_tiles<KEYS>(L);
+    // the workers that have some of the lane's tiles (Runs::t_lo and t_hi): consecutive ones
+    int v0 = w - 1, v1 = (job.start + item_cost(job.tile) - 1) / job.run;
+    while (v0 <= v1 && run_tile<KEYS>(job.run * (v0 + 1) - job.start) == 0) ++v0;
+    while (v1 >= v0 && run_tile<KEYS>(job.run * v1 - job.start) >= all) --v1;
+    if (v0 >= v1) return;                                // one has written all of it
+    float M[R] = {-INFINITY, -INFINITY}, l[R] = {};
+    float4 O[R] = {};
+    for (int v = v0; v <= v1; ++v) {
+        const int64_t slot = 2 * v + (job.run * v > job.start ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = r0 + i * RW + threadIdx.x % RW;
+            const float2 ml = a.pml[slot * 256 + r];
+            const float4 o = *reinterpret_cast<const float4*>(a.po + (slot * DH + c4 * 4) * 256 + r * 4);
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;   // only -inf scores
+            if (ml.x > M[i]) {
+                const float f = __expf(M[i] - ml.x);
+                l[i] *= f;
+                O[i].x *= f; O[i].y *= f; O[i].z *= f; O[i].w *= f;
+                M[i] = ml.x;
+            }
+            const float p = ml.x == M[i] ? 1.f : __expf(ml.x - M[i]);
+            l[i] = fmaf(ml.y, p, l[i]);
+            O[i].x = fmaf(p, o.x, O[i].x);
+            O[i].y = fmaf(p, o.y, O[i].y);
+            O[i].z = fmaf(p, o.z, O[i].z);
+            O[i].w = fmaf(p, o.w, O[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = r0 + i * RW + threadIdx.x % RW;
+        if (it.tile * 256 + r >= it.len) continue;
+        const int64_t row = it.first + it.tile * 256 + r;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        bf16* dst = (bf16*)a.o + row * a.o_row + (int64_t)it.head * DH + c4 * 4;
+        const uint32_t x = pack2(O[i].x * inv, O[i].y * inv), y = pack2(O[i].z * inv, O[i].w * inv);
+        if (a.o_vec) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(x, y);
+        } else {
+            uint16_t* to = reinterpret_cast<uint16_t*>(dst);
+            to[0] = (uint16_t)x; to[1] = (uint16_t)(x >> 16); to[2] = (uint16_t)y; to[3] = (uint16_t)(y >> 16);
+        }
+        if (c4 == 0 && a.lse) a.lse[row * a.H + it.head] = l[i] == 0.f ? -INFINITY : M[i] + logf(l[i]);
+    }
 }
 
 // =========================================================================================
@@ -449,22 +654,59 @@ bool tensor_ok(const evs_prompt_attn_args& c) {
            map_ok(c.v, c.kv_row, c.kv_head, 0, c.kv_heads > 1, false);
 }
 
-template <int DH>
-cudaError_t launch_tensor(const evs_prompt_attn_args& c, const PromptArgs& a, cudaStream_t stream) {
+// Whether items are dealt in runs: where the longest of them would end far behind the mean of the SMs, if the
+// sequences were of one length (the lengths are on the device). Runs cost their own starts, partials and a launch:
+// 256 items of 8192 tokens, 54 units apart, 104 us in runs and 98 whole; 700 tokens x 8 heads (56) 19 and 14; 2048
+// tokens x 8 heads (109) 25.5 and 29.6; 4096 (145) 42 and 52; 16384 x 2 heads 97 and 180.
+constexpr int RUNS_WORTH = 80;
+bool use_runs(const evs_prompt_attn_args& c) {
+    if (c.dtype != EVS_DTYPE_BF16 || (c.head_dim != 64 && c.head_dim != 128)) return false;
+    const long long n = ((long long)c.tokens + c.batch * 256LL - 1) / (c.batch * 256LL);   // items of a head
+    if (n * c.batch * c.heads > 4096) return false;
+    const double longest = item_cost((int)n - 1), mean = (double)items_cost((int)n) * c.batch * c.heads / kAttnGrid;
+    return longest > mean + RUNS_WORTH;
+}
+size_t runs_workspace(const evs_prompt_attn_args& c, PromptArgs* a) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char* p = a ? (char*)c.workspace + off : nullptr;
+        off = round256(off + bytes);
+        return p;
+    };
+    char* po = take((size_t)2 * kAttnGrid * 256 * c.head_dim * 4);
+    char* ml = take((size_t)2 * kAttnGrid * 256 * 8);
+    char* jobs = take((size_t)kAttnGrid * sizeof(Job));
+    if (a) {
+        a->po = (float*)po;
+        a->pml = (float2*)ml;
+        a->jobs = (Job*)jobs;
+    }
+    return off;
+}
+
+template <int DH, class It>
+cudaError_t launch_items(const evs_prompt_attn_args& c, const PromptArgs& a, int grid, cudaStream_t stream) {
     // First: the runtime makes the device's context this thread's own, which the driver's encoding of the
     // maps does not and wants to find. The limit is that of any batch: this call's own would be lowered by
     // another thread's smaller call before the launch.
     const cudaError_t e =
-        cudaFuncSetAttribute(prompt_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(DH, 1024));
+        cudaFuncSetAttribute(prompt_tc_kernel<DH, It>, cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(DH, 1024));
     if (e != cudaSuccess) return e;
     CUtensorMap q, k, v;
     if (!make_rows_map(&q, c.q, Q_ROWS, DH, c.tokens, c.heads, 1, c.q_row, c.q_head, 0) ||
         !make_rows_map(&k, c.k, tile_keys(DH), DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0) ||
         !make_rows_map(&v, c.v, tile_keys(DH), DH, c.tokens, c.kv_heads, 1, c.kv_row, c.kv_head, 0))
         return cudaErrorInvalidValue;
+    return launch_s(stream, prompt_tc_kernel<DH, It>, dim3(grid), dim3(THREADS), (size_t)prompt_smem(DH, c.batch), q, k, v, a);
+}
+
+template <int DH> cudaError_t launch_tensor(const evs_prompt_attn_args& c, PromptArgs& a, cudaStream_t stream) {
     const long long items = ((long long)c.tokens / 256 + c.batch) * c.heads;     // at most
-    const int grid = (int)(items < kAttnGrid ? items : kAttnGrid);
-    return launch_s(stream, prompt_tc_kernel<DH>, dim3(grid), dim3(THREADS), (size_t)prompt_smem(DH, c.batch), q, k, v, a);
+    if (!use_runs(c)) return launch_items<DH, Items>(c, a, (int)(items < kAttnGrid ? items : kAttnGrid), stream);
+    runs_workspace(c, &a);
+    const cudaError_t e = launch_items<DH, Runs>(c, a, kAttnGrid, stream);
+    if (e != cudaSuccess) return e;
+    return launch_s(stream, prompt_join_kernel<DH>, dim3(256 * DH / 1024, kAttnGrid - 1), dim3(128), 0, a);
 }
 
 template <typename T, int DH>
@@ -502,7 +744,8 @@ cudaError_t launch(const evs_prompt_attn_args& c, cudaStream_t stream) {
 }  // namespace evs
 
 extern "C" size_t evs_prompt_attention_workspace(const evs_prompt_attn_args* c) {
-    return 0;
+    using namespace evs;
+    return valid_shape(c) && c->tokens > 0 && use_runs(*c) ? runs_workspace(*c, nullptr) : 0;
 }
 
 extern "C" evs_status evs_prompt_attention(const evs_prompt_attn_args* c, void* stream) {
@@ -515,5 +758,8 @@ extern "C" evs_status evs_prompt_attention(const evs_prompt_attn_args* c, void* 
     if (c->q_row < c->head_dim || c->kv_row < c->head_dim || c->o_row < (long long)c->heads * c->head_dim) return EVS_ERR_INVALID_ARG;
     if ((c->heads > 1 && c->q_head < c->head_dim) || (c->kv_heads > 1 && c->kv_head < c->head_dim)) return EVS_ERR_INVALID_ARG;
     if (!(c->scale >= 0.f) || isinf(c->scale) || (c->scale > 0.f && c->scale < 1e-30f)) return EVS_ERR_INVALID_ARG;
+    const size_t need = evs_prompt_attention_workspace(c);
+    if (need > 0 && (!c->workspace || (uintptr_t)c->workspace % 256)) return EVS_ERR_INVALID_ARG;
+    if (c->ws_bytes < need) return EVS_ERR_CAPACITY;
     return status_of(launch(*c, (cudaStream_t)stream));
 }

@@ -336,11 +336,14 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
     flag = _vec("flags", flags, torch.int32, (1,), dev)
     lse = torch.empty(N, H, dtype=torch.float32, device=dev) if return_lse else None
     if N > 0:
-        a = L.pack_prompt_shapes(N, starts.shape[0] - 1, H, G, dh, _DT[q.dtype], out is None,
-                                 0.0 if scale is None else scale) + \
-            L.pack_prompt_rest(q.data_ptr(), q_row, q_head, k.data_ptr(), v.data_ptr(), kv_row, kv_head, at,
-                               o.data_ptr(), o_row, _p(lse), 0, 0, flag)
-        _enqueue(L.load().evs_prompt_attention, "evs_prompt_attention", a, dev)
+        lib = L.load()
+        shapes = L.pack_prompt_shapes(N, starts.shape[0] - 1, H, G, dh, _DT[q.dtype], out is None,
+                                      0.0 if scale is None else scale)
+        n = lib.evs_prompt_attention_workspace(shapes + L.PROMPT_NO_REST)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        a = shapes + L.pack_prompt_rest(q.data_ptr(), q_row, q_head, k.data_ptr(), v.data_ptr(), kv_row, kv_head, at,
+                                        o.data_ptr(), o_row, _p(lse), _p(ws), n, flag)
+        _enqueue(lib.evs_prompt_attention, "evs_prompt_attention", a, dev)
     return o if lse is None else [o, lse]
 
 

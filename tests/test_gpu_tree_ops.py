@@ -204,8 +204,40 @@ def test_prompt_offsets_past_32_bits(evs):
     at = N - 300
     q[at:], k[at:], v[at:] = d["q"], d["k"], d["v"]
     got = evs.prompt_attention(q, k, v, i32([at, N]), return_lse=True)
-    want = run_prompt(evs, d)
-    assert torch.equal(got[0][at:], want[0]) and torch.equal(got[1][at:], want[1])
+    check((got[0][at:], got[1][at:]), ref.prompt(d["q"], d["k"], d["v"], d["starts"]), BF16, dh, 300)
+
+
+RUNS = [
+    # few items of uneven length: dealt in runs of tiles, some of which no item begins in, or several do
+    ([2048], 8, 8, 128), ([5000], 1, 1, 128), ([5001], 2, 1, 64), ([4096, 700], 2, 2, 128), ([0, 3000, 0, 1, 0, 2999], 3, 1, 128),
+    ([8192], 4, 2, 64), ([1, 6000, 1], 2, 2, 64), ([255, 4097, 257], 1, 1, 128), ([300] * 5 + [4000], 1, 1, 64),
+]
+
+
+@pytest.mark.parametrize("case", RUNS, ids=lambda c: "_".join(map(str, c[0][:4])) + f"-{c[1]}-{c[3]}")
+def test_prompt_in_runs(evs, case):
+    lens, H, G, dh = case
+    d = make_prompt(sum(lens) + H, BF16, lens, H, G, dh, before=3, behind=5)
+    want = ref.prompt(d["q"], d["k"], d["v"], d["starts"])
+    a, b = run_prompt(evs, d), run_prompt(evs, d)
+    check(a, want, BF16, dh, max(lens))
+    assert same(a, b)
+    wide = torch.zeros(d["q"].shape[0], H * dh + 3, device="cuda", dtype=BF16)      # rows off 8 bytes
+    view = wide[:, :H * dh].unflatten(1, (H, dh))
+    c = run_prompt(evs, d, out=view)
+    n = sum(lens)
+    assert torch.equal(view[3:3 + n], a[0][3:3 + n]) and torch.equal(c[1], a[1])
+
+
+def test_prompt_runs_of_infinities(evs):
+    """Partials of a row without any score: the first 2000 keys are -inf for all, the first 2000 rows read nothing else."""
+    d = make_prompt(77, BF16, [4000], 1, 1, 128)
+    q, k, v = (d[x].contiguous().clone() for x in "qkv")
+    q.abs_()
+    k[:2000] = -math.inf
+    o, lse = evs.prompt_attention(q, k, v, i32([0, 4000]), return_lse=True)
+    assert (o[:2000] == 0).all() and torch.isneginf(lse[:2000]).all()
+    check((o[2000:], lse[2000:]), ref.prompt(q[2000:], k[2000:], v[2000:], [0, 2000]), BF16, 128, 4000)
 
 
 def test_prompt_refusals(evs):
