@@ -713,8 +713,10 @@ template <typename T, int DH>
 cudaError_t launch_simt(const evs_prompt_attn_args& c, const PromptArgs& a, cudaStream_t stream) {
     using S = Simt<T, DH, 4>;
     constexpr size_t most = sizeof(typename S::Smem) + (1024 + 1) * 4 + 16;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    if (e != cudaSuccess) return e;
+    if (most > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+    }
     const size_t smem = sizeof(typename S::Smem) + ((c.batch + 1) * 4 + 15) / 16 * 16;
     // one more than the sequences can fill, for the rest
     const dim3 grid(c.tokens / S::ROWS + c.batch + 1, c.heads);

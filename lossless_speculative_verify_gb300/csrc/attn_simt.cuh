@@ -18,6 +18,9 @@ template <> __device__ __forceinline__ float simt_exp<__nv_bfloat16>(float x) { 
 template <typename T, int DH, int R> struct Simt {
     static constexpr int ROWS = 16 * R, KEYS = 64, LD = DH + 4, LDP = KEYS + 4;
     static constexpr int CW = DH / 16, VEC = CW < 4 ? CW : 4, NU = CW / VEC;   // columns of a thread, in a piece, pieces
+    static constexpr int PIECES = KEYS * DH / 4 / 256;   // of four columns, of a tile of K or V, a thread brings
+    // V of a tile on its way while its scores are worked out, where registers allow
+    static constexpr bool AHEAD = R * DH <= 256 && DH <= 128 && !(R == 4 && DH > 64);
     struct Smem {
         float q[ROWS][LD];
         float kv[KEYS][LD];
@@ -44,18 +47,20 @@ template <typename T, int DH, int R> struct Simt {
             sm.q[r][c] = p ? to_f32(p[c]) * scale : 0.f;
         }
     }
+    template <typename F> __device__ __forceinline__ float4 fetch(F rows, int nk, int piece) {
+        const int e = tid + piece * 256, r = e / (DH / 4), c = e % (DH / 4) * 4;
+        if (r >= nk) return make_float4(0.f, 0.f, 0.f, 0.f);
+        const T* p = rows(r) + c;
+        if (sizeof(T) == 4 && (uintptr_t)p % 16 == 0) return *reinterpret_cast<const float4*>(p);
+        return make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+    }
+    __device__ __forceinline__ void put(int piece, float4 x) {
+        const int e = tid + piece * 256;
+        *reinterpret_cast<float4*>(&sm.kv[e / (DH / 4)][e % (DH / 4) * 4]) = x;
+    }
     template <typename F> __device__ __forceinline__ void stage_kv(F rows, int nk) {
 #pragma unroll 4
-        for (int e = tid; e < KEYS * (DH / 4); e += 256) {
-            const int r = e / (DH / 4), c = e % (DH / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < nk) {
-                const T* p = rows(r) + c;
-                if (sizeof(T) == 4 && (uintptr_t)p % 16 == 0) x = *reinterpret_cast<const float4*>(p);
-                else x = make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
-            }
-            *reinterpret_cast<float4*>(&sm.kv[r][c]) = x;
-        }
+        for (int i = 0; i < PIECES; ++i) put(i, fetch(rows, nk, i));
     }
     static __device__ __forceinline__ uint64_t as_pair(float a, float b) {
         uint64_t r;
@@ -70,7 +75,18 @@ template <typename T, int DH, int R> struct Simt {
     }
     // nk keys (1 .. 64) whose rows k(j) and v(j) are; sees(r, j): row r reads key j
     template <typename FK, typename FV, typename FM> __device__ __forceinline__ void tile(FK k, FV v, int nk, FM sees) {
-        stage_kv(k, nk);
+        float4 ahead[AHEAD ? PIECES : 1];
+        if constexpr (AHEAD) {
+            float4 x[PIECES];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) x[i] = fetch(k, nk, i);
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) ahead[i] = fetch(v, nk, i);
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) put(i, x[i]);
+        } else {
+            stage_kv(k, nk);
+        }
         __syncthreads();
         uint64_t acc[R][4];
 #pragma unroll
@@ -130,7 +146,12 @@ template <typename T, int DH, int R> struct Simt {
             l[i] += sum;
         }
         __syncthreads();
-        stage_kv(v, nk);
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) put(i, ahead[i]);
+        } else {
+            stage_kv(v, nk);
+        }
         __syncthreads();
         const int end = (nk + 3) & ~3;                   // rows behind nk are zero, and so are their weights
 #pragma unroll 1

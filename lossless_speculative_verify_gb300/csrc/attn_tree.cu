@@ -86,6 +86,15 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(256) tree
     const bool report = rt == 0 && slot == 0 && g == 0 && threadIdx.x == 0;
     const int nodes = nodes_of(a, b, report), cached = cached_of(a, b, report), keys = node_keys(a, cached, nodes, report);
     const int r0 = rt * S::ROWS, rows = nodes * grp;
+    if (a.slots == 1) {                                  // no second launch: nodes behind the tree's, too
+        for (int r = max(r0, rows) + (int)threadIdx.x / 16; r < min(r0 + S::ROWS, a.T * grp); r += 16) {
+            const int node = r / grp, h = g * grp + r - node * grp;
+            const int64_t row = (int64_t)b * a.T + node;
+            if (a.zero_rest)
+                for (int c = threadIdx.x % 16; c < DH; c += 16) ((T*)a.o)[row * a.o_ld + (int64_t)h * DH + c] = from_f32<T>(0.f);
+            if (a.lse && threadIdx.x % 16 == 0) a.lse[row * a.H + h] = -INFINITY;
+        }
+    }
     if (r0 >= rows) return;
     for (int i = threadIdx.x; i < nodes; i += 256) up[i] = parent_of(a, b, i, rt == 0 && slot == 0 && g == 0);
     S w(sm);
@@ -118,6 +127,17 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(256) tree
         for (int j0 = 0; j0 < keys; j0 += S::KEYS)
             w.tile([&](int j) { return kn + (int64_t)(j0 + j) * ld; }, [&](int j) { return vn + (int64_t)(j0 + j) * ld; },
                    min(S::KEYS, keys - j0), [&](int r, int j) { return path[r][(j0 + j) >> 5] >> ((j0 + j) & 31) & 1u; });
+    }
+    if (a.slots == 1) {                                  // all of the keys: no partials
+        w.finish([&](int r, int c, float o, float m, float l) {
+            r += r0;
+            const int node = r / grp, h = g * grp + r - node * grp;
+            if (r >= rows) return;
+            const int64_t row = (int64_t)b * a.T + node;
+            ((T*)a.o)[row * a.o_ld + (int64_t)h * DH + c] = from_f32<T>(l > 0.f ? o / l : (l == 0.f ? 0.f : l));
+            if (c == 0 && a.lse) a.lse[row * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
+        });
+        return;
     }
     const int64_t at = ((int64_t)b * a.G + g) * a.slots + slot;
     float* po = a.po + at * rows4(a.seg_rows) * DH;
@@ -647,7 +667,11 @@ bool valid_shape(const evs_tree_attn_args* c) {
     return c->dtype == EVS_DTYPE_F32 || c->dtype == EVS_DTYPE_BF16;
 }
 
-// Row sizes and slots of the CUDA-core path: about four waves of the SMs at two CTAs each.
+// Row sizes and slots of the CUDA-core path: about four waves of the SMs at two CTAs each, or one slot, which needs
+// no second launch, where the keys are few tiles of little work (4 sequences x 7 nodes x 4 heads of 16 over 256 rows:
+// 21 us a call for 25, though 10.0 for 7.6 in a
+// replayed graph; over 512 rows 16 for 8).
+constexpr long long ONE_SLOT = 2048;     // key tiles x rows x columns
 int simt_rows(const evs_tree_attn_args& c) { return c.nodes * (c.heads / c.kv_heads) > 16 ? 64 : 16; }
 void plan_simt(const evs_tree_attn_args& c, TreeArgs& a) {
     const int rows = c.nodes * (c.heads / c.kv_heads), per = simt_rows(c);
@@ -657,6 +681,7 @@ void plan_simt(const evs_tree_attn_args& c, TreeArgs& a) {
     long long s = items > 0 ? (4 * 152 + items - 1) / items : 1;
     const long long most = c.capacity / 64 + 1;
     s = s < most ? s : most;
+    if ((c.capacity / 64 + 1) * (long long)per * c.head_dim <= ONE_SLOT) s = 1;
     a.slots = (int)(s < 1 ? 1 : s);
 }
 
@@ -723,9 +748,11 @@ cudaError_t launch_tensor(const evs_tree_attn_args& c, const TreeArgs& a, int gr
 
 template <typename T, int DH, int R> cudaError_t launch_rows(const evs_tree_attn_args& c, const TreeArgs& a, cudaStream_t stream) {
     using S = Simt<T, DH, R>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(tree_simt_kernel<T, DH, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename S::Smem));
-    if (e != cudaSuccess) return e;
+    if (sizeof(typename S::Smem) > 40 * 1024) {          // (beside the kernel's own)
+        const cudaError_t e =
+            cudaFuncSetAttribute(tree_simt_kernel<T, DH, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename S::Smem));
+        if (e != cudaSuccess) return e;
+    }
     const dim3 grid((a.seg_rows + S::ROWS - 1) / S::ROWS * a.slots, c.kv_heads, c.batch);
     return launch_s(stream, tree_simt_kernel<T, DH, R>, grid, dim3(256), sizeof(typename S::Smem), a);
 }
@@ -764,7 +791,7 @@ cudaError_t launch(const evs_tree_attn_args& c, cudaStream_t stream) {
             case 32: e = half ? launch_simt<bf16, 32>(c, a, stream) : launch_simt<float, 32>(c, a, stream); break;
             default: e = half ? launch_simt<bf16, 16>(c, a, stream) : launch_simt<float, 16>(c, a, stream);
         }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || (!tensor && a.slots == 1)) return e;
     // sets of rows: two where one each would not run at once; groups: one for eight partials of a row, as many as do
     const int rw = 512 / c.head_dim, rows = c.nodes * (c.heads / c.kv_heads);
     const long long sets = (long long)((rows + rw - 1) / rw) * c.kv_heads * c.batch, room = 152 * 4;

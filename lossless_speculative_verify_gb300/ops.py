@@ -294,6 +294,21 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, k_bloc
     return o if lse is None else [o, lse]
 
 
+def _rows4(name, t, dtype, shape, dev):
+    """Row stride of a [batch, nodes, heads, dh] tensor whose rows are evenly spaced."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on {dev}")
+    _no_grad(name, t)
+    B, T, H, dh = shape
+    s0, s1, s2, s3 = t.stride()
+    ld = s1 if T > 1 else s0 if B > 1 else H * dh
+    if not (s3 == 1 and (H == 1 or s2 == dh)):
+        raise ValueError(f"{name}: heads have to be contiguous")
+    if not (ld >= H * dh and (B == 1 or s0 == T * ld)):
+        raise ValueError(f"{name}: rows have to be evenly spaced")
+    return ld
+
+
 def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False, flags=None):
     """Causal attention over whole prompts packed behind each other: q [tokens, heads, dh], k and v [tokens, kv_heads,
     dh], all fp32 or all bf16. Sequence b is rows starts[b] up to starts[b + 1] of starts [batch + 1] (int32, on the
@@ -382,10 +397,9 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
     _need(cache_len is not None, "cache_len: missing")
     cached = _vec("cache_len", cache_len, torch.int32, (B,), dev)
     sizes = _vec("lens", lens, torch.int32, (B,), dev)
-    q_ld = _flat("q", q.unsqueeze(1), dt, (B, 1, T, H, dh), dev)
+    q_ld = _rows4("q", q, dt, (B, T, H, dh), dev)
     if out is not None:
-        _need(isinstance(out, torch.Tensor) and out.dim() == 4, f"out: want {dt} {tuple(q.shape)} on {dev}")
-        o, o_ld = out, _flat("out", out.unsqueeze(1), dt, (B, 1, T, H, dh), dev)
+        o, o_ld = out, _rows4("out", out, dt, (B, T, H, dh), dev)
     else:
         o, o_ld = torch.empty(B, T, H, dh, dtype=dt, device=dev), H * dh
     _need(scale is None or 1e-30 <= scale < math.inf, "scale: above zero")
