@@ -17,11 +17,11 @@ namespace {
 using namespace attn;
 
 constexpr int MAX_NODES = 128;
-// What a segment costs beside its tiles, in tiles: Q, the partials. About 2.5 us, where a tile takes a pair of lanes
-// 0.95 and a lane of its own 1.8 (heads of 64: half as much). With 1 everywhere the CTA with the segments of a
-// sequence that has just begun ended 20 us behind the others of 60 (60 nodes x 32 heads x 16), and 64 single tokens
-// with heads of 64 took 65 us for 60.
-constexpr int over_tiles(bool pair, int dh) { return pair ? 4 : dh == 64 ? 3 : 1; }
+// What a segment costs beside its tiles, in tiles: Q, the partials. About 2.5 us, and 6 us where it has but a tile or
+// two; a tile takes a pair of lanes 0.95 and a lane of its own 1.8 (heads of 64: half as much). With 1 everywhere the
+// CTA with the segments of a sequence that has just begun ended 20 us behind the others of 60 (60 nodes x 32 heads x
+// 16 sequences: 99 us, with 4 88, with 6 82), and 64 single tokens with heads of 64 took 65 us for 60.
+constexpr int over_tiles(bool pair, int dh) { return pair ? 6 : dh == 64 ? 3 : 1; }
 
 struct TreeArgs {
     const void *q, *kc, *vc, *kn, *vn;

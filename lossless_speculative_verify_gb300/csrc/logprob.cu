@@ -31,6 +31,7 @@ typedef unsigned long long u64;
 constexpr int LP_MAX_CS = 8;             // portable cluster size
 constexpr int LP_MAX_TOP = 64;
 constexpr uint32_t FULL = 0xffffffffu;
+constexpr float LP_LOG2E = 1.44269502162933349609375f, LP_LOG2E_REST = 1.9259629911e-8f;
 constexpr int LP_FOUND = 256;            // tokens that one warp ranks
 constexpr int LP_BORDER_BIT = 14;        // the border's sign, exponent and nine bits of its mantissa
 
@@ -207,13 +208,10 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
     const float t_in = a.temperature ? a.temperature[r] : 1.f;
     const bool greedy = !(t_in > 0.f);
     const float t = greedy ? 1.f : fminf(t_in, 1e30f);   // above: as 1e30, so that ruled-out tokens stay so
-    // log2(e) / T rounded would move every exponent the same way: its remainder is kept
+    // log2(e) / T rounded would move every exponent the same way: its remainder is kept (and that of log2(e) itself)
     float2 c;
-    {
-        const double cd = 1.4426950408889634 / (double)t;
-        c.x = (float)fmin(cd, (double)FLT_MAX);
-        c.y = cd < (double)FLT_MAX ? (float)(cd - (double)c.x) : 0.f;
-    }
+    c.x = fminf(LP_LOG2E / t, FLT_MAX);
+    c.y = c.x < FLT_MAX ? (fmaf(-c.x, t, LP_LOG2E) + LP_LOG2E_REST) / t : 0.f;
 
     // ---- the pass
     float m = -INFINITY, s = 0.f, w = 0.f;
