@@ -514,7 +514,8 @@ evs_status evs_token_logprobs(const evs_logprob_args* args, void* stream);
  * zero_rest is zero, and lse is -inf. Starts are made to ascend within [0, tokens] (EVS_FLAG_BAD_LEN where
  * they did not). A query whose every score is -inf gives o = 0 and lse = -inf; one whose kernel gave up a
  * bounded wait gives NaN for both (EVS_FLAG_TIMEOUT). Types, statistics and weights as in
- * evs_shared_attention. */
+ * evs_shared_attention. A value of V that is not finite shows in the rows that read it, and in no other. How the keys are dealt, and with it the last bits,
+ * goes by tokens, batch and heads. */
 typedef struct {
     int32_t tokens, batch;               /* rows of the buffers, sequences (<= 1024)        */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
@@ -529,11 +530,12 @@ typedef struct {
     void* o;                             /* device [tokens][heads][head_dim], heads contiguous */
     int64_t o_row;
     float* lse;                          /* device [tokens][heads] or NULL                  */
-    void* workspace;                     /* device, 256-byte aligned; not shared by calls that may overlap */
+    void* workspace;                     /* device, 256-byte aligned, or NULL where none is needed; not shared by
+                                            calls that may overlap                          */
     size_t ws_bytes;
     uint32_t* flags;
 } evs_prompt_attn_args;
-/* Bytes of workspace for these sizes (pointers may still be null; 0 if invalid). */
+/* Bytes of workspace for these sizes (pointers may still be null; 0: none is needed, or invalid). */
 size_t evs_prompt_attention_workspace(const evs_prompt_attn_args* args);
 evs_status evs_prompt_attention(const evs_prompt_attn_args* args, void* stream);
 
@@ -545,9 +547,8 @@ evs_status evs_prompt_attention(const evs_prompt_attn_args* args, void* stream);
  * zero, and their lse is -inf. A tree of one node is a decode step, a chain a verify block.
  * The nodes' K/V lie in k_nodes / v_nodes, or (both NULL) in the cache behind the readable rows, row
  * cache_len[b] + j; rows past the capacity are left out (EVS_FLAG_KV_OVERFLOW). Lengths outside [0,
- * capacity] are clamped (EVS_FLAG_BAD_LEN). Rows that no query reads may hold anything, but the nodes of a
- * tree are read together: a node's V that is not finite shows in all nodes of its tree. Everything else as
- * in evs_shared_attention. */
+ * capacity] are clamped (EVS_FLAG_BAD_LEN). Rows that no query reads may hold anything, and a
+ * node's V that is not finite shows in the nodes below it alone. Everything else as in evs_shared_attention. */
 typedef struct {
     int32_t batch, nodes;                /* 1 .. 1024 sequences, 1 .. 128 nodes             */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */

@@ -78,7 +78,8 @@ __device__ __forceinline__ void rest_rows(const PromptArgs& a, int s0, int s1, i
 // Shared memory of the tensor-core kernel: exchange [2][128] floats, barriers, then st [B + 1], order [B] and of [B]
 // (sequences by length, longest first: which, and their items of 256 rows; or with runs where each begins on the
 // axis), then Q and the ring on 1024 bytes.
-constexpr int BARRIERS = 320;
+constexpr int SCANNERS = 3;              // warps that look through V
+constexpr int BARRIERS = 384;           // and whether V had values that are not finite
 constexpr int small_smem(int B) { return 1024 + BARRIERS + (3 * B + 3) * 4; }
 
 // The item a CTA is at: its sequence's first row and length, its head and 256 rows.
@@ -241,6 +242,38 @@ struct Runs : Item {
 constexpr int prompt_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
 static_assert(prompt_smem(64, 1024) <= 227 * 1024 && prompt_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
+// Adds the values of V that are not finite, which were cleared in the item's tiles of its own rows, to the rows that
+// read them: in the output, or in partials. part: 0 and 1 are the lanes, the rest has nothing to do.
+template <int DH, class It> __device__ __forceinline__ void mend(const PromptArgs& a, const It& it, int part, int lane) {
+    constexpr int KEYS = tile_keys(DH);
+    if (part > 1) return;
+    const int L = part, n = it.template tiles<KEYS>(L), k0 = it.template t_lo<KEYS>() * KEYS, row0 = it.row0(L), rows = it.rows(L);
+    int slot = -1;
+    if constexpr (It::RUNS) {
+        if (n < it.template lane_tiles<KEYS>(L)) slot = 2 * blockIdx.x + (it.lo() > it.start ? 0 : 1);
+    }
+    const bf16* v = (const bf16*)a.v + (int64_t)it.first * a.kv_row + it.head / (a.H / a.G) * a.kv_head;
+    const int end = min(k0 + n * KEYS, row0 + rows);
+#pragma unroll 1
+    for (int j = max(it.tile * 256, k0); j < end; ++j) {
+        float x[DH / 32];
+        if (!bad_values<DH>(v + j * a.kv_row, lane, x)) continue;
+#pragma unroll 1
+        for (int r = max(j - row0, 0); r < rows; ++r)
+#pragma unroll 1
+            for (int u = 0; u < DH / 32; ++u) {
+                const int c = lane * (DH / 32) + u;
+                if (x[u] == 0.f) continue;
+                if (slot >= 0) {
+                    a.po[((int64_t)slot * DH + (c & ~3)) * 256 + (L * 128 + r) * 4 + (c & 3)] += x[u];
+                } else {
+                    bf16* o = (bf16*)a.o + (int64_t)(it.first + row0 + r) * a.o_row + (int64_t)it.head * DH + c;
+                    *o = __float2bfloat16_rn(__bfloat162float(*o) + x[u]);
+                }
+            }
+    }
+}
+
 template <int DH, class It>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -258,18 +291,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint64_t* q_full = pv_done + 4;                                        // [2] Q of an item there
     uint64_t* q_free = q_full + 2;                                         // [2] and read for the last time
     uint64_t* drain = q_free + 2;                                          // [4]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 4);
+    uint64_t* scanned = drain + 4;                                         // [NST] V there and looked through
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scanned + NST);
+    volatile uint32_t* cleared = tmem_slot + 1;
     int* st = Items::starts();
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;
-    static_assert((2 * NST + 20) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((3 * NST + 20) * 8 + 2 * 4 <= BARRIERS, "barriers");
     // an even number: a slot is K's or V's, and each thread that waits for one has seen its phase before
     static_assert(NST % 2 == 0 && NST >= 4, "ring");
     static_assert(TILE == tile_bytes(DH) && HALF % 1024 == 0, "tiles on 1024 bytes");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     pdl_wait();
-    pdl_trigger();
     // not before the wait: a predecessor's CTA on this SM may have yet to allocate
     if (warp == SOFT_WARPS) {
         tmem_alloc(tmem_slot, 512);
@@ -277,6 +311,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
+            mbar_init(&scanned[s], SCANNERS);
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 2);
         }
@@ -294,11 +329,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         fence_barrier_init();
     }
+    if (tid == 0) *cleared = 0;
     load_starts(a, st);
     It::prepare(a);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // not before the allocation: a dependent's CTA that holds columns and waits for this grid could share the SM
+    pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     It it(a);
     if constexpr (It::RUNS) {
@@ -392,15 +430,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             uint32_t cnt = 0;
             bool ok = true;
             while (ok && it.next()) {
-                const int n = it.template tiles<KEYS>(L), all = it.template tiles<KEYS>(), keys = it.keys(L) - it.template t_lo<KEYS>() * KEYS;
+                const int n = it.template tiles<KEYS>(L), all = it.template tiles<KEYS>(), k0 = it.template t_lo<KEYS>() * KEYS;
+                const int keys = it.keys(L) - k0;        // from the piece's first on
                 for (int t = 0; t < all; ++t, v.next()) {
-                    if (!all_wait(&full[v.slot], v.phase)) { ok = false; break; }
+                    if (!all_wait(&scanned[v.slot], v.phase)) { ok = false; break; }
                     if (t >= n) {
                         if (leader) mbar_arrive(&empty[v.slot]);
                         continue;
                     }
                     const int nv = keys - t * KEYS;      // keys from this tile on
-                    if (nv < KEYS && (nv & 15)) clear_rows<DH>(ring + (size_t)v.slot * TILE, nv, lane);
+                    uint8_t* tile = ring + (size_t)v.slot * TILE;
+                    if (nv < KEYS && (nv & 15)) clear_rows<DH>(tile, nv, lane);
                     if (!all_wait(&p_full[2 * L + (cnt & 1u)], cnt >> 1 & 1u)) { ok = false; break; }
                     tc_fence_after();
                     issue_pv<DH>(leader, at, cnt, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), nv, t > 0);
@@ -411,6 +451,24 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
             commit(leader, &drain[2 + L]);
             mbar_wait(&drain[2 + L], 0);
+        } else if (role >= 5) {
+            // ---- V of the item's own rows looked through
+            const uint32_t leader = elect_leader();
+            Cursor v(1, NST);
+            bool ok = true;
+            while (ok && it.next()) {
+                const int all = it.template tiles<KEYS>(), k0 = it.template t_lo<KEYS>() * KEYS, end = it.keys(1) - k0, own = it.tile * 256 - k0;
+                for (int t = 0; t < all; ++t, v.next()) {
+                    if (!all_wait(&full[v.slot], v.phase)) { ok = false; break; }
+                    const int from = max(own - t * KEYS, 0), to = min(end - t * KEYS, KEYS);
+                    uint8_t* tile = ring + (size_t)v.slot * TILE;
+                    if (from < to && scan_rows<DH>(tile, from, to, role - 5, SCANNERS, lane)) {
+                        *cleared = 1;
+                        clear_values<DH>(tile, from, to, role - 5, SCANNERS, lane);
+                    }
+                    if (leader) mbar_arrive(&scanned[v.slot]);
+                }
+            }
         }
         __syncwarp();
         tc_fence_before();
@@ -418,6 +476,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (warp == SOFT_WARPS) {
             tc_fence_after();
             tmem_dealloc(tmem, 512);
+        }
+        if (*cleared) {
+            // all is written: the lanes of this CTA's items, dealt among the warps here
+            It again(a);
+            for (int i = 0; again.next(); ++i) mend<DH>(a, again, (i + role) & 7, lane);
         }
         return;
     }
@@ -628,8 +691,10 @@ template <typename T, int DH> __global__ void __launch_bounds__(256) prompt_simt
     const int end = min(len, r0 + S::ROWS);
     for (int j0 = 0; j0 < end; j0 += S::KEYS) {
         const int nk = min(S::KEYS, end - j0);
-        w.tile([&](int j) { return k + (int64_t)(j0 + j) * a.kv_row; }, [&](int j) { return v + (int64_t)(j0 + j) * a.kv_row; }, nk,
-               [&](int r, int j) { return j0 + j <= r0 + r; });
+        auto k_at = [&](int j) { return k + (int64_t)(j0 + j) * a.kv_row; };
+        auto v_at = [&](int j) { return v + (int64_t)(j0 + j) * a.kv_row; };
+        if (j0 < r0) w.template tile<false>(k_at, v_at, nk, [](int, int) { return true; });
+        else w.template tile<true>(k_at, v_at, nk, [&](int r, int j) { return j0 + j <= r0 + r; });
     }
     w.finish([&](int r, int c, float o, float m, float l) {
         if (r0 + r >= len) return;

@@ -73,8 +73,10 @@ template <typename T, int DH, int R> struct Simt {
     static __device__ __forceinline__ void of_pair(uint64_t v, float& a, float& b) {
         asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
     }
-    // nk keys (1 .. 64) whose rows k(j) and v(j) are; sees(r, j): row r reads key j
-    template <typename FK, typename FV, typename FM> __device__ __forceinline__ void tile(FK k, FV v, int nk, FM sees) {
+    // nk keys (1 .. 64) whose rows k(j) and v(j) are; sees(r, j): row r reads key j. MASKED: some may not, and V that
+    // is not finite is kept from those (a weight of 0 does not)
+    template <bool MASKED, typename FK, typename FV, typename FM>
+    __device__ __forceinline__ void tile(FK k, FV v, int nk, FM sees) {
         float4 ahead[AHEAD ? PIECES : 1];
         if constexpr (AHEAD) {
             float4 x[PIECES];
@@ -170,6 +172,7 @@ template <typename T, int DH, int R> struct Simt {
 #pragma unroll
                         for (int i = 0; i < R; ++i) {
                             const float w = (&p[i].x)[j];
+                            if (MASKED && w == 0.f) continue;
                             const uint64_t w2 = as_pair(w, w);
                             uint64_t o01 = as_pair(o[i][u * 4], o[i][u * 4 + 1]), o23 = as_pair(o[i][u * 4 + 2], o[i][u * 4 + 3]);
                             fma_pair(w2, v01, o01);
@@ -182,7 +185,8 @@ template <typename T, int DH, int R> struct Simt {
                         for (int c = 0; c < VEC; ++c) {
                             const float x = row[c];
 #pragma unroll
-                            for (int i = 0; i < R; ++i) o[i][u * VEC + c] = fmaf((&p[i].x)[j], x, o[i][u * VEC + c]);
+                            for (int i = 0; i < R; ++i)
+                                if (!MASKED || (&p[i].x)[j] != 0.f) o[i][u * VEC + c] = fmaf((&p[i].x)[j], x, o[i][u * VEC + c]);
                         }
                     }
                 }

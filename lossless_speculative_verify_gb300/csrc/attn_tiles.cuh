@@ -246,6 +246,50 @@ template <int DH> __device__ __forceinline__ void clear_rows(uint8_t* tile, int 
     __syncwarp();
 }
 
+// V of keys that some rows of the tile do not read: the weight 0 does not silence what is not finite there. So warps
+// that have nothing else to do look through such rows first, ahead of the weights, and where they find any clear
+// those values; a CTA that has cleared any goes through its work once more at its end and adds them to the rows that
+// do read them, where nothing else counts beside them.
+// Any bf16 of these two that is not finite
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// part: the warp's of `parts` that share the rows from .. to - 1
+template <int DH> __device__ __forceinline__ bool scan_rows(const uint8_t* tile, int from, int to, int part, int parts, int lane) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int hf = 0; hf < DH / 64; ++hf) {
+        const uint8_t* at = tile + hf * tile_keys(DH) * 128 + (lane & 7) * 16;
+#pragma unroll 2
+        for (int k = from + part * 4 + (lane >> 3); k < to; k += parts * 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + k * 128);
+            bad |= not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w);
+        }
+    }
+    return __any_sync(0xffffffffu, bad != 0) != 0;
+}
+template <int DH> __device__ __forceinline__ void clear_values(uint8_t* tile, int from, int to, int part, int parts, int lane) {
+#pragma unroll 1
+    for (int e = lane; e < (to - from) * (DH / 2); e += 32) {
+        const int k = from + e / (DH / 2), c = e % (DH / 2);
+        if ((k - from) / 4 % parts != part) continue;
+        uint32_t* x = reinterpret_cast<uint32_t*>(tile + (c >> 5) * tile_keys(DH) * 128 + k * 128 + (c & 31) * 4);
+        const uint32_t bad = not_finite2(*x);
+        if (bad) *x &= ~((bad >> 15 & 1u) * 0xffffu | (bad >> 31) * 0xffff0000u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+// The lane's columns (DH / 32 of them) of a row of V, what is finite as 0; true where any lane's is not.
+template <int DH> __device__ __forceinline__ bool bad_values(const bf16* v, int lane, float (&x)[DH / 32]) {
+    bool any = false;
+#pragma unroll
+    for (int u = 0; u < DH / 32; ++u) {
+        const bf16 y = v[lane * (DH / 32) + u];
+        const bool bad = not_finite2(__bfloat16_as_ushort(y)) != 0;
+        x[u] = bad ? __bfloat162float(y) : 0.f;
+        any |= bad;
+    }
+    return __any_sync(0xffffffffu, any) != 0;
+}
 // A wait of a whole warp, which agrees on how it ended
 __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase)) != 0; }
 // One thread of a warp issues its products, but all of it runs the code around them: descriptors and addresses

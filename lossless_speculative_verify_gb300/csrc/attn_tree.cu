@@ -118,14 +118,14 @@ template <typename T, int DH, int R> __global__ void __launch_bounds__(256) tree
     const T *kc = (const T*)a.kc + b * a.c_seq + g * a.c_head, *vc = (const T*)a.vc + b * a.c_seq + g * a.c_head;
     const int lo = (int)((int64_t)cached * slot / a.slots), hi = (int)((int64_t)cached * (slot + 1) / a.slots);
     for (int j0 = lo; j0 < hi; j0 += S::KEYS)
-        w.tile([&](int j) { return kc + (int64_t)(j0 + j) * a.c_row; }, [&](int j) { return vc + (int64_t)(j0 + j) * a.c_row; },
+        w.template tile<false>([&](int j) { return kc + (int64_t)(j0 + j) * a.c_row; }, [&](int j) { return vc + (int64_t)(j0 + j) * a.c_row; },
                min(S::KEYS, hi - j0), [](int, int) { return true; });
     if (slot == a.slots - 1) {
         const T *kn = a.kn ? (const T*)a.kn + b * a.n_seq + g * a.n_head : kc + cached * a.c_row;
         const T *vn = a.kn ? (const T*)a.vn + b * a.n_seq + g * a.n_head : vc + cached * a.c_row;
         const int64_t ld = a.kn ? a.n_row : a.c_row;
         for (int j0 = 0; j0 < keys; j0 += S::KEYS)
-            w.tile([&](int j) { return kn + (int64_t)(j0 + j) * ld; }, [&](int j) { return vn + (int64_t)(j0 + j) * ld; },
+            w.template tile<true>([&](int j) { return kn + (int64_t)(j0 + j) * ld; }, [&](int j) { return vn + (int64_t)(j0 + j) * ld; },
                    min(S::KEYS, keys - j0), [&](int r, int j) { return path[r][(j0 + j) >> 5] >> ((j0 + j) & 31) & 1u; });
     }
     if (a.slots == 1) {                                  // all of the keys: no partials
@@ -163,10 +163,36 @@ struct Piece {
 template <int DH> __device__ __forceinline__ int cache_tiles(int cached) { return (cached + tile_keys(DH) - 1) / tile_keys(DH); }
 template <int DH> __device__ __forceinline__ int node_tiles(int nodes) { return (nodes + tile_keys(DH) - 1) / tile_keys(DH); }
 
-constexpr int BARRIERS = 288;
+constexpr int BARRIERS = 304;           // and whether nodes' V had values that are not finite
 constexpr int small_smem(int B) { return 1024 + BARRIERS + 2 * MAX_NODES + (3 * B + 1) * 4; }
 constexpr int tree_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROWS * dh * 2 + ring_slots(dh) * tile_bytes(dh); }
 static_assert(tree_smem(64, 1024) <= 227 * 1024 && tree_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
+
+// Adds the values of V that are not finite, which were cleared in the piece's tiles of nodes, to the partials of the
+// rows below those nodes: the 128 of a lane from r_lane on.
+template <int DH> __device__ __forceinline__ void mend(const TreeArgs& a, const Piece& p, int worker, int r_lane, int lane) {
+    constexpr int KEYS = tile_keys(DH);
+    const int grp = a.H / a.G, r_end = min(a.seg_rows, min(r_lane + 128, p.nodes * grp - p.rt * a.seg_rows));
+    const bf16* v = a.kn ? (const bf16*)a.vn + p.b * a.n_seq + p.g * a.n_head
+                         : (const bf16*)a.vc + p.b * a.c_seq + p.g * a.c_head + p.cached * a.c_row;
+    float* po = a.po + (int64_t)(worker + p.seg) * rows4(a.seg_rows) * DH;
+#pragma unroll 1
+    for (int j = max(p.t0 - p.ntc, 0) * KEYS; j < min(p.keys, (p.t0 + p.n - p.ntc) * KEYS); ++j) {
+        float x[DH / 32];
+        if (!bad_values<DH>(v + j * (a.kn ? a.n_row : a.c_row), lane, x)) continue;
+#pragma unroll 1
+        for (int r = r_lane; r < r_end; ++r) {
+            int i = (p.rt * a.seg_rows + r) / grp;
+            while (i > j) i = (int)parent_of(a, p.b, i, false) - 1;
+            if (i != j) continue;
+#pragma unroll 1
+            for (int u = 0; u < DH / 32; ++u) {
+                const int c = lane * (DH / 32) + u;
+                if (x[u] != 0.f) po[((c >> 2) * rows4(a.seg_rows) + r) * 4 + (c & 3)] += x[u];
+            }
+        }
+    }
+}
 
 template <int DH>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -185,19 +211,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     uint64_t* q_ready = pv_done + 4;                                       // [2] Q of a piece staged
     uint64_t* drain = q_ready + 2;                                         // [4]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 4);
+    volatile uint32_t* cleared = tmem_slot + 1;                            // [2] of the lanes
     uint8_t* up = smem_raw + 1024 + BARRIERS;                               // [2][MAX_NODES] a lane's tree
     int* pre = reinterpret_cast<int*>(up + 2 * MAX_NODES);                 // [B + 1] cost of one row tile's axis before b
     int* len = pre + a.B + 1;                                              // [B] cached rows
     int* size = len + a.B;                                                 // [B] nodes
     uint8_t* sQ = smem_raw + ((smem_u32(smem_raw) + small_smem(a.B) + 1023u & ~1023u) - smem_u32(smem_raw));
     uint8_t* ring = sQ + 2 * Q_TILE;                                       // sQ: [2 lanes][halves][128 rows][128 B]
-    static_assert((2 * NST + 18) * 8 + 4 <= BARRIERS, "barriers");
+    static_assert((2 * NST + 18) * 8 + 3 * 4 <= BARRIERS, "barriers");
     static_assert(NST >= 6, "three slots a worker");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool pairs = a.pair != 0;
 
     pdl_wait();
-    pdl_trigger();
     // not before the wait: a predecessor's CTA on this SM may have yet to allocate
     if (warp == SOFT_WARPS) {
         tmem_alloc(tmem_slot, 512);
@@ -221,6 +247,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
         }
         fence_barrier_init();
     }
+    if (tid < 2) cleared[tid] = 0;
     for (int b = tid; b < a.B; b += THREADS) {
         len[b] = cached_of(a, b, blockIdx.x == 0);
         size[b] = nodes_of(a, b, blockIdx.x == 0);
@@ -245,6 +272,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // not before the allocation: a dependent's CTA that holds columns and waits for this grid could share the SM
+    pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     const int per_b = a.G * a.tiles, total = per_b * pre[a.B], workers = (int)gridDim.x * (pairs ? 1 : 2);
     const int W = max(1, (total + workers - 1) / workers);
@@ -382,7 +411,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                     // a tile without keys (nodes past the capacity) still clears O where it is the first: one step of
                     // cleared rows
                     const int nv = max(keys_of(p, p.t0 + t), 0);
-                    if (nv < KEYS && ((nv & 15) || nv == 0)) clear_rows<DH>(ring + (size_t)(slot0 + v.slot) * TILE, nv, lane);
+                    uint8_t* tile = ring + (size_t)(slot0 + v.slot) * TILE;
+                    if (nv < KEYS && ((nv & 15) || nv == 0)) clear_rows<DH>(tile, nv, lane);
+                    if (p.t0 + t >= p.ntc && scan_rows<DH>(tile, 0, min(nv, KEYS), 0, 1, lane)) {
+                        cleared[L] = 1;
+                        clear_values<DH>(tile, 0, min(nv, KEYS), 0, 1, lane);
+                    }
                     if (!all_wait(&p_full[2 * L + (cnt & 1u)], cnt >> 1 & 1u)) { ok = false; break; }
                     tc_fence_after();
                     issue_pv<DH>(leader, at, cnt, dv + (uint64_t)((uint32_t)(v.slot * TILE) >> 4), max(nv, 1), t > 0);
@@ -401,6 +435,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
             tc_fence_after();
             tmem_dealloc(tmem, 512);
         }
+        // (where lanes share pieces, one may have cleared what the other would have found)
+        if (role == 2 && (cleared[L] || (pairs && cleared[L ^ 1])))
+            for (Piece p = first_piece(); p.n > 0; p = next_piece(p)) mend<DH>(a, p, worker, pairs ? L * 128 : 0, lane);
         return;
     }
 

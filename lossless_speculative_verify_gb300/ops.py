@@ -316,8 +316,8 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
 
     Any strides but the last (k and v alike), so that q, k and v may be parts of one projection's output. heads is
     a multiple of kv_heads; dh 16, 32, 64 or 128. Rows of no sequence may hold anything; they are left as they were
-    in ``out``, and zero where none is given. Returns out [tokens, heads, dh], or [out, lse fp32 [tokens, heads]],
-    whose rows of no sequence are -inf."""
+    in ``out``, and zero where none is given. Returns out [tokens, heads, dh], or [out,
+    lse fp32 [tokens, heads]], whose rows of no sequence are -inf."""
     dev = _device("q", q)
     _need(q.dim() == 3 and q.dtype in _DT, "q: want fp32 or bf16 [tokens, heads, dh]")
     N, H, dh = q.shape

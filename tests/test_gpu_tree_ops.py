@@ -240,6 +240,30 @@ def test_prompt_runs_of_infinities(evs):
     check((o[2000:], lse[2000:]), ref.prompt(q[2000:], k[2000:], v[2000:], [0, 2000]), BF16, 128, 4000)
 
 
+@pytest.mark.parametrize("dtype,dh", [(BF16, 128), (BF16, 64), (F32, 64), (BF16, 32), (F32, 16)])
+@pytest.mark.parametrize("lens,H", [([700, 33], 2), ([3000], 1), ([130], 40), ([257], 1)], ids=str)
+def test_prompt_values_that_are_not_finite(evs, dtype, dh, lens, H):
+    """Infinities and NaN in V reach the rows that read them, and no other: those are what they are without them."""
+    d = make_prompt(78, dtype, lens, H, 1, dh)
+    q, k, v = (d[x].contiguous().clone() for x in "qkv")
+    n = lens[0]
+    bad = {5: (0, math.inf), n - 3: (dh - 1, NAN), n // 2: (dh // 2, -math.inf), min(n - 1, 129): (3, math.inf), n - 20: (3, -math.inf)}
+    clean = evs.prompt_attention(q, k, v, i32(d["starts"]), return_lse=True)
+    for j, (c, x) in bad.items():
+        v[j, 0, c] = x
+    o, lse = evs.prompt_attention(q, k, v, i32(d["starts"]), return_lse=True)
+    assert torch.equal(lse, clean[1])
+    want = clean[0].float()
+    hit = torch.zeros_like(want, dtype=torch.bool)
+    for j, (c, x) in bad.items():
+        want[j:n, :, c] += x                                         # a later one of the other sign: NaN
+        hit[j:n, :, c] = True
+    assert torch.equal(torch.isnan(o), torch.isnan(want)) and torch.equal(torch.isinf(o), torch.isinf(want))
+    assert torch.equal(o[torch.isinf(o)].float(), want[torch.isinf(want)])
+    # (a cleared value leaves other values of its row in the sums: the rest is the same to the last bit)
+    assert torch.equal(o[~hit], clean[0][~hit])
+
+
 def test_prompt_refusals(evs):
     d = make_prompt(12, BF16, [20], 4, 2, 64)
     q, k, v, s = d["q"], d["k"], d["v"], i32([0, 20])
@@ -507,6 +531,34 @@ def test_tree_keeps_to_its_workspace(evs, case):
         torch.cuda.synchronize()
         assert (ws[n:] == 0x5a).all()
         check((o, lse), want_tree(dict(d, cached=lens)), dtype, dh, S + T)
+
+
+@pytest.mark.parametrize("dtype,dh,T,H", [(BF16, 128, 128, 2), (BF16, 64, 100, 4), (BF16, 128, 30, 2), (BF16, 64, 7, 2),
+                                          (F32, 32, 40, 2), (F32, 16, 5, 2), (BF16, 16, 20, 2)])
+@pytest.mark.parametrize("own", [True, False], ids=["nodes", "cache"])
+def test_tree_values_that_are_not_finite(evs, dtype, dh, T, H, own):
+    """A node's V that is not finite reaches the nodes below it alone."""
+    cached = [300, 0, 77]
+    d = make_tree(79, dtype, T, H, 1, dh, 300 + T, cached)
+    vn = d["vn"]
+    if not own:
+        for b, m in enumerate(cached):
+            d["kc"][b, :, m:m + T], d["vc"][b, :, m:m + T] = d["kn"][b], d["vn"][b]
+        d["kn"] = d["vn"] = None
+    clean = run_tree(evs, d)
+    bad = {0: (1, NAN), T // 2: (dh - 1, math.inf), T - 1: (2, -math.inf), T // 3: (2, math.inf)}
+    want, hit = clean[0].float(), torch.zeros_like(clean[0], dtype=torch.bool)
+    for b in (0, 1):
+        sees = ref.ancestry(d["parents"][b], T).cuda()
+        for j, (c, x) in bad.items():
+            (vn[b, :, j] if own else d["vc"][b, :, cached[b] + j])[:, c] = x
+            want[b, sees[:, j], :, c] += x
+            hit[b, sees[:, j], :, c] = True
+    o, lse = run_tree(evs, d)
+    assert torch.equal(lse, clean[1])
+    assert torch.equal(torch.isnan(o), torch.isnan(want)) and torch.equal(torch.isinf(o), torch.isinf(want))
+    assert torch.equal(o[torch.isinf(o)].float(), want[torch.isinf(want)])
+    assert torch.equal(o[~hit], clean[0][~hit])
 
 
 def test_tree_refusals(evs):
