@@ -5,7 +5,14 @@
 // On the tensor cores an item is 256 query rows of one head of one sequence, 128 for each lane (see
 // attn_tiles.cuh), and the K/V tiles up to its diagonal, which TMA brings once for both. A persistent grid
 // takes the items in the order of their length, longest first, forwards and backwards in turn, so that the
-// CTAs end together: lengths are on the device, and each role of a CTA walks the same order by itself.
+// CTAs end together: lengths are on the device, and each role of a CTA walks the same order by itself. Few
+// items are dealt in runs of tiles instead.
+// Warps 0-15: softmax and output; 16: TMA of K and V; 17 and 18: Q and the scores of the lanes; 19 and 20: P V;
+// 21-23 look through V.
+//
+// Measured, bf16, heads of 128: 32768 tokens x 8 heads 1.30 ms (1.7 PFLOP/s; 0.92 us for a tile of 80 keys x 256
+// rows, 0.82 with the products alone), 8192 x 8 100 us (256 items on 152 SMs), 13 prompts of 16381 tokens x 32
+// heads 205 us (an item's start and end about 2.5 us, and a third of its tiles' work is on the diagonal).
 #include "attn_simt.cuh"
 #include "attn_tiles.cuh"
 

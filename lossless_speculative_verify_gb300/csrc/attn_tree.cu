@@ -8,6 +8,10 @@
 // the heads that share it (row r = node * group + head in the group), its keys the cached rows in tiles
 // and then the nodes in one or two more, masked by ancestry. The segments' tiles laid end to end make an
 // axis that workers take in equal runs, so ragged lengths balance on the device; a run may cross segments.
+//
+// Measured, bf16, heads of 128: 64 single tokens x 32 heads of 8 K/V heads over up to 4096 rows 104 us (its K/V at
+// 6.5 TB/s), 4 x 41 nodes x 32 heads over up to 32768 rows 200 us (6.7 TB/s), 16 x 60 nodes x 32 heads of 8 over up
+// to 8192 rows 82 us, of which the join is 10.
 #include "attn_simt.cuh"
 #include "attn_tiles.cuh"
 
