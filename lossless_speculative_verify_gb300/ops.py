@@ -385,11 +385,13 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
           "head dimension 16, 32, 64 or 128, at most 1024 heads, a multiple of kv_heads")
     _need(1 <= T <= 128 and B <= 1024 and S <= 1 << 30, "at most 1024 sequences, 1 to 128 nodes, 2**30 rows")
     cs = _kv("cache", k_cache, v_cache, dt, (B, G, S, dh), dev)
+    _need(S <= 1 or cs[2] >= dh, "k_cache: rows overlap")
     _need((k_nodes is None) == (v_nodes is None), "k_nodes and v_nodes go together")
     n_row = n_head = n_seq = 0
     if k_nodes is not None:
         ns = _kv("nodes", k_nodes, v_nodes, dt, (B, G, T, dh), dev)
         n_row, n_head, n_seq = (ns[2] if T > 1 else dh), ns[1], ns[0]
+        _need(n_row >= dh, "k_nodes: rows overlap")
     else:
         _need(S > 0, "nodes in the cache want a capacity")
     _need(isinstance(parents, torch.Tensor) and parents.shape in ((B, T), (T,)), "parents: want [batch, nodes] or [nodes]")
@@ -438,7 +440,7 @@ def token_logprobs(logits, tokens, *, temperature=None, top=0, return_entropy=Fa
           "tokens: want int32 [rows] or [rows, n]")
     n = tokens.shape[1] if tokens.dim() == 2 else 1
     _need(n <= 1 << 20, "tokens: at most 2**20 a row")
-    _need(0 <= top <= min(64, V), "top: 0 to 64, at most the vocabulary")
+    _need(isinstance(top, int) and 0 <= top <= min(64, V), "top: 0 to 64, at most the vocabulary")
     f32 = torch.float32
     tok = _vec("tokens", tokens, torch.int32, tokens.shape, dev)
     logprob = torch.empty(tokens.shape, dtype=f32, device=dev)

@@ -579,6 +579,8 @@ def test_tree_refusals(evs):
                 lambda: f(q, kc, vc, n, par, kn[:, :, :4], vn[:, :, :4]), lambda: f(q, kc, vc.transpose(0, 1).contiguous().transpose(0, 1), n, par, kn, vn),
                 lambda: f(q, kc, vc, n, par, kn, vn, out=q.float()), lambda: f(q, kc, vc, n, par, kn, vn, out=q[0]),
                 lambda: f(q.transpose(1, 2).contiguous().transpose(1, 2), kc, vc, n, par, kn, vn),
+                lambda: f(q, kc[:, :, :1].expand(2, 2, 30, 64), vc[:, :, :1].expand(2, 2, 30, 64), n, par, kn, vn),
+                lambda: f(q, kc, vc, n, par, kn[:, :, :1].expand(2, 2, 5, 64), vn[:, :, :1].expand(2, 2, 5, 64)),
                 lambda: f(q, kc.clone().requires_grad_(), vc, n, par, kn, vn)):
         with pytest.raises(ValueError):
             bad()
@@ -719,7 +721,7 @@ def test_logprob_refusals(evs):
     l, tok = make_logits(1, 3, 40, F32), i32([[1, 2]] * 3)
     f = evs.token_logprobs
     for bad in (lambda: f(l[0], tok), lambda: f(l.half(), tok), lambda: f(l.t().contiguous().t(), tok), lambda: f(l, tok[:2]),
-                lambda: f(l, tok.long()), lambda: f(l, tok, top=41), lambda: f(l, tok, top=-1), lambda: f(l.cpu(), tok),
+                lambda: f(l, tok.long()), lambda: f(l, tok, top=41), lambda: f(l, tok, top=2.0), lambda: f(l, tok, top=-1), lambda: f(l.cpu(), tok),
                 lambda: f(torch.zeros(3, 100, device="cuda"), tok, top=65), lambda: f(l, tok.cpu()),
                 lambda: f(l, tok, temperature=torch.ones(3, device="cuda").double()), lambda: f(l, tok[:, ::2]),
                 lambda: f(l, tok, temperature=torch.ones(2, device="cuda")), lambda: f(l, None),
