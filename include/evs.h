@@ -514,8 +514,9 @@ evs_status evs_token_logprobs(const evs_logprob_args* args, void* stream);
  * zero_rest is zero, and lse is -inf. Starts are made to ascend within [0, tokens] (EVS_FLAG_BAD_LEN where
  * they did not). A query whose every score is -inf gives o = 0 and lse = -inf; one whose kernel gave up a
  * bounded wait gives NaN for both (EVS_FLAG_TIMEOUT). Types, statistics and weights as in
- * evs_shared_attention. A value of V that is not finite shows in the rows that read it, and in no other. How the keys are dealt, and with it the last bits,
- * goes by tokens, batch and heads. */
+ * evs_shared_attention. A value of V that is not finite shows in the rows that read it (0 times it, where their
+ * weights of it are 0, may be NaN, even in a row whose every score is -inf), and in no other. How the keys are
+ * dealt, and with it the last bits, goes by tokens, batch and heads. */
 typedef struct {
     int32_t tokens, batch;               /* rows of the buffers, sequences (<= 1024)        */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
@@ -548,7 +549,8 @@ evs_status evs_prompt_attention(const evs_prompt_attn_args* args, void* stream);
  * The nodes' K/V lie in k_nodes / v_nodes, or (both NULL) in the cache behind the readable rows, row
  * cache_len[b] + j; rows past the capacity are left out (EVS_FLAG_KV_OVERFLOW). Lengths outside [0,
  * capacity] are clamped (EVS_FLAG_BAD_LEN). Rows that no query reads may hold anything, and a
- * node's V that is not finite shows in the nodes below it alone. Everything else as in evs_shared_attention. */
+ * node's V that is not finite shows in that node and those below it alone (as in evs_prompt_attention).
+ * Everything else as in evs_shared_attention. */
 typedef struct {
     int32_t batch, nodes;                /* 1 .. 1024 sequences, 1 .. 128 nodes             */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */

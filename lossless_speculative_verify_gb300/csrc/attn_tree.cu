@@ -420,6 +420,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
                     if (p.t0 + t >= p.ntc && scan_rows<DH>(tile, 0, min(nv, KEYS), 0, 1, lane)) {
                         cleared[L] = 1;
                         clear_values<DH>(tile, 0, min(nv, KEYS), 0, 1, lane);
+                    } else if (pairs && p.t0 + t >= p.ntc) {
+                        // zeros that the other lane's warp wrote and this one read are for this lane's products, too
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                     if (!all_wait(&p_full[2 * L + (cnt & 1u)], cnt >> 1 & 1u)) { ok = false; break; }
                     tc_fence_after();
