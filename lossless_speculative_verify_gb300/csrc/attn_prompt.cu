@@ -739,7 +739,7 @@ bool tensor_ok(const evs_prompt_attn_args& c) {
 // Whether items are dealt in runs: where the longest of them would end far behind the mean of the SMs, if the
 // sequences were of one length (the lengths are on the device). Runs cost their own starts, partials and a launch:
 // 256 items of 8192 tokens, 54 units apart, 104 us in runs and 98 whole; 700 tokens x 8 heads (56) 19 and 14; 2048
-// tokens x 8 heads (109) 25.5 and 29.6; 4096 (145) 42 and 52; 16384 x 2 heads 97 and 180.
+// tokens x 8 heads (109) 24.6 and 29.6; 4096 (145) 43 and 52; 16384 x 2 heads 104 and 180.
 constexpr int RUNS_WORTH = 80;
 bool use_runs(const evs_prompt_attn_args& c) {
     if (c.dtype != EVS_DTYPE_BF16 || (c.head_dim != 64 && c.head_dim != 128)) return false;

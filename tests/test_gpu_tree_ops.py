@@ -229,6 +229,25 @@ def test_prompt_in_runs(evs, case):
     assert torch.equal(view[3:3 + n], a[0][3:3 + n]) and torch.equal(c[1], a[1])
 
 
+@pytest.mark.parametrize("dtype,dh,N,H,starts", [
+    (BF16, 128, 2000, 2, [5, 5]), (BF16, 64, 2000, 2, [0, 0, 0]), (BF16, 128, 300, 64, [300, 300]), (F32, 16, 90, 2, [7, 7, 7, 7]),
+    (BF16, 128, 2000, 2, [9, 9, 10, 10, 10]), (BF16, 64, 300, 64, [0, 0, 1, 1]), (F32, 64, 70, 1, [69, 69, 70])], ids=str)
+def test_prompt_without_rows(evs, dtype, dh, N, H, starts):
+    """Sequences of no rows, or of one, which reads itself: its V."""
+    g = gen(N + H)
+    q, k, v = (randn(g, N, H, dh, dtype=dtype) for _ in range(3))
+    flags = i32([0])
+    for _ in range(2):
+        o, lse = evs.prompt_attention(q, k, v, i32(starts), return_lse=True, flags=flags)
+        one = torch.zeros(N, dtype=torch.bool, device="cuda")
+        one[starts[0]:starts[-1]] = True
+        assert torch.equal(o[one], v[one]) and (o[~one] == 0).all()
+        assert torch.isfinite(lse[one]).all() and torch.isneginf(lse[~one]).all() and flags.item() == 0
+    out = torch.full_like(q, 2.0)
+    evs.prompt_attention(q, k, v, i32(starts), out=out)
+    assert torch.equal(out[one], v[one]) and (out[~one] == 2.0).all()
+
+
 def test_prompt_runs_of_infinities(evs):
     """Partials of a row without any score: the first 2000 keys are -inf for all, the first 2000 rows read nothing else."""
     d = make_prompt(77, BF16, [4000], 1, 1, 128)
@@ -399,6 +418,22 @@ def test_tree_lengths(evs, dtype, dh, T):
     bad = dict(d, lens=[T + 5, 1, -3, T - 1, 17], cached=[301, -1, 129, 16, 250])
     again = run_tree(evs, bad, flags=flags)
     assert flags.item() == 32 and same(again, got)
+
+
+@pytest.mark.parametrize("dtype,dh,T,S,own", [(BF16, 128, 20, 300, True), (BF16, 64, 128, 300, True), (BF16, 128, 1, 40, False),
+                                              (F32, 16, 7, 100, True), (F32, 64, 40, 2000, False), (BF16, 64, 90, 0, True)])
+def test_tree_without_nodes(evs, dtype, dh, T, S, own):
+    """Trees that are all empty, and then but the last, of one node."""
+    d = make_tree(8, dtype, T, 4, 2, dh, S, [S // 2, 0, S // 3], nodes=own)
+    for last in (0, 1):
+        d["lens"] = [0, 0, last]
+        flags = i32([0])
+        got = run_tree(evs, d, flags=flags)
+        check(got, want_tree(d), dtype, dh, S + T)
+        assert flags.item() == 0 and (got[0][:2] == 0).all() and torch.isneginf(got[1][:2]).all()
+        out = torch.full_like(d["q"], 5.0)
+        o, _ = run_tree(evs, d, out=out)
+        assert (o[:2] == 5.0).all() and (o[2, last:] == 5.0).all() and torch.equal(o[2, :last], got[0][2, :last])
 
 
 @pytest.mark.parametrize("dtype,dh", [(BF16, 128), (F32, 32)])
