@@ -14,8 +14,8 @@
 // border (its leading bits, found by counting) are ranked by one warp in registers. Where more than 256 do,
 // as among equal logits, every warp keeps a sorted list and the lists are joined. No order of execution shows.
 //
-// Measured (replayed graphs): 13 x 512 fp32 2.6 us, 208 x 4096 with eight alternatives 7.6, 64 x 50021 bf16 with
-// 20 11.6, 512 x 131072 fp32 with five 58 (4.6 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
+// Measured (replayed graphs): 13 x 512 fp32 2.2 us, 208 x 4096 with eight alternatives 6.8, 64 x 50021 bf16 with
+// 20 10.9, 512 x 131072 fp32 with five 54 (4.9 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
 // place on an SM a fifth of it, start and ranking about 10).
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
