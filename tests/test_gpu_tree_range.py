@@ -1,0 +1,110 @@
+"""Prompt attention, tree attention and token log probabilities at the far ends of the ranges that they take.
+
+Tolerances count roundings, as in the tests of the same operators at small sizes."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import tree_reference as ref
+from test_gpu_tree_ops import BF16, F32, NAN, RUNS, U, check, evs, gen, i32, make_prompt, make_tree, randn  # noqa: F401
+from test_gpu_tree_ops import run_prompt, run_tree, same, want_tree
+
+pytestmark = pytest.mark.gpu
+FAR = 1 << 31
+
+
+def offset_of(t, *at):
+    """Elements from the tensor's first to the one at these indices."""
+    return sum(i * s for i, s in zip(at, t.stride()))
+
+
+# ---- offsets -----------------------------------------------------------------------------------
+def test_tree_tensor_maps_past_32_bits(evs):  # noqa: F811
+    """The ninth sequence of a cache begins 2^31 elements into it."""
+    B, G, S, dh, T, H = 9, 2, 1 << 20, 128, 3, 4
+    kc, vc = (torch.empty(B, G, S, dh, dtype=BF16, device="cuda") for _ in range(2))     # 4.8 GB each
+    assert offset_of(kc, 8, 0, 0, 0) >= FAR
+    small = make_tree(1, BF16, T, H, G, dh, 500, [500], nodes=False)
+    small["cached"], small["parents"] = [500 - T], [[-1, 0, 0]]
+    kc[8, :, :500], vc[8, :, :500] = small["kc"][0], small["vc"][0]
+    kc[:8, :, 0], vc[:8, :, 0] = 0.0, 0.0
+    q = torch.zeros(B, T, H, dh, dtype=BF16, device="cuda")
+    q[8] = small["q"][0]
+    lens, cached, parents = i32([1] * 8 + [T]), i32([0] * 8 + [500 - T]), i32([-1, 0, 0])
+
+    def last(kn=None, vn=None):
+        o, lse = evs.tree_attention(q, kc, vc, cached, parents, kn, vn, lens=lens, return_lse=True)
+        assert (o[:8] == 0).all()
+        return o[8:], lse[8:]
+
+    want = want_tree(small)
+    in_cache = last()
+    check(in_cache, want, BF16, dh, 500)
+    # the nodes' own K/V: rows of the same tensors, as far apart
+    kn, vn = (t[:, :, 500 - T:500] for t in (kc, vc))
+    kn[:8], vn[:8] = 0.0, 0.0
+    assert same(last(kn, vn), in_cache)
+    # values that are not finite are added where they belong by the kernel's own addresses
+    vc[8, 1, 500 - T + 1, 7] = NAN
+    for o, lse in (last(), last(kn, vn)):
+        hit = torch.zeros_like(o, dtype=torch.bool)
+        hit[0, 1, 2:, 7] = True
+        assert torch.equal(torch.isnan(o), hit) and torch.equal(o[~hit], in_cache[0][~hit]) and torch.equal(lse, in_cache[1])
+
+
+@pytest.mark.parametrize("dtype,dh", [(F32, 16), (BF16, 32), (BF16, 128)])
+@pytest.mark.parametrize("T", [1, 20])
+def test_tree_cuda_cores_past_32_bits(evs, dtype, dh, T):  # noqa: F811
+    """Rows of 2^18 elements, where what is behind row 8191 is past 2^31; sequences of 2^30 elements. Rows off 16 bytes
+    keep heads of 128 on the CUDA cores."""
+    H, G, S = 4, 2, 8700
+    odd = 1 if dh == 128 else 0
+    buf = torch.empty(S << 18, dtype=dtype, device="cuda")
+
+    def view(at, B, s, row, head, seq):
+        return buf[at:].as_strided((B, G, s, dh), (seq, head, row, 1))
+
+    d = make_tree(T, dtype, T, H, G, dh, S, [S - T], nodes=False)
+    kc, vc = (view(at, 1, S, 1 << 18, 512, 1 << 30) for at in (odd, 2048 + odd))
+    assert offset_of(kc, 0, 0, S - T, 0) > FAR
+    kc.copy_(d["kc"])
+    vc.copy_(d["vc"])
+    far = dict(d, kc=kc, vc=vc)
+    check(run_tree(evs, far), want_tree(d), dtype, dh, S)
+    # and the nodes' own rows there
+    own = dict(d, kn=d["kc"][:, :, S - T:], vn=d["vc"][:, :, S - T:])
+    check(run_tree(evs, dict(far, kn=kc[:, :, S - T:], vn=vc[:, :, S - T:])), want_tree(own), dtype, dh, S)
+    # sequences
+    d = make_tree(T + 1, dtype, T, H, G, dh, 130 + T, [77, 0, 130], nodes=False)
+    kc, vc = (view(at, 3, 130 + T, 1 << 10, 512, 1 << 30) for at in (odd, (1 << 20) + odd))
+    assert offset_of(kc, 2, 0, 0, 0) >= FAR
+    kc.copy_(d["kc"])
+    vc.copy_(d["vc"])
+    check(run_tree(evs, dict(d, kc=kc, vc=vc)), want_tree(d), dtype, dh, 130 + T)
+
+
+@pytest.mark.parametrize("dtype,dh,odd", [(F32, 16, 0), (BF16, 16, 0), (BF16, 128, 1), (BF16, 128, 0), (BF16, 64, 0)])
+@pytest.mark.parametrize("empty", [0, 63])
+def test_prompt_past_32_bits(evs, dtype, dh, odd, empty):  # noqa: F811
+    """Rows of 2^18 elements of q, k, v and out, read and written behind 2^31; on CUDA cores, in whole items (with empty
+    sequences before it) and in runs of tiles. Values that are not finite among the last rows."""
+    N, H, G, n = 9000, 2, 1, 300
+    d = make_prompt(dh, dtype, [n], H, G, dh)
+    big = torch.empty(N, 1 << 18, dtype=dtype, device="cuda")
+    part = lambda at, heads: big[:, at + odd:at + odd + heads * dh].unflatten(1, (heads, dh))  # noqa: E731
+    q, k, v, out = part(0, H), part(512, G), part(1024, G), part(2048, H)
+    at = N - n
+    assert offset_of(q, at, 0, 0) > FAR and offset_of(out, at, 0, 0) > FAR
+    q[at:], k[at:], v[at:] = d["q"], d["k"], d["v"]
+    starts = i32([at] * (empty + 1) + [N])
+    o, lse = evs.prompt_attention(q, k, v, starts, out=out, return_lse=True)
+    clean = o[at:].clone()
+    check((clean, lse[at:]), ref.prompt(d["q"], d["k"], d["v"], d["starts"]), dtype, dh, n)
+    v[N - 5, 0, 3], v[at + 40, 0, dh - 1] = math.inf, NAN
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    hit[n - 5:, :, 3] = hit[40:, :, dh - 1] = True
+    again, _ = evs.prompt_attention(q, k, v, starts, out=out, return_lse=True)
+    again = again[at:]
+    assert torch.equal(~torch.isfinite(again), hit) and torch.equal(again[~hit], clean[~hit])
