@@ -108,3 +108,55 @@ def test_prompt_past_32_bits(evs, dtype, dh, odd, empty):  # noqa: F811
     again, _ = evs.prompt_attention(q, k, v, starts, out=out, return_lse=True)
     again = again[at:]
     assert torch.equal(~torch.isfinite(again), hit) and torch.equal(again[~hit], clean[~hit])
+
+
+# ---- many keys ---------------------------------------------------------------------------------
+def measures(n, dh, dtype):
+    """V [n, dh] whose column c is 1 for the c-th part of the keys: an output is the weights that such a part has, all of
+    one sign, so that a tile or a partial that is left out, or taken twice, shows in a column by far more than its
+    tolerance."""
+    j = torch.arange(n, device="cuda")
+    v = torch.zeros(n, dh, device="cuda", dtype=dtype)
+    v[j, j * dh // n] = 1.0
+    return v
+
+
+LONG = [
+    (BF16, 1, 32, 8, 128, 50000, [50000, 20011, 3]), (BF16, 1, 8, 8, 64, 20480, [20480, 20479]), (BF16, 1, 2, 1, 128, 49999, [49999]),
+    (BF16, 41, 8, 8, 128, 32768, [32768, 20001]), (BF16, 60, 16, 4, 128, 24000, [24000, 23999, 77]), (BF16, 100, 8, 1, 64, 20001, [20001]),
+    (BF16, 5, 4, 2, 32, 20000, [20000, 7]), (F32, 1, 4, 2, 64, 20000, [20000, 19937]), (F32, 9, 4, 4, 128, 20000, [20000]),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: ("b" if c[0] == BF16 else "f") + "-" + "-".join(map(str, c[1:6])))
+def test_tree_over_long_caches(evs, case):  # noqa: F811
+    dtype, T, H, G, dh, S, cached = case
+    d = make_tree(S + T, dtype, T, H, G, dh, S, cached)
+    a = run_tree(evs, d)
+    check(a, want_tree(d), dtype, dh, S + T)
+    assert same(a, run_tree(evs, d))
+    for b, m in enumerate(cached):
+        d["vc"][b, :, :m] = measures(m, dh, dtype)
+    d["vn"][:] = measures(T, dh, dtype)
+    check(run_tree(evs, d), want_tree(d), dtype, dh, S + T)
+
+
+PACKED = [
+    # one long prompt beside short requests, before and behind; whole items and runs of tiles
+    ([16384] + [24] * 7, 2, 1, 128), ([24] * 15 + [16384], 2, 2, 128), ([8192, 512, 512, 512, 512], 4, 2, 128), ([20001], 1, 1, 128),
+    ([9000, 300, 5000], 16, 4, 128), ([33, 7000, 1, 0, 6000], 12, 4, 64), ([16385], 2, 1, 64), ([24] * 40 + [12000], 3, 3, 64),
+    ([3000, 40], 4, 2, 32),
+]
+
+
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: "_".join(map(str, c[0][:3])) + f"-{len(c[0])}-{c[1]}-{c[3]}")
+def test_prompt_over_many_rows(evs, case):  # noqa: F811
+    lens, H, G, dh = case
+    d = make_prompt(sum(lens) + dh, BF16, lens, H, G, dh)
+    a = run_prompt(evs, d)
+    check(a, ref.prompt(d["q"], d["k"], d["v"], d["starts"]), BF16, dh, max(lens))
+    assert same(a, run_prompt(evs, d))
+    for s, n in zip(d["starts"], lens):
+        if n:
+            d["v"][s:s + n] = measures(n, dh, BF16)[:, None]
+    check(run_prompt(evs, d), ref.prompt(d["q"], d["k"], d["v"], d["starts"]), BF16, dh, max(lens))
