@@ -160,3 +160,47 @@ def test_prompt_over_many_rows(evs, case):  # noqa: F811
         if n:
             d["v"][s:s + n] = measures(n, dh, BF16)[:, None]
     check(run_prompt(evs, d), ref.prompt(d["q"], d["k"], d["v"], d["starts"]), BF16, dh, max(lens))
+
+
+# ---- a prompt's workspace ----------------------------------------------------------------------
+IN_RUNS = [c for c in RUNS if len(c[0]) < 6] + [([0, 6000, 0, 1, 0, 5999], 1, 1, 128), ([300] * 5 + [9000], 1, 1, 64)]
+STARTS = {
+    "as given": lambda s, N: s,
+    "one sequence": lambda s, N: [0] * (len(s) - 1) + [N],
+    "the first": lambda s, N: [0] + [N] * (len(s) - 1),
+    "empty": lambda s, N: [N // 2] * len(s),
+    "out of order": lambda s, N: [N // 3] + [N + 7, -5, 0, N // 2] * len(s),
+}
+
+
+@pytest.mark.parametrize("how", STARTS)
+@pytest.mark.parametrize("case", IN_RUNS, ids=lambda c: "_".join(map(str, c[0][:4])) + f"-{c[1]}-{c[3]}")
+def test_prompt_keeps_to_its_workspace(evs, case, how):  # noqa: F811
+    """The bytes asked for and no others, whatever the lengths on the device are."""
+    from lossless_speculative_verify_gb300 import _lib
+    lens, H, G, dh = case
+    d = make_prompt(sum(lens) + H, BF16, lens, H, G, dh, before=3, behind=5)
+    N, B, lib = d["q"].shape[0], len(lens), evs.load()
+    at = STARTS[how](d["starts"], N)[:B + 1]
+    starts, p = i32(at), lambda t: t.data_ptr()  # noqa: E731
+    q, k, v = d["q"], d["k"], d["v"]
+    o, lse = torch.full((N, H, dh), 5.0, dtype=BF16, device="cuda"), torch.empty(N, H, device="cuda")
+    a = _lib.PromptAttnArgs(tokens=N, batch=B, heads=H, kv_heads=G, head_dim=dh, dtype=1, zero_rest=1, q=p(q),
+                            q_row=q.stride(0), q_head=q.stride(1), k=p(k), v=p(v), kv_row=k.stride(0), kv_head=k.stride(1),
+                            starts=p(starts), o=p(o), o_row=H * dh, lse=p(lse))
+    n = lib.evs_prompt_attention_workspace(ctypes.byref(a))
+    assert n > 0
+    ws = torch.full((n + 65536,), 0xff, dtype=torch.uint8, device="cuda")        # NaN, if it is read before it is written
+    a.workspace, a.ws_bytes = p(ws), n
+    assert lib.evs_prompt_attention(ctypes.byref(a), None) == 0
+    torch.cuda.synchronize()
+    assert (ws[n:] == 0xff).all()
+    read, run = [], 0
+    for x in at:
+        run = max(run, min(max(x, 0), N))
+        read.append(run)
+    want = ref.prompt(q, k, v, read)
+    check((o, lse), want, BF16, dh, N)
+    rest = torch.ones(N, dtype=torch.bool)
+    rest[read[0]:read[-1]] = False
+    assert (o[rest] == 0).all() and torch.isneginf(lse[rest]).all()

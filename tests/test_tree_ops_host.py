@@ -88,6 +88,24 @@ def test_prompt_empty_and_null(L):
     assert _prompt(L, tokens=0, q=None) == OK and _prompt(L, tokens=0, batch=0) == OK
 
 
+def test_prompt_workspace(L):
+    """Sizes whose items are dealt in runs of tiles need one; it follows neither the addresses nor the lengths."""
+    lib = L.load()
+    base = dict(tokens=2048, batch=1, heads=8, kv_heads=8, head_dim=128, dtype=1, q_row=1024, q_head=128, kv_row=1024,
+                kv_head=128, o_row=1024)
+    size = lambda **kw: lib.evs_prompt_attention_workspace(C.byref(L.PromptAttnArgs(**{**base, **kw})))  # noqa: E731
+    n = size()
+    # partials of two slots for each of 152 workers: 256 rows of outputs, maxima and sums; a job of each worker
+    assert n >= 2 * 152 * 256 * (128 + 2) * 4 + 152 * 32 and n == size(q=P + 2, k=P + 2, q_row=1 << 20)
+    assert _prompt(L, **base, workspace=None, ws_bytes=n) == INV
+    assert _prompt(L, **base, workspace=P + 16, ws_bytes=n) == INV
+    assert _prompt(L, **base, workspace=P, ws_bytes=n - 1) == CAP and _prompt(L, **base, workspace=P) == CAP
+    # none is needed, or the sizes are none
+    assert size(tokens=10) == 0 and size(tokens=0) == 0 and size(dtype=0) == 0 and size(head_dim=32) == 0
+    assert size(head_dim=48) == 0 and size(heads=6, kv_heads=4) == 0 and size(batch=0) == 0
+    assert lib.evs_prompt_attention_workspace(None) == 0
+
+
 def _tree(L, **kw):
     base = dict(batch=2, nodes=5, heads=8, kv_heads=4, head_dim=64, dtype=1, capacity=50, q=P, q_ld=512, k_cache=P,
                 v_cache=P, cache_row=64, cache_head=3200, cache_seq=12800, cache_len=P, parents=P, parents_seq=5,
