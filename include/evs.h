@@ -490,7 +490,8 @@ evs_status evs_selective_scan(const evs_scan_args* args, void* stream);
  * mass. A temperature that is not above zero puts all mass on the first largest token; one above 1e30 is
  * taken as 1e30. Places of top behind the last token that is not ruled out hold id -1 and -inf. A given id
  * outside [0, vocab) has -inf (EVS_FLAG_BAD_TOKEN); a row with every token ruled out has -inf, entropy 0,
- * ids -1 (EVS_FLAG_EMPTY_ROW). Sums are fp32 over a running maximum; the ids are exact. */
+ * ids -1 (EVS_FLAG_EMPTY_ROW). Sums are fp32 over a running maximum, and carry along what their additions
+ * lose; the ids are exact. */
 typedef struct {
     int32_t rows, vocab;         /* at most 2^24 each                                       */
     int32_t n_tokens, top;       /* given tokens a row; largest ones, at most 64 and vocab  */

@@ -15,7 +15,7 @@
 // as among equal logits, every warp keeps a sorted list and the lists are joined. No order of execution shows.
 //
 // Measured (replayed graphs): 13 x 512 fp32 2.2 us, 208 x 4096 with eight alternatives 6.8, 64 x 50021 bf16 with
-// 20 10.9, 512 x 131072 fp32 with five 54 (4.9 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
+// 20 10.8, 512 x 131072 fp32 with five 56 (4.8 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
 // place on an SM a fifth of it, start and ranking about 10).
 #include "evs_common.cuh"
 #include "sm100_ptx.cuh"
@@ -213,8 +213,17 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
     c.x = fminf(LP_LOG2E / t, FLT_MAX);
     c.y = c.x < FLT_MAX ? (fmaf(-c.x, t, LP_LOG2E) + LP_LOG2E_REST) / t : 0.f;
 
-    // ---- the pass
-    float m = -INFINITY, s = 0.f, w = 0.f;
+    // ---- the pass. A thread has up to 65536 tokens, and terms that are alike make every addition to a sum round the same
+    // way (off by 8e-4 of the sum with 2^24 tokens a row, where a step of the result is 1e-6): so the U E tokens that it
+    // works on at a time are added up by themselves, and their sum goes to s (w) with what the additions before lost
+    // (sums of 32 bits compensated as Kahan described): 55.7 us for 54.7 (512 x 131072); the sums alone cost nothing, and
+    // leave 2e-5.
+    float m = -INFINITY, s = 0.f, w = 0.f, s_lost = 0.f, w_lost = 0.f;
+    auto add_to = [](float& sum, float& lost, float x) {
+        const float y = x - lost, t = sum + y;
+        lost = (t - sum) - y;
+        sum = t;
+    };
     // U vectors at a time, the next ones on their way while these are worked on
     uint4 ahead[U];
     auto fetch = [&](int v0) {
@@ -239,10 +248,13 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
             if (m > -INFINITY) {
                 const float d = fmaxf(m - cm, -FLT_MAX), f = lp_exp(d, c);
                 w = f > 0.f ? fmaf(s, d, w) * f : 0.f;
+                w_lost = f > 0.f ? fmaf(s_lost, d, w_lost) * f : 0.f;
                 s *= f;
+                s_lost *= f;
             }
             m = cm;
         }
+        float part_s = 0.f, part_w = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float x[E];
@@ -251,10 +263,12 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobArgs a) {
             for (int j = 0; j < E; ++j) {
                 // -inf, NaN and what +inf leaves behind: no weight, and no NaN in w
                 const float d = fmaxf(x[j] - m, -FLT_MAX), e = lp_exp(d, c);
-                s += e;
-                w = fmaf(e, d, w);
+                part_s += e;
+                part_w = fmaf(e, d, part_w);
             }
         }
+        add_to(s, s_lost, part_s);
+        add_to(w, w_lost, part_w);
     }
     // ---- the row's statistics: the maximum of all, then every thread's sums moved to it once
     uint32_t key = lp_order(m);

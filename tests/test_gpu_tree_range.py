@@ -204,3 +204,49 @@ def test_prompt_keeps_to_its_workspace(evs, case, how):  # noqa: F811
     rest = torch.ones(N, dtype=torch.bool)
     rest[read[0]:read[-1]] = False
     assert (o[rest] == 0).all() and torch.isneginf(lse[rest]).all()
+
+
+# ---- large vocabularies ------------------------------------------------------------------------
+@pytest.mark.parametrize("R,V,dtype,kind", [
+    # eight CTAs a row; one CTA a row, whose threads have 65536 tokens each (and rows further than 2^31 elements apart)
+    (1, 1 << 24, F32, "flat"), (304, 1 << 24, BF16, "flat"), (304, 1 << 22, F32, "flat"), (3, (1 << 24) - 5, BF16, "normal"),
+    (2, 1 << 24, F32, "normal"), (304, (1 << 20) + 1, F32, "rising"), (5, 1 << 19, BF16, "flat")], ids=str)
+def test_logprob_of_many_tokens(evs, R, V, dtype, kind):  # noqa: F811
+    """Sums whose every addition rounds the same way, of tokens that are alike; of scattered ones; with a maximum that
+    grows as the row goes on."""
+    g = gen(V + R)
+    logits = torch.empty(R, V, dtype=dtype, device="cuda")
+    for r in range(R):
+        if kind == "flat":
+            # every thread sees the maximum first: then all of its terms are the same fraction of it
+            logits[r] = -0.3 - 1.2 * (r % 7)
+            logits[r].view(8, V // 8)[:, :8192] = 0.0
+        elif kind == "normal":
+            logits[r] = torch.randn(V, device="cuda", generator=g) * 2
+        else:
+            logits[r] = torch.linspace(-20.0 - r, 3.0, V, device="cuda")
+    rows = sorted({0, 1 % R, R // 2, R - 1})
+    if R == 304 and V == 1 << 24:
+        assert offset_of(logits, rows[-1], 0) > FAR
+    tok = torch.randint(0, V, (R, 2), device="cuda", generator=g).int()
+    lp, ent, tlp, tid = evs.token_logprobs(logits, tok, top=3, return_entropy=True)
+    for r in rows:
+        l = logits[r].double()
+        y = l - l.max()
+        z = float(torch.logsumexp(y, 0))
+        p = torch.exp(y - z)
+        py, pyy = float((p * -y).sum()), float((p * y * y).sum())
+        # a weight: the exponent's three roundings and the exponential's four; 32 at most added up one after another; those
+        # sums added with what each addition lost carried along, two roundings; the tree of threads, warps and CTAs. A
+        # sum that is moved to a larger maximum is rounded and scaled by such a weight, six roundings: a few times, or where
+        # the row rises once for 16 tokens of a thread, after which what was before weighs less by what it rose
+        moves = 6 * 16 if kind != "rising" else 6 / (float(l[-1] - l[0]) / (V / (256 * 16)))
+        soft = U * (3 * py + 4 + 32 + 2 + 64 + moves)
+        order = torch.sort(l, descending=True, stable=True).indices[:3]
+        assert torch.equal(tid[r].long(), order)
+        for got, ids in ((lp[r], tok[r].long()), (tlp[r], order)):
+            for a, i in zip(got.tolist(), ids.tolist()):
+                b = float(y[i]) - z
+                assert abs(a - b) <= soft + U * (4 * abs(float(y[i])) + abs(b)), (r, a, b)
+        h = z + py
+        assert abs(float(ent[r]) - h) <= 2 * soft * (1 + py) + U * (8 * pyy + 4), (r, float(ent[r]), h)
