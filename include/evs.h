@@ -523,7 +523,7 @@ typedef struct {
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
     int32_t dtype;                       /* EVS_DTYPE_* of all                              */
     int32_t zero_rest;
-    float scale;                         /* 0: 1 / sqrt(head_dim)                           */
+    float scale;                         /* 1e-30 to 1e30; 0: 1 / sqrt(head_dim)            */
     const void* q;                       /* device [tokens][heads][head_dim]                */
     int64_t q_row, q_head;
     const void *k, *v;                   /* device [tokens][kv_heads][head_dim]             */
@@ -558,7 +558,7 @@ typedef struct {
     int32_t dtype;                       /* EVS_DTYPE_* of all                              */
     int32_t capacity;                    /* rows of one sequence's cache                    */
     int32_t zero_rest;
-    float scale;                         /* 0: 1 / sqrt(head_dim)                           */
+    float scale;                         /* 1e-30 to 1e30; 0: 1 / sqrt(head_dim)            */
     const void* q;                       /* device, row b * nodes + i: heads x head_dim     */
     int64_t q_ld;
     const void *k_cache, *v_cache;       /* device [batch][kv_heads][capacity][head_dim]    */

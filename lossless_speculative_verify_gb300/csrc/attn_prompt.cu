@@ -841,7 +841,7 @@ extern "C" evs_status evs_prompt_attention(const evs_prompt_attn_args* c, void* 
     if (((uintptr_t)c->q | (uintptr_t)c->k | (uintptr_t)c->v | (uintptr_t)c->o) % es) return EVS_ERR_INVALID_ARG;
     if (c->q_row < c->head_dim || c->kv_row < c->head_dim || c->o_row < (long long)c->heads * c->head_dim) return EVS_ERR_INVALID_ARG;
     if ((c->heads > 1 && c->q_head < c->head_dim) || (c->kv_heads > 1 && c->kv_head < c->head_dim)) return EVS_ERR_INVALID_ARG;
-    if (!(c->scale >= 0.f) || isinf(c->scale) || (c->scale > 0.f && c->scale < 1e-30f)) return EVS_ERR_INVALID_ARG;
+    if (!(c->scale == 0.f || (c->scale >= 1e-30f && c->scale <= 1e30f))) return EVS_ERR_INVALID_ARG;
     const size_t need = evs_prompt_attention_workspace(c);
     if (need > 0 && (!c->workspace || (uintptr_t)c->workspace % 256)) return EVS_ERR_INVALID_ARG;
     if (c->ws_bytes < need) return EVS_ERR_CAPACITY;

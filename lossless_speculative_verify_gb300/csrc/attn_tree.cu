@@ -888,7 +888,7 @@ extern "C" evs_status evs_tree_attention(const evs_tree_attn_args* c, void* stre
     if (((uintptr_t)c->q | (uintptr_t)c->k_cache | (uintptr_t)c->v_cache | (uintptr_t)c->k_nodes | (uintptr_t)c->v_nodes |
          (uintptr_t)c->o) % es)
         return EVS_ERR_INVALID_ARG;
-    if (!(c->scale >= 0.f) || isinf(c->scale) || (c->scale > 0.f && c->scale < 1e-30f)) return EVS_ERR_INVALID_ARG;
+    if (!(c->scale == 0.f || (c->scale >= 1e-30f && c->scale <= 1e30f))) return EVS_ERR_INVALID_ARG;
     if (!c->workspace || (uintptr_t)c->workspace % 256) return EVS_ERR_INVALID_ARG;
     if (c->ws_bytes < evs_tree_attention_workspace(c)) return EVS_ERR_CAPACITY;
     return status_of(launch(*c, (cudaStream_t)stream));

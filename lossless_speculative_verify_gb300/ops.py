@@ -13,8 +13,6 @@ refused, whichever argument it is (``torch.no_grad()`` or ``detach()`` lets it i
 """
 from __future__ import annotations
 
-import math
-
 import torch
 
 from . import _lib as L
@@ -315,9 +313,9 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
     device, ascending); its row i reads its rows j <= i.
 
     Any strides but the last (k and v alike), so that q, k and v may be parts of one projection's output. heads is
-    a multiple of kv_heads; dh 16, 32, 64 or 128. Rows of no sequence may hold anything; they are left as they were
-    in ``out``, and zero where none is given. Returns out [tokens, heads, dh], or [out,
-    lse fp32 [tokens, heads]], whose rows of no sequence are -inf."""
+    a multiple of kv_heads; dh 16, 32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Rows of no sequence may
+    hold anything; they are left as they were in ``out``, and zero where none is given. Returns out [tokens, heads,
+    dh], or [out, lse fp32 [tokens, heads]], whose rows of no sequence are -inf."""
     dev = _device("q", q)
     _need(q.dim() == 3 and q.dtype in _DT, "q: want fp32 or bf16 [tokens, heads, dh]")
     N, H, dh = q.shape
@@ -347,7 +345,7 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
         _need(o_row >= H * dh, "out: rows overlap")
     else:
         o, o_row = torch.empty(N, H, dh, dtype=q.dtype, device=dev), H * dh
-    _need(scale is None or 1e-30 <= scale < math.inf, "scale: above zero")
+    _need(scale is None or 1e-30 <= scale <= 1e30, "scale: 1e-30 to 1e30")
     flag = _vec("flags", flags, torch.int32, (1,), dev)
     lse = torch.empty(N, H, dtype=torch.float32, device=dev) if return_lse else None
     if N > 0:
@@ -373,8 +371,8 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
 
     The nodes' K/V are k_nodes and v_nodes [batch, kv_heads, nodes, dh], or without them the cache's rows
     cache_len[b] + i. All fp32 or all bf16, with any strides but the last (K and V of a pair alike); heads is a
-    multiple of kv_heads; dh 16, 32, 64 or 128. Returns out [batch, nodes, heads, dh], or [out, lse fp32 [batch,
-    nodes, heads]]."""
+    multiple of kv_heads; dh 16, 32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Returns out [batch, nodes,
+    heads, dh], or [out, lse fp32 [batch, nodes, heads]]."""
     dev = _device("q", q)
     _need(q.dim() == 4 and q.dtype in _DT, "q: want fp32 or bf16 [batch, nodes, heads, dh]")
     B, T, H, dh = q.shape
@@ -404,7 +402,7 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
         o, o_ld = out, _rows4("out", out, dt, (B, T, H, dh), dev)
     else:
         o, o_ld = torch.empty(B, T, H, dh, dtype=dt, device=dev), H * dh
-    _need(scale is None or 1e-30 <= scale < math.inf, "scale: above zero")
+    _need(scale is None or 1e-30 <= scale <= 1e30, "scale: 1e-30 to 1e30")
     flag = _vec("flags", flags, torch.int32, (1,), dev)
     lse = torch.empty(B, T, H, dtype=torch.float32, device=dev) if return_lse else None
     if B > 0:

@@ -110,6 +110,25 @@ def test_prompt_past_32_bits(evs, dtype, dh, odd, empty):  # noqa: F811
     assert torch.equal(~torch.isfinite(again), hit) and torch.equal(again[~hit], clean[~hit])
 
 
+# ---- scales ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,dh", [(BF16, 128), (BF16, 64), (F32, 16)])
+def test_scales(evs, dtype, dh):  # noqa: F811
+    """From 1e-30 to 1e30, where queries of zeros still weigh all keys alike; others are refused, also those that are no
+    value of the struct's type."""
+    d = make_prompt(dh, dtype, [150], 2, 1, dh)
+    d["q"][:] = 0.0
+    t = make_tree(dh, dtype, 5, 2, 1, dh, 150, [150])
+    t["q"][:] = 0.0
+    for scale in (1e-30, 1.0, 1e30):
+        check(run_prompt(evs, d, scale=scale), ref.prompt(d["q"], d["k"], d["v"], d["starts"], scale), dtype, dh, 150)
+        check(run_tree(evs, t, scale=scale), want_tree(t, scale), dtype, dh, 155)
+    for scale in (3e38, 1e39, 1e300, 1e-31, math.inf, -1.0, 0.0, NAN):
+        with pytest.raises(ValueError):
+            run_prompt(evs, d, scale=scale)
+        with pytest.raises(ValueError):
+            run_tree(evs, t, scale=scale)
+
+
 # ---- many keys ---------------------------------------------------------------------------------
 def measures(n, dh, dtype):
     """V [n, dh] whose column c is 1 for the c-th part of the keys: an output is the weights that such a part has, all of

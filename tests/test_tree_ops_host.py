@@ -132,6 +132,13 @@ def test_tree_refuses(L, bad):
     assert L.load().evs_tree_attention(C.byref(a), None) == INV
 
 
+@pytest.mark.parametrize("scale", [1.1e30, 3e38, 1e-31, 1e-45])
+def test_scales_are_of_a_range(L, scale):
+    """In log2 units a scale near the type's largest value is an infinity, which makes a score of 0 NaN."""
+    assert _prompt(L, scale=scale) == INV
+    assert L.load().evs_tree_attention(C.byref(_tree(L, scale=scale)), None) == INV
+
+
 def test_tree_workspace(L):
     lib = L.load()
     a = _tree(L)
