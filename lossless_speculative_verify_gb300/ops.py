@@ -343,6 +343,7 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
         _need(s2 == 1 and (H == 1 or s1 == dh), "out: heads have to be contiguous")
         o_row = s0 if N > 1 else H * dh
         _need(o_row >= H * dh, "out: rows overlap")
+        _need(N == 0 or o.data_ptr() not in (k.data_ptr(), v.data_ptr()), "out: may not be k or v")
     else:
         o, o_row = torch.empty(N, H, dh, dtype=q.dtype, device=dev), H * dh
     _need(scale is None or 1e-30 <= scale <= 1e30, "scale: 1e-30 to 1e30")
@@ -400,6 +401,8 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
     q_ld = _rows4("q", q, dt, (B, T, H, dh), dev)
     if out is not None:
         o, o_ld = out, _rows4("out", out, dt, (B, T, H, dh), dev)
+        _need(B == 0 or o.data_ptr() not in (k_cache.data_ptr(), v_cache.data_ptr(), _p(k_nodes), _p(v_nodes)),
+              "out: may not be k or v")
     else:
         o, o_ld = torch.empty(B, T, H, dh, dtype=dt, device=dev), H * dh
     _need(scale is None or 1e-30 <= scale <= 1e30, "scale: 1e-30 to 1e30")

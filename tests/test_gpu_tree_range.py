@@ -129,6 +129,21 @@ def test_scales(evs, dtype, dh):  # noqa: F811
             run_tree(evs, t, scale=scale)
 
 
+def test_outputs_are_no_keys_or_values(evs):  # noqa: F811
+    """Rows of K and V are read after others of the output are written."""
+    d = make_prompt(3, BF16, [100], 2, 2, 64)
+    q, k, v, s = d["q"], d["k"].contiguous(), d["v"].contiguous(), i32(d["starts"])
+    t = make_tree(4, BF16, 6, 2, 2, 64, 6, [3, 2])
+    tree = lambda out, own=True: evs.tree_attention(  # noqa: E731
+        t["q"], t["kc"], t["vc"], i32(t["cached"]), i32(t["parents"]), *((t["kn"], t["vn"]) if own else ()), out=out)
+    for call in (lambda: evs.prompt_attention(q, k, v, s, out=k), lambda: evs.prompt_attention(q, k, v, s, out=v),
+                 lambda: tree(t["kn"].view_as(t["q"])), lambda: tree(t["vn"].view_as(t["q"])),
+                 lambda: tree(t["kc"].view_as(t["q"]), False), lambda: tree(t["vc"].view_as(t["q"]), False)):
+        with pytest.raises(ValueError, match="may not be k or v"):
+            call()
+    assert evs.prompt_attention(q, k, v, s, out=torch.empty_like(v)).shape == v.shape
+
+
 # ---- many keys ---------------------------------------------------------------------------------
 def measures(n, dh, dtype):
     """V [n, dh] whose column c is 1 for the c-th part of the keys: an output is the weights that such a part has, all of
