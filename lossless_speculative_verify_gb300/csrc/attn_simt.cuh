@@ -20,7 +20,7 @@ template <typename T, int DH, int R> struct Simt {
     static constexpr int CW = DH / 16, VEC = CW < 4 ? CW : 4, NU = CW / VEC;   // columns of a thread, in a piece, pieces
     static constexpr int PIECES = KEYS * DH / 4 / 256;   // of four columns, of a tile of K or V, a thread brings
     // V of a tile on its way while its scores are worked out, where registers allow
-    static constexpr bool AHEAD = R * DH <= 256 && DH <= 128 && !(R == 4 && DH > 64);
+    static constexpr bool AHEAD = R * DH <= 256;
     struct Smem {
         float q[ROWS][LD];
         float kv[KEYS][LD];

@@ -116,6 +116,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
 // A softmax thread: row `row` of lane `lane`, the columns of half `half`.
 template <int DH> struct SoftThread {
     static constexpr int N = tile_keys(DH) / 2;   // its scores of a tile
+    static_assert(N == 40 || N == 48, "loads and stores of a tile");
     int lane, half, row, bar;            // bar: named barrier of its 64 threads
     uint32_t s_at, p_at, o_at;           // its scores and weights of an even tile, its output columns
     float* xch;                          // [128] of its lane, for what the two threads of a row exchange
@@ -155,8 +156,7 @@ template <int DH> struct SoftThread {
         const uint32_t at = s_at + s_col(DH, tile);
         tmem_ld32(at, x);
         if constexpr (N == 40) tmem_ld8(at + 32, x + 32);
-        else if constexpr (N == 48) tmem_ld16_issue(at + 32, *reinterpret_cast<uint32_t(*)[16]>(x + 32));
-        else tmem_ld32(at + 32, x + 32);
+        else tmem_ld16_issue(at + 32, *reinterpret_cast<uint32_t(*)[16]>(x + 32));
         tmem_wait_ld();
     }
     // Scores behind the first n of the thread's: no weight
@@ -210,9 +210,8 @@ template <int DH> struct SoftThread {
             w[j] = pack2(e0, e1);
             if (j == 15) tmem_st16(to, *reinterpret_cast<const uint32_t(*)[16]>(w));
         }
-        if constexpr (N == 40) tmem_st4(to + 16, w + 16);
-        else if constexpr (N == 48) { tmem_st4(to + 16, w + 16); tmem_st4(to + 20, w + 20); }
-        else tmem_st16(to + 16, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
+        tmem_st4(to + 16, w + 16);
+        if constexpr (N == 48) tmem_st4(to + 20, w + 20);
         float l0, l1;
         unpair(add2(sum0, sum1), l0, l1);
         l += l0 + l1;
