@@ -173,27 +173,52 @@ constexpr int tree_smem(int dh, int B) { return small_smem(B) + 1024 + 2 * Q_ROW
 static_assert(tree_smem(64, 1024) <= 227 * 1024 && tree_smem(128, 1024) <= 227 * 1024, "shared memory of an SM");
 
 // Adds the values of V that are not finite, which were cleared in the piece's tiles of nodes, to the partials of the
-// rows below those nodes: the 128 of a lane from r_lane on.
+// rows below those nodes: the 128 of a lane from r_lane on. Each row is written once, with the sums over its node's path:
+// those of the node before it where that is the same node or its parent, else gone through anew (a chain of 128 nodes of
+// nothing else x 8 heads x 4 sequences: 0.16 ms, with a walk up for every node and row 75). The tree's parents and which nodes
+// have such values are kept in the warp's registers.
 template <int DH> __device__ __forceinline__ void mend(const TreeArgs& a, const Piece& p, int worker, int r_lane, int lane) {
     constexpr int KEYS = tile_keys(DH);
     const int grp = a.H / a.G, r_end = min(a.seg_rows, min(r_lane + 128, p.nodes * grp - p.rt * a.seg_rows));
+    const int64_t ld = a.kn ? a.n_row : a.c_row;
     const bf16* v = a.kn ? (const bf16*)a.vn + p.b * a.n_seq + p.g * a.n_head
                          : (const bf16*)a.vc + p.b * a.c_seq + p.g * a.c_head + p.cached * a.c_row;
     float* po = a.po + (int64_t)(worker + p.seg) * rows4(a.seg_rows) * DH;
+    uint32_t ups = 0, bad = 0;       // byte w: of node 32 w + lane; bits of nodes 32 lane ..
+#pragma unroll
+    for (int w = 0; w < MAX_NODES / 32; ++w)
+        if (32 * w + lane < p.nodes) ups |= (uint32_t)parent_of(a, p.b, 32 * w + lane, false) << 8 * w;
+    float x[DH / 32], sum[DH / 32] = {};
 #pragma unroll 1
-    for (int j = max(p.t0 - p.ntc, 0) * KEYS; j < min(p.keys, (p.t0 + p.n - p.ntc) * KEYS); ++j) {
-        float x[DH / 32];
-        if (!bad_values<DH>(v + j * (a.kn ? a.n_row : a.c_row), lane, x)) continue;
+    for (int j = max(p.t0 - p.ntc, 0) * KEYS; j < min(p.keys, (p.t0 + p.n - p.ntc) * KEYS); ++j)
+        if (bad_values<DH>(v + j * ld, lane, x) && lane == j >> 5) bad |= 1u << (j & 31);
+    if (!__any_sync(0xffffffffu, bad != 0)) return;
+    auto take = [&](int i) {
+        if (!(__shfl_sync(0xffffffffu, bad, i >> 5) >> (i & 31) & 1u)) return;
+        bad_values<DH>(v + i * ld, lane, x);
+#pragma unroll
+        for (int u = 0; u < DH / 32; ++u) sum[u] += x[u];
+    };
+    auto above = [&](int i) { return (int)(__shfl_sync(0xffffffffu, ups, i & 31) >> (i >> 5) * 8 & 0xffu) - 1; };
+    int at = -1;                         // the node that sum is of
 #pragma unroll 1
-        for (int r = r_lane; r < r_end; ++r) {
-            int i = (p.rt * a.seg_rows + r) / grp;
-            while (i > j) i = (int)parent_of(a, p.b, i, false) - 1;
-            if (i != j) continue;
+    for (int r = r_lane; r < r_end; ++r) {
+        const int node = (p.rt * a.seg_rows + r) / grp;
+        if (node != at) {
+            const int parent = above(node);
+            if (parent != at) {
+#pragma unroll
+                for (int u = 0; u < DH / 32; ++u) sum[u] = 0.f;
 #pragma unroll 1
-            for (int u = 0; u < DH / 32; ++u) {
-                const int c = lane * (DH / 32) + u;
-                if (x[u] != 0.f) po[((c >> 2) * rows4(a.seg_rows) + r) * 4 + (c & 3)] += x[u];
+                for (int i = parent; i >= 0; i = above(i)) take(i);
             }
+            take(node);
+            at = node;
+        }
+#pragma unroll
+        for (int u = 0; u < DH / 32; ++u) {
+            const int c = lane * (DH / 32) + u;
+            if (sum[u] != 0.f) po[((c >> 2) * rows4(a.seg_rows) + r) * 4 + (c & 3)] += sum[u];
         }
     }
 }

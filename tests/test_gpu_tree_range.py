@@ -9,7 +9,7 @@ import torch
 
 import tree_reference as ref
 from test_gpu_tree_ops import BF16, F32, NAN, RUNS, U, check, evs, gen, i32, make_prompt, make_tree, randn  # noqa: F401
-from test_gpu_tree_ops import run_prompt, run_tree, same, want_tree
+from test_gpu_tree_ops import run_prompt, run_tree, same, shape_of, want_tree
 
 pytestmark = pytest.mark.gpu
 FAR = 1 << 31
@@ -142,6 +142,83 @@ def test_outputs_are_no_keys_or_values(evs):  # noqa: F811
         with pytest.raises(ValueError, match="may not be k or v"):
             call()
     assert evs.prompt_attention(q, k, v, s, out=torch.empty_like(v)).shape == v.shape
+
+
+# ---- values that are not finite ----------------------------------------------------------------
+def comb(n):
+    """Two chains in turn: no node's parent is the node before it."""
+    return [i - 2 if i > 1 else -1 for i in range(n)]
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "binary", "comb"])
+@pytest.mark.parametrize("dtype,dh,T,H,G,own", [(BF16, 128, 128, 8, 2, True), (BF16, 64, 127, 4, 4, True), (BF16, 128, 100, 4, 2, False),
+                                                (BF16, 64, 90, 8, 1, False), (F32, 32, 40, 2, 1, True)])
+def test_tree_of_values_that_are_not_finite(evs, kind, dtype, dh, T, H, G, own):  # noqa: F811
+    """An infinity in every node's V, each in a column of its own: a row has those of the nodes on its path."""
+    cached = [300, 0, 77]
+    d = make_tree(80, dtype, T, H, G, dh, 300 + T, cached)
+    d["parents"] = [comb(T) if kind == "comb" else shape_of(kind, T, None)] * 3
+    vn = d["vn"]
+    if not own:
+        for b, m in enumerate(cached):
+            d["kc"][b, :, m:m + T], d["vc"][b, :, m:m + T] = d["kn"][b], d["vn"][b]
+        d["kn"] = d["vn"] = None
+    clean = run_tree(evs, d)
+    at = torch.arange(T, device="cuda")
+    column = (at * 5) % dh
+    for b, m in enumerate(cached):
+        (vn[b] if own else d["vc"][b, :, m:m + T])[:, at, column] = math.inf
+    hit = (ref.ancestry(d["parents"][0], T).double() @ torch.nn.functional.one_hot(column.cpu(), dh).double()).cuda() > 0
+    o, lse = run_tree(evs, d)
+    assert torch.equal(lse, clean[1])
+    assert torch.equal(torch.isposinf(o), hit[None, :, None].expand_as(o))
+    assert torch.equal(o[:, ~hit.any(1)], clean[0][:, ~hit.any(1)]) and torch.equal(torch.where(hit[:, None], 0, o), torch.where(hit[:, None], 0, clean[0]))
+
+
+@pytest.mark.parametrize("dtype,dh", [(BF16, 128), (BF16, 64), (F32, 32)])
+@pytest.mark.parametrize("lens,H", [([700, 33, 300], 2), ([3000], 1), ([257] * 3, 40)], ids=str)
+def test_prompt_of_values_that_are_not_finite(evs, dtype, dh, lens, H):  # noqa: F811
+    d = make_prompt(81, dtype, lens, H, 1, dh)
+    d["v"] = d["v"].contiguous()
+    d["q"], d["k"] = d["q"].contiguous(), d["k"].contiguous()
+    N = sum(lens)
+    # a few columns: the ones that begin to be infinite in the middle of a tile, of a lane, of an item, and late
+    begins = {1: 0, 2: 5, 4: 100, 5: 128, 7: 200, 8: 255, 10: 256, 11: 300, 13: 690, 14: 2990}
+    d["v"][:, 0, list(begins)] = 1.0
+    clean = run_prompt(evs, dict(d, v=d["v"].expand(N, 1, dh)))
+    hit = torch.zeros(N, dh, dtype=torch.bool, device="cuda")
+    for s, n in zip(d["starts"], lens):
+        for c, j in begins.items():
+            d["v"][s + j:s + n, 0, c] = math.inf
+            hit[s + min(j, n):s + n, c] = True
+    o, lse = run_prompt(evs, d)
+    assert torch.equal(lse, clean[1])
+    assert torch.equal(torch.isposinf(o), hit[:, None].expand_as(o))
+    assert torch.equal(torch.where(hit[:, None], 0, o), torch.where(hit[:, None], 0, clean[0]))
+
+
+def test_no_finite_value_at_all(evs):  # noqa: F811
+    """What a model that has diverged gives: NaN everywhere, in about the time of a call (a walk for each key and row took
+    75 and 40 ms here)."""
+    d = make_tree(82, BF16, 128, 8, 8, 128, 500, [500] * 4, "chain")
+    p = make_prompt(83, BF16, [1260] * 13, 32, 8, 128)
+    d["vn"][:] = NAN
+    p["v"][:] = NAN
+
+    def timed(call):
+        best = math.inf
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            o, lse = call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        assert torch.isnan(o).all() and torch.isfinite(lse).all()
+        return best
+
+    assert timed(lambda: run_tree(evs, d)) < 5.0
+    assert timed(lambda: run_prompt(evs, p)) < 8.0
 
 
 # ---- many keys ---------------------------------------------------------------------------------
