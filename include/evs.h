@@ -517,7 +517,9 @@ evs_status evs_token_logprobs(const evs_logprob_args* args, void* stream);
  * bounded wait gives NaN for both (EVS_FLAG_TIMEOUT). Types, statistics and weights as in
  * evs_shared_attention. A value of V that is not finite shows in the rows that read it (0 times it, where their
  * weights of it are 0, may be NaN, even in a row whose every score is -inf), and in no other. How the keys are
- * dealt, and with it the last bits, goes by tokens, batch and heads. */
+ * dealt, and with it the last bits and the time, goes by tokens, batch and heads, as if all sequences were of one
+ * length. bf16 with heads of 64 or 128 and q, k and v on 16 bytes (their strides, too) runs on the tensor cores,
+ * everything else on CUDA cores. */
 typedef struct {
     int32_t tokens, batch;               /* rows of the buffers, sequences (<= 1024)        */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */
@@ -551,7 +553,9 @@ evs_status evs_prompt_attention(const evs_prompt_attn_args* args, void* stream);
  * cache_len[b] + j; rows past the capacity are left out (EVS_FLAG_KV_OVERFLOW). Lengths outside [0,
  * capacity] are clamped (EVS_FLAG_BAD_LEN). Rows that no query reads may hold anything, and a
  * node's V that is not finite shows in that node and those below it alone (as in evs_prompt_attention).
- * Everything else as in evs_shared_attention. */
+ * bf16 with heads of 64 or 128 and K and V on 16 bytes (their strides, too, none of them 0) runs on the tensor cores,
+ * everything else on CUDA cores: one cache expanded over a batch, as well. Everything else as in
+ * evs_shared_attention. */
 typedef struct {
     int32_t batch, nodes;                /* 1 .. 1024 sequences, 1 .. 128 nodes             */
     int32_t heads, kv_heads, head_dim;   /* heads a multiple of kv_heads; 16, 32, 64 or 128 */

@@ -10,9 +10,11 @@
 // Warps 0-15: softmax and output; 16: TMA of K and V; 17 and 18: Q and the scores of the lanes; 19 and 20: P V;
 // 21-23 look through V.
 //
-// Measured, bf16, heads of 128: 32768 tokens x 8 heads 1.30 ms (1.7 PFLOP/s; 0.92 us for a tile of 80 keys x 256
-// rows, 0.82 with the products alone), 8192 x 8 100 us (256 items on 152 SMs), 13 prompts of 16381 tokens x 32
-// heads 205 us (an item's start and end about 2.5 us, and a third of its tiles' work is on the diagonal).
+// Measured, bf16, heads of 128: 32768 tokens x 8 heads 1.30 ms alone (1.7 PFLOP/s; 0.92 us for a tile of 80 keys x 256
+// rows, 0.82 with the products alone) and up to 1.44 back to back, at the power limit; 8192 x 8 100 us (256 items on
+// 152 SMs), 13 prompts of 16381 tokens x 32 heads 205 us (an item's start and end about 2.5 us, and a third of its
+// tiles' work is on the diagonal). Heads of 64: 16384 x 16 600 us (0.92 PFLOP/s: a score's softmax costs the same
+// beside half of the products).
 #include "attn_simt.cuh"
 #include "attn_tiles.cuh"
 
@@ -612,6 +614,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 // =========================================================================================
 // Joins the partials of items that a run ended in: a CTA takes 1024 / dh rows of the item that worker
 // blockIdx.y's run begins within, if that is the first run to do so; four columns of two rows a thread.
+// A partial is scaled by __expf, of x <= 0: where it weighs (x > -10) off by 2^-19 at most, far inside the 2^-9 of the
+// output's own rounding.
 // Bounded by the latency of its loads: with those of one row behind the work on the other 2048 rows x 8 heads took
 // 26.2 us in all for 24.6; two or four partials of both rows on their way at once take 24.6 and 26.1 (8192 rows: 100.6
 // and 100.9 for 99.9).
@@ -751,7 +755,9 @@ bool tensor_ok(const evs_prompt_attn_args& c) {
 // Whether items are dealt in runs: where the longest of them would end far behind the mean of the SMs, if the
 // sequences were of one length (the lengths are on the device). Runs cost their own starts, partials and a launch:
 // 256 items of 8192 tokens, 54 units apart, 104 us in runs and 98 whole; 700 tokens x 8 heads (56) 19 and 14; 2048
-// tokens x 8 heads (109) 24.6 and 29.6; 4096 (145) 43 and 52; 16384 x 2 heads 104 and 180.
+// tokens x 8 heads (109) 24.6 and 29.6; 4096 (145) 43 and 52; 16384 x 2 heads 104 and 180. Batches of one long prompt
+// and many short ones look shorter than they are: 16384 rows x 2 heads beside three requests of 24 rows take 97 to 105
+// us, in runs, and 188 beside seven, in whole items; 8192 x 4 heads 60 to 64 alone, 99 beside four of 512.
 constexpr int RUNS_WORTH = 80;
 bool use_runs(const evs_prompt_attn_args& c) {
     if (c.dtype != EVS_DTYPE_BF16 || (c.head_dim != 64 && c.head_dim != 128)) return false;

@@ -12,8 +12,10 @@
 // registers by then), S of an odd tile in b and c and its P in c. So S of a tile does not touch the weights
 // of the one before, and touches those of the one before that only when their product is done. That sets the
 // tile's width: 128 columns for heads of 128 are three slots of 40, 80 keys. For heads of 64, 192 columns would
-// be 128 keys, but 96 is what fits a softmax thread's registers (619 us for 629 with 16384 tokens x 16 heads). (With P over S, tiles of 128 keys and turns at the softmax: 1.58 ms for 32768
-// tokens x 8 heads of 128; with a place of its own for P, but one only: 1.63; this: 1.42.)
+// be 128 keys, but 96 is what fits a softmax thread's registers (619 us for 629 with 16384 tokens x 16 heads when
+// it was chosen; 600 now). (With P over S, tiles of 128 keys and turns at the softmax: 1.58 ms for 32768 tokens x 8
+// heads of 128; with a place of its own for P, but one only: 1.64; with this 1.62, of which the steps after it, products
+// issued from uniform code by a warp for each kind and a ring of six slots, left 1.30.)
 // Eight warps serve a lane, two threads a row with half of the scores each: their maxima meet in a barrier
 // that carries one bit, "the maximum of some row has grown by more than 2^8": only then do they exchange
 // them and rescale O. So weights are at most 2^8, and the sum stays fp32.

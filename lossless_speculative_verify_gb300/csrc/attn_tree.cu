@@ -619,7 +619,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmKC, const __grid_constant__
 // =========================================================================================
 // Combine. 128 threads take 512 / dh (node, head) rows of a sequence and K/V head at a time, four columns of
 // one row each, and R such sets of rows at once, so that the loads of many small rows overlap (240 rows x 128
-// segments of two or three partials: 18 us with one set, 10 with two, 12 with four). Where rows have many partials
+// segments of two or three partials: 18 us with one set, 10 with two; four were tried, and took 12). Where rows have many partials
 // (and a CTA one set), up to four such groups of threads deal them among themselves.
 // =========================================================================================
 constexpr int GROUPS = 4;
@@ -738,9 +738,9 @@ bool valid_shape(const evs_tree_attn_args* c) {
 }
 
 // Row sizes and slots of the CUDA-core path: about four waves of the SMs at two CTAs each, or one slot, which needs
-// no second launch, where the keys are few tiles of little work (4 sequences x 7 nodes x 4 heads of 16 over 256 rows:
-// 21 us a call for 25, though 10.0 for 7.6 in a
-// replayed graph; over 512 rows 16 for 8).
+// no second launch, where the keys are few tiles of little work: that saves a call its host time and costs a replayed
+// graph (4 sequences x 7 nodes x 4 heads of 16 over 128, 256, 448, 512 rows: a call 24 us with one slot and 28 with
+// several; in a graph 6.7, 9.5, 13.6, 14.9 and 7.1, 7.4, 8.0, 8.4. The border lies between the last two).
 constexpr long long ONE_SLOT = 2048;     // key tiles x rows x columns
 int simt_rows(const evs_tree_attn_args& c) { return c.nodes * (c.heads / c.kv_heads) > 16 ? 64 : 16; }
 void plan_simt(const evs_tree_attn_args& c, TreeArgs& a) {

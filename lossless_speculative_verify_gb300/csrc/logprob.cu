@@ -12,7 +12,7 @@
 // that the K-th largest token reaches, too, and a token that does is one of a thread whose maximum does. So
 // only those threads' tokens (K / 256 of the row, from L2) are read a second time, and the few that reach the
 // border (its leading bits, found by counting) are ranked by one warp in registers. Where more than 256 do,
-// as among equal logits, every warp keeps a sorted list and the lists are joined. No order of execution shows.
+// as among equal logits, every warp keeps a sorted list and the lists are joined (512 x 131072 of zeros: 330 us). No order of execution shows.
 //
 // Measured (replayed graphs): 13 x 512 fp32 2.2 us, 208 x 4096 with eight alternatives 6.8, 64 x 50021 bf16 with
 // 20 10.8, 512 x 131072 fp32 with five 56 (4.8 TB/s; the row's passage is 40 at the rate of a copy, the uneven last
@@ -478,9 +478,10 @@ extern "C" evs_status evs_token_logprobs(const evs_logprob_args* c, void* stream
     LogprobArgs a{c->logits, c->ld, c->vocab, c->n_tokens, c->top, c->temperature, c->tokens, c->logprob, c->entropy,
                   c->top_logprob, c->top_token, c->flags};
     // CTAs of a row: two, four or eight where the rows leave SMs without any and a CTA's share stays some passes long,
-    // or where rows of the largest vocabularies would make an uneven wave (64 x 50021 bf16: 11.6 us with two, 12.4
-    // with one, 14 with four; 256 x 131072: 33 with two, 39 with one). A CTA has 128 threads for a short share, whose
-    // time is the ranking's steps (4096 x 4096: 29 us, 256 threads 52), and 256 for a long one (512 x 131072: 58, 67).
+    // or where rows of the largest vocabularies would make an uneven wave (64 x 50021 bf16: 10.7 us with two, 11.5
+    // with one, 13.0 with four; 256 x 131072: 31 with two, 39 with one, 34 with four). A CTA has 128 threads for a short
+    // share, whose time is the ranking's steps (4096 x 4096: 24 us, 256 threads 40), and 256 for a long one (512 x
+    // 131072: 55, 128 threads 83).
     const long long rows = c->rows;
     int cs = 1;
     while (cs < LP_MAX_CS && ((2 * rows * cs <= 152 && c->vocab / (2 * cs) >= 8192) || (rows * cs < 304 && c->vocab / (2 * cs) >= 65536)))

@@ -312,10 +312,10 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, return_lse=False,
     dh], all fp32 or all bf16. Sequence b is rows starts[b] up to starts[b + 1] of starts [batch + 1] (int32, on the
     device, ascending); its row i reads its rows j <= i.
 
-    Any strides but the last (k and v alike), so that q, k and v may be parts of one projection's output. heads is
-    a multiple of kv_heads; dh 16, 32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Rows of no sequence may
-    hold anything; they are left as they were in ``out``, and zero where none is given. Returns out [tokens, heads,
-    dh], or [out, lse fp32 [tokens, heads]], whose rows of no sequence are -inf."""
+    Any strides but the last (k and v alike), so that q, k and v may be parts of one projection's output; bf16 with
+    heads of 64 or 128 whose rows start on 16 bytes is what runs on the tensor cores. heads is a multiple of kv_heads; dh 16, 32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Rows of no sequence may hold
+    anything; they are left as they were in ``out``, and zero where none is given. Returns out [tokens, heads, dh], or
+    [out, lse fp32 [tokens, heads]], whose rows of no sequence are -inf."""
     dev = _device("q", q)
     _need(q.dim() == 3 and q.dtype in _DT, "q: want fp32 or bf16 [tokens, heads, dh]")
     N, H, dh = q.shape
@@ -371,9 +371,12 @@ def tree_attention(q, k_cache, v_cache, cache_len, parents, k_nodes=None, v_node
     ``out``, and zero where none is given.
 
     The nodes' K/V are k_nodes and v_nodes [batch, kv_heads, nodes, dh], or without them the cache's rows
-    cache_len[b] + i. All fp32 or all bf16, with any strides but the last (K and V of a pair alike); heads is a
-    multiple of kv_heads; dh 16, 32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Returns out [batch, nodes,
-    heads, dh], or [out, lse fp32 [batch, nodes, heads]]."""
+    cache_len[b] + i. All fp32 or all bf16. K and V have any strides but the last (those of a pair alike); q's and out's
+    heads are contiguous and their rows evenly spaced over nodes and batch. bf16 with heads of 64 or 128 whose K/V rows
+    start on 16 bytes is what runs on the tensor cores; a cache that is expanded over the batch or the heads (a stride
+    of 0) does not, and is many times slower than one with rows of its own. heads is a multiple of kv_heads; dh 16,
+    32, 64 or 128; scale None (1 / sqrt(dh)) or 1e-30 to 1e30. Returns out [batch, nodes, heads, dh], or [out, lse fp32
+    [batch, nodes, heads]]."""
     dev = _device("q", q)
     _need(q.dim() == 4 and q.dtype in _DT, "q: want fp32 or bf16 [batch, nodes, heads, dh]")
     B, T, H, dh = q.shape
